@@ -75,6 +75,7 @@ typedef enum carat_status {
 #define CARAT_DEV_BAD_CONTEXT 0x1 /* context_length < 0, or key_count > capacity */
 #define CARAT_DEV_BAD_CACHE_ID 0x2 /* ring/cache id outside [0, num_rings) */
 #define CARAT_DEV_TIMEOUT 0x4      /* a kernel gave up waiting (bounded wait); results invalid */
+#define CARAT_DEV_BAD_POSITION 0x8 /* a rotary position outside the table */
 
 /* Largest proposal_count the attention entry points accept. */
 #define CARAT_MAX_PROPOSALS 16
@@ -426,6 +427,130 @@ carat_status carat_swa_attention_fp8(float *out, const void *queries, const void
                                      int batch, int q_heads, int kv_heads, int head_dim,
                                      int window, float scale, float k_scale, float v_scale,
                                      void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Rotary paged appends: the rotary position embedding applied to this step's
+ * queries and keys on their way, in one launch.
+ *
+ * Token j of request b is rotated by row t = positions[b][j] (or
+ * context_lengths[b] + j when positions is NULL) of the table: with r =
+ * rotary_dim, c_i = cos_sin[t][i] and s_i = cos_sin[t][r/2 + i] for i < r/2,
+ * each pair (x, y) of a row's first r elements becomes
+ * (x c_i - y s_i, y c_i + x s_i).  The pair is elements (i, i + r/2), or
+ * (2i, 2i + 1) when interleaved != 0; elements past r stay as they are.  The
+ * arithmetic is fp32, rounded once.  Values are not rotated.
+ *
+ * carat_paged_rope_append -- carat_paged_append with the rotation: rows for
+ * positions context_lengths[b] + j of the bf16 pages.
+ *
+ *   k_new, v_new     bf16, token (b, j) at element (b * proposal_count + j) *
+ *                    kv_token_stride: [kv_heads][head_dim] dense.  Parts of a
+ *                    fused projection's output are taken in place.
+ *   queries          bf16, token (b, j) at (b * proposal_count + j) *
+ *                    q_token_stride; NULL with q_heads = 0: keys and values only.
+ *   queries_out      bf16 [batch][proposal_count][q_heads][head_dim] dense; may be
+ *                    `queries` itself when that is dense.
+ *   cos_sin          fp32 [table_rows][rotary_dim].
+ *   positions        int32 [batch][proposal_count] or NULL.  Gives the angle
+ *                    only (a token tree's siblings share one); the row a token
+ *                    is stored in is always that of position
+ *                    context_lengths[b] + j.
+ *   new_counts       int32 [batch] or NULL (= proposal_count each): the rows
+ *                    request b really appends, 0 <= new_counts[b] <=
+ *                    proposal_count.  Rows behind them are neither read nor
+ *                    written, in the caches as in queries_out.
+ *
+ * On the device: a request with context_length < 0, a count out of range or
+ * context_length + count > max_pages * page_rows is skipped, its queries_out
+ * rows are NaN and CARAT_DEV_BAD_CONTEXT is set; a token whose table row lies
+ * outside [0, table_rows) is not stored, its queries_out rows are NaN and
+ * CARAT_DEV_BAD_POSITION is set; a row whose page id lies outside the pool is
+ * not stored and CARAT_DEV_BAD_CACHE_ID is set.
+ * Limits: head_dim and rotary_dim multiples of 16, rotary_dim <= head_dim;
+ * token strides multiples of 8 elements; page_rows a multiple of 128.
+ * Supported head_dim: multiples of 16 up to 128, of 32 up to 256, of 64 up to 512
+ * and of 128 up to 1024 (others: CARAT_ERR_UNSUPPORTED).
+ *
+ * carat_paged_rope_append_fp8 -- the same into e4m3 pages (uint8, same shape)
+ * with one scale per block of block_rows consecutive tokens and KV head:
+ *   k_scales, v_scales  fp32 [num_pages][page_rows / block_rows][kv_heads]; the
+ *                    value of a stored byte is e4m3(byte) * its block's scale.
+ *   block_rows       16, 32, 64 or 128.
+ * A call finds, for each block and head it stores into, the largest finite
+ * magnitude of its own new rows (keys after rotation) and from it the least
+ * power of two s with magnitude <= 448 s (exponent kept in [-100, 100]).  A
+ * block whose first position is >= context_lengths[b] starts afresh with scale
+ * s, whatever its page held before; any other keeps max(its scale, s), and when
+ * that grows, the bytes of its earlier rows are rounded to the new scale (exact,
+ * both being powers of two, but for values that become e4m3 subnormals).  Each
+ * new element x is stored as e4m3_rn_satfinite(fp32(x * fp32(1 / scale))).  A
+ * scale never shrinks while its block is in use: rows of rejected proposals
+ * may leave it larger than the rows that stay need.  A page must not be
+ * appended to by two requests of one call.
+ */
+carat_status carat_paged_rope_append(void *key_pages, void *value_pages, int num_pages,
+                                     const int32_t *page_table, int max_pages, int page_rows,
+                                     const void *k_new, const void *v_new, int64_t kv_token_stride,
+                                     void *queries_out, const void *queries, int64_t q_token_stride,
+                                     const float *cos_sin, int table_rows, int rotary_dim,
+                                     int interleaved, const int32_t *positions,
+                                     const int32_t *new_counts, const int32_t *context_lengths,
+                                     int proposal_count, int batch, int q_heads, int kv_heads,
+                                     int head_dim, void *stream);
+carat_status carat_paged_rope_append_fp8(
+    void *key_pages, void *value_pages, float *k_scales, float *v_scales, int num_pages,
+    const int32_t *page_table, int max_pages, int page_rows, int block_rows, const void *k_new,
+    const void *v_new, int64_t kv_token_stride, void *queries_out, const void *queries,
+    int64_t q_token_stride, const float *cos_sin, int table_rows, int rotary_dim, int interleaved,
+    const int32_t *positions, const int32_t *new_counts, const int32_t *context_lengths,
+    int proposal_count, int batch, int q_heads, int kv_heads, int head_dim, void *stream);
+
+/*
+ * carat_global_verify_attention_paged -- carat_global_verify_attention over
+ * bf16 pages that already hold this step's rows (e.g. after
+ * carat_paged_rope_append).  workspace as in
+ * carat_global_append_verify_attention_paged.
+ */
+carat_status carat_global_verify_attention_paged(
+    float *out, const void *queries, const void *key_pages, const void *value_pages, int num_pages,
+    const int32_t *page_table, int max_pages, int page_rows, const int32_t *context_lengths,
+    int proposal_count, int batch, int q_heads, int kv_heads, int head_dim, float scale,
+    void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * carat_paged_verify_attention_fp8 -- decode / verify attention over e4m3
+ * pages with block scales, as carat_paged_rope_append_fp8 writes them (any
+ * positive normal scales are taken).  This step's rows must already be stored.
+ *
+ *   out              bf16 [batch][proposal_count][q_heads][head_dim], what the
+ *                    output projection takes: the weights of the PV product are
+ *                    rounded to f16, so an fp32 output would promise digits that
+ *                    are not there.
+ *   queries          bf16, same shape, after the rotation.
+ *   window           0: query j attends to every position up to its own,
+ *                    context_lengths[b] + j; w > 0: to the last w of those.
+ *                    Pages that hold none of them are never read.
+ *   Pages, page table, block scales as in carat_paged_rope_append_fp8;
+ *   scale, context_lengths and device-side errors as in
+ *   carat_global_append_verify_attention_paged.  A page id outside the pool
+ *   reads as zeros and sets CARAT_DEV_BAD_CACHE_ID.  Bytes of rows at or past
+ *   the key count (context_length + proposal_count) never reach the result.
+ *   workspace        >= carat_paged_fp8_workspace_bytes(..., max_pages *
+ *                    page_rows) bytes; needs no initialisation; calls that
+ *                    overlap on the GPU need separate workspaces.
+ *
+ * Supported: head_dim 256 or 512; (q_heads/kv_heads) * proposal_count <= 128;
+ * q_heads/kv_heads <= 64; proposal_count <= 16; batch * q_heads *
+ * proposal_count < 2^24 (other shapes: CARAT_ERR_UNSUPPORTED).
+ */
+carat_status carat_paged_verify_attention_fp8(
+    void *out, const void *queries, const void *key_pages, const void *value_pages,
+    const float *k_scales, const float *v_scales, int num_pages, const int32_t *page_table,
+    int max_pages, int page_rows, int block_rows, const int32_t *context_lengths,
+    int proposal_count, int batch, int q_heads, int kv_heads, int head_dim, int window,
+    float scale, void *workspace, size_t workspace_bytes, void *stream);
+size_t carat_paged_fp8_workspace_bytes(int batch, int proposal_count, int q_heads, int kv_heads,
+                                       int head_dim, int capacity);
 
 /* Workspace bytes the attention calls need for these sizes (the same for the
  * plain and the fused-append entry points; 0 if the sizes are invalid, or if

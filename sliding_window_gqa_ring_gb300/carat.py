@@ -32,6 +32,7 @@ CARAT_ERR_CUDA = 4
 CARAT_DEV_BAD_CONTEXT = 0x1
 CARAT_DEV_BAD_CACHE_ID = 0x2
 CARAT_DEV_TIMEOUT = 0x4
+CARAT_DEV_BAD_POSITION = 0x8
 MAX_PROPOSALS = 16
 MAX_TILE_ROWS = 128
 
@@ -46,6 +47,9 @@ EXPORTED = (
     "carat_pool_alloc_pages", "carat_pool_free_pages", "carat_pool_stats",
     "carat_ring_append_fp8", "carat_ring_rollback_fp8", "carat_swa_attention_fp8",
     "carat_check_bounded_wait", "carat_launch_floor",
+    "carat_paged_rope_append", "carat_paged_rope_append_fp8",
+    "carat_global_verify_attention_paged", "carat_paged_verify_attention_fp8",
+    "carat_paged_fp8_workspace_bytes",
 )
 
 
@@ -124,6 +128,24 @@ def _declare(lib):
     lib.carat_swa_attention_fp8.restype = i32
     lib.carat_swa_attention_fp8.argtypes = [vp, vp, vp, vp, i32, vp, vp, vp, i32, i32, i32, i32,
                                             i32, i32, f32, f32, f32, vp, sz, vp]
+    i64 = ctypes.c_int64
+    lib.carat_paged_rope_append.restype = i32
+    lib.carat_paged_rope_append.argtypes = [
+        vp, vp, i32, vp, i32, i32, vp, vp, i64, vp, vp, i64, vp, i32, i32, i32, vp, vp, vp, i32, i32,
+        i32, i32, i32, vp]
+    lib.carat_paged_rope_append_fp8.restype = i32
+    lib.carat_paged_rope_append_fp8.argtypes = [
+        vp, vp, vp, vp, i32, vp, i32, i32, i32, vp, vp, i64, vp, vp, i64, vp, i32, i32, i32, vp, vp,
+        vp, i32, i32, i32, i32, i32, vp]
+    lib.carat_global_verify_attention_paged.restype = i32
+    lib.carat_global_verify_attention_paged.argtypes = [
+        vp, vp, vp, vp, i32, vp, i32, i32, vp, i32, i32, i32, i32, i32, f32, vp, sz, vp]
+    lib.carat_paged_verify_attention_fp8.restype = i32
+    lib.carat_paged_verify_attention_fp8.argtypes = [
+        vp, vp, vp, vp, vp, vp, i32, vp, i32, i32, i32, vp, i32, i32, i32, i32, i32, i32, f32, vp, sz,
+        vp]
+    lib.carat_paged_fp8_workspace_bytes.restype = sz
+    lib.carat_paged_fp8_workspace_bytes.argtypes = [i32] * 6
     lib.carat_global_append_verify_attention.restype = i32
     lib.carat_global_append_verify_attention.argtypes = [vp, vp, vp, vp, i32, vp, vp, vp, vp, i32,
                                                          i32, i32, i32, i32, i32, f32, vp, sz, vp]
@@ -502,3 +524,198 @@ def carat_swa_attention_fp8(out, queries, k_ring, v_ring, context_lengths, *, sc
         float(scale), float(k_scale), float(v_scale), _ptr(workspace),
         workspace.numel() * workspace.element_size(), _stream(stream)),
         "carat_swa_attention_fp8")
+
+
+# ---------------------------------------------------------------------------
+# Rotary paged appends, and attention over e4m3 pages with a scale per block of
+# tokens and KV head
+# ---------------------------------------------------------------------------
+
+def _on_device(what, **tensors):
+    """Every tensor given is on the current CUDA device (a kernel would fault on
+    a host pointer)."""
+    device = torch.cuda.current_device()
+    for name, t in tensors.items():
+        if t is not None and not (t.is_cuda and t.get_device() == device):
+            raise ValueError(f"{what}: {name} must be on the current CUDA device")
+
+
+def _tokens(t, heads, head_dim, batch, k, name):
+    """(pointer, token stride in elements) of a [B][k][heads][head_dim] tensor
+    whose tokens are dense rows a fixed stride apart."""
+    _expect(t, torch.bfloat16, name)
+    if tuple(t.shape) != (batch, k, heads, head_dim):
+        raise ValueError(f"{name} must be [batch][k][heads][head_dim] = "
+                         f"{(batch, k, heads, head_dim)}, got {tuple(t.shape)}")
+    s0, s1, s2, s3 = t.stride()
+    if k == 1:
+        s1 = s0 if batch > 1 else heads * head_dim
+    if (head_dim > 1 and s3 != 1) or (heads > 1 and s2 != head_dim) or \
+            (batch > 1 and s0 != k * s1):
+        raise ValueError(f"{name}: a token's heads must be dense and its tokens equally spaced")
+    return ctypes.c_void_p(t.data_ptr()), s1
+
+
+def _paged_pool(key_pages, value_pages, page_table, context_lengths, dtype, batch, what):
+    _expect(key_pages, dtype, f"{what}: key_pages")
+    _expect(value_pages, dtype, f"{what}: value_pages")
+    _expect(page_table, torch.int32, f"{what}: page_table")
+    _expect(context_lengths, torch.int32, f"{what}: context_lengths")
+    if key_pages.dim() != 4 or key_pages.shape != value_pages.shape:
+        raise ValueError(f"{what}: key and value pages must be 4-D and alike")
+    if page_table.dim() != 2 or page_table.shape[0] != batch:
+        raise ValueError(f"{what}: page_table must be [batch][max_pages]")
+    if tuple(context_lengths.shape) != (batch,):
+        raise ValueError(f"{what}: context_lengths must be [batch]")
+    return key_pages.shape
+
+
+def _block_scales(k_scales, v_scales, num_pages, page_rows, kv_heads, what):
+    """block_rows from the shape of the scales [num_pages][blocks][kv_heads]."""
+    _expect(k_scales, torch.float32, f"{what}: k_scales")
+    _expect(v_scales, torch.float32, f"{what}: v_scales")
+    if k_scales.dim() != 3 or k_scales.shape != v_scales.shape or \
+            k_scales.shape[0] != num_pages or k_scales.shape[2] != kv_heads or \
+            k_scales.shape[1] < 1 or page_rows % k_scales.shape[1]:
+        raise ValueError(f"{what}: scales must be [num_pages][page_rows / block_rows][kv_heads]")
+    return page_rows // k_scales.shape[1]
+
+
+def _rope_args(what, dtype, key_pages, value_pages, page_table, k_new, v_new, context_lengths,
+               cos_sin, queries, queries_out, positions, new_counts, k_scales=None,
+               v_scales=None):
+    if k_new.dim() != 4:
+        raise ValueError(f"{what}: k_new must be [batch][k][kv_heads][head_dim]")
+    batch, k = k_new.shape[0], k_new.shape[1]
+    num_pages, page_rows, kv_heads, head_dim = _paged_pool(
+        key_pages, value_pages, page_table, context_lengths, dtype, batch, what)
+    _expect(cos_sin, torch.float32, f"{what}: cos_sin")
+    if cos_sin.dim() != 2:
+        raise ValueError(f"{what}: cos_sin must be [table_rows][rotary_dim]")
+    kp, kv_stride = _tokens(k_new, kv_heads, head_dim, batch, k, f"{what}: k_new")
+    vp, v_stride = _tokens(v_new, kv_heads, head_dim, batch, k, f"{what}: v_new")
+    if kv_stride != v_stride:
+        raise ValueError(f"{what}: k_new and v_new must have one token stride")
+    q_heads, qp, q_stride = 0, None, 0
+    if (queries is None) != (queries_out is None):
+        raise ValueError(f"{what}: queries and queries_out go together")
+    if queries is not None:
+        if queries.dim() != 4:
+            raise ValueError(f"{what}: queries must be [batch][k][q_heads][head_dim]")
+        q_heads = queries.shape[2]
+        qp, q_stride = _tokens(queries, q_heads, head_dim, batch, k, f"{what}: queries")
+        _expect(queries_out, torch.bfloat16, f"{what}: queries_out")
+        if queries_out.shape != queries.shape:
+            raise ValueError(f"{what}: queries_out must have the queries' shape")
+    if positions is not None:
+        _expect(positions, torch.int32, f"{what}: positions")
+        if tuple(positions.shape) != (batch, k):
+            raise ValueError(f"{what}: positions must be [batch][k]")
+    if new_counts is not None:
+        _expect(new_counts, torch.int32, f"{what}: new_counts")
+        if tuple(new_counts.shape) != (batch,):
+            raise ValueError(f"{what}: new_counts must be [batch]")
+    _on_device(what, key_pages=key_pages, value_pages=value_pages, page_table=page_table,
+               k_new=k_new, v_new=v_new, context_lengths=context_lengths, cos_sin=cos_sin,
+               queries=queries, queries_out=queries_out, positions=positions,
+               new_counts=new_counts, k_scales=k_scales, v_scales=v_scales)
+    head = (num_pages, _ptr(page_table), page_table.shape[1], page_rows)
+    tail = (kp, vp, kv_stride, _ptr(queries_out), qp, q_stride, _ptr(cos_sin), cos_sin.shape[0],
+            cos_sin.shape[1])
+    rest = (_ptr(positions), _ptr(new_counts), _ptr(context_lengths), k, batch, q_heads, kv_heads,
+            head_dim)
+    return head, tail, rest
+
+
+def carat_paged_rope_append(key_pages, value_pages, page_table, k_new, v_new, context_lengths, *,
+                            cos_sin, interleaved=False, queries=None, queries_out=None,
+                            positions=None, new_counts=None, stream=None):
+    """Rotate this step's keys (and queries, into queries_out) and write keys and
+    values into bf16 pages [num_pages][page_rows][Hkv][D] at positions
+    context_lengths[b] + j.
+
+    k_new, v_new bf16 [B][k][Hkv][D] and queries bf16 [B][k][Hq][D] may be parts
+    of a fused projection's output: a token's heads are dense, tokens a fixed
+    stride apart.  cos_sin fp32 [table_rows][rotary_dim] (engine.rotary_table).
+    positions int32 [B][k] (angles only; default context_lengths[b] + j);
+    new_counts int32 [B]: rows request b really appends (default k)."""
+    what = "carat_paged_rope_append"
+    head, tail, rest = _rope_args(what, torch.bfloat16, key_pages, value_pages, page_table, k_new,
+                                  v_new, context_lengths, cos_sin, queries, queries_out, positions,
+                                  new_counts)
+    _check(library().carat_paged_rope_append(
+        _ptr(key_pages), _ptr(value_pages), *head, *tail, 1 if interleaved else 0, *rest,
+        _stream(stream)), what)
+
+
+def carat_paged_rope_append_fp8(key_pages, value_pages, k_scales, v_scales, page_table, k_new,
+                                v_new, context_lengths, *, cos_sin, interleaved=False,
+                                queries=None, queries_out=None, positions=None, new_counts=None,
+                                stream=None):
+    """carat_paged_rope_append into e4m3 pages (uint8) with one power-of-two
+    scale per block of tokens and KV head: k_scales, v_scales fp32
+    [num_pages][page_rows / block_rows][Hkv], block_rows 16, 32, 64 or 128.  A
+    block that starts in this call takes the least scale that holds its rows;
+    one that already held rows keeps its scale or grows it, its older bytes
+    then being rounded to the new one."""
+    what = "carat_paged_rope_append_fp8"
+    head, tail, rest = _rope_args(what, torch.uint8, key_pages, value_pages, page_table, k_new,
+                                  v_new, context_lengths, cos_sin, queries, queries_out, positions,
+                                  new_counts, k_scales, v_scales)
+    num_pages, page_rows, kv_heads, _ = key_pages.shape
+    block_rows = _block_scales(k_scales, v_scales, num_pages, page_rows, kv_heads, what)
+    _check(library().carat_paged_rope_append_fp8(
+        _ptr(key_pages), _ptr(value_pages), _ptr(k_scales), _ptr(v_scales), *head, block_rows,
+        *tail, 1 if interleaved else 0, *rest, _stream(stream)), what)
+
+
+def carat_global_verify_attention_paged(out, queries, key_pages, value_pages, page_table,
+                                        context_lengths, *, scale, workspace, stream=None):
+    """Grouped causal verify attention over bf16 pages that already hold this
+    step's rows (e.g. after carat_paged_rope_append); out fp32 [B][k][Hq][D]."""
+    what = "carat_global_verify_attention_paged"
+    batch, k, q_heads, head_dim, num_pages, page_rows, kv_heads = _attention_args(
+        out, queries, key_pages, value_pages, context_lengths, torch.bfloat16, what)
+    _paged_pool(key_pages, value_pages, page_table, context_lengths, torch.bfloat16, batch, what)
+    _on_device(what, out=out, queries=queries, key_pages=key_pages, value_pages=value_pages,
+               page_table=page_table, context_lengths=context_lengths, workspace=workspace)
+    _check(library().carat_global_verify_attention_paged(
+        _ptr(out), _ptr(queries), _ptr(key_pages), _ptr(value_pages), num_pages, _ptr(page_table),
+        page_table.shape[1], page_rows, _ptr(context_lengths), k, batch, q_heads, kv_heads,
+        head_dim, float(scale), _ptr(workspace), workspace.numel() * workspace.element_size(),
+        _stream(stream)), what)
+
+
+def paged_fp8_workspace_bytes(batch, proposal_count, q_heads, kv_heads, head_dim, capacity) -> int:
+    return int(library().carat_paged_fp8_workspace_bytes(batch, proposal_count, q_heads, kv_heads,
+                                                         head_dim, capacity))
+
+
+def carat_paged_verify_attention_fp8(out, queries, key_pages, value_pages, k_scales, v_scales,
+                                     page_table, context_lengths, *, scale, workspace, window=0,
+                                     stream=None):
+    """Decode / verify attention over e4m3 pages with block scales (as
+    carat_paged_rope_append_fp8 writes them) that already hold this step's rows.
+
+    out and queries bf16 [B][k][Hq][D]; window 0: every position up to the
+    query's own, w > 0: the last w of them; workspace: a CUDA tensor of at
+    least paged_fp8_workspace_bytes(...) bytes."""
+    what = "carat_paged_verify_attention_fp8"
+    _expect(out, torch.bfloat16, f"{what}: out")
+    _expect(queries, torch.bfloat16, f"{what}: queries")
+    if queries.dim() != 4 or out.shape != queries.shape:
+        raise ValueError(f"{what}: queries must be [batch][k][q_heads][head_dim], out alike")
+    batch, k, q_heads, head_dim = queries.shape
+    num_pages, page_rows, kv_heads, cache_dim = _paged_pool(
+        key_pages, value_pages, page_table, context_lengths, torch.uint8, batch, what)
+    if cache_dim != head_dim:
+        raise ValueError(f"{what}: cache head_dim {cache_dim} != query head_dim {head_dim}")
+    block_rows = _block_scales(k_scales, v_scales, num_pages, page_rows, kv_heads, what)
+    _on_device(what, out=out, queries=queries, key_pages=key_pages, value_pages=value_pages,
+               k_scales=k_scales, v_scales=v_scales, page_table=page_table,
+               context_lengths=context_lengths, workspace=workspace)
+    _check(library().carat_paged_verify_attention_fp8(
+        _ptr(out), _ptr(queries), _ptr(key_pages), _ptr(value_pages), _ptr(k_scales),
+        _ptr(v_scales), num_pages, _ptr(page_table), page_table.shape[1], page_rows, block_rows,
+        _ptr(context_lengths), k, batch, q_heads, kv_heads, head_dim, int(window), float(scale),
+        _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream)), what)

@@ -25,6 +25,8 @@ constexpr int kMaxDevices = 64;
 std::mutex g_status_mutex;
 int *g_status_ptr[kMaxDevices];
 
+}  // namespace
+
 // Device address of this device's status word (looked up once per device).
 int *device_status_ptr() {
     int dev = 0;
@@ -37,24 +39,6 @@ int *device_status_ptr() {
     }
     return g_status_ptr[dev];
 }
-
-bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-bool supported_head_dim(int d) { return d == 256 || d == 512; }
-
-struct SplitPlan {
-    bool unit_mode = false;    // whole units from a work counter (else stream-K)
-    bool fp8 = false;          // FP8 e4m3 rings
-    bool deep = false;         // a call with at most one tile per SM: one CTA per SM, deep ring
-    int grid = 0;              // CTAs launched
-    size_t ml_bytes = 0;
-    size_t o_bytes = 0;
-    size_t unit_bytes = 0;
-    size_t sched_bytes = 0;
-    size_t total = 0;
-};
-
-size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
 // SMs of the current device (looked up once per device); 152, a GB300's
 // count, when no device can be queried -- workspace sizes asked for without a
@@ -75,6 +59,26 @@ int device_sm_count() {
     cached[dev].store(n, std::memory_order_relaxed);
     return n;
 }
+
+namespace {
+
+bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+bool supported_head_dim(int d) { return d == 256 || d == 512; }
+
+struct SplitPlan {
+    bool unit_mode = false;    // whole units from a work counter (else stream-K)
+    bool fp8 = false;          // FP8 e4m3 rings
+    bool deep = false;         // a call with at most one tile per SM: one CTA per SM, deep ring
+    int grid = 0;              // CTAs launched
+    size_t ml_bytes = 0;
+    size_t o_bytes = 0;
+    size_t unit_bytes = 0;
+    size_t sched_bytes = 0;
+    size_t total = 0;
+};
+
+size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
 // Tensor-core path.  Units (request, KV head, row group) that fill every
 // resident CTA slot and are all short (at most 16 tiles of 128 keys) are
@@ -299,13 +303,19 @@ carat_status carat_swa_attention(float *out, const void *queries, const void *k_
     return launch_status(launch_attention(p, plan, static_cast<cudaStream_t>(stream)));
 }
 
-carat_status carat_global_verify_attention(float *out, const void *queries, const void *key_cache,
-                                           const void *value_cache, int num_caches,
-                                           const int32_t *cache_ids,
-                                           const int32_t *context_lengths, int proposal_count,
-                                           int batch, int q_heads, int kv_heads, int head_dim,
-                                           int capacity, float scale, void *workspace,
-                                           size_t workspace_bytes, void *stream) {
+struct PagedArgs {
+    const int32_t *page_table = nullptr;
+    int max_pages = 0, page_rows = 0, num_pages = 0;
+};
+
+// Grouped verify attention over caches that already hold this step's rows.
+static carat_status verify_attention(float *out, const void *queries, const void *key_cache,
+                                     const void *value_cache, int num_caches,
+                                     const int32_t *cache_ids, const int32_t *context_lengths,
+                                     int proposal_count, int batch, int q_heads, int kv_heads,
+                                     int head_dim, int capacity, float scale, void *workspace,
+                                     size_t workspace_bytes, void *stream, KeySource source,
+                                     PagedArgs pg = PagedArgs()) {
     if (!attention_shape_ok(batch, proposal_count, q_heads, kv_heads, head_dim) ||
         capacity < proposal_count || !std::isfinite(scale))
         return CARAT_ERR_INVALID_ARG;
@@ -340,19 +350,31 @@ carat_status carat_global_verify_attention(float *out, const void *queries, cons
     p.window = 0;
     p.capacity = capacity;
     p.scale_log2 = scale * 1.4426950408889634f;
-    p.source = KeySource::kLinear;
+    p.source = source;
+    p.page_table = pg.page_table;
+    p.max_pages = pg.max_pages;
+    p.page_rows = pg.page_rows;
+    p.num_pages = pg.num_pages;
     return launch_status(launch_attention(p, plan, static_cast<cudaStream_t>(stream)));
+}
+
+carat_status carat_global_verify_attention(float *out, const void *queries, const void *key_cache,
+                                           const void *value_cache, int num_caches,
+                                           const int32_t *cache_ids,
+                                           const int32_t *context_lengths, int proposal_count,
+                                           int batch, int q_heads, int kv_heads, int head_dim,
+                                           int capacity, float scale, void *workspace,
+                                           size_t workspace_bytes, void *stream) {
+    return verify_attention(out, queries, key_cache, value_cache, num_caches, cache_ids,
+                            context_lengths, proposal_count, batch, q_heads, kv_heads, head_dim,
+                            capacity, scale, workspace, workspace_bytes, stream,
+                            KeySource::kLinear);
 }
 
 // Shared by the two fused entry points: attention over the caches as they are
 // before this step plus this step's rows, which are then written into the
 // caches (by the attention kernel itself, or by a ring append launched after
 // it when several CTAs read each ring tile).
-struct PagedArgs {
-    const int32_t *page_table = nullptr;
-    int max_pages = 0, page_rows = 0, num_pages = 0;
-};
-
 static carat_status append_attention(float *out, const void *queries, void *k_base, void *v_base,
                                      int num_ids, const int32_t *ids, void *displaced,
                                      const void *k_new,
@@ -492,6 +514,23 @@ carat_status carat_global_append_verify_attention_paged(
                             nullptr, k_new, v_new, context_lengths, proposal_count, batch,
                             q_heads, kv_heads, head_dim, 0, max_pages * page_rows, scale,
                             workspace, workspace_bytes, stream, KeySource::kPaged, pg);
+}
+
+carat_status carat_global_verify_attention_paged(
+    float *out, const void *queries, const void *key_pages, const void *value_pages, int num_pages,
+    const int32_t *page_table, int max_pages, int page_rows, const int32_t *context_lengths,
+    int proposal_count, int batch, int q_heads, int kv_heads, int head_dim, float scale,
+    void *workspace, size_t workspace_bytes, void *stream) {
+    if (!paged_args_ok(num_pages, page_table, max_pages, page_rows)) return CARAT_ERR_INVALID_ARG;
+    PagedArgs pg;
+    pg.page_table = page_table;
+    pg.max_pages = max_pages;
+    pg.page_rows = page_rows;
+    pg.num_pages = num_pages;
+    return verify_attention(out, queries, key_pages, value_pages, batch > 0 ? batch : 1, nullptr,
+                            context_lengths, proposal_count, batch, q_heads, kv_heads, head_dim,
+                            max_pages * page_rows, scale, workspace, workspace_bytes, stream,
+                            KeySource::kPaged, pg);
 }
 
 carat_status carat_paged_append(void *key_pages, void *value_pages, int num_pages,

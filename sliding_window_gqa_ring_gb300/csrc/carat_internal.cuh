@@ -190,8 +190,50 @@ __device__ __forceinline__ long long paged_row(const int32_t *page_table, int ma
     return (long long)page * page_rows + t % page_rows;
 }
 
+// Everything a rotary paged append needs; passed by value as a kernel argument.
+struct RopeParams {
+    const uint16_t *q;          // [B][k][Hq][D], tokens q_stride elements apart
+    uint16_t *q_out;            // [B][k][Hq][D]
+    const uint16_t *k_new;      // [B][k][Hkv][D], tokens kv_stride elements apart
+    const uint16_t *v_new;
+    long long q_stride, kv_stride;
+    void *k_pages, *v_pages;    // bf16 or e4m3 [num_pages][page_rows][Hkv][D]
+    float *k_scales, *v_scales; // e4m3: [num_pages][page_rows / block_rows][Hkv]
+    const float *table;         // [table_rows][rotary_dim]: cosines, then sines
+    const int32_t *positions;   // [B][k] or nullptr (context length + j)
+    const int32_t *new_counts;  // [B] or nullptr (k)
+    const int32_t *context_lengths;
+    const int32_t *page_table;  // [B][max_pages]
+    int *dev_status;
+    int table_rows, rotary_dim, interleaved;
+    int batch, k, q_heads, kv_heads, head_dim;
+    int max_pages, page_rows, num_pages, block_rows;
+};
+
+// Everything an attention over e4m3 pages needs.
+struct PagedFp8Params {
+    uint16_t *out;              // bf16 [B][k][Hq][D]
+    const uint16_t *q;          // bf16 [B][k][Hq][D]
+    const uint8_t *k_pages, *v_pages;   // e4m3 [num_pages][page_rows][Hkv][D]
+    const float *k_scales, *v_scales;   // [num_pages][page_rows / block_rows][Hkv]
+    const int32_t *page_table;  // [B][max_pages]
+    const int32_t *context_lengths;
+    void *workspace;
+    int *dev_status;
+    int max_pages, page_rows, num_pages, block_rows;
+    int batch, k, q_heads, kv_heads, head_dim, group;
+    int capacity;               // max_pages * page_rows
+    int window;                 // 0: every position up to the query's own
+    float scale_log2;           // softmax scale * log2(e)
+};
+
 // Host-side count of kernel launches (carat_kernel_launches).
 void count_launches(int n);
+
+// Device address of the current device's status word, and its SM count (a
+// GB300's 152 when no device can be queried).
+int *device_status_ptr();
+int device_sm_count();
 
 // ---------------------------------------------------------------------------
 // Host-side launchers (defined in the .cu files)
@@ -200,6 +242,15 @@ cudaError_t launch_ring_append(const AppendParams &p, cudaStream_t stream);
 cudaError_t launch_ring_append_fp8(const AppendParams &p, cudaStream_t stream);
 cudaError_t launch_ring_rollback(const AppendParams &p, const int32_t *accepted,
                                  cudaStream_t stream);
+
+// Rotary paged appends (paged_rope.cu) and the attention over e4m3 pages
+// (paged_fp8_attention.cu).
+bool rope_shape_ok(int head_dim);
+cudaError_t launch_rope_append(const RopeParams &p, cudaStream_t stream);
+cudaError_t launch_rope_append_fp8(const RopeParams &p, cudaStream_t stream);
+bool paged_fp8_supported(int head_dim);
+size_t paged_fp8_workspace(int batch, int proposal_count, int q_heads, int kv_heads, int head_dim);
+cudaError_t launch_paged_fp8_attention(const PagedFp8Params &p, cudaStream_t stream);
 
 // Tensor-core path (attention_tc.cu): rows per tile (16, 32 or 64) for a
 // group size and proposal count, CTAs resident per SM, whether the shape is

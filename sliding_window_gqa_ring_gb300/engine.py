@@ -204,14 +204,37 @@ class SharedPool:
         shape = (self.num_pages, self.page_bytes // row_bytes, kv_heads, head_dim)
         return self.k.view(shape), self.v.view(shape)
 
+    def pages_fp8(self, kv_heads: int, head_dim: int):
+        """The same pages as uint8 (e4m3) [num_pages][page_rows][kv_heads][head_dim]."""
+        row_bytes = kv_heads * head_dim
+        if self.page_bytes % row_bytes or (self.page_bytes // row_bytes) % 128:
+            raise ValueError("a page must hold a multiple of 128 rows")
+        shape = (self.num_pages, self.page_bytes // row_bytes, kv_heads, head_dim)
+        return self.k.view(torch.uint8).view(shape), self.v.view(torch.uint8).view(shape)
+
+
+def rotary_table(rows: int, rotary_dim: int, base: float = 10000.0, device="cuda"):
+    """fp32 [rows][rotary_dim] for the rotary appends: cosines then sines of
+    position * base^(-2 i / rotary_dim).  The angles are formed in 64 bits: in
+    32 a far position's angle would be off by whole thousandths of a turn."""
+    half = rotary_dim // 2
+    freq = base ** (-torch.arange(half, dtype=torch.float64, device=device) / half)
+    angle = torch.arange(rows, dtype=torch.float64, device=device)[:, None] * freq
+    return torch.cat([angle.cos(), angle.sin()], 1).to(torch.float32).contiguous()
+
 
 class PagedGlobalLayer:
     """A global layer whose caches are pages of a SharedPool: request b's
-    position t is row t % page_rows of page page_table[b][t // page_rows]."""
+    position t is row t % page_rows of page page_table[b][t // page_rows].
+
+    cos_sin (rotary_table): queries and new keys arrive unrotated and are
+    rotated on their way; step() is then the rotary append and the attention
+    over the pages (two calls) instead of one fused call."""
 
     def __init__(self, pool: SharedPool, page_table: torch.Tensor, *, q_heads: int = 16,
                  kv_heads: int = 2, head_dim: int = 512, max_proposals: int = 4,
-                 scale: float | None = None):
+                 scale: float | None = None, cos_sin=None, interleaved: bool = False):
+        self.cos_sin, self.interleaved = cos_sin, interleaved
         self.key_pages, self.value_pages = pool.pages(kv_heads, head_dim)
         self.page_rows = self.key_pages.shape[1]
         self.page_table = page_table
@@ -223,18 +246,101 @@ class PagedGlobalLayer:
         self.workspace = carat.workspace_tensor(
             max(carat.global_workspace_bytes(batch, p, q_heads, kv_heads, head_dim, self.capacity)
                 for p in range(1, max_proposals + 1)), self.device)
+        if cos_sin is not None:
+            self.rotated = torch.empty(batch * max_proposals * q_heads * head_dim,
+                                       dtype=torch.bfloat16, device=self.device)
 
-    def append(self, k_new, v_new, context_lengths, stream=None):
+    def append(self, k_new, v_new, context_lengths, stream=None, new_counts=None):
+        """Write rows (a prompt's after prefill, say); rotated when the layer
+        has a rotary table."""
+        if self.cos_sin is not None:
+            carat.carat_paged_rope_append(self.key_pages, self.value_pages, self.page_table, k_new,
+                                          v_new, context_lengths, cos_sin=self.cos_sin,
+                                          interleaved=self.interleaved, new_counts=new_counts,
+                                          stream=stream)
+            return
+        if new_counts is not None:
+            raise ValueError("new_counts needs a layer with a rotary table")
         carat.carat_paged_append(self.key_pages, self.value_pages, self.page_table, k_new, v_new,
                                  context_lengths, stream=stream)
 
     def step(self, queries, k_new, v_new, context_lengths, out=None, stream=None):
         if out is None:
             out = torch.empty(queries.shape, dtype=torch.float32, device=self.device)
+        if self.cos_sin is not None:
+            rotated = self.rotated[:queries.numel()].view(queries.shape)
+            carat.carat_paged_rope_append(self.key_pages, self.value_pages, self.page_table, k_new,
+                                          v_new, context_lengths, cos_sin=self.cos_sin,
+                                          interleaved=self.interleaved, queries=queries,
+                                          queries_out=rotated, stream=stream)
+            carat.carat_global_verify_attention_paged(
+                out, rotated, self.key_pages, self.value_pages, self.page_table, context_lengths,
+                scale=self.scale, workspace=self.workspace, stream=stream)
+            return out
         carat.carat_global_append_verify_attention_paged(
             out, queries, self.key_pages, self.value_pages, self.page_table, k_new, v_new,
             context_lengths, scale=self.scale, workspace=self.workspace, stream=stream)
         return out
+
+
+class Fp8PagedLayer:
+    """A layer whose caches are e4m3 pages with one scale per block of
+    `block_rows` tokens and KV head, global (window 0) or sliding (window w).
+    Queries and new keys arrive unrotated; step() is the rotary append
+    (quantising on the way) and the attention over the pages.  Outputs are
+    bf16.  The pages come from a SharedPool (a page of the pool holds twice the
+    rows it holds in bf16)."""
+
+    out_dtype = torch.bfloat16
+
+    def __init__(self, pool: SharedPool, page_table: torch.Tensor, cos_sin: torch.Tensor, *,
+                 q_heads: int = 16, kv_heads: int = 2, head_dim: int = 512,
+                 max_proposals: int = 4, block_rows: int = 32, window: int = 0,
+                 scale: float | None = None, interleaved: bool = False):
+        self.key_pages, self.value_pages = pool.pages_fp8(kv_heads, head_dim)
+        num_pages, self.page_rows = self.key_pages.shape[:2]
+        if block_rows not in (16, 32, 64, 128):
+            raise ValueError("block_rows must be 16, 32, 64 or 128")
+        self.page_table, self.cos_sin, self.interleaved = page_table, cos_sin, interleaved
+        self.q_heads, self.kv_heads, self.head_dim, self.window = q_heads, kv_heads, head_dim, window
+        self.capacity = page_table.shape[1] * self.page_rows
+        self.scale = (1.0 / math.sqrt(head_dim)) if scale is None else scale
+        self.device = pool.device
+        shape = (num_pages, self.page_rows // block_rows, kv_heads)
+        self.k_scales = torch.ones(shape, dtype=torch.float32, device=self.device)
+        self.v_scales = torch.ones(shape, dtype=torch.float32, device=self.device)
+        batch = page_table.shape[0]
+        self.rotated = torch.empty(batch * max_proposals * q_heads * head_dim,
+                                   dtype=torch.bfloat16, device=self.device)
+        self.workspace = carat.workspace_tensor(
+            max(carat.paged_fp8_workspace_bytes(batch, p, q_heads, kv_heads, head_dim,
+                                                self.capacity)
+                for p in range(1, max_proposals + 1)), self.device)
+
+    def append(self, k_new, v_new, context_lengths, stream=None, new_counts=None, queries=None,
+               queries_out=None):
+        """Write rows (a prompt's after prefill, say): new_counts[b] of request
+        b's, or all of them."""
+        carat.carat_paged_rope_append_fp8(
+            self.key_pages, self.value_pages, self.k_scales, self.v_scales, self.page_table, k_new,
+            v_new, context_lengths, cos_sin=self.cos_sin, interleaved=self.interleaved,
+            queries=queries, queries_out=queries_out, new_counts=new_counts, stream=stream)
+
+    def attend(self, queries, context_lengths, out=None, stream=None):
+        """Attention of rotated queries over rows already stored."""
+        if out is None:
+            out = torch.empty(queries.shape, dtype=torch.bfloat16, device=self.device)
+        carat.carat_paged_verify_attention_fp8(
+            out, queries, self.key_pages, self.value_pages, self.k_scales, self.v_scales,
+            self.page_table, context_lengths, scale=self.scale, window=self.window,
+            workspace=self.workspace, stream=stream)
+        return out
+
+    def step(self, queries, k_new, v_new, context_lengths, out=None, stream=None):
+        rotated = self.rotated[:queries.numel()].view(queries.shape)
+        self.append(k_new, v_new, context_lengths, queries=queries, queries_out=rotated,
+                    stream=stream)
+        return self.attend(rotated, context_lengths, out=out, stream=stream)
 
 
 class GlobalLayer:
@@ -387,8 +493,8 @@ def stage_global(w: synth.Workload, layer_index: int, layer: GlobalLayer, reques
 # ---------------------------------------------------------------------------
 
 class DecodeStep:
-    """One decode / verify step over a list of layers (SlidingLayer or
-    GlobalLayer), each with its own queries and new K/V rows.
+    """One decode / verify step over a list of layers (sliding, global or paged),
+    each with its own queries and new K/V rows.
 
     run()        -- every layer's fused append+attention on the current stream
                     (inputs already on the device).
@@ -407,14 +513,15 @@ class DecodeStep:
                     launch of the whole step from the host).
 
     `inputs[i]` = (queries, k_new, v_new, context_lengths) device tensors of
-    layer i; `outputs[i]` its fp32 output tensor.
+    layer i; `outputs[i]` its output tensor (fp32, or the layer's out_dtype).
     """
 
     def __init__(self, layers, inputs, outputs=None):
         self.layers = list(layers)
         self.inputs = [tuple(x) for x in inputs]
-        self.outputs = outputs or [torch.empty(q.shape, dtype=torch.float32, device=q.device)
-                                   for (q, _, _, _) in self.inputs]
+        self.outputs = outputs or [
+            torch.empty(q.shape, dtype=getattr(layer, "out_dtype", torch.float32), device=q.device)
+            for layer, (q, _, _, _) in zip(self.layers, self.inputs)]
         self.device = self.inputs[0][0].device
         self.copy_stream = torch.cuda.Stream(device=self.device)      # host -> device
         self.copy_out_stream = torch.cuda.Stream(device=self.device)  # device -> host
