@@ -1,108 +1,1128 @@
 // paged_fp8_attention.cu -- decode / verify attention over paged e4m3 caches
-// with one scale per block of tokens and KV head.
+// with one scale per block of tokens and KV head, on the 5th-generation
+// tensor cores with 8-bit operands.
 //
 // For query row (j, h) of request b at position p = context_length + j, over
-// the positions t in [max(0, p - window + 1), p]:
-//     s_t = scale * ks[t] * sum_d q_d e4m3(k_td),
+// the positions t in [max(0, p - window + 1), p] (log2 units throughout):
+//     s_t = scale * log2(e) * ks[t] * sum_d q_d e4m3(k_td),
 //     out_d = sum_t 2^(s_t - m) vs[t] e4m3(v_td) / sum_t 2^(s_t - m)
-// with ks, vs the scales of the token's block.  One CTA per row: eight warps
-// take every eighth key with a running maximum and sum each, merged at the end.
+// with ks, vs the scales of the token's block.
+//
+// Bytes as operands.  A decode step reads each cached byte once and does few
+// operations with it, so the cache has to reach the tensor core as it lies in
+// memory: K and V tiles of 128 keys go from HBM through TMA into shared memory
+// and from there straight into tcgen05.mma (kind::f8f6f4), with no thread
+// touching them.  The other operands are split exactly into 8-bit pieces that
+// stand side by side as more columns of the same product:
+//   * a query row, scaled by a power of two so its largest element lies in
+//     [128, 256), is hi + lo / 16, both e4m3: four bits each and a sign make
+//     up a bf16 value's eight, down to 2^-13 of the row's largest element
+//     (smaller elements are rounded to 2^-21 of it);
+//   * a weight w_t = 2^(s_t - m) vs[t], rounded to f16 (its 2^-11 is below the
+//     output's own bf16 rounding), is w1 + w2 / 8 + w3 / 64, all e5m2: three
+//     bits each and two signs make up f16's eleven.
+// Keys are the M dimension of both products:
+//     S^T [128 keys x 2N]  = K_tile [128 x D] . [q_hi | q_lo]^T      (K-major A)
+//     O^T [128 d x 3N]    += V_tile^T [d x 128 keys] . [w1 | w2 | w3]^T (MN-major A)
+// for N = 16 or 32 rows; more rows (up to 128) are cut into row groups of 32.
+// The scales cost nothing in the products: thread t of the softmax owns key t,
+// so ks[t] is one factor of its scores, and vs[t] one of its weights.
+//
+// The running maximum m is that of s_t + log2 vs[t] (by vs's exponent), not of
+// s_t: it bounds the weights that are really rounded, whatever the scales'
+// range.  It moves only when exceeded by more than kSlack, and the sum
+// of 2^(s_t - m) is taken over the rounded weights, in fp32.
+//
+// Schedule: stream-K.  All (request, KV head) units' tiles form one sequence,
+// cut into ranges of equal cost, one per CTA (one CTA per SM; with G row groups
+// CTAs G r .. G r + G - 1 walk range r together, one group each, so the tiles
+// they share come from L2).  A segment that covers a whole unit writes its
+// output; the others leave a partial (max, sum, O) for the merge launch, which
+// finds them through a table with one entry per unit.
+//
+// Warps: 0 loads tiles (TMA), 1 issues the products, 2 fetches the tiles' block
+// scales ahead of the softmax, 4-11 run it: warps 4-7 own the first half of
+// the rows, 8-11 the second, thread t of each half key t of the tile.  Every
+// wait is bounded.
+#include <atomic>
+
 #include "carat_internal.cuh"
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include "tc_common.cuh"
+#include "tma_host.h"
+
 namespace carat {
 namespace {
 
-constexpr int kWarps = 8;
+constexpr int kKeys = 128;                 // keys of a tile
+constexpr int kStage = kKeys * 128;        // bytes of a stage: 128 keys x 128 d
+constexpr int kSoftWarps = 8;
+constexpr int kThreads = 12 * 32;
+constexpr int kSlots = 4;                  // tiles whose scales are fetched ahead
+constexpr int kMaxPieces = 256;            // pieces of one unit
+constexpr uint32_t kFull = 0xffffffffu;
+constexpr float kSlack = 8.f;
+// Weights carry this factor: 2^kSlack * 2 * 64 = 2^15 fits e5m2 and f16, and a
+// weight 2^-29 of the largest is still rounded to within its own half.
+constexpr float kWeight = 64.f;
 
-__device__ __forceinline__ void e4m3x4_to_f32(uint32_t w, float *f) {
-    uint32_t lo, hi;
-    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
-        "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
-        : "=r"(lo), "=r"(hi)
-        : "r"(w));
-    const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&lo));
-    const float2 b = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
-    f[0] = a.x, f[1] = a.y, f[2] = b.x, f[3] = b.y;
+template <int D, int N>
+struct Lay {
+    static constexpr int KS = D / 128;                // stages of a K (or V) tile
+    static constexpr int NS = D == 512 && N == 32 ? 11 : 12;
+    static constexpr int kQBlock = 2 * N * 128;       // 128 d of the query pieces
+    static constexpr int kOffQ = NS * kStage;
+    static constexpr int kOffP = kOffQ + KS * kQBlock;
+    static constexpr int kOffRed = kOffP + 3 * N * 128;
+    // floats: the four key quarters' maxima or sums per row, the running
+    // maxima, the rescale factors, the query scales of two segments
+    static constexpr int kRedM = 4 * N, kRedAlpha = 5 * N, kRedQ = 6 * N, kRedRow = 8 * N;
+    static constexpr int kRedFloats = 10 * N;         // last 2 N: output rows (int)
+    static constexpr int kOffSc = kOffRed + kRedFloats * 4;      // [kSlots][2][8] scales
+    static constexpr int kOffBar = kOffSc + kSlots * 64;
+    static constexpr int kBars = 2 * NS + 6 + 2 * kSlots;
+    static constexpr int kOffMisc = kOffBar + kBars * 8;
+    static constexpr int kBytes = kOffMisc + 128;
+    static constexpr int kAlloc = kBytes + 1024;
+    static constexpr int kTmemO = 4 * N;              // two S^T buffers of 2 N columns first
+    static constexpr int kTmem = 4 * N + KS * 3 * N <= 256 ? 256 : 512;
+    static_assert(4 * N + KS * 3 * N <= kTmem, "tensor memory");
+    static_assert(kAlloc <= 232448, "shared memory");
+    // the softmax zeroes V rows while the tile's stages are all resident, with the
+    // next tile's K in front of them
+    static_assert(NS >= 2 * KS, "the ring holds a K and a V tile");
+    static_assert(kOffQ % 1024 == 0 && kOffP % 1024 == 0 && kQBlock % 1024 == 0, "swizzle");
+};
+
+struct Plan {
+    int groups;     // row groups of a unit
+    int ranges;     // ranges of the tile sequence (grid = ranges * groups)
+    float2 *part_ml;    // [2 * grid][N] (max, sum)
+    float *part_o;      // [2 * grid][N][D]
+    int4 *units;        // [B * Hkv * groups] first range, pieces (0: whole), first slot
+};
+
+// Tiles of request b: [first, first + count) of its 128-position tiles; 0 when
+// its context length is out of range.
+__device__ __forceinline__ int request_tiles(const PagedFp8Params &p, long long ctx, int *first) {
+    *first = 0;
+    if (ctx < 0 || ctx + p.k > p.capacity) return 0;
+    if (p.window > 0 && ctx + 1 > p.window) *first = (int)((ctx + 1 - p.window) / kKeys);
+    return (int)((ctx + p.k - 1) / kKeys) - *first + 1;
 }
 
-template <int D>
-__global__ void __launch_bounds__(kWarps * 32) paged_fp8_simple_kernel(const PagedFp8Params p) {
-    constexpr int E = D / 32;   // elements a lane holds
-    const int h = blockIdx.x, j = blockIdx.y, b = blockIdx.z;
+// What a CTA's roles share besides the barriers.
+struct Shared {
+    uint32_t tmem;
+    int abort_flag;
+    int b0, c0, off0;       // first segment: request, KV head, tiles of the unit before it
+    int charge;             // cost of a unit besides its tiles
+    long long s, e;         // the CTA's tiles of the sequence
+    long long len;          // cost of a range
+    long long ucost0;       // cost position of the first segment's unit
+};
+
+struct Segment {
+    int b, c;
+    long long ctx;
+    int first, ntiles;      // the unit's tiles
+    int x0, x1;             // those of this segment
+    bool opens;             // the segment opens the CTA's range
+    long long ucost;
+};
+
+// Walks a CTA's range as segments, one per unit it touches.
+struct SegIter {
+    long long pos, end, start, ucost, ctx;
+    int b, c, off, first, ntiles, charge;
+
+    __device__ void init(const PagedFp8Params &p, const volatile Shared *sh) {
+        pos = start = sh->s;
+        end = sh->e;
+        b = sh->b0;
+        c = sh->c0;
+        off = sh->off0;
+        ucost = sh->ucost0;
+        charge = sh->charge;
+        ntiles = 0;
+        if (pos < end) {
+            ctx = p.context_lengths[b];
+            ntiles = request_tiles(p, ctx, &first);
+        }
+    }
+
+    __device__ bool next(const PagedFp8Params &p, Segment &sg) {
+        if (pos >= end || off >= ntiles) return false;
+        const long long left = end - pos;
+        const int len = (long long)(ntiles - off) < left ? ntiles - off : (int)left;
+        sg.b = b;
+        sg.c = c;
+        sg.ctx = ctx;
+        sg.first = first;
+        sg.ntiles = ntiles;
+        sg.x0 = off;
+        sg.x1 = off + len;
+        sg.opens = pos == start;
+        sg.ucost = ucost;
+        pos += len;
+        off += len;
+        if (off == ntiles && pos < end) {
+            off = 0;
+            ucost += ntiles + charge;
+            if (++c == p.kv_heads) {
+                c = 0;
+                ntiles = 0;
+                while (ntiles == 0 && b + 1 < p.batch) {
+                    ++b;
+                    ctx = p.context_lengths[b];
+                    ntiles = request_tiles(p, ctx, &first);
+                }
+            }
+        }
+        return true;
+    }
+};
+
+__device__ __forceinline__ long long warp_sum(long long v) {
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
+    return v;
+}
+
+// Warp 0: this CTA's range.  A unit costs its tiles and `charge` more (its
+// segment boundary: a new Q, an output or partial); tile o of the unit that
+// begins at cost U sits at U + charge + o, and tile t belongs to range
+// floor(cost(t) / len).  A call with fewer tiles than ranges charges nothing,
+// and every tile has a range to itself.
+__device__ __noinline__ void locate_range(const PagedFp8Params &p, int ranges, int rix, int lane,
+                                          Shared *sh) {
+    long long tiles = 0, units = 0;
+#pragma unroll 1
+    for (int b = lane; b < p.batch; b += 32) {
+        int first;
+        const int v = request_tiles(p, p.context_lengths[b], &first);
+        tiles += v;
+        units += v > 0 ? 1 : 0;
+    }
+    tiles = warp_sum(tiles) * p.kv_heads;
+    units = warp_sum(units) * p.kv_heads;
+    const int charge = tiles >= ranges ? 1 : 0;
+    const long long cost = tiles + charge * units;
+    long long len = (cost + ranges - 1) / ranges;
+    if (len < charge + 1) len = charge + 1;
+    // The first tiles at cost positions >= X0 and >= X1 (none: `tiles`).
+    const long long X0 = rix * len, X1 = rix + 1 < ranges ? X0 + len : cost;
+    long long at0 = tiles, at1 = tiles, u0 = 0;
+    int b0 = 0, c0 = 0, off0 = 0;
+    long long cum_cost = 0, cum_tiles = 0;
+#pragma unroll 1
+    for (int base = 0; base < p.batch && cum_cost <= X1; base += 32) {
+        const int b = base + lane;
+        int v = 0, first;
+        if (b < p.batch) v = request_tiles(p, p.context_lengths[b], &first);
+        const long long per = v + charge;
+        const long long vc = v > 0 ? p.kv_heads * per : 0, vt = (long long)p.kv_heads * v;
+        long long ic = vc, it = vt;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long yc = __shfl_up_sync(kFull, ic, o), yt = __shfl_up_sync(kFull, it, o);
+            if (lane >= o) ic += yc, it += yt;
+        }
+        const long long lo = cum_cost + ic - vc, tlo = cum_tiles + it - vt;
+#pragma unroll 1
+        for (int which = 0; which < 2; ++which) {
+            const long long X = which ? X1 : X0;
+            const bool mine = vc > 0 && X >= lo && X < lo + vc;
+            const unsigned hit = __ballot_sync(kFull, mine);
+            if (!hit) continue;
+            const int src = __ffs(hit) - 1;
+            long long at = 0, uc = 0;
+            int j = 0, o = 0;
+            if (mine) {
+                j = (int)((X - lo) / per);
+                const long long r = X - lo - j * per;
+                o = r <= charge ? 0 : (int)(r - charge);
+                at = tlo + (long long)j * v + o;
+                uc = lo + j * per;
+            }
+            at = __shfl_sync(kFull, at, src);
+            if (which) {
+                at1 = at;
+            } else {
+                at0 = at;
+                u0 = __shfl_sync(kFull, uc, src);
+                b0 = base + src;
+                c0 = __shfl_sync(kFull, j, src);
+                off0 = __shfl_sync(kFull, o, src);
+            }
+        }
+        cum_cost += __shfl_sync(kFull, ic, 31);
+        cum_tiles += __shfl_sync(kFull, it, 31);
+    }
+    if (lane == 0) {
+        sh->s = at0;
+        sh->e = at1;
+        sh->len = len;
+        sh->charge = charge;
+        sh->b0 = b0;
+        sh->c0 = c0;
+        sh->off0 = off0;
+        sh->ucost0 = u0;
+    }
+    __syncwarp();
+}
+
+// Wait for a barrier phase; false after two seconds, or when another role gave
+// up (which is recorded and reported once).
+__device__ __forceinline__ bool await(uint64_t *bar, uint32_t parity, volatile int *abort_flag,
+                                      int *dev_status) {
+    if (tc::mbar_try_wait(bar, parity)) return true;
+    const uint64_t t0 = tc::globaltimer_ns();
+    for (uint32_t round = 1;; ++round) {
+#pragma unroll 1
+        for (int i = 0; i < 32; ++i)
+            if (tc::mbar_try_wait(bar, parity)) return true;
+        if (*abort_flag) return false;
+        if (tc::wait_expired(t0, round, 2000000000ull)) {
+            *abort_flag = 1;
+            set_status(dev_status, CARAT_DEV_TIMEOUT);
+            return false;
+        }
+    }
+}
+
+// Barrier of the 128 threads of one half of the softmax; true when any of them
+// says so.
+__device__ __forceinline__ bool half_any(int half, bool pred) {
+    uint32_t out;
+    asm volatile(
+        "{\n\t.reg .pred pin, pout;\n\t"
+        "setp.ne.u32 pin, %1, 0;\n\t"
+        "bar.red.or.pred pout, %2, 128, pin;\n\t"
+        "selp.u32 %0, 1, 0, pout;\n\t}"
+        : "=r"(out)
+        : "r"((uint32_t)pred), "r"(half + 1)
+        : "memory");
+    return out != 0;
+}
+
+// v[i] is this lane's value of row i; returns the row this lane ends up with,
+// whose reduction over the 32 lanes is then v[0].
+template <int NC, bool kMax>
+__device__ __forceinline__ int transpose_reduce(float (&v)[NC], int lane) {
+    int row = 0;
+#pragma unroll
+    for (int s = 0; s < 5; ++s) {
+        const int off = 16 >> s, cnt = (NC >> s) > 1 ? (NC >> s) : 1;
+        const bool upper = (lane & off) != 0;
+        if (cnt >= 2) {
+            const int h = cnt / 2;
+#pragma unroll
+            for (int i = 0; i < h; ++i) {
+                const float send = upper ? v[i] : v[i + h], keep = upper ? v[i + h] : v[i];
+                const float got = __shfl_xor_sync(kFull, send, off);
+                v[i] = kMax ? fmaxf(keep, got) : keep + got;
+            }
+            if (upper) row += h;
+        } else {
+            const float got = __shfl_xor_sync(kFull, v[0], off);
+            v[0] = kMax ? fmaxf(v[0], got) : v[0] + got;
+        }
+    }
+    return row;
+}
+
+template <int NC>
+__device__ __forceinline__ void tmem_load(uint32_t addr, uint32_t (&r)[NC]) {
+    if constexpr (NC == 16) tc::tmem_ld16(addr, r);
+    else tc::tmem_ld8(addr, r);
+}
+
+template <int NC>
+__device__ __forceinline__ void tmem_store(uint32_t addr, const uint32_t (&r)[NC]) {
+    if constexpr (NC == 16) tc::tmem_st16(addr, r);
+    else tc::tmem_st8(addr, r);
+}
+
+__device__ __forceinline__ uint32_t low_mask(int n) { return n >= 32 ? kFull : (1u << n) - 1u; }
+
+__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+__device__ __forceinline__ float2 e4m3x2_to_f32(uint32_t b) {
+    uint32_t h;
+    asm("{\n\t.reg .b16 x;\n\tcvt.u16.u32 x, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, x;\n\t}"
+        : "=r"(h)
+        : "r"(b));
+    return __half22float2(*reinterpret_cast<const __half2 *>(&h));
+}
+
+// Two f16 values -> their nearest e5m2 bytes (first in the low one).
+__device__ __forceinline__ uint32_t e5m2x2(__half2 h) {
+    uint16_t r;
+    asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;"
+        : "=h"(r)
+        : "r"(*reinterpret_cast<const uint32_t *>(&h)));
+    return r;
+}
+
+// e5m2 is f16's upper byte.
+__device__ __forceinline__ __half2 e5m2x2_to_f16x2(uint32_t b) {
+    const uint32_t w = __byte_perm(b, 0, 0x1404);
+    return *reinterpret_cast<const __half2 *>(&w);
+}
+
+// One query row into the two pieces' rows of the Q operand (row r and N + r of
+// every 128-d block), by one warp.  Returns the factor that takes the power
+// of two out of the scores again (NaN for a row that is not finite, 0 for none).
+template <int D, int N>
+__device__ __forceinline__ float split_query(uint8_t *s_q, const uint16_t *row, int r, int lane) {
+    constexpr int E = D / 32;   // 16 or 8 elements of a lane
+    uint32_t w[E / 2];
+    uint32_t top = 0;           // largest |q|, as bits
+    if (row) {
+#pragma unroll
+        for (int i = 0; i < E / 8; ++i) {
+            const uint4 v = __ldg(reinterpret_cast<const uint4 *>(row + lane * E) + i);
+            w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
+        }
+#pragma unroll
+        for (int i = 0; i < E / 2; ++i)
+            top = max(top, max((w[i] << 16) & 0x7fffffffu, w[i] & 0x7fff0000u));
+    } else {
+#pragma unroll
+        for (int i = 0; i < E / 2; ++i) w[i] = 0;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(kFull, top, o));
+    int s = 7 - ((int)(top >> 23) - 127);
+    s = min(s, 100);            // zero and subnormal rows
+    const float up = __int_as_float((127 + s) << 23);
+    uint32_t hi[E / 4], lo[E / 4];
+#pragma unroll
+    for (int i = 0; i < E / 4; ++i) {
+        uint32_t h2[2], l2[2];
+#pragma unroll
+        for (int z = 0; z < 2; ++z) {
+            const float a = bf16lo(w[2 * i + z]) * up, b = bf16hi(w[2 * i + z]) * up;
+            h2[z] = e4m3x2(a, b);
+            const float2 f = e4m3x2_to_f32(h2[z]);
+            l2[z] = e4m3x2((a - f.x) * 16.f, (b - f.y) * 16.f);
+        }
+        hi[i] = h2[0] | (h2[1] << 16);
+        lo[i] = l2[0] | (l2[1] << 16);
+    }
+    uint8_t *block = s_q + (lane * E / 128) * (2 * N * 128);
+    const int byte = lane * E % 128, chunk = byte / 16;
+    uint8_t *ph = block + r * 128 + ((chunk ^ (r & 7)) << 4) + byte % 16;
+    uint8_t *pl = ph + N * 128;   // N is a multiple of 8: the same swizzle
+    if constexpr (E == 16) {
+        *reinterpret_cast<uint4 *>(ph) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        *reinterpret_cast<uint4 *>(pl) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    } else {
+        *reinterpret_cast<uint2 *>(ph) = make_uint2(hi[0], hi[1]);
+        *reinterpret_cast<uint2 *>(pl) = make_uint2(lo[0], lo[1]);
+    }
+    if (!row) return 0.f;
+    return top >= 0x7f800000u ? __int_as_float(0x7fc00000) : __int_as_float((127 - s) << 23);
+}
+
+template <int D, int N>
+__global__ void __launch_bounds__(kThreads, 1)
+    paged_fp8_kernel(const PagedFp8Params p, const Plan plan,
+                     const __grid_constant__ CUtensorMap map_k,
+                     const __grid_constant__ CUtensorMap map_v) {
+    using L = Lay<D, N>;
+    constexpr int KS = L::KS, NS = L::NS, NC = N / 2;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const size_t row = ((size_t)b * p.k + j) * p.q_heads + h;
+    const int rix = blockIdx.x / plan.groups, rg = blockIdx.x % plan.groups;
+
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + L::kOffBar);
+    uint64_t *empty = full + NS;
+    uint64_t *s_full = empty + NS;      // [2] scores of a tile ready
+    uint64_t *p_full = s_full + 2;      // weights of a tile written
+    uint64_t *o_done = s_full + 3;      // PV product of a tile done
+    uint64_t *q_full = s_full + 4;      // queries of a segment written
+    uint64_t *fin = s_full + 5;
+    uint64_t *sc_full = s_full + 6;     // [kSlots] scales of a tile fetched
+    uint64_t *sc_empty = sc_full + kSlots;
+    uint8_t *s_q = smem + L::kOffQ;
+    uint8_t *s_p = smem + L::kOffP;
+    float *red = reinterpret_cast<float *>(smem + L::kOffRed);
+    float *s_sc = reinterpret_cast<float *>(smem + L::kOffSc);
+    Shared *sh = reinterpret_cast<Shared *>(smem + L::kOffMisc);
+    volatile int *abort_flag = &sh->abort_flag;
+    int *status = p.dev_status;
+
+    // the merge launch may start once every CTA of this grid runs
+    if (threadIdx.x == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+    // Pool row of a tile's first position; -1 for a page outside the pool.
+    const int pages_shift_tiles = p.page_rows / kKeys;   // tiles of a page
+    auto tile_row = [&](int page, int tile) -> long long {
+        if (page < 0 || page >= p.num_pages) return -1;
+        return (long long)page * p.page_rows + (long long)(tile % pages_shift_tiles) * kKeys;
+    };
+
+    if (warp == 0) {
+        // ------------------------------------------------------------ tiles
+        if (lane == 0) {
+            tc::tma_prefetch_map(&map_k);
+            tc::tma_prefetch_map(&map_v);
+            for (int i = 0; i < NS; ++i) {
+                tc::mbar_init(&full[i], 1);
+                tc::mbar_init(&empty[i], 1);
+            }
+            tc::mbar_init(&s_full[0], 1);
+            tc::mbar_init(&s_full[1], 1);
+            tc::mbar_init(p_full, kSoftWarps);
+            tc::mbar_init(o_done, 1);
+            tc::mbar_init(q_full, kSoftWarps);
+            tc::mbar_init(fin, 1);
+            for (int i = 0; i < kSlots; ++i) {
+                tc::mbar_init(&sc_full[i], 1);
+                tc::mbar_init(&sc_empty[i], kSoftWarps);
+            }
+            sh->abort_flag = 0;
+            tc::fence_mbar_init();
+        }
+        locate_range(p, plan.ranges, rix, lane, sh);
+        __threadfence_block();
+        __syncwarp();
+        // the others wait for this; the loads need not wait for them
+        asm volatile("bar.arrive 3, %0;" ::"n"(kThreads) : "memory");
+        if (lane == 0) {
+            // K and V rows are read once, unless row groups share them
+            const uint64_t pol = plan.groups > 1 ? tc::l2_evict_normal_policy()
+                                                 : tc::l2_evict_first_policy();
+            SegIter it;
+            it.init(p, sh);
+            Segment sg;
+            bool have = it.next(p, sg);
+            int x = have ? sg.x0 : 0;
+            int pi = -1, page = 0, pi_next = -1, page_next = 0;   // a page read ahead
+            uint32_t cnt = 0;
+            bool alive = true;
+            auto issue = [&](const CUtensorMap *map, long long row, int c) {
+                for (int ks = 0; ks < KS && alive; ++ks) {
+                    const int s = cnt % NS;
+                    if (cnt >= NS &&
+                        !await(&empty[s], ((cnt / NS) & 1) ^ 1, abort_flag, status)) {
+                        alive = false;
+                        return;
+                    }
+                    tc::mbar_arrive_expect_tx(&full[s], kStage);
+                    tc::tma_load_4d(smem + s * kStage, map, 0, (int)row, ks, c, &full[s], pol);
+                    ++cnt;
+                }
+            };
+            long long prev_row = 0;
+            int prev_c = 0;
+            bool prev = false;
+            // K of a tile before V of the one in front of it
+            while (alive) {
+                long long row = 0;
+                int c = 0;
+                const bool cur = have;
+                if (have) {
+                    const int tile = sg.first + x, want = tile / pages_shift_tiles;
+                    if (want != pi) {
+                        page = want == pi_next
+                                   ? page_next
+                                   : p.page_table[(size_t)sg.b * p.max_pages + want];
+                        pi = want;
+                        pi_next = want + 1;
+                        if (pi_next < p.max_pages)
+                            page_next = p.page_table[(size_t)sg.b * p.max_pages + pi_next];
+                        else
+                            pi_next = -1;
+                    }
+                    row = tile_row(page, tile);
+                    if (row < 0) {   // loads the zero fill past the pool's end
+                        set_status(status, CARAT_DEV_BAD_CACHE_ID);
+                        row = (long long)p.num_pages * p.page_rows;
+                    }
+                    c = sg.c;
+                    issue(&map_k, row, c);
+                    if (++x == sg.x1) {
+                        const int b_was = sg.b;
+                        have = it.next(p, sg);
+                        x = have ? sg.x0 : 0;
+                        if (have && sg.b != b_was) pi = pi_next = -1;
+                    }
+                }
+                if (prev) issue(&map_v, prev_row, prev_c);
+                prev = cur;
+                prev_row = row;
+                prev_c = c;
+                if (!cur) break;
+            }
+            if (!alive || *abort_flag)
+                // a role stopped early: the copies in flight land first
+                for (uint32_t i = cnt > (uint32_t)NS ? cnt - NS : 0; i < cnt; ++i)
+                    tc::mbar_wait(&full[i % NS], (i / NS) & 1, 100000000ull);
+        }
+        __syncwarp();
+    } else {
+        if (warp == 1) {
+            tc::tmem_alloc(&sh->tmem, L::kTmem);
+            tc::tmem_relinquish();
+        } else if (warp >= 4) {
+            // requests rejected on the device: NaN and a status bit
+            for (int b = blockIdx.x; b < p.batch; b += gridDim.x) {
+                const long long ctx = p.context_lengths[b];
+                if (ctx >= 0 && ctx + p.k <= p.capacity) continue;
+                const int t = threadIdx.x - 128;
+                if (t == 0) set_status(status, CARAT_DEV_BAD_CONTEXT);
+                const size_t per = (size_t)p.k * p.q_heads * D / 2;
+                uint32_t *o = reinterpret_cast<uint32_t *>(p.out) + (size_t)b * per;
+                for (size_t i = t; i < per; i += kSoftWarps * 32) o[i] = 0x7fc07fc0u;
+            }
+        }
+        tc::tc_fence_before();
+        asm volatile("bar.sync 3, %0;" ::"n"(kThreads) : "memory");
+        tc::tc_fence_after();
+    }
+
+    if (warp == 1 && lane == 0) {
+        // ------------------------------------------------------------ products
+        constexpr uint32_t idesc_qk = tc::idesc_e4m3_f32(128, 2 * N, false, false);
+        constexpr uint32_t idesc_pv = tc::idesc_e4m3_f32(128, 3 * N, true, true);
+        const uint32_t tmem = sh->tmem;
+        const uint32_t q_base = tc::smem_u32(s_q), p_base = tc::smem_u32(s_p);
+        SegIter it;
+        it.init(p, sh);
+        Segment sg;
+        bool alive = true, have = it.next(p, sg);
+        int x = have ? sg.x0 : 0, si = 0;
+        uint32_t mcnt = 0, g = 0;
+        bool prev = false, prev_first = false;   // the tile whose PV product is due
+        while (alive) {
+            const bool cur = have, first = cur && x == sg.x0;
+            if (cur) {
+                // S^T[g & 1] = K . [q_hi | q_lo]^T
+                if (first && !await(q_full, si & 1, abort_flag, status)) break;
+                const uint32_t d = tmem + (g & 1) * 2 * N;
+                for (int ks = 0; ks < KS && alive; ++ks) {
+                    const int s = mcnt % NS;
+                    alive = await(&full[s], (mcnt / NS) & 1, abort_flag, status);
+                    if (!alive) break;
+                    tc::tc_fence_after();
+                    const uint32_t a = tc::smem_u32(smem + s * kStage);
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        tc::mma_f8_ss(d, tc::sdesc_sw128(a + kk * 32, 16, 1024),
+                                      tc::sdesc_sw128(q_base + ks * L::kQBlock + kk * 32, 16, 1024),
+                                      idesc_qk, (ks | kk) != 0);
+                    tc::mma_commit(&empty[s]);
+                    ++mcnt;
+                }
+                if (!alive) break;
+                tc::mma_commit(&s_full[g & 1]);
+                if (first) ++si;
+                if (++x == sg.x1) {
+                    have = it.next(p, sg);
+                    x = have ? sg.x0 : 0;
+                }
+            }
+            if (prev) {
+                // O^T += V^T . [w1 | w2 | w3]^T of the tile before
+                if (!(alive = await(p_full, (g - 1) & 1, abort_flag, status))) break;
+                tc::tc_fence_after();
+                for (int vs = 0; vs < KS && alive; ++vs) {
+                    const int s = mcnt % NS;
+                    alive = await(&full[s], (mcnt / NS) & 1, abort_flag, status);
+                    if (!alive) break;
+                    tc::tc_fence_after();
+                    const uint32_t a = tc::smem_u32(smem + s * kStage);
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        tc::mma_f8_ss(tmem + L::kTmemO + vs * 3 * N,
+                                      tc::sdesc_sw128(a + kk * 4096, kStage, 1024),
+                                      tc::sdesc_sw128(p_base + kk * 32, 16, 1024), idesc_pv,
+                                      !(prev_first && kk == 0));
+                    tc::mma_commit(&empty[s]);
+                    ++mcnt;
+                }
+                if (!alive) break;
+                tc::mma_commit(o_done);
+            }
+            if (!cur) break;
+            prev = true;
+            prev_first = first;
+            ++g;
+        }
+        if (!alive || *abort_flag) {
+            tc::mma_commit(fin);
+            tc::mbar_wait(fin, 0, 100000000ull);
+        }
+    } else if (warp == 2) {
+        // ------------------------------------------------------------ scales
+        // Two tiles at a time: lanes 0-7 the K scales and 8-15 the V scales of
+        // the first tile's (up to) eight blocks, lanes 16-31 those of the second.
+        SegIter it;
+        it.init(p, sh);
+        Segment sg;
+        bool have = it.next(p, sg);
+        int x = have ? sg.x0 : 0;
+        const int blocks = kKeys / p.block_rows, i = lane & 7;
+        const float *src = (lane & 8) ? p.v_scales : p.k_scales;
+        uint32_t g = 0;
+        bool alive = true;
+        while (have && alive) {
+            int n = 0, my_b = 0, my_c = 0, my_tile = 0;
+            for (; n < 2 && have; ++n) {
+                if (lane / 16 == n) {
+                    my_b = sg.b;
+                    my_c = sg.c;
+                    my_tile = sg.first + x;
+                }
+                if (++x == sg.x1) {
+                    have = it.next(p, sg);
+                    x = have ? sg.x0 : 0;
+                }
+            }
+            float v = 1.f;   // a page outside the pool: K and V are zeros, any scale will do
+            if (lane / 16 < n && i < blocks) {
+                const int page =
+                    p.page_table[(size_t)my_b * p.max_pages + my_tile / pages_shift_tiles];
+                const long long row = tile_row(page, my_tile);
+                if (row >= 0) v = src[(size_t)(row / p.block_rows + i) * p.kv_heads + my_c];
+            }
+            for (int z = 0; z < n; ++z, ++g) {
+                const int slot = g % kSlots;
+                alive = alive && (g < kSlots || await(&sc_empty[slot], ((g / kSlots) & 1) ^ 1,
+                                                      abort_flag, status));
+                alive = __all_sync(kFull, alive);
+                if (!alive) break;
+                if (lane / 16 == z) s_sc[slot * 16 + (lane & 15)] = v;
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(&sc_full[slot]);
+            }
+        }
+    } else if (warp >= 4) {
+        // ------------------------------------------------------------ softmax
+        const int half = (warp - 4) / 4, q4 = warp & 3;
+        const int t = q4 * 32 + lane;                  // key of the tile, or d of an O block
+        const uint32_t tmem = sh->tmem;
+        const uint32_t lanes = (uint32_t)(q4 * 32) << 16;
+        const int r0 = half * NC;                      // first row of this half
+        const int row0 = rg * N;                       // first of the unit's rows in this group
+        const int rows_here = min(N, p.group * p.k - row0);
+        const int block = t / p.block_rows;
+        float *red_max = red, *s_m = red + L::kRedM, *s_alpha = red + L::kRedAlpha;
+        float *s_qs = red + L::kRedQ;
+        int *s_row = reinterpret_cast<int *>(red + L::kRedRow);
+        const uint32_t total = (uint32_t)(sh->e - sh->s);
+
+        // A segment's queries: this half's warps take its rows in turn.
+        auto write_queries = [&](const Segment &sg, int si) {
+#pragma unroll
+            for (int i = 0; i < NC / 4; ++i) {
+                const int r = r0 + i * 4 + q4;
+                const int ur = row0 + r, j = ur / p.group;
+                const int at = r < rows_here
+                                   ? (sg.b * p.k + j) * p.q_heads + sg.c * p.group + ur - j * p.group
+                                   : -1;
+                const float f = split_query<D, N>(
+                    s_q, at >= 0 ? p.q + (size_t)at * D : nullptr, r, lane);
+                if (lane == 0) {
+                    s_qs[(si & 1) * N + r] = f * p.scale_log2;
+                    s_row[(si & 1) * N + r] = at;
+                }
+            }
+            tc::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(q_full);
+        };
+
+        SegIter it;
+        it.init(p, sh);
+        Segment sg, nx;
+        bool alive = true, have = it.next(p, sg);
+        int si = 0;
+        uint32_t g = 0;
+        if (have) write_queries(sg, 0);
+        half_any(half, false);
+        while (have && alive) {
+            const bool have_next = it.next(p, nx);
+            const bool whole = sg.x0 == 0 && sg.x1 == sg.ntiles;
+            if (half == 0 && t == 0 && sg.x0 == 0) {
+                long long last = (sg.ucost + sh->charge + sg.ntiles - 1) / sh->len;
+                if (last > plan.ranges - 1) last = plan.ranges - 1;
+                plan.units[((size_t)sg.b * p.kv_heads + sg.c) * plan.groups + rg] =
+                    make_int4(rix, whole ? 0 : (int)(last - rix + 1), sg.opens ? 0 : 1, 0);
+            }
+            const long long lowest = p.window > 0 && sg.ctx + 1 > p.window ? sg.ctx + 1 - p.window : 0;
+            float m[NC], l[NC];
+#pragma unroll
+            for (int e = 0; e < NC; ++e) m[e] = -INFINITY, l[e] = 0.f;
+            const float *qs = s_qs + (si & 1) * N + r0;
+            for (int x = sg.x0; x < sg.x1; ++x, ++g) {
+                const bool first = x == sg.x0;
+                const int slot = g % kSlots;
+                const bool ok = __all_sync(
+                    kFull, alive && await(&s_full[g & 1], (g >> 1) & 1, abort_flag, status) &&
+                               await(&sc_full[slot], (g / kSlots) & 1, abort_flag, status));
+                float ks = 0.f, vs = 1.f;
+                if (ok) {
+                    tc::tc_fence_after();
+                    // the segment's last scores are there: its queries may go
+                    if (have_next && x + 1 == sg.x1) write_queries(nx, si + 1);
+                    ks = s_sc[slot * 16 + block];
+                    vs = s_sc[slot * 16 + 8 + block];
+                }
+                __syncwarp();
+                if (ok && lane == 0) tc::mbar_arrive(&sc_empty[slot]);
+                // Rows that see key t, at position pos: those of queries j with
+                // ctx + j >= pos > ctx + j - window.
+                const long long pos = (long long)(sg.first + x) * kKeys + t;
+                const bool data = pos >= lowest && pos < sg.ctx + p.k;
+                uint32_t seen = 0;
+                if (data) {
+                    const long long dj = pos - sg.ctx;
+                    const int jlo = dj > 0 ? (int)dj : 0;
+                    const int jhi = p.window > 0 && dj + p.window < p.k ? (int)(dj + p.window) : p.k;
+                    const int lo = min(max(jlo * p.group - row0 - r0, 0), NC);
+                    const int hi = min(max(min(jhi * p.group - row0, rows_here) - r0, 0), NC);
+                    seen = low_mask(hi) & ~low_mask(lo);
+                }
+                // the value scale: exponent and mantissa
+                const uint32_t vbits = __float_as_uint(vs);
+                const float ev = (float)((int)(vbits >> 23) - 127);
+                const float wf = __uint_as_float((vbits & 0x7fffffu) | 0x3f800000u) * kWeight;
+                const float iv = 1.f / (vs * kWeight);
+                float v[NC];
+                if (ok) {
+                    uint32_t h[NC], w[NC];
+                    const uint32_t at = tmem + (g & 1) * 2 * N + lanes + r0;
+                    tmem_load<NC>(at, h);
+                    tmem_load<NC>(at + N, w);
+                    tc::tmem_ld_wait();
+#pragma unroll
+                    for (int e = 0; e < NC; ++e) {
+                        const float s = fmaf(__uint_as_float(w[e]), 0.0625f, __uint_as_float(h[e]));
+                        v[e] = ((seen >> e) & 1u) ? fmaf(s * ks, qs[e], ev) : -INFINITY;
+                    }
+                } else {
+#pragma unroll
+                    for (int e = 0; e < NC; ++e) v[e] = -INFINITY;
+                }
+                bool need = first;
+#pragma unroll
+                for (int e = 0; e < NC; ++e) need |= v[e] > m[e] + kSlack;
+                bool rescale = false;
+                if (half_any(half, need || !ok || *abort_flag)) {
+                    float y[NC];
+#pragma unroll
+                    for (int e = 0; e < NC; ++e) y[e] = v[e];
+                    const int rr = transpose_reduce<NC, true>(y, lane);
+                    red_max[q4 * N + r0 + rr] = y[0];
+                    if (half_any(half, !ok || *abort_flag)) {
+                        alive = false;
+                        break;
+                    }
+                    bool moved = false;
+                    if (t < NC) {
+                        const int r = r0 + t;
+                        const float top = fmaxf(fmaxf(red_max[r], red_max[N + r]),
+                                                fmaxf(red_max[2 * N + r], red_max[3 * N + r]));
+                        const float old = first ? -INFINITY : s_m[r];
+                        const float now = top > old + kSlack ? top : old;
+                        s_alpha[r] = fast_exp2(old - (now == -INFINITY ? 0.f : now));
+                        s_m[r] = now;
+                        moved = now != old && old != -INFINITY;
+                    }
+                    rescale = half_any(half, moved);
+#pragma unroll
+                    for (int e = 0; e < NC; ++e) m[e] = s_m[r0 + e];
+                }
+                // The PV product before this one has read its weights and is in O.
+                if (g > 0) {
+                    alive = __all_sync(kFull, await(o_done, (g - 1) & 1, abort_flag, status));
+                    tc::tc_fence_after();
+                }
+                if (alive) {
+                    if (rescale) {
+#pragma unroll
+                        for (int e = 0; e < NC; ++e) l[e] *= s_alpha[r0 + e];
+#pragma unroll 1
+                        for (int z = 0; z < 3 * KS; ++z) {
+                            uint32_t o[NC];
+                            const uint32_t at = tmem + L::kTmemO + z * N + lanes + r0;
+                            tmem_load<NC>(at, o);
+                            tc::tmem_ld_wait();
+#pragma unroll
+                            for (int e = 0; e < NC; ++e)
+                                o[e] = __float_as_uint(__uint_as_float(o[e]) * s_alpha[r0 + e]);
+                            tmem_store<NC>(at, o);
+                        }
+                        tc::tmem_st_wait();
+                    }
+                    // weights, two rows at a time
+#pragma unroll
+                    for (int e = 0; e < NC; e += 2) {
+                        const float w0 =
+                            fast_exp2(v[e] - (m[e] == -INFINITY ? 0.f : m[e])) * wf;
+                        const float w1 =
+                            fast_exp2(v[e + 1] - (m[e + 1] == -INFINITY ? 0.f : m[e + 1])) * wf;
+                        __half2 h = __floats2half2_rn(w0, w1);
+                        const float2 f = __half22float2(h);
+                        l[e] = fmaf(f.x, iv, l[e]);
+                        l[e + 1] = fmaf(f.y, iv, l[e + 1]);
+                        const __half2 eight = __floats2half2_rn(8.f, 8.f);
+#pragma unroll
+                        for (int z = 0; z < 3; ++z) {
+                            const uint32_t b = e5m2x2(h);
+                            const int ra = z * N + r0 + e, rb = ra + 1;
+                            s_p[ra * 128 + (((t >> 4) ^ (ra & 7)) << 4) + (t & 15)] = (uint8_t)b;
+                            s_p[rb * 128 + (((t >> 4) ^ (rb & 7)) << 4) + (t & 15)] =
+                                (uint8_t)(b >> 8);
+                            h = __hmul2(__hsub2(h, e5m2x2_to_f16x2(b)), eight);
+                        }
+                    }
+                    // A tile with rows outside the request's keys: their V bytes must not
+                    // meet a zero weight (0 x NaN), so they are zeroed.
+                    const long long t0 = (long long)(sg.first + x) * kKeys;
+                    if (t0 < lowest || t0 + kKeys > sg.ctx + p.k) {
+                        const uint32_t base = g + 1 < total ? KS * (2 * g + 2) : KS * (2 * g + 1);
+                        for (int z = half; z < KS; z += 2) {
+                            const uint32_t c = base + z;
+                            const int s = c % NS;
+                            if (!await(&full[s], (c / NS) & 1, abort_flag, status)) {
+                                alive = false;
+                                break;
+                            }
+                            if (!data) {
+                                uint4 *row = reinterpret_cast<uint4 *>(smem + s * kStage + t * 128);
+#pragma unroll
+                                for (int q = 0; q < 8; ++q) row[q] = make_uint4(0, 0, 0, 0);
+                            }
+                        }
+                    }
+                }
+                alive = __all_sync(kFull, alive);
+                tc::fence_proxy_async_smem();
+                tc::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(p_full);
+            }
+            if (!alive) break;
+            // ------------------------------------------------ segment end
+            float y[NC];
+#pragma unroll
+            for (int e = 0; e < NC; ++e) y[e] = l[e];
+            const int rr = transpose_reduce<NC, false>(y, lane);
+            alive = __all_sync(kFull, await(o_done, (g - 1) & 1, abort_flag, status));
+            tc::tc_fence_after();
+            red_max[q4 * N + r0 + rr] = y[0];
+            if (half_any(half, !alive || *abort_flag)) {
+                alive = false;
+                break;
+            }
+            const size_t slot_row = ((size_t)blockIdx.x * 2 + (sg.opens ? 0 : 1)) * N + r0;
+            const int *out_row = s_row + (si & 1) * N + r0;
+#pragma unroll
+            for (int e = 0; e < NC; ++e) {
+                const int r = r0 + e;
+                l[e] = (red_max[r] + red_max[N + r]) + (red_max[2 * N + r] + red_max[3 * N + r]);
+                if (!whole && t == 0 && out_row[e] >= 0)
+                    plan.part_ml[slot_row + e] = make_float2(m[e], l[e]);
+                if (whole) l[e] = 1.f / (l[e] * kWeight);
+            }
+#pragma unroll 1
+            for (int z = 0; z < KS; ++z) {
+                uint32_t o1[NC], o2[NC], o3[NC];
+                const uint32_t at = tmem + L::kTmemO + z * 3 * N + lanes + r0;
+                tmem_load<NC>(at, o1);
+                tmem_load<NC>(at + N, o2);
+                tmem_load<NC>(at + 2 * N, o3);
+                tc::tmem_ld_wait();
+#pragma unroll
+                for (int e = 0; e < NC; ++e) {
+                    const int ro = out_row[e];
+                    const float o = fmaf(fmaf(__uint_as_float(o3[e]), 0.125f, __uint_as_float(o2[e])),
+                                         0.125f, __uint_as_float(o1[e]));
+                    if (ro < 0) continue;
+                    if (whole)
+                        p.out[(size_t)ro * D + z * 128 + t] =
+                            __bfloat16_as_ushort(__float2bfloat16_rn(o * l[e]));
+                    else
+                        plan.part_o[(slot_row + e) * D + z * 128 + t] = o * (1.f / kWeight);
+                }
+            }
+            // all reads of the reduction area and of O come before the next segment's
+            tc::tc_fence_before();
+            half_any(half, false);
+            have = have_next;
+            sg = nx;
+            ++si;
+        }
+    }
+
+    tc::tc_fence_before();
+    __syncthreads();
+    tc::tc_fence_after();
+    if (warp == 1) {
+        __syncwarp();
+        tc::tmem_dealloc(sh->tmem, L::kTmem);
+    }
+}
+
+// Merge of the split units: out = sum_q 2^(m_q - M) O_q / sum_q 2^(m_q - M) l_q
+// over the pieces q, M their largest maximum (a piece whose l is 0 saw no key of
+// the row).  One CTA per (unit and row group, row).
+template <int D, int N>
+__global__ void __launch_bounds__(D / 4) paged_fp8_merge_kernel(const PagedFp8Params p,
+                                                                const Plan plan) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int u = blockIdx.x, r = blockIdx.y;
+    const int rg = u % plan.groups, bc = u / plan.groups;
+    const int b = bc / p.kv_heads, c = bc % p.kv_heads;
     const long long ctx = p.context_lengths[b];
-    if (ctx < 0 || ctx + p.k > p.capacity) {
-        if (threadIdx.x == 0) set_status(p.dev_status, CARAT_DEV_BAD_CONTEXT);
-        for (int d = threadIdx.x; d < D; d += blockDim.x) p.out[row * D + d] = 0x7fc0;
+    const int4 e = plan.units[u];
+    const int ur = rg * N + r;
+    if (ctx < 0 || ctx + p.k > p.capacity || ur >= p.group * p.k) return;
+    const int np = e.y;
+    if (np == 0) return;   // whole: written already
+    // an entry that the attention grid did not write this time (it gave up before)
+    if (e.x < 0 || np < 0 || np > kMaxPieces || e.x > plan.ranges - np || (e.z & ~1)) {
+        if (threadIdx.x == 0) set_status(p.dev_status, CARAT_DEV_TIMEOUT);
         return;
     }
-    const int c = h / p.group;
-    float q[E], o[E];
-#pragma unroll
-    for (int i = 0; i < E; ++i) {
-        q[i] = __uint_as_float((uint32_t)p.q[row * D + lane * E + i] << 16);
-        o[i] = 0.f;
-    }
-    float m = -INFINITY, l = 0.f;
-    const long long pos = ctx + j;
-    const long long first = p.window > 0 && pos - p.window + 1 > 0 ? pos - p.window + 1 : 0;
-    for (long long t = first + warp; t <= pos; t += kWarps) {
-        const long long r = paged_row(p.page_table, p.max_pages, p.page_rows, p.num_pages, b, t);
-        if (r < 0) {   // a page outside the pool reads as zeros
-            if (lane == 0) set_status(p.dev_status, CARAT_DEV_BAD_CACHE_ID);
-            const float mn = fmaxf(m, 0.f), a = exp2f(m - mn);
-            l = l * a + exp2f(-mn);
-#pragma unroll
-            for (int i = 0; i < E; ++i) o[i] *= a;
-            m = mn;
-            continue;
-        }
-        const size_t at = ((size_t)r * p.kv_heads + c) * D + lane * E;
-        const size_t sc = (size_t)(r / p.block_rows) * p.kv_heads + c;
-        float s = 0.f, x[4];
-#pragma unroll
-        for (int i = 0; i < E; i += 4) {
-            e4m3x4_to_f32(*reinterpret_cast<const uint32_t *>(p.k_pages + at + i), x);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) s = fmaf(q[i + e], x[e], s);
+    auto piece = [&](int q) -> size_t {
+        return ((size_t)((e.x + q) * plan.groups + rg) * 2 + (q == 0 ? e.z : 0)) * N + r;
+    };
+    __shared__ float s_w[kMaxPieces];
+    const int lane = threadIdx.x % 32;
+    if (threadIdx.x < 32) {
+        float M = -INFINITY;
+        for (int q = lane; q < np; q += 32) {
+            const float2 v = plan.part_ml[piece(q)];
+            if (v.y != 0.f) M = fmaxf(M, v.x);
         }
 #pragma unroll
-        for (int z = 16; z > 0; z >>= 1) s += __shfl_xor_sync(0xffffffffu, s, z);
-        s *= p.scale_log2 * p.k_scales[sc];
-        const float mn = fmaxf(m, s);
-        const float a = exp2f(m - mn), w = exp2f(s - mn);
-        l = l * a + w;
-        const float wv = w * p.v_scales[sc];
-#pragma unroll
-        for (int i = 0; i < E; i += 4) {
-            e4m3x4_to_f32(*reinterpret_cast<const uint32_t *>(p.v_pages + at + i), x);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) o[i + e] = fmaf(wv, x[e], o[i + e] * a);
+        for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, o));
+        float sum = 0.f;
+        for (int q = lane; q < np; q += 32) {
+            const float2 v = plan.part_ml[piece(q)];
+            const float w = v.y != 0.f ? fast_exp2(v.x - M) : 0.f;
+            s_w[q] = w;
+            sum = fmaf(w, v.y, sum);
         }
-        m = mn;
-    }
-    __shared__ float s_m[kWarps], s_l[kWarps], s_o[kWarps][D];
-    if (lane == 0) {
-        s_m[warp] = m;
-        s_l[warp] = l;
-    }
 #pragma unroll
-    for (int i = 0; i < E; ++i) s_o[warp][lane * E + i] = o[i];
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
+        const float inv = 1.f / sum;
+        for (int q = lane; q < np; q += 32) s_w[q] *= inv;
+    }
     __syncthreads();
-    float M = -INFINITY;
-    for (int w = 0; w < kWarps; ++w) M = fmaxf(M, s_m[w]);
-    float L = 0.f;
-    for (int w = 0; w < kWarps; ++w) L += s_l[w] * (s_m[w] == -INFINITY ? 0.f : exp2f(s_m[w] - M));
-    for (int d = threadIdx.x; d < D; d += blockDim.x) {
-        float acc = 0.f;
-        for (int w = 0; w < kWarps; ++w)
-            acc += s_o[w][d] * (s_m[w] == -INFINITY ? 0.f : exp2f(s_m[w] - M));
-        p.out[row * D + d] = __bfloat16_as_ushort(__float2bfloat16_rn(acc / L));
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int q0 = 0; q0 < np; q0 += 8) {
+        float4 v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (q0 + i < np)
+                v[i] = reinterpret_cast<const float4 *>(plan.part_o + piece(q0 + i) * D)[threadIdx.x];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if (q0 + i >= np) continue;
+            const float w = s_w[q0 + i];
+            if (w == 0.f) continue;
+            acc.x = fmaf(v[i].x, w, acc.x);
+            acc.y = fmaf(v[i].y, w, acc.y);
+            acc.z = fmaf(v[i].z, w, acc.z);
+            acc.w = fmaf(v[i].w, w, acc.w);
+        }
     }
+    const int j = ur / p.group;
+    const size_t row = ((size_t)b * p.k + j) * p.q_heads + (size_t)c * p.group + ur - j * p.group;
+    const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x, acc.y);
+    const __nv_bfloat162 hi = __floats2bfloat162_rn(acc.z, acc.w);
+    reinterpret_cast<uint2 *>(p.out + row * D)[threadIdx.x] =
+        make_uint2(*reinterpret_cast<const uint32_t *>(&lo), *reinterpret_cast<const uint32_t *>(&hi));
+}
+
+size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
+
+// Rows of a tile: 16, or groups of 32.
+int tile_rows(int rows) { return rows <= 16 ? 16 : 32; }
+
+struct Sizes {
+    int n, groups, grid;
+    size_t ml, o, units, total;
+};
+
+Sizes sizes_of(int batch, int k, int q_heads, int kv_heads, int head_dim) {
+    Sizes z{};
+    const int rows = q_heads / kv_heads * k;
+    z.n = tile_rows(rows);
+    z.groups = (rows + z.n - 1) / z.n;
+    const int sms = device_sm_count();
+    const int ranges = sms / z.groups < kMaxPieces ? sms / z.groups : kMaxPieces;
+    z.grid = (ranges < 1 ? 1 : ranges) * z.groups;
+    const size_t slots = (size_t)z.grid * 2 * z.n;
+    z.ml = align256(slots * sizeof(float2));
+    z.o = align256(slots * (size_t)head_dim * sizeof(float));
+    z.units = align256((size_t)batch * kv_heads * z.groups * sizeof(int4));
+    z.total = z.ml + z.o + z.units;
+    return z;
+}
+
+template <int D, int N>
+cudaError_t launch(const PagedFp8Params &p, const Sizes &z, cudaStream_t stream) {
+    using L = Lay<D, N>;
+    Plan plan{};
+    plan.groups = z.groups;
+    plan.ranges = z.grid / z.groups;
+    char *w = static_cast<char *>(p.workspace);
+    plan.part_ml = reinterpret_cast<float2 *>(w);
+    plan.part_o = reinterpret_cast<float *>(w + z.ml);
+    plan.units = reinterpret_cast<int4 *>(w + z.ml + z.o);
+    // (128 d, rows, 128-d block, head); a stage is 128 rows of one block
+    CUtensorMap map_k{}, map_v{};
+    const uint64_t row = (uint64_t)p.kv_heads * D;
+    const uint64_t dims[4] = {128, (uint64_t)p.num_pages * p.page_rows, D / 128,
+                              (uint64_t)p.kv_heads};
+    const uint64_t strides[3] = {row, 128, D};
+    const uint32_t box[4] = {128, kKeys, 1, 1};
+    if (!make_u8_tensor_map(&map_k, p.k_pages, 4, dims, strides, box, true) ||
+        !make_u8_tensor_map(&map_v, p.v_pages, 4, dims, strides, box, true))
+        return cudaErrorInvalidValue;
+    auto kernel = paged_fp8_kernel<D, N>;
+    static std::atomic<int> configured[64];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64 || !configured[dev].load(std::memory_order_acquire)) {
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAlloc);
+        if (e != cudaSuccess) return e;
+        if (dev >= 0 && dev < 64) configured[dev].store(1, std::memory_order_release);
+    }
+    kernel<<<z.grid, kThreads, L::kAlloc, stream>>>(p, plan, map_k, map_v);
+    count_launches(1);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(p.batch * p.kv_heads * z.groups, N);
+    cfg.blockDim = dim3(D / 4);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, paged_fp8_merge_kernel<D, N>, p, plan);
+    count_launches(1);
+    return e;
 }
 
 }  // namespace
@@ -111,17 +1131,14 @@ bool paged_fp8_supported(int head_dim) { return head_dim == 256 || head_dim == 5
 
 size_t paged_fp8_workspace(int batch, int proposal_count, int q_heads, int kv_heads,
                            int head_dim) {
-    return batch > 0 ? 256 : 0;
+    return batch > 0 ? sizes_of(batch, proposal_count, q_heads, kv_heads, head_dim).total : 0;
 }
 
 cudaError_t launch_paged_fp8_attention(const PagedFp8Params &p, cudaStream_t stream) {
-    const dim3 grid(p.q_heads, p.k, p.batch);
+    const Sizes z = sizes_of(p.batch, p.k, p.q_heads, p.kv_heads, p.head_dim);
     if (p.head_dim == 256)
-        paged_fp8_simple_kernel<256><<<grid, kWarps * 32, 0, stream>>>(p);
-    else
-        paged_fp8_simple_kernel<512><<<grid, kWarps * 32, 0, stream>>>(p);
-    count_launches(1);
-    return cudaGetLastError();
+        return z.n == 16 ? launch<256, 16>(p, z, stream) : launch<256, 32>(p, z, stream);
+    return z.n == 16 ? launch<512, 16>(p, z, stream) : launch<512, 32>(p, z, stream);
 }
 
 }  // namespace carat

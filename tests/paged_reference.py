@@ -47,11 +47,13 @@ def scale_exponent(amax: float) -> int:
     return e
 
 
-def attention(q, keys, values, positions, window, scale):
+def attention(q, keys, values, positions, window, scale, value_scales=None):
     """out [k][Hq][D] doubles and W = sum_t p_t |v_t| for one request.
 
     q [k][Hq][D]; keys, values [n][Hkv][D] (positions 0..n-1); positions[j] of
-    query j."""
+    query j; value_scales [n][Hkv]: the scales within the values (their bytes stand
+    for value / scale).  With them W also holds the floor of the weights'
+    rounding (see attention_tolerance)."""
     k, hq, d = q.shape
     hkv = keys.shape[1]
     g = hq // hkv
@@ -65,6 +67,11 @@ def attention(q, keys, values, positions, window, scale):
             w = torch.softmax(s, -1)
             out[j, c * g:(c + 1) * g] = w @ values[lo:p + 1, c]
             weight[j, c * g:(c + 1) * g] = w @ values[lo:p + 1, c].abs()
+            if value_scales is not None:
+                vs = value_scales[lo:p + 1, c]
+                top = (w * vs).amax(-1, keepdim=True)
+                bytes_ = (values[lo:p + 1, c].abs() / vs[:, None]).sum(0)
+                weight[j, c * g:(c + 1) * g] += 2.0 ** -18 * top * bytes_
     return out, weight
 
 
@@ -83,7 +90,13 @@ def attention_tolerance(out, weight, q, keys, scale):
     (2^-11), and its score, a sum of D products accumulated in fp32, by
     (D + 64) 2^-24 of sum |q k| (64: the scales' products, the exponential's 2
     ulp and the conversion to log2 units).  Numerator and denominator both
-    carry it.  The result is rounded to bf16 once (2^-8)."""
+    carry it.  The result is rounded to bf16 once (2^-8).
+
+    Floor: the weights p_t vs_t that meet the bytes are formed times 64 / (a weight
+    of the row), so the row's largest is at least 64 then, as f16 (off by at most
+    2^-25) and as three e5m2 pieces, the last in steps of 2^-16 / 64 (off by at most
+    2^-23): less than 2^-28 of the largest weight, times the byte's value.
+    attention() adds 2^-18 of that product to W, which delta >= 2^-10 makes 2^-28."""
     d = q.shape[2]
     delta = 2 * (2.0 ** -11 + score_magnitude(q, keys, scale) * (d + 64) * 2.0 ** -24)
     return 2.0 ** -8 * out.abs() + delta * weight * (1 + 2.0 ** -8) + math.ulp(0.0)

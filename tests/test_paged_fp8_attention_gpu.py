@@ -54,7 +54,7 @@ class Case:
             return torch.exp2(e).float()
 
         self.ks, self.vs = scales(), scales()
-        self.keys, self.values = [], []
+        self.keys, self.values, self.value_scales = [], [], []
         for b, n in enumerate(self.n):
             pages = [perm.pop() for _ in range(-(-max(n, 1) // page_rows))]
             self.table[b, :len(pages)] = torch.tensor(pages)
@@ -73,6 +73,8 @@ class Case:
                 hist.append(val)
             self.keys.append(hist[0])
             self.values.append(hist[1])
+            self.value_scales.append(self.vs[pages].double().repeat_interleave(block_rows, 1)
+                                     .flatten(0, 1)[:n])
         self.q = torch.randn((self.B, k, q_heads, head_dim), generator=g).bfloat16()
         self.upload()
 
@@ -96,7 +98,8 @@ class Case:
     def expected(self, b):
         q = self.q[b].double()
         pos = [self.n[b] - self.k + j for j in range(self.k)]
-        return ref.attention(q, self.keys[b], self.values[b], pos, self.window, self.scale)
+        return ref.attention(q, self.keys[b], self.values[b], pos, self.window, self.scale,
+                             self.value_scales[b][:self.n[b]])
 
     def check(self, out, requests=None):
         out = out.cpu().double()
