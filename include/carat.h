@@ -541,7 +541,8 @@ carat_status carat_global_verify_attention_paged(
  *
  * Supported: head_dim 256 or 512; (q_heads/kv_heads) * proposal_count <= 128;
  * q_heads/kv_heads <= 64; proposal_count <= 16; batch * q_heads *
- * proposal_count < 2^24 (other shapes: CARAT_ERR_UNSUPPORTED).
+ * proposal_count < 2^24; batch * kv_heads * (max_pages * page_rows / 128 + 4)
+ * < 2^29 (other shapes: CARAT_ERR_UNSUPPORTED).
  */
 carat_status carat_paged_verify_attention_fp8(
     void *out, const void *queries, const void *key_pages, const void *value_pages,

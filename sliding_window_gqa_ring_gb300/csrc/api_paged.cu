@@ -144,7 +144,8 @@ static carat_status check_paged_fp8(int batch, int proposal_count, int q_heads, 
     const int group = q_heads / kv_heads;
     if (!paged_fp8_supported(head_dim) || group > 64 ||
         (long long)group * proposal_count > kMaxTileRows ||
-        (long long)batch * q_heads * proposal_count >= (1LL << 24))
+        (long long)batch * q_heads * proposal_count >= (1LL << 24) ||
+        (long long)batch * kv_heads * (capacity / kTcTileKeys + 4) >= (1LL << 29))
         return CARAT_ERR_UNSUPPORTED;
     return CARAT_OK;
 }

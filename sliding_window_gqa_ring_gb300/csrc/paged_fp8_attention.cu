@@ -28,8 +28,7 @@
 // The scales cost nothing in the products: thread t of the softmax owns key t,
 // so ks[t] is one factor of its scores, and vs[t] one of its weights.
 //
-// The running maximum m is that of s_t + log2 vs[t] (by vs's exponent), not of
-// s_t: it bounds the weights that are really rounded, whatever the scales'
+// The running maximum m is that of s_t + log2 vs[t], not of s_t: it bounds the weights that are really rounded, whatever the scales'
 // range.  It moves only when exceeded by more than kSlack, and the sum
 // of 2^(s_t - m) is taken over the rounded weights, in fp32.
 //
@@ -65,25 +64,30 @@ constexpr int kSlots = 4;                  // tiles whose scales are fetched ahe
 constexpr int kMaxPieces = 256;            // pieces of one unit
 constexpr uint32_t kFull = 0xffffffffu;
 constexpr float kSlack = 8.f;
-// Weights carry this factor: 2^kSlack * 2 * 64 = 2^15 fits e5m2 and f16, and a
-// weight 2^-29 of the largest is still rounded to within its own half.
-constexpr float kWeight = 64.f;
+// Weights carry the factor 2^kBoost = kWeight: 2^(kSlack + kBoost) = 2^14 fits
+// e5m2 and f16, and weights are resolved down to 2^-28 of the largest.
+constexpr float kBoost = 6.f, kWeight = 64.f;
+constexpr float kUnset = -1e30f;           // maximum of a row that has seen no key yet
 
 template <int D, int N>
 struct Lay {
     static constexpr int KS = D / 128;                // stages of a K (or V) tile
-    static constexpr int NS = D == 512 && N == 32 ? 11 : 12;
+    static constexpr int NS = N == 16 ? 12 : D == 256 ? 11 : 10;
+    // tiles a unit's boundary costs: O must be read out before the next unit's first
+    // product (measured)
+    static constexpr int kCharge = D == 512 && N == 32 ? 2 : 1;
     static constexpr int kQBlock = 2 * N * 128;       // 128 d of the query pieces
+    static constexpr int kPBytes = 3 * N * 128;       // a tile's weights (two buffers)
     static constexpr int kOffQ = NS * kStage;
     static constexpr int kOffP = kOffQ + KS * kQBlock;
-    static constexpr int kOffRed = kOffP + 3 * N * 128;
+    static constexpr int kOffRed = kOffP + 2 * kPBytes;
     // floats: the four key quarters' maxima or sums per row, the running
     // maxima, the rescale factors, the query scales of two segments
     static constexpr int kRedM = 4 * N, kRedAlpha = 5 * N, kRedQ = 6 * N, kRedRow = 8 * N;
     static constexpr int kRedFloats = 10 * N;         // last 2 N: output rows (int)
     static constexpr int kOffSc = kOffRed + kRedFloats * 4;      // [kSlots][2][8] scales
     static constexpr int kOffBar = kOffSc + kSlots * 64;
-    static constexpr int kBars = 2 * NS + 6 + 2 * kSlots;
+    static constexpr int kBars = 2 * NS + 8 + 2 * kSlots;
     static constexpr int kOffMisc = kOffBar + kBars * 8;
     static constexpr int kBytes = kOffMisc + 128;
     static constexpr int kAlloc = kBytes + 1024;
@@ -102,7 +106,10 @@ struct Plan {
     int ranges;     // ranges of the tile sequence (grid = ranges * groups)
     float2 *part_ml;    // [2 * grid][N] (max, sum)
     float *part_o;      // [2 * grid][N][D]
-    int4 *units;        // [B * Hkv * groups] first range, pieces (0: whole), first slot
+    // per (request, KV head, row group): range of the first piece and its slot
+    // (-1: whole, nothing to merge), range of the last piece
+    int2 *first;
+    int *last;
 };
 
 // Tiles of request b: [first, first + count) of its 128-position tiles; 0 when
@@ -119,10 +126,7 @@ struct Shared {
     uint32_t tmem;
     int abort_flag;
     int b0, c0, off0;       // first segment: request, KV head, tiles of the unit before it
-    int charge;             // cost of a unit besides its tiles
-    long long s, e;         // the CTA's tiles of the sequence
-    long long len;          // cost of a range
-    long long ucost0;       // cost position of the first segment's unit
+    int s, e;               // the CTA's tiles of the sequence
 };
 
 struct Segment {
@@ -131,13 +135,12 @@ struct Segment {
     int first, ntiles;      // the unit's tiles
     int x0, x1;             // those of this segment
     bool opens;             // the segment opens the CTA's range
-    long long ucost;
 };
 
 // Walks a CTA's range as segments, one per unit it touches.
 struct SegIter {
-    long long pos, end, start, ucost, ctx;
-    int b, c, off, first, ntiles, charge;
+    long long ctx;
+    int pos, end, start, b, c, off, first, ntiles;
 
     __device__ void init(const PagedFp8Params &p, const volatile Shared *sh) {
         pos = start = sh->s;
@@ -145,8 +148,6 @@ struct SegIter {
         b = sh->b0;
         c = sh->c0;
         off = sh->off0;
-        ucost = sh->ucost0;
-        charge = sh->charge;
         ntiles = 0;
         if (pos < end) {
             ctx = p.context_lengths[b];
@@ -154,10 +155,9 @@ struct SegIter {
         }
     }
 
-    __device__ bool next(const PagedFp8Params &p, Segment &sg) {
+    __device__ __noinline__ bool next(const PagedFp8Params &p, Segment &sg) {
         if (pos >= end || off >= ntiles) return false;
-        const long long left = end - pos;
-        const int len = (long long)(ntiles - off) < left ? ntiles - off : (int)left;
+        const int len = min(ntiles - off, end - pos);
         sg.b = b;
         sg.c = c;
         sg.ctx = ctx;
@@ -166,12 +166,10 @@ struct SegIter {
         sg.x0 = off;
         sg.x1 = off + len;
         sg.opens = pos == start;
-        sg.ucost = ucost;
         pos += len;
         off += len;
         if (off == ntiles && pos < end) {
             off = 0;
-            ucost += ntiles + charge;
             if (++c == p.kv_heads) {
                 c = 0;
                 ntiles = 0;
@@ -186,74 +184,78 @@ struct SegIter {
     }
 };
 
-__device__ __forceinline__ long long warp_sum(long long v) {
-#pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
-    return v;
-}
-
-// Warp 0: this CTA's range.  A unit costs its tiles and `charge` more (its
+// Warp 0: this CTA's range.  A unit costs its tiles and kCharge more (its
 // segment boundary: a new Q, an output or partial); tile o of the unit that
 // begins at cost U sits at U + charge + o, and tile t belongs to range
 // floor(cost(t) / len).  A call with fewer tiles than ranges charges nothing,
-// and every tile has a range to itself.
+// and every tile has a range to itself.  The requests' tile counts are read
+// once, four loads of a lane in flight, and kept in `held` (room for `room`
+// of them) for the second pass.
 __device__ __noinline__ void locate_range(const PagedFp8Params &p, int ranges, int rix, int lane,
-                                          Shared *sh) {
-    long long tiles = 0, units = 0;
+                                          int unit_charge, int *held, int room, Shared *sh) {
+    int tiles = 0, units = 0;
 #pragma unroll 1
-    for (int b = lane; b < p.batch; b += 32) {
-        int first;
-        const int v = request_tiles(p, p.context_lengths[b], &first);
-        tiles += v;
-        units += v > 0 ? 1 : 0;
+    for (int base = 0; base < p.batch; base += 128) {
+        long long ctx[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int b = base + 32 * i + lane;
+            ctx[i] = b < p.batch ? p.context_lengths[b] : -1;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int b = base + 32 * i + lane;
+            int first;
+            const int v = request_tiles(p, ctx[i], &first);
+            tiles += v;
+            units += v > 0 ? 1 : 0;
+            if (b < p.batch && b < room) held[b] = v;
+        }
     }
-    tiles = warp_sum(tiles) * p.kv_heads;
-    units = warp_sum(units) * p.kv_heads;
-    const int charge = tiles >= ranges ? 1 : 0;
-    const long long cost = tiles + charge * units;
-    long long len = (cost + ranges - 1) / ranges;
+    __syncwarp();
+    tiles = __reduce_add_sync(kFull, tiles) * p.kv_heads;
+    units = __reduce_add_sync(kFull, units) * p.kv_heads;
+    const int charge = tiles >= ranges ? unit_charge : 0;
+    const int cost = tiles + charge * units;
+    int len = (cost + ranges - 1) / ranges;
     if (len < charge + 1) len = charge + 1;
     // The first tiles at cost positions >= X0 and >= X1 (none: `tiles`).
-    const long long X0 = rix * len, X1 = rix + 1 < ranges ? X0 + len : cost;
-    long long at0 = tiles, at1 = tiles, u0 = 0;
-    int b0 = 0, c0 = 0, off0 = 0;
-    long long cum_cost = 0, cum_tiles = 0;
+    const int X0 = rix * len, X1 = rix + 1 < ranges ? X0 + len : cost;
+    int at0 = tiles, at1 = tiles, b0 = 0, c0 = 0, off0 = 0;
+    int cum_cost = 0, cum_tiles = 0;
 #pragma unroll 1
     for (int base = 0; base < p.batch && cum_cost <= X1; base += 32) {
         const int b = base + lane;
         int v = 0, first;
-        if (b < p.batch) v = request_tiles(p, p.context_lengths[b], &first);
-        const long long per = v + charge;
-        const long long vc = v > 0 ? p.kv_heads * per : 0, vt = (long long)p.kv_heads * v;
-        long long ic = vc, it = vt;
+        if (b < p.batch) v = b < room ? held[b] : request_tiles(p, p.context_lengths[b], &first);
+        const int per = v + charge;
+        const int vc = v > 0 ? p.kv_heads * per : 0, vt = p.kv_heads * v;
+        int ic = vc, it = vt;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const long long yc = __shfl_up_sync(kFull, ic, o), yt = __shfl_up_sync(kFull, it, o);
+            const int yc = __shfl_up_sync(kFull, ic, o), yt = __shfl_up_sync(kFull, it, o);
             if (lane >= o) ic += yc, it += yt;
         }
-        const long long lo = cum_cost + ic - vc, tlo = cum_tiles + it - vt;
+        const int lo = cum_cost + ic - vc, tlo = cum_tiles + it - vt;
 #pragma unroll 1
         for (int which = 0; which < 2; ++which) {
-            const long long X = which ? X1 : X0;
+            const int X = which ? X1 : X0;
             const bool mine = vc > 0 && X >= lo && X < lo + vc;
             const unsigned hit = __ballot_sync(kFull, mine);
             if (!hit) continue;
             const int src = __ffs(hit) - 1;
-            long long at = 0, uc = 0;
-            int j = 0, o = 0;
+            int at = 0, j = 0, o = 0;
             if (mine) {
-                j = (int)((X - lo) / per);
-                const long long r = X - lo - j * per;
-                o = r <= charge ? 0 : (int)(r - charge);
-                at = tlo + (long long)j * v + o;
-                uc = lo + j * per;
+                j = (X - lo) / per;
+                const int r = X - lo - j * per;
+                o = r <= charge ? 0 : r - charge;
+                at = tlo + j * v + o;
             }
             at = __shfl_sync(kFull, at, src);
             if (which) {
                 at1 = at;
             } else {
                 at0 = at;
-                u0 = __shfl_sync(kFull, uc, src);
                 b0 = base + src;
                 c0 = __shfl_sync(kFull, j, src);
                 off0 = __shfl_sync(kFull, o, src);
@@ -265,21 +267,18 @@ __device__ __noinline__ void locate_range(const PagedFp8Params &p, int ranges, i
     if (lane == 0) {
         sh->s = at0;
         sh->e = at1;
-        sh->len = len;
-        sh->charge = charge;
         sh->b0 = b0;
         sh->c0 = c0;
         sh->off0 = off0;
-        sh->ucost0 = u0;
     }
     __syncwarp();
 }
 
 // Wait for a barrier phase; false after two seconds, or when another role gave
-// up (which is recorded and reported once).
-__device__ __forceinline__ bool await(uint64_t *bar, uint32_t parity, volatile int *abort_flag,
-                                      int *dev_status) {
-    if (tc::mbar_try_wait(bar, parity)) return true;
+// up (which is recorded and reported once).  The polling is out of line: the
+// roles' loops share one small instruction cache.
+__device__ __noinline__ bool await_slow(uint64_t *bar, uint32_t parity, volatile int *abort_flag,
+                                        int *dev_status) {
     const uint64_t t0 = tc::globaltimer_ns();
     for (uint32_t round = 1;; ++round) {
 #pragma unroll 1
@@ -292,6 +291,11 @@ __device__ __forceinline__ bool await(uint64_t *bar, uint32_t parity, volatile i
             return false;
         }
     }
+}
+
+__device__ __forceinline__ bool await(uint64_t *bar, uint32_t parity, volatile int *abort_flag,
+                                      int *dev_status) {
+    return tc::mbar_try_wait(bar, parity) || await_slow(bar, parity, abort_flag, dev_status);
 }
 
 // Barrier of the 128 threads of one half of the softmax; true when any of them
@@ -347,6 +351,35 @@ __device__ __forceinline__ void tmem_store(uint32_t addr, const uint32_t (&r)[NC
     else tc::tmem_st8(addr, r);
 }
 
+// Two fp32 values in one register pair, for the packed instructions.
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+
+__device__ __forceinline__ void unpack2(uint64_t v, float &a, float &b) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
 __device__ __forceinline__ uint32_t low_mask(int n) { return n >= 32 ? kFull : (1u << n) - 1u; }
 
 __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
@@ -389,7 +422,7 @@ __device__ __forceinline__ float split_query(uint8_t *s_q, const uint16_t *row, 
     if (row) {
 #pragma unroll
         for (int i = 0; i < E / 8; ++i) {
-            const uint4 v = __ldg(reinterpret_cast<const uint4 *>(row + lane * E) + i);
+            const uint4 v = reinterpret_cast<const uint4 *>(row + lane * E)[i];
             w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
         }
 #pragma unroll
@@ -433,9 +466,40 @@ __device__ __forceinline__ float split_query(uint8_t *s_q, const uint16_t *row, 
     return top >= 0x7f800000u ? __int_as_float(0x7fc00000) : __int_as_float((127 - s) << 23);
 }
 
+// A segment's queries, rows r0 .. r0 + N / 2 of it, by four warps in turn; the
+// rows' score factors and their places in the output.
+template <int D, int N>
+__device__ __noinline__ void split_queries(const PagedFp8Params &p, uint8_t *s_q, float *s_qs,
+                                           int *s_row, int b, int c, int row0, int rows_here,
+                                           int r0, int q4, int lane) {
+    // each lane touches one 128-byte line of the warp's rows, so that they all
+    // come at once
+    constexpr int kLines = D / 64;
+    if (lane < N / 8 * kLines) {
+        const int r = r0 + q4 + 4 * (lane / kLines), ur = row0 + r, j = ur / p.group;
+        if (r < rows_here) {
+            const uint16_t *a = p.q + ((size_t)(b * p.k + j) * p.q_heads + c * p.group + ur -
+                                       j * p.group) * D + lane % kLines * 64;
+            asm volatile("{\n\t.reg .u32 x;\n\tld.global.u32 x, [%0];\n\t}" ::"l"(a));
+        }
+    }
+#pragma unroll 1
+    for (int r = r0 + q4; r < r0 + N / 2; r += 4) {
+        const int ur = row0 + r, j = ur / p.group;
+        const int at =
+            r < rows_here ? (b * p.k + j) * p.q_heads + c * p.group + ur - j * p.group : -1;
+        const float f =
+            split_query<D, N>(s_q, at >= 0 ? p.q + (size_t)at * D : nullptr, r, lane);
+        if (lane == 0) {
+            s_qs[r] = f * p.scale_log2;
+            s_row[r] = at;
+        }
+    }
+}
+
 template <int D, int N>
 __global__ void __launch_bounds__(kThreads, 1)
-    paged_fp8_kernel(const PagedFp8Params p, const Plan plan,
+    paged_fp8_kernel(const __grid_constant__ PagedFp8Params p, const Plan plan,
                      const __grid_constant__ CUtensorMap map_k,
                      const __grid_constant__ CUtensorMap map_v) {
     using L = Lay<D, N>;
@@ -449,11 +513,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + L::kOffBar);
     uint64_t *empty = full + NS;
     uint64_t *s_full = empty + NS;      // [2] scores of a tile ready
-    uint64_t *p_full = s_full + 2;      // weights of a tile written
-    uint64_t *o_done = s_full + 3;      // PV product of a tile done
-    uint64_t *q_full = s_full + 4;      // queries of a segment written
-    uint64_t *fin = s_full + 5;
-    uint64_t *sc_full = s_full + 6;     // [kSlots] scales of a tile fetched
+    uint64_t *p_full = s_full + 2;      // [2] weights of a tile written
+    uint64_t *o_done = s_full + 4;      // [2] PV product of a tile done
+    uint64_t *q_full = s_full + 6;      // queries of a segment written
+    uint64_t *fin = s_full + 7;
+    uint64_t *sc_full = s_full + 8;     // [kSlots] scales of a tile fetched
     uint64_t *sc_empty = sc_full + kSlots;
     uint8_t *s_q = smem + L::kOffQ;
     uint8_t *s_p = smem + L::kOffP;
@@ -482,10 +546,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc::mbar_init(&full[i], 1);
                 tc::mbar_init(&empty[i], 1);
             }
-            tc::mbar_init(&s_full[0], 1);
-            tc::mbar_init(&s_full[1], 1);
-            tc::mbar_init(p_full, kSoftWarps);
-            tc::mbar_init(o_done, 1);
+            for (int i = 0; i < 2; ++i) {
+                tc::mbar_init(&s_full[i], 1);
+                tc::mbar_init(&p_full[i], kSoftWarps);
+                tc::mbar_init(&o_done[i], 1);
+            }
             tc::mbar_init(q_full, kSoftWarps);
             tc::mbar_init(fin, 1);
             for (int i = 0; i < kSlots; ++i) {
@@ -495,7 +560,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             sh->abort_flag = 0;
             tc::fence_mbar_init();
         }
-        locate_range(p, plan.ranges, rix, lane, sh);
+        locate_range(p, plan.ranges, rix, lane, L::kCharge, reinterpret_cast<int *>(s_p),
+                     2 * L::kPBytes / 4, sh);
         __threadfence_block();
         __syncwarp();
         // the others wait for this; the loads need not wait for them
@@ -593,41 +659,57 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc::tc_fence_after();
     }
 
-    if (warp == 1 && lane == 0) {
+    if (warp == 1) {
         // ------------------------------------------------------------ products
         constexpr uint32_t idesc_qk = tc::idesc_e4m3_f32(128, 2 * N, false, false);
         constexpr uint32_t idesc_pv = tc::idesc_e4m3_f32(128, 3 * N, true, true);
         const uint32_t tmem = sh->tmem;
-        const uint32_t q_base = tc::smem_u32(s_q), p_base = tc::smem_u32(s_p);
+        // descriptors in units of 16 bytes of shared memory: 32 elements along K
+        // are 2 units in a K-major operand, 32 rows of 128 bytes in V
+        const uint64_t k_desc = tc::sdesc_sw128(tc::smem_u32(smem), 16, 1024);
+        const uint64_t v_desc = tc::sdesc_sw128(tc::smem_u32(smem), kStage, 1024);
+        const uint64_t q_desc = tc::sdesc_sw128(tc::smem_u32(s_q), 16, 1024);
+        const uint64_t p_desc = tc::sdesc_sw128(tc::smem_u32(s_p), 16, 1024);
         SegIter it;
         it.init(p, sh);
         Segment sg;
         bool alive = true, have = it.next(p, sg);
         int x = have ? sg.x0 : 0, si = 0;
-        uint32_t mcnt = 0, g = 0;
+        uint32_t g = 0;
+        int ms = 0;                     // the next stage and its phase
+        uint32_t mphase = 0;
+        auto advance = [&]() {
+            if (++ms == NS) {
+                ms = 0;
+                mphase ^= 1;
+            }
+        };
+        // the warp stays together: one lane issues, all hold the operands
+        auto wait_all = [&](uint64_t *bar, uint32_t parity) {
+            return __all_sync(kFull, await(bar, parity, abort_flag, status)) != 0;
+        };
         bool prev = false, prev_first = false;   // the tile whose PV product is due
         while (alive) {
             const bool cur = have, first = cur && x == sg.x0;
             if (cur) {
                 // S^T[g & 1] = K . [q_hi | q_lo]^T
-                if (first && !await(q_full, si & 1, abort_flag, status)) break;
+                if (first && !(alive = wait_all(q_full, si & 1))) break;
                 const uint32_t d = tmem + (g & 1) * 2 * N;
-                for (int ks = 0; ks < KS && alive; ++ks) {
-                    const int s = mcnt % NS;
-                    alive = await(&full[s], (mcnt / NS) & 1, abort_flag, status);
-                    if (!alive) break;
+                uint64_t q = q_desc;
+#pragma unroll 1
+                for (int ks = 0; ks < KS; ++ks) {
+                    if (!(alive = wait_all(&full[ms], mphase))) break;
                     tc::tc_fence_after();
-                    const uint32_t a = tc::smem_u32(smem + s * kStage);
+                    const uint64_t a = k_desc + (uint32_t)ms * (kStage / 16);
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)
-                        tc::mma_f8_ss(d, tc::sdesc_sw128(a + kk * 32, 16, 1024),
-                                      tc::sdesc_sw128(q_base + ks * L::kQBlock + kk * 32, 16, 1024),
-                                      idesc_qk, (ks | kk) != 0);
-                    tc::mma_commit(&empty[s]);
-                    ++mcnt;
+                        tc::mma_f8_ss_warp(d, a + 2 * kk, q + 2 * kk, idesc_qk, (ks | kk) != 0);
+                    tc::mma_commit_warp(&empty[ms]);
+                    q += L::kQBlock / 16;
+                    advance();
                 }
                 if (!alive) break;
-                tc::mma_commit(&s_full[g & 1]);
+                tc::mma_commit_warp(&s_full[g & 1]);
                 if (first) ++si;
                 if (++x == sg.x1) {
                     have = it.next(p, sg);
@@ -636,25 +718,26 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (prev) {
                 // O^T += V^T . [w1 | w2 | w3]^T of the tile before
-                if (!(alive = await(p_full, (g - 1) & 1, abort_flag, status))) break;
+                const uint32_t h = g - 1;
+                if (!(alive = wait_all(&p_full[h & 1], (h >> 1) & 1))) break;
                 tc::tc_fence_after();
-                for (int vs = 0; vs < KS && alive; ++vs) {
-                    const int s = mcnt % NS;
-                    alive = await(&full[s], (mcnt / NS) & 1, abort_flag, status);
-                    if (!alive) break;
+                const uint64_t w = p_desc + (h & 1) * (L::kPBytes / 16);
+                uint32_t d = tmem + L::kTmemO;
+#pragma unroll 1
+                for (int vs = 0; vs < KS; ++vs) {
+                    if (!(alive = wait_all(&full[ms], mphase))) break;
                     tc::tc_fence_after();
-                    const uint32_t a = tc::smem_u32(smem + s * kStage);
+                    const uint64_t a = v_desc + (uint32_t)ms * (kStage / 16);
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)
-                        tc::mma_f8_ss(tmem + L::kTmemO + vs * 3 * N,
-                                      tc::sdesc_sw128(a + kk * 4096, kStage, 1024),
-                                      tc::sdesc_sw128(p_base + kk * 32, 16, 1024), idesc_pv,
+                        tc::mma_f8_ss_warp(d, a + 256 * kk, w + 2 * kk, idesc_pv,
                                       !(prev_first && kk == 0));
-                    tc::mma_commit(&empty[s]);
-                    ++mcnt;
+                    tc::mma_commit_warp(&empty[ms]);
+                    d += 3 * N;
+                    advance();
                 }
                 if (!alive) break;
-                tc::mma_commit(o_done);
+                tc::mma_commit_warp(&o_done[h & 1]);
             }
             if (!cur) break;
             prev = true;
@@ -662,7 +745,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             ++g;
         }
         if (!alive || *abort_flag) {
-            tc::mma_commit(fin);
+            tc::mma_commit_warp(fin);
             tc::mbar_wait(fin, 0, 100000000ull);
         }
     } else if (warp == 2) {
@@ -724,22 +807,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         int *s_row = reinterpret_cast<int *>(red + L::kRedRow);
         const uint32_t total = (uint32_t)(sh->e - sh->s);
 
-        // A segment's queries: this half's warps take its rows in turn.
         auto write_queries = [&](const Segment &sg, int si) {
-#pragma unroll
-            for (int i = 0; i < NC / 4; ++i) {
-                const int r = r0 + i * 4 + q4;
-                const int ur = row0 + r, j = ur / p.group;
-                const int at = r < rows_here
-                                   ? (sg.b * p.k + j) * p.q_heads + sg.c * p.group + ur - j * p.group
-                                   : -1;
-                const float f = split_query<D, N>(
-                    s_q, at >= 0 ? p.q + (size_t)at * D : nullptr, r, lane);
-                if (lane == 0) {
-                    s_qs[(si & 1) * N + r] = f * p.scale_log2;
-                    s_row[(si & 1) * N + r] = at;
-                }
-            }
+            split_queries<D, N>(p, s_q, s_qs + (si & 1) * N, s_row + (si & 1) * N, sg.b, sg.c, row0,
+                                rows_here, r0, q4, lane);
             tc::fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(q_full);
@@ -754,18 +824,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (have) write_queries(sg, 0);
         half_any(half, false);
         while (have && alive) {
-            const bool have_next = it.next(p, nx);
+            // the next segment is looked up early, behind the first tile
+            bool have_next = sg.x1 - sg.x0 == 1 && it.next(p, nx);
             const bool whole = sg.x0 == 0 && sg.x1 == sg.ntiles;
-            if (half == 0 && t == 0 && sg.x0 == 0) {
-                long long last = (sg.ucost + sh->charge + sg.ntiles - 1) / sh->len;
-                if (last > plan.ranges - 1) last = plan.ranges - 1;
-                plan.units[((size_t)sg.b * p.kv_heads + sg.c) * plan.groups + rg] =
-                    make_int4(rix, whole ? 0 : (int)(last - rix + 1), sg.opens ? 0 : 1, 0);
+            if (half == 0 && t == 0) {
+                const size_t u = ((size_t)sg.b * p.kv_heads + sg.c) * plan.groups + rg;
+                if (sg.x0 == 0) plan.first[u] = make_int2(rix, whole ? -1 : sg.opens ? 0 : 1);
+                if (sg.x1 == sg.ntiles) plan.last[u] = rix;
             }
             const long long lowest = p.window > 0 && sg.ctx + 1 > p.window ? sg.ctx + 1 - p.window : 0;
-            float m[NC], l[NC];
+            // nm: kBoost - running maximum of each row (0 while it has none)
+            float nm[NC], l[NC];
 #pragma unroll
-            for (int e = 0; e < NC; ++e) m[e] = -INFINITY, l[e] = 0.f;
+            for (int e = 0; e < NC; ++e) nm[e] = 0.f, l[e] = 0.f;
+            bool unset = true;   // some row has no maximum yet
             const float *qs = s_qs + (si & 1) * N + r0;
             for (int x = sg.x0; x < sg.x1; ++x, ++g) {
                 const bool first = x == sg.x0;
@@ -776,55 +848,63 @@ __global__ void __launch_bounds__(kThreads, 1)
                 float ks = 0.f, vs = 1.f;
                 if (ok) {
                     tc::tc_fence_after();
-                    // the segment's last scores are there: its queries may go
-                    if (have_next && x + 1 == sg.x1) write_queries(nx, si + 1);
                     ks = s_sc[slot * 16 + block];
                     vs = s_sc[slot * 16 + 8 + block];
                 }
                 __syncwarp();
                 if (ok && lane == 0) tc::mbar_arrive(&sc_empty[slot]);
-                // Rows that see key t, at position pos: those of queries j with
-                // ctx + j >= pos > ctx + j - window.
-                const long long pos = (long long)(sg.first + x) * kKeys + t;
+                // d = score + log2 vs - maximum + kBoost, the weight's exponent
+                const float lv = log2f(vs), iv = 1.f / (vs * kWeight);
+                const long long t0 = (long long)(sg.first + x) * kKeys, pos = t0 + t;
                 const bool data = pos >= lowest && pos < sg.ctx + p.k;
-                uint32_t seen = 0;
-                if (data) {
-                    const long long dj = pos - sg.ctx;
-                    const int jlo = dj > 0 ? (int)dj : 0;
-                    const int jhi = p.window > 0 && dj + p.window < p.k ? (int)(dj + p.window) : p.k;
-                    const int lo = min(max(jlo * p.group - row0 - r0, 0), NC);
-                    const int hi = min(max(min(jhi * p.group - row0, rows_here) - r0, 0), NC);
-                    seen = low_mask(hi) & ~low_mask(lo);
-                }
-                // the value scale: exponent and mantissa
-                const uint32_t vbits = __float_as_uint(vs);
-                const float ev = (float)((int)(vbits >> 23) - 127);
-                const float wf = __uint_as_float((vbits & 0x7fffffu) | 0x3f800000u) * kWeight;
-                const float iv = 1.f / (vs * kWeight);
-                float v[NC];
+                float d[NC];
                 if (ok) {
                     uint32_t h[NC], w[NC];
                     const uint32_t at = tmem + (g & 1) * 2 * N + lanes + r0;
                     tmem_load<NC>(at, h);
                     tmem_load<NC>(at + N, w);
+                    const uint64_t ks2 = pack2(ks, ks), lv2 = pack2(lv, lv);
+                    const uint64_t lo2 = pack2(0.0625f, 0.0625f);
                     tc::tmem_ld_wait();
 #pragma unroll
-                    for (int e = 0; e < NC; ++e) {
-                        const float s = fmaf(__uint_as_float(w[e]), 0.0625f, __uint_as_float(h[e]));
-                        v[e] = ((seen >> e) & 1u) ? fmaf(s * ks, qs[e], ev) : -INFINITY;
+                    for (int e = 0; e < NC; e += 2) {
+                        const uint64_t q2 = *reinterpret_cast<const uint64_t *>(qs + e);
+                        const uint64_t s2 = fma2(pack2(__uint_as_float(w[e]), __uint_as_float(w[e + 1])),
+                                                 lo2, pack2(__uint_as_float(h[e]), __uint_as_float(h[e + 1])));
+                        unpack2(fma2(s2, mul2(ks2, q2), add2(lv2, pack2(nm[e], nm[e + 1]))), d[e],
+                                d[e + 1]);
                     }
                 } else {
 #pragma unroll
-                    for (int e = 0; e < NC; ++e) v[e] = -INFINITY;
+                    for (int e = 0; e < NC; ++e) d[e] = -INFINITY;
                 }
-                bool need = first;
+                // A tile that not every row sees whole: mask by position.  Query j
+                // sees key t when ctx + j >= pos > ctx + j - window.
+                const bool edge = t0 + kKeys > sg.ctx + 1 ||
+                                  (p.window > 0 && t0 <= sg.ctx + p.k - 1 - p.window);
+                if (edge) {
+                    uint32_t seen = 0;
+                    if (data) {
+                        const long long dj = pos - sg.ctx;
+                        const int jlo = dj > 0 ? (int)dj : 0;
+                        const int jhi =
+                            p.window > 0 && dj + p.window < p.k ? (int)(dj + p.window) : p.k;
+                        const int lo = min(max(jlo * p.group - row0 - r0, 0), NC);
+                        const int hi = min(max(min(jhi * p.group - row0, rows_here) - r0, 0), NC);
+                        seen = low_mask(hi) & ~low_mask(lo);
+                    }
 #pragma unroll
-                for (int e = 0; e < NC; ++e) need |= v[e] > m[e] + kSlack;
+                    for (int e = 0; e < NC; ++e)
+                        if (!((seen >> e) & 1u)) d[e] = -INFINITY;
+                }
+                float top = d[0];
+#pragma unroll
+                for (int e = 1; e < NC; ++e) top = fmaxf(top, d[e]);
                 bool rescale = false;
-                if (half_any(half, need || !ok || *abort_flag)) {
+                if (half_any(half, unset || edge || top > kSlack + kBoost || !ok || *abort_flag)) {
                     float y[NC];
 #pragma unroll
-                    for (int e = 0; e < NC; ++e) y[e] = v[e];
+                    for (int e = 0; e < NC; ++e) y[e] = d[e] = d[e] - nm[e];
                     const int rr = transpose_reduce<NC, true>(y, lane);
                     red_max[q4 * N + r0 + rr] = y[0];
                     if (half_any(half, !ok || *abort_flag)) {
@@ -834,21 +914,33 @@ __global__ void __launch_bounds__(kThreads, 1)
                     bool moved = false;
                     if (t < NC) {
                         const int r = r0 + t;
-                        const float top = fmaxf(fmaxf(red_max[r], red_max[N + r]),
-                                                fmaxf(red_max[2 * N + r], red_max[3 * N + r]));
-                        const float old = first ? -INFINITY : s_m[r];
-                        const float now = top > old + kSlack ? top : old;
-                        s_alpha[r] = fast_exp2(old - (now == -INFINITY ? 0.f : now));
+                        const float best = fmaxf(fmaxf(red_max[r], red_max[N + r]),
+                                                 fmaxf(red_max[2 * N + r], red_max[3 * N + r]));
+                        const float old = first ? kUnset : s_m[r];
+                        const float now = best > old + kSlack ? best : old;
+                        s_alpha[r] = old == kUnset ? 1.f : fast_exp2(old - now);
                         s_m[r] = now;
-                        moved = now != old && old != -INFINITY;
+                        moved = now != old && old != kUnset;
                     }
                     rescale = half_any(half, moved);
+                    unset = false;
 #pragma unroll
-                    for (int e = 0; e < NC; ++e) m[e] = s_m[r0 + e];
+                    for (int e = 0; e < NC; ++e) {
+                        const float mx = s_m[r0 + e];
+                        unset |= mx == kUnset;
+                        nm[e] = mx == kUnset ? 0.f : kBoost - mx;
+                        d[e] += nm[e];
+                    }
                 }
-                // The PV product before this one has read its weights and is in O.
-                if (g > 0) {
-                    alive = __all_sync(kFull, await(o_done, (g - 1) & 1, abort_flag, status));
+                // The PV product two tiles back has read the weights' buffer; a
+                // rescale needs the last one in O as well.
+                if (g > 1) {
+                    alive = __all_sync(kFull, await(&o_done[g & 1], ((g - 2) >> 1) & 1, abort_flag,
+                                                    status));
+                }
+                if (rescale && alive && g > 0) {
+                    alive = __all_sync(kFull, await(&o_done[(g - 1) & 1], ((g - 1) >> 1) & 1,
+                                                    abort_flag, status));
                     tc::tc_fence_after();
                 }
                 if (alive) {
@@ -868,31 +960,29 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                         tc::tmem_st_wait();
                     }
-                    // weights, two rows at a time
+                    // weights, two rows at a time; byte t of row r of the K-major
+                    // operand, 16-byte pieces swizzled by r % 8 (r0 and N are
+                    // multiples of 8)
+                    uint8_t *pw = s_p + (g & 1) * L::kPBytes + r0 * 128 + (t & 15);
+                    const __half2 eight = __floats2half2_rn(8.f, 8.f);
 #pragma unroll
                     for (int e = 0; e < NC; e += 2) {
-                        const float w0 =
-                            fast_exp2(v[e] - (m[e] == -INFINITY ? 0.f : m[e])) * wf;
-                        const float w1 =
-                            fast_exp2(v[e + 1] - (m[e + 1] == -INFINITY ? 0.f : m[e + 1])) * wf;
-                        __half2 h = __floats2half2_rn(w0, w1);
+                        __half2 h = __floats2half2_rn(fast_exp2(d[e]), fast_exp2(d[e + 1]));
                         const float2 f = __half22float2(h);
                         l[e] = fmaf(f.x, iv, l[e]);
                         l[e + 1] = fmaf(f.y, iv, l[e + 1]);
-                        const __half2 eight = __floats2half2_rn(8.f, 8.f);
+                        uint8_t *pa = pw + ((((t >> 4) ^ e) & 7) << 4) + e * 128;
+                        uint8_t *pb = pw + ((((t >> 4) ^ (e + 1)) & 7) << 4) + (e + 1) * 128;
 #pragma unroll
                         for (int z = 0; z < 3; ++z) {
                             const uint32_t b = e5m2x2(h);
-                            const int ra = z * N + r0 + e, rb = ra + 1;
-                            s_p[ra * 128 + (((t >> 4) ^ (ra & 7)) << 4) + (t & 15)] = (uint8_t)b;
-                            s_p[rb * 128 + (((t >> 4) ^ (rb & 7)) << 4) + (t & 15)] =
-                                (uint8_t)(b >> 8);
-                            h = __hmul2(__hsub2(h, e5m2x2_to_f16x2(b)), eight);
+                            pa[z * N * 128] = (uint8_t)b;
+                            pb[z * N * 128] = (uint8_t)(b >> 8);
+                            if (z < 2) h = __hmul2(__hsub2(h, e5m2x2_to_f16x2(b)), eight);
                         }
                     }
                     // A tile with rows outside the request's keys: their V bytes must not
                     // meet a zero weight (0 x NaN), so they are zeroed.
-                    const long long t0 = (long long)(sg.first + x) * kKeys;
                     if (t0 < lowest || t0 + kKeys > sg.ctx + p.k) {
                         const uint32_t base = g + 1 < total ? KS * (2 * g + 2) : KS * (2 * g + 1);
                         for (int z = half; z < KS; z += 2) {
@@ -914,50 +1004,62 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc::fence_proxy_async_smem();
                 tc::tc_fence_before();
                 __syncwarp();
-                if (lane == 0) tc::mbar_arrive(p_full);
+                if (lane == 0) tc::mbar_arrive(&p_full[g & 1]);
+                if (first && x + 1 < sg.x1) have_next = it.next(p, nx);
             }
             if (!alive) break;
             // ------------------------------------------------ segment end
+            // While the last PV product runs: the next segment's queries (this one's
+            // last scores are there), and the rows' sums over the 128 keys.
+            if (have_next) write_queries(nx, si + 1);
             float y[NC];
 #pragma unroll
             for (int e = 0; e < NC; ++e) y[e] = l[e];
             const int rr = transpose_reduce<NC, false>(y, lane);
-            alive = __all_sync(kFull, await(o_done, (g - 1) & 1, abort_flag, status));
-            tc::tc_fence_after();
             red_max[q4 * N + r0 + rr] = y[0];
+            half_any(half, false);
+            const size_t slot_row = ((size_t)blockIdx.x * 2 + (sg.opens ? 0 : 1)) * N + r0;
+            if (t < NC) {
+                const int r = r0 + t;
+                const float sum =
+                    (red_max[r] + red_max[N + r]) + (red_max[2 * N + r] + red_max[3 * N + r]);
+                if (!whole) plan.part_ml[slot_row + t] = make_float2(s_m[r], sum);
+                s_alpha[r] = 1.f / (sum * kWeight);
+            }
+            alive = __all_sync(kFull, await(&o_done[(g - 1) & 1], ((g - 1) >> 1) & 1, abort_flag,
+                                            status));
+            tc::tc_fence_after();
             if (half_any(half, !alive || *abort_flag)) {
                 alive = false;
                 break;
             }
-            const size_t slot_row = ((size_t)blockIdx.x * 2 + (sg.opens ? 0 : 1)) * N + r0;
+            // O of 8 rows and 128 d at a time: the pieces' sum, then the output row or
+            // the partial.  Rolled: this code runs once a segment, from an instruction
+            // cache that holds the tile loop, and its fetches are its cost.
             const int *out_row = s_row + (si & 1) * N + r0;
-#pragma unroll
-            for (int e = 0; e < NC; ++e) {
-                const int r = r0 + e;
-                l[e] = (red_max[r] + red_max[N + r]) + (red_max[2 * N + r] + red_max[3 * N + r]);
-                if (!whole && t == 0 && out_row[e] >= 0)
-                    plan.part_ml[slot_row + e] = make_float2(m[e], l[e]);
-                if (whole) l[e] = 1.f / (l[e] * kWeight);
-            }
 #pragma unroll 1
-            for (int z = 0; z < KS; ++z) {
-                uint32_t o1[NC], o2[NC], o3[NC];
-                const uint32_t at = tmem + L::kTmemO + z * 3 * N + lanes + r0;
-                tmem_load<NC>(at, o1);
-                tmem_load<NC>(at + N, o2);
-                tmem_load<NC>(at + 2 * N, o3);
+            for (int i = 0; i < KS * (NC / 8); ++i) {
+                const int z = i / (NC / 8), e0 = i % (NC / 8) * 8;
+                uint32_t o1[8], o2[8], o3[8];
+                const uint32_t at = tmem + L::kTmemO + z * 3 * N + lanes + r0 + e0;
+                tc::tmem_ld8(at, o1);
+                tc::tmem_ld8(at + N, o2);
+                tc::tmem_ld8(at + 2 * N, o3);
+                float *po = plan.part_o + (slot_row + e0) * D + z * 128 + t;
+                uint16_t *out = p.out + z * 128 + t;
                 tc::tmem_ld_wait();
 #pragma unroll
-                for (int e = 0; e < NC; ++e) {
-                    const int ro = out_row[e];
+                for (int e = 0; e < 8; ++e) {
                     const float o = fmaf(fmaf(__uint_as_float(o3[e]), 0.125f, __uint_as_float(o2[e])),
                                          0.125f, __uint_as_float(o1[e]));
-                    if (ro < 0) continue;
-                    if (whole)
-                        p.out[(size_t)ro * D + z * 128 + t] =
-                            __bfloat16_as_ushort(__float2bfloat16_rn(o * l[e]));
-                    else
-                        plan.part_o[(slot_row + e) * D + z * 128 + t] = o * (1.f / kWeight);
+                    if (whole) {
+                        const int ro = out_row[e0 + e];
+                        const uint16_t h =
+                            __bfloat16_as_ushort(__float2bfloat16_rn(o * s_alpha[r0 + e0 + e]));
+                        if (ro >= 0) out[(size_t)ro * D] = h;
+                    } else {
+                        po[e * D] = o * (1.f / kWeight);
+                    }
                 }
             }
             // all reads of the reduction area and of O come before the next segment's
@@ -980,62 +1082,76 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // Merge of the split units: out = sum_q 2^(m_q - M) O_q / sum_q 2^(m_q - M) l_q
 // over the pieces q, M their largest maximum (a piece whose l is 0 saw no key of
-// the row).  One CTA per (unit and row group, row).
+// the row).  One CTA per (unit and row group, row): D / 4 threads take 16 bytes of
+// the row each, and blockDim.x / (D / 4) such teams take the pieces in turn, so a
+// unit cut into many pieces has many loads in flight.
+constexpr int kMergeThreads = 512;
+
 template <int D, int N>
-__global__ void __launch_bounds__(D / 4) paged_fp8_merge_kernel(const PagedFp8Params p,
-                                                                const Plan plan) {
+__global__ void __launch_bounds__(kMergeThreads) paged_fp8_merge_kernel(
+    const __grid_constant__ PagedFp8Params p, const Plan plan) {
+    constexpr int T = D / 4;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int u = blockIdx.x, r = blockIdx.y;
     const int rg = u % plan.groups, bc = u / plan.groups;
     const int b = bc / p.kv_heads, c = bc % p.kv_heads;
     const long long ctx = p.context_lengths[b];
-    const int4 e = plan.units[u];
+    const int2 e = plan.first[u];
+    const int np = plan.last[u] - e.x + 1;
     const int ur = rg * N + r;
     if (ctx < 0 || ctx + p.k > p.capacity || ur >= p.group * p.k) return;
-    const int np = e.y;
-    if (np == 0) return;   // whole: written already
-    // an entry that the attention grid did not write this time (it gave up before)
-    if (e.x < 0 || np < 0 || np > kMaxPieces || e.x > plan.ranges - np || (e.z & ~1)) {
+    if (e.y < 0) return;   // whole: written already
+    // entries that the attention grid did not write this time (it gave up before)
+    if (e.x < 0 || np < 2 || np > kMaxPieces || e.x > plan.ranges - np || e.y > 1) {
         if (threadIdx.x == 0) set_status(p.dev_status, CARAT_DEV_TIMEOUT);
         return;
     }
     auto piece = [&](int q) -> size_t {
-        return ((size_t)((e.x + q) * plan.groups + rg) * 2 + (q == 0 ? e.z : 0)) * N + r;
+        return ((size_t)((e.x + q) * plan.groups + rg) * 2 + (q == 0 ? e.y : 0)) * N + r;
     };
     __shared__ float s_w[kMaxPieces];
+    __shared__ float4 s_o[kMergeThreads];
     const int lane = threadIdx.x % 32;
     if (threadIdx.x < 32) {
-        float M = -INFINITY;
-        for (int q = lane; q < np; q += 32) {
-            const float2 v = plan.part_ml[piece(q)];
-            if (v.y != 0.f) M = fmaxf(M, v.x);
+        float2 v[kMaxPieces / 32];
+        float M = kUnset;
+#pragma unroll
+        for (int i = 0; i < kMaxPieces / 32; ++i) {
+            const int q = lane + 32 * i;
+            v[i] = q < np ? plan.part_ml[piece(q)] : make_float2(kUnset, 0.f);
         }
+#pragma unroll
+        for (int i = 0; i < kMaxPieces / 32; ++i)
+            if (v[i].y != 0.f) M = fmaxf(M, v[i].x);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, o));
         float sum = 0.f;
-        for (int q = lane; q < np; q += 32) {
-            const float2 v = plan.part_ml[piece(q)];
-            const float w = v.y != 0.f ? fast_exp2(v.x - M) : 0.f;
-            s_w[q] = w;
-            sum = fmaf(w, v.y, sum);
+#pragma unroll
+        for (int i = 0; i < kMaxPieces / 32; ++i) {
+            v[i].x = v[i].y != 0.f ? fast_exp2(v[i].x - M) : 0.f;
+            sum = fmaf(v[i].x, v[i].y, sum);
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
         const float inv = 1.f / sum;
-        for (int q = lane; q < np; q += 32) s_w[q] *= inv;
+#pragma unroll
+        for (int i = 0; i < kMaxPieces / 32; ++i)
+            if (lane + 32 * i < np) s_w[lane + 32 * i] = v[i].x * inv;
     }
-    __syncthreads();
+    const int team = threadIdx.x / T, teams = blockDim.x / T, d = threadIdx.x % T;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int q0 = 0; q0 < np; q0 += 8) {
+#pragma unroll 1
+    for (int q0 = team; q0 < np; q0 += 8 * teams) {
         float4 v[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            if (q0 + i < np)
-                v[i] = reinterpret_cast<const float4 *>(plan.part_o + piece(q0 + i) * D)[threadIdx.x];
+            if (q0 + i * teams < np)
+                v[i] = reinterpret_cast<const float4 *>(plan.part_o + piece(q0 + i * teams) * D)[d];
+        if (q0 == team) __syncthreads();   // the weights, once the first loads are on their way
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            if (q0 + i >= np) continue;
-            const float w = s_w[q0 + i];
+            if (q0 + i * teams >= np) continue;
+            const float w = s_w[q0 + i * teams];
             if (w == 0.f) continue;
             acc.x = fmaf(v[i].x, w, acc.x);
             acc.y = fmaf(v[i].y, w, acc.y);
@@ -1043,11 +1159,21 @@ __global__ void __launch_bounds__(D / 4) paged_fp8_merge_kernel(const PagedFp8Pa
             acc.w = fmaf(v[i].w, w, acc.w);
         }
     }
+    if (team >= np) __syncthreads();
+    if (teams > 1) {
+        s_o[threadIdx.x] = acc;
+        __syncthreads();
+        if (team > 0) return;
+        for (int i = 1; i < teams; ++i) {
+            const float4 v = s_o[i * T + d];
+            acc.x += v.x, acc.y += v.y, acc.z += v.z, acc.w += v.w;
+        }
+    }
     const int j = ur / p.group;
     const size_t row = ((size_t)b * p.k + j) * p.q_heads + (size_t)c * p.group + ur - j * p.group;
     const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x, acc.y);
     const __nv_bfloat162 hi = __floats2bfloat162_rn(acc.z, acc.w);
-    reinterpret_cast<uint2 *>(p.out + row * D)[threadIdx.x] =
+    reinterpret_cast<uint2 *>(p.out + row * D)[d] =
         make_uint2(*reinterpret_cast<const uint32_t *>(&lo), *reinterpret_cast<const uint32_t *>(&hi));
 }
 
@@ -1072,8 +1198,8 @@ Sizes sizes_of(int batch, int k, int q_heads, int kv_heads, int head_dim) {
     const size_t slots = (size_t)z.grid * 2 * z.n;
     z.ml = align256(slots * sizeof(float2));
     z.o = align256(slots * (size_t)head_dim * sizeof(float));
-    z.units = align256((size_t)batch * kv_heads * z.groups * sizeof(int4));
-    z.total = z.ml + z.o + z.units;
+    z.units = align256((size_t)batch * kv_heads * z.groups * sizeof(int2));
+    z.total = z.ml + z.o + z.units + align256((size_t)batch * kv_heads * z.groups * sizeof(int));
     return z;
 }
 
@@ -1086,7 +1212,8 @@ cudaError_t launch(const PagedFp8Params &p, const Sizes &z, cudaStream_t stream)
     char *w = static_cast<char *>(p.workspace);
     plan.part_ml = reinterpret_cast<float2 *>(w);
     plan.part_o = reinterpret_cast<float *>(w + z.ml);
-    plan.units = reinterpret_cast<int4 *>(w + z.ml + z.o);
+    plan.first = reinterpret_cast<int2 *>(w + z.ml + z.o);
+    plan.last = reinterpret_cast<int *>(w + z.ml + z.o + z.units);
     // (128 d, rows, 128-d block, head); a stage is 128 rows of one block
     CUtensorMap map_k{}, map_v{};
     const uint64_t row = (uint64_t)p.kv_heads * D;
@@ -1113,7 +1240,11 @@ cudaError_t launch(const PagedFp8Params &p, const Sizes &z, cudaStream_t stream)
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(p.batch * p.kv_heads * z.groups, N);
-    cfg.blockDim = dim3(D / 4);
+    // a unit is cut into about ranges / units + 1 pieces: a team for every eight
+    const int pieces = plan.ranges / (p.batch * p.kv_heads) + 1;
+    int teams = 1;
+    while (teams < kMergeThreads / (D / 4) && pieces > 8 * teams) teams *= 2;
+    cfg.blockDim = dim3(D / 4 * teams);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -15,11 +15,11 @@ def request_tiles(ctx, k, window, capacity):
     return first, (ctx + k - 1) // KEYS - first + 1
 
 
-def locate(tiles, kv_heads, ranges, rix):
+def locate(tiles, kv_heads, ranges, rix, unit_charge):
     """As the kernel's first warp does it, 32 requests a pass."""
     total = sum(tiles) * kv_heads
     units = sum(t > 0 for t in tiles) * kv_heads
-    charge = 1 if total >= ranges else 0
+    charge = unit_charge if total >= ranges else 0
     cost = total + charge * units
     length = max((cost + ranges - 1) // ranges, charge + 1)
     x0 = rix * length
@@ -39,26 +39,25 @@ def locate(tiles, kv_heads, ranges, rix):
                     j = (x - lo) // per
                     r = x - lo - j * per
                     o = 0 if r <= charge else r - charge
-                    found[which] = (tlo + j * v + o, lo + j * per, b, j, o)
+                    found[which] = (tlo + j * v + o, b, j, o)
             lo += vc
             tlo += kv_heads * v
         cum_cost, cum_tiles = lo, tlo
-    s, ucost, b0, c0, off0 = found.get(0, (total, 0, 0, 0, 0))
+    s, b0, c0, off0 = found.get(0, (total, 0, 0, 0))
     e = found[1][0] if 1 in found else total
-    return dict(s=s, e=e, ucost=ucost, b=b0, c=c0, off=off0, len=length, charge=charge)
+    return dict(s=s, e=e, b=b0, c=c0, off=off0)
 
 
 def segments(st, tiles, kv_heads):
-    pos, end, b, c, off, ucost = st["s"], st["e"], st["b"], st["c"], st["off"], st["ucost"]
+    pos, end, b, c, off = st["s"], st["e"], st["b"], st["c"], st["off"]
     n = tiles[b] if pos < end else 0
     while pos < end and off < n:
         ln = min(n - off, end - pos)
-        yield dict(b=b, c=c, x0=off, x1=off + ln, n=n, opens=pos == st["s"], ucost=ucost)
+        yield dict(b=b, c=c, x0=off, x1=off + ln, n=n, opens=pos == st["s"])
         pos += ln
         off += ln
         if off == n and pos < end:
             off = 0
-            ucost += n + st["charge"]
             c += 1
             if c == kv_heads:
                 c, n = 0, 0
@@ -84,9 +83,10 @@ def test_every_tile_once_and_every_piece_found(seed):
             assert first * KEYS <= lowest < (first + 1) * KEYS
             assert (first + t - 1) * KEYS <= c + k - 1 < (first + t) * KEYS
     ranges = rng.choice([152, 76, 50, 38, 7, 1])
-    seen, pieces, table, next_s = {}, {}, {}, 0
+    charge = rng.choice([1, 2, 3])
+    seen, pieces, table, lasts, next_s = {}, {}, {}, {}, 0
     for rix in range(ranges):
-        st = locate(tiles, kv_heads, ranges, rix)
+        st = locate(tiles, kv_heads, ranges, rix, charge)
         assert st["s"] == next_s
         next_s = st["e"]
         segs = list(segments(st, tiles, kv_heads))
@@ -99,8 +99,9 @@ def test_every_tile_once_and_every_piece_found(seed):
                 seen[(u, x)] = rix
             whole = s["x0"] == 0 and s["x1"] == s["n"]
             if s["x0"] == 0:
-                last = min((s["ucost"] + st["charge"] + s["n"] - 1) // st["len"], ranges - 1)
-                table[u] = (rix, 0 if whole else last - rix + 1, 0 if s["opens"] else 1)
+                table[u] = (rix, -1 if whole else 0 if s["opens"] else 1)
+            if s["x1"] == s["n"]:
+                lasts[u] = rix
             if not whole:
                 slot = 0 if s["opens"] else 1
                 assert slot not in partial_slots
@@ -112,10 +113,12 @@ def test_every_tile_once_and_every_piece_found(seed):
             assert all(((b, c), x) in seen for x in range(t))
             if t == 0:
                 continue
-            first, n, slot = table[(b, c)]
-            if n == 0:
-                assert (b, c) not in pieces
+            first, slot = table[(b, c)]
+            n = lasts[(b, c)] - first + 1
+            if slot < 0:
+                assert (b, c) not in pieces and n == 1
             else:
+                assert n >= 2
                 assert pieces[(b, c)] == [(first + q, slot if q == 0 else 0) for q in range(n)]
                 assert n <= 256
 
