@@ -82,12 +82,13 @@ struct Lay {
     static constexpr int kOffP = kOffQ + KS * kQBlock;
     static constexpr int kOffRed = kOffP + 2 * kPBytes;
     // floats: the four key quarters' maxima or sums per row, the running
-    // maxima, the rescale factors, the query scales of two segments
-    static constexpr int kRedM = 4 * N, kRedAlpha = 5 * N, kRedQ = 6 * N, kRedRow = 8 * N;
-    static constexpr int kRedFloats = 10 * N;         // last 2 N: output rows (int)
+    // maxima, the rescale factors, and of two segments the score factors and
+    // output rows (int) of the queries
+    static constexpr int kRedM = 4 * N, kRedAlpha = 5 * N, kRedQ = 6 * N;
+    static constexpr int kRedFloats = 10 * N;
     static constexpr int kOffSc = kOffRed + kRedFloats * 4;      // [kSlots][2][8] scales
     static constexpr int kOffBar = kOffSc + kSlots * 64;
-    static constexpr int kBars = 2 * NS + 8 + 2 * kSlots;
+    static constexpr int kBars = 2 * NS + 12 + 2 * kSlots;
     static constexpr int kOffMisc = kOffBar + kBars * 8;
     static constexpr int kBytes = kOffMisc + 128;
     static constexpr int kAlloc = kBytes + 1024;
@@ -101,7 +102,17 @@ struct Lay {
     static_assert(kOffQ % 1024 == 0 && kOffP % 1024 == 0 && kQBlock % 1024 == 0, "swizzle");
 };
 
+// A unit and row group's queries as the split launch leaves them: the Q operand
+// as it lies in shared memory, then each row's score factor, then its row in the
+// output (-1: none).
+template <int D, int N>
+struct Image {
+    static constexpr int kOperand = D / 128 * 2 * N * 128;
+    static constexpr int kBytes = kOperand + 2 * N * 4;
+};
+
 struct Plan {
+    uint8_t *images;    // [B * Hkv * groups] Image
     int groups;     // row groups of a unit
     int ranges;     // ranges of the tile sequence (grid = ranges * groups)
     float2 *part_ml;    // [2 * grid][N] (max, sum)
@@ -466,33 +477,41 @@ __device__ __forceinline__ float split_query(uint8_t *s_q, const uint16_t *row, 
     return top >= 0x7f800000u ? __int_as_float(0x7fc00000) : __int_as_float((127 - s) << 23);
 }
 
-// A segment's queries, rows r0 .. r0 + N / 2 of it, by four warps in turn; the
-// rows' score factors and their places in the output.
+// The queries of every unit and row group as 8-bit pieces (Image), and NaN outputs
+// for the requests that are rejected on the device.  One CTA per unit and row
+// group, a warp per row in turn.  It runs ahead of the attention, which starts
+// loading keys meanwhile: there each CTA fetches an image with one copy when it
+// comes to the unit, where splitting rows in place took the softmax 5000 to 8000
+// cycles at every unit's start.
 template <int D, int N>
-__device__ __noinline__ void split_queries(const PagedFp8Params &p, uint8_t *s_q, float *s_qs,
-                                           int *s_row, int b, int c, int row0, int rows_here,
-                                           int r0, int q4, int lane) {
-    // each lane touches one 128-byte line of the warp's rows, so that they all
-    // come at once
-    constexpr int kLines = D / 64;
-    if (lane < N / 8 * kLines) {
-        const int r = r0 + q4 + 4 * (lane / kLines), ur = row0 + r, j = ur / p.group;
-        if (r < rows_here) {
-            const uint16_t *a = p.q + ((size_t)(b * p.k + j) * p.q_heads + c * p.group + ur -
-                                       j * p.group) * D + lane % kLines * 64;
-            asm volatile("{\n\t.reg .u32 x;\n\tld.global.u32 x, [%0];\n\t}" ::"l"(a));
+__global__ void __launch_bounds__(256) paged_fp8_split_kernel(
+    const __grid_constant__ PagedFp8Params p, const Plan plan) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int u = blockIdx.x, rg = u % plan.groups, bc = u / plan.groups;
+    const int b = bc / p.kv_heads, c = bc % p.kv_heads;
+    const long long ctx = p.context_lengths[b];
+    const bool ok = ctx >= 0 && ctx + p.k <= p.capacity;
+    if (!ok && threadIdx.x == 0 && c == 0 && rg == 0) set_status(p.dev_status, CARAT_DEV_BAD_CONTEXT);
+    uint8_t *image = plan.images + (size_t)u * Image<D, N>::kBytes;
+    float *factor = reinterpret_cast<float *>(image + Image<D, N>::kOperand);
+    int *out_row = reinterpret_cast<int *>(factor + N);
+    for (int r = warp; r < N; r += 8) {
+        const int ur = rg * N + r, j = ur / p.group;
+        const int at = ur < p.group * p.k
+                           ? (b * p.k + j) * p.q_heads + c * p.group + ur - j * p.group
+                           : -1;
+        if (!ok) {
+            if (at >= 0)
+                for (int i = lane; i < D / 2; i += 32)
+                    reinterpret_cast<uint32_t *>(p.out + (size_t)at * D)[i] = 0x7fc07fc0u;
+            continue;
         }
-    }
-#pragma unroll 1
-    for (int r = r0 + q4; r < r0 + N / 2; r += 4) {
-        const int ur = row0 + r, j = ur / p.group;
-        const int at =
-            r < rows_here ? (b * p.k + j) * p.q_heads + c * p.group + ur - j * p.group : -1;
         const float f =
-            split_query<D, N>(s_q, at >= 0 ? p.q + (size_t)at * D : nullptr, r, lane);
+            split_query<D, N>(image, at >= 0 ? p.q + (size_t)at * D : nullptr, r, lane);
         if (lane == 0) {
-            s_qs[r] = f * p.scale_log2;
-            s_row[r] = at;
+            factor[r] = f * p.scale_log2;
+            out_row[r] = at;
         }
     }
 }
@@ -515,9 +534,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t *s_full = empty + NS;      // [2] scores of a tile ready
     uint64_t *p_full = s_full + 2;      // [2] weights of a tile written
     uint64_t *o_done = s_full + 4;      // [2] PV product of a tile done
-    uint64_t *q_full = s_full + 6;      // queries of a segment written
-    uint64_t *fin = s_full + 7;
-    uint64_t *sc_full = s_full + 8;     // [kSlots] scales of a tile fetched
+    uint64_t *q_full = s_full + 6;      // [2] queries of a segment landed
+    uint64_t *q_empty = s_full + 8;     // last QK product of a segment done
+    uint64_t *q_free = s_full + 9;      // [2] factors of a segment's queries used
+    uint64_t *fin = s_full + 11;
+    uint64_t *sc_full = s_full + 12;    // [kSlots] scales of a tile fetched
     uint64_t *sc_empty = sc_full + kSlots;
     uint8_t *s_q = smem + L::kOffQ;
     uint8_t *s_p = smem + L::kOffP;
@@ -550,8 +571,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc::mbar_init(&s_full[i], 1);
                 tc::mbar_init(&p_full[i], kSoftWarps);
                 tc::mbar_init(&o_done[i], 1);
+                tc::mbar_init(&q_full[i], 1);
+                tc::mbar_init(&q_free[i], kSoftWarps);
             }
-            tc::mbar_init(q_full, kSoftWarps);
+            tc::mbar_init(q_empty, 1);
             tc::mbar_init(fin, 1);
             for (int i = 0; i < kSlots; ++i) {
                 tc::mbar_init(&sc_full[i], 1);
@@ -594,12 +617,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             long long prev_row = 0;
             int prev_c = 0;
             bool prev = false;
-            // K of a tile before V of the one in front of it
+            // K of a tile before V of the one in front of it, but for a segment's
+            // last tile, whose V comes first
             while (alive) {
                 long long row = 0;
-                int c = 0;
-                const bool cur = have;
-                if (have) {
+                const bool cur = have, first = cur && x == sg.x0;
+                const int c = sg.c;
+                if (cur) {
                     const int tile = sg.first + x, want = tile / pages_shift_tiles;
                     if (want != pi) {
                         page = want == pi_next
@@ -617,8 +641,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                         set_status(status, CARAT_DEV_BAD_CACHE_ID);
                         row = (long long)p.num_pages * p.page_rows;
                     }
-                    c = sg.c;
-                    issue(&map_k, row, c);
                     if (++x == sg.x1) {
                         const int b_was = sg.b;
                         have = it.next(p, sg);
@@ -626,7 +648,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (have && sg.b != b_was) pi = pi_next = -1;
                     }
                 }
-                if (prev) issue(&map_v, prev_row, prev_c);
+#pragma unroll 1
+                for (int z = 0; z < 2; ++z) {
+                    const bool is_k = (z == 0) != (first && prev);
+                    if (is_k && cur) issue(&map_k, row, c);
+                    if (!is_k && prev) issue(&map_v, prev_row, prev_c);
+                }
                 prev = cur;
                 prev_row = row;
                 prev_c = c;
@@ -642,17 +669,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (warp == 1) {
             tc::tmem_alloc(&sh->tmem, L::kTmem);
             tc::tmem_relinquish();
-        } else if (warp >= 4) {
-            // requests rejected on the device: NaN and a status bit
-            for (int b = blockIdx.x; b < p.batch; b += gridDim.x) {
-                const long long ctx = p.context_lengths[b];
-                if (ctx >= 0 && ctx + p.k <= p.capacity) continue;
-                const int t = threadIdx.x - 128;
-                if (t == 0) set_status(status, CARAT_DEV_BAD_CONTEXT);
-                const size_t per = (size_t)p.k * p.q_heads * D / 2;
-                uint32_t *o = reinterpret_cast<uint32_t *>(p.out) + (size_t)b * per;
-                for (size_t i = t; i < per; i += kSoftWarps * 32) o[i] = 0x7fc07fc0u;
-            }
         }
         tc::tc_fence_before();
         asm volatile("bar.sync 3, %0;" ::"n"(kThreads) : "memory");
@@ -691,53 +707,60 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool prev = false, prev_first = false;   // the tile whose PV product is due
         while (alive) {
             const bool cur = have, first = cur && x == sg.x0;
-            if (cur) {
-                // S^T[g & 1] = K . [q_hi | q_lo]^T
-                if (first && !(alive = wait_all(q_full, si & 1))) break;
-                const uint32_t d = tmem + (g & 1) * 2 * N;
-                uint64_t q = q_desc;
+            // The loads' order: QK of a tile before PV of the one in front of it, but
+            // at a segment's start PV first, so that its output can be read out.
 #pragma unroll 1
-                for (int ks = 0; ks < KS; ++ks) {
-                    if (!(alive = wait_all(&full[ms], mphase))) break;
-                    tc::tc_fence_after();
-                    const uint64_t a = k_desc + (uint32_t)ms * (kStage / 16);
-#pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)
-                        tc::mma_f8_ss_warp(d, a + 2 * kk, q + 2 * kk, idesc_qk, (ks | kk) != 0);
-                    tc::mma_commit_warp(&empty[ms]);
-                    q += L::kQBlock / 16;
-                    advance();
-                }
-                if (!alive) break;
-                tc::mma_commit_warp(&s_full[g & 1]);
-                if (first) ++si;
-                if (++x == sg.x1) {
-                    have = it.next(p, sg);
-                    x = have ? sg.x0 : 0;
-                }
-            }
-            if (prev) {
-                // O^T += V^T . [w1 | w2 | w3]^T of the tile before
-                const uint32_t h = g - 1;
-                if (!(alive = wait_all(&p_full[h & 1], (h >> 1) & 1))) break;
-                tc::tc_fence_after();
-                const uint64_t w = p_desc + (h & 1) * (L::kPBytes / 16);
-                uint32_t d = tmem + L::kTmemO;
+            for (int z = 0; z < 2 && alive; ++z) {
+                const bool qk = (z == 0) != (first && prev);
+                if (qk && cur) {
+                    // S^T[g & 1] = K . [q_hi | q_lo]^T
+                    if (first && !(alive = wait_all(&q_full[si & 1], (si >> 1) & 1))) break;
+                    const uint32_t d = tmem + (g & 1) * 2 * N;
+                    uint64_t q = q_desc;
 #pragma unroll 1
-                for (int vs = 0; vs < KS; ++vs) {
-                    if (!(alive = wait_all(&full[ms], mphase))) break;
-                    tc::tc_fence_after();
-                    const uint64_t a = v_desc + (uint32_t)ms * (kStage / 16);
+                    for (int ks = 0; ks < KS; ++ks) {
+                        if (!(alive = wait_all(&full[ms], mphase))) break;
+                        tc::tc_fence_after();
+                        const uint64_t a = k_desc + (uint32_t)ms * (kStage / 16);
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)
-                        tc::mma_f8_ss_warp(d, a + 256 * kk, w + 2 * kk, idesc_pv,
-                                      !(prev_first && kk == 0));
-                    tc::mma_commit_warp(&empty[ms]);
-                    d += 3 * N;
-                    advance();
+                        for (int kk = 0; kk < 4; ++kk)
+                            tc::mma_f8_ss_warp(d, a + 2 * kk, q + 2 * kk, idesc_qk, (ks | kk) != 0);
+                        tc::mma_commit_warp(&empty[ms]);
+                        q += L::kQBlock / 16;
+                        advance();
+                    }
+                    if (!alive) break;
+                    tc::mma_commit_warp(&s_full[g & 1]);
+                    if (first) ++si;
+                    if (++x == sg.x1) {
+                        tc::mma_commit_warp(q_empty);
+                        have = it.next(p, sg);
+                        x = have ? sg.x0 : 0;
+                    }
                 }
-                if (!alive) break;
-                tc::mma_commit_warp(&o_done[h & 1]);
+                if (!qk && prev) {
+                    // O^T += V^T . [w1 | w2 | w3]^T of the tile before
+                    const uint32_t h = g - 1;
+                    if (!(alive = wait_all(&p_full[h & 1], (h >> 1) & 1))) break;
+                    tc::tc_fence_after();
+                    const uint64_t w = p_desc + (h & 1) * (L::kPBytes / 16);
+                    uint32_t d = tmem + L::kTmemO;
+#pragma unroll 1
+                    for (int vs = 0; vs < KS; ++vs) {
+                        if (!(alive = wait_all(&full[ms], mphase))) break;
+                        tc::tc_fence_after();
+                        const uint64_t a = v_desc + (uint32_t)ms * (kStage / 16);
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk)
+                            tc::mma_f8_ss_warp(d, a + 256 * kk, w + 2 * kk, idesc_pv,
+                                               !(prev_first && kk == 0));
+                        tc::mma_commit_warp(&empty[ms]);
+                        d += 3 * N;
+                        advance();
+                    }
+                    if (!alive) break;
+                    tc::mma_commit_warp(&o_done[h & 1]);
+                }
             }
             if (!cur) break;
             prev = true;
@@ -792,6 +815,34 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (lane == 0) tc::mbar_arrive(&sc_full[slot]);
             }
         }
+    } else if (warp == 3) {
+        // ------------------------------------------------------------ queries
+        // Each segment's queries as the split launch left them, once the last QK
+        // product of the segment before has read its own.
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        if (lane == 0) {
+            SegIter it;
+            it.init(p, sh);
+            Segment sg;
+            bool alive = true;
+            int si = 0;
+            for (; it.next(p, sg); ++si) {
+                alive = (si < 1 || await(q_empty, (si - 1) & 1, abort_flag, status)) &&
+                        (si < 2 || await(&q_free[si & 1], ((si - 2) >> 1) & 1, abort_flag, status));
+                if (!alive) break;
+                const uint8_t *image =
+                    plan.images + (((size_t)sg.b * p.kv_heads + sg.c) * plan.groups + rg) *
+                                      Image<D, N>::kBytes;
+                tc::mbar_arrive_expect_tx(&q_full[si & 1], Image<D, N>::kBytes);
+                tc::bulk_load(s_q, image, Image<D, N>::kOperand, &q_full[si & 1]);
+                tc::bulk_load(red + L::kRedQ + (si & 1) * 2 * N, image + Image<D, N>::kOperand,
+                              2 * N * 4, &q_full[si & 1]);
+            }
+            if (!alive || *abort_flag)   // the copies in flight land first
+                for (int i = si > 2 ? si - 2 : 0; i < si; ++i)
+                    tc::mbar_wait(&q_full[i & 1], (i >> 1) & 1, 100000000ull);
+        }
+        __syncwarp();
     } else if (warp >= 4) {
         // ------------------------------------------------------------ softmax
         const int half = (warp - 4) / 4, q4 = warp & 3;
@@ -803,17 +854,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int rows_here = min(N, p.group * p.k - row0);
         const int block = t / p.block_rows;
         float *red_max = red, *s_m = red + L::kRedM, *s_alpha = red + L::kRedAlpha;
-        float *s_qs = red + L::kRedQ;
-        int *s_row = reinterpret_cast<int *>(red + L::kRedRow);
-        const uint32_t total = (uint32_t)(sh->e - sh->s);
-
-        auto write_queries = [&](const Segment &sg, int si) {
-            split_queries<D, N>(p, s_q, s_qs + (si & 1) * N, s_row + (si & 1) * N, sg.b, sg.c, row0,
-                                rows_here, r0, q4, lane);
-            tc::fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) tc::mbar_arrive(q_full);
-        };
 
         SegIter it;
         it.init(p, sh);
@@ -821,8 +861,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool alive = true, have = it.next(p, sg);
         int si = 0;
         uint32_t g = 0;
-        if (have) write_queries(sg, 0);
-        half_any(half, false);
         while (have && alive) {
             // the next segment is looked up early, behind the first tile
             bool have_next = sg.x1 - sg.x0 == 1 && it.next(p, nx);
@@ -838,7 +876,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int e = 0; e < NC; ++e) nm[e] = 0.f, l[e] = 0.f;
             bool unset = true;   // some row has no maximum yet
-            const float *qs = s_qs + (si & 1) * N + r0;
+            const float *qs = red + L::kRedQ + (si & 1) * 2 * N + r0;
+            const int *out_row = reinterpret_cast<const int *>(qs) + N;
+            alive = __all_sync(kFull, await(&q_full[si & 1], (si >> 1) & 1, abort_flag, status));
             for (int x = sg.x0; x < sg.x1; ++x, ++g) {
                 const bool first = x == sg.x0;
                 const int slot = g % kSlots;
@@ -984,7 +1024,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // A tile with rows outside the request's keys: their V bytes must not
                     // meet a zero weight (0 x NaN), so they are zeroed.
                     if (t0 < lowest || t0 + kKeys > sg.ctx + p.k) {
-                        const uint32_t base = g + 1 < total ? KS * (2 * g + 2) : KS * (2 * g + 1);
+                        const uint32_t base = KS * (2 * g + (x + 1 < sg.x1 ? 2 : 1));
                         for (int z = half; z < KS; z += 2) {
                             const uint32_t c = base + z;
                             const int s = c % NS;
@@ -1009,9 +1049,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (!alive) break;
             // ------------------------------------------------ segment end
-            // While the last PV product runs: the next segment's queries (this one's
-            // last scores are there), and the rows' sums over the 128 keys.
-            if (have_next) write_queries(nx, si + 1);
+            // While the last PV product runs: the rows' sums over the 128 keys.
             float y[NC];
 #pragma unroll
             for (int e = 0; e < NC; ++e) y[e] = l[e];
@@ -1036,35 +1074,48 @@ __global__ void __launch_bounds__(kThreads, 1)
             // O of 8 rows and 128 d at a time: the pieces' sum, then the output row or
             // the partial.  Rolled: this code runs once a segment, from an instruction
             // cache that holds the tile loop, and its fetches are its cost.
-            const int *out_row = s_row + (si & 1) * N + r0;
-#pragma unroll 1
-            for (int i = 0; i < KS * (NC / 8); ++i) {
-                const int z = i / (NC / 8), e0 = i % (NC / 8) * 8;
+            const int parts = KS * ((min(rows_here - r0, NC) + 7) / 8);
+            auto pieces = [&](int i, float (&o)[8]) {
                 uint32_t o1[8], o2[8], o3[8];
-                const uint32_t at = tmem + L::kTmemO + z * 3 * N + lanes + r0 + e0;
+                const uint32_t at = tmem + L::kTmemO + i % KS * 3 * N + lanes + r0 + i / KS * 8;
                 tc::tmem_ld8(at, o1);
                 tc::tmem_ld8(at + N, o2);
                 tc::tmem_ld8(at + 2 * N, o3);
-                float *po = plan.part_o + (slot_row + e0) * D + z * 128 + t;
-                uint16_t *out = p.out + z * 128 + t;
                 tc::tmem_ld_wait();
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float o = fmaf(fmaf(__uint_as_float(o3[e]), 0.125f, __uint_as_float(o2[e])),
-                                         0.125f, __uint_as_float(o1[e]));
-                    if (whole) {
+                for (int e = 0; e < 8; ++e)
+                    o[e] = fmaf(fmaf(__uint_as_float(o3[e]), 0.125f, __uint_as_float(o2[e])), 0.125f,
+                                __uint_as_float(o1[e]));
+            };
+            if (whole) {
+#pragma unroll 1
+                for (int i = 0; i < parts; ++i) {
+                    float o[8];
+                    pieces(i, o);
+                    const int e0 = i / KS * 8;
+                    uint16_t *out = p.out + i % KS * 128 + t;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
                         const int ro = out_row[e0 + e];
                         const uint16_t h =
-                            __bfloat16_as_ushort(__float2bfloat16_rn(o * s_alpha[r0 + e0 + e]));
+                            __bfloat16_as_ushort(__float2bfloat16_rn(o[e] * s_alpha[r0 + e0 + e]));
                         if (ro >= 0) out[(size_t)ro * D] = h;
-                    } else {
-                        po[e * D] = o * (1.f / kWeight);
                     }
+                }
+            } else {
+#pragma unroll 1
+                for (int i = 0; i < parts; ++i) {
+                    float o[8];
+                    pieces(i, o);
+                    float *po = plan.part_o + (slot_row + i / KS * 8) * D + i % KS * 128 + t;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) po[e * D] = o[e] * (1.f / kWeight);
                 }
             }
             // all reads of the reduction area and of O come before the next segment's
             tc::tc_fence_before();
             half_any(half, false);
+            if (lane == 0) tc::mbar_arrive(&q_free[si & 1]);
             have = have_next;
             sg = nx;
             ++si;
@@ -1184,7 +1235,7 @@ int tile_rows(int rows) { return rows <= 16 ? 16 : 32; }
 
 struct Sizes {
     int n, groups, grid;
-    size_t ml, o, units, total;
+    size_t ml, o, units, last, total;
 };
 
 Sizes sizes_of(int batch, int k, int q_heads, int kv_heads, int head_dim) {
@@ -1198,8 +1249,11 @@ Sizes sizes_of(int batch, int k, int q_heads, int kv_heads, int head_dim) {
     const size_t slots = (size_t)z.grid * 2 * z.n;
     z.ml = align256(slots * sizeof(float2));
     z.o = align256(slots * (size_t)head_dim * sizeof(float));
-    z.units = align256((size_t)batch * kv_heads * z.groups * sizeof(int2));
-    z.total = z.ml + z.o + z.units + align256((size_t)batch * kv_heads * z.groups * sizeof(int));
+    const size_t count = (size_t)batch * kv_heads * z.groups;
+    z.units = align256(count * sizeof(int2));
+    z.last = align256(count * sizeof(int));
+    // Image<head_dim, n>
+    z.total = z.ml + z.o + z.units + z.last + align256(count * (2 * z.n * (head_dim + 4)));
     return z;
 }
 
@@ -1214,6 +1268,7 @@ cudaError_t launch(const PagedFp8Params &p, const Sizes &z, cudaStream_t stream)
     plan.part_o = reinterpret_cast<float *>(w + z.ml);
     plan.first = reinterpret_cast<int2 *>(w + z.ml + z.o);
     plan.last = reinterpret_cast<int *>(w + z.ml + z.o + z.units);
+    plan.images = reinterpret_cast<uint8_t *>(w + z.ml + z.o + z.units + z.last);
     // (128 d, rows, 128-d block, head); a stage is 128 rows of one block
     CUtensorMap map_k{}, map_v{};
     const uint64_t row = (uint64_t)p.kv_heads * D;
@@ -1234,23 +1289,33 @@ cudaError_t launch(const PagedFp8Params &p, const Sizes &z, cudaStream_t stream)
         if (e != cudaSuccess) return e;
         if (dev >= 0 && dev < 64) configured[dev].store(1, std::memory_order_release);
     }
-    kernel<<<z.grid, kThreads, L::kAlloc, stream>>>(p, plan, map_k, map_v);
+    const int units = p.batch * p.kv_heads * z.groups;
+    paged_fp8_split_kernel<D, N><<<units, 256, 0, stream>>>(p, plan);
     count_launches(1);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
+    // each of the next two may start while the launch before it drains, and waits
+    // for it where it needs its results
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(p.batch * p.kv_heads * z.groups, N);
-    // a unit is cut into about ranges / units + 1 pieces: a team for every eight
-    const int pieces = plan.ranges / (p.batch * p.kv_heads) + 1;
-    int teams = 1;
-    while (teams < kMergeThreads / (D / 4) && pieces > 8 * teams) teams *= 2;
-    cfg.blockDim = dim3(D / 4 * teams);
-    cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
+    cfg.stream = stream;
+    cfg.gridDim = dim3(z.grid);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = L::kAlloc;
+    e = cudaLaunchKernelEx(&cfg, kernel, p, plan, map_k, map_v);
+    count_launches(1);
+    if (e != cudaSuccess) return e;
+    cfg.dynamicSmemBytes = 0;
+    cfg.gridDim = dim3(units, N);
+    // a unit is cut into about ranges / units + 1 pieces: a team for every eight
+    const int pieces = plan.ranges / (p.batch * p.kv_heads) + 1;
+    int teams = 1;
+    while (teams < kMergeThreads / (D / 4) && pieces > 8 * teams) teams *= 2;
+    cfg.blockDim = dim3(D / 4 * teams);
     e = cudaLaunchKernelEx(&cfg, paged_fp8_merge_kernel<D, N>, p, plan);
     count_launches(1);
     return e;
