@@ -540,6 +540,26 @@ def _on_device(what, **tensors):
             raise ValueError(f"{what}: {name} must be on the current CUDA device")
 
 
+_BF16, _F32, _I32, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
+# The current stream's handle and the current device without the objects torch
+# makes for them (a call here is a few microseconds of host work in all).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda device: torch.cuda.current_stream(device).cuda_stream)
+_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
+def _stream_of(stream, device):
+    return _raw_stream(device) if stream is None else _stream(stream)
+
+
+def _plain(device, dtype, *tensors):
+    """Every tensor is a contiguous one of this type on this device."""
+    for t in tensors:
+        if not (t.dtype is dtype and t.get_device() == device and t.is_contiguous()):
+            return False
+    return True
+
+
 def _tokens(t, heads, head_dim, batch, k, name):
     """(pointer, token stride in elements) of a [B][k][heads][head_dim] tensor
     whose tokens are dense rows a fixed stride apart."""
@@ -572,6 +592,11 @@ def _paged_pool(key_pages, value_pages, page_table, context_lengths, dtype, batc
 
 def _block_scales(k_scales, v_scales, num_pages, page_rows, kv_heads, what):
     """block_rows from the shape of the scales [num_pages][blocks][kv_heads]."""
+    shape = k_scales.shape
+    if len(shape) == 3 and shape[0] == num_pages and shape[2] == kv_heads and shape[1] > 0 and \
+            page_rows % shape[1] == 0 and v_scales.shape == shape and \
+            k_scales.dtype is _F32 and v_scales.dtype is _F32:
+        return page_rows // shape[1]
     _expect(k_scales, torch.float32, f"{what}: k_scales")
     _expect(v_scales, torch.float32, f"{what}: v_scales")
     if k_scales.dim() != 3 or k_scales.shape != v_scales.shape or \
@@ -584,6 +609,63 @@ def _block_scales(k_scales, v_scales, num_pages, page_rows, kv_heads, what):
 def _rope_args(what, dtype, key_pages, value_pages, page_table, k_new, v_new, context_lengths,
                cos_sin, queries, queries_out, positions, new_counts, k_scales=None,
                v_scales=None):
+    """The entry points' arguments.  The usual layout is recognised at once; any
+    other goes through _rope_args_slow, which says what is wrong with it."""
+    slow = (what, dtype, key_pages, value_pages, page_table, k_new, v_new, context_lengths,
+            cos_sin, queries, queries_out, positions, new_counts, k_scales, v_scales)
+    try:
+        pool, new = key_pages.shape, k_new.shape
+        num_pages, page_rows, kv_heads, head_dim = pool
+        batch, k, h, d = new
+        strides = k_new.stride()
+        s0, s1, s2, s3 = strides
+        rows, max_pages = page_table.shape
+        table_rows, rotary_dim = cos_sin.shape
+        device = key_pages.get_device()
+        if not (h == kv_heads and d == head_dim and rows == batch and value_pages.shape == pool and
+                v_new.shape == new and v_new.stride() == strides and s3 == 1 and s2 == d and
+                s0 == k * s1 and k_new.dtype is _BF16 and v_new.dtype is _BF16 and
+                k_new.get_device() == device and v_new.get_device() == device and
+                device == _device() and context_lengths.shape == (batch,) and
+                _plain(device, dtype, key_pages, value_pages) and
+                _plain(device, _I32, page_table, context_lengths) and
+                _plain(device, _F32, cos_sin)):
+            return _rope_args_slow(*slow)
+        q_heads, qp, qo, q_stride = 0, None, None, 0
+        if queries is not None:
+            qshape = queries.shape
+            qb, qk, q_heads, qd = qshape
+            t0, q_stride, t2, t3 = queries.stride()
+            if not (qb == batch and qk == k and qd == d and t3 == 1 and t2 == d and
+                    t0 == k * q_stride and queries.dtype is _BF16 and
+                    queries.get_device() == device and queries_out.shape == qshape and
+                    _plain(device, _BF16, queries_out)):
+                return _rope_args_slow(*slow)
+            qp, qo = queries.data_ptr(), queries_out.data_ptr()
+        elif queries_out is not None:
+            return _rope_args_slow(*slow)
+        pp = cp = None
+        if positions is not None:
+            if positions.shape != (batch, k) or not _plain(device, _I32, positions):
+                return _rope_args_slow(*slow)
+            pp = positions.data_ptr()
+        if new_counts is not None:
+            if new_counts.shape != (batch,) or not _plain(device, _I32, new_counts):
+                return _rope_args_slow(*slow)
+            cp = new_counts.data_ptr()
+        if k_scales is not None and not _plain(device, _F32, k_scales, v_scales):
+            return _rope_args_slow(*slow)
+    except (AttributeError, TypeError, ValueError):
+        return _rope_args_slow(*slow)
+    return ((num_pages, page_table.data_ptr(), max_pages, page_rows),
+            (k_new.data_ptr(), v_new.data_ptr(), s1, qo, qp, q_stride, cos_sin.data_ptr(),
+             table_rows, rotary_dim),
+            (pp, cp, context_lengths.data_ptr(), k, batch, q_heads, kv_heads, head_dim), device)
+
+
+def _rope_args_slow(what, dtype, key_pages, value_pages, page_table, k_new, v_new,
+                    context_lengths, cos_sin, queries, queries_out, positions, new_counts,
+                    k_scales, v_scales):
     if k_new.dim() != 4:
         raise ValueError(f"{what}: k_new must be [batch][k][kv_heads][head_dim]")
     batch, k = k_new.shape[0], k_new.shape[1]
@@ -624,7 +706,9 @@ def _rope_args(what, dtype, key_pages, value_pages, page_table, k_new, v_new, co
             cos_sin.shape[1])
     rest = (_ptr(positions), _ptr(new_counts), _ptr(context_lengths), k, batch, q_heads, kv_heads,
             head_dim)
-    return head, tail, rest
+    for t in (key_pages, value_pages, k_scales, v_scales):
+        _ptr(t)
+    return head, tail, rest, key_pages.get_device()
 
 
 def carat_paged_rope_append(key_pages, value_pages, page_table, k_new, v_new, context_lengths, *,
@@ -640,12 +724,12 @@ def carat_paged_rope_append(key_pages, value_pages, page_table, k_new, v_new, co
     positions int32 [B][k] (angles only; default context_lengths[b] + j);
     new_counts int32 [B]: rows request b really appends (default k)."""
     what = "carat_paged_rope_append"
-    head, tail, rest = _rope_args(what, torch.bfloat16, key_pages, value_pages, page_table, k_new,
-                                  v_new, context_lengths, cos_sin, queries, queries_out, positions,
-                                  new_counts)
-    _check(library().carat_paged_rope_append(
-        _ptr(key_pages), _ptr(value_pages), *head, *tail, 1 if interleaved else 0, *rest,
-        _stream(stream)), what)
+    head, tail, rest, device = _rope_args(
+        what, _BF16, key_pages, value_pages, page_table, k_new, v_new, context_lengths, cos_sin,
+        queries, queries_out, positions, new_counts)
+    _check((_lib or library()).carat_paged_rope_append(
+        key_pages.data_ptr(), value_pages.data_ptr(), *head, *tail, 1 if interleaved else 0, *rest,
+        _stream_of(stream, device)), what)
 
 
 def carat_paged_rope_append_fp8(key_pages, value_pages, k_scales, v_scales, page_table, k_new,
@@ -659,14 +743,13 @@ def carat_paged_rope_append_fp8(key_pages, value_pages, k_scales, v_scales, page
     one that already held rows keeps its scale or grows it, its older bytes
     then being rounded to the new one."""
     what = "carat_paged_rope_append_fp8"
-    head, tail, rest = _rope_args(what, torch.uint8, key_pages, value_pages, page_table, k_new,
-                                  v_new, context_lengths, cos_sin, queries, queries_out, positions,
-                                  new_counts, k_scales, v_scales)
-    num_pages, page_rows, kv_heads, _ = key_pages.shape
-    block_rows = _block_scales(k_scales, v_scales, num_pages, page_rows, kv_heads, what)
-    _check(library().carat_paged_rope_append_fp8(
-        _ptr(key_pages), _ptr(value_pages), _ptr(k_scales), _ptr(v_scales), *head, block_rows,
-        *tail, 1 if interleaved else 0, *rest, _stream(stream)), what)
+    head, tail, rest, device = _rope_args(
+        what, _U8, key_pages, value_pages, page_table, k_new, v_new, context_lengths, cos_sin,
+        queries, queries_out, positions, new_counts, k_scales, v_scales)
+    block_rows = _block_scales(k_scales, v_scales, head[0], head[3], rest[6], what)
+    _check((_lib or library()).carat_paged_rope_append_fp8(
+        key_pages.data_ptr(), value_pages.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(),
+        *head, block_rows, *tail, 1 if interleaved else 0, *rest, _stream_of(stream, device)), what)
 
 
 def carat_global_verify_attention_paged(out, queries, key_pages, value_pages, page_table,
@@ -701,21 +784,50 @@ def carat_paged_verify_attention_fp8(out, queries, key_pages, value_pages, k_sca
     query's own, w > 0: the last w of them; workspace: a CUDA tensor of at
     least paged_fp8_workspace_bytes(...) bytes."""
     what = "carat_paged_verify_attention_fp8"
+    try:
+        shape, pool = queries.shape, key_pages.shape
+        batch, k, q_heads, head_dim = shape
+        num_pages, page_rows, kv_heads, cache_dim = pool
+        rows, max_pages = page_table.shape
+        device = queries.get_device()
+        usual = (cache_dim == head_dim and rows == batch and out.shape == shape and
+                 value_pages.shape == pool and context_lengths.shape == (batch,) and
+                 device == _device() and workspace.get_device() == device and
+                 workspace.is_contiguous() and _plain(device, _BF16, out, queries) and
+                 _plain(device, _U8, key_pages, value_pages) and
+                 _plain(device, _I32, page_table, context_lengths) and
+                 _plain(device, _F32, k_scales, v_scales))
+    except (AttributeError, TypeError, ValueError):
+        usual = False
+    if not usual:
+        _paged_fp8_explain(what, out, queries, key_pages, value_pages, k_scales, v_scales,
+                           page_table, context_lengths, workspace)
+    block_rows = _block_scales(k_scales, v_scales, num_pages, page_rows, kv_heads, what)
+    _check((_lib or library()).carat_paged_verify_attention_fp8(
+        out.data_ptr(), queries.data_ptr(), key_pages.data_ptr(), value_pages.data_ptr(),
+        k_scales.data_ptr(), v_scales.data_ptr(), num_pages, page_table.data_ptr(), max_pages,
+        page_rows, block_rows, context_lengths.data_ptr(), k, batch, q_heads, kv_heads, head_dim,
+        int(window), float(scale), workspace.data_ptr(),
+        workspace.numel() * workspace.element_size(), _stream_of(stream, device)), what)
+
+
+def _paged_fp8_explain(what, out, queries, key_pages, value_pages, k_scales, v_scales, page_table,
+                       context_lengths, workspace):
+    """Raises what is wrong with the arguments."""
     _expect(out, torch.bfloat16, f"{what}: out")
     _expect(queries, torch.bfloat16, f"{what}: queries")
     if queries.dim() != 4 or out.shape != queries.shape:
         raise ValueError(f"{what}: queries must be [batch][k][q_heads][head_dim], out alike")
-    batch, k, q_heads, head_dim = queries.shape
+    batch, head_dim = queries.shape[0], queries.shape[3]
     num_pages, page_rows, kv_heads, cache_dim = _paged_pool(
         key_pages, value_pages, page_table, context_lengths, torch.uint8, batch, what)
     if cache_dim != head_dim:
         raise ValueError(f"{what}: cache head_dim {cache_dim} != query head_dim {head_dim}")
-    block_rows = _block_scales(k_scales, v_scales, num_pages, page_rows, kv_heads, what)
+    _block_scales(k_scales, v_scales, num_pages, page_rows, kv_heads, what)
     _on_device(what, out=out, queries=queries, key_pages=key_pages, value_pages=value_pages,
                k_scales=k_scales, v_scales=v_scales, page_table=page_table,
                context_lengths=context_lengths, workspace=workspace)
-    _check(library().carat_paged_verify_attention_fp8(
-        _ptr(out), _ptr(queries), _ptr(key_pages), _ptr(value_pages), _ptr(k_scales),
-        _ptr(v_scales), num_pages, _ptr(page_table), page_table.shape[1], page_rows, block_rows,
-        _ptr(context_lengths), k, batch, q_heads, kv_heads, head_dim, int(window), float(scale),
-        _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream)), what)
+    for t in (out, queries, key_pages, value_pages, k_scales, v_scales, page_table,
+              context_lengths, workspace):
+        _ptr(t)
+    raise ValueError(f"{what}: arguments do not fit together")
