@@ -48,6 +48,7 @@ struct Piece {
     int freq;      // first of the eight frequencies; -1: not rotated
 };
 
+template <bool kInter>
 __device__ __forceinline__ Piece piece_of(const RopeParams &p, int c, bool rotated) {
     Piece t;
     t.a = 16 * c;
@@ -55,7 +56,7 @@ __device__ __forceinline__ Piece piece_of(const RopeParams &p, int c, bool rotat
     t.freq = -1;
     if (rotated && t.a < p.rotary_dim) {
         t.freq = 8 * c;
-        if (!p.interleaved) {
+        if (!kInter) {
             t.a = 8 * c;
             t.b = t.a + p.rotary_dim / 2;
         }
@@ -85,10 +86,11 @@ __device__ __forceinline__ void widen8(const uint4 &w, float *x) {
 }
 
 // x[0..8) and x[8..16): the thread's pieces, rotated in place.
-__device__ __forceinline__ void rotate16(float (&x)[16], const Angles &a, bool interleaved) {
+template <bool kInter>
+__device__ __forceinline__ void rotate16(float (&x)[16], const Angles &a) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        const int ia = interleaved ? 2 * i : i, ib = interleaved ? 2 * i + 1 : i + 8;
+        const int ia = kInter ? 2 * i : i, ib = kInter ? 2 * i + 1 : i + 8;
         const float u = x[ia], v = x[ib];
         x[ia] = fmaf(u, a.c[i], -(v * a.s[i]));
         x[ib] = fmaf(v, a.c[i], u * a.s[i]);
@@ -105,10 +107,22 @@ __device__ __forceinline__ uint4 narrow8(const float *x) {
                       bf16x2(x[6], x[7]));
 }
 
-// One thread's part of token (b, j)'s rows in a bf16 launch: chunks of 16
-// elements first, first + step, ... of the row of `heads` heads (queries,
-// then with `cache` keys and values).  step is a multiple of head_dim / 16,
-// so a thread keeps its place within a head and loads its angles once.
+// Chunks a thread has in flight in a call of many tokens (one in a call of few,
+// see spread), the CTAs of an SM the registers are fitted to, and the rows of an
+// e4m3 block in flight.  Measured on 8 ragged prompts of 2048 tokens, 16 + 2 x 8
+// heads x 256 (bf16 / e4m3 pages) and a chunk of 8191 tokens, 16 + 2 x 2 heads x
+// 512: 3 chunks at 4 CTAs 58.5 / 65.5 / 65.2 us (the bytes at the copy rate: 51.1 /
+// 44.8 / 49.4); 4 at 3 CTAs 60.7 / 68.8 / 60.7; 2 at 4 71.0 / 69.9 / 64.4; one at
+// a time 81.4 / 95.4 / 71.2.
+constexpr int kFlight = 3, kMany = 4, kFew = 4;
+constexpr int kRows = 2;
+
+// One thread's part of token (b, j)'s rows: chunks of 16 elements first,
+// first + step, ... of its rows (queries, then with `cache` keys and
+// values).  step is a multiple of head_dim / 16, so a thread keeps its place
+// within a head and loads its angles once.  The loads of F chunks go out
+// before the first is used.
+template <bool kInter, int F>
 __device__ __forceinline__ void move_token(const RopeParams &p, int b, int j, const Request &rq,
                                            int first, int step, bool cache) {
     const int per = p.head_dim / 16;
@@ -127,57 +141,85 @@ __device__ __forceinline__ void move_token(const RopeParams &p, int b, int j, co
     } else if (rq.ok) {
         return;   // a row behind the request's last: nothing is written
     }
-    const bool bad = trow < 0;   // rejected request, or a position outside the table
-    const Piece turned = piece_of(p, c, true), plain = piece_of(p, c, false);
-    Angles ang;
-    if (!bad && turned.freq >= 0) load_angles(p, trow, turned.freq, ang);
+    const Piece turned = piece_of<kInter>(p, c, true), plain = piece_of<kInter>(p, c, false);
     const int heads = p.q_heads + (cache ? 2 * p.kv_heads : 0);
-    for (int x = first; x < heads * per; x += step) {
-        const int h = x / per;
-        const bool is_q = h < p.q_heads;
-        const bool is_v = h >= p.q_heads + p.kv_heads;
-        const int hk = is_q ? h : is_v ? h - p.q_heads - p.kv_heads : h - p.q_heads;
-        uint16_t *dst;
-        const uint16_t *src;
-        if (is_q) {
-            src = p.q + token * p.q_stride + (size_t)h * p.head_dim;
-            dst = p.q_out + (token * p.q_heads + h) * p.head_dim;
-        } else {
-            if (drow < 0) continue;
-            src = (is_v ? p.v_new : p.k_new) + token * p.kv_stride + (size_t)hk * p.head_dim;
-            dst = reinterpret_cast<uint16_t *>(is_v ? p.v_pages : p.k_pages) +
-                  ((size_t)drow * p.kv_heads + hk) * p.head_dim;
+    const int hstep = step / per;
+    const uint16_t *q = p.q + token * p.q_stride;
+    uint16_t *q_out = p.q_out + token * p.q_heads * p.head_dim;
+    if (trow < 0) {   // rejected request, or a position outside the table
+        const uint4 nan = make_uint4(0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u);
+        for (int h = first / per; h < p.q_heads; h += hstep) {
+            *reinterpret_cast<uint4 *>(q_out + (size_t)h * p.head_dim + turned.a) = nan;
+            *reinterpret_cast<uint4 *>(q_out + (size_t)h * p.head_dim + turned.b) = nan;
         }
-        const Piece t = is_v ? plain : turned;
-        if (bad) {   // only queries come here
-            const uint4 nan = make_uint4(0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u);
-            *reinterpret_cast<uint4 *>(dst + t.a) = nan;
-            *reinterpret_cast<uint4 *>(dst + t.b) = nan;
-            continue;
+        return;
+    }
+    Angles ang;
+    if (turned.freq >= 0) load_angles(p, trow, turned.freq, ang);
+    // queries, keys and values are one run of heads; where head h comes from
+    // and goes to is formed again for the store rather than held in registers
+    const int v0 = p.q_heads + p.kv_heads;
+    const size_t kv = token * p.kv_stride, at = (size_t)drow * p.kv_heads * p.head_dim;
+    const int end = drow < 0 ? p.q_heads : heads;
+    for (int h0 = first / per; h0 < end; h0 += F * hstep) {
+        uint4 wa[F], wb[F];
+#pragma unroll
+        for (int i = 0; i < F; ++i) {
+            const int h = h0 + i * hstep;
+            if (h >= end) break;
+            const uint16_t *src = h < p.q_heads ? q + h * p.head_dim
+                                  : h < v0      ? p.k_new + kv + (h - p.q_heads) * p.head_dim
+                                                : p.v_new + kv + (h - v0) * p.head_dim;
+            wa[i] = __ldcs(reinterpret_cast<const uint4 *>(src + (h < v0 ? turned.a : plain.a)));
+            wb[i] = __ldcs(reinterpret_cast<const uint4 *>(src + (h < v0 ? turned.b : plain.b)));
         }
-        uint4 wa = *reinterpret_cast<const uint4 *>(src + t.a);
-        uint4 wb = *reinterpret_cast<const uint4 *>(src + t.b);
-        if (t.freq >= 0) {
-            float v[16];
-            widen8(wa, v);
-            widen8(wb, v + 8);
-            rotate16(v, ang, p.interleaved != 0);
-            wa = narrow8(v);
-            wb = narrow8(v + 8);
+#pragma unroll
+        for (int i = 0; i < F; ++i) {
+            const int h = h0 + i * hstep;
+            if (h >= end) break;
+            if (turned.freq >= 0 && h < v0) {
+                float v[16];
+                widen8(wa[i], v);
+                widen8(wb[i], v + 8);
+                rotate16<kInter>(v, ang);
+                wa[i] = narrow8(v);
+                wb[i] = narrow8(v + 8);
+            }
+            uint16_t *dst =
+                h < p.q_heads ? q_out + h * p.head_dim
+                : h < v0 ? reinterpret_cast<uint16_t *>(p.k_pages) + at + (h - p.q_heads) * p.head_dim
+                         : reinterpret_cast<uint16_t *>(p.v_pages) + at + (h - v0) * p.head_dim;
+            *reinterpret_cast<uint4 *>(dst + (h < v0 ? turned.a : plain.a)) = wa[i];
+            *reinterpret_cast<uint4 *>(dst + (h < v0 ? turned.b : plain.b)) = wb[i];
         }
-        *reinterpret_cast<uint4 *>(dst + t.a) = wa;
-        *reinterpret_cast<uint4 *>(dst + t.b) = wb;
     }
 }
 
-// bf16 pages: `splits` CTAs per token (b, j).
-__global__ void __launch_bounds__(kThreads) rope_append_kernel(const RopeParams p, int splits) {
-    const unsigned token = blockIdx.x / splits, part = blockIdx.x % splits;
+// How a launch spreads tokens over CTAs: `per_cta` tokens each, or (per_cta 1)
+// one token over `splits` CTAs.
+struct Spread {
+    int per_cta, splits;
+    bool many;
+};
+
+template <bool kInter, int F>
+__device__ __forceinline__ void move_tokens(const RopeParams &p, unsigned cta, Spread s,
+                                            bool cache) {
+    const int team = blockDim.x / s.per_cta;
+    const unsigned token = cta / s.splits * s.per_cta + threadIdx.x / team;
+    if (token >= (unsigned)p.batch * p.k) return;
     const int b = token / p.k, j = token % p.k;
     const Request rq = load_request(p, b);
-    if (!rq.ok && threadIdx.x == 0 && part == 0 && j == 0)
-        set_status(p.dev_status, CARAT_DEV_BAD_CONTEXT);
-    move_token(p, b, j, rq, part * blockDim.x + threadIdx.x, splits * blockDim.x, true);
+    const int first = cta % s.splits * blockDim.x + threadIdx.x % team;
+    if (!rq.ok && first == 0 && j == 0) set_status(p.dev_status, CARAT_DEV_BAD_CONTEXT);
+    move_token<kInter, F>(p, b, j, rq, first, s.splits * team, cache);
+}
+
+// bf16 pages.
+template <bool kInter, int F>
+__global__ void __launch_bounds__(kThreads, F == 1 ? kFew : kMany) rope_append_kernel(
+    const __grid_constant__ RopeParams p, Spread s) {
+    move_tokens<kInter, F>(p, blockIdx.x, s, true);
 }
 
 // Least e in [kExpMin, kExpMax] with amax <= 448 * 2^e (448 = 1.75 * 2^8).
@@ -230,14 +272,11 @@ __device__ __forceinline__ uint32_t requantise4(uint32_t w, float ratio) {
 // values that become subnormal (a power of two moves an e4m3 exponent only).
 // One CTA owns the block's rows of its head and their scale, so nothing is
 // shared between CTAs.
-__global__ void __launch_bounds__(kThreads) rope_append_fp8_kernel(const RopeParams p, int blocks,
-                                                                   unsigned kv_ctas, int splits) {
+template <bool kInter, int F>
+__global__ void __launch_bounds__(kThreads, F == 1 ? kFew : kMany) rope_append_fp8_kernel(
+    const __grid_constant__ RopeParams p, int blocks, unsigned kv_ctas, Spread s) {
     if (blockIdx.x >= kv_ctas) {
-        const unsigned id = blockIdx.x - kv_ctas;
-        const unsigned token = id / splits, part = id % splits;
-        const int b = token / p.k, j = token % p.k;
-        const Request rq = load_request(p, b);
-        move_token(p, b, j, rq, part * blockDim.x + threadIdx.x, splits * blockDim.x, false);
+        move_tokens<kInter, F>(p, blockIdx.x - kv_ctas, s, false);
         return;
     }
     unsigned id = blockIdx.x;
@@ -266,38 +305,53 @@ __global__ void __launch_bounds__(kThreads) rope_append_fp8_kernel(const RopePar
     const int per = p.head_dim / 16;
     const int rows = blockDim.x / per;   // rows a pass of the CTA covers
     const int c = threadIdx.x % per, r0 = threadIdx.x / per;
-    const Piece t = piece_of(p, c, !is_v);
+    const Piece t = piece_of<kInter>(p, c, !is_v);
     const uint16_t *src = is_v ? p.v_new : p.k_new;
     uint8_t *dst = reinterpret_cast<uint8_t *>(is_v ? p.v_pages : p.k_pages);
     float *scale_at = (is_v ? p.v_scales : p.k_scales) + (size_t)(row0 / R) * p.kv_heads + h;
 
-    // This thread's 16 values of position pos (false: outside the table).
-    auto values = [&](long long pos, float (&x)[16]) -> bool {
-        const int j = (int)(pos - rq.ctx);
-        const long long trow = table_row(p, b, j, rq.ctx);
+    // Rows pos, pos + rows, ... (kRows of them) of this thread: loaded together,
+    // and their values one by one (false: no such row, or no angle for it).
+    uint4 wa[kRows], wb[kRows];
+    auto load = [&](long long pos) {
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) {
+            if (pos + i * rows >= hi) break;
+            const uint16_t *s = src + ((size_t)b * p.k + (pos + i * rows - rq.ctx)) * p.kv_stride +
+                                (size_t)h * p.head_dim;
+            wa[i] = *reinterpret_cast<const uint4 *>(s + t.a);
+            wb[i] = *reinterpret_cast<const uint4 *>(s + t.b);
+        }
+    };
+    auto values = [&](int i, long long pos, float (&x)[16]) -> bool {
+        if (pos >= hi) return false;
+        const long long trow = table_row(p, b, (int)(pos - rq.ctx), rq.ctx);
         if (trow < 0) return false;
-        const uint16_t *s = src + ((size_t)b * p.k + j) * p.kv_stride + (size_t)h * p.head_dim;
-        widen8(*reinterpret_cast<const uint4 *>(s + t.a), x);
-        widen8(*reinterpret_cast<const uint4 *>(s + t.b), x + 8);
+        widen8(wa[i], x);
+        widen8(wb[i], x + 8);
         if (t.freq >= 0) {
             Angles a;
             load_angles(p, trow, t.freq, a);
-            rotate16(x, a, p.interleaved != 0);
+            rotate16<kInter>(x, a);
         }
         return true;
     };
 
     float amax = 0.f;
     bool any = false, outside = false;
-    for (long long pos = lo + r0; pos < hi; pos += rows) {
-        float x[16];
-        if (!values(pos, x)) {
-            outside = true;
-            continue;
-        }
-        any = true;
+    for (long long pos = lo + r0; pos < hi; pos += kRows * rows) {
+        load(pos);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) amax = fmaxf(amax, finite_abs(x[i]));
+        for (int i = 0; i < kRows; ++i) {
+            float x[16];
+            if (!values(i, pos + i * rows, x)) {
+                outside |= pos + i * rows < hi;
+                continue;
+            }
+            any = true;
+#pragma unroll
+            for (int e = 0; e < 16; ++e) amax = fmaxf(amax, finite_abs(x[e]));
+        }
     }
     if (outside && c == 0) set_status(p.dev_status, CARAT_DEV_BAD_POSITION);
     __shared__ float s_max[kThreads / 32];
@@ -323,17 +377,24 @@ __global__ void __launch_bounds__(kThreads) rope_append_fp8_kernel(const RopePar
                             requantise4(v.z, ratio), requantise4(v.w, ratio));
         }
     }
-    for (long long pos = lo + r0; pos < hi; pos += rows) {
-        float x[16];
-        if (!values(pos, x)) continue;
-        uint8_t *d = dst + ((size_t)(row0 + (pos - t0)) * p.kv_heads + h) * p.head_dim;
-        uint32_t o[4];
+    // Rows are read again (from cache) unless one load held them all.
+    const bool held = hi - lo <= kRows * rows;
+    for (long long pos = lo + r0; pos < hi; pos += kRows * rows) {
+        if (!held) load(pos);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            o[i] = e4m3x4(x[4 * i] * inv, x[4 * i + 1] * inv, x[4 * i + 2] * inv,
-                          x[4 * i + 3] * inv);
-        *reinterpret_cast<uint2 *>(d + t.a) = make_uint2(o[0], o[1]);
-        *reinterpret_cast<uint2 *>(d + t.b) = make_uint2(o[2], o[3]);
+        for (int i = 0; i < kRows; ++i) {
+            float x[16];
+            if (!values(i, pos + i * rows, x)) continue;
+            uint8_t *d =
+                dst + ((size_t)(row0 + (pos + i * rows - t0)) * p.kv_heads + h) * p.head_dim;
+            uint32_t o[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                o[e] = e4m3x4(x[4 * e] * inv, x[4 * e + 1] * inv, x[4 * e + 2] * inv,
+                              x[4 * e + 3] * inv);
+            *reinterpret_cast<uint2 *>(d + t.a) = make_uint2(o[0], o[1]);
+            *reinterpret_cast<uint2 *>(d + t.b) = make_uint2(o[2], o[3]);
+        }
     }
 }
 
@@ -350,14 +411,27 @@ int cta_threads(int head_dim) {
     return kThreads;
 }
 
-// CTAs a token's rows are spread over: enough that a call of few tokens
-// gives each thread one chunk.
-int token_splits(const RopeParams &p, int heads, int threads) {
-    const long long chunks = (long long)heads * (p.head_dim / 16);
-    const long long full = (chunks + threads - 1) / threads;
-    const long long tokens = (long long)p.batch * p.k;
-    const long long want = (8ll * 152 + tokens - 1) / tokens;
-    return (int)(want < full ? (want < 1 ? 1 : want) : full);
+// A call of many tokens gives a thread kFlight chunks or more of one token; a
+// call of few spreads each token over more CTAs while there are SMs without one
+// (64 requests x 4 proposals: 4.9 us with a CTA a token, 6.1 with three).
+Spread spread(const RopeParams &p, int heads, int threads) {
+    const int per = p.head_dim / 16;
+    const long long chunks = (long long)heads * per, tokens = (long long)p.batch * p.k;
+    Spread s{1, 1, tokens * chunks >= 152ll * 1024 * kFlight};
+    if (s.many) {
+        while (threads % (2 * s.per_cta) == 0 && threads / (2 * s.per_cta) % per == 0 &&
+               chunks * s.per_cta < (long long)kFlight * threads)
+            s.per_cta *= 2;
+    } else {
+        const long long full = (chunks + threads - 1) / threads;
+        const long long want = (152 + tokens - 1) / tokens;
+        s.splits = (int)(want < full ? want : full);
+    }
+    return s;
+}
+
+long long ctas(const RopeParams &p, Spread s) {
+    return ((long long)p.batch * p.k + s.per_cta - 1) / s.per_cta * s.splits;
 }
 
 }  // namespace
@@ -366,23 +440,29 @@ bool rope_shape_ok(int head_dim) { return head_dim <= 1024 && cta_threads(head_d
 
 cudaError_t launch_rope_append(const RopeParams &p, cudaStream_t stream) {
     const int threads = cta_threads(p.head_dim);
-    const int splits = token_splits(p, p.q_heads + 2 * p.kv_heads, threads);
-    const long long grid = (long long)p.batch * p.k * splits;
+    const Spread s = spread(p, p.q_heads + 2 * p.kv_heads, threads);
+    const long long grid = ctas(p, s);
     if (grid >= (1ll << 31)) return cudaErrorInvalidValue;
-    rope_append_kernel<<<(unsigned)grid, threads, 0, stream>>>(p, splits);
+    auto kernel = s.many ? (p.interleaved ? rope_append_kernel<true, kFlight>
+                                          : rope_append_kernel<false, kFlight>)
+                         : (p.interleaved ? rope_append_kernel<true, 1> : rope_append_kernel<false, 1>);
+    kernel<<<(unsigned)grid, threads, 0, stream>>>(p, s);
     count_launches(1);
     return cudaGetLastError();
 }
 
 cudaError_t launch_rope_append_fp8(const RopeParams &p, cudaStream_t stream) {
     const int threads = cta_threads(p.head_dim);
-    const int splits = p.q_heads > 0 ? token_splits(p, p.q_heads, threads) : 0;
+    const Spread s = spread(p, p.q_heads, threads);
     const int blocks = (p.k + p.block_rows - 2) / p.block_rows + 1;
     const long long kv = (long long)p.batch * blocks * p.kv_heads * 2;
-    const long long grid = kv + (long long)p.batch * p.k * splits;
+    const long long grid = kv + (p.q_heads > 0 ? ctas(p, s) : 0);
     if (grid >= (1ll << 31)) return cudaErrorInvalidValue;
-    rope_append_fp8_kernel<<<(unsigned)grid, threads, 0, stream>>>(p, blocks, (unsigned)kv,
-                                                                   splits);
+    auto kernel =
+        s.many ? (p.interleaved ? rope_append_fp8_kernel<true, kFlight>
+                                : rope_append_fp8_kernel<false, kFlight>)
+               : (p.interleaved ? rope_append_fp8_kernel<true, 1> : rope_append_fp8_kernel<false, 1>);
+    kernel<<<(unsigned)grid, threads, 0, stream>>>(p, blocks, (unsigned)kv, s);
     count_launches(1);
     return cudaGetLastError();
 }
