@@ -230,6 +230,34 @@ struct PagedFp8Params {
 // Host-side count of kernel launches (carat_kernel_launches).
 void count_launches(int n);
 
+// A launch that may begin while the one before it in the stream drains
+// (programmatic dependent launch).  The kernel waits for that one itself, with
+// griddepcontrol.wait, before it touches memory; after an ordinary kernel the
+// launch is an ordinary one.
+template <typename... Params, typename... Args>
+cudaError_t launch_dependent(void (*kernel)(Params...), dim3 grid, dim3 block, size_t smem,
+                             cudaStream_t stream, Args &&...args) {
+    cudaLaunchConfig_t cfg{};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    count_launches(1);
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+__device__ __forceinline__ void wait_for_prior_launch() {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+__device__ __forceinline__ void let_next_launch_start() {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
 // Device address of the current device's status word, and its SM count (a
 // GB300's 152 when no device can be queried).
 int *device_status_ptr();

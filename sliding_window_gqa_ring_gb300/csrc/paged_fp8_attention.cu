@@ -43,6 +43,7 @@
 // scales ahead of the softmax, 4-11 run it: warps 4-7 own the first half of
 // the rows, 8-11 the second, thread t of each half key t of the tile.  Every
 // wait is bounded.
+#include <algorithm>
 #include <atomic>
 
 #include "carat_internal.cuh"
@@ -58,10 +59,8 @@ namespace {
 
 constexpr int kKeys = 128;                 // keys of a tile
 constexpr int kStage = kKeys * 128;        // bytes of a stage: 128 keys x 128 d
-constexpr int kSoftWarps = 8;
-constexpr int kThreads = 12 * 32;
 constexpr int kSlots = 4;                  // tiles whose scales are fetched ahead
-constexpr int kMaxPieces = 256;            // pieces of one unit
+constexpr int kMaxPieces = 320;            // pieces of one unit
 constexpr uint32_t kFull = 0xffffffffu;
 constexpr float kSlack = 8.f;
 // Weights carry the factor 2^kBoost = kWeight: 2^(kSlack + kBoost) = 2^14 fits
@@ -69,18 +68,26 @@ constexpr float kSlack = 8.f;
 constexpr float kBoost = 6.f, kWeight = 64.f;
 constexpr float kUnset = -1e30f;           // maximum of a row that has seen no key yet
 
+// Two shapes of CTA.  With 16-row tiles at head_dim 256 two CTAs share an SM, so
+// that one streams while the other is at a unit's boundary or starting up; else one
+// CTA takes the SM, its shared memory and eight softmax warps.
 template <int D, int N>
 struct Lay {
     static constexpr int KS = D / 128;                // stages of a K (or V) tile
-    static constexpr int NS = N == 16 ? 12 : D == 256 ? 11 : 10;
+    static constexpr int OCC = D == 256 && N == 16 ? 2 : 1;
+    static constexpr int H = OCC == 2 ? 1 : 2;        // groups of four softmax warps
+    static constexpr int NC = N / H;                  // rows of a group
+    static constexpr int kSoftWarps = 4 * H, kThreads = 128 + 128 * H;
+    static constexpr int PB = OCC == 2 ? 1 : 2;       // buffers of weights
+    static constexpr int NS = OCC == 2 ? 6 : N == 16 ? 12 : D == 256 ? 11 : 10;
     // tiles a unit's boundary costs: O must be read out before the next unit's first
     // product (measured)
-    static constexpr int kCharge = D == 512 && N == 32 ? 2 : 1;
+    static constexpr int kCharge = 5;
     static constexpr int kQBlock = 2 * N * 128;       // 128 d of the query pieces
-    static constexpr int kPBytes = 3 * N * 128;       // a tile's weights (two buffers)
+    static constexpr int kPBytes = 3 * N * 128;       // a tile's weights
     static constexpr int kOffQ = NS * kStage;
     static constexpr int kOffP = kOffQ + KS * kQBlock;
-    static constexpr int kOffRed = kOffP + 2 * kPBytes;
+    static constexpr int kOffRed = kOffP + PB * kPBytes;
     // floats: the four key quarters' maxima or sums per row, the running
     // maxima, the rescale factors, and of two segments the score factors and
     // output rows (int) of the queries
@@ -95,7 +102,8 @@ struct Lay {
     static constexpr int kTmemO = 4 * N;              // two S^T buffers of 2 N columns first
     static constexpr int kTmem = 4 * N + KS * 3 * N <= 256 ? 256 : 512;
     static_assert(4 * N + KS * 3 * N <= kTmem, "tensor memory");
-    static_assert(kAlloc <= 232448, "shared memory");
+    static_assert(OCC * (kAlloc + 1024) <= 233472 && kAlloc <= 232448, "shared memory");
+    static_assert(OCC * kTmem <= 512, "tensor memory");
     // the softmax zeroes V rows while the tile's stages are all resident, with the
     // next tile's K in front of them
     static_assert(NS >= 2 * KS, "the ring holds a K and a V tile");
@@ -309,18 +317,30 @@ __device__ __forceinline__ bool await(uint64_t *bar, uint32_t parity, volatile i
     return tc::mbar_try_wait(bar, parity) || await_slow(bar, parity, abort_flag, dev_status);
 }
 
-// Barrier of the 128 threads of one half of the softmax; true when any of them
-// says so.
+// Barrier of the 128 threads of one group of softmax warps (of H); true when any
+// of them says so.
+template <int H>
 __device__ __forceinline__ bool half_any(int half, bool pred) {
     uint32_t out;
-    asm volatile(
-        "{\n\t.reg .pred pin, pout;\n\t"
-        "setp.ne.u32 pin, %1, 0;\n\t"
-        "bar.red.or.pred pout, %2, 128, pin;\n\t"
-        "selp.u32 %0, 1, 0, pout;\n\t}"
-        : "=r"(out)
-        : "r"((uint32_t)pred), "r"(half + 1)
-        : "memory");
+    if constexpr (H == 1) {
+        asm volatile(
+            "{\n\t.reg .pred pin, pout;\n\t"
+            "setp.ne.u32 pin, %1, 0;\n\t"
+            "bar.red.or.pred pout, 1, 128, pin;\n\t"
+            "selp.u32 %0, 1, 0, pout;\n\t}"
+            : "=r"(out)
+            : "r"((uint32_t)pred)
+            : "memory");
+    } else {
+        asm volatile(
+            "{\n\t.reg .pred pin, pout;\n\t"
+            "setp.ne.u32 pin, %1, 0;\n\t"
+            "bar.red.or.pred pout, %2, 128, pin;\n\t"
+            "selp.u32 %0, 1, 0, pout;\n\t}"
+            : "=r"(out)
+            : "r"((uint32_t)pred), "r"(half + 1)
+            : "memory");
+    }
     return out != 0;
 }
 
@@ -479,14 +499,15 @@ __device__ __forceinline__ float split_query(uint8_t *s_q, const uint16_t *row, 
 
 // The queries of every unit and row group as 8-bit pieces (Image), and NaN outputs
 // for the requests that are rejected on the device.  One CTA per unit and row
-// group, a warp per row in turn.  It runs ahead of the attention, which starts
+// group, one warp per row.  It runs ahead of the attention, which starts
 // loading keys meanwhile: there each CTA fetches an image with one copy when it
 // comes to the unit, where splitting rows in place took the softmax 5000 to 8000
 // cycles at every unit's start.
 template <int D, int N>
-__global__ void __launch_bounds__(256) paged_fp8_split_kernel(
+__global__ void __launch_bounds__(32 * N) paged_fp8_split_kernel(
     const __grid_constant__ PagedFp8Params p, const Plan plan) {
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    wait_for_prior_launch();
+    let_next_launch_start();
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int u = blockIdx.x, rg = u % plan.groups, bc = u / plan.groups;
     const int b = bc / p.kv_heads, c = bc % p.kv_heads;
@@ -496,33 +517,31 @@ __global__ void __launch_bounds__(256) paged_fp8_split_kernel(
     uint8_t *image = plan.images + (size_t)u * Image<D, N>::kBytes;
     float *factor = reinterpret_cast<float *>(image + Image<D, N>::kOperand);
     int *out_row = reinterpret_cast<int *>(factor + N);
-    for (int r = warp; r < N; r += 8) {
-        const int ur = rg * N + r, j = ur / p.group;
-        const int at = ur < p.group * p.k
-                           ? (b * p.k + j) * p.q_heads + c * p.group + ur - j * p.group
-                           : -1;
-        if (!ok) {
-            if (at >= 0)
-                for (int i = lane; i < D / 2; i += 32)
-                    reinterpret_cast<uint32_t *>(p.out + (size_t)at * D)[i] = 0x7fc07fc0u;
-            continue;
-        }
-        const float f =
-            split_query<D, N>(image, at >= 0 ? p.q + (size_t)at * D : nullptr, r, lane);
-        if (lane == 0) {
-            factor[r] = f * p.scale_log2;
-            out_row[r] = at;
-        }
+    const int r = warp, ur = rg * N + r, j = ur / p.group;
+    const int at = ur < p.group * p.k
+                       ? (b * p.k + j) * p.q_heads + c * p.group + ur - j * p.group
+                       : -1;
+    if (!ok) {
+        if (at >= 0)
+            for (int i = lane; i < D / 2; i += 32)
+                reinterpret_cast<uint32_t *>(p.out + (size_t)at * D)[i] = 0x7fc07fc0u;
+        return;
+    }
+    const float f = split_query<D, N>(image, at >= 0 ? p.q + (size_t)at * D : nullptr, r, lane);
+    if (lane == 0) {
+        factor[r] = f * p.scale_log2;
+        out_row[r] = at;
     }
 }
 
 template <int D, int N>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Lay<D, N>::kThreads, Lay<D, N>::OCC)
     paged_fp8_kernel(const __grid_constant__ PagedFp8Params p, const Plan plan,
                      const __grid_constant__ CUtensorMap map_k,
                      const __grid_constant__ CUtensorMap map_v) {
     using L = Lay<D, N>;
-    constexpr int KS = L::KS, NS = L::NS, NC = N / 2;
+    constexpr int KS = L::KS, NS = L::NS, NC = L::NC;
+    constexpr int kSoftWarps = L::kSoftWarps, kThreads = L::kThreads;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int rix = blockIdx.x / plan.groups, rg = blockIdx.x % plan.groups;
 
@@ -549,7 +568,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int *status = p.dev_status;
 
     // the merge launch may start once every CTA of this grid runs
-    if (threadIdx.x == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (threadIdx.x == 0) let_next_launch_start();
 
     // Pool row of a tile's first position; -1 for a page outside the pool.
     const int pages_shift_tiles = p.page_rows / kKeys;   // tiles of a page
@@ -584,7 +603,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc::fence_mbar_init();
         }
         locate_range(p, plan.ranges, rix, lane, L::kCharge, reinterpret_cast<int *>(s_p),
-                     2 * L::kPBytes / 4, sh);
+                     L::PB * L::kPBytes / 4, sh);
         __threadfence_block();
         __syncwarp();
         // the others wait for this; the loads need not wait for them
@@ -743,7 +762,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const uint32_t h = g - 1;
                     if (!(alive = wait_all(&p_full[h & 1], (h >> 1) & 1))) break;
                     tc::tc_fence_after();
-                    const uint64_t w = p_desc + (h & 1) * (L::kPBytes / 16);
+                    const uint64_t w = p_desc + h % L::PB * (L::kPBytes / 16);
                     uint32_t d = tmem + L::kTmemO;
 #pragma unroll 1
                     for (int vs = 0; vs < KS; ++vs) {
@@ -819,7 +838,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ------------------------------------------------------------ queries
         // Each segment's queries as the split launch left them, once the last QK
         // product of the segment before has read its own.
-        asm volatile("griddepcontrol.wait;" ::: "memory");
+        // (Lengths, page table and caches were there before the split launch began.)
+        wait_for_prior_launch();
         if (lane == 0) {
             SegIter it;
             it.init(p, sh);
@@ -845,7 +865,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
     } else if (warp >= 4) {
         // ------------------------------------------------------------ softmax
-        const int half = (warp - 4) / 4, q4 = warp & 3;
+        const int half = L::H == 1 ? 0 : (warp - 4) / 4, q4 = warp & 3;
         const int t = q4 * 32 + lane;                  // key of the tile, or d of an O block
         const uint32_t tmem = sh->tmem;
         const uint32_t lanes = (uint32_t)(q4 * 32) << 16;
@@ -941,13 +961,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int e = 1; e < NC; ++e) top = fmaxf(top, d[e]);
                 bool rescale = false;
-                if (half_any(half, unset || edge || top > kSlack + kBoost || !ok || *abort_flag)) {
+                if (half_any<L::H>(half, unset || edge || top > kSlack + kBoost || !ok || *abort_flag)) {
                     float y[NC];
 #pragma unroll
                     for (int e = 0; e < NC; ++e) y[e] = d[e] = d[e] - nm[e];
                     const int rr = transpose_reduce<NC, true>(y, lane);
                     red_max[q4 * N + r0 + rr] = y[0];
-                    if (half_any(half, !ok || *abort_flag)) {
+                    if (half_any<L::H>(half, !ok || *abort_flag)) {
                         alive = false;
                         break;
                     }
@@ -962,7 +982,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         s_m[r] = now;
                         moved = now != old && old != kUnset;
                     }
-                    rescale = half_any(half, moved);
+                    rescale = half_any<L::H>(half, moved);
                     unset = false;
 #pragma unroll
                     for (int e = 0; e < NC; ++e) {
@@ -972,13 +992,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                         d[e] += nm[e];
                     }
                 }
-                // The PV product two tiles back has read the weights' buffer; a
+                // The PV product PB tiles back has read the weights' buffer; a
                 // rescale needs the last one in O as well.
-                if (g > 1) {
+                if (L::PB == 2 && g > 1) {
                     alive = __all_sync(kFull, await(&o_done[g & 1], ((g - 2) >> 1) & 1, abort_flag,
                                                     status));
                 }
-                if (rescale && alive && g > 0) {
+                if ((L::PB == 1 || rescale) && alive && g > 0) {
                     alive = __all_sync(kFull, await(&o_done[(g - 1) & 1], ((g - 1) >> 1) & 1,
                                                     abort_flag, status));
                     tc::tc_fence_after();
@@ -1003,7 +1023,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // weights, two rows at a time; byte t of row r of the K-major
                     // operand, 16-byte pieces swizzled by r % 8 (r0 and N are
                     // multiples of 8)
-                    uint8_t *pw = s_p + (g & 1) * L::kPBytes + r0 * 128 + (t & 15);
+                    uint8_t *pw = s_p + g % L::PB * L::kPBytes + r0 * 128 + (t & 15);
                     const __half2 eight = __floats2half2_rn(8.f, 8.f);
 #pragma unroll
                     for (int e = 0; e < NC; e += 2) {
@@ -1025,7 +1045,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // meet a zero weight (0 x NaN), so they are zeroed.
                     if (t0 < lowest || t0 + kKeys > sg.ctx + p.k) {
                         const uint32_t base = KS * (2 * g + (x + 1 < sg.x1 ? 2 : 1));
-                        for (int z = half; z < KS; z += 2) {
+                        for (int z = half; z < KS; z += L::H) {
                             const uint32_t c = base + z;
                             const int s = c % NS;
                             if (!await(&full[s], (c / NS) & 1, abort_flag, status)) {
@@ -1055,7 +1075,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int e = 0; e < NC; ++e) y[e] = l[e];
             const int rr = transpose_reduce<NC, false>(y, lane);
             red_max[q4 * N + r0 + rr] = y[0];
-            half_any(half, false);
+            half_any<L::H>(half, false);
             const size_t slot_row = ((size_t)blockIdx.x * 2 + (sg.opens ? 0 : 1)) * N + r0;
             if (t < NC) {
                 const int r = r0 + t;
@@ -1067,7 +1087,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             alive = __all_sync(kFull, await(&o_done[(g - 1) & 1], ((g - 1) >> 1) & 1, abort_flag,
                                             status));
             tc::tc_fence_after();
-            if (half_any(half, !alive || *abort_flag)) {
+            if (half_any<L::H>(half, !alive || *abort_flag)) {
                 alive = false;
                 break;
             }
@@ -1088,18 +1108,32 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 __uint_as_float(o1[e]));
             };
             if (whole) {
+                // lanes 2i and 2i + 1 hold d and d + 1 of every row: one keeps the even
+                // rows' pair, the other the odd rows', so stores are 4 bytes wide
+                const bool odd = t & 1;
+                const int base = out_row[0];   // the unit's first row here
 #pragma unroll 1
                 for (int i = 0; i < parts; ++i) {
                     float o[8];
                     pieces(i, o);
                     const int e0 = i / KS * 8;
-                    uint16_t *out = p.out + i % KS * 128 + t;
+                    const float4 fa = *reinterpret_cast<const float4 *>(s_alpha + r0 + e0);
+                    const float4 fb = *reinterpret_cast<const float4 *>(s_alpha + r0 + e0 + 4);
+                    const int4 ra = *reinterpret_cast<const int4 *>(out_row + e0);
+                    const int4 rb = *reinterpret_cast<const int4 *>(out_row + e0 + 4);
+                    const float f[8] = {fa.x, fa.y, fa.z, fa.w, fb.x, fb.y, fb.z, fb.w};
+                    const int ro[8] = {ra.x, ra.y, ra.z, ra.w, rb.x, rb.y, rb.z, rb.w};
+                    uint16_t *out = p.out + (size_t)base * D + i % KS * 128 + (t & ~1);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const int ro = out_row[e0 + e];
-                        const uint16_t h =
-                            __bfloat16_as_ushort(__float2bfloat16_rn(o[e] * s_alpha[r0 + e0 + e]));
-                        if (ro >= 0) out[(size_t)ro * D] = h;
+                    for (int e = 0; e < 8; e += 2) {
+                        const float a = o[e] * f[e], b = o[e + 1] * f[e + 1];
+                        const float got = __shfl_xor_sync(kFull, odd ? a : b, 1);
+                        const __nv_bfloat162 h =
+                            odd ? __floats2bfloat162_rn(got, b) : __floats2bfloat162_rn(a, got);
+                        const int row = odd ? ro[e + 1] : ro[e];
+                        if (row >= 0)
+                            *reinterpret_cast<uint32_t *>(out + (long long)(row - base) * D) =
+                                *reinterpret_cast<const uint32_t *>(&h);
                     }
                 }
             } else {
@@ -1114,7 +1148,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             // all reads of the reduction area and of O come before the next segment's
             tc::tc_fence_before();
-            half_any(half, false);
+            half_any<L::H>(half, false);
             if (lane == 0) tc::mbar_arrive(&q_free[si & 1]);
             have = have_next;
             sg = nx;
@@ -1133,93 +1167,126 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // Merge of the split units: out = sum_q 2^(m_q - M) O_q / sum_q 2^(m_q - M) l_q
 // over the pieces q, M their largest maximum (a piece whose l is 0 saw no key of
-// the row).  One CTA per (unit and row group, row): D / 4 threads take 16 bytes of
-// the row each, and blockDim.x / (D / 4) such teams take the pieces in turn, so a
-// unit cut into many pieces has many loads in flight.
-constexpr int kMergeThreads = 512;
+// the row).  A CTA takes `rows` rows of one unit and row group; a row has D / 4
+// threads of 16 bytes each, `teams` times over: the teams take the pieces in
+// turn, so that a unit cut into many pieces has many loads in flight, F a thread.
+constexpr int kMergeThreads = 512, kMergeRows = 8;
 
-template <int D, int N>
-__global__ void __launch_bounds__(kMergeThreads) paged_fp8_merge_kernel(
-    const __grid_constant__ PagedFp8Params p, const Plan plan) {
+template <int D, int N, int F>
+__global__ void __launch_bounds__(kMergeThreads, F > 4 ? 1 : 3) paged_fp8_merge_kernel(
+    const __grid_constant__ PagedFp8Params p, const Plan plan, int rows, int teams) {
     constexpr int T = D / 4;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int u = blockIdx.x, r = blockIdx.y;
+    wait_for_prior_launch();
+    let_next_launch_start();
+    const int u = blockIdx.x;
     const int rg = u % plan.groups, bc = u / plan.groups;
     const int b = bc / p.kv_heads, c = bc % p.kv_heads;
     const long long ctx = p.context_lengths[b];
     const int2 e = plan.first[u];
     const int np = plan.last[u] - e.x + 1;
-    const int ur = rg * N + r;
-    if (ctx < 0 || ctx + p.k > p.capacity || ur >= p.group * p.k) return;
+    if (ctx < 0 || ctx + p.k > p.capacity) return;
     if (e.y < 0) return;   // whole: written already
     // entries that the attention grid did not write this time (it gave up before)
     if (e.x < 0 || np < 2 || np > kMaxPieces || e.x > plan.ranges - np || e.y > 1) {
         if (threadIdx.x == 0) set_status(p.dev_status, CARAT_DEV_TIMEOUT);
         return;
     }
+    const int d = threadIdx.x % T, rt = threadIdx.x / T;
+    const int team = rt / rows, mine = rt % rows;
+    const int r = blockIdx.y * rows + mine, ur = rg * N + r;
+    const bool valid = r < N && ur < p.group * p.k;
     auto piece = [&](int q) -> size_t {
         return ((size_t)((e.x + q) * plan.groups + rg) * 2 + (q == 0 ? e.y : 0)) * N + r;
     };
-    __shared__ float s_w[kMaxPieces];
+    __shared__ float s_w[kMergeRows][kMaxPieces];
     __shared__ float4 s_o[kMergeThreads];
     const int lane = threadIdx.x % 32;
-    if (threadIdx.x < 32) {
-        float2 v[kMaxPieces / 32];
-        float M = kUnset;
+    // the first pieces' values on their way before the weights are formed
+    float4 v[F];
 #pragma unroll
-        for (int i = 0; i < kMaxPieces / 32; ++i) {
-            const int q = lane + 32 * i;
-            v[i] = q < np ? plan.part_ml[piece(q)] : make_float2(kUnset, 0.f);
-        }
-#pragma unroll
-        for (int i = 0; i < kMaxPieces / 32; ++i)
-            if (v[i].y != 0.f) M = fmaxf(M, v[i].x);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, o));
-        float sum = 0.f;
-#pragma unroll
-        for (int i = 0; i < kMaxPieces / 32; ++i) {
-            v[i].x = v[i].y != 0.f ? fast_exp2(v[i].x - M) : 0.f;
-            sum = fmaf(v[i].x, v[i].y, sum);
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
-        const float inv = 1.f / sum;
-#pragma unroll
-        for (int i = 0; i < kMaxPieces / 32; ++i)
-            if (lane + 32 * i < np) s_w[lane + 32 * i] = v[i].x * inv;
+    for (int i = 0; i < F; ++i) {
+        const int q = team + i * teams;
+        if (valid && q < np)
+            v[i] = reinterpret_cast<const float4 *>(plan.part_o + piece(q) * D)[d];
     }
-    const int team = threadIdx.x / T, teams = blockDim.x / T, d = threadIdx.x % T;
+    if (valid && team == 0 && d < 32) {
+        float M = kUnset, sum = 0.f;
+        if constexpr (F > 4) {   // many pieces: all of them in registers at once
+            constexpr int G = kMaxPieces / 32;
+            float2 ml[G];
+#pragma unroll
+            for (int i = 0; i < G; ++i)
+                ml[i] = lane + 32 * i < np ? plan.part_ml[piece(lane + 32 * i)]
+                                           : make_float2(kUnset, 0.f);
+#pragma unroll
+            for (int i = 0; i < G; ++i)
+                if (ml[i].y != 0.f) M = fmaxf(M, ml[i].x);
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, o));
+#pragma unroll
+            for (int i = 0; i < G; ++i) {
+                ml[i].x = ml[i].y != 0.f ? fast_exp2(ml[i].x - M) : 0.f;
+                sum = fmaf(ml[i].x, ml[i].y, sum);
+            }
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
+            const float inv = 1.f / sum;
+#pragma unroll
+            for (int i = 0; i < G; ++i)
+                if (lane + 32 * i < np) s_w[mine][lane + 32 * i] = ml[i].x * inv;
+        } else {                 // a few
+            for (int q = lane; q < np; q += 32) {
+                const float2 ml = plan.part_ml[piece(q)];
+                if (ml.y != 0.f) M = fmaxf(M, ml.x);
+            }
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, o));
+            for (int q = lane; q < np; q += 32) {
+                const float2 ml = plan.part_ml[piece(q)];
+                const float w = ml.y != 0.f ? fast_exp2(ml.x - M) : 0.f;
+                s_w[mine][q] = w;
+                sum = fmaf(w, ml.y, sum);
+            }
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
+            const float inv = 1.f / sum;
+            for (int q = lane; q < np; q += 32) s_w[mine][q] *= inv;
+        }
+    }
+    __syncthreads();
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (valid) {
 #pragma unroll 1
-    for (int q0 = team; q0 < np; q0 += 8 * teams) {
-        float4 v[8];
+        for (int q0 = team; q0 < np; q0 += F * teams) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (q0 + i * teams < np)
-                v[i] = reinterpret_cast<const float4 *>(plan.part_o + piece(q0 + i * teams) * D)[d];
-        if (q0 == team) __syncthreads();   // the weights, once the first loads are on their way
+            for (int i = 0; i < F; ++i) {
+                const int q = q0 + i * teams;
+                if (q >= np) continue;
+                const float w = s_w[mine][q];
+                if (w != 0.f) {
+                    acc.x = fmaf(v[i].x, w, acc.x);
+                    acc.y = fmaf(v[i].y, w, acc.y);
+                    acc.z = fmaf(v[i].z, w, acc.z);
+                    acc.w = fmaf(v[i].w, w, acc.w);
+                }
+            }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            if (q0 + i * teams >= np) continue;
-            const float w = s_w[q0 + i * teams];
-            if (w == 0.f) continue;
-            acc.x = fmaf(v[i].x, w, acc.x);
-            acc.y = fmaf(v[i].y, w, acc.y);
-            acc.z = fmaf(v[i].z, w, acc.z);
-            acc.w = fmaf(v[i].w, w, acc.w);
+            for (int i = 0; i < F; ++i) {
+                const int q = q0 + (i + F) * teams;
+                if (q < np) v[i] = reinterpret_cast<const float4 *>(plan.part_o + piece(q) * D)[d];
+            }
         }
     }
-    if (team >= np) __syncthreads();
     if (teams > 1) {
         s_o[threadIdx.x] = acc;
         __syncthreads();
         if (team > 0) return;
         for (int i = 1; i < teams; ++i) {
-            const float4 v = s_o[i * T + d];
-            acc.x += v.x, acc.y += v.y, acc.z += v.z, acc.w += v.w;
+            const float4 w = s_o[(i * rows + mine) * T + d];
+            acc.x += w.x, acc.y += w.y, acc.z += w.z, acc.w += w.w;
         }
     }
+    if (!valid) return;
     const int j = ur / p.group;
     const size_t row = ((size_t)b * p.k + j) * p.q_heads + (size_t)c * p.group + ur - j * p.group;
     const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x, acc.y);
@@ -1244,7 +1311,8 @@ Sizes sizes_of(int batch, int k, int q_heads, int kv_heads, int head_dim) {
     z.n = tile_rows(rows);
     z.groups = (rows + z.n - 1) / z.n;
     const int sms = device_sm_count();
-    const int ranges = sms / z.groups < kMaxPieces ? sms / z.groups : kMaxPieces;
+    const int slots_sm = head_dim == 256 && z.n == 16 ? Lay<256, 16>::OCC : 1;
+    const int ranges = std::min(slots_sm * sms / z.groups, kMaxPieces);
     z.grid = (ranges < 1 ? 1 : ranges) * z.groups;
     const size_t slots = (size_t)z.grid * 2 * z.n;
     z.ml = align256(slots * sizeof(float2));
@@ -1289,36 +1357,24 @@ cudaError_t launch(const PagedFp8Params &p, const Sizes &z, cudaStream_t stream)
         if (e != cudaSuccess) return e;
         if (dev >= 0 && dev < 64) configured[dev].store(1, std::memory_order_release);
     }
+    // The attention may start while the split launch runs, and the merge while the
+    // attention drains; each waits where it needs the other's results.
     const int units = p.batch * p.kv_heads * z.groups;
-    paged_fp8_split_kernel<D, N><<<units, 256, 0, stream>>>(p, plan);
-    count_launches(1);
-    e = cudaGetLastError();
+    e = launch_dependent(paged_fp8_split_kernel<D, N>, dim3(units), dim3(32 * N), 0, stream, p, plan);
     if (e != cudaSuccess) return e;
-    // each of the next two may start while the launch before it drains, and waits
-    // for it where it needs its results
-    cudaLaunchConfig_t cfg{};
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    cfg.stream = stream;
-    cfg.gridDim = dim3(z.grid);
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = L::kAlloc;
-    e = cudaLaunchKernelEx(&cfg, kernel, p, plan, map_k, map_v);
-    count_launches(1);
+    e = launch_dependent(kernel, dim3(z.grid), dim3(L::kThreads), L::kAlloc, stream, p, plan, map_k,
+                         map_v);
     if (e != cudaSuccess) return e;
-    cfg.dynamicSmemBytes = 0;
-    cfg.gridDim = dim3(units, N);
-    // a unit is cut into about ranges / units + 1 pieces: a team for every eight
+    // A unit is cut into about ranges / units + 1 pieces, and one long unit among
+    // short ones into as many as there are ranges.
+    const int held = std::min(N, p.group * p.k), most = kMergeThreads / (D / 4);
     const int pieces = plan.ranges / (p.batch * p.kv_heads) + 1;
-    int teams = 1;
-    while (teams < kMergeThreads / (D / 4) && pieces > 8 * teams) teams *= 2;
-    cfg.blockDim = dim3(D / 4 * teams);
-    e = cudaLaunchKernelEx(&cfg, paged_fp8_merge_kernel<D, N>, p, plan);
-    count_launches(1);
-    return e;
+    int teams = 1, rows = 1;
+    while (teams < most && pieces > 8 * teams) teams *= 2;
+    while (rows < kMergeRows && rows * teams < most && rows < held) rows *= 2;
+    auto merge = teams > 1 ? paged_fp8_merge_kernel<D, N, 8> : paged_fp8_merge_kernel<D, N, 4>;
+    return launch_dependent(merge, dim3(units, (held + rows - 1) / rows), dim3(D / 4 * rows * teams),
+                            0, stream, p, plan, rows, teams);
 }
 
 }  // namespace

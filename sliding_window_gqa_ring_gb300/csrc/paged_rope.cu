@@ -219,6 +219,8 @@ __device__ __forceinline__ void move_tokens(const RopeParams &p, unsigned cta, S
 template <bool kInter, int F>
 __global__ void __launch_bounds__(kThreads, F == 1 ? kFew : kMany) rope_append_kernel(
     const __grid_constant__ RopeParams p, Spread s) {
+    wait_for_prior_launch();
+    let_next_launch_start();
     move_tokens<kInter, F>(p, blockIdx.x, s, true);
 }
 
@@ -275,6 +277,8 @@ __device__ __forceinline__ uint32_t requantise4(uint32_t w, float ratio) {
 template <bool kInter, int F>
 __global__ void __launch_bounds__(kThreads, F == 1 ? kFew : kMany) rope_append_fp8_kernel(
     const __grid_constant__ RopeParams p, int blocks, unsigned kv_ctas, Spread s) {
+    wait_for_prior_launch();
+    let_next_launch_start();
     if (blockIdx.x >= kv_ctas) {
         move_tokens<kInter, F>(p, blockIdx.x - kv_ctas, s, false);
         return;
@@ -446,9 +450,7 @@ cudaError_t launch_rope_append(const RopeParams &p, cudaStream_t stream) {
     auto kernel = s.many ? (p.interleaved ? rope_append_kernel<true, kFlight>
                                           : rope_append_kernel<false, kFlight>)
                          : (p.interleaved ? rope_append_kernel<true, 1> : rope_append_kernel<false, 1>);
-    kernel<<<(unsigned)grid, threads, 0, stream>>>(p, s);
-    count_launches(1);
-    return cudaGetLastError();
+    return launch_dependent(kernel, dim3((unsigned)grid), dim3(threads), 0, stream, p, s);
 }
 
 cudaError_t launch_rope_append_fp8(const RopeParams &p, cudaStream_t stream) {
@@ -462,9 +464,8 @@ cudaError_t launch_rope_append_fp8(const RopeParams &p, cudaStream_t stream) {
         s.many ? (p.interleaved ? rope_append_fp8_kernel<true, kFlight>
                                 : rope_append_fp8_kernel<false, kFlight>)
                : (p.interleaved ? rope_append_fp8_kernel<true, 1> : rope_append_fp8_kernel<false, 1>);
-    kernel<<<(unsigned)grid, threads, 0, stream>>>(p, blocks, (unsigned)kv, s);
-    count_launches(1);
-    return cudaGetLastError();
+    return launch_dependent(kernel, dim3((unsigned)grid), dim3(threads), 0, stream, p, blocks,
+                            (unsigned)kv, s);
 }
 
 }  // namespace carat
