@@ -24,7 +24,7 @@
 // Keys are the M dimension of both products:
 //     S^T [128 keys x 2N]  = K_tile [128 x D] . [q_hi | q_lo]^T      (K-major A)
 //     O^T [128 d x 3N]    += V_tile^T [d x 128 keys] . [w1 | w2 | w3]^T (MN-major A)
-// for N = 16 or 32 rows; more rows (up to 128) are cut into row groups of 32.
+// for N = 8, 16 or 32 rows; more rows (up to 128) are cut into row groups of 32.
 // The scales cost nothing in the products: thread t of the softmax owns key t,
 // so ks[t] is one factor of its scores, and vs[t] one of its weights.
 //
@@ -58,7 +58,8 @@ namespace carat {
 namespace {
 
 constexpr int kKeys = 128;                 // keys of a tile
-constexpr int kStage = kKeys * 128;        // bytes of a stage: 128 keys x 128 d
+constexpr int kSlab = kKeys * 128;         // bytes of 128 keys x 128 d
+constexpr int kStage = 2 * kSlab;          // a stage: 128 keys x 256 d, one copy
 constexpr int kSlots = 4;                  // tiles whose scales are fetched ahead
 constexpr int kMaxPieces = 320;            // pieces of one unit
 constexpr uint32_t kFull = 0xffffffffu;
@@ -68,25 +69,29 @@ constexpr float kSlack = 8.f;
 constexpr float kBoost = 6.f, kWeight = 64.f;
 constexpr float kUnset = -1e30f;           // maximum of a row that has seen no key yet
 
-// Two shapes of CTA.  With 16-row tiles at head_dim 256 two CTAs share an SM, so
+// Two shapes of CTA.  With up to 16 rows at head_dim 256 two CTAs share an SM, so
 // that one streams while the other is at a unit's boundary or starting up; else one
-// CTA takes the SM, its shared memory and eight softmax warps.
+// CTA takes the SM and its shared memory, with eight softmax warps (four for 8 rows).
 template <int D, int N>
 struct Lay {
-    static constexpr int KS = D / 128;                // stages of a K (or V) tile
-    static constexpr int OCC = D == 256 && N == 16 ? 2 : 1;
-    static constexpr int H = OCC == 2 ? 1 : 2;        // groups of four softmax warps
+    static constexpr int KS = D / 128;                // 128-d blocks
+    static constexpr int TS = D / 256;                // stages of a K (or V) tile
+    static constexpr int OCC = D == 256 && N <= 16 ? 2 : 1;
+    static constexpr int H = OCC == 2 || N == 8 ? 1 : 2;   // groups of four softmax warps
     static constexpr int NC = N / H;                  // rows of a group
     static constexpr int kSoftWarps = 4 * H, kThreads = 128 + 128 * H;
     static constexpr int PB = OCC == 2 ? 1 : 2;       // buffers of weights
-    static constexpr int NS = OCC == 2 ? 6 : N == 16 ? 12 : D == 256 ? 11 : 10;
+    static constexpr int QB = N == 8 || (D == 256 && N == 32) ? 2 : 1;   // of queries
+    static constexpr int NS = OCC == 2 ? 3 : N <= 16 ? 6 : 5;
+    static constexpr int PR = (3 * N + 15) / 16 * 16; // rows of the weights' operand
     // tiles a unit's boundary costs: O must be read out before the next unit's first
     // product (measured)
     static constexpr int kCharge = 5;
     static constexpr int kQBlock = 2 * N * 128;       // 128 d of the query pieces
-    static constexpr int kPBytes = 3 * N * 128;       // a tile's weights
+    static constexpr int kQBytes = KS * kQBlock;
+    static constexpr int kPBytes = PR * 128;          // a tile's weights
     static constexpr int kOffQ = NS * kStage;
-    static constexpr int kOffP = kOffQ + KS * kQBlock;
+    static constexpr int kOffP = kOffQ + QB * kQBytes;
     static constexpr int kOffRed = kOffP + PB * kPBytes;
     // floats: the four key quarters' maxima or sums per row, the running
     // maxima, the rescale factors, and of two segments the score factors and
@@ -95,19 +100,21 @@ struct Lay {
     static constexpr int kRedFloats = 10 * N;
     static constexpr int kOffSc = kOffRed + kRedFloats * 4;      // [kSlots][2][8] scales
     static constexpr int kOffBar = kOffSc + kSlots * 64;
-    static constexpr int kBars = 2 * NS + 12 + 2 * kSlots;
+    static constexpr int kBars = 2 * NS + 13 + 2 * kSlots;
     static constexpr int kOffMisc = kOffBar + kBars * 8;
     static constexpr int kBytes = kOffMisc + 128;
     static constexpr int kAlloc = kBytes + 1024;
     static constexpr int kTmemO = 4 * N;              // two S^T buffers of 2 N columns first
-    static constexpr int kTmem = 4 * N + KS * 3 * N <= 256 ? 256 : 512;
-    static_assert(4 * N + KS * 3 * N <= kTmem, "tensor memory");
+    static constexpr int kTmem = 4 * N + KS * PR <= 256 ? 256 : 512;
+    static_assert(4 * N + KS * PR <= kTmem, "tensor memory");
     static_assert(OCC * (kAlloc + 1024) <= 233472 && kAlloc <= 232448, "shared memory");
     static_assert(OCC * kTmem <= 512, "tensor memory");
     // the softmax zeroes V rows while the tile's stages are all resident, with the
     // next tile's K in front of them
-    static_assert(NS >= 2 * KS, "the ring holds a K and a V tile");
-    static_assert(kOffQ % 1024 == 0 && kOffP % 1024 == 0 && kQBlock % 1024 == 0, "swizzle");
+    static_assert(NS >= 2 * TS, "the ring holds a K and a V tile");
+    static_assert(kOffQ % 1024 == 0 && kOffP % 1024 == 0 && kQBlock % 1024 == 0 &&
+                      kPBytes % 1024 == 0, "swizzle");
+    static_assert(kOffSc % 16 == 0 && kRedQ % 4 == 0 && kRedAlpha % 4 == 0, "alignment");
 };
 
 // A unit and row group's queries as the split launch leaves them: the Q operand
@@ -540,7 +547,7 @@ __global__ void __launch_bounds__(Lay<D, N>::kThreads, Lay<D, N>::OCC)
                      const __grid_constant__ CUtensorMap map_k,
                      const __grid_constant__ CUtensorMap map_v) {
     using L = Lay<D, N>;
-    constexpr int KS = L::KS, NS = L::NS, NC = L::NC;
+    constexpr int KS = L::KS, TS = L::TS, NS = L::NS, NC = L::NC;
     constexpr int kSoftWarps = L::kSoftWarps, kThreads = L::kThreads;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int rix = blockIdx.x / plan.groups, rg = blockIdx.x % plan.groups;
@@ -554,10 +561,10 @@ __global__ void __launch_bounds__(Lay<D, N>::kThreads, Lay<D, N>::OCC)
     uint64_t *p_full = s_full + 2;      // [2] weights of a tile written
     uint64_t *o_done = s_full + 4;      // [2] PV product of a tile done
     uint64_t *q_full = s_full + 6;      // [2] queries of a segment landed
-    uint64_t *q_empty = s_full + 8;     // last QK product of a segment done
-    uint64_t *q_free = s_full + 9;      // [2] factors of a segment's queries used
-    uint64_t *fin = s_full + 11;
-    uint64_t *sc_full = s_full + 12;    // [kSlots] scales of a tile fetched
+    uint64_t *q_empty = s_full + 8;     // [2] last QK product of a segment done
+    uint64_t *q_free = s_full + 10;     // [2] factors of a segment's queries used
+    uint64_t *fin = s_full + 12;
+    uint64_t *sc_full = s_full + 13;    // [kSlots] scales of a tile fetched
     uint64_t *sc_empty = sc_full + kSlots;
     uint8_t *s_q = smem + L::kOffQ;
     uint8_t *s_p = smem + L::kOffP;
@@ -592,8 +599,8 @@ __global__ void __launch_bounds__(Lay<D, N>::kThreads, Lay<D, N>::OCC)
                 tc::mbar_init(&o_done[i], 1);
                 tc::mbar_init(&q_full[i], 1);
                 tc::mbar_init(&q_free[i], kSoftWarps);
+                tc::mbar_init(&q_empty[i], 1);
             }
-            tc::mbar_init(q_empty, 1);
             tc::mbar_init(fin, 1);
             for (int i = 0; i < kSlots; ++i) {
                 tc::mbar_init(&sc_full[i], 1);
@@ -621,7 +628,7 @@ __global__ void __launch_bounds__(Lay<D, N>::kThreads, Lay<D, N>::OCC)
             uint32_t cnt = 0;
             bool alive = true;
             auto issue = [&](const CUtensorMap *map, long long row, int c) {
-                for (int ks = 0; ks < KS && alive; ++ks) {
+                for (int ks = 0; ks < TS && alive; ++ks) {
                     const int s = cnt % NS;
                     if (cnt >= NS &&
                         !await(&empty[s], ((cnt / NS) & 1) ^ 1, abort_flag, status)) {
@@ -629,7 +636,7 @@ __global__ void __launch_bounds__(Lay<D, N>::kThreads, Lay<D, N>::OCC)
                         return;
                     }
                     tc::mbar_arrive_expect_tx(&full[s], kStage);
-                    tc::tma_load_4d(smem + s * kStage, map, 0, (int)row, ks, c, &full[s], pol);
+                    tc::tma_load_4d(smem + s * kStage, map, 0, (int)row, 2 * ks, c, &full[s], pol);
                     ++cnt;
                 }
             };
@@ -697,12 +704,12 @@ __global__ void __launch_bounds__(Lay<D, N>::kThreads, Lay<D, N>::OCC)
     if (warp == 1) {
         // ------------------------------------------------------------ products
         constexpr uint32_t idesc_qk = tc::idesc_e4m3_f32(128, 2 * N, false, false);
-        constexpr uint32_t idesc_pv = tc::idesc_e4m3_f32(128, 3 * N, true, true);
+        constexpr uint32_t idesc_pv = tc::idesc_e4m3_f32(128, L::PR, true, true);
         const uint32_t tmem = sh->tmem;
         // descriptors in units of 16 bytes of shared memory: 32 elements along K
         // are 2 units in a K-major operand, 32 rows of 128 bytes in V
         const uint64_t k_desc = tc::sdesc_sw128(tc::smem_u32(smem), 16, 1024);
-        const uint64_t v_desc = tc::sdesc_sw128(tc::smem_u32(smem), kStage, 1024);
+        const uint64_t v_desc = tc::sdesc_sw128(tc::smem_u32(smem), kSlab, 1024);
         const uint64_t q_desc = tc::sdesc_sw128(tc::smem_u32(s_q), 16, 1024);
         const uint64_t p_desc = tc::sdesc_sw128(tc::smem_u32(s_p), 16, 1024);
         SegIter it;
@@ -735,24 +742,26 @@ __global__ void __launch_bounds__(Lay<D, N>::kThreads, Lay<D, N>::OCC)
                     // S^T[g & 1] = K . [q_hi | q_lo]^T
                     if (first && !(alive = wait_all(&q_full[si & 1], (si >> 1) & 1))) break;
                     const uint32_t d = tmem + (g & 1) * 2 * N;
-                    uint64_t q = q_desc;
+                    uint64_t q = q_desc + si % L::QB * (L::kQBytes / 16);
 #pragma unroll 1
-                    for (int ks = 0; ks < KS; ++ks) {
+                    for (int ks = 0; ks < TS; ++ks) {
                         if (!(alive = wait_all(&full[ms], mphase))) break;
                         tc::tc_fence_after();
                         const uint64_t a = k_desc + (uint32_t)ms * (kStage / 16);
 #pragma unroll
-                        for (int kk = 0; kk < 4; ++kk)
-                            tc::mma_f8_ss_warp(d, a + 2 * kk, q + 2 * kk, idesc_qk, (ks | kk) != 0);
+                        for (int kk = 0; kk < 8; ++kk)
+                            tc::mma_f8_ss_warp(d, a + kk / 4 * (kSlab / 16) + 2 * (kk % 4),
+                                               q + kk / 4 * (L::kQBlock / 16) + 2 * (kk % 4), idesc_qk,
+                                               (ks | kk) != 0);
                         tc::mma_commit_warp(&empty[ms]);
-                        q += L::kQBlock / 16;
+                        q += 2 * L::kQBlock / 16;
                         advance();
                     }
                     if (!alive) break;
                     tc::mma_commit_warp(&s_full[g & 1]);
-                    if (first) ++si;
                     if (++x == sg.x1) {
-                        tc::mma_commit_warp(q_empty);
+                        tc::mma_commit_warp(&q_empty[si & 1]);
+                        ++si;
                         have = it.next(p, sg);
                         x = have ? sg.x0 : 0;
                     }
@@ -765,16 +774,18 @@ __global__ void __launch_bounds__(Lay<D, N>::kThreads, Lay<D, N>::OCC)
                     const uint64_t w = p_desc + h % L::PB * (L::kPBytes / 16);
                     uint32_t d = tmem + L::kTmemO;
 #pragma unroll 1
-                    for (int vs = 0; vs < KS; ++vs) {
+                    for (int vs = 0; vs < TS; ++vs) {
                         if (!(alive = wait_all(&full[ms], mphase))) break;
                         tc::tc_fence_after();
                         const uint64_t a = v_desc + (uint32_t)ms * (kStage / 16);
 #pragma unroll
-                        for (int kk = 0; kk < 4; ++kk)
-                            tc::mma_f8_ss_warp(d, a + 256 * kk, w + 2 * kk, idesc_pv,
-                                               !(prev_first && kk == 0));
+                        for (int kk = 0; kk < 8; ++kk)
+                            tc::mma_f8_ss_warp(d + kk / 4 * L::PR,
+                                               a + kk / 4 * (kSlab / 16) + 256 * (kk % 4),
+                                               w + 2 * (kk % 4), idesc_pv,
+                                               !(prev_first && kk % 4 == 0));
                         tc::mma_commit_warp(&empty[ms]);
-                        d += 3 * N;
+                        d += 2 * L::PR;
                         advance();
                     }
                     if (!alive) break;
@@ -837,7 +848,7 @@ __global__ void __launch_bounds__(Lay<D, N>::kThreads, Lay<D, N>::OCC)
     } else if (warp == 3) {
         // ------------------------------------------------------------ queries
         // Each segment's queries as the split launch left them, once the last QK
-        // product of the segment before has read its own.
+        // product of the segment whose buffer they take has read its own.
         // (Lengths, page table and caches were there before the split launch began.)
         wait_for_prior_launch();
         if (lane == 0) {
@@ -847,14 +858,16 @@ __global__ void __launch_bounds__(Lay<D, N>::kThreads, Lay<D, N>::OCC)
             bool alive = true;
             int si = 0;
             for (; it.next(p, sg); ++si) {
-                alive = (si < 1 || await(q_empty, (si - 1) & 1, abort_flag, status)) &&
+                const int was = si - L::QB;   // the segment whose buffer this one takes
+                alive = (was < 0 || await(&q_empty[was & 1], (was >> 1) & 1, abort_flag, status)) &&
                         (si < 2 || await(&q_free[si & 1], ((si - 2) >> 1) & 1, abort_flag, status));
                 if (!alive) break;
                 const uint8_t *image =
                     plan.images + (((size_t)sg.b * p.kv_heads + sg.c) * plan.groups + rg) *
                                       Image<D, N>::kBytes;
                 tc::mbar_arrive_expect_tx(&q_full[si & 1], Image<D, N>::kBytes);
-                tc::bulk_load(s_q, image, Image<D, N>::kOperand, &q_full[si & 1]);
+                tc::bulk_load(s_q + si % L::QB * L::kQBytes, image, Image<D, N>::kOperand,
+                              &q_full[si & 1]);
                 tc::bulk_load(red + L::kRedQ + (si & 1) * 2 * N, image + Image<D, N>::kOperand,
                               2 * N * 4, &q_full[si & 1]);
             }
@@ -1010,7 +1023,8 @@ __global__ void __launch_bounds__(Lay<D, N>::kThreads, Lay<D, N>::OCC)
 #pragma unroll 1
                         for (int z = 0; z < 3 * KS; ++z) {
                             uint32_t o[NC];
-                            const uint32_t at = tmem + L::kTmemO + z * N + lanes + r0;
+                            const uint32_t at =
+                                tmem + L::kTmemO + z / 3 * L::PR + z % 3 * N + lanes + r0;
                             tmem_load<NC>(at, o);
                             tc::tmem_ld_wait();
 #pragma unroll
@@ -1044,16 +1058,17 @@ __global__ void __launch_bounds__(Lay<D, N>::kThreads, Lay<D, N>::OCC)
                     // A tile with rows outside the request's keys: their V bytes must not
                     // meet a zero weight (0 x NaN), so they are zeroed.
                     if (t0 < lowest || t0 + kKeys > sg.ctx + p.k) {
-                        const uint32_t base = KS * (2 * g + (x + 1 < sg.x1 ? 2 : 1));
-                        for (int z = half; z < KS; z += L::H) {
+                        const uint32_t base = TS * (2 * g + (x + 1 < sg.x1 ? 2 : 1));
+                        for (int z = 0; z < TS; ++z) {
                             const uint32_t c = base + z;
                             const int s = c % NS;
                             if (!await(&full[s], (c / NS) & 1, abort_flag, status)) {
                                 alive = false;
                                 break;
                             }
-                            if (!data) {
-                                uint4 *row = reinterpret_cast<uint4 *>(smem + s * kStage + t * 128);
+                            for (int y = half; !data && y < 2; y += L::H) {
+                                uint4 *row = reinterpret_cast<uint4 *>(smem + s * kStage + y * kSlab +
+                                                                       t * 128);
 #pragma unroll
                                 for (int q = 0; q < 8; ++q) row[q] = make_uint4(0, 0, 0, 0);
                             }
@@ -1097,7 +1112,7 @@ __global__ void __launch_bounds__(Lay<D, N>::kThreads, Lay<D, N>::OCC)
             const int parts = KS * ((min(rows_here - r0, NC) + 7) / 8);
             auto pieces = [&](int i, float (&o)[8]) {
                 uint32_t o1[8], o2[8], o3[8];
-                const uint32_t at = tmem + L::kTmemO + i % KS * 3 * N + lanes + r0 + i / KS * 8;
+                const uint32_t at = tmem + L::kTmemO + i % KS * L::PR + lanes + r0 + i / KS * 8;
                 tc::tmem_ld8(at, o1);
                 tc::tmem_ld8(at + N, o2);
                 tc::tmem_ld8(at + 2 * N, o3);
@@ -1173,9 +1188,9 @@ __global__ void __launch_bounds__(Lay<D, N>::kThreads, Lay<D, N>::OCC)
 constexpr int kMergeThreads = 512, kMergeRows = 8;
 
 template <int D, int N, int F>
-__global__ void __launch_bounds__(kMergeThreads, F > 4 ? 1 : 3) paged_fp8_merge_kernel(
+__global__ void __launch_bounds__(kMergeThreads, F > 4 ? 1 : 2) paged_fp8_merge_kernel(
     const __grid_constant__ PagedFp8Params p, const Plan plan, int rows, int teams) {
-    constexpr int T = D / 4;
+    constexpr int V = F > 4 ? 1 : 2, T = D / 4 / V;   // 16-byte vectors a thread
     wait_for_prior_launch();
     let_next_launch_start();
     const int u = blockIdx.x;
@@ -1199,16 +1214,21 @@ __global__ void __launch_bounds__(kMergeThreads, F > 4 ? 1 : 3) paged_fp8_merge_
         return ((size_t)((e.x + q) * plan.groups + rg) * 2 + (q == 0 ? e.y : 0)) * N + r;
     };
     __shared__ float s_w[kMergeRows][kMaxPieces];
-    __shared__ float4 s_o[kMergeThreads];
+    __shared__ float4 s_o[F > 4 ? kMergeThreads : 1];
     const int lane = threadIdx.x % 32;
     // the first pieces' values on their way before the weights are formed
-    float4 v[F];
+    float4 v[F][V];
+    auto load = [&](int q0) {
 #pragma unroll
-    for (int i = 0; i < F; ++i) {
-        const int q = team + i * teams;
-        if (valid && q < np)
-            v[i] = reinterpret_cast<const float4 *>(plan.part_o + piece(q) * D)[d];
-    }
+        for (int i = 0; i < F; ++i) {
+            const int q = q0 + i * teams;
+            if (!valid || q >= np) continue;
+            const float4 *o = reinterpret_cast<const float4 *>(plan.part_o + piece(q) * D) + d;
+#pragma unroll
+            for (int z = 0; z < V; ++z) v[i][z] = o[z * T];
+        }
+    };
+    load(team);
     if (valid && team == 0 && d < 32) {
         float M = kUnset, sum = 0.f;
         if constexpr (F > 4) {   // many pieces: all of them in registers at once
@@ -1254,51 +1274,51 @@ __global__ void __launch_bounds__(kMergeThreads, F > 4 ? 1 : 3) paged_fp8_merge_
         }
     }
     __syncthreads();
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (valid) {
+    float4 acc[V] = {};
 #pragma unroll 1
-        for (int q0 = team; q0 < np; q0 += F * teams) {
+    for (int q0 = team; q0 < np; q0 += F * teams) {
 #pragma unroll
-            for (int i = 0; i < F; ++i) {
-                const int q = q0 + i * teams;
-                if (q >= np) continue;
-                const float w = s_w[mine][q];
-                if (w != 0.f) {
-                    acc.x = fmaf(v[i].x, w, acc.x);
-                    acc.y = fmaf(v[i].y, w, acc.y);
-                    acc.z = fmaf(v[i].z, w, acc.z);
-                    acc.w = fmaf(v[i].w, w, acc.w);
-                }
-            }
+        for (int i = 0; i < F; ++i) {
+            const int q = q0 + i * teams;
+            if (!valid || q >= np) continue;
+            const float w = s_w[mine][q];
+            if (w == 0.f) continue;
 #pragma unroll
-            for (int i = 0; i < F; ++i) {
-                const int q = q0 + (i + F) * teams;
-                if (q < np) v[i] = reinterpret_cast<const float4 *>(plan.part_o + piece(q) * D)[d];
+            for (int z = 0; z < V; ++z) {
+                acc[z].x = fmaf(v[i][z].x, w, acc[z].x);
+                acc[z].y = fmaf(v[i][z].y, w, acc[z].y);
+                acc[z].z = fmaf(v[i][z].z, w, acc[z].z);
+                acc[z].w = fmaf(v[i][z].w, w, acc[z].w);
             }
         }
+        load(q0 + F * teams);
     }
-    if (teams > 1) {
-        s_o[threadIdx.x] = acc;
+    if constexpr (F > 4) {
+        s_o[threadIdx.x] = acc[0];
         __syncthreads();
         if (team > 0) return;
         for (int i = 1; i < teams; ++i) {
             const float4 w = s_o[(i * rows + mine) * T + d];
-            acc.x += w.x, acc.y += w.y, acc.z += w.z, acc.w += w.w;
+            acc[0].x += w.x, acc[0].y += w.y, acc[0].z += w.z, acc[0].w += w.w;
         }
     }
     if (!valid) return;
     const int j = ur / p.group;
     const size_t row = ((size_t)b * p.k + j) * p.q_heads + (size_t)c * p.group + ur - j * p.group;
-    const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x, acc.y);
-    const __nv_bfloat162 hi = __floats2bfloat162_rn(acc.z, acc.w);
-    reinterpret_cast<uint2 *>(p.out + row * D)[d] =
-        make_uint2(*reinterpret_cast<const uint32_t *>(&lo), *reinterpret_cast<const uint32_t *>(&hi));
+#pragma unroll
+    for (int z = 0; z < V; ++z) {
+        const __nv_bfloat162 lo = __floats2bfloat162_rn(acc[z].x, acc[z].y);
+        const __nv_bfloat162 hi = __floats2bfloat162_rn(acc[z].z, acc[z].w);
+        reinterpret_cast<uint2 *>(p.out + row * D)[d + z * T] =
+            make_uint2(*reinterpret_cast<const uint32_t *>(&lo),
+                       *reinterpret_cast<const uint32_t *>(&hi));
+    }
 }
 
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
-// Rows of a tile: 16, or groups of 32.
-int tile_rows(int rows) { return rows <= 16 ? 16 : 32; }
+// Rows of a tile: 8, 16, or groups of 32.
+int tile_rows(int rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : 32; }
 
 struct Sizes {
     int n, groups, grid;
@@ -1311,7 +1331,7 @@ Sizes sizes_of(int batch, int k, int q_heads, int kv_heads, int head_dim) {
     z.n = tile_rows(rows);
     z.groups = (rows + z.n - 1) / z.n;
     const int sms = device_sm_count();
-    const int slots_sm = head_dim == 256 && z.n == 16 ? Lay<256, 16>::OCC : 1;
+    const int slots_sm = head_dim == 256 && z.n <= 16 ? Lay<256, 16>::OCC : 1;
     const int ranges = std::min(slots_sm * sms / z.groups, kMaxPieces);
     z.grid = (ranges < 1 ? 1 : ranges) * z.groups;
     const size_t slots = (size_t)z.grid * 2 * z.n;
@@ -1337,13 +1357,13 @@ cudaError_t launch(const PagedFp8Params &p, const Sizes &z, cudaStream_t stream)
     plan.first = reinterpret_cast<int2 *>(w + z.ml + z.o);
     plan.last = reinterpret_cast<int *>(w + z.ml + z.o + z.units);
     plan.images = reinterpret_cast<uint8_t *>(w + z.ml + z.o + z.units + z.last);
-    // (128 d, rows, 128-d block, head); a stage is 128 rows of one block
+    // (128 d, rows, 128-d block, head); a stage is 128 rows of two blocks
     CUtensorMap map_k{}, map_v{};
     const uint64_t row = (uint64_t)p.kv_heads * D;
     const uint64_t dims[4] = {128, (uint64_t)p.num_pages * p.page_rows, D / 128,
                               (uint64_t)p.kv_heads};
     const uint64_t strides[3] = {row, 128, D};
-    const uint32_t box[4] = {128, kKeys, 1, 1};
+    const uint32_t box[4] = {128, kKeys, 2, 1};
     if (!make_u8_tensor_map(&map_k, p.k_pages, 4, dims, strides, box, true) ||
         !make_u8_tensor_map(&map_v, p.v_pages, 4, dims, strides, box, true))
         return cudaErrorInvalidValue;
@@ -1367,14 +1387,16 @@ cudaError_t launch(const PagedFp8Params &p, const Sizes &z, cudaStream_t stream)
     if (e != cudaSuccess) return e;
     // A unit is cut into about ranges / units + 1 pieces, and one long unit among
     // short ones into as many as there are ranges.
-    const int held = std::min(N, p.group * p.k), most = kMergeThreads / (D / 4);
+    const int held = std::min(N, p.group * p.k);
     const int pieces = plan.ranges / (p.batch * p.kv_heads) + 1;
+    const bool many = pieces > 8;
+    const int row_threads = many ? D / 4 : D / 8, most = kMergeThreads / row_threads;
     int teams = 1, rows = 1;
-    while (teams < most && pieces > 8 * teams) teams *= 2;
+    while (many && teams < most && pieces > 8 * teams) teams *= 2;
     while (rows < kMergeRows && rows * teams < most && rows < held) rows *= 2;
-    auto merge = teams > 1 ? paged_fp8_merge_kernel<D, N, 8> : paged_fp8_merge_kernel<D, N, 4>;
-    return launch_dependent(merge, dim3(units, (held + rows - 1) / rows), dim3(D / 4 * rows * teams),
-                            0, stream, p, plan, rows, teams);
+    auto merge = many ? paged_fp8_merge_kernel<D, N, 8> : paged_fp8_merge_kernel<D, N, 3>;
+    return launch_dependent(merge, dim3(units, (held + rows - 1) / rows),
+                            dim3(row_threads * rows * teams), 0, stream, p, plan, rows, teams);
 }
 
 }  // namespace
@@ -1389,8 +1411,12 @@ size_t paged_fp8_workspace(int batch, int proposal_count, int q_heads, int kv_he
 cudaError_t launch_paged_fp8_attention(const PagedFp8Params &p, cudaStream_t stream) {
     const Sizes z = sizes_of(p.batch, p.k, p.q_heads, p.kv_heads, p.head_dim);
     if (p.head_dim == 256)
-        return z.n == 16 ? launch<256, 16>(p, z, stream) : launch<256, 32>(p, z, stream);
-    return z.n == 16 ? launch<512, 16>(p, z, stream) : launch<512, 32>(p, z, stream);
+        return z.n == 8    ? launch<256, 8>(p, z, stream)
+               : z.n == 16 ? launch<256, 16>(p, z, stream)
+                           : launch<256, 32>(p, z, stream);
+    return z.n == 8    ? launch<512, 8>(p, z, stream)
+           : z.n == 16 ? launch<512, 16>(p, z, stream)
+                       : launch<512, 32>(p, z, stream);
 }
 
 }  // namespace carat

@@ -123,17 +123,24 @@ def test_every_tile_once_and_every_piece_found(seed):
                 assert n <= 256
 
 
-@pytest.mark.parametrize("total", [1, 2, 3, 7])
-def test_stage_numbers_of_the_value_tiles(total):
-    """K of a tile is loaded before V of the one in front of it; the softmax
-    finds a tile's V stages by arithmetic."""
-    ks, count, at = 4, 0, {}
+@pytest.mark.parametrize("lengths", [[1], [2], [1, 1, 1], [3, 1, 4], [7], [1, 5]])
+@pytest.mark.parametrize("ts", [1, 2])
+def test_stage_numbers_of_the_value_tiles(lengths, ts):
+    """K of a tile is loaded before V of the one in front of it, except across a
+    segment's end, where V comes first; the softmax finds a tile's V stages by
+    arithmetic on its number and on whether it ends its segment."""
+    firsts = {sum(lengths[:i]) for i in range(len(lengths))}
+    total, count, at = sum(lengths), 0, {}
     for g in range(total + 1):
-        if g < total:
-            at["k", g] = count
-            count += ks
-        if g > 0:
-            at["v", g - 1] = count
-            count += ks
+        boundary = g in firsts and g > 0
+        for z in range(2):
+            is_k = (z == 0) != boundary
+            if is_k and g < total:
+                at["k", g] = count
+                count += ts
+            if not is_k and g > 0:
+                at["v", g - 1] = count
+                count += ts
+    ends = {f - 1 for f in firsts if f} | {total - 1}
     for g in range(total):
-        assert at["v", g] == (ks * (2 * g + 2) if g + 1 < total else ks * (2 * g + 1))
+        assert at["v", g] == ts * (2 * g + (1 if g in ends else 2))
