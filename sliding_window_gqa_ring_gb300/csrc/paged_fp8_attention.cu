@@ -1082,8 +1082,12 @@ __global__ void __launch_bounds__(Lay<D, N>::kThreads, Lay<D, N>::OCC)
                 if (lane == 0) tc::mbar_arrive(&p_full[g & 1]);
                 if (first && x + 1 < sg.x1) have_next = it.next(p, nx);
             }
-            if (!alive) break;
             // ------------------------------------------------ segment end
+            // (a wait of one warp may have run out: all leave together)
+            if (half_any<L::H>(half, !alive || *abort_flag)) {
+                alive = false;
+                break;
+            }
             // While the last PV product runs: the rows' sums over the 128 keys.
             float y[NC];
 #pragma unroll
