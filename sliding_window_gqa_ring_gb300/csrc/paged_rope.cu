@@ -341,29 +341,63 @@ __global__ void __launch_bounds__(kThreads, F == 1 ? kFew : kMany) rope_append_f
         return true;
     };
 
+    // Largest magnitude of the thread's rows; +inf when one of them may not be
+    // finite.  Values that are not turned are compared as bits, two at a time.
     float amax = 0.f;
+    uint32_t bits = 0;
     bool any = false, outside = false;
     for (long long pos = lo + r0; pos < hi; pos += kRows * rows) {
         load(pos);
 #pragma unroll
         for (int i = 0; i < kRows; ++i) {
-            float x[16];
-            if (!values(i, pos + i * rows, x)) {
-                outside |= pos + i * rows < hi;
+            if (pos + i * rows >= hi) continue;
+            if (table_row(p, b, (int)(pos + i * rows - rq.ctx), rq.ctx) < 0) {
+                outside = true;
                 continue;
             }
             any = true;
+            if (t.freq < 0) {
+                const uint32_t w[8] = {wa[i].x, wa[i].y, wa[i].z, wa[i].w,
+                                       wb[i].x, wb[i].y, wb[i].z, wb[i].w};
 #pragma unroll
-            for (int e = 0; e < 16; ++e) amax = fmaxf(amax, finite_abs(x[e]));
+                for (int e = 0; e < 8; ++e) bits = __vmaxu2(bits, w[e] & 0x7fff7fffu);
+            } else {
+                float x[16];
+                values(i, pos + i * rows, x);
+#pragma unroll
+                for (int e = 0; e < 16; ++e) amax = fmaxf(amax, fabsf(x[e]));
+            }
         }
     }
+    bits = max(bits & 0xffffu, bits >> 16);
+    amax = bits >= 0x7f80u ? INFINITY : fmaxf(amax, __uint_as_float(bits << 16));
     if (outside && c == 0) set_status(p.dev_status, CARAT_DEV_BAD_POSITION);
     __shared__ float s_max[kThreads / 32];
+    auto block_max = [&](float v) -> float {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-    if (threadIdx.x % 32 == 0) s_max[threadIdx.x / 32] = amax;
+        for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+        if (threadIdx.x % 32 == 0) s_max[threadIdx.x / 32] = v;
+        __syncthreads();
+        for (int w = 0; w < (int)(blockDim.x + 31) / 32; ++w) v = fmaxf(v, s_max[w]);
+        return v;
+    };
     if (!__syncthreads_or(any)) return;   // no row of the block is written
-    for (int w = 0; w < (int)(blockDim.x + 31) / 32; ++w) amax = fmaxf(amax, s_max[w]);
+    amax = block_max(amax);
+    if (amax == INFINITY) {               // over the finite values alone
+        float finite = 0.f;
+        for (long long pos = lo + r0; pos < hi; pos += kRows * rows) {
+            load(pos);
+#pragma unroll
+            for (int i = 0; i < kRows; ++i) {
+                float x[16];
+                if (!values(i, pos + i * rows, x)) continue;
+#pragma unroll
+                for (int e = 0; e < 16; ++e) finite = fmaxf(finite, finite_abs(x[e]));
+            }
+        }
+        __syncthreads();
+        amax = block_max(finite);
+    }
     const float need = scale_for(amax);
     const bool fresh = t0 >= rq.ctx;
     const float old = fresh ? need : *scale_at;
