@@ -520,7 +520,8 @@ carat_status carat_global_verify_attention_paged(
 /*
  * carat_paged_verify_attention_fp8 -- decode / verify attention over e4m3
  * pages with block scales, as carat_paged_rope_append_fp8 writes them (any
- * positive normal scales are taken).  This step's rows must already be stored.
+ * scales from 2^-100 to 2^100 are taken, powers of two or not).  This step's rows
+ * must already be stored.
  *
  *   out              bf16 [batch][proposal_count][q_heads][head_dim], what the
  *                    output projection takes: the weights of the PV product are
@@ -530,14 +531,22 @@ carat_status carat_global_verify_attention_paged(
  *   window           0: query j attends to every position up to its own,
  *                    context_lengths[b] + j; w > 0: to the last w of those.
  *                    Pages that hold none of them are never read.
+ *   new_counts       int32 [batch] or NULL (= proposal_count each): request b has
+ *                    queries j < new_counts[b] and no keys behind theirs; the rows
+ *                    of out behind them are left as they were.
  *   Pages, page table, block scales as in carat_paged_rope_append_fp8;
  *   scale, context_lengths and device-side errors as in
- *   carat_global_append_verify_attention_paged.  A page id outside the pool
- *   reads as zeros and sets CARAT_DEV_BAD_CACHE_ID.  Bytes of rows at or past
- *   the key count (context_length + proposal_count) never reach the result.
+ *   carat_global_append_verify_attention_paged (a count out of range rejects its
+ *   request).  A page id outside the pool reads as zeros and sets
+ *   CARAT_DEV_BAD_CACHE_ID.  Bytes and scales of rows at or past the key count
+ *   (context_length + new_counts[b]) never reach the result, nor do those of a key
+ *   the rows of a query that does not attend to it, NaN or not.  A NaN among the
+ *   value bytes of a key that every query of the step attends to makes the
+ *   elements it belongs to NaN; of a key that only some attend to, their whole rows.
  *   workspace        >= carat_paged_fp8_workspace_bytes(..., max_pages *
- *                    page_rows) bytes; needs no initialisation; calls that
- *                    overlap on the GPU need separate workspaces.
+ *                    page_rows) bytes; needs no initialisation; calls that may
+ *                    overlap on the GPU (graphs captured with one workspace and
+ *                    replayed on two streams, say) need separate workspaces.
  *
  * Supported: head_dim 256 or 512; (q_heads/kv_heads) * proposal_count <= 128;
  * q_heads/kv_heads <= 64; proposal_count <= 16; batch * q_heads *
@@ -547,9 +556,9 @@ carat_status carat_global_verify_attention_paged(
 carat_status carat_paged_verify_attention_fp8(
     void *out, const void *queries, const void *key_pages, const void *value_pages,
     const float *k_scales, const float *v_scales, int num_pages, const int32_t *page_table,
-    int max_pages, int page_rows, int block_rows, const int32_t *context_lengths,
-    int proposal_count, int batch, int q_heads, int kv_heads, int head_dim, int window,
-    float scale, void *workspace, size_t workspace_bytes, void *stream);
+    int max_pages, int page_rows, int block_rows, const int32_t *new_counts,
+    const int32_t *context_lengths, int proposal_count, int batch, int q_heads, int kv_heads,
+    int head_dim, int window, float scale, void *workspace, size_t workspace_bytes, void *stream);
 size_t carat_paged_fp8_workspace_bytes(int batch, int proposal_count, int q_heads, int kv_heads,
                                        int head_dim, int capacity);
 

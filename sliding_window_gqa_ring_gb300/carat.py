@@ -142,8 +142,8 @@ def _declare(lib):
         vp, vp, vp, vp, i32, vp, i32, i32, vp, i32, i32, i32, i32, i32, f32, vp, sz, vp]
     lib.carat_paged_verify_attention_fp8.restype = i32
     lib.carat_paged_verify_attention_fp8.argtypes = [
-        vp, vp, vp, vp, vp, vp, i32, vp, i32, i32, i32, vp, i32, i32, i32, i32, i32, i32, f32, vp, sz,
-        vp]
+        vp, vp, vp, vp, vp, vp, i32, vp, i32, i32, i32, vp, vp, i32, i32, i32, i32, i32, i32, f32, vp,
+        sz, vp]
     lib.carat_paged_fp8_workspace_bytes.restype = sz
     lib.carat_paged_fp8_workspace_bytes.argtypes = [i32] * 6
     lib.carat_global_append_verify_attention.restype = i32
@@ -776,14 +776,16 @@ def paged_fp8_workspace_bytes(batch, proposal_count, q_heads, kv_heads, head_dim
 
 def carat_paged_verify_attention_fp8(out, queries, key_pages, value_pages, k_scales, v_scales,
                                      page_table, context_lengths, *, scale, workspace, window=0,
-                                     stream=None):
+                                     new_counts=None, stream=None):
     """Decode / verify attention over e4m3 pages with block scales (as
     carat_paged_rope_append_fp8 writes them) that already hold this step's rows.
 
     out and queries bf16 [B][k][Hq][D]; window 0: every position up to the
-    query's own, w > 0: the last w of them; workspace: a CUDA tensor of at
-    least paged_fp8_workspace_bytes(...) bytes."""
+    query's own, w > 0: the last w of them; new_counts int32 [B]: the queries
+    request b really has (default k; rows of out behind them stay as they are);
+    workspace: a CUDA tensor of at least paged_fp8_workspace_bytes(...) bytes."""
     what = "carat_paged_verify_attention_fp8"
+    counts = None
     try:
         shape, pool = queries.shape, key_pages.shape
         batch, k, q_heads, head_dim = shape
@@ -797,22 +799,25 @@ def carat_paged_verify_attention_fp8(out, queries, key_pages, value_pages, k_sca
                  _plain(device, _U8, key_pages, value_pages) and
                  _plain(device, _I32, page_table, context_lengths) and
                  _plain(device, _F32, k_scales, v_scales))
+        if new_counts is not None:
+            usual = usual and new_counts.shape == (batch,) and _plain(device, _I32, new_counts)
+            counts = new_counts.data_ptr()
     except (AttributeError, TypeError, ValueError):
         usual = False
     if not usual:
         _paged_fp8_explain(what, out, queries, key_pages, value_pages, k_scales, v_scales,
-                           page_table, context_lengths, workspace)
+                           page_table, context_lengths, workspace, new_counts)
     block_rows = _block_scales(k_scales, v_scales, num_pages, page_rows, kv_heads, what)
     _check((_lib or library()).carat_paged_verify_attention_fp8(
         out.data_ptr(), queries.data_ptr(), key_pages.data_ptr(), value_pages.data_ptr(),
         k_scales.data_ptr(), v_scales.data_ptr(), num_pages, page_table.data_ptr(), max_pages,
-        page_rows, block_rows, context_lengths.data_ptr(), k, batch, q_heads, kv_heads, head_dim,
-        int(window), float(scale), workspace.data_ptr(),
+        page_rows, block_rows, counts, context_lengths.data_ptr(), k, batch, q_heads, kv_heads,
+        head_dim, min(int(window), 0x7fffffff), float(scale), workspace.data_ptr(),
         workspace.numel() * workspace.element_size(), _stream_of(stream, device)), what)
 
 
 def _paged_fp8_explain(what, out, queries, key_pages, value_pages, k_scales, v_scales, page_table,
-                       context_lengths, workspace):
+                       context_lengths, workspace, new_counts):
     """Raises what is wrong with the arguments."""
     _expect(out, torch.bfloat16, f"{what}: out")
     _expect(queries, torch.bfloat16, f"{what}: queries")
@@ -824,10 +829,14 @@ def _paged_fp8_explain(what, out, queries, key_pages, value_pages, k_scales, v_s
     if cache_dim != head_dim:
         raise ValueError(f"{what}: cache head_dim {cache_dim} != query head_dim {head_dim}")
     _block_scales(k_scales, v_scales, num_pages, page_rows, kv_heads, what)
+    if new_counts is not None:
+        _expect(new_counts, torch.int32, f"{what}: new_counts")
+        if tuple(new_counts.shape) != (batch,):
+            raise ValueError(f"{what}: new_counts must be [batch]")
     _on_device(what, out=out, queries=queries, key_pages=key_pages, value_pages=value_pages,
                k_scales=k_scales, v_scales=v_scales, page_table=page_table,
-               context_lengths=context_lengths, workspace=workspace)
+               context_lengths=context_lengths, workspace=workspace, new_counts=new_counts)
     for t in (out, queries, key_pages, value_pages, k_scales, v_scales, page_table,
-              context_lengths, workspace):
+              context_lengths, workspace, new_counts):
         _ptr(t)
     raise ValueError(f"{what}: arguments do not fit together")

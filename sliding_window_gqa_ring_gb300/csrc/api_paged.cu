@@ -160,9 +160,9 @@ size_t carat_paged_fp8_workspace_bytes(int batch, int proposal_count, int q_head
 carat_status carat_paged_verify_attention_fp8(
     void *out, const void *queries, const void *key_pages, const void *value_pages,
     const float *k_scales, const float *v_scales, int num_pages, const int32_t *page_table,
-    int max_pages, int page_rows, int block_rows, const int32_t *context_lengths,
-    int proposal_count, int batch, int q_heads, int kv_heads, int head_dim, int window,
-    float scale, void *workspace, size_t workspace_bytes, void *stream) {
+    int max_pages, int page_rows, int block_rows, const int32_t *new_counts,
+    const int32_t *context_lengths, int proposal_count, int batch, int q_heads, int kv_heads,
+    int head_dim, int window, float scale, void *workspace, size_t workspace_bytes, void *stream) {
     if (!pages_ok(num_pages, page_table, max_pages, page_rows) || !block_rows_ok(block_rows) ||
         window < 0 || !std::isfinite(scale))
         return CARAT_ERR_INVALID_ARG;
@@ -186,6 +186,7 @@ carat_status carat_paged_verify_attention_fp8(
     p.k_scales = k_scales;
     p.v_scales = v_scales;
     p.page_table = page_table;
+    p.new_counts = new_counts;
     p.context_lengths = context_lengths;
     p.workspace = workspace;
     p.dev_status = device_status_ptr();

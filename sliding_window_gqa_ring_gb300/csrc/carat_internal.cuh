@@ -217,6 +217,7 @@ struct PagedFp8Params {
     const uint8_t *k_pages, *v_pages;   // e4m3 [num_pages][page_rows][Hkv][D]
     const float *k_scales, *v_scales;   // [num_pages][page_rows / block_rows][Hkv]
     const int32_t *page_table;  // [B][max_pages]
+    const int32_t *new_counts;  // [B] or nullptr (k)
     const int32_t *context_lengths;
     void *workspace;
     int *dev_status;

@@ -100,7 +100,7 @@ struct Lay {
     static constexpr int kRedFloats = 10 * N;
     static constexpr int kOffSc = kOffRed + kRedFloats * 4;      // [kSlots][2][8] scales
     static constexpr int kOffBar = kOffSc + kSlots * 64;
-    static constexpr int kBars = 2 * NS + 13 + 2 * kSlots;
+    static constexpr int kBars = 2 * NS + 15 + 2 * kSlots;
     static constexpr int kOffMisc = kOffBar + kBars * 8;
     static constexpr int kBytes = kOffMisc + 128;
     static constexpr int kAlloc = kBytes + 1024;
@@ -138,13 +138,26 @@ struct Plan {
     int *last;
 };
 
-// Tiles of request b: [first, first + count) of its 128-position tiles; 0 when
-// its context length is out of range.
-__device__ __forceinline__ int request_tiles(const PagedFp8Params &p, long long ctx, int *first) {
+// One request of the call: its tokens before this step and its queries.
+struct Request {
+    int ctx, n;
+};
+
+__device__ __forceinline__ Request load_request(const PagedFp8Params &p, int b) {
+    return {p.context_lengths[b], p.new_counts ? p.new_counts[b] : p.k};
+}
+
+__device__ __forceinline__ bool request_ok(const PagedFp8Params &p, Request r) {
+    return r.ctx >= 0 && r.n >= 0 && r.n <= p.k && r.n <= p.capacity - r.ctx;
+}
+
+// Tiles of a request: [first, first + count) of its 128-position tiles; 0 when it
+// has no queries or is rejected.
+__device__ __forceinline__ int request_tiles(const PagedFp8Params &p, Request r, int *first) {
     *first = 0;
-    if (ctx < 0 || ctx + p.k > p.capacity) return 0;
-    if (p.window > 0 && ctx + 1 > p.window) *first = (int)((ctx + 1 - p.window) / kKeys);
-    return (int)((ctx + p.k - 1) / kKeys) - *first + 1;
+    if (!request_ok(p, r) || r.n == 0) return 0;
+    if (p.window > 0 && r.ctx >= p.window) *first = (r.ctx - p.window + 1) / kKeys;
+    return (r.ctx + (r.n - 1)) / kKeys - *first + 1;
 }
 
 // What a CTA's roles share besides the barriers.
@@ -153,11 +166,11 @@ struct Shared {
     int abort_flag;
     int b0, c0, off0;       // first segment: request, KV head, tiles of the unit before it
     int s, e;               // the CTA's tiles of the sequence
+    int nans[2];            // of two segments: NaNs among values that not every query sees
 };
 
 struct Segment {
-    int b, c;
-    long long ctx;
+    int b, c, ctx, n;
     int first, ntiles;      // the unit's tiles
     int x0, x1;             // those of this segment
     bool opens;             // the segment opens the CTA's range
@@ -165,7 +178,7 @@ struct Segment {
 
 // Walks a CTA's range as segments, one per unit it touches.
 struct SegIter {
-    long long ctx;
+    Request rq;
     int pos, end, start, b, c, off, first, ntiles;
 
     __device__ void init(const PagedFp8Params &p, const volatile Shared *sh) {
@@ -176,8 +189,8 @@ struct SegIter {
         off = sh->off0;
         ntiles = 0;
         if (pos < end) {
-            ctx = p.context_lengths[b];
-            ntiles = request_tiles(p, ctx, &first);
+            rq = load_request(p, b);
+            ntiles = request_tiles(p, rq, &first);
         }
     }
 
@@ -186,7 +199,8 @@ struct SegIter {
         const int len = min(ntiles - off, end - pos);
         sg.b = b;
         sg.c = c;
-        sg.ctx = ctx;
+        sg.ctx = rq.ctx;
+        sg.n = rq.n;
         sg.first = first;
         sg.ntiles = ntiles;
         sg.x0 = off;
@@ -201,8 +215,8 @@ struct SegIter {
                 ntiles = 0;
                 while (ntiles == 0 && b + 1 < p.batch) {
                     ++b;
-                    ctx = p.context_lengths[b];
-                    ntiles = request_tiles(p, ctx, &first);
+                    rq = load_request(p, b);
+                    ntiles = request_tiles(p, rq, &first);
                 }
             }
         }
@@ -222,17 +236,17 @@ __device__ __noinline__ void locate_range(const PagedFp8Params &p, int ranges, i
     int tiles = 0, units = 0;
 #pragma unroll 1
     for (int base = 0; base < p.batch; base += 128) {
-        long long ctx[4];
+        Request rq[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int b = base + 32 * i + lane;
-            ctx[i] = b < p.batch ? p.context_lengths[b] : -1;
+            rq[i] = b < p.batch ? load_request(p, b) : Request{-1, 0};
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int b = base + 32 * i + lane;
             int first;
-            const int v = request_tiles(p, ctx[i], &first);
+            const int v = request_tiles(p, rq[i], &first);
             tiles += v;
             units += v > 0 ? 1 : 0;
             if (b < p.batch && b < room) held[b] = v;
@@ -253,7 +267,7 @@ __device__ __noinline__ void locate_range(const PagedFp8Params &p, int ranges, i
     for (int base = 0; base < p.batch && cum_cost <= X1; base += 32) {
         const int b = base + lane;
         int v = 0, first;
-        if (b < p.batch) v = b < room ? held[b] : request_tiles(p, p.context_lengths[b], &first);
+        if (b < p.batch) v = b < room ? held[b] : request_tiles(p, load_request(p, b), &first);
         const int per = v + charge;
         const int vc = v > 0 ? p.kv_heads * per : 0, vt = p.kv_heads * v;
         int ic = vc, it = vt;
@@ -504,6 +518,61 @@ __device__ __forceinline__ float split_query(uint8_t *s_q, const uint16_t *row, 
     return top >= 0x7f800000u ? __int_as_float(0x7fc00000) : __int_as_float((127 - s) << 23);
 }
 
+// Which bytes of a word of e4m3 are NaN.
+__device__ __forceinline__ uint32_t nan_bytes(uint32_t w) {
+    return __vcmpeq4(w & 0x7f7f7f7fu, 0x7f7f7f7fu);
+}
+
+// A key that some of the request's queries see and others do not is one of
+// [ctx + 1, keys), or with a window one of [lowest, keys - window).  A warp looks
+// through the value bytes of such keys in a segment for NaNs.
+template <int D>
+__device__ __noinline__ bool some_nan(const PagedFp8Params &p, const Segment &sg, int lane) {
+    constexpr int kChunks = D / 16;
+    const int keys = sg.ctx + sg.n, begin = (sg.first + sg.x0) * kKeys;
+    const int end = min(keys, begin + (sg.x1 - sg.x0 - 1) * kKeys + kKeys);
+    const int lowest = p.window > 0 && sg.ctx >= p.window ? sg.ctx - p.window + 1 : 0;
+    const int a0 = max(sg.ctx + 1, begin), na = max(end - a0, 0);
+    const int b0 = max(lowest, begin);
+    const int nb = p.window > 0 ? max(min(keys - p.window, end) - b0, 0) : 0;
+    uint32_t found = 0;
+#pragma unroll 4
+    for (int i = lane; i < (na + nb) * kChunks; i += 32) {
+        const int key = i / kChunks, pos = key < na ? a0 + key : b0 + key - na;
+        const long long row =
+            paged_row(p.page_table, p.max_pages, p.page_rows, p.num_pages, sg.b, pos);
+        if (row < 0) continue;
+        const uint4 w = *reinterpret_cast<const uint4 *>(
+            p.v_pages + ((size_t)row * p.kv_heads + sg.c) * D + i % kChunks * 16);
+        found |= nan_bytes(w.x) | nan_bytes(w.y) | nan_bytes(w.z) | nan_bytes(w.w);
+    }
+    return __any_sync(kFull, found != 0);
+}
+
+// Replaces the NaNs in the V row of a tile's key t by negative zeros; whether it has
+// any.  The tile's V lies in ring slots base, base + 1, ...  The bytes come from the
+// page: the other group of softmax warps may have replaced them already.
+template <int D, int NS>
+__device__ __noinline__ bool remove_nans(const PagedFp8Params &p, uint8_t *smem, uint32_t base,
+                                         int t, int b, int c, int pos) {
+    const long long row = paged_row(p.page_table, p.max_pages, p.page_rows, p.num_pages, b, pos);
+    if (row < 0) return false;
+    const uint8_t *src = p.v_pages + ((size_t)row * p.kv_heads + c) * D;
+    bool any = false;
+#pragma unroll 1
+    for (int i = 0; i < D / 4; ++i) {
+        const uint32_t w = reinterpret_cast<const uint32_t *>(src)[i], nan = nan_bytes(w);
+        if (!nan) continue;
+        any = true;
+        const int chunk = i / 4;
+        *reinterpret_cast<uint32_t *>(smem + (base + chunk / 16) % NS * kStage +
+                                      chunk / 8 % 2 * kSlab + t * 128 +
+                                      ((chunk ^ t) & 7) * 16 + i % 4 * 4) =
+            (w & ~nan) | (nan & 0x80808080u);
+    }
+    return any;
+}
+
 // The queries of every unit and row group as 8-bit pieces (Image), and NaN outputs
 // for the requests that are rejected on the device.  One CTA per unit and row
 // group, one warp per row.  It runs ahead of the attention, which starts
@@ -518,22 +587,23 @@ __global__ void __launch_bounds__(32 * N) paged_fp8_split_kernel(
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int u = blockIdx.x, rg = u % plan.groups, bc = u / plan.groups;
     const int b = bc / p.kv_heads, c = bc % p.kv_heads;
-    const long long ctx = p.context_lengths[b];
-    const bool ok = ctx >= 0 && ctx + p.k <= p.capacity;
+    const Request rq = load_request(p, b);
+    const bool ok = request_ok(p, rq);
     if (!ok && threadIdx.x == 0 && c == 0 && rg == 0) set_status(p.dev_status, CARAT_DEV_BAD_CONTEXT);
     uint8_t *image = plan.images + (size_t)u * Image<D, N>::kBytes;
     float *factor = reinterpret_cast<float *>(image + Image<D, N>::kOperand);
     int *out_row = reinterpret_cast<int *>(factor + N);
     const int r = warp, ur = rg * N + r, j = ur / p.group;
-    const int at = ur < p.group * p.k
-                       ? (b * p.k + j) * p.q_heads + c * p.group + ur - j * p.group
-                       : -1;
+    int at = ur < p.group * p.k
+                 ? (b * p.k + j) * p.q_heads + c * p.group + ur - j * p.group
+                 : -1;
     if (!ok) {
         if (at >= 0)
             for (int i = lane; i < D / 2; i += 32)
                 reinterpret_cast<uint32_t *>(p.out + (size_t)at * D)[i] = 0x7fc07fc0u;
         return;
     }
+    if (j >= rq.n) at = -1;   // a query behind the request's last
     const float f = split_query<D, N>(image, at >= 0 ? p.q + (size_t)at * D : nullptr, r, lane);
     if (lane == 0) {
         factor[r] = f * p.scale_log2;
@@ -564,7 +634,8 @@ __global__ void __launch_bounds__(Lay<D, N>::kThreads, Lay<D, N>::OCC)
     uint64_t *q_empty = s_full + 8;     // [2] last QK product of a segment done
     uint64_t *q_free = s_full + 10;     // [2] factors of a segment's queries used
     uint64_t *fin = s_full + 12;
-    uint64_t *sc_full = s_full + 13;    // [kSlots] scales of a tile fetched
+    uint64_t *nan_full = s_full + 13;   // [2] a segment looked through for NaNs
+    uint64_t *sc_full = s_full + 15;    // [kSlots] scales of a tile fetched
     uint64_t *sc_empty = sc_full + kSlots;
     uint8_t *s_q = smem + L::kOffQ;
     uint8_t *s_p = smem + L::kOffP;
@@ -598,6 +669,7 @@ __global__ void __launch_bounds__(Lay<D, N>::kThreads, Lay<D, N>::OCC)
                 tc::mbar_init(&p_full[i], kSoftWarps);
                 tc::mbar_init(&o_done[i], 1);
                 tc::mbar_init(&q_full[i], 1);
+                tc::mbar_init(&nan_full[i], 1);
                 tc::mbar_init(&q_free[i], kSoftWarps);
                 tc::mbar_init(&q_empty[i], 1);
             }
@@ -685,10 +757,9 @@ __global__ void __launch_bounds__(Lay<D, N>::kThreads, Lay<D, N>::OCC)
                 prev_c = c;
                 if (!cur) break;
             }
-            if (!alive || *abort_flag)
-                // a role stopped early: the copies in flight land first
-                for (uint32_t i = cnt > (uint32_t)NS ? cnt - NS : 0; i < cnt; ++i)
-                    tc::mbar_wait(&full[i % NS], (i / NS) & 1, 100000000ull);
+            // the last copies land before the CTA goes, whichever role stops early
+            for (uint32_t i = cnt > (uint32_t)NS ? cnt - NS : 0; i < cnt; ++i)
+                tc::mbar_wait(&full[i % NS], (i / NS) & 1, 100000000ull);
         }
         __syncwarp();
     } else {
@@ -797,10 +868,9 @@ __global__ void __launch_bounds__(Lay<D, N>::kThreads, Lay<D, N>::OCC)
             prev_first = first;
             ++g;
         }
-        if (!alive || *abort_flag) {
-            tc::mma_commit_warp(fin);
-            tc::mbar_wait(fin, 0, 100000000ull);
-        }
+        // so do the last products
+        tc::mma_commit_warp(fin);
+        tc::mbar_wait(fin, 0, 100000000ull);
     } else if (warp == 2) {
         // ------------------------------------------------------------ scales
         // Two tiles at a time: lanes 0-7 the K scales and 8-15 the V scales of
@@ -851,31 +921,36 @@ __global__ void __launch_bounds__(Lay<D, N>::kThreads, Lay<D, N>::OCC)
         // product of the segment whose buffer they take has read its own.
         // (Lengths, page table and caches were there before the split launch began.)
         wait_for_prior_launch();
-        if (lane == 0) {
-            SegIter it;
-            it.init(p, sh);
-            Segment sg;
+        SegIter it;
+        it.init(p, sh);
+        Segment sg;
+        int si = 0;
+        for (; it.next(p, sg); ++si) {
             bool alive = true;
-            int si = 0;
-            for (; it.next(p, sg); ++si) {
+            if (lane == 0) {
                 const int was = si - L::QB;   // the segment whose buffer this one takes
                 alive = (was < 0 || await(&q_empty[was & 1], (was >> 1) & 1, abort_flag, status)) &&
                         (si < 2 || await(&q_free[si & 1], ((si - 2) >> 1) & 1, abort_flag, status));
-                if (!alive) break;
-                const uint8_t *image =
-                    plan.images + (((size_t)sg.b * p.kv_heads + sg.c) * plan.groups + rg) *
-                                      Image<D, N>::kBytes;
-                tc::mbar_arrive_expect_tx(&q_full[si & 1], Image<D, N>::kBytes);
-                tc::bulk_load(s_q + si % L::QB * L::kQBytes, image, Image<D, N>::kOperand,
-                              &q_full[si & 1]);
-                tc::bulk_load(red + L::kRedQ + (si & 1) * 2 * N, image + Image<D, N>::kOperand,
-                              2 * N * 4, &q_full[si & 1]);
+                if (alive) {
+                    const uint8_t *image =
+                        plan.images + (((size_t)sg.b * p.kv_heads + sg.c) * plan.groups + rg) *
+                                          Image<D, N>::kBytes;
+                    tc::mbar_arrive_expect_tx(&q_full[si & 1], Image<D, N>::kBytes);
+                    tc::bulk_load(s_q + si % L::QB * L::kQBytes, image, Image<D, N>::kOperand,
+                                  &q_full[si & 1]);
+                    tc::bulk_load(red + L::kRedQ + (si & 1) * 2 * N, image + Image<D, N>::kOperand,
+                                  2 * N * 4, &q_full[si & 1]);
+                }
             }
-            if (!alive || *abort_flag)   // the copies in flight land first
-                for (int i = si > 2 ? si - 2 : 0; i < si; ++i)
-                    tc::mbar_wait(&q_full[i & 1], (i >> 1) & 1, 100000000ull);
+            if (!__all_sync(kFull, alive)) break;
+            const bool any = sg.n > 1 && some_nan<D>(p, sg, lane);
+            if (lane == 0) {
+                sh->nans[si & 1] = any;
+                tc::mbar_arrive(&nan_full[si & 1]);
+            }
         }
-        __syncwarp();
+        for (int i = si > 2 ? si - 2 : 0; i < si; ++i)   // the last copies land
+            tc::mbar_wait(&q_full[i & 1], (i >> 1) & 1, 100000000ull);
     } else if (warp >= 4) {
         // ------------------------------------------------------------ softmax
         const int half = L::H == 1 ? 0 : (warp - 4) / 4, q4 = warp & 3;
@@ -884,7 +959,6 @@ __global__ void __launch_bounds__(Lay<D, N>::kThreads, Lay<D, N>::OCC)
         const uint32_t lanes = (uint32_t)(q4 * 32) << 16;
         const int r0 = half * NC;                      // first row of this half
         const int row0 = rg * N;                       // first of the unit's rows in this group
-        const int rows_here = min(N, p.group * p.k - row0);
         const int block = t / p.block_rows;
         float *red_max = red, *s_m = red + L::kRedM, *s_alpha = red + L::kRedAlpha;
 
@@ -903,12 +977,25 @@ __global__ void __launch_bounds__(Lay<D, N>::kThreads, Lay<D, N>::OCC)
                 if (sg.x0 == 0) plan.first[u] = make_int2(rix, whole ? -1 : sg.opens ? 0 : 1);
                 if (sg.x1 == sg.ntiles) plan.last[u] = rix;
             }
-            const long long lowest = p.window > 0 && sg.ctx + 1 > p.window ? sg.ctx + 1 - p.window : 0;
+            // first key of query 0, and the keys' end
+            const int lowest = p.window > 0 && sg.ctx >= p.window ? sg.ctx - p.window + 1 : 0;
+            const int keys = sg.ctx + sg.n;
+            const int rows_here = min(N, p.group * sg.n - row0);
             // nm: kBoost - running maximum of each row (0 while it has none)
             float nm[NC], l[NC];
 #pragma unroll
             for (int e = 0; e < NC; ++e) nm[e] = 0.f, l[e] = 0.f;
             bool unset = true;   // some row has no maximum yet
+            // Rows of this half that see the key at a position: query j does when
+            // ctx + j >= pos > ctx + j - window.
+            auto seen_rows = [&](int pos) -> uint32_t {
+                const int dj = pos - sg.ctx;
+                const int jlo = max(dj, 0);
+                const int jhi = p.window > 0 && dj < sg.n - p.window ? dj + p.window : sg.n;
+                const int lo = min(max(jlo * p.group - row0 - r0, 0), NC);
+                const int hi = min(max(min(jhi * p.group - row0, rows_here) - r0, 0), NC);
+                return low_mask(hi) & ~low_mask(lo);
+            };
             const float *qs = red + L::kRedQ + (si & 1) * 2 * N + r0;
             const int *out_row = reinterpret_cast<const int *>(qs) + N;
             alive = __all_sync(kFull, await(&q_full[si & 1], (si >> 1) & 1, abort_flag, status));
@@ -918,25 +1005,27 @@ __global__ void __launch_bounds__(Lay<D, N>::kThreads, Lay<D, N>::OCC)
                 const bool ok = __all_sync(
                     kFull, alive && await(&s_full[g & 1], (g >> 1) & 1, abort_flag, status) &&
                                await(&sc_full[slot], (g / kSlots) & 1, abort_flag, status));
+                const int t0 = (sg.first + x) * kKeys, pos = t0 + t;
+                const bool data = pos >= lowest && pos < keys;
                 float ks = 0.f, vs = 1.f;
                 if (ok) {
                     tc::tc_fence_after();
                     ks = s_sc[slot * 16 + block];
-                    vs = s_sc[slot * 16 + 8 + block];
+                    // (a block without keys may have any scale)
+                    if (data) vs = s_sc[slot * 16 + 8 + block];
                 }
                 __syncwarp();
                 if (ok && lane == 0) tc::mbar_arrive(&sc_empty[slot]);
-                // d = score + log2 vs - maximum + kBoost, the weight's exponent
-                const float lv = log2f(vs), iv = 1.f / (vs * kWeight);
-                const long long t0 = (long long)(sg.first + x) * kKeys, pos = t0 + t;
-                const bool data = pos >= lowest && pos < sg.ctx + p.k;
+                // d = score - maximum + kBoost: 2^d is the key's part of the sum, and
+                // 2^d vs, at most 2^(kSlack + kBoost), its weight
+                float lv = log2f(vs);
                 float d[NC];
                 if (ok) {
                     uint32_t h[NC], w[NC];
                     const uint32_t at = tmem + (g & 1) * 2 * N + lanes + r0;
                     tmem_load<NC>(at, h);
                     tmem_load<NC>(at + N, w);
-                    const uint64_t ks2 = pack2(ks, ks), lv2 = pack2(lv, lv);
+                    const uint64_t ks2 = pack2(ks, ks);
                     const uint64_t lo2 = pack2(0.0625f, 0.0625f);
                     tc::tmem_ld_wait();
 #pragma unroll
@@ -944,40 +1033,37 @@ __global__ void __launch_bounds__(Lay<D, N>::kThreads, Lay<D, N>::OCC)
                         const uint64_t q2 = *reinterpret_cast<const uint64_t *>(qs + e);
                         const uint64_t s2 = fma2(pack2(__uint_as_float(w[e]), __uint_as_float(w[e + 1])),
                                                  lo2, pack2(__uint_as_float(h[e]), __uint_as_float(h[e + 1])));
-                        unpack2(fma2(s2, mul2(ks2, q2), add2(lv2, pack2(nm[e], nm[e + 1]))), d[e],
-                                d[e + 1]);
+                        unpack2(fma2(s2, mul2(ks2, q2), pack2(nm[e], nm[e + 1])), d[e], d[e + 1]);
                     }
                 } else {
 #pragma unroll
                     for (int e = 0; e < NC; ++e) d[e] = -INFINITY;
                 }
-                // A tile that not every row sees whole: mask by position.  Query j
-                // sees key t when ctx + j >= pos > ctx + j - window.
-                const bool edge = t0 + kKeys > sg.ctx + 1 ||
-                                  (p.window > 0 && t0 <= sg.ctx + p.k - 1 - p.window);
+                // A tile that not every row sees whole: mask by position.
+                const bool edge = t0 + kKeys - 1 > sg.ctx ||
+                                  (p.window > 0 && t0 <= keys - 1 - p.window);
                 if (edge) {
-                    uint32_t seen = 0;
-                    if (data) {
-                        const long long dj = pos - sg.ctx;
-                        const int jlo = dj > 0 ? (int)dj : 0;
-                        const int jhi =
-                            p.window > 0 && dj + p.window < p.k ? (int)(dj + p.window) : p.k;
-                        const int lo = min(max(jlo * p.group - row0 - r0, 0), NC);
-                        const int hi = min(max(min(jhi * p.group - row0, rows_here) - r0, 0), NC);
-                        seen = low_mask(hi) & ~low_mask(lo);
-                    }
+                    const uint32_t seen = data ? seen_rows(pos) : 0u;
+                    // rows that see a key without a scale are NaN, the others not
+                    const bool bad = !(vs > 0.f && vs < INFINITY);
+                    if (bad) vs = 1.f, lv = 0.f;
 #pragma unroll
-                    for (int e = 0; e < NC; ++e)
+                    for (int e = 0; e < NC; ++e) {
+                        if (bad) d[e] = __int_as_float(0x7fc00000);
                         if (!((seen >> e) & 1u)) d[e] = -INFINITY;
+                    }
                 }
                 float top = d[0];
 #pragma unroll
                 for (int e = 1; e < NC; ++e) top = fmaxf(top, d[e]);
                 bool rescale = false;
-                if (half_any<L::H>(half, unset || edge || top > kSlack + kBoost || !ok || *abort_flag)) {
+                if (half_any<L::H>(half, unset || edge || top > kSlack + kBoost - lv || !ok || *abort_flag)) {
                     float y[NC];
 #pragma unroll
-                    for (int e = 0; e < NC; ++e) y[e] = d[e] = d[e] - nm[e];
+                    for (int e = 0; e < NC; ++e) {
+                        d[e] -= nm[e];
+                        y[e] = d[e] + lv;
+                    }
                     const int rr = transpose_reduce<NC, true>(y, lane);
                     red_max[q4 * N + r0 + rr] = y[0];
                     if (half_any<L::H>(half, !ok || *abort_flag)) {
@@ -1039,12 +1125,16 @@ __global__ void __launch_bounds__(Lay<D, N>::kThreads, Lay<D, N>::OCC)
                     // multiples of 8)
                     uint8_t *pw = s_p + g % L::PB * L::kPBytes + r0 * 128 + (t & 15);
                     const __half2 eight = __floats2half2_rn(8.f, 8.f);
+                    const uint64_t vs2 = pack2(vs, vs);
 #pragma unroll
                     for (int e = 0; e < NC; e += 2) {
-                        __half2 h = __floats2half2_rn(fast_exp2(d[e]), fast_exp2(d[e + 1]));
-                        const float2 f = __half22float2(h);
-                        l[e] = fmaf(f.x, iv, l[e]);
-                        l[e + 1] = fmaf(f.y, iv, l[e + 1]);
+                        // the sum takes 2^d itself: a block of small (or zero) values has a
+                        // small scale, and its keys' weights may vanish, not their share
+                        const uint64_t x2 = pack2(fast_exp2(d[e]), fast_exp2(d[e + 1]));
+                        unpack2(add2(pack2(l[e], l[e + 1]), x2), l[e], l[e + 1]);
+                        float wa, wb;
+                        unpack2(mul2(x2, vs2), wa, wb);
+                        __half2 h = __floats2half2_rn(wa, wb);
                         uint8_t *pa = pw + ((((t >> 4) ^ e) & 7) << 4) + e * 128;
                         uint8_t *pb = pw + ((((t >> 4) ^ (e + 1)) & 7) << 4) + (e + 1) * 128;
 #pragma unroll
@@ -1056,8 +1146,16 @@ __global__ void __launch_bounds__(Lay<D, N>::kThreads, Lay<D, N>::OCC)
                         }
                     }
                     // A tile with rows outside the request's keys: their V bytes must not
-                    // meet a zero weight (0 x NaN), so they are zeroed.
-                    if (t0 < lowest || t0 + kKeys > sg.ctx + p.k) {
+                    // meet a zero weight (0 x NaN), so they are zeroed.  NaNs among the
+                    // values of a key that only some queries see are taken out of the
+                    // tile and put into those rows' weights instead.
+                    bool nans = false;
+                    if (edge && sg.n > 1) {
+                        alive = __all_sync(kFull, await(&nan_full[si & 1], (si >> 1) & 1, abort_flag,
+                                                        status));
+                        nans = alive && sh->nans[si & 1];
+                    }
+                    if (t0 < lowest || t0 + kKeys > keys || nans) {
                         const uint32_t base = TS * (2 * g + (x + 1 < sg.x1 ? 2 : 1));
                         for (int z = 0; z < TS; ++z) {
                             const uint32_t c = base + z;
@@ -1072,6 +1170,15 @@ __global__ void __launch_bounds__(Lay<D, N>::kThreads, Lay<D, N>::OCC)
 #pragma unroll
                                 for (int q = 0; q < 8; ++q) row[q] = make_uint4(0, 0, 0, 0);
                             }
+                        }
+                        if (nans && alive && data &&
+                            (pos > sg.ctx || (p.window > 0 && pos < keys - p.window)) &&
+                            remove_nans<D, NS>(p, smem, base, t, sg.b, sg.c, pos)) {
+                            const uint32_t seen = seen_rows(pos);
+#pragma unroll 1
+                            for (int e = 0; e < NC; ++e)
+                                if ((seen >> e) & 1u)
+                                    pw[((((t >> 4) ^ e) & 7) << 4) + e * 128] = 0x7f;
                         }
                     }
                 }
@@ -1098,10 +1205,12 @@ __global__ void __launch_bounds__(Lay<D, N>::kThreads, Lay<D, N>::OCC)
             const size_t slot_row = ((size_t)blockIdx.x * 2 + (sg.opens ? 0 : 1)) * N + r0;
             if (t < NC) {
                 const int r = r0 + t;
-                const float sum =
+                float sum =
                     (red_max[r] + red_max[N + r]) + (red_max[2 * N + r] + red_max[3 * N + r]);
-                if (!whole) plan.part_ml[slot_row + t] = make_float2(s_m[r], sum);
-                s_alpha[r] = 1.f / (sum * kWeight);
+                // (values of next to nothing, in many keys: the output is 0, not inf x 0)
+                if (sum > 3e38f) sum = 3e38f;
+                if (!whole) plan.part_ml[slot_row + t] = make_float2(s_m[r], sum * (1.f / kWeight));
+                s_alpha[r] = 1.f / sum;
             }
             alive = __all_sync(kFull, await(&o_done[(g - 1) & 1], ((g - 1) >> 1) & 1, abort_flag,
                                             status));
@@ -1200,10 +1309,10 @@ __global__ void __launch_bounds__(kMergeThreads, F > 4 ? 1 : 2) paged_fp8_merge_
     const int u = blockIdx.x;
     const int rg = u % plan.groups, bc = u / plan.groups;
     const int b = bc / p.kv_heads, c = bc % p.kv_heads;
-    const long long ctx = p.context_lengths[b];
+    const Request rq = load_request(p, b);
     const int2 e = plan.first[u];
     const int np = plan.last[u] - e.x + 1;
-    if (ctx < 0 || ctx + p.k > p.capacity) return;
+    if (!request_ok(p, rq) || rq.n == 0) return;
     if (e.y < 0) return;   // whole: written already
     // entries that the attention grid did not write this time (it gave up before)
     if (e.x < 0 || np < 2 || np > kMaxPieces || e.x > plan.ranges - np || e.y > 1) {
@@ -1213,7 +1322,7 @@ __global__ void __launch_bounds__(kMergeThreads, F > 4 ? 1 : 2) paged_fp8_merge_
     const int d = threadIdx.x % T, rt = threadIdx.x / T;
     const int team = rt / rows, mine = rt % rows;
     const int r = blockIdx.y * rows + mine, ur = rg * N + r;
-    const bool valid = r < N && ur < p.group * p.k;
+    const bool valid = r < N && ur < p.group * rq.n;
     auto piece = [&](int q) -> size_t {
         return ((size_t)((e.x + q) * plan.groups + rg) * 2 + (q == 0 ? e.y : 0)) * N + r;
     };

@@ -326,21 +326,24 @@ class Fp8PagedLayer:
             v_new, context_lengths, cos_sin=self.cos_sin, interleaved=self.interleaved,
             queries=queries, queries_out=queries_out, new_counts=new_counts, stream=stream)
 
-    def attend(self, queries, context_lengths, out=None, stream=None):
-        """Attention of rotated queries over rows already stored."""
+    def attend(self, queries, context_lengths, out=None, stream=None, new_counts=None):
+        """Attention of rotated queries (new_counts[b] of request b, or all) over
+        rows already stored."""
         if out is None:
             out = torch.empty(queries.shape, dtype=torch.bfloat16, device=self.device)
         carat.carat_paged_verify_attention_fp8(
             out, queries, self.key_pages, self.value_pages, self.k_scales, self.v_scales,
             self.page_table, context_lengths, scale=self.scale, window=self.window,
-            workspace=self.workspace, stream=stream)
+            new_counts=new_counts, workspace=self.workspace, stream=stream)
         return out
 
-    def step(self, queries, k_new, v_new, context_lengths, out=None, stream=None):
+    def step(self, queries, k_new, v_new, context_lengths, out=None, stream=None,
+             new_counts=None):
         rotated = self.rotated[:queries.numel()].view(queries.shape)
         self.append(k_new, v_new, context_lengths, queries=queries, queries_out=rotated,
-                    stream=stream)
-        return self.attend(rotated, context_lengths, out=out, stream=stream)
+                    new_counts=new_counts, stream=stream)
+        return self.attend(rotated, context_lengths, out=out, new_counts=new_counts,
+                           stream=stream)
 
 
 class GlobalLayer:

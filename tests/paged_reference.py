@@ -89,8 +89,9 @@ def attention_tolerance(out, weight, q, keys, scale):
     Every weight p_t is off by at most a relative delta: its rounding to f16
     (2^-11), and its score, a sum of D products accumulated in fp32, by
     (D + 64) 2^-24 of sum |q k| (64: the scales' products, the exponential's 2
-    ulp and the conversion to log2 units).  Numerator and denominator both
-    carry it.  The result is rounded to bf16 once (2^-8).
+    ulp and the conversion to log2 units).  The numerator carries both; the
+    denominator, a sum of the weights before that rounding, the second.  The
+    result is rounded to bf16 once (2^-8).
 
     Floor: the weights p_t vs_t that meet the bytes are formed times 64 / (a weight
     of the row), so the row's largest is at least 64 then, as f16 (off by at most

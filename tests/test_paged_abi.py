@@ -71,7 +71,7 @@ def _attn(lib, **kw):
     a.update(kw)
     return lib.carat_paged_verify_attention_fp8(
         a["out"], a["q"], a["kp"], a["vp"], a["ks"], a["vs"], a["num"], a["table"], a["mp"],
-        a["rows"], a["R"], a["ctx"], a["k"], a["B"], a["hq"], a["hkv"], a["d"], a["window"],
+        a["rows"], a["R"], None, a["ctx"], a["k"], a["B"], a["hq"], a["hkv"], a["d"], a["window"],
         a["scale"], a["ws"], a["wsb"], a["stream"])
 
 

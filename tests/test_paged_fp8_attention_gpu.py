@@ -85,19 +85,22 @@ class Case:
             self.B, self.k, self.hq, self.hkv, self.d, self.table.shape[1] * self.kp.shape[1]))
         self.ws.fill_(0xff)
 
-    def call(self, ctx=None, stream=None, out=None, workspace=None):
+    def call(self, ctx=None, stream=None, out=None, workspace=None, counts=None):
         q, kp, vp, ks, vs, table = self.dev
         if out is None:
             out = torch.full(q.shape, 3.0, dtype=torch.bfloat16, device="cuda")
         carat.carat_paged_verify_attention_fp8(
             out, q, kp, vp, ks, vs, table, self.ctx if ctx is None else ctx, scale=self.scale,
             window=self.window, workspace=self.ws if workspace is None else workspace,
-            stream=stream)
+            new_counts=counts, stream=stream)
         return out
 
-    def expected(self, b):
-        q = self.q[b].double()
-        pos = [self.n[b] - self.k + j for j in range(self.k)]
+    def expected(self, b, count=None):
+        """Of a request's `count` queries (default all k), the last of which sits
+        on its last key."""
+        count = self.k if count is None else count
+        q = self.q[b, :count].double()
+        pos = [self.n[b] - count + j for j in range(count)]
         return ref.attention(q, self.keys[b], self.values[b], pos, self.window, self.scale,
                              self.value_scales[b][:self.n[b]])
 
@@ -163,6 +166,234 @@ CASES = {
 @pytest.mark.parametrize("name", sorted(CASES))
 def test_matches_the_definition(name):
     Case(seed=len(name), **CASES[name]).run()
+
+
+@pytest.mark.parametrize("stale", [0.0, -1.0, float("nan"), float("inf"), 3e38])
+@pytest.mark.parametrize("shape", [dict(key_counts=[1, 300, 16, 129], k=1, q_heads=16, kv_heads=8,
+                                        head_dim=256),
+                                   dict(key_counts=[250, 4], k=4, q_heads=16, kv_heads=2,
+                                        head_dim=512, block_rows=32)])
+def test_scales_of_blocks_without_keys_may_be_anything(shape, stale):
+    c = Case(seed=12, **shape)
+    R = c.kp.shape[1] // c.ks.shape[1]
+    used = torch.zeros(c.ks.shape[:2], dtype=torch.bool)
+    for b, n in enumerate(c.n):
+        for t in range(0, n, R):
+            used[int(c.table[b, t // 128]), t % 128 // R] = True
+    c.ks[~used], c.vs[~used] = stale, stale
+    c.upload()
+    c.run()
+
+
+@pytest.mark.parametrize("head_dim", [256, 512])
+def test_blocks_of_zero_values_keep_their_share(head_dim):
+    """Zero values have the least scale, 2^-100: their keys add nothing to the
+    sum of values but all of their weight to the denominator."""
+    c = Case([700, 130], 3, 8, 2, head_dim, seed=13)
+    for b, n in enumerate(c.n):
+        for t in range(0, n, 16):
+            if t // 16 % 3 == 1:
+                page, i = int(c.table[b, t // 128]), t % 128 // 16
+                c.vp[page, 16 * i:16 * i + 16] = 0
+                c.vs[page, i] = 2.0 ** -100
+                c.values[b][t:t + 16] = 0
+                c.value_scales[b][t:t + 16] = 2.0 ** -100
+    c.upload()
+    c.run()
+
+
+@pytest.mark.parametrize("where", ["key", "value", "key scale", "value scale"])
+@pytest.mark.parametrize("q_heads,head_dim,window", [(2, 256, 0), (8, 256, 0), (16, 512, 0),
+                                                     (2, 512, 97), (16, 256, 97)])
+def test_a_nan_reaches_only_the_queries_that_see_it(where, q_heads, head_dim, window):
+    """Request 0's queries sit at 302..305; the NaN is at key 304, the first of its
+    block of 16 and seen by the last two, or with a window of 97 at key 207, the last
+    of its block, seen by the first two (from 206 and 207 on)."""
+    c = Case([306, 200], 4, q_heads, 2, head_dim, seed=14, window=window)
+    clean = c.run().clone()
+    pos = 207 if window else 304
+    page, row = int(c.table[0, pos // 128]), pos % 128
+    if where == "key":
+        c.kp[page, row, 1, 3] = 0x7f
+    elif where == "value":
+        c.vp[page, row, 1, head_dim - 3] = 0xff
+    else:
+        (c.ks if where == "key scale" else c.vs)[page, row // 16, 1] = float("nan")
+    c.upload()
+    out = c.call()
+    torch.cuda.synchronize()
+    half = q_heads // 2
+    seen = slice(0, 2) if window else slice(2, 4)
+    assert out[0, seen, half:].isnan().all()
+    out[0, seen, half:] = clean[0, seen, half:]
+    assert torch.equal(out.view(torch.int16), clean.view(torch.int16))
+
+
+RAGGED = {
+    "verify": (dict(k=4, q_heads=16, kv_heads=2, head_dim=512), [300, 1, 4, 129, 0, 515],
+               [4, 1, 2, 3, 0, 0]),
+    "decode": (dict(k=1, q_heads=16, kv_heads=8, head_dim=256), [300, 17, 128], [1, 0, 1]),
+    "row_groups": (dict(k=15, q_heads=16, kv_heads=2, head_dim=512), [400, 700, 33, 15],
+                   [1, 15, 7, 15]),
+    "window": (dict(k=8, q_heads=4, kv_heads=2, head_dim=256, window=50), [400, 55, 1030],
+               [5, 8, 1]),
+    "long": (dict(k=4, q_heads=16, kv_heads=2, head_dim=512), [30000, 128], [2, 1]),
+    "many": (dict(k=4, q_heads=4, kv_heads=2, head_dim=256), [5 + 13 * i % 300 for i in range(400)],
+             [i * 7 % 5 for i in range(400)]),
+}
+
+
+@pytest.mark.parametrize("name", sorted(RAGGED))
+def test_requests_with_fewer_queries(name):
+    """new_counts: the keys end with the last query's (NaN bytes follow), and the
+    rows of out behind it stay as they were."""
+    shape, key_counts, counts = RAGGED[name]
+    c = Case(key_counts, seed=15, **shape)
+    ctx = i32([n - m for n, m in zip(key_counts, counts)])
+    out = c.call(ctx=ctx, counts=i32(counts)).cpu().double()
+    torch.cuda.synchronize()
+    assert carat.carat_get_device_status(clear=True) == 0
+    for b, m in enumerate(counts):
+        assert (out[b, m:] == 3.0).all()
+        if m:
+            want, weight = c.expected(b, m)
+            tol = ref.attention_tolerance(want, weight, c.q[b, :m].double(), c.keys[b], c.scale)
+            assert ((out[b, :m] - want).abs() <= tol).all(), b
+
+
+def test_counts_at_the_capacity_and_out_of_range():
+    c = Case([256, 256, 256, 256], 4, 16, 2, 512, seed=16)
+    ctx = i32([254, 100, 100, 253])
+    out = c.call(ctx=ctx, counts=i32([2, -1, 5, 4]))
+    torch.cuda.synchronize()
+    assert carat.carat_get_device_status(clear=True) == carat.CARAT_DEV_BAD_CONTEXT
+    assert out[1].isnan().all() and out[2].isnan().all() and out[3].isnan().all()
+    want, weight = c.expected(0, 2)
+    tol = ref.attention_tolerance(want, weight, c.q[0, :2].double(), c.keys[0], c.scale)
+    assert ((out[0, :2].cpu().double() - want).abs() <= tol).all()
+    assert (out[0, 2:] == 3.0).all()
+
+
+def test_several_hundred_requests():
+    """More requests than the range search keeps in a warp's first pass, empty and
+    rejected ones among them."""
+    n = [1 + (i * 37) % 300 for i in range(333)]
+    c = Case(n, 1, 2, 1, 256, seed=17)
+    ctx, counts = c.ctx.clone(), torch.ones_like(c.ctx)
+    ctx[5::50] = -3
+    counts[7::50] = 0
+    out = c.call(ctx=ctx, counts=counts)
+    torch.cuda.synchronize()
+    assert carat.carat_get_device_status(clear=True) == carat.CARAT_DEV_BAD_CONTEXT
+    rejected, empty = set(range(5, 333, 50)), set(range(7, 333, 50))
+    c.check(out, [b for b in range(333) if b not in rejected | empty])
+    assert all(out[b].isnan().all() for b in rejected)
+    assert all((out[b] == 3.0).all() for b in empty)
+
+
+def test_requests_that_share_pages():
+    """A common prefix's pages in several requests' tables."""
+    c = Case([300, 300, 300], 2, 4, 2, 256, seed=18)
+    c.table[1, :2] = c.table[0, :2]
+    c.table[2, 0] = c.table[0, 0]
+    for x in (c.keys, c.values, c.value_scales):
+        x[1][:256] = x[0][:256]
+        x[2][:128] = x[0][:128]
+    c.upload()
+    c.run()
+
+
+def test_two_graphs_with_one_workspace_on_one_stream():
+    a, b = Case([900, 40], 2, 16, 2, 512, seed=19), Case([70, 1500], 2, 16, 2, 512, seed=20)
+    need = max(a.ws.numel(), b.ws.numel())
+    ws = torch.full((need,), 0xff, dtype=a.ws.dtype, device="cuda")
+    outs = [torch.zeros(c.q.shape, dtype=torch.bfloat16, device="cuda") for c in (a, b)]
+    graphs, side = [], torch.cuda.Stream()
+    for c, o in zip((a, b), outs):
+        c.call(out=o, workspace=ws)
+        torch.cuda.synchronize()
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1], stream=side):
+            c.call(stream=side, out=o, workspace=ws)
+    for _ in range(3):
+        for o in outs:
+            o.zero_()
+        for graph in graphs:
+            graph.replay()
+        torch.cuda.synchronize()
+        a.check(outs[0])
+        b.check(outs[1])
+
+
+def test_a_pool_past_32_bits():
+    """Pages behind the 2^32-th byte of the pool: bit-equal to the same pages in a
+    small pool, through the append and the attention."""
+    B, k, hq, hkv, d, R = 2, 4, 16, 8, 512, 32
+    rows = (1 << 32) // (hkv * d) + 1024
+    num = rows // 128
+    g = torch.Generator().manual_seed(23)
+    ctx0, ctx = i32([0, 0]), i32([200, 130])
+    kn, vn = (torch.randn((B, 200, hkv, d), generator=g).bfloat16().cuda() for _ in range(2))
+    q = torch.randn((B, k, hq, d), generator=g).bfloat16().cuda()
+    cs = engine.rotary_table(512, d)
+    outs = []
+    for pages, first in ((8, 0), (num, num - 8)):
+        table = i32([[first + 5, first + 2], [first + 7, first]])
+        kp, vp = (torch.empty((pages, 128, hkv, d), dtype=torch.uint8, device="cuda")
+                  for _ in range(2))
+        ks, vs = (torch.ones((pages, 128 // R, hkv), device="cuda") for _ in range(2))
+        carat.carat_paged_rope_append_fp8(kp, vp, ks, vs, table, kn, vn, ctx0, cos_sin=cs,
+                                          new_counts=ctx)
+        turned = torch.empty_like(q)
+        carat.carat_paged_rope_append_fp8(kp, vp, ks, vs, table, kn[:, :k].contiguous(),
+                                          vn[:, :k].contiguous(), ctx, cos_sin=cs, queries=q,
+                                          queries_out=turned)
+        ws = carat.workspace_tensor(carat.paged_fp8_workspace_bytes(B, k, hq, hkv, d, 256))
+        out = torch.zeros_like(q)
+        carat.carat_paged_verify_attention_fp8(out, turned, kp, vp, ks, vs, table, ctx, scale=0.05,
+                                               workspace=ws)
+        got = [out.view(torch.int16), turned.view(torch.int16)]
+        for x in (kp, vp):
+            for b, n in enumerate((204, 134)):
+                got.append(x[table[b].long()].flatten(0, 1)[:n].clone())
+        outs.append(got)
+        del kp, vp
+    torch.cuda.synchronize()
+    assert carat.carat_get_device_status(clear=True) == 0
+    for x, y in zip(*outs):
+        assert torch.equal(x, y)
+    assert outs[0][0].view(torch.bfloat16).isfinite().all()
+
+
+def test_steps_in_a_row_without_waiting():
+    """Appends and attentions follow each other on one stream, each starting while
+    the one before drains: the same bits as with a wait after every call."""
+    B, k, hq, hkv, d = 5, 4, 16, 2, 512
+    g = torch.Generator().manual_seed(22)
+    cs = engine.rotary_table(1024, d)
+    steps = [[torch.randn((B, k, h, d), generator=g).bfloat16().cuda() for h in (hq, hkv, hkv)]
+             for _ in range(40)]
+    ctxs = [i32([50 * b + 3 * i for b in range(B)]) for i in range(40)]
+    results = []
+    for wait in (True, False):
+        pool = engine.SharedPool(num_pages=16, page_bytes=128 * hkv * d * 2, pages_per_ring=4,
+                                 fill=0.0)
+        table = i32([pool.alloc.alloc_pages(3) for _ in range(B)])
+        layer = engine.Fp8PagedLayer(pool, table, cs, q_heads=hq, kv_heads=hkv, head_dim=d,
+                                     max_proposals=k)
+        first = torch.randn((B, 256, hkv, d), generator=torch.Generator().manual_seed(1))
+        layer.append(first.bfloat16().cuda(), first.bfloat16().cuda(), i32([0] * B),
+                     new_counts=ctxs[0])
+        torch.cuda.synchronize()
+        outs = []
+        for (q, kn, vn), ctx in zip(steps, ctxs):
+            outs.append(layer.step(q, kn, vn, ctx))
+            if wait:
+                torch.cuda.synchronize()
+        torch.cuda.synchronize()
+        results.append(torch.stack(outs))
+    assert torch.equal(results[0].view(torch.int16), results[1].view(torch.int16))
+    assert results[0].isfinite().all()
 
 
 def test_small_weights_of_a_long_tail_survive():
@@ -302,12 +533,13 @@ def test_refusals():
 
     def refused(error, **kw):
         a = dict(out=out, q=q, kp=kp, vp=vp, ks=ks, vs=vs, table=table, ctx=c.ctx, ws=c.ws,
-                 window=0, scale=0.1)
+                 window=0, scale=0.1, counts=None)
         a.update(kw)
         with pytest.raises(error) as e:
             carat.carat_paged_verify_attention_fp8(
                 a["out"], a["q"], a["kp"], a["vp"], a["ks"], a["vs"], a["table"], a["ctx"],
-                scale=a["scale"], window=a["window"], workspace=a["ws"])
+                scale=a["scale"], window=a["window"], workspace=a["ws"],
+                new_counts=a["counts"])
         return e.value
 
     refused(TypeError, out=out.float())
@@ -322,6 +554,9 @@ def test_refusals():
     refused(ValueError, ctx=c.ctx[:1])
     refused(ValueError, out=out[:1])
     refused(ValueError, q=q.transpose(1, 2).contiguous().transpose(1, 2))
+    refused(TypeError, counts=torch.ones_like(c.ctx).long())
+    refused(ValueError, counts=torch.ones_like(c.ctx)[:1])
+    refused(ValueError, counts=torch.ones_like(c.ctx).cpu())
     assert refused(carat.CaratError, window=-1).status == carat.CARAT_ERR_INVALID_ARG
     assert refused(carat.CaratError, scale=float("nan")).status == carat.CARAT_ERR_INVALID_ARG
     assert refused(carat.CaratError, ws=c.ws[:16]).status == carat.CARAT_ERR_WORKSPACE

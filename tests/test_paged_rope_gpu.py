@@ -410,3 +410,40 @@ def test_binding_refuses_what_would_fault():
     refused(ValueError, positions=s.i32([1, 2]))
     refused(ValueError, new_counts=s.i32([1]))
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("block_rows", [0, 32])
+def test_offsets_past_32_bits(block_rows):
+    """Pages behind the pool's 2^32-th element and tokens 2^28 elements apart: the
+    same bytes as from a small pool and dense tokens."""
+    B, k, hkv, d = 1, 17, 8, 512
+    g = torch.Generator().manual_seed(31)
+    dense = [torch.randn((B, k, hkv, d), generator=g).bfloat16().cuda() for _ in range(2)]
+    stride = 1 << 28
+    far = torch.empty((k - 1) * stride + 2 * hkv * d, dtype=torch.bfloat16, device="cuda")
+    wide = [far[i * hkv * d:].as_strided((B, k, hkv, d), (k * stride, stride, d, 1))
+            for i in range(2)]
+    for x, y in zip(wide, dense):
+        x.copy_(y)
+    cs = engine.rotary_table(512, d)
+    ctx = torch.tensor([120], dtype=torch.int32, device="cuda")
+    many = (1 << 32) // (hkv * d) // 128 + 4
+    got = []
+    for pages, first, (kn, vn) in ((4, 0, dense), (many, many - 4, wide)):
+        table = torch.tensor([[first + 3, first + 1]], dtype=torch.int32, device="cuda")
+        dtype = torch.uint8 if block_rows else torch.bfloat16
+        kp, vp = (torch.empty((pages, 128, hkv, d), dtype=dtype, device="cuda") for _ in range(2))
+        for x in (kp, vp):
+            x[table[0].long()] = 0
+        if block_rows:
+            ks, vs = (torch.ones((pages, 128 // block_rows, hkv), device="cuda") for _ in range(2))
+            carat.carat_paged_rope_append_fp8(kp, vp, ks, vs, table, kn, vn, ctx, cos_sin=cs)
+            got.append([x[table[0].long()].clone() for x in (kp, vp, ks, vs)])
+        else:
+            carat.carat_paged_rope_append(kp, vp, table, kn, vn, ctx, cos_sin=cs)
+            got.append([x[table[0].long()].view(torch.int16).clone() for x in (kp, vp)])
+        del kp, vp
+    torch.cuda.synchronize()
+    assert carat.carat_get_device_status(clear=True) == 0
+    for x, y in zip(*got):
+        assert torch.equal(x, y) and (x != 0).any()
