@@ -1157,6 +1157,11 @@ __global__ void __launch_bounds__(Lay<D, N>::kThreads, Lay<D, N>::OCC)
                     }
                     if (t0 < lowest || t0 + kKeys > keys || nans) {
                         const uint32_t base = TS * (2 * g + (x + 1 < sg.x1 ? 2 : 1));
+                        // A wait for a phase by its parity means that phase only if the one
+                        // before it is over: the stage may have been the last tile's V's.
+                        if (g > 0 && !await(&o_done[(g - 1) & 1], ((g - 1) >> 1) & 1, abort_flag,
+                                            status))
+                            alive = false;
                         for (int z = 0; z < TS; ++z) {
                             const uint32_t c = base + z;
                             const int s = c % NS;

@@ -136,6 +136,11 @@ CASES = {
     "odd_group": dict(key_counts=[33, 900], k=7, q_heads=6, kv_heads=2, head_dim=512),
     "120_rows": dict(key_counts=[15, 640, 129], k=15, q_heads=16, kv_heads=2, head_dim=512),
     "128_rows": dict(key_counts=[16, 400], k=16, q_heads=8, kv_heads=1, head_dim=256),
+    "40_rows": dict(key_counts=[20, 1300, 257], k=5, q_heads=16, kv_heads=2, head_dim=512),
+    "64_rows_256": dict(key_counts=[16, 900, 5000], k=16, q_heads=8, kv_heads=2, head_dim=256,
+                        window=700),
+    "80_rows": dict(key_counts=[10, 1100], k=10, q_heads=16, kv_heads=2, head_dim=512),
+    "long_120_rows": dict(key_counts=[6000, 2500], k=15, q_heads=16, kv_heads=2, head_dim=512),
     "64_heads": dict(key_counts=[2, 270], k=2, q_heads=64, kv_heads=1, head_dim=512),
     "long": dict(key_counts=[9000], k=2, q_heads=16, kv_heads=2, head_dim=512),
     "long_256": dict(key_counts=[20011], k=1, q_heads=8, kv_heads=4, head_dim=256),

@@ -66,7 +66,7 @@ def segments(st, tiles, kv_heads):
                     n = tiles[b]
 
 
-@pytest.mark.parametrize("seed", range(150))
+@pytest.mark.parametrize("seed", range(400))
 def test_every_tile_once_and_every_piece_found(seed):
     rng = random.Random(seed)
     batch = rng.choice([1, 1, 2, 3, 8, 31, 32, 33, 64, 70])
@@ -144,3 +144,240 @@ def test_stage_numbers_of_the_value_tiles(lengths, ts):
     ends = {f - 1 for f in firsts if f} | {total - 1}
     for g in range(total):
         assert at["v", g] == ts * (2 * g + (1 if g in ends else 2))
+
+
+# ---------------------------------------------------------------------------
+# The barriers between a CTA's warps, under random interleavings.  A wait for a
+# phase is a wait for its parity, so it may mistake an older phase of the same
+# parity for its own; every wait here knows the phase it means and checks.
+
+class Barrier:
+    def __init__(self, count=1):
+        self.count, self.pending, self.tx, self.done = count, count, 0, 0
+
+    def arrive(self, tx=0):
+        assert self.pending > 0, "more arrivals than a phase takes"
+        self.pending -= 1
+        self.tx += tx
+        self.flip()
+
+    def land(self, n=1):
+        self.tx -= n
+        self.flip()
+
+    def flip(self):
+        if self.pending == 0 and self.tx == 0:
+            self.done += 1
+            self.pending = self.count
+
+    def passes(self, phase):
+        """A wait for `phase` (0, 1, ...) by its parity; phase -1 passes at once."""
+        if (self.done - 1) % 2 != phase % 2:
+            return False
+        assert self.done >= phase + 1, "an older phase of the same parity"
+        return True
+
+
+class Cta:
+    """The kernel's roles as generators that yield the waits they stand at."""
+
+    def __init__(self, lengths, ts, ns, pb, qb, halves, slots=4):
+        self.lengths, self.ts, self.ns, self.pb, self.qb, self.slots = lengths, ts, ns, pb, qb, slots
+        two = lambda n, c=1: [Barrier(c) for _ in range(n)]
+        self.full, self.empty = two(ns), two(ns)
+        self.s_full, self.p_full, self.o_done = two(2), two(2, halves), two(2)
+        self.q_full, self.q_empty, self.q_free = two(2), two(2), two(2, halves)
+        self.nan_full, self.sc_full, self.sc_empty = two(2), two(slots), two(slots, halves)
+        self.stage = [None] * ns          # what a stage holds: (load, landed)
+        self.scores, self.weights = [None] * 2, [None] * pb
+        self.queries, self.factors = [None] * qb, [None] * 2
+        self.reading = [0] * ns           # products that still read a stage
+        self.o_of = None                  # segment O belongs to
+        self.written = 0
+        self.flying = []                  # copies in flight
+        self.queue = []                   # the products' signals, in order
+        self.roles = {"load": self.load(), "scales": self.scales(), "fetch": self.fetch(),
+                      "mma": self.mma()}
+        for h in range(halves):
+            self.roles["soft%d" % h] = self.softmax(h)
+        self.at = {}
+
+    def tiles(self):
+        g = 0
+        for si, n in enumerate(self.lengths):
+            for x in range(n):
+                yield si, g, x == 0, x + 1 == n
+                g += 1
+
+    def k_index(self, g, first):
+        return self.ts * (2 * g if first else 2 * g - 1)
+
+    def v_index(self, g, last):
+        return self.ts * (2 * g + (1 if last else 2))
+
+    def load(self):
+        order, prev = [], None
+        for t in list(self.tiles()) + [None]:
+            pair = [("k", t), ("v", prev)]
+            for kind, tile in pair[::-1] if t and t[2] and prev else pair:
+                if tile:
+                    order += [(kind, tile[1], z) for z in range(self.ts)]
+            prev = t
+        for i, what in enumerate(order):
+            s = i % self.ns
+            if i >= self.ns:
+                yield self.empty[s], i // self.ns - 1
+            assert self.reading[s] == 0, "a stage overwritten while it is read"
+            self.stage[s] = (what, False)
+            self.full[s].arrive(tx=1)
+            self.flying.append(("stage", s, what))
+
+    def scales(self):
+        for _, g, _, _ in self.tiles():
+            if g >= self.slots:
+                yield self.sc_empty[g % self.slots], g // self.slots - 1
+            self.sc_full[g % self.slots].arrive()
+
+    def fetch(self):
+        for si in range(len(self.lengths)):
+            was = si - self.qb
+            if was >= 0:
+                yield self.q_empty[was & 1], was >> 1
+            if si >= 2:
+                yield self.q_free[si & 1], (si - 2) >> 1
+            self.queries[si % self.qb] = self.factors[si & 1] = None
+            self.q_full[si & 1].arrive(tx=1)
+            self.flying.append(("q", si, None))
+            self.nan_full[si & 1].arrive()
+
+    def use(self, kind, g, index):
+        for z in range(self.ts):
+            s = (index + z) % self.ns
+            yield self.full[s], (index + z) // self.ns
+            assert self.stage[s] == ((kind, g, z), True), "a product reads another load's stage"
+            self.reading[s] += 1
+            self.queue.append(("free", s))
+
+    def mma(self):
+        prev = None
+        for t in list(self.tiles()) + [None]:
+            pair = [("k", t), ("v", prev)]
+            for kind, tile in pair[::-1] if t and t[2] and prev else pair:
+                if not tile:
+                    continue
+                si, g, first, last = tile
+                if kind == "k":
+                    if first:
+                        yield self.q_full[si & 1], si >> 1
+                    assert self.queries[si % self.qb] == si
+                    self.scores[g & 1] = None
+                    yield from self.use("k", g, self.k_index(g, first))
+                    self.queue.append(("scores", g))
+                    if last:
+                        self.queue.append(("q", si))
+                else:
+                    yield self.p_full[g & 1], g >> 1
+                    assert self.weights[g % self.pb] == (g, len(self.soft()))
+                    yield from self.use("v", g, self.v_index(g, last))
+                    assert first is (self.o_of != si)
+                    self.o_of = si
+                    self.queue.append(("o", g))
+            prev = t
+
+    def soft(self):
+        return [r for r in self.roles if r.startswith("soft")]
+
+    def softmax(self, half):
+        for si, g, first, last in self.tiles():
+            if first:
+                yield self.q_full[si & 1], si >> 1
+            assert self.factors[si & 1] == si
+            yield self.s_full[g & 1], g >> 1
+            yield self.sc_full[g % self.slots], g // self.slots
+            assert self.scores[g & 1] == g
+            self.sc_empty[g % self.slots].arrive()
+            if self.pb == 2 and g > 1:
+                yield self.o_done[g & 1], (g - 2) >> 1
+            if g > 0 and (self.pb == 1 or random.random() < 0.2):
+                yield self.o_done[(g - 1) & 1], (g - 1) >> 1
+            w = self.weights[g % self.pb]
+            assert w is None or w[0] == g or w[0] < g
+            self.weights[g % self.pb] = (g, 1 + (w[1] if w and w[0] == g else 0))
+            if last or random.random() < 0.2:      # an edge tile
+                yield self.nan_full[si & 1], si >> 1
+                if g > 0:
+                    yield self.o_done[(g - 1) & 1], (g - 1) >> 1
+                for z in range(self.ts):
+                    i = self.v_index(g, last) + z
+                    yield self.full[i % self.ns], i // self.ns
+                    assert self.stage[i % self.ns] == (("v", g, z), True)
+            self.p_full[g & 1].arrive()
+            if last:
+                yield self.o_done[g & 1], g >> 1
+                assert self.o_of == si
+                self.written += 1
+                self.q_free[si & 1].arrive()
+
+    def step(self, rng, bias):
+        """One random thing that can happen; False when nothing can."""
+        can = []
+        for name, role in self.roles.items():
+            wait = self.at.get(name)
+            if wait == "end" or (wait and not wait[0].passes(wait[1])):
+                continue
+            can.append(("role", name))
+        can += [("land", i) for i in range(len(self.flying))]
+        can += [("tensor", 0)] if self.queue else []
+        if not can:
+            return False
+        kind, what = rng.choices(can, [bias.get(c[1] if c[0] == "role" else c[0], 1.0)
+                                       for c in can])[0]
+        if kind == "role":
+            try:
+                self.at[what] = next(self.roles[what])
+            except StopIteration:
+                self.at[what] = "end"
+        elif kind == "land":
+            k, a, b = self.flying.pop(what)
+            if k == "stage":
+                assert self.stage[a] == (b, False)
+                self.stage[a] = (b, True)
+                self.full[a].land()
+            else:
+                self.queries[a % self.qb] = self.factors[a & 1] = a
+                self.q_full[a & 1].land()
+        else:
+            k, a = self.queue.pop(0)
+            if k == "free":
+                self.reading[a] -= 1
+                self.empty[a].arrive()
+            elif k == "scores":
+                self.scores[a & 1] = a
+                self.s_full[a & 1].arrive()
+            elif k == "q":
+                self.q_empty[a & 1].arrive()
+            else:
+                self.o_done[a & 1].arrive()
+        return True
+
+
+# (stages of a K tile, ring, weights' buffers, queries' buffers, softmax groups)
+LAYOUTS = {"512 x 32": (2, 5, 2, 1, 2), "512 x 16": (2, 6, 2, 1, 2), "512 x 8": (2, 6, 2, 2, 1),
+           "256 x 32": (1, 5, 2, 2, 2), "256 x 16": (1, 3, 1, 1, 1), "256 x 8": (1, 3, 1, 2, 1)}
+
+
+@pytest.mark.parametrize("layout", sorted(LAYOUTS))
+def test_the_warps_never_wait_for_the_wrong_phase(layout):
+    for seed in range(400):
+        rng = random.Random(seed)
+        random.seed(seed)
+        lengths = [rng.choice([1, 1, 2, 3, 9]) for _ in range(rng.randrange(0, 7))]
+        cta = Cta(lengths, *LAYOUTS[layout])
+        names = list(cta.roles) + ["land", "tensor"]
+        bias = {n: rng.choice([1.0, 1.0, 0.02, 30.0]) for n in names}
+        steps = 0
+        while cta.step(rng, bias):
+            steps += 1
+        assert all(cta.at.get(n) == "end" for n in cta.roles), (seed, lengths, cta.at)
+        assert not cta.flying and not cta.queue
+        assert cta.written == len(lengths) * len(cta.soft())
