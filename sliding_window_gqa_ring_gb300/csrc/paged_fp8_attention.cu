@@ -194,6 +194,19 @@ struct SegIter {
         }
     }
 
+    // To the next unit that has tiles.
+    __device__ void advance(const PagedFp8Params &p) {
+        off = 0;
+        if (++c < p.kv_heads) return;
+        c = 0;
+        ntiles = 0;
+        while (ntiles == 0 && b + 1 < p.batch) {
+            ++b;
+            rq = load_request(p, b);
+            ntiles = request_tiles(p, rq, &first);
+        }
+    }
+
     __device__ __noinline__ bool next(const PagedFp8Params &p, Segment &sg) {
         if (pos >= end || off >= ntiles) return false;
         const int len = min(ntiles - off, end - pos);
@@ -208,18 +221,7 @@ struct SegIter {
         sg.opens = pos == start;
         pos += len;
         off += len;
-        if (off == ntiles && pos < end) {
-            off = 0;
-            if (++c == p.kv_heads) {
-                c = 0;
-                ntiles = 0;
-                while (ntiles == 0 && b + 1 < p.batch) {
-                    ++b;
-                    rq = load_request(p, b);
-                    ntiles = request_tiles(p, rq, &first);
-                }
-            }
-        }
+        if (off == ntiles && pos < end) advance(p);
         return true;
     }
 };
@@ -693,10 +695,13 @@ __global__ void __launch_bounds__(Lay<D, N>::kThreads, Lay<D, N>::OCC)
                                                  : tc::l2_evict_first_policy();
             SegIter it;
             it.init(p, sh);
-            Segment sg;
-            bool have = it.next(p, sg);
-            int x = have ? sg.x0 : 0;
+            Segment sg, nx;
+            bool have = it.next(p, sg), have_next = false;
             int pi = -1, page = 0, pi_next = -1, page_next = 0;   // a page read ahead
+            auto read_ahead = [&](const Segment &to, int want) {
+                pi_next = want < p.max_pages ? want : -1;
+                if (pi_next >= 0) page_next = p.page_table[(size_t)to.b * p.max_pages + want];
+            };
             uint32_t cnt = 0;
             bool alive = true;
             auto issue = [&](const CUtensorMap *map, long long row, int c) {
@@ -712,50 +717,35 @@ __global__ void __launch_bounds__(Lay<D, N>::kThreads, Lay<D, N>::OCC)
                     ++cnt;
                 }
             };
-            long long prev_row = 0;
-            int prev_c = 0;
-            bool prev = false;
-            // K of a tile before V of the one in front of it, but for a segment's
-            // last tile, whose V comes first
-            while (alive) {
-                long long row = 0;
-                const bool cur = have, first = cur && x == sg.x0;
-                const int c = sg.c;
-                if (cur) {
-                    const int tile = sg.first + x, want = tile / pages_shift_tiles;
-                    if (want != pi) {
-                        page = want == pi_next
-                                   ? page_next
-                                   : p.page_table[(size_t)sg.b * p.max_pages + want];
-                        pi = want;
-                        pi_next = want + 1;
-                        if (pi_next < p.max_pages)
-                            page_next = p.page_table[(size_t)sg.b * p.max_pages + pi_next];
-                        else
-                            pi_next = -1;
+            while (have && alive) {
+                long long row = 0, prev_row = 0;
+                // K of a tile before V of the one in front of it
+                for (int x = sg.x0; x <= sg.x1 && alive; ++x) {
+                    prev_row = row;
+                    if (x < sg.x1) {
+                        const int tile = sg.first + x, want = tile / pages_shift_tiles;
+                        if (want != pi) {
+                            if (want != pi_next) read_ahead(sg, want);
+                            page = page_next;
+                            pi = want;
+                            read_ahead(sg, want + 1);
+                        }
+                        row = tile_row(page, tile);
+                        if (row < 0) {   // loads the zero fill past the pool's end
+                            set_status(status, CARAT_DEV_BAD_CACHE_ID);
+                            row = (long long)p.num_pages * p.page_rows;
+                        }
+                        issue(&map_k, row, sg.c);
                     }
-                    row = tile_row(page, tile);
-                    if (row < 0) {   // loads the zero fill past the pool's end
-                        set_status(status, CARAT_DEV_BAD_CACHE_ID);
-                        row = (long long)p.num_pages * p.page_rows;
-                    }
-                    if (++x == sg.x1) {
-                        const int b_was = sg.b;
-                        have = it.next(p, sg);
-                        x = have ? sg.x0 : 0;
-                        if (have && sg.b != b_was) pi = pi_next = -1;
-                    }
+                    if (x > sg.x0) issue(&map_v, prev_row, sg.c);
+                    // The next segment is looked up early, with the ring full: its code and
+                    // data come late from a memory system that is kept busy.
+                    if (x == sg.x0 + 1) have_next = it.next(p, nx);
                 }
-#pragma unroll 1
-                for (int z = 0; z < 2; ++z) {
-                    const bool is_k = (z == 0) != (first && prev);
-                    if (is_k && cur) issue(&map_k, row, c);
-                    if (!is_k && prev) issue(&map_v, prev_row, prev_c);
-                }
-                prev = cur;
-                prev_row = row;
-                prev_c = c;
-                if (!cur) break;
+                have = have_next;
+                sg = nx;
+                pi = -1;
+                if (have) read_ahead(sg, (sg.first + sg.x0) / pages_shift_tiles);
             }
             // the last copies land before the CTA goes, whichever role stops early
             for (uint32_t i = cnt > (uint32_t)NS ? cnt - NS : 0; i < cnt; ++i)
@@ -785,10 +775,9 @@ __global__ void __launch_bounds__(Lay<D, N>::kThreads, Lay<D, N>::OCC)
         const uint64_t p_desc = tc::sdesc_sw128(tc::smem_u32(s_p), 16, 1024);
         SegIter it;
         it.init(p, sh);
-        Segment sg;
+        Segment sg, nx;
         bool alive = true, have = it.next(p, sg);
-        int x = have ? sg.x0 : 0, si = 0;
-        uint32_t g = 0;
+        uint32_t g = 0;                 // tiles before this segment
         int ms = 0;                     // the next stage and its phase
         uint32_t mphase = 0;
         auto advance = [&]() {
@@ -801,18 +790,16 @@ __global__ void __launch_bounds__(Lay<D, N>::kThreads, Lay<D, N>::OCC)
         auto wait_all = [&](uint64_t *bar, uint32_t parity) {
             return __all_sync(kFull, await(bar, parity, abort_flag, status)) != 0;
         };
-        bool prev = false, prev_first = false;   // the tile whose PV product is due
-        while (alive) {
-            const bool cur = have, first = cur && x == sg.x0;
-            // The loads' order: QK of a tile before PV of the one in front of it, but
-            // at a segment's start PV first, so that its output can be read out.
+        // In the loads' order: QK of a tile before PV of the one in front of it.
+        for (int si = 0; have && alive; ++si) {
+            alive = wait_all(&q_full[si & 1], (si >> 1) & 1);
+            const int n = sg.x1 - sg.x0;
+            bool have_next = false;
 #pragma unroll 1
-            for (int z = 0; z < 2 && alive; ++z) {
-                const bool qk = (z == 0) != (first && prev);
-                if (qk && cur) {
-                    // S^T[g & 1] = K . [q_hi | q_lo]^T
-                    if (first && !(alive = wait_all(&q_full[si & 1], (si >> 1) & 1))) break;
-                    const uint32_t d = tmem + (g & 1) * 2 * N;
+            for (int x = 0; x <= n && alive; ++x) {
+                if (x < n) {
+                    // S^T[y & 1] = K . [q_hi | q_lo]^T
+                    const uint32_t y = g + x, d = tmem + (y & 1) * 2 * N;
                     uint64_t q = q_desc + si % L::QB * (L::kQBytes / 16);
 #pragma unroll 1
                     for (int ks = 0; ks < TS; ++ks) {
@@ -829,17 +816,13 @@ __global__ void __launch_bounds__(Lay<D, N>::kThreads, Lay<D, N>::OCC)
                         advance();
                     }
                     if (!alive) break;
-                    tc::mma_commit_warp(&s_full[g & 1]);
-                    if (++x == sg.x1) {
-                        tc::mma_commit_warp(&q_empty[si & 1]);
-                        ++si;
-                        have = it.next(p, sg);
-                        x = have ? sg.x0 : 0;
-                    }
+                    tc::mma_commit_warp(&s_full[y & 1]);
+                    if (x + 1 == n) tc::mma_commit_warp(&q_empty[si & 1]);
+                    if (x == 0) have_next = it.next(p, nx);   // early, as the loads do
                 }
-                if (!qk && prev) {
+                if (x > 0) {
                     // O^T += V^T . [w1 | w2 | w3]^T of the tile before
-                    const uint32_t h = g - 1;
+                    const uint32_t h = g + x - 1;
                     if (!(alive = wait_all(&p_full[h & 1], (h >> 1) & 1))) break;
                     tc::tc_fence_after();
                     const uint64_t w = p_desc + h % L::PB * (L::kPBytes / 16);
@@ -854,7 +837,7 @@ __global__ void __launch_bounds__(Lay<D, N>::kThreads, Lay<D, N>::OCC)
                             tc::mma_f8_ss_warp(d + kk / 4 * L::PR,
                                                a + kk / 4 * (kSlab / 16) + 256 * (kk % 4),
                                                w + 2 * (kk % 4), idesc_pv,
-                                               !(prev_first && kk % 4 == 0));
+                                               !(x == 1 && kk % 4 == 0));
                         tc::mma_commit_warp(&empty[ms]);
                         d += 2 * L::PR;
                         advance();
@@ -863,10 +846,9 @@ __global__ void __launch_bounds__(Lay<D, N>::kThreads, Lay<D, N>::OCC)
                     tc::mma_commit_warp(&o_done[h & 1]);
                 }
             }
-            if (!cur) break;
-            prev = true;
-            prev_first = first;
-            ++g;
+            g += n;
+            have = have_next;
+            sg = nx;
         }
         // so do the last products
         tc::mma_commit_warp(fin);
@@ -877,43 +859,36 @@ __global__ void __launch_bounds__(Lay<D, N>::kThreads, Lay<D, N>::OCC)
         // the first tile's (up to) eight blocks, lanes 16-31 those of the second.
         SegIter it;
         it.init(p, sh);
-        Segment sg;
-        bool have = it.next(p, sg);
-        int x = have ? sg.x0 : 0;
+        Segment sg, nx;
+        bool alive = true, have = it.next(p, sg);
         const int blocks = kKeys / p.block_rows, i = lane & 7;
         const float *src = (lane & 8) ? p.v_scales : p.k_scales;
         uint32_t g = 0;
-        bool alive = true;
         while (have && alive) {
-            int n = 0, my_b = 0, my_c = 0, my_tile = 0;
-            for (; n < 2 && have; ++n) {
-                if (lane / 16 == n) {
-                    my_b = sg.b;
-                    my_c = sg.c;
-                    my_tile = sg.first + x;
+            bool have_next = false;
+            for (int x = sg.x0; x < sg.x1 && alive; x += 2) {
+                const int n = min(sg.x1 - x, 2), tile = sg.first + x + lane / 16;
+                float v = 1.f;   // a page outside the pool: K and V are zeros, any scale will do
+                if (lane / 16 < n && i < blocks) {
+                    const int page =
+                        p.page_table[(size_t)sg.b * p.max_pages + tile / pages_shift_tiles];
+                    const long long row = tile_row(page, tile);
+                    if (row >= 0) v = src[(size_t)(row / p.block_rows + i) * p.kv_heads + sg.c];
                 }
-                if (++x == sg.x1) {
-                    have = it.next(p, sg);
-                    x = have ? sg.x0 : 0;
+                for (int z = 0; z < n; ++z, ++g) {
+                    const int slot = g % kSlots;
+                    alive = alive && (g < kSlots || await(&sc_empty[slot], ((g / kSlots) & 1) ^ 1,
+                                                          abort_flag, status));
+                    alive = __all_sync(kFull, alive);
+                    if (!alive) break;
+                    if (lane / 16 == z) s_sc[slot * 16 + (lane & 15)] = v;
+                    __syncwarp();
+                    if (lane == 0) tc::mbar_arrive(&sc_full[slot]);
                 }
+                if (x == sg.x0) have_next = it.next(p, nx);
             }
-            float v = 1.f;   // a page outside the pool: K and V are zeros, any scale will do
-            if (lane / 16 < n && i < blocks) {
-                const int page =
-                    p.page_table[(size_t)my_b * p.max_pages + my_tile / pages_shift_tiles];
-                const long long row = tile_row(page, my_tile);
-                if (row >= 0) v = src[(size_t)(row / p.block_rows + i) * p.kv_heads + my_c];
-            }
-            for (int z = 0; z < n; ++z, ++g) {
-                const int slot = g % kSlots;
-                alive = alive && (g < kSlots || await(&sc_empty[slot], ((g / kSlots) & 1) ^ 1,
-                                                      abort_flag, status));
-                alive = __all_sync(kFull, alive);
-                if (!alive) break;
-                if (lane / 16 == z) s_sc[slot * 16 + (lane & 15)] = v;
-                __syncwarp();
-                if (lane == 0) tc::mbar_arrive(&sc_full[slot]);
-            }
+            have = have_next;
+            sg = nx;
         }
     } else if (warp == 3) {
         // ------------------------------------------------------------ queries
