@@ -90,6 +90,10 @@ struct Lay {
     static constexpr int kQBlock = 2 * N * 128;       // 128 d of the query pieces
     static constexpr int kQBytes = KS * kQBlock;
     static constexpr int kPBytes = PR * 128;          // a tile's weights
+    // Weights of 32 rows lie as three pieces [128 keys][32 rows], so a thread stores
+    // the 16 rows of its key with one instruction a piece; of fewer as
+    // [3N rows][128 keys].
+    static constexpr bool kWide = N == 32;
     static constexpr int kOffQ = NS * kStage;
     static constexpr int kOffP = kOffQ + QB * kQBytes;
     static constexpr int kOffRed = kOffP + PB * kPBytes;
@@ -765,14 +769,16 @@ __global__ void __launch_bounds__(Lay<D, N>::kThreads, Lay<D, N>::OCC)
     if (warp == 1) {
         // ------------------------------------------------------------ products
         constexpr uint32_t idesc_qk = tc::idesc_e4m3_f32(128, 2 * N, false, false);
-        constexpr uint32_t idesc_pv = tc::idesc_e4m3_f32(128, L::PR, true, true);
+        constexpr uint32_t idesc_pv = tc::idesc_e4m3_f32(128, L::PR, true, true, L::kWide);
         const uint32_t tmem = sh->tmem;
         // descriptors in units of 16 bytes of shared memory: 32 elements along K
         // are 2 units in a K-major operand, 32 rows of 128 bytes in V
         const uint64_t k_desc = tc::sdesc_sw128(tc::smem_u32(smem), 16, 1024);
         const uint64_t v_desc = tc::sdesc_sw128(tc::smem_u32(smem), kSlab, 1024);
         const uint64_t q_desc = tc::sdesc_sw128(tc::smem_u32(s_q), 16, 1024);
-        const uint64_t p_desc = tc::sdesc_sw128(tc::smem_u32(s_p), 16, 1024);
+        const uint64_t p_desc = L::kWide ? tc::sdesc_sw32(tc::smem_u32(s_p), kKeys * 32, 256)
+                                         : tc::sdesc_sw128(tc::smem_u32(s_p), 16, 1024);
+        constexpr int kPStep = L::kWide ? 64 : 2;   // 32 keys of the weights
         SegIter it;
         it.init(p, sh);
         Segment sg, nx;
@@ -836,7 +842,7 @@ __global__ void __launch_bounds__(Lay<D, N>::kThreads, Lay<D, N>::OCC)
                         for (int kk = 0; kk < 8; ++kk)
                             tc::mma_f8_ss_warp(d + kk / 4 * L::PR,
                                                a + kk / 4 * (kSlab / 16) + 256 * (kk % 4),
-                                               w + 2 * (kk % 4), idesc_pv,
+                                               w + kPStep * (kk % 4), idesc_pv,
                                                !(x == 1 && kk % 4 == 0));
                         tc::mma_commit_warp(&empty[ms]);
                         d += 2 * L::PR;
@@ -1095,10 +1101,14 @@ __global__ void __launch_bounds__(Lay<D, N>::kThreads, Lay<D, N>::OCC)
                         }
                         tc::tmem_st_wait();
                     }
-                    // weights, two rows at a time; byte t of row r of the K-major
-                    // operand, 16-byte pieces swizzled by r % 8 (r0 and N are
+                    // weights, two rows at a time: the thread's 16 bytes of key t, the two
+                    // halves of 32 swapped in every other four keys; or byte t of row r of
+                    // the K-major operand, 16-byte pieces swizzled by r % 8 (r0 and N are
                     // multiples of 8)
-                    uint8_t *pw = s_p + g % L::PB * L::kPBytes + r0 * 128 + (t & 15);
+                    uint8_t *pw = s_p + g % L::PB * L::kPBytes +
+                                  (L::kWide ? t * 32 + ((half ^ (t >> 2)) & 1) * 16
+                                            : r0 * 128 + (t & 15));
+                    uint32_t wide[3][NC / 4];
                     const __half2 eight = __floats2half2_rn(8.f, 8.f);
                     const uint64_t vs2 = pack2(vs, vs);
 #pragma unroll
@@ -1115,10 +1125,20 @@ __global__ void __launch_bounds__(Lay<D, N>::kThreads, Lay<D, N>::OCC)
 #pragma unroll
                         for (int z = 0; z < 3; ++z) {
                             const uint32_t b = e5m2x2(h);
-                            pa[z * N * 128] = (uint8_t)b;
-                            pb[z * N * 128] = (uint8_t)(b >> 8);
+                            if constexpr (L::kWide) {
+                                wide[z][e / 4] = e % 4 == 0 ? b : wide[z][e / 4] | b << 16;
+                            } else {
+                                pa[z * N * 128] = (uint8_t)b;
+                                pb[z * N * 128] = (uint8_t)(b >> 8);
+                            }
                             if (z < 2) h = __hmul2(__hsub2(h, e5m2x2_to_f16x2(b)), eight);
                         }
+                    }
+                    if constexpr (L::kWide) {
+#pragma unroll
+                        for (int z = 0; z < 3; ++z)
+                            *reinterpret_cast<uint4 *>(pw + z * kKeys * 32) =
+                                make_uint4(wide[z][0], wide[z][1], wide[z][2], wide[z][3]);
                     }
                     // A tile with rows outside the request's keys: their V bytes must not
                     // meet a zero weight (0 x NaN), so they are zeroed.  NaNs among the
@@ -1158,7 +1178,7 @@ __global__ void __launch_bounds__(Lay<D, N>::kThreads, Lay<D, N>::OCC)
 #pragma unroll 1
                             for (int e = 0; e < NC; ++e)
                                 if ((seen >> e) & 1u)
-                                    pw[((((t >> 4) ^ e) & 7) << 4) + e * 128] = 0x7f;
+                                    pw[L::kWide ? e : ((((t >> 4) ^ e) & 7) << 4) + e * 128] = 0x7f;
                         }
                     }
                 }

@@ -305,6 +305,14 @@ __device__ __forceinline__ uint64_t sdesc_sw128(uint32_t saddr, uint32_t lbo_byt
     return d;
 }
 
+// The same with SWIZZLE_32B (value 6): MN-major tiles stored as blocks of 32 bytes
+// of MN by the K rows; LBO = bytes between the blocks, SBO = 256 (next group of 8 K
+// rows).
+__device__ __forceinline__ uint64_t sdesc_sw32(uint32_t saddr, uint32_t lbo_bytes,
+                                               uint32_t sbo_bytes) {
+    return (sdesc_sw128(saddr, lbo_bytes, sbo_bytes) & ~((uint64_t)7 << 61)) | (uint64_t)6 << 61;
+}
+
 // Instruction descriptor for tcgen05.mma kind::f16 with bf16 A and B and an
 // fp32 accumulator: D format (bits 4-5) = 1, A format (7-9) = 1, B format
 // (10-12) = 1, A major (15), B major (16) (0 = K-major, 1 = MN-major),
@@ -325,8 +333,10 @@ __host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, bool a_mn_maj
 
 // Instruction descriptor for kind::f8f6f4 with e4m3 A and e4m3 (type field 0)
 // or e5m2 (1) B, fp32 accumulator.
-__host__ __device__ constexpr uint32_t idesc_e4m3_f32(int M, int N, bool a_mn_major, bool b_e5m2) {
+__host__ __device__ constexpr uint32_t idesc_e4m3_f32(int M, int N, bool a_mn_major, bool b_e5m2,
+                                                     bool b_mn_major = false) {
     return (1u << 4) | ((b_e5m2 ? 1u : 0u) << 10) | ((a_mn_major ? 1u : 0u) << 15) |
+           ((b_mn_major ? 1u : 0u) << 16) |
            ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
