@@ -90,10 +90,10 @@ struct Lay {
     static constexpr int kQBlock = 2 * N * 128;       // 128 d of the query pieces
     static constexpr int kQBytes = KS * kQBlock;
     static constexpr int kPBytes = PR * 128;          // a tile's weights
-    // Weights of 32 rows lie as three pieces [128 keys][32 rows], so a thread stores
-    // the 16 rows of its key with one instruction a piece; of fewer as
-    // [3N rows][128 keys].
-    static constexpr bool kWide = N == 32;
+    // Weights of 32 rows lie as three pieces [128 keys][32 rows], of 8 rows as one
+    // block [128 keys][w1 w2 w3 -], so a thread stores 16 bytes of its key at a time;
+    // of 16 rows as [3N rows][128 keys].
+    static constexpr bool kWide = N != 16;
     static constexpr int kOffQ = NS * kStage;
     static constexpr int kOffP = kOffQ + QB * kQBytes;
     static constexpr int kOffRed = kOffP + PB * kPBytes;
@@ -1135,10 +1135,18 @@ __global__ void __launch_bounds__(Lay<D, N>::kThreads, Lay<D, N>::OCC)
                         }
                     }
                     if constexpr (L::kWide) {
+                        if constexpr (N == 8) {
+                            *reinterpret_cast<uint4 *>(pw) =
+                                make_uint4(wide[0][0], wide[0][1], wide[1][0], wide[1][1]);
+                            *reinterpret_cast<uint2 *>(
+                                reinterpret_cast<uintptr_t>(pw) ^ 16) =
+                                make_uint2(wide[2][0], wide[2][1]);
+                        } else {
 #pragma unroll
-                        for (int z = 0; z < 3; ++z)
-                            *reinterpret_cast<uint4 *>(pw + z * kKeys * 32) =
-                                make_uint4(wide[z][0], wide[z][1], wide[z][2], wide[z][3]);
+                            for (int z = 0; z < 3; ++z)
+                                *reinterpret_cast<uint4 *>(pw + z * kKeys * 32) =
+                                    make_uint4(wide[z][0], wide[z][1], wide[z][2], wide[z][3]);
+                        }
                     }
                     // A tile with rows outside the request's keys: their V bytes must not
                     // meet a zero weight (0 x NaN), so they are zeroed.  NaNs among the
