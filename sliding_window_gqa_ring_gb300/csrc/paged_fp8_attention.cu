@@ -28,21 +28,47 @@
 // The scales cost nothing in the products: thread t of the softmax owns key t,
 // so ks[t] is one factor of its scores, and vs[t] one of its weights.
 //
-// The running maximum m is that of s_t + log2 vs[t], not of s_t: it bounds the weights that are really rounded, whatever the scales'
-// range.  It moves only when exceeded by more than kSlack, and the sum
-// of 2^(s_t - m) is taken over the rounded weights, in fp32.
+// The running maximum m is that of s_t + log2 vs[t], not of s_t: it bounds the
+// weights that are rounded, whatever the scales' range.  It moves only when
+// exceeded by more than kSlack.  The denominator is the sum of 2^(s_t - m) itself,
+// in fp32, before vs[t] and the rounding: keys with a tiny scale (a block of zero
+// values) keep their share of it although their weights vanish.
+//
+// NaN.  Keys that a row does not see get weight 0, and 0 x NaN is NaN in a product.
+// So V rows outside the request's keys are zeroed in shared memory, and keys that
+// some of a step's queries see and others do not are looked through for NaNs by
+// warp 3; found ones are taken out of V and put into the weights of the rows that
+// see them.
 //
 // Schedule: stream-K.  All (request, KV head) units' tiles form one sequence,
-// cut into ranges of equal cost, one per CTA (one CTA per SM; with G row groups
-// CTAs G r .. G r + G - 1 walk range r together, one group each, so the tiles
-// they share come from L2).  A segment that covers a whole unit writes its
-// output; the others leave a partial (max, sum, O) for the merge launch, which
-// finds them through a table with one entry per unit.
+// cut into ranges of equal cost, one per CTA (with G row groups CTAs
+// G r .. G r + G - 1 walk range r together, one group each, so the tiles they
+// share come from L2).  A segment that covers a whole unit writes its output; the
+// others leave a partial (max, sum, O) for the merge launch, which finds them
+// through a table with one entry per unit.  A unit's start is charged kCharge = 5
+// tiles.  Measured, 2 to 7 (us): 64 requests x 4 proposals up to 32768 keys 201, 198,
+// 191, 188, 187, 187; 56 x 1 in a window of 1024 65.5, 65.5, 63.0, 62.0, 62.8, 64.0.
+//
+// Three launches, each started while the one before it runs (programmatic
+// dependent launch): the queries' split, this kernel, the merge.
 //
 // Warps: 0 loads tiles (TMA), 1 issues the products, 2 fetches the tiles' block
-// scales ahead of the softmax, 4-11 run it: warps 4-7 own the first half of
-// the rows, 8-11 the second, thread t of each half key t of the tile.  Every
-// wait is bounded.
+// scales ahead of the softmax, 3 fetches the split queries and looks for NaNs, 4 and
+// up run the softmax: one or two groups of four warps, each with half the rows (or
+// all), thread t of a group key t of the tile.  Every wait is bounded.  A wait for a
+// barrier's phase is a wait for its parity, so it may only be made once the phase
+// before is known to be over; a model of the roles on the CPU checks that.
+//
+// What it reaches (copy rate of the device: 6796 GB/s), all launches included:
+// 64 requests x 4 proposals, 16/2 heads of 512, up to 32768 keys each (1044 MB):
+// 185 us, 5640 GB/s, bound by the loads but for the start, the units' boundaries and
+// the merge.  56 x 1, 16/8 heads of 256, window 1024 (236 MB): 59 us, of which about
+// 20 do not grow with the batch (start, first loads, drain, merge; 224 x 1: 171 us,
+// 5530 GB/s).  8 x 15 (173 MB, 120 rows in four groups): 90 us, bound by a tile's
+// products and softmax, not by its loads (a quarter of the products: 86 us before
+// the wide stores of the weights, then 100; pairs of row groups loading for one
+// another by multicast: no change).  One request of 1500 or 6005 keys: 17 and 22 us,
+// a chain of latencies (split 2, first load to last output 11 to 15, merge 4 to 6).
 #include <algorithm>
 #include <atomic>
 
@@ -70,8 +96,12 @@ constexpr float kBoost = 6.f, kWeight = 64.f;
 constexpr float kUnset = -1e30f;           // maximum of a row that has seen no key yet
 
 // Two shapes of CTA.  With up to 16 rows at head_dim 256 two CTAs share an SM, so
-// that one streams while the other is at a unit's boundary or starting up; else one
-// CTA takes the SM and its shared memory, with eight softmax warps (four for 8 rows).
+// that one streams while the other is at a unit's boundary or starting up (56
+// requests x 1, window 1024: 63 us, one CTA 75); else one CTA takes the SM and its
+// shared memory, with eight softmax warps (four for 8 rows; sixteen for 32 rows
+// gave 101 against 100 us at 8 x 15 and 192 against 188 at 64 x 4).
+// A stage is 32 KB: of 16 KB, 8 x 15 took 104 us against 95.  Tiles of 8 rows and a
+// second buffer of queries where they fit: 62.7 -> 59.7 us at 56 x 1.
 template <int D, int N>
 struct Lay {
     static constexpr int KS = D / 128;                // 128-d blocks
@@ -84,15 +114,14 @@ struct Lay {
     static constexpr int QB = N == 8 || (D == 256 && N == 32) ? 2 : 1;   // of queries
     static constexpr int NS = OCC == 2 ? 3 : N <= 16 ? 6 : 5;
     static constexpr int PR = (3 * N + 15) / 16 * 16; // rows of the weights' operand
-    // tiles a unit's boundary costs: O must be read out before the next unit's first
-    // product (measured)
-    static constexpr int kCharge = 5;
+    static constexpr int kCharge = 5;                 // tiles a unit's boundary costs
     static constexpr int kQBlock = 2 * N * 128;       // 128 d of the query pieces
     static constexpr int kQBytes = KS * kQBlock;
     static constexpr int kPBytes = PR * 128;          // a tile's weights
     // Weights of 32 rows lie as three pieces [128 keys][32 rows], of 8 rows as one
     // block [128 keys][w1 w2 w3 -], so a thread stores 16 bytes of its key at a time;
-    // of 16 rows as [3N rows][128 keys].
+    // of 16 rows as [3N rows][128 keys], byte by byte (as 32 rows first were: 8 x 15
+    // 96.6 us against 90.1), for want of 2 KB of shared memory.
     static constexpr bool kWide = N != 16;
     static constexpr int kOffQ = NS * kStage;
     static constexpr int kOffP = kOffQ + QB * kQBytes;
@@ -743,7 +772,8 @@ __global__ void __launch_bounds__(Lay<D, N>::kThreads, Lay<D, N>::OCC)
                     }
                     if (x > sg.x0) issue(&map_v, prev_row, sg.c);
                     // The next segment is looked up early, with the ring full: its code and
-                    // data come late from a memory system that is kept busy.
+                    // data come late from a memory system that is kept busy (at the last
+                    // tile, the ring ran empty for 3 to 6 us: 64 x 4 184.5 us against 182.3).
                     if (x == sg.x0 + 1) have_next = it.next(p, nx);
                 }
                 have = have_next;
@@ -1306,6 +1336,9 @@ __global__ void __launch_bounds__(Lay<D, N>::kThreads, Lay<D, N>::OCC)
 // the row).  A CTA takes `rows` rows of one unit and row group; a row has D / 4
 // threads of 16 bytes each, `teams` times over: the teams take the pieces in
 // turn, so that a unit cut into many pieces has many loads in flight, F a thread.
+// F = 8 and teams for more than 8 pieces a unit (one request of 6005 keys, 47 pieces:
+// 4.4 us); F = 3 of 32 bytes else, with two CTAs an SM (64 x 4, at most a few pieces:
+// 5 us, about 60 MB read and written).
 constexpr int kMergeThreads = 512, kMergeRows = 8;
 
 template <int D, int N, int F>
