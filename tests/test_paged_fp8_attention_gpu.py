@@ -664,3 +664,52 @@ def test_bf16_pages_after_the_rotary_append():
             t = 2.0 ** -8 * y.abs() + 2.0 ** -22 * ref.pair_magnitude(x, cs.cpu(), False)
             assert ((turned[j] - y).abs() <= t).all()
     assert carat.carat_get_device_status(clear=True) == 0
+
+
+@pytest.mark.parametrize("window", [0, 150])
+def test_ragged_layer_steps_over_stale_memory(window):
+    """step() with counts per request, over pages and scales that hold NaNs
+    wherever nothing was appended: rows within a count match the definition,
+    rows behind it stay as they were."""
+    B, k, hq, hkv, d, R = 4, 4, 16, 2, 512, 16
+    pool = engine.SharedPool(num_pages=16, page_bytes=128 * hkv * d, pages_per_ring=4,
+                             fill=float("nan"))
+    table = torch.tensor([pool.alloc.alloc_pages(3) for _ in range(B)], dtype=torch.int32)
+    cs = engine.rotary_table(384, d)
+    layer = engine.Fp8PagedLayer(pool, table.cuda(), cs, q_heads=hq, kv_heads=hkv, head_dim=d,
+                                 max_proposals=k, block_rows=R, window=window)
+    layer.k_scales.fill_(float("nan"))
+    layer.v_scales.fill_(float("nan"))
+    g = torch.Generator().manual_seed(41)
+
+    def rows(n, h):
+        return torch.randn((B, n, h, d), generator=g).bfloat16().cuda()
+
+    have = [207, 127, 1, 32]
+    layer.append(rows(207, hkv), rows(207, hkv), i32([0] * B), new_counts=i32(have))
+    for counts in ([4, 2, 1, 0], [1, 0, 4, 3]):
+        q = rows(k, hq)
+        out = torch.full(q.shape, 3.0, dtype=torch.bfloat16, device="cuda")
+        layer.step(q, rows(k, hkv), rows(k, hkv), i32(have), out=out, new_counts=i32(counts))
+        torch.cuda.synchronize()
+        out = out.cpu().double()
+        for b, m in enumerate(counts):
+            assert (out[b, m:] == 3.0).all()
+            if not m:
+                continue
+            n, pages = have[b] + m, table[b].long()
+            keys, values = (
+                (ref.decode(p.cpu())[pages]
+                 * s.cpu().double()[pages].repeat_interleave(R, 1)[..., None]).flatten(0, 1)[:n]
+                for p, s in ((layer.key_pages, layer.k_scales), (layer.value_pages, layer.v_scales)))
+            pos = [have[b] + j for j in range(m)]
+            turned = torch.stack([ref.rotate(q[b, j].cpu().double(), cs.cpu(), pos[j], False)
+                                  for j in range(m)])
+            want, weight = ref.attention(turned, keys, values, pos, window, layer.scale)
+            # the rotated queries are rounded to bf16, as in the test above
+            a = ref.score_magnitude(turned, keys, layer.scale)
+            tol = ref.attention_tolerance(want, weight, turned, keys, layer.scale) \
+                + 2 * math.expm1(2.0 ** -8 * a) * weight
+            assert ((out[b, :m] - want).abs() <= tol).all(), (counts, b)
+        have = [n + m for n, m in zip(have, counts)]
+    assert carat.carat_get_device_status(clear=True) == 0
