@@ -989,10 +989,12 @@ __global__ void __launch_bounds__(Lay<D, N>::kThreads, Lay<D, N>::OCC)
                 if (sg.x0 == 0) plan.first[u] = make_int2(rix, whole ? -1 : sg.opens ? 0 : 1);
                 if (sg.x1 == sg.ntiles) plan.last[u] = rix;
             }
+            // (copies: what its address is taken of is read from memory again and again)
+            const int x0 = sg.x0, x1 = sg.x1, ctx = sg.ctx, nq = sg.n, from = sg.first * kKeys;
             // first key of query 0, and the keys' end
-            const int lowest = p.window > 0 && sg.ctx >= p.window ? sg.ctx - p.window + 1 : 0;
-            const int keys = sg.ctx + sg.n;
-            const int rows_here = min(N, p.group * sg.n - row0);
+            const int lowest = p.window > 0 && ctx >= p.window ? ctx - p.window + 1 : 0;
+            const int keys = ctx + nq;
+            const int rows_here = min(N, p.group * nq - row0);
             // nm: kBoost - running maximum of each row (0 while it has none)
             float nm[NC], l[NC];
 #pragma unroll
@@ -1001,9 +1003,9 @@ __global__ void __launch_bounds__(Lay<D, N>::kThreads, Lay<D, N>::OCC)
             // Rows of this half that see the key at a position: query j does when
             // ctx + j >= pos > ctx + j - window.
             auto seen_rows = [&](int pos) -> uint32_t {
-                const int dj = pos - sg.ctx;
+                const int dj = pos - ctx;
                 const int jlo = max(dj, 0);
-                const int jhi = p.window > 0 && dj < sg.n - p.window ? dj + p.window : sg.n;
+                const int jhi = p.window > 0 && dj < nq - p.window ? dj + p.window : nq;
                 const int lo = min(max(jlo * p.group - row0 - r0, 0), NC);
                 const int hi = min(max(min(jhi * p.group - row0, rows_here) - r0, 0), NC);
                 return low_mask(hi) & ~low_mask(lo);
@@ -1011,13 +1013,13 @@ __global__ void __launch_bounds__(Lay<D, N>::kThreads, Lay<D, N>::OCC)
             const float *qs = red + L::kRedQ + (si & 1) * 2 * N + r0;
             const int *out_row = reinterpret_cast<const int *>(qs) + N;
             alive = __all_sync(kFull, await(&q_full[si & 1], (si >> 1) & 1, abort_flag, status));
-            for (int x = sg.x0; x < sg.x1; ++x, ++g) {
-                const bool first = x == sg.x0;
+            for (int x = x0; x < x1; ++x, ++g) {
+                const bool first = x == x0;
                 const int slot = g % kSlots;
                 const bool ok = __all_sync(
-                    kFull, alive && await(&s_full[g & 1], (g >> 1) & 1, abort_flag, status) &&
-                               await(&sc_full[slot], (g / kSlots) & 1, abort_flag, status));
-                const int t0 = (sg.first + x) * kKeys, pos = t0 + t;
+                    kFull, alive && await(&sc_full[slot], (g / kSlots) & 1, abort_flag, status) &&
+                               await(&s_full[g & 1], (g >> 1) & 1, abort_flag, status));
+                const int t0 = from + x * kKeys, pos = t0 + t;
                 const bool data = pos >= lowest && pos < keys;
                 float ks = 0.f, vs = 1.f;
                 if (ok) {
@@ -1030,7 +1032,7 @@ __global__ void __launch_bounds__(Lay<D, N>::kThreads, Lay<D, N>::OCC)
                 if (ok && lane == 0) tc::mbar_arrive(&sc_empty[slot]);
                 // d = score - maximum + kBoost: 2^d is the key's part of the sum, and
                 // 2^d vs, at most 2^(kSlack + kBoost), its weight
-                float lv = log2f(vs);
+                float lv = __log2f(vs);   // (a bound: any value near will do)
                 float d[NC];
                 if (ok) {
                     uint32_t h[NC], w[NC];
@@ -1052,7 +1054,7 @@ __global__ void __launch_bounds__(Lay<D, N>::kThreads, Lay<D, N>::OCC)
                     for (int e = 0; e < NC; ++e) d[e] = -INFINITY;
                 }
                 // A tile that not every row sees whole: mask by position.
-                const bool edge = t0 + kKeys - 1 > sg.ctx ||
+                const bool edge = t0 + kKeys - 1 > ctx ||
                                   (p.window > 0 && t0 <= keys - 1 - p.window);
                 if (edge) {
                     const uint32_t seen = data ? seen_rows(pos) : 0u;
@@ -1184,13 +1186,13 @@ __global__ void __launch_bounds__(Lay<D, N>::kThreads, Lay<D, N>::OCC)
                     // values of a key that only some queries see are taken out of the
                     // tile and put into those rows' weights instead.
                     bool nans = false;
-                    if (edge && sg.n > 1) {
+                    if (edge && nq > 1) {
                         alive = __all_sync(kFull, await(&nan_full[si & 1], (si >> 1) & 1, abort_flag,
                                                         status));
                         nans = alive && sh->nans[si & 1];
                     }
                     if (t0 < lowest || t0 + kKeys > keys || nans) {
-                        const uint32_t base = TS * (2 * g + (x + 1 < sg.x1 ? 2 : 1));
+                        const uint32_t base = TS * (2 * g + (x + 1 < x1 ? 2 : 1));
                         // A wait for a phase by its parity means that phase only if the one
                         // before it is over: the stage may have been the last tile's V's.
                         if (g > 0 && !await(&o_done[(g - 1) & 1], ((g - 1) >> 1) & 1, abort_flag,
@@ -1211,7 +1213,7 @@ __global__ void __launch_bounds__(Lay<D, N>::kThreads, Lay<D, N>::OCC)
                             }
                         }
                         if (nans && alive && data &&
-                            (pos > sg.ctx || (p.window > 0 && pos < keys - p.window)) &&
+                            (pos > ctx || (p.window > 0 && pos < keys - p.window)) &&
                             remove_nans<D, NS>(p, smem, base, t, sg.b, sg.c, pos)) {
                             const uint32_t seen = seen_rows(pos);
 #pragma unroll 1
@@ -1226,7 +1228,7 @@ __global__ void __launch_bounds__(Lay<D, N>::kThreads, Lay<D, N>::OCC)
                 tc::tc_fence_before();
                 __syncwarp();
                 if (lane == 0) tc::mbar_arrive(&p_full[g & 1]);
-                if (first && x + 1 < sg.x1) have_next = it.next(p, nx);
+                if (first && x + 1 < x1) have_next = it.next(p, nx);
             }
             // ------------------------------------------------ segment end
             // (a wait of one warp may have run out: all leave together)
