@@ -64,9 +64,9 @@
 // 185 us, 5640 GB/s, bound by the loads but for the start, the units' boundaries and
 // the merge.  56 x 1, 16/8 heads of 256, window 1024 (236 MB): 59 us, of which about
 // 20 do not grow with the batch (start, first loads, drain, merge; 224 x 1: 171 us,
-// 5530 GB/s).  8 x 15 (173 MB, 120 rows in four groups): 90 us, bound by
+// 5530 GB/s).  8 x 15 (173 MB, 120 rows in four groups): 88 us, bound by
 // its products: 32 a tile at 75 cycles each (60 at their best; their operands share
-// shared memory's bandwidth with the loads) are 2400 of the 2900 cycles a tile takes.
+// shared memory's bandwidth with the loads) are 2400 of about 2850 cycles a tile.
 // The same rows at head_dim 256 have half the products and wait for the softmax,
 // 2400 cycles a tile.  One request of 1500 or 6005 keys: 17 and 22 us,
 // a chain of latencies (split 2, first load to last output 11 to 15, merge 4 to 6).
