@@ -713,3 +713,23 @@ def test_ragged_layer_steps_over_stale_memory(window):
             assert ((out[b, :m] - want).abs() <= tol).all(), (counts, b)
         have = [n + m for n, m in zip(have, counts)]
     assert carat.carat_get_device_status(clear=True) == 0
+
+
+def test_different_calls_at_once():
+    """Three shapes of tile on three streams at the same time, each with its own
+    workspace: the same bits as one after the other."""
+    cases = [Case([3000, 700, 90, 1500], 1, 16, 8, 256, seed=50, window=1024),
+             Case([2500, 300], 4, 16, 2, 512, seed=51),
+             Case([1800, 640], 15, 16, 2, 512, seed=52)]
+    first = [c.run().clone() for c in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    outs = [[torch.zeros_like(f) for _ in range(30)] for f in first]
+    torch.cuda.synchronize()
+    for i in range(30):
+        for c, s, o in zip(cases, streams, outs):
+            c.call(stream=s, out=o[i])
+    torch.cuda.synchronize()
+    assert carat.carat_get_device_status(clear=True) == 0
+    for f, o in zip(first, outs):
+        for x in o:
+            assert torch.equal(x.view(torch.int16), f.view(torch.int16))
