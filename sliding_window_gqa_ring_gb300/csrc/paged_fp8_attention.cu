@@ -34,6 +34,14 @@
 // in fp32, before vs[t] and the rounding: keys with a tiny scale (a block of zero
 // values) keep their share of it although their weights vanish.
 //
+// Range of that sum.  Scales lie in [2^-100, 2^100], so with kBoost and kSlack a
+// term is at most 2^114, and the key that gave m adds at least 2^-94: terms below
+// 2^-126, flushed to zero, are less than 2^-32 of it.  When m moves, by up to 200 and
+// more at equal scores, 2^(old - new) itself may be below 2^-126 where its product
+// with the sum is not: it is applied as two factors 2^((old - new) / 2), one after
+// the other, here and in the merge.  (O may lose what lies below 2^-126 of its new
+// weights.)
+//
 // NaN.  Keys that a row does not see get weight 0, and 0 x NaN is NaN in a product.
 // So V rows outside the request's keys are zeroed in shared memory, and keys that
 // some of a step's queries see and others do not are looked through for NaNs by
@@ -128,7 +136,7 @@ struct Lay {
     static constexpr int kOffP = kOffQ + QB * kQBytes;
     static constexpr int kOffRed = kOffP + PB * kPBytes;
     // floats: the four key quarters' maxima or sums per row, the running
-    // maxima, the rescale factors, and of two segments the score factors and
+    // maxima, the rescale factors' roots, and of two segments the score factors and
     // output rows (int) of the queries
     static constexpr int kRedM = 4 * N, kRedAlpha = 5 * N, kRedQ = 6 * N;
     static constexpr int kRedFloats = 10 * N;
@@ -1091,7 +1099,7 @@ __global__ void __launch_bounds__(Lay<D, N>::kThreads, Lay<D, N>::OCC)
                                                  fmaxf(red_max[2 * N + r], red_max[3 * N + r]));
                         const float old = first ? kUnset : s_m[r];
                         const float now = best > old + kSlack ? best : old;
-                        s_alpha[r] = old == kUnset ? 1.f : fast_exp2(old - now);
+                        s_alpha[r] = old == kUnset ? 1.f : fast_exp2(0.5f * (old - now));
                         s_m[r] = now;
                         moved = now != old && old != kUnset;
                     }
@@ -1119,7 +1127,7 @@ __global__ void __launch_bounds__(Lay<D, N>::kThreads, Lay<D, N>::OCC)
                 if (alive) {
                     if (rescale) {
 #pragma unroll
-                        for (int e = 0; e < NC; ++e) l[e] *= s_alpha[r0 + e];
+                        for (int e = 0; e < NC; ++e) l[e] = l[e] * s_alpha[r0 + e] * s_alpha[r0 + e];
 #pragma unroll 1
                         for (int z = 0; z < 3 * KS; ++z) {
                             uint32_t o[NC];
@@ -1129,7 +1137,8 @@ __global__ void __launch_bounds__(Lay<D, N>::kThreads, Lay<D, N>::OCC)
                             tc::tmem_ld_wait();
 #pragma unroll
                             for (int e = 0; e < NC; ++e)
-                                o[e] = __float_as_uint(__uint_as_float(o[e]) * s_alpha[r0 + e]);
+                                o[e] = __float_as_uint(__uint_as_float(o[e]) *
+                                                       (s_alpha[r0 + e] * s_alpha[r0 + e]));
                             tmem_store<NC>(at, o);
                         }
                         tc::tmem_st_wait();
@@ -1336,7 +1345,8 @@ __global__ void __launch_bounds__(Lay<D, N>::kThreads, Lay<D, N>::OCC)
 
 // Merge of the split units: out = sum_q 2^(m_q - M) O_q / sum_q 2^(m_q - M) l_q
 // over the pieces q, M their largest maximum (a piece whose l is 0 saw no key of
-// the row).  A CTA takes `rows` rows of one unit and row group; a row has D / 4
+// the row).  2^(m_q - M) may underflow where its product with l_q is the larger part
+// of the sum (see the sum's range above): it is two factors, applied in turn.  A CTA takes `rows` rows of one unit and row group; a row has D / 4
 // threads of 16 bytes each, `teams` times over: the teams take the pieces in
 // turn, so that a unit cut into many pieces has many loads in flight, F a thread.
 // F = 8 and teams for more than 8 pieces a unit (one request of 6005 keys, 47 pieces:
@@ -1402,15 +1412,15 @@ __global__ void __launch_bounds__(kMergeThreads, F > 4 ? 1 : 2) paged_fp8_merge_
             for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, o));
 #pragma unroll
             for (int i = 0; i < G; ++i) {
-                ml[i].x = ml[i].y != 0.f ? fast_exp2(ml[i].x - M) : 0.f;
-                sum = fmaf(ml[i].x, ml[i].y, sum);
+                ml[i].x = ml[i].y != 0.f ? fast_exp2(0.5f * (ml[i].x - M)) : 0.f;
+                sum = fmaf(ml[i].x, ml[i].x * ml[i].y, sum);
             }
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
             const float inv = 1.f / sum;
 #pragma unroll
             for (int i = 0; i < G; ++i)
-                if (lane + 32 * i < np) s_w[mine][lane + 32 * i] = ml[i].x * inv;
+                if (lane + 32 * i < np) s_w[mine][lane + 32 * i] = ml[i].x * inv * ml[i].x;
         } else {                 // a few
             for (int q = lane; q < np; q += 32) {
                 const float2 ml = plan.part_ml[piece(q)];
@@ -1420,14 +1430,14 @@ __global__ void __launch_bounds__(kMergeThreads, F > 4 ? 1 : 2) paged_fp8_merge_
             for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, o));
             for (int q = lane; q < np; q += 32) {
                 const float2 ml = plan.part_ml[piece(q)];
-                const float w = ml.y != 0.f ? fast_exp2(ml.x - M) : 0.f;
+                const float w = ml.y != 0.f ? fast_exp2(0.5f * (ml.x - M)) : 0.f;
                 s_w[mine][q] = w;
-                sum = fmaf(w, ml.y, sum);
+                sum = fmaf(w, w * ml.y, sum);
             }
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
             const float inv = 1.f / sum;
-            for (int q = lane; q < np; q += 32) s_w[mine][q] *= inv;
+            for (int q = lane; q < np; q += 32) s_w[mine][q] *= inv * s_w[mine][q];
         }
     }
     __syncthreads();

@@ -1,0 +1,92 @@
+"""Attention over e4m3 pages at the ends of the value scales' range, 2^-100 to
+2^100: the softmax's denominator does not depend on the value scales, however
+far they lie apart and whatever order they come in (GPU, against 64 bits;
+tolerances: paged_reference.attention_tolerance)."""
+import pytest
+import torch
+
+import paged_reference as ref
+from sliding_window_gqa_ring_gb300 import carat
+from test_paged_fp8_attention_gpu import Case
+
+pytestmark = pytest.mark.gpu
+
+TINY = 2.0 ** -100
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _cuda():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    carat.library()
+    carat.carat_get_device_status(clear=True)
+    yield
+    assert carat.carat_get_device_status(clear=True) == 0
+
+
+def set_value_scales(c, b, scale_of_tile):
+    """Gives the 128-key tiles of request b the value scales scale_of_tile(i), on
+    the same bytes, or all-zero bytes under the least scale where it says None."""
+    rows = c.kp.shape[1]
+    per = rows // c.vs.shape[1]
+    for i in range(-(-c.n[b] // 128)):
+        scale = scale_of_tile(i)
+        page, r0 = int(c.table[b, 128 * i // rows]), 128 * i % rows
+        if scale is None:
+            c.vp[page, r0:r0 + 128][:max(0, c.n[b] - 128 * i)] = 0
+        c.vs[page, r0 // per:(r0 + 128) // per] = TINY if scale is None else scale
+        held = slice(128 * i, min(128 * i + 128, c.n[b]))
+        bytes_ = c.vp[page, r0:r0 + held.stop - held.start]
+        c.values[b][held] = ref.decode(bytes_) * (TINY if scale is None else scale)
+        c.value_scales[b][held] = TINY if scale is None else scale
+
+
+def repeat(c, batch, seed):
+    """The case's one request `batch` times over, on the same pages, with queries
+    of their own: enough units that a CTA walks whole ones."""
+    c.n, c.B, c.table = c.n * batch, batch, c.table.repeat(batch, 1)
+    c.keys, c.values, c.value_scales = c.keys * batch, c.values * batch, c.value_scales * batch
+    c.q = torch.randn((batch, *c.q.shape[1:]), generator=torch.Generator().manual_seed(seed)
+                      ).bfloat16()
+
+
+ORDERS = {
+    "zeros first": lambda n, big: lambda i: None if i < n // 2 else big,
+    "zeros last": lambda n, big: lambda i: big if i < n // 2 else None,
+    "in turn": lambda n, big: lambda i: None if i % 2 == 0 else big,
+    "rising": lambda n, big: lambda i: (None, 2.0 ** -40, 1.0, big)[min(3, 4 * i // n)],
+}
+SHAPES = {
+    "8 rows": dict(k=1, q_heads=8, kv_heads=1, head_dim=256),
+    "16 rows": dict(k=4, q_heads=4, kv_heads=1, head_dim=256),
+    "32 rows": dict(k=4, q_heads=16, kv_heads=2, head_dim=512, block_rows=64),
+    "40 rows": dict(k=5, q_heads=8, kv_heads=1, head_dim=512),
+}
+
+
+@pytest.mark.parametrize("order", sorted(ORDERS))
+@pytest.mark.parametrize("exponent", [0, 27, 30, 100])
+@pytest.mark.parametrize("shape", sorted(SHAPES))
+def test_whole_tiles_of_zero_values_keep_their_share_over_pieces(shape, exponent, order):
+    """Few requests: a tile or two of a unit to a CTA, joined by the merge."""
+    c = Case([1500, 700], seed=61, **SHAPES[shape])
+    for b, n in enumerate(c.n):
+        set_value_scales(c, b, ORDERS[order](-(-n // 128), 2.0 ** exponent))
+    c.upload()
+    c.run()
+
+
+@pytest.mark.parametrize("order", sorted(ORDERS))
+@pytest.mark.parametrize("exponent", [0, 30, 100])
+@pytest.mark.parametrize("shape", sorted(SHAPES))
+def test_whole_tiles_of_zero_values_keep_their_share_within_a_cta(shape, exponent, order):
+    """Many requests on the same pages: the running sum is rescaled from tile to
+    tile."""
+    c = Case([1000], seed=62, **SHAPES[shape])
+    set_value_scales(c, 0, ORDERS[order](8, 2.0 ** exponent))
+    repeat(c, 330, seed=63)
+    c.upload()
+    out = c.call()
+    torch.cuda.synchronize()
+    assert carat.carat_get_device_status(clear=True) == 0
+    c.check(out, range(0, 330, 11))
