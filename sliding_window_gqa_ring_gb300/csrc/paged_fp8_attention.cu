@@ -40,7 +40,9 @@
 // more at equal scores, 2^(old - new) itself may be below 2^-126 where its product
 // with the sum is not: it is applied as two factors 2^((old - new) / 2), one after
 // the other, here and in the merge.  (O may lose what lies below 2^-126 of its new
-// weights.)
+// weights.)  A thread's part of a sum (its key of every
+// tile of a segment) stays below 2^127 up to 2^20 keys a segment; it is scaled by
+// kSum = 2^-10 before the 128 threads' parts meet, and O with it.
 //
 // NaN.  Keys that a row does not see get weight 0, and 0 x NaN is NaN in a product.
 // So V rows outside the request's keys are zeroed in shared memory, and keys that
@@ -102,6 +104,7 @@ constexpr float kSlack = 8.f;
 // Weights carry the factor 2^kBoost = kWeight: 2^(kSlack + kBoost) = 2^14 fits
 // e5m2 and f16, and weights are resolved down to 2^-28 of the largest.
 constexpr float kBoost = 6.f, kWeight = 64.f;
+constexpr float kSum = 1.f / 1024;         // of a row's sum and O at a segment's end
 constexpr float kUnset = -1e30f;           // maximum of a row that has seen no key yet
 
 // Two shapes of CTA.  With up to 16 rows at head_dim 256 two CTAs share an SM, so
@@ -1248,7 +1251,7 @@ __global__ void __launch_bounds__(Lay<D, N>::kThreads, Lay<D, N>::OCC)
             // While the last PV product runs: the rows' sums over the 128 keys.
             float y[NC];
 #pragma unroll
-            for (int e = 0; e < NC; ++e) y[e] = l[e];
+            for (int e = 0; e < NC; ++e) y[e] = l[e] * kSum;
             const int rr = transpose_reduce<NC, false>(y, lane);
             red_max[q4 * N + r0 + rr] = y[0];
             half_any<L::H>(half, false);
@@ -1257,7 +1260,7 @@ __global__ void __launch_bounds__(Lay<D, N>::kThreads, Lay<D, N>::OCC)
                 const int r = r0 + t;
                 float sum =
                     (red_max[r] + red_max[N + r]) + (red_max[2 * N + r] + red_max[3 * N + r]);
-                // (values of next to nothing, in many keys: the output is 0, not inf x 0)
+                // (more than 2^20 keys of next to nothing: the output is 0, not inf x 0)
                 if (sum > 3e38f) sum = 3e38f;
                 if (!whole) plan.part_ml[slot_row + t] = make_float2(s_m[r], sum * (1.f / kWeight));
                 s_alpha[r] = 1.f / sum;
@@ -1269,8 +1272,8 @@ __global__ void __launch_bounds__(Lay<D, N>::kThreads, Lay<D, N>::OCC)
                 alive = false;
                 break;
             }
-            // O of 8 rows and 128 d at a time: the pieces' sum, then the output row or
-            // the partial.  Rolled: this code runs once a segment, from an instruction
+            // O of 8 rows and 128 d at a time: the pieces' sum (times kSum), then the output
+            // row or the partial.  Rolled: this code runs once a segment, from an instruction
             // cache that holds the tile loop, and its fetches are its cost.
             const int parts = KS * ((min(rows_here - r0, NC) + 7) / 8);
             auto pieces = [&](int i, float (&o)[8]) {
@@ -1283,7 +1286,7 @@ __global__ void __launch_bounds__(Lay<D, N>::kThreads, Lay<D, N>::OCC)
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
                     o[e] = fmaf(fmaf(__uint_as_float(o3[e]), 0.125f, __uint_as_float(o2[e])), 0.125f,
-                                __uint_as_float(o1[e]));
+                                __uint_as_float(o1[e])) * kSum;
             };
             if (whole) {
                 // lanes 2i and 2i + 1 hold d and d + 1 of every row: one keeps the even

@@ -2,6 +2,8 @@
 2^100: the softmax's denominator does not depend on the value scales, however
 far they lie apart and whatever order they come in (GPU, against 64 bits;
 tolerances: paged_reference.attention_tolerance)."""
+import math
+
 import pytest
 import torch
 
@@ -90,3 +92,40 @@ def test_whole_tiles_of_zero_values_keep_their_share_within_a_cta(shape, exponen
     torch.cuda.synchronize()
     assert carat.carat_get_device_status(clear=True) == 0
     c.check(out, range(0, 330, 11))
+
+
+@pytest.mark.parametrize("q_heads,k", [(8, 1), (8, 2)])
+def test_a_long_sum_under_the_least_scale(q_heads, k):
+    """40000 keys of scale 2^-100 whose scores lie 7.75 octaves above the first
+    tile's: the sum of 2^(score - maximum) is 2^129.5 where the maximum is that of
+    the weighted scores and has not moved."""
+    n = 40000
+    c = Case([n], k, q_heads, 1, 256, seed=64, scale=7.75 * math.log(2.0), spread=0.5)
+    g = torch.Generator().manual_seed(65)
+    x = (torch.rand((n, 1, 256), generator=g) * 100 + 20).to(ref.E4M3).view(torch.uint8)
+    c.ks.fill_(1.0), c.vs.fill_(TINY)
+    for i in range(-(-n // 128)):
+        page, m = int(c.table[0, i]), min(128, n - 128 * i)
+        c.kp[page, :m] = 0
+        if i > 0:
+            c.kp[page, :m, 0, 0] = 0x38                                # 1.0
+        c.vp[page, :m] = x[128 * i:128 * i + m]
+    c.keys[0].zero_()
+    c.keys[0][128:, 0, 0] = 1.0
+    c.values[0] = ref.decode(x) * TINY
+    c.value_scales[0].fill_(TINY)
+    c.q.zero_()
+    c.q[..., 0] = 1.0
+    one = c.q
+    repeat(c, 304, seed=66)
+    c.q = one.repeat(304, 1, 1, 1)
+    c.upload()
+    out = c.call()
+    torch.cuda.synchronize()
+    assert carat.carat_get_device_status(clear=True) == 0
+    c.check(out, [0])
+    want = out[:1].view(torch.int16)
+    # (units that are cut add up in another order)
+    whole = (out.view(torch.int16) == want).flatten(1).all(1)
+    assert whole.sum() >= 152
+    assert ((out.float() / out[:1].float() - 1).abs() <= 2.0 ** -7).all()
