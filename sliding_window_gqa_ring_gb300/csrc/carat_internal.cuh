@@ -233,8 +233,9 @@ void count_launches(int n);
 
 // A launch that may begin while the one before it in the stream drains
 // (programmatic dependent launch).  The kernel waits for that one itself, with
-// griddepcontrol.wait, before it touches memory; after an ordinary kernel the
-// launch is an ordinary one.
+// griddepcontrol.wait, before it touches memory and before it lets the next launch
+// start; after an ordinary kernel the launch is an ordinary one.  The attention over
+// e4m3 pages alone reads ahead of its wait: it says there why it may.
 template <typename... Params, typename... Args>
 cudaError_t launch_dependent(void (*kernel)(Params...), dim3 grid, dim3 block, size_t smem,
                              cudaStream_t stream, Args &&...args) {
