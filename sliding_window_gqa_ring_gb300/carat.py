@@ -812,7 +812,7 @@ def carat_paged_verify_attention_fp8(out, queries, key_pages, value_pages, k_sca
         out.data_ptr(), queries.data_ptr(), key_pages.data_ptr(), value_pages.data_ptr(),
         k_scales.data_ptr(), v_scales.data_ptr(), num_pages, page_table.data_ptr(), max_pages,
         page_rows, block_rows, counts, context_lengths.data_ptr(), k, batch, q_heads, kv_heads,
-        head_dim, min(int(window), 0x7fffffff), float(scale), workspace.data_ptr(),
+        head_dim, max(-1, min(int(window), 0x7fffffff)), float(scale), workspace.data_ptr(),
         workspace.numel() * workspace.element_size(), _stream_of(stream, device)), what)
 
 
