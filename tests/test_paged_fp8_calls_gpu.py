@@ -4,7 +4,7 @@ and refusals of numbers that do not fit an int (GPU, against 64 bits)."""
 import pytest
 import torch
 
-from sliding_window_gqa_ring_gb300 import carat
+from sliding_window_gqa_ring_gb300 import carat, engine
 from test_paged_fp8_attention_gpu import Case
 
 pytestmark = pytest.mark.gpu
@@ -74,3 +74,77 @@ def test_windows_past_every_length_are_no_window(window):
     first = c.run()
     c.window = window
     assert torch.equal(c.call().view(torch.int16), first.view(torch.int16))
+
+
+@pytest.mark.parametrize("captured", [False, True])
+def test_a_step_whose_inputs_come_from_two_other_streams(captured):
+    """Lengths written on one stream, keys and values on another, both joined before
+    the step: its launches, which may start while the one before them drains, start
+    behind both."""
+    B, k, hq, hkv, d = 6, 4, 16, 2, 512
+    g = torch.Generator().manual_seed(75)
+    cs = engine.rotary_table(1024, d)
+    new = [[torch.randn((B, k, h, d), generator=g).bfloat16().cuda() for h in (hq, hkv, hkv)]
+           for _ in range(12)]
+    first = torch.randn((B, 300, hkv, d), generator=g).bfloat16().cuda()
+    start = torch.tensor([300 - 40 * b for b in range(B)], dtype=torch.int32, device="cuda")
+    heavy = torch.randn((4096, 4096), device="cuda")
+
+    def layer():
+        pool = engine.SharedPool(num_pages=24, page_bytes=128 * hkv * d * 2, pages_per_ring=4,
+                                 fill=0.0)
+        table = torch.tensor([pool.alloc.alloc_pages(3) for _ in range(B)], dtype=torch.int32)
+        made = engine.Fp8PagedLayer(pool, table.cuda(), cs, q_heads=hq, kv_heads=hkv, head_dim=d,
+                                    max_proposals=k)
+        made.append(first, first, torch.zeros_like(start), new_counts=start)
+        return made
+
+    plain = layer()
+    want = []
+    for i, (q, kn, vn) in enumerate(new):
+        want.append(plain.step(q, kn, vn, start + 3 * i))
+    torch.cuda.synchronize()
+
+    joined = layer()
+    q, kn, vn = (torch.zeros_like(x) for x in new[0])
+    ctx, step = torch.zeros_like(start), torch.zeros_like(start)
+    source = [torch.stack([n[j] for n in new]) for j in range(3)]
+    which = torch.zeros(1, dtype=torch.int64, device="cuda")
+    out = torch.empty_like(q)
+    sides = [torch.cuda.Stream(), torch.cuda.Stream()]
+
+    def run(stream):
+        forks = torch.cuda.Event()
+        forks.record(stream)
+        for s in sides:
+            s.wait_event(forks)
+        with torch.cuda.stream(sides[0]):
+            torch.mm(heavy, heavy)                  # late
+            ctx.copy_(start + 3 * step)
+        with torch.cuda.stream(sides[1]):
+            torch.mm(heavy, heavy)
+            for dst, src in zip((q, kn, vn), source):
+                dst.copy_(src.index_select(0, which)[0])
+        for s in sides:
+            e = torch.cuda.Event()
+            e.record(s)
+            stream.wait_event(e)
+        joined.step(q, kn, vn, ctx, out=out, stream=stream)
+
+    stream = torch.cuda.Stream()
+    run(stream)                                     # step 0 twice over: the same rows
+    torch.cuda.synchronize()
+    if captured:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=stream):
+            run(stream)
+    got = []
+    for i in range(len(new)):
+        which.fill_(i), step.fill_(i)
+        torch.cuda.synchronize()
+        graph.replay() if captured else run(stream)
+        torch.cuda.synchronize()
+        got.append(out.clone())
+    assert carat.carat_get_device_status(clear=True) == 0
+    for a, b in zip(got, want):
+        assert torch.equal(a.view(torch.int16), b.view(torch.int16))
