@@ -467,7 +467,8 @@ carat_status carat_swa_attention_fp8(float *out, const void *queries, const void
  * CARAT_DEV_BAD_POSITION is set; a row whose page id lies outside the pool is
  * not stored and CARAT_DEV_BAD_CACHE_ID is set.
  * Limits: head_dim and rotary_dim multiples of 16, rotary_dim <= head_dim;
- * token strides multiples of 8 elements; page_rows a multiple of 128.
+ * token strides multiples of 8 elements; page_rows a multiple of 128;
+ * proposal_count <= max_pages * page_rows, whatever new_counts says.
  * Supported head_dim: multiples of 16 up to 128, of 32 up to 256, of 64 up to 512
  * and of 128 up to 1024 (others: CARAT_ERR_UNSUPPORTED).
  *
@@ -522,6 +523,11 @@ carat_status carat_global_verify_attention_paged(
  * pages with block scales, as carat_paged_rope_append_fp8 writes them (any
  * scales from 2^-100 to 2^100 are taken, powers of two or not).  This step's rows
  * must already be stored.
+ *
+ * Accuracy: scores and the softmax's sum are fp32.  A key's weight times its value
+ * scale is rounded to f16, relative to a row's largest such product and no finer than
+ * 2^-28 of it: a block whose value scale lies far above its values (rows of rejected
+ * proposals may leave it so) takes that resolution from the row's other keys.
  *
  *   out              bf16 [batch][proposal_count][q_heads][head_dim], what the
  *                    output projection takes: the weights of the PV product are

@@ -12,15 +12,18 @@
 // operations with it, so the cache has to reach the tensor core as it lies in
 // memory: K and V tiles of 128 keys go from HBM through TMA into shared memory
 // and from there straight into tcgen05.mma (kind::f8f6f4), with no thread
-// touching them.  The other operands are split exactly into 8-bit pieces that
-// stand side by side as more columns of the same product:
+// touching them.  The other operands are split into 8-bit pieces that stand side by
+// side as more columns of the same product:
 //   * a query row, scaled by a power of two so its largest element lies in
 //     [128, 256), is hi + lo / 16, both e4m3: four bits each and a sign make
-//     up a bf16 value's eight, down to 2^-13 of the row's largest element
-//     (smaller elements are rounded to 2^-21 of it);
-//   * a weight w_t = 2^(s_t - m) vs[t], rounded to f16 (its 2^-11 is below the
-//     output's own bf16 rounding), is w1 + w2 / 8 + w3 / 64, all e5m2: three
-//     bits each and two signs make up f16's eleven.
+//     up a bf16 value's eight.  That is exact down to 2^-13 of the row's largest
+//     element; smaller ones are rounded to 2^-21 of it (a score that is off by
+//     2^-21 of its largest products is what an fp32 sum of them gives);
+//   * a weight w_t = 2^(s_t - m) vs[t] is first rounded to f16: its 2^-11 is below
+//     the output's own bf16 rounding, and a third more pieces would be the price of
+//     three bits more.  It then is w1 + w2 / 8 + w3 / 64, all e5m2, exactly: three
+//     bits each and two signs make up f16's eleven (down to 2^-28 of the row's
+//     largest weight, see kBoost).
 // Keys are the M dimension of both products:
 //     S^T [128 keys x 2N]  = K_tile [128 x D] . [q_hi | q_lo]^T      (K-major A)
 //     O^T [128 d x 3N]    += V_tile^T [d x 128 keys] . [w1 | w2 | w3]^T (MN-major A)
@@ -40,9 +43,9 @@
 // more at equal scores, 2^(old - new) itself may be below 2^-126 where its product
 // with the sum is not: it is applied as two factors 2^((old - new) / 2), one after
 // the other, here and in the merge.  (O may lose what lies below 2^-126 of its new
-// weights.)  A thread's part of a sum (its key of every
-// tile of a segment) stays below 2^127 up to 2^20 keys a segment; it is scaled by
-// kSum = 2^-10 before the 128 threads' parts meet, and O with it.
+// weights.)  A thread's part of a sum (its key of every tile of a segment) stays
+// below 2^127 up to 2^20 keys a segment; it is scaled by kSum = 2^-10 before the 128
+// threads' parts meet, and O with it.
 //
 // NaN.  Keys that a row does not see get weight 0, and 0 x NaN is NaN in a product.
 // So V rows outside the request's keys are zeroed in shared memory, and keys that
@@ -66,7 +69,8 @@
 // the split launch.  The other warps read lengths, counts, page table, scales and
 // pages at once: all of them were written by launches before the split, which has
 // waited for those before it lets this one start.  (Every warp waiting for the whole
-// split: one request of 1500 or 6005 keys 17.3 -> 18.1, 21.5 -> 23.3 us.)  That
+// split: one request of 1500 or 6005 keys 15.5 -> 16.2, 19.8 -> 21.6 us, 8 x 15
+// 86.6 -> 89.7, 64 x 4 180.1 -> 182.4.)  That
 // orders the writes before the reads in time; visibility is promised to a grid that
 // waits, so the reads go to L2, where a finished launch's writes are, and not to an
 // SM's own cache: __ldcg, and TMA, which has no other way.
@@ -80,15 +84,17 @@
 //
 // What it reaches (copy rate of the device: 6796 GB/s), all launches included:
 // 64 requests x 4 proposals, 16/2 heads of 512, up to 32768 keys each (1044 MB):
-// 185 us, 5640 GB/s, bound by the loads but for the start, the units' boundaries and
-// the merge.  56 x 1, 16/8 heads of 256, window 1024 (236 MB): 59 us, of which about
-// 20 do not grow with the batch (start, first loads, drain, merge; 224 x 1: 171 us,
-// 5530 GB/s).  8 x 15 (173 MB, 120 rows in four groups): 88 us, bound by
-// its products: 32 a tile at 75 cycles each (60 at their best; their operands share
+// 180 to 184 us, 5680 to 5800 GB/s, bound by the loads but for the start, the units'
+// boundaries and the merge.  56 x 1, 16/8 heads of 256, window 1024 (236 MB): 55 to 57
+// us, of which about 20 do not grow with the batch (start, first loads, drain, merge;
+// 224 x 1: 185 us).  8 x 15 (173 MB, 120 rows in four groups): 86 us, bound by its
+// products: 32 a tile at 75 cycles each (60 at their best; their operands share
 // shared memory's bandwidth with the loads) are 2400 of about 2850 cycles a tile.
 // The same rows at head_dim 256 have half the products and wait for the softmax,
-// 2400 cycles a tile.  One request of 1500 or 6005 keys: 17 and 22 us,
-// a chain of latencies (split 2, first load to last output 11 to 15, merge 4 to 6).
+// 2400 cycles a tile.  One request of 1500 or 6005 keys: 15.5 and 20 us, a chain of
+// latencies (split, first load to last output, merge).  One request of 32768 keys
+// among 9 or 19 of 400 (16/2 heads of 512, 4 proposals): 40 us, where the same keys
+// spread evenly take 29: the merge's shape goes by the average number of pieces.
 #include <algorithm>
 #include <atomic>
 
@@ -1129,8 +1135,9 @@ __global__ void __launch_bounds__(Lay<D, N>::kThreads, Lay<D, N>::OCC)
                         d[e] += nm[e];
                     }
                 }
-                // The PV product PB tiles back has read the weights' buffer; a
-                // rescale needs the last one in O as well.
+                // The PV product PB tiles back has read the weights' buffer (with two
+                // buffers it had when this tile's scores came, which were issued behind
+                // it); a rescale needs the last one in O as well.
                 if (L::PB == 2 && g > 1) {
                     alive = __all_sync(kFull, await(&o_done[g & 1], ((g - 2) >> 1) & 1, abort_flag,
                                                     status));
@@ -1568,8 +1575,9 @@ cudaError_t launch(const PagedFp8Params &p, const Sizes &z, cudaStream_t stream)
     e = launch_dependent(kernel, dim3(z.grid), dim3(L::kThreads), L::kAlloc, stream, p, plan, map_k,
                          map_v);
     if (e != cudaSuccess) return e;
-    // A unit is cut into about ranges / units + 1 pieces, and one long unit among
-    // short ones into as many as there are ranges.
+    // A unit is cut into about ranges / units + 1 pieces.  One long unit among short
+    // ones, cut into many more, is walked by the threads of a few: its lengths are on the
+    // device (what that costs: see the head of this file).
     const int held = std::min(N, p.group * p.k);
     const int pieces = plan.ranges / (p.batch * p.kv_heads) + 1;
     const bool many = pieces > 8;

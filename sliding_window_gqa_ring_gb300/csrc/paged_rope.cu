@@ -115,6 +115,8 @@ __device__ __forceinline__ uint4 narrow8(const float *x) {
 // 44.8 / 49.4); 4 at 3 CTAs 60.7 / 68.8 / 60.7; 2 at 4 71.0 / 69.9 / 64.4; one at
 // a time 81.4 / 95.4 / 71.2.  (With the e4m3 blocks' unturned values compared as bits:
 // 58.4 / 63.6 / 62.6.)  Few tokens: 2.7 us for one, 4.8 for 256.
+// The interleaved instances fit their 64 registers; the half-split e4m3 ones spill 9 of
+// them (36 bytes stored, 64 loaded), the half-split bf16 one of many tokens 1.
 constexpr int kFlight = 3, kMany = 4, kFew = 4;
 constexpr int kRows = 2;
 

@@ -38,6 +38,8 @@ PAGED = {
     # attention over e4m3 pages with block scales, 268 MB of them
     "paged_fp8": (64, 4, 16, 2, 512, 2048),
     "paged_fp8_120_rows": (8, 15, 16, 2, 512, 8192),
+    # its tiles of 8 rows, two CTAs an SM (235 MB of pages)
+    "paged_fp8_decode": (56, 1, 16, 8, 256, 1024),
     # rotary appends of eight ragged prompts (the keys are the prompt's)
     "paged_rope": (8, 1024, 16, 8, 256, 0),
     "paged_rope_fp8": (8, 1024, 16, 8, 256, 0),
