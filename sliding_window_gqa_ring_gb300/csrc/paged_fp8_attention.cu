@@ -120,7 +120,9 @@ constexpr float kSlack = 8.f;
 // e5m2 and f16, and weights are resolved down to 2^-28 of the largest.
 constexpr float kBoost = 6.f, kWeight = 64.f;
 constexpr float kSum = 1.f / 1024;         // of a row's sum and O at a segment's end
-constexpr float kUnset = -1e30f;           // maximum of a row that has seen no key yet
+// Maximum of a row that has seen no key yet: below every score, which key scales of
+// 2^100 take to -1e32 and further.
+constexpr float kUnset = -3e38f;
 
 // Two shapes of CTA.  With up to 16 rows at head_dim 256 two CTAs share an SM, so
 // that one streams while the other is at a unit's boundary or starting up (56

@@ -129,3 +129,39 @@ def test_a_long_sum_under_the_least_scale(q_heads, k):
     whole = (out.view(torch.int16) == want).flatten(1).all(1)
     assert whole.sum() >= 152
     assert ((out.float() / out[:1].float() - 1).abs() <= 2.0 ** -7).all()
+
+
+@pytest.mark.parametrize("kw", [dict(k=1, q_heads=8, kv_heads=1, head_dim=256),
+                                dict(k=4, q_heads=16, kv_heads=2, head_dim=512),
+                                dict(k=3, q_heads=4, kv_heads=1, head_dim=256, window=200)])
+@pytest.mark.parametrize("sign", [-1, 1])
+@pytest.mark.parametrize("distinct", [False, True])
+@pytest.mark.parametrize("batch", [1, 330])
+def test_scores_of_keys_under_the_largest_scale(kw, sign, distinct, batch):
+    """Key scales of 2^100: scores of +-3e31 in log2 units, all alike, or every
+    seventh key's half of that (then the smaller magnitude, or the larger value, takes
+    all)."""
+    c = Case([700], seed=67, scale=1.0 / 16.0, **kw)
+    c.ks.fill_(2.0 ** 100)
+    c.q.zero_()
+    c.q[..., 0] = 16.0
+    c.keys[0].zero_()
+    for t in range(700):
+        half = distinct and t % 7 == 3
+        page, row = int(c.table[0, t // 128]), t % 128
+        c.kp[page, row] = 0
+        c.kp[page, row, :, 0] = (0x80 if sign < 0 else 0) | (0x50 if half else 0x58)   # 8, 16
+        c.keys[0][t, :, 0] = sign * (8.0 if half else 16.0) * 2.0 ** 100
+    if batch > 1:
+        q = c.q
+        repeat(c, batch, seed=68)
+        c.q = q.repeat(batch, 1, 1, 1)
+    c.upload()
+    out = c.call()
+    torch.cuda.synchronize()
+    assert carat.carat_get_device_status(clear=True) == 0
+    for b in {0, batch - 1, batch // 2}:
+        want, weight = c.expected(b)
+        # (the scores are exact: powers of two and equal products)
+        tol = 2.0 ** -8 * want.abs() + 2.0 ** -10 * (1 + 2.0 ** -8) * weight
+        assert ((out[b].cpu().double() - want).abs() <= tol).all(), b
