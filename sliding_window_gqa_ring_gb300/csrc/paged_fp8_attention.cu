@@ -552,7 +552,11 @@ __device__ __forceinline__ float split_query(uint8_t *s_q, const uint16_t *row, 
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(kFull, top, o));
     int s = 7 - ((int)(top >> 23) - 127);
-    s = min(s, 100);            // zero and subnormal rows
+    // Zero and tiny rows.  Up to 2^120 the factor 2^-s and the score factor formed from
+    // it stay normal numbers, and a row of 2^-126 still has bf16's eight bits; what
+    // is lost below is less than 2^-15 of the softmax scale in any score, whatever the
+    // key scales.
+    s = min(s, 120);
     const float up = __int_as_float((127 + s) << 23);
     uint32_t hi[E / 4], lo[E / 4];
 #pragma unroll

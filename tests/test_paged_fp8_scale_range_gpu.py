@@ -165,3 +165,20 @@ def test_scores_of_keys_under_the_largest_scale(kw, sign, distinct, batch):
         # (the scores are exact: powers of two and equal products)
         tol = 2.0 ** -8 * want.abs() + 2.0 ** -10 * (1 + 2.0 ** -8) * weight
         assert ((out[b].cpu().double() - want).abs() <= tol).all(), b
+
+
+@pytest.mark.parametrize("exponent", [-93, -100, -110, -118])
+@pytest.mark.parametrize("kw", [dict(k=2, q_heads=8, kv_heads=1, head_dim=256),
+                                dict(k=4, q_heads=16, kv_heads=2, head_dim=512)])
+def test_small_queries_meet_large_key_scales(kw, exponent):
+    """Queries of 2^-118 to 2^-93 and key scales that make ordinary scores of them
+    keep the precision of ordinary queries."""
+    c = Case([500, 130], seed=69, scale=2.0 ** (-exponent - 100 - 10), **kw)
+    c.ks.fill_(2.0 ** 100)
+    for b, n in enumerate(c.n):
+        for i in range(-(-n // 128)):
+            m = min(128, n - 128 * i)
+            c.keys[b][128 * i:128 * i + m] = ref.decode(c.kp[int(c.table[b, i]), :m]) * 2.0 ** 100
+    c.q = (c.q.double() * 2.0 ** exponent).bfloat16()
+    c.upload()
+    c.run()
