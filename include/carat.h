@@ -376,6 +376,23 @@ int carat_pool_free_ring(carat_pool *pool, int ring_id);
 int carat_pool_alloc_pages(carat_pool *pool, int n, int32_t *out_pages);
 int carat_pool_free_pages(carat_pool *pool, int n, const int32_t *pages);
 int carat_pool_stats(carat_pool *pool, int32_t *out4);
+/* Shared pages.  alloc_pages gives a page one owner; carat_pool_share_pages adds
+ * one for every time a page is listed (requests that share a beginning, see
+ * carat_paged_fork), and carat_pool_free_pages takes one away: the page is free
+ * when the last is gone.  Returns 0, or -1 for an id that is not an allocated
+ * single page (then nothing changes).
+ *
+ * carat_pool_plan_compaction -- make room for rings: empties blocks that single
+ * pages broke up, fewest pages first, into free places past the last block and
+ * in other such blocks, a block wholly or not at all, at most max_moves pages in
+ * all.  Writes the moves (out_src[i] to out_dst[i]) and returns their number, or
+ * -1.  The allocator counts them as done: owners follow, the sources are free.
+ * The caller has carat_pages_move carry them out, for every page table that may
+ * name such a page, before anything that is allocated afterwards is written.  No
+ * source of a plan is a destination of the same plan. */
+int carat_pool_share_pages(carat_pool *pool, int n, const int32_t *pages);
+int carat_pool_plan_compaction(carat_pool *pool, int max_moves, int32_t *out_src,
+                               int32_t *out_dst);
 
 /*
  * FP8 (e4m3) sliding-window rings -- "gemma-cuda-hybrid", "Features" /
@@ -567,6 +584,106 @@ carat_status carat_paged_verify_attention_fp8(
     int head_dim, int window, float scale, void *workspace, size_t workspace_bytes, void *stream);
 size_t carat_paged_fp8_workspace_bytes(int batch, int proposal_count, int q_heads, int kv_heads,
                                        int head_dim, int capacity);
+
+/*
+ * carat_paged_chunk_attention -- attention of a chunk of new tokens (a prompt, a
+ * part of one, a decode or verify step) over bf16 pages that already hold this
+ * chunk's rows (e.g. after carat_paged_rope_append).
+ *
+ * Query j of request b, at position p = context_lengths[b] + j, sees key t when
+ * t <= p and (window == 0, or t > p - window, or t < sinks): every position up to
+ * its own, or the last `window` of them and the first `sinks` tokens of the request.
+ *
+ *   out              bf16 [batch][proposal_count][q_heads][head_dim]: scores, the
+ *                    softmax's maximum and sum and the accumulated output are fp32;
+ *                    a key's weight is rounded to bf16 for its product with the
+ *                    value, and it is the rounded weights that are summed.
+ *   queries          bf16, same shape, after the rotation.
+ *   proposal_count   new tokens of a request, any number up to the capacity.
+ *   new_counts       int32 [batch] or NULL (= proposal_count each): request b has
+ *                    queries j < new_counts[b] and no keys behind theirs; the rows
+ *                    of out behind them are left as they were.
+ *   window, sinks    as above; sinks has no meaning when window is 0.  Pages that
+ *                    hold no key that some query sees are never read: their table
+ *                    entries may be stale.
+ *   Pages, page table, context_lengths, device-side errors and bad page ids as in
+ *   carat_paged_verify_attention_fp8 (a rejected request's rows are NaN).  What lies
+ *   in rows at or past a request's key count (context_length + new_counts[b]) never
+ *   reaches the result, nor does what lies in a key the rows of a query that does not
+ *   see it, NaN and infinities included.  A NaN or infinity among the values of a key
+ *   makes the elements it belongs to non-finite for every query that sees it, or
+ *   the whole rows NaN where other queries of the request do not see it.
+ *   workspace        >= carat_paged_chunk_workspace_bytes(...) bytes; NULL when that
+ *                    is 0.  Needs no initialisation; calls that may overlap on the
+ *                    GPU need separate workspaces.
+ *
+ * Supported: head_dim 256 or 512; q_heads/kv_heads <= 64; batch * proposal_count *
+ * q_heads < 2^31; kv_heads * head_dim <= 2^24 (others: CARAT_ERR_UNSUPPORTED).
+ */
+carat_status carat_paged_chunk_attention(
+    void *out, const void *queries, const void *key_pages, const void *value_pages, int num_pages,
+    const int32_t *page_table, int max_pages, int page_rows, const int32_t *new_counts,
+    const int32_t *context_lengths, int proposal_count, int batch, int q_heads, int kv_heads,
+    int head_dim, int window, int sinks, float scale, void *workspace, size_t workspace_bytes,
+    void *stream);
+size_t carat_paged_chunk_workspace_bytes(int batch, int proposal_count, int q_heads, int kv_heads,
+                                         int head_dim);
+
+/*
+ * Operators on pages: copying, forking and moving pages of a shared pool on the
+ * device, keys, values, (e4m3 pages) scales and the page tables that name them.
+ *
+ *   key_pages, value_pages  num_pages pages of page_rows rows of row_bytes bytes
+ *                    (kv_heads * head_dim * 2 for bf16 pages; any multiple of 16).
+ *                    A page may also be taken as one row of its whole size.
+ *   k_scales, v_scales  fp32 [num_pages][page_rows / block_rows][kv_heads], or both
+ *                    NULL (then block_rows and kv_heads have no meaning).  Copied
+ *                    for every block of which a row is copied.
+ *   src, dst         int32 [count], device memory.  A source below 0 is skipped
+ *                    without an error, so a captured list can hold fewer jobs.
+ * Bytes are moved as they are, whatever they stand for.  An id outside the pool skips
+ * its job and sets CARAT_DEV_BAD_CACHE_ID; a row count outside [0, page_rows] or a
+ * context length outside [0, max_pages * page_rows] skips it and sets
+ * CARAT_DEV_BAD_CONTEXT.  A page that one call writes must not be written twice by
+ * it nor read by another of its jobs (the contents would be either's).
+ * Limits: page_rows * row_bytes <= 2^40.
+ *
+ * carat_pages_copy -- the first rows[i] rows (rows NULL: all) of page src[i] into
+ *   page dst[i]; the rows behind them stay as they were.
+ *
+ * carat_paged_fork -- requests that go on from another one's tokens (parallel
+ *   samples, beams, a shared beginning).  Child i takes over the c =
+ *   context_lengths[parents[i]] tokens of its parent: the first c / page_rows entries
+ *   of its line of child_table are the parent's (whole pages are shared: nobody
+ *   writes them any more), and the next one is new_pages[i], into which the c %
+ *   page_rows rows of the parent's last page are copied.  new_pages[i] < 0: the child
+ *   takes the parent's last page itself (one child of a parent may, when the parent
+ *   does not go on).  Entries behind it are left as they were, and there is none when
+ *   c = max_pages * page_rows.  child_lengths[i] = c (child_lengths may be NULL).
+ *   A parent below 0 skips its child.
+ *     page_table int32 [num_parents][max_pages], child_table int32
+ *     [children][max_pages]; they must not overlap, nor may context_lengths and
+ *     child_lengths (CARAT_ERR_INVALID_ARG).
+ *
+ * carat_pages_move -- whole pages src[i] to dst[i] (carat_pool_plan_compaction's
+ *   list), and every one of the table_entries entries at page_table that equals
+ *   src[i] becomes dst[i].  key_pages and value_pages both NULL: only scales and
+ *   table (further layers of a pool whose bytes have been moved already).
+ */
+carat_status carat_pages_copy(void *key_pages, void *value_pages, float *k_scales, float *v_scales,
+                              int num_pages, int page_rows, int64_t row_bytes, int block_rows,
+                              int kv_heads, const int32_t *src, const int32_t *dst,
+                              const int32_t *rows, int count, void *stream);
+carat_status carat_paged_fork(void *key_pages, void *value_pages, float *k_scales, float *v_scales,
+                              int num_pages, int page_rows, int64_t row_bytes, int block_rows,
+                              int kv_heads, const int32_t *page_table, int num_parents,
+                              int max_pages, const int32_t *context_lengths, int32_t *child_table,
+                              int32_t *child_lengths, const int32_t *parents,
+                              const int32_t *new_pages, int children, void *stream);
+carat_status carat_pages_move(void *key_pages, void *value_pages, float *k_scales, float *v_scales,
+                              int num_pages, int page_rows, int64_t row_bytes, int block_rows,
+                              int kv_heads, const int32_t *src, const int32_t *dst, int count,
+                              int32_t *page_table, int64_t table_entries, void *stream);
 
 /* Workspace bytes the attention calls need for these sizes (the same for the
  * plain and the fused-append entry points; 0 if the sizes are invalid, or if

@@ -50,6 +50,9 @@ EXPORTED = (
     "carat_paged_rope_append", "carat_paged_rope_append_fp8",
     "carat_global_verify_attention_paged", "carat_paged_verify_attention_fp8",
     "carat_paged_fp8_workspace_bytes",
+    "carat_paged_chunk_attention", "carat_paged_chunk_workspace_bytes",
+    "carat_pages_copy", "carat_paged_fork", "carat_pages_move",
+    "carat_pool_share_pages", "carat_pool_plan_compaction",
 )
 
 
@@ -146,6 +149,23 @@ def _declare(lib):
         sz, vp]
     lib.carat_paged_fp8_workspace_bytes.restype = sz
     lib.carat_paged_fp8_workspace_bytes.argtypes = [i32] * 6
+    lib.carat_paged_chunk_attention.restype = i32
+    lib.carat_paged_chunk_attention.argtypes = [
+        vp, vp, vp, vp, i32, vp, i32, i32, vp, vp, i32, i32, i32, i32, i32, i32, i32, f32, vp, sz, vp]
+    lib.carat_paged_chunk_workspace_bytes.restype = sz
+    lib.carat_paged_chunk_workspace_bytes.argtypes = [i32] * 5
+    pages = [vp, vp, vp, vp, i32, i32, i64, i32, i32]
+    lib.carat_pages_copy.restype = i32
+    lib.carat_pages_copy.argtypes = pages + [vp, vp, vp, i32, vp]
+    lib.carat_paged_fork.restype = i32
+    lib.carat_paged_fork.argtypes = pages + [vp, i32, i32, vp, vp, vp, vp, vp, i32, vp]
+    lib.carat_pages_move.restype = i32
+    lib.carat_pages_move.argtypes = pages + [vp, vp, i32, vp, i64, vp]
+    ids = ctypes.POINTER(ctypes.c_int32)
+    lib.carat_pool_share_pages.restype = i32
+    lib.carat_pool_share_pages.argtypes = [vp, i32, ids]
+    lib.carat_pool_plan_compaction.restype = i32
+    lib.carat_pool_plan_compaction.argtypes = [vp, i32, ids, ids]
     lib.carat_global_append_verify_attention.restype = i32
     lib.carat_global_append_verify_attention.argtypes = [vp, vp, vp, vp, i32, vp, vp, vp, vp, i32,
                                                          i32, i32, i32, i32, i32, f32, vp, sz, vp]
@@ -434,6 +454,22 @@ class Pool:
         pages = list(pages)
         buf = (ctypes.c_int32 * max(len(pages), 1))(*pages)
         return self._lib.carat_pool_free_pages(self._h, len(pages), buf) == 0
+
+    def share_pages(self, pages) -> bool:
+        """One more owner for every listed page; free_pages takes one away."""
+        pages = list(pages)
+        buf = (ctypes.c_int32 * max(len(pages), 1))(*pages)
+        return self._lib.carat_pool_share_pages(self._h, len(pages), buf) == 0
+
+    def plan_compaction(self, max_moves: int):
+        """(sources, destinations) of page moves that empty broken-up blocks.  The
+        allocator counts them as done; carat_pages_move carries them out."""
+        n = max(0, min(int(max_moves), self.num_pages))
+        src, dst = (ctypes.c_int32 * max(n, 1))(), (ctypes.c_int32 * max(n, 1))()
+        got = self._lib.carat_pool_plan_compaction(self._h, n, src, dst)
+        if got < 0:
+            raise CaratError(CARAT_ERR_INVALID_ARG, "carat_pool_plan_compaction")
+        return list(src[:got]), list(dst[:got])
 
     def stats(self) -> dict:
         out = (ctypes.c_int32 * 4)()
@@ -840,3 +876,196 @@ def _paged_fp8_explain(what, out, queries, key_pages, value_pages, k_scales, v_s
               context_lengths, workspace, new_counts):
         _ptr(t)
     raise ValueError(f"{what}: arguments do not fit together")
+
+
+# ---------------------------------------------------------------------------
+# Attention of a chunk of new tokens over bf16 pages
+# ---------------------------------------------------------------------------
+
+def paged_chunk_workspace_bytes(batch, proposal_count, q_heads, kv_heads, head_dim) -> int:
+    return int(library().carat_paged_chunk_workspace_bytes(batch, proposal_count, q_heads,
+                                                           kv_heads, head_dim))
+
+
+def _int32(x):
+    """An integer as a C int; one past its range keeps its sign."""
+    return max(-1, min(int(x), 0x7fffffff))
+
+
+def carat_paged_chunk_attention(out, queries, key_pages, value_pages, page_table, context_lengths,
+                                *, scale, workspace=None, window=0, sinks=0, new_counts=None,
+                                stream=None):
+    """Attention of a chunk of new tokens (a prompt, a part of one, a decode or verify
+    step) over bf16 pages [num_pages][page_rows][Hkv][D] that already hold their rows.
+
+    out and queries bf16 [B][k][Hq][D], any k up to the capacity; window 0: every
+    position up to the query's own, w > 0: the last w of them and the request's first
+    `sinks` tokens; new_counts int32 [B]: the queries request b really has (default k;
+    rows of out behind them stay as they are); workspace: a CUDA tensor of at least
+    paged_chunk_workspace_bytes(...) bytes (None where that is 0)."""
+    what = "carat_paged_chunk_attention"
+    counts = None
+    try:
+        shape, pool = queries.shape, key_pages.shape
+        batch, k, q_heads, head_dim = shape
+        num_pages, page_rows, kv_heads, cache_dim = pool
+        rows, max_pages = page_table.shape
+        device = queries.get_device()
+        usual = (cache_dim == head_dim and rows == batch and out.shape == shape and
+                 value_pages.shape == pool and context_lengths.shape == (batch,) and
+                 device == _device() and
+                 _plain(device, _BF16, out, queries, key_pages, value_pages) and
+                 _plain(device, _I32, page_table, context_lengths))
+        if workspace is not None:
+            usual = usual and workspace.get_device() == device and workspace.is_contiguous()
+        if new_counts is not None:
+            usual = usual and new_counts.shape == (batch,) and _plain(device, _I32, new_counts)
+            counts = new_counts.data_ptr()
+    except (AttributeError, TypeError, ValueError):
+        usual = False
+    if not usual:
+        _paged_chunk_explain(what, out, queries, key_pages, value_pages, page_table,
+                             context_lengths, workspace, new_counts)
+    space, room = ((None, 0) if workspace is None else
+                   (workspace.data_ptr(), workspace.numel() * workspace.element_size()))
+    _check((_lib or library()).carat_paged_chunk_attention(
+        out.data_ptr(), queries.data_ptr(), key_pages.data_ptr(), value_pages.data_ptr(),
+        num_pages, page_table.data_ptr(), max_pages, page_rows, counts,
+        context_lengths.data_ptr(), k, batch, q_heads, kv_heads, head_dim, _int32(window),
+        _int32(sinks), float(scale), space, room, _stream_of(stream, device)), what)
+
+
+def _paged_chunk_explain(what, out, queries, key_pages, value_pages, page_table, context_lengths,
+                         workspace, new_counts):
+    """Raises what is wrong with the arguments."""
+    _expect(out, torch.bfloat16, f"{what}: out")
+    _expect(queries, torch.bfloat16, f"{what}: queries")
+    if queries.dim() != 4 or out.shape != queries.shape:
+        raise ValueError(f"{what}: queries must be [batch][k][q_heads][head_dim], out alike")
+    pool = _paged_pool(key_pages, value_pages, page_table, context_lengths, torch.bfloat16,
+                       queries.shape[0], what)
+    if pool[3] != queries.shape[3]:
+        raise ValueError(f"{what}: cache head_dim {pool[3]} != query head_dim {queries.shape[3]}")
+    if new_counts is not None:
+        _expect(new_counts, torch.int32, f"{what}: new_counts")
+        if tuple(new_counts.shape) != (queries.shape[0],):
+            raise ValueError(f"{what}: new_counts must be [batch]")
+    _on_device(what, out=out, queries=queries, key_pages=key_pages, value_pages=value_pages,
+               page_table=page_table, context_lengths=context_lengths, workspace=workspace,
+               new_counts=new_counts)
+    for t in (out, queries, key_pages, value_pages, page_table, context_lengths, workspace,
+              new_counts):
+        _ptr(t)
+    raise ValueError(f"{what}: arguments do not fit together")
+
+
+# ---------------------------------------------------------------------------
+# Operators on the pages of a pool
+# ---------------------------------------------------------------------------
+
+def hidden_pages(context_length: int, window: int, sinks: int, page_rows: int):
+    """(first, end) of the entries of a request's page table whose pages no query at or
+    behind position context_length sees any more under a sliding window with `sinks`
+    first tokens: they can be freed (carat_pool_free_pages).  Empty without a window."""
+    if window <= 0:
+        return 0, 0
+    first = -(-int(sinks) // page_rows)
+    end = max(0, int(context_length) - int(window) + 1) // page_rows
+    return (first, end) if end > first else (first, first)
+
+
+def _page_args(what, key_pages, value_pages, k_scales, v_scales, lists, tables=None,
+               num_pages=None):
+    """The leading arguments of the operators on pages.  key_pages None (a move whose
+    bytes have been moved already): the scales' shape, or num_pages, gives the pool."""
+    if (k_scales is None) != (v_scales is None):
+        raise ValueError(f"{what}: k_scales and v_scales go together")
+    if (key_pages is None) != (value_pages is None):
+        raise ValueError(f"{what}: key_pages and value_pages go together")
+    first = next(iter(lists.values()))
+    device = first.get_device()
+    if key_pages is None:
+        page_rows, row_bytes, block_rows, kv_heads = 1, 16, 0, 1
+        if k_scales is not None:
+            _expect(k_scales, torch.float32, f"{what}: k_scales")
+            _expect(v_scales, torch.float32, f"{what}: v_scales")
+            if k_scales.dim() != 3 or k_scales.shape != v_scales.shape:
+                raise ValueError(f"{what}: scales must be 3-D and alike")
+            num_pages, page_rows, kv_heads = k_scales.shape
+            block_rows = 1
+        if num_pages is None:
+            raise ValueError(f"{what}: num_pages is needed without pages and scales")
+    else:
+        if key_pages.dtype not in (_BF16, _U8):
+            raise TypeError(f"{what}: pages must be bf16 or uint8 (e4m3), got {key_pages.dtype}")
+        _expect(value_pages, key_pages.dtype, f"{what}: value_pages")
+        if key_pages.dim() != 4 or key_pages.shape != value_pages.shape:
+            raise ValueError(f"{what}: key and value pages must be 4-D and alike")
+        num_pages, page_rows, kv_heads, head_dim = key_pages.shape
+        row_bytes = kv_heads * head_dim * key_pages.element_size()
+        block_rows = 0
+        if k_scales is not None:
+            block_rows = _block_scales(k_scales, v_scales, num_pages, page_rows, kv_heads, what)
+    for name, t in lists.items():
+        if t is not None:
+            _expect(t, torch.int32, f"{what}: {name}")
+            if t.dim() != 1 or t.shape != first.shape:
+                raise ValueError(f"{what}: {name} must be one-dimensional, all lists alike")
+    _on_device(what, key_pages=key_pages, value_pages=value_pages, k_scales=k_scales,
+               v_scales=v_scales, **lists, **(tables or {}))
+    return (_ptr(key_pages), _ptr(value_pages), _ptr(k_scales), _ptr(v_scales), int(num_pages),
+            page_rows, row_bytes, block_rows, kv_heads), device
+
+
+def carat_pages_copy(key_pages, value_pages, src, dst, *, rows=None, k_scales=None, v_scales=None,
+                     stream=None):
+    """Copy the first rows[i] rows (default: all) of page src[i] into page dst[i], keys,
+    values and (e4m3 pages, uint8) the scales of their blocks.  src, dst, rows: int32
+    lists on the device; a source below 0 is skipped."""
+    what = "carat_pages_copy"
+    head, device = _page_args(what, key_pages, value_pages, k_scales, v_scales,
+                              {"src": src, "dst": dst, "rows": rows})
+    _check((_lib or library()).carat_pages_copy(
+        *head, _ptr(src), _ptr(dst), _ptr(rows), src.shape[0], _stream_of(stream, device)), what)
+
+
+def carat_paged_fork(key_pages, value_pages, page_table, context_lengths, child_table, parents,
+                     new_pages, *, child_lengths=None, k_scales=None, v_scales=None, stream=None):
+    """Children of requests: child i's line of child_table takes over the whole pages of
+    request parents[i], and the rows of its last, partly filled page are copied into page
+    new_pages[i] (below 0: the child takes that page itself).  child_lengths[i] (optional)
+    becomes the parent's context length."""
+    what = "carat_paged_fork"
+    head, device = _page_args(
+        what, key_pages, value_pages, k_scales, v_scales,
+        {"parents": parents, "new_pages": new_pages, "child_lengths": child_lengths},
+        {"page_table": page_table, "context_lengths": context_lengths, "child_table": child_table})
+    for name, t in (("page_table", page_table), ("context_lengths", context_lengths),
+                    ("child_table", child_table)):
+        _expect(t, torch.int32, f"{what}: {name}")
+    if page_table.dim() != 2 or child_table.dim() != 2 or \
+            child_table.shape[1] != page_table.shape[1] or \
+            child_table.shape[0] != parents.shape[0]:
+        raise ValueError(f"{what}: child_table must be [children][max_pages]")
+    if tuple(context_lengths.shape) != (page_table.shape[0],):
+        raise ValueError(f"{what}: context_lengths must be [parents' batch]")
+    _check((_lib or library()).carat_paged_fork(
+        *head, _ptr(page_table), page_table.shape[0], page_table.shape[1], _ptr(context_lengths),
+        _ptr(child_table), _ptr(child_lengths), _ptr(parents), _ptr(new_pages), parents.shape[0],
+        _stream_of(stream, device)), what)
+
+
+def carat_pages_move(key_pages, value_pages, src, dst, *, page_table=None, k_scales=None,
+                     v_scales=None, num_pages=None, stream=None):
+    """Move whole pages src[i] to dst[i] (Pool.plan_compaction's list) and make every entry
+    of page_table that names src[i] name dst[i].  key_pages and value_pages None: the bytes
+    have been moved already, only scales and table follow (num_pages: the pool's, where
+    there are no scales to tell)."""
+    what = "carat_pages_move"
+    if page_table is not None:
+        _expect(page_table, torch.int32, f"{what}: page_table")
+    head, device = _page_args(what, key_pages, value_pages, k_scales, v_scales,
+                              {"src": src, "dst": dst}, {"page_table": page_table}, num_pages)
+    _check((_lib or library()).carat_pages_move(
+        *head, _ptr(src), _ptr(dst), src.shape[0], _ptr(page_table),
+        0 if page_table is None else page_table.numel(), _stream_of(stream, device)), what)

@@ -228,6 +228,43 @@ struct PagedFp8Params {
     float scale_log2;           // softmax scale * log2(e)
 };
 
+// Everything an attention of a chunk of new tokens over bf16 pages needs.
+struct PagedChunkParams {
+    uint16_t *out;              // bf16 [B][k][Hq][D]
+    const uint16_t *q;          // bf16 [B][k][Hq][D]
+    const uint16_t *k_pages, *v_pages;  // bf16 [num_pages][page_rows][Hkv][D]
+    const int32_t *page_table;  // [B][max_pages]
+    const int32_t *new_counts;  // [B] or nullptr (k)
+    const int32_t *context_lengths;
+    void *workspace;
+    int *dev_status;
+    int max_pages, page_rows, num_pages;
+    int batch, k, q_heads, kv_heads, head_dim, group;
+    int capacity;               // max_pages * page_rows
+    int window, sinks;          // window 0: every position up to the query's own
+    float scale_log2;           // softmax scale * log2(e)
+};
+
+// Everything a copy, fork or move of pages needs.
+struct PagesParams {
+    void *key_pages, *value_pages;      // [num_pages][page_rows] rows of row_bytes
+    float *k_scales, *v_scales; // [num_pages][page_rows / block_rows][kv_heads] or nullptr
+    int num_pages, page_rows, block_rows, kv_heads;
+    long long row_bytes;        // a multiple of 16
+    int pieces;                 // pieces of a page that CTAs copy
+    int count;                  // jobs
+    const int32_t *src, *dst;   // copy, move
+    const int32_t *rows;        // copy: rows of each job or nullptr (whole pages)
+    // fork
+    const int32_t *parents, *new_pages, *context_lengths, *page_table;
+    int32_t *child_table, *child_lengths;
+    int num_parents, max_pages;
+    // move
+    int32_t *table;
+    long long table_entries;
+    int *dev_status;
+};
+
 // Host-side count of kernel launches (carat_kernel_launches).
 void count_launches(int n);
 
@@ -281,6 +318,15 @@ cudaError_t launch_rope_append_fp8(const RopeParams &p, cudaStream_t stream);
 bool paged_fp8_supported(int head_dim);
 size_t paged_fp8_workspace(int batch, int proposal_count, int q_heads, int kv_heads, int head_dim);
 cudaError_t launch_paged_fp8_attention(const PagedFp8Params &p, cudaStream_t stream);
+
+// The attention of a chunk over bf16 pages (paged_chunk.cu), and the operators on
+// pages (pages.cu).
+bool paged_chunk_supported(int head_dim);
+size_t paged_chunk_workspace(int batch, int k, int q_heads, int kv_heads, int head_dim);
+cudaError_t launch_paged_chunk_attention(const PagedChunkParams &p, cudaStream_t stream);
+cudaError_t launch_pages_copy(const PagesParams &p, cudaStream_t stream);
+cudaError_t launch_paged_fork(const PagesParams &p, cudaStream_t stream);
+cudaError_t launch_pages_move(const PagesParams &p, cudaStream_t stream);
 
 // Tensor-core path (attention_tc.cu): rows per tile (16, 32 or 64) for a
 // group size and proposal count, CTAs resident per SM, whether the shape is

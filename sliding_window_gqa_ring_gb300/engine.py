@@ -212,6 +212,24 @@ class SharedPool:
         shape = (self.num_pages, self.page_bytes // row_bytes, kv_heads, head_dim)
         return self.k.view(torch.uint8).view(shape), self.v.view(torch.uint8).view(shape)
 
+    def compact(self, layers, max_moves: int, stream=None) -> int:
+        """Empty blocks that single pages broke up, so that rings find room: at most
+        max_moves pages move, and the page tables (and block scales) of `layers`, every
+        layer with pages in this pool, follow.  Returns the pages moved; their old ids
+        are free, so whoever keeps ids on the host reads the tables again."""
+        src, dst = self.alloc.plan_compaction(max_moves)
+        if src:
+            src, dst = _i32(src, self.device), _i32(dst, self.device)
+            whole = (self.num_pages, 1, 1, self.page_bytes)
+            carat.carat_pages_move(self.k.view(torch.uint8).view(whole),
+                                   self.v.view(torch.uint8).view(whole), src, dst, stream=stream)
+            for layer in layers:
+                carat.carat_pages_move(None, None, src, dst, page_table=layer.page_table,
+                                       k_scales=getattr(layer, "k_scales", None),
+                                       v_scales=getattr(layer, "v_scales", None),
+                                       num_pages=self.num_pages, stream=stream)
+        return len(src)
+
 
 def rotary_table(rows: int, rotary_dim: int, base: float = 10000.0, device="cuda"):
     """fp32 [rows][rotary_dim] for the rotary appends: cosines then sines of
@@ -229,12 +247,22 @@ class PagedGlobalLayer:
 
     cos_sin (rotary_table): queries and new keys arrive unrotated and are
     rotated on their way; step() is then the rotary append and the attention
-    over the pages (two calls) instead of one fused call."""
+    over the pages (two calls) instead of one fused call.
+
+    window (with `sinks` first tokens that stay visible): a sliding layer in pages;
+    step() is then the append and carat_paged_chunk_attention, its outputs bf16, and
+    pages behind the window may be freed (hidden()).
+
+    chunk(): the same for more new tokens than a step has, up to max_chunk of each
+    request (a prompt, or a part of one)."""
 
     def __init__(self, pool: SharedPool, page_table: torch.Tensor, *, q_heads: int = 16,
                  kv_heads: int = 2, head_dim: int = 512, max_proposals: int = 4,
-                 scale: float | None = None, cos_sin=None, interleaved: bool = False):
+                 scale: float | None = None, cos_sin=None, interleaved: bool = False,
+                 window: int = 0, sinks: int = 0, max_chunk: int = 0):
         self.cos_sin, self.interleaved = cos_sin, interleaved
+        self.window, self.sinks = window, sinks
+        self.out_dtype = torch.bfloat16 if window else torch.float32
         self.key_pages, self.value_pages = pool.pages(kv_heads, head_dim)
         self.page_rows = self.key_pages.shape[1]
         self.page_table = page_table
@@ -246,17 +274,29 @@ class PagedGlobalLayer:
         self.workspace = carat.workspace_tensor(
             max(carat.global_workspace_bytes(batch, p, q_heads, kv_heads, head_dim, self.capacity)
                 for p in range(1, max_proposals + 1)), self.device)
+        most = max(max_proposals, max_chunk)
         if cos_sin is not None:
-            self.rotated = torch.empty(batch * max_proposals * q_heads * head_dim,
+            self.rotated = torch.empty(batch * most * q_heads * head_dim,
                                        dtype=torch.bfloat16, device=self.device)
+        need = 0
+        if window or max_chunk:
+            # needs shrink to nothing once a call has rows enough for every SM
+            for k in range(1, most + 1):
+                bytes_ = carat.paged_chunk_workspace_bytes(batch, k, q_heads, kv_heads, head_dim)
+                need = max(need, bytes_)
+                if bytes_ == 0:
+                    break
+        self.chunk_workspace = carat.workspace_tensor(need, self.device) if need else None
 
-    def append(self, k_new, v_new, context_lengths, stream=None, new_counts=None):
+    def append(self, k_new, v_new, context_lengths, stream=None, new_counts=None, queries=None,
+               queries_out=None):
         """Write rows (a prompt's after prefill, say); rotated when the layer
-        has a rotary table."""
+        has a rotary table, queries (into queries_out) too."""
         if self.cos_sin is not None:
             carat.carat_paged_rope_append(self.key_pages, self.value_pages, self.page_table, k_new,
                                           v_new, context_lengths, cos_sin=self.cos_sin,
-                                          interleaved=self.interleaved, new_counts=new_counts,
+                                          interleaved=self.interleaved, queries=queries,
+                                          queries_out=queries_out, new_counts=new_counts,
                                           stream=stream)
             return
         if new_counts is not None:
@@ -264,7 +304,39 @@ class PagedGlobalLayer:
         carat.carat_paged_append(self.key_pages, self.value_pages, self.page_table, k_new, v_new,
                                  context_lengths, stream=stream)
 
+    def chunk(self, queries, k_new, v_new, context_lengths, out=None, stream=None,
+              new_counts=None):
+        """Append a chunk's rows (new_counts[b] of request b, or all; counts need a layer
+        with a rotary table) and attend to them and to what the pages held: out bf16."""
+        if out is None:
+            out = torch.empty(queries.shape, dtype=torch.bfloat16, device=self.device)
+        if self.cos_sin is not None:
+            rotated = self.rotated[:queries.numel()].view(queries.shape)
+            self.append(k_new, v_new, context_lengths, stream=stream, new_counts=new_counts,
+                        queries=queries, queries_out=rotated)
+            queries = rotated
+        else:
+            self.append(k_new, v_new, context_lengths, stream=stream, new_counts=new_counts)
+        carat.carat_paged_chunk_attention(
+            out, queries, self.key_pages, self.value_pages, self.page_table, context_lengths,
+            scale=self.scale, window=self.window, sinks=self.sinks, new_counts=new_counts,
+            workspace=self.chunk_workspace, stream=stream)
+        return out
+
+    def fork(self, context_lengths, child_table, parents, new_pages, child_lengths=None,
+             stream=None):
+        """Children of this table's requests (carat_paged_fork)."""
+        carat.carat_paged_fork(self.key_pages, self.value_pages, self.page_table, context_lengths,
+                               child_table, parents, new_pages, child_lengths=child_lengths,
+                               stream=stream)
+
+    def hidden(self, context_length: int):
+        """Entries [first, end) of a request's line whose pages are behind the window."""
+        return carat.hidden_pages(context_length, self.window, self.sinks, self.page_rows)
+
     def step(self, queries, k_new, v_new, context_lengths, out=None, stream=None):
+        if self.window:
+            return self.chunk(queries, k_new, v_new, context_lengths, out=out, stream=stream)
         if out is None:
             out = torch.empty(queries.shape, dtype=torch.float32, device=self.device)
         if self.cos_sin is not None:
@@ -336,6 +408,17 @@ class Fp8PagedLayer:
             self.page_table, context_lengths, scale=self.scale, window=self.window,
             new_counts=new_counts, workspace=self.workspace, stream=stream)
         return out
+
+    def fork(self, context_lengths, child_table, parents, new_pages, child_lengths=None,
+             stream=None):
+        """Children of this table's requests (carat_paged_fork), block scales too."""
+        carat.carat_paged_fork(self.key_pages, self.value_pages, self.page_table, context_lengths,
+                               child_table, parents, new_pages, child_lengths=child_lengths,
+                               k_scales=self.k_scales, v_scales=self.v_scales, stream=stream)
+
+    def hidden(self, context_length: int):
+        """Entries [first, end) of a request's line whose pages are behind the window."""
+        return carat.hidden_pages(context_length, self.window, 0, self.page_rows)
 
     def step(self, queries, k_new, v_new, context_lengths, out=None, stream=None,
              new_counts=None):

@@ -1,0 +1,332 @@
+"""Attention of a chunk of new tokens over bf16 pages against its definition in 64 bits
+(GPU, through the C ABI).  Tolerance: tests/chunk_reference.py."""
+import math
+
+import pytest
+import torch
+
+import chunk_reference as ref
+from sliding_window_gqa_ring_gb300 import carat
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _cuda():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    carat.library()
+    carat.carat_get_device_status(clear=True)
+    yield
+    assert carat.carat_get_device_status(clear=True) == 0
+
+
+class Case:
+    """Pages with known contents under a table in no order; every row that holds no key of
+    its request, every page of nobody and every row of `out` behind a count holds NaNs."""
+
+    def __init__(self, ctx, k, q_heads, kv_heads, head_dim, *, page_rows=128, counts=None,
+                 window=0, sinks=0, seed=0, spread=1.0, scale=None):
+        g = torch.Generator().manual_seed(seed)
+        self.ctx, self.k, self.B = list(ctx), k, len(ctx)
+        self.counts = list(counts) if counts is not None else None
+        self.n = self.counts or [k] * self.B
+        self.window, self.sinks, self.page_rows = window, sinks, page_rows
+        self.scale = 1.0 / math.sqrt(head_dim) if scale is None else scale
+        per = max(1, -(-max(max(c, 0) + k for c in ctx) // page_rows))
+        self.num_pages = self.B * per + 3
+        self.table = torch.randperm(self.num_pages, generator=g)[:self.B * per].view(
+            self.B, per).to(torch.int32)
+        pool = (self.num_pages, page_rows, kv_heads, head_dim)
+        self.kp = torch.full(pool, float("nan"), dtype=torch.bfloat16)
+        self.vp = torch.full(pool, float("nan"), dtype=torch.bfloat16)
+        self.keys, self.values = [], []
+        for b in range(self.B):
+            m = max(self.ctx[b], 0) + max(0, min(self.n[b], k))
+            kk = torch.randn((m, kv_heads, head_dim), generator=g).bfloat16()
+            vv = torch.randn((m, kv_heads, head_dim), generator=g).bfloat16()
+            self.keys.append(kk)
+            self.values.append(vv)
+        self.write()
+        self.q = (torch.randn((self.B, k, q_heads, head_dim), generator=g) * spread).bfloat16()
+
+    def write(self):
+        for b in range(self.B):
+            for x, pages in ((self.keys[b], self.kp), (self.values[b], self.vp)):
+                for i in range(0, x.shape[0], self.page_rows):
+                    part = x[i:i + self.page_rows]
+                    pages[self.table[b, i // self.page_rows], :part.shape[0]] = part
+
+    def device(self):
+        self.dq, self.dk, self.dv = self.q.cuda(), self.kp.cuda(), self.vp.cuda()
+        self.dt = self.table.cuda()
+        self.dc = torch.tensor(self.ctx, dtype=torch.int32, device="cuda")
+        self.dn = (torch.tensor(self.counts, dtype=torch.int32, device="cuda")
+                   if self.counts is not None else None)
+        self.out = torch.full(self.q.shape, 7.0, dtype=torch.bfloat16, device="cuda")
+        B, k, hq, d = self.q.shape
+        need = carat.paged_chunk_workspace_bytes(B, k, hq, self.kp.shape[2], d)
+        # a workspace that holds NaNs: it needs no initialisation
+        self.ws = carat.workspace_tensor(need).fill_(0xff) if need else None
+        return self
+
+    def call(self, **kw):
+        carat.carat_paged_chunk_attention(
+            self.out, self.dq, self.dk, self.dv, self.dt, self.dc, scale=self.scale,
+            window=self.window, sinks=self.sinks, new_counts=self.dn, workspace=self.ws, **kw)
+        return self.out
+
+    def want(self, b, rows=None):
+        rows = range(self.n[b]) if rows is None else rows
+        if not len(rows):
+            return None
+        parts = [ref.attention(self.q[b, j:j + 1].double(), self.keys[b].double(),
+                               self.values[b].double(), self.ctx[b] + j, self.window, self.sinks,
+                               self.scale) for j in rows]
+        return tuple(torch.cat(x) for x in zip(*parts))
+
+    def check(self, out, rows=None):
+        out = out.cpu()
+        for b in range(self.B):
+            r = list(range(self.n[b])) if rows is None else [j for j in rows if j < self.n[b]]
+            if r:
+                want, bound = self.want(b, r)
+                got = out[b, r].double()
+                assert got.isfinite().all(), (b, "not finite")
+                off = (got - want).abs() - bound
+                assert (off <= 0).all(), (b, float(off.max()), off.argmax())
+            assert (out[b, self.n[b]:] == 7.0).all(), (b, "rows behind the count")
+
+
+SHAPES = [(16, 2, 512), (16, 8, 256), (3, 1, 256), (5, 1, 512), (4, 4, 256), (64, 1, 256)]
+
+
+@pytest.mark.parametrize("q_heads,kv_heads,head_dim", SHAPES)
+@pytest.mark.parametrize("k,ctx", [
+    (1, [0]), (1, [1, 126, 127, 128, 1000]), (4, [0, 125, 700]), (17, [0, 111, 112, 113]),
+    (64, [64, 300]), (129, [0, 127]), (300, [5])])
+def test_lengths(k, ctx, q_heads, kv_heads, head_dim):
+    c = Case(ctx, k, q_heads, kv_heads, head_dim, seed=k, spread=2.0).device()
+    c.check(c.call())
+
+
+@pytest.mark.parametrize("q_heads,kv_heads,head_dim", [(16, 2, 512), (16, 8, 256), (6, 2, 256)])
+@pytest.mark.parametrize("window,sinks", [(1, 0), (1, 1), (2, 5), (127, 4), (128, 0), (129, 128),
+                                          (200, 130), (300, 1), (1 << 30, 3), (50, 1 << 30)])
+@pytest.mark.parametrize("k,ctx", [(1, [0, 40, 900]), (3, [129, 640]), (200, [0, 333])])
+def test_windows_and_sinks(window, sinks, k, ctx, q_heads, kv_heads, head_dim):
+    c = Case(ctx, k, q_heads, kv_heads, head_dim, window=window, sinks=sinks, seed=window,
+             page_rows=256, spread=2.0).device()
+    c.check(c.call())
+
+
+@pytest.mark.parametrize("q_heads,kv_heads,head_dim", [(16, 2, 512), (8, 4, 256)])
+@pytest.mark.parametrize("window", [0, 150])
+@pytest.mark.parametrize("counts,ctx,k", [([5, 0, 1, 40], [0, 70, 300, 127], 40),
+                                          ([0, 0], [3, 4], 5), ([130, 257, 0, 1], [1, 0, 0, 0], 257)])
+def test_counts(counts, ctx, k, window, q_heads, kv_heads, head_dim):
+    c = Case(ctx, k, q_heads, kv_heads, head_dim, counts=counts, window=window, sinks=2,
+             seed=7).device()
+    c.check(c.call())
+
+
+@pytest.mark.parametrize("q_heads,kv_heads,head_dim,window,sinks", [
+    (16, 2, 512, 0, 0), (16, 8, 256, 1024, 4), (2, 1, 512, 700, 300), (16, 8, 256, 0, 0)])
+def test_long_contexts(q_heads, kv_heads, head_dim, window, sinks):
+    c = Case([9000, 20000], 3, q_heads, kv_heads, head_dim, window=window, sinks=sinks, seed=3,
+             spread=3.0, page_rows=384).device()
+    c.check(c.call())
+
+
+@pytest.mark.parametrize("q_heads,kv_heads,head_dim,window", [(16, 2, 512, 0), (16, 8, 256, 1024)])
+def test_a_long_chunk(q_heads, kv_heads, head_dim, window):
+    c = Case([500], 2500, q_heads, kv_heads, head_dim, window=window, sinks=100, seed=4,
+             spread=2.0).device()
+    out = c.call()
+    c.check(out, rows=[0, 1, 17, 127, 128, 600, 1023, 1024, 1600, 2047, 2400, 2498, 2499])
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.05, 1e-30, 3.0, 1e4])
+@pytest.mark.parametrize("head_dim", [256, 512])
+def test_scales(scale, head_dim):
+    """Flat, inverted and one-hot softmaxes.  (At 1e4 the scores' fp32 rounding alone moves
+    every weight, so there the one-hot result is compared where it is one.)"""
+    c = Case([200], 30, 4, 2, head_dim, scale=scale, seed=5).device()
+    out = c.call()
+    if abs(scale) < 1:
+        c.check(out)
+        return
+    got = out.cpu()[0].double()
+    assert got.isfinite().all()
+    for j in range(30):
+        for h in range(4):
+            s = (c.q[0, j, h].double() @ c.keys[0][:200 + j + 1, h // 2].double().T) * scale
+            top = s.topk(2).values
+            if top[0] - top[1] > 40 + abs(scale) * 1e-2:
+                want = c.values[0][int(s.argmax()), h // 2].double()
+                assert ((got[j, h] - want).abs() <= 2.0 ** -7 * want.abs() + 2.0 ** -20).all()
+
+
+def test_rising_scores_move_the_running_maximum():
+    """Keys whose scores grow from tile to tile, by far more than any slack, and back."""
+    for head_dim in (256, 512):
+        c = Case([700], 60, 4, 2, head_dim, seed=6)
+        direction = torch.ones(head_dim)
+        c.q[:] = direction.bfloat16() * 0.5
+        for x, sign in ((c.keys[0], 1.0),):
+            n = x.shape[0]
+            ramp = torch.cat([torch.linspace(-4, 4, n // 2), torch.linspace(4, -4, n - n // 2)])
+            x[:] = (x.float() * 0.05 + sign * ramp[:, None, None]).bfloat16()
+        c.write()
+        c.device()
+        c.check(c.call())
+
+
+@pytest.mark.parametrize("head_dim", [256, 512])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+def test_non_finite_values_reach_only_the_queries_that_see_them(bad, head_dim):
+    """In key 290 (value and key rows): queries before it and, under the window, long after
+    it are as without."""
+    for where in ("v", "k"):
+        for window in (0, 40):
+            clean = Case([250], 120, 4, 2, head_dim, window=window, sinks=3, seed=8)
+            c = Case([250], 120, 4, 2, head_dim, window=window, sinks=3, seed=8)
+            rows = c.values[0] if where == "v" else c.keys[0]
+            rows[290, 1, 5] = bad
+            c.write()
+            got = c.device().call().cpu()[0]
+            want, bound = clean.want(0)
+            for j in range(120):
+                sees = bool(ref.seen(250 + j, 370, window, 3)[290])
+                for h in range(4):
+                    if sees and h // 2 == 1:
+                        if where == "v":
+                            assert not got[j, h, 5].isfinite(), (j, h)
+                    else:
+                        assert ((got[j, h].double() - want[j, h]).abs() <= bound[j, h]).all(), (j, h)
+
+
+@pytest.mark.parametrize("head_dim", [256, 512])
+def test_a_non_finite_value_that_every_query_sees_stays_in_its_element(head_dim):
+    c = Case([2000], 5, 4, 2, head_dim, seed=9)
+    c.values[0][100, 0, 7] = float("inf")
+    c.write()
+    clean = Case([2000], 5, 4, 2, head_dim, seed=9)
+    want, bound = clean.want(0)
+    got = c.device().call().cpu()[0].double()
+    assert not got[:, :2, 7].isfinite().any()
+    ok = torch.ones_like(got, dtype=torch.bool)
+    ok[:, :2, 7] = False
+    assert ((got - want).abs() <= bound)[ok].all()
+
+
+def test_queries_that_are_not_finite_stay_in_their_rows():
+    for head_dim in (256, 512):
+        c = Case([100], 40, 4, 2, head_dim, seed=10)
+        clean = Case([100], 40, 4, 2, head_dim, seed=10)
+        c.q[0, 3, 1, 0] = float("nan")
+        c.q[0, 20, 2, 9] = float("inf")
+        got = c.device().call().cpu()[0].double()
+        want, bound = clean.want(0)
+        ok = torch.ones((40, 4), dtype=torch.bool)
+        ok[3, 1] = ok[20, 2] = False
+        assert ((got - want).abs() <= bound)[ok].all()
+        assert got[3, 1].isnan().all()
+
+
+@pytest.mark.parametrize("head_dim", [256, 512])
+def test_rejected_requests_are_nan_and_reported(head_dim):
+    c = Case([-1, 50, 300, 20], 20, 4, 2, head_dim, counts=[20, 21, 20, 20], seed=11)
+    c.device()
+    c.dt = c.table[:, :2].contiguous().cuda()      # room for 256 rows: request 2 does not fit
+    out = c.call().cpu()
+    assert carat.carat_get_device_status(clear=True) == carat.CARAT_DEV_BAD_CONTEXT
+    assert out[:3].isnan().all()
+    want, bound = c.want(3)
+    assert ((out[3].double() - want).abs() <= bound).all()
+
+
+@pytest.mark.parametrize("head_dim", [256, 512])
+def test_a_page_outside_the_pool_reads_as_zeros_and_is_reported(head_dim):
+    c = Case([200, 200], 30, 4, 2, head_dim, seed=12)
+    c.device()
+    c.dt[0, 0] = 1 << 20
+    c.keys[0][:128] = 0
+    c.values[0][:128] = 0
+    out = c.call().cpu()
+    assert carat.carat_get_device_status(clear=True) == carat.CARAT_DEV_BAD_CACHE_ID
+    for b in range(2):
+        want, bound = c.want(b)
+        assert ((out[b].double() - want).abs() <= bound).all(), b
+
+
+def test_pages_that_nobody_sees_are_not_read():
+    """Entries behind the window and past the keys hold ids of no page: no error."""
+    for head_dim in (256, 512):
+        c = Case([1000, 130], 5, 4, 2, head_dim, window=100, sinks=3, seed=13)
+        c.device()
+        c.dt[0, 1:7] = -1
+        c.dt[1, 2:] = 1 << 20
+        c.check(c.call())
+        assert carat.carat_get_device_status(clear=True) == 0
+
+
+def test_streams_graphs_and_repeats_give_the_same_bits():
+    c = Case([3000, 77], 9, 16, 2, 512, window=2000, sinks=5, seed=14).device()
+    first = c.call().clone()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        c.out.fill_(7.0)
+        c.call()
+    torch.cuda.current_stream().wait_stream(s)
+    assert torch.equal(first, c.out)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        c.call()
+    for _ in range(3):
+        c.out.fill_(7.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(first, c.out)
+    # the captured call follows what the device holds: other lengths and another table
+    c.dc.copy_(torch.tensor([1500, 10], dtype=torch.int32))
+    graph.replay()
+    torch.cuda.synchronize()
+    replayed = c.out.clone()
+    c.out.fill_(7.0)
+    assert torch.equal(replayed, c.call())
+
+
+def test_two_calls_at_once_with_workspaces_of_their_own():
+    cases = [Case([4000], 3, 16, 2, 512, seed=15).device(),
+             Case([2000, 9], 2, 16, 8, 256, window=1024, sinks=4, seed=16).device()]
+    alone = [c.call().clone() for c in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for s, c in zip(streams, cases):
+            with torch.cuda.stream(s):
+                c.call()
+    torch.cuda.synchronize()
+    for a, c in zip(alone, cases):
+        assert torch.equal(a, c.out)
+
+
+def test_no_requests_and_bad_arguments():
+    c = Case([10], 4, 4, 2, 256, seed=17).device()
+    carat.carat_paged_chunk_attention(c.out[:0], c.dq[:0], c.dk, c.dv, c.dt[:0], c.dc[:0],
+                                      scale=1.0)
+    with pytest.raises(TypeError):
+        carat.carat_paged_chunk_attention(c.out.float(), c.dq, c.dk, c.dv, c.dt, c.dc, scale=1.0)
+    with pytest.raises(ValueError):
+        carat.carat_paged_chunk_attention(c.out, c.dq, c.dk, c.dv, c.dt.cpu(), c.dc, scale=1.0)
+    with pytest.raises(ValueError):
+        carat.carat_paged_chunk_attention(c.out, c.dq.transpose(1, 2), c.dk, c.dv, c.dt, c.dc,
+                                          scale=1.0)
+    with pytest.raises(ValueError):
+        carat.carat_paged_chunk_attention(c.out, c.dq, c.dk, c.dv, c.dt, c.dc[:0], scale=1.0)
+    for kw in (dict(window=-1), dict(sinks=-1), dict(window=-(1 << 40))):
+        with pytest.raises(carat.CaratError):
+            carat.carat_paged_chunk_attention(c.out, c.dq, c.dk, c.dv, c.dt, c.dc, scale=1.0,
+                                              workspace=c.ws, **kw)
