@@ -618,7 +618,7 @@ size_t carat_paged_fp8_workspace_bytes(int batch, int proposal_count, int q_head
  *                    GPU need separate workspaces.
  *
  * Supported: head_dim 256 or 512; q_heads/kv_heads <= 64; batch * proposal_count *
- * q_heads < 2^31; kv_heads * head_dim <= 2^24 (others: CARAT_ERR_UNSUPPORTED).
+ * q_heads <= 2^28; kv_heads * head_dim <= 2^24 (others: CARAT_ERR_UNSUPPORTED).
  */
 carat_status carat_paged_chunk_attention(
     void *out, const void *queries, const void *key_pages, const void *value_pages, int num_pages,

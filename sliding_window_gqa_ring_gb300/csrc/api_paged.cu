@@ -216,7 +216,7 @@ static carat_status check_paged_chunk(int batch, int k, int q_heads, int kv_head
         head_dim < 1)
         return CARAT_ERR_INVALID_ARG;
     if (!paged_chunk_supported(head_dim) || q_heads / kv_heads > 64 ||
-        (long long)batch * k * q_heads >= (1LL << 31) || (long long)kv_heads * head_dim > (1 << 24))
+        (long long)batch * k > (1LL << 28) / q_heads || (long long)kv_heads * head_dim > (1 << 24))
         return CARAT_ERR_UNSUPPORTED;
     return CARAT_OK;
 }

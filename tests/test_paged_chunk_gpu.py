@@ -330,3 +330,22 @@ def test_no_requests_and_bad_arguments():
         with pytest.raises(carat.CaratError):
             carat.carat_paged_chunk_attention(c.out, c.dq, c.dk, c.dv, c.dt, c.dc, scale=1.0,
                                               workspace=c.ws, **kw)
+
+
+@pytest.mark.parametrize("q_heads,kv_heads,head_dim,ctx,k,window", [
+    (16, 2, 512, [9000, 20000], 3, 0), (16, 8, 256, [9000, 20000], 3, 0),
+    (16, 2, 512, [500, 90], 300, 0), (16, 8, 256, [500, 2000], 300, 700)])
+def test_cold_and_warm_caches_give_the_same_bits(q_heads, kv_heads, head_dim, ctx, k, window):
+    """Loads that come late from memory change the order in which the roles of a CTA pair
+    meet, and nothing else."""
+    c = Case(ctx, k, q_heads, kv_heads, head_dim, window=window, sinks=9, seed=18, spread=3.0,
+             page_rows=384).device()
+    first = c.call().clone()
+    c.check(first, rows=[0, 1, 2, 151, 299])
+    flush = torch.empty(300 << 20, dtype=torch.uint8, device="cuda")
+    for i in range(40):
+        if i % 2:
+            flush.fill_(i)
+        c.out.fill_(7.0)
+        c.call()
+        assert torch.equal(first, c.out), i
