@@ -36,10 +36,17 @@
 // Few items (fewer than pairs of SMs): the key tiles of an item are split over CTA pairs,
 // each writes (max, sum, unnormalised O), and a second launch merges them.
 //
-// Warp roles (256 threads): warp 0 TMA producer (each CTA its own halves, counted on the
-// leader's barriers), warp 1 of the leader issues the products, warps 4-7 softmax, rescale
-// and output.  Every wait is bounded: on a timeout CARAT_DEV_TIMEOUT is set and the CTA
-// stops, waits for its own copies and products, and returns.
+// Schedule.  One CTA pair for every two SMs; the items that have rows, request after
+// request, are dealt to them in turn (forth and back, so that the longer ones of a causal
+// mask are shared out), each role walking its pair's items by itself.  The next item's keys
+// and queries are loaded and its first scores computed while the last one's output leaves.
+//
+// Warp roles (384 threads): warp 0 TMA producer (each CTA its own halves, counted on the
+// leader's barriers), warp 1 of the leader issues the products, warps 4-11 softmax, rescale
+// and output: two threads a row, the first 64 keys of a tile and the others (one thread a
+// row took 1.9 us a tile at head_dim 256, nearly twice the products' time).  Every wait is
+// bounded: on a timeout CARAT_DEV_TIMEOUT is set and the CTA stops, waits for its own
+// copies and products, and returns.
 #include <algorithm>
 #include <atomic>
 #include <cfloat>
@@ -58,7 +65,7 @@ constexpr int kKeys = 128;              // keys of a tile
 constexpr int kRows = 128;              // rows of a CTA
 constexpr int kDV = 256;                // value dimensions of an item
 constexpr int kStage = 32768;           // K: 64 keys x 256 d, or V: 128 keys x 128 d
-constexpr int kThreads = 256;
+constexpr int kThreads = 384, kSoftmax = 256;
 constexpr int kMasked = 8;              // masked tiles of an item: 3 + 3 + 1 at most
 constexpr uint32_t kFull = 0xffffffffu;
 constexpr float kSlack = 8.0f;          // log2 units
@@ -70,8 +77,8 @@ struct Lay {
     static constexpr int kSlab = kRows * 128;           // 64 d of Q
     static constexpr int kOffQ = NS * kStage;
     static constexpr int kOffMisc = kOffQ + D / 64 * kSlab;
-    static constexpr int kBytes = kOffMisc + 1024;
-    static constexpr int kAlloc = kBytes + 1024;        // base alignment
+    static constexpr int kMisc = 3072;
+    static constexpr int kAlloc = kOffMisc + kMisc;
     static_assert(kAlloc <= 232448, "more dynamic shared memory than one CTA may use");
 };
 
@@ -80,6 +87,7 @@ struct Shared {
     uint64_t full[NS];      // leader: a stage's bytes of both CTAs have landed
     uint64_t empty[NS];     // both: the products that read the stage are done
     uint64_t q_full;        // leader
+    uint64_t q_empty;       // both: an item's last scores are computed
     uint64_t s_full[2];     // both: a tile's scores are in tensor memory
     uint64_t p_full[2];     // leader: its weights are, and V is looked through
     uint64_t pv_done;       // both: a tile's value product is done
@@ -87,9 +95,12 @@ struct Shared {
     uint64_t drain;
     uint32_t tmem;
     int abort_flag;
-    int poison;             // some masked tile held a value that is not finite
-    int tile_base[kMasked];
-    uint32_t bad[kMasked][2][4];   // such keys of masked tile i, by CTA of the pair
+    // Keys of masked tiles with values that are not finite, of three items in turn: the
+    // other CTA may be at the next item's first tile already, and the third is cleared
+    // while nobody can be at its item.
+    uint32_t poison[3];
+    uint32_t bad[3][kMasked][4];
+    float row[2][2][kRows];           // a row's two threads tell each other
 };
 
 struct Request {
@@ -107,9 +118,9 @@ __device__ __forceinline__ bool request_ok(const PagedChunkParams &p, const Requ
 
 struct Plan {
     int tokens;      // of a CTA
-    int tiles;       // row tiles (of a pair) of a request's chunk
     int halves;      // value halves
     int splits;
+    int pairs;       // CTA pairs of the grid
     float2 *part_ml; // [B k Hq][splits]
     float *part_o;   // [B k Hq][splits][D]
 };
@@ -142,15 +153,81 @@ __device__ __forceinline__ int split_at(int count, int s, int splits) {
     return (int)((long long)count * s / splits);
 }
 
-// Bounded wait; false on a timeout or when another role of this CTA gave up.
+// One pair's share of a request's chunk for one KV head.
+struct Item {
+    int b, c, vh, split;
+    int j0, n;             // the pair's first token; the request's tokens
+    long long ctx;
+};
+
+// The items of this pair, in order: the same for every warp that walks them (whole warps).
+// Requests are looked at 32 at a time, one a lane.
+struct Items {
+    int base = -32;        // first request held
+    int upto = 0;          // items of the held requests up to this lane's, and before
+    int before = 0;        // items before the held requests
+    int n = 0, tiles = 0;  // this lane's request
+    long long ctx = 0;
+    int round = 0;
+
+    __device__ __forceinline__ bool next(const PagedChunkParams &p, const Plan &plan, int lane,
+                                         int pair, Item &it) {
+        const int id = round * plan.pairs + ((round & 1) ? plan.pairs - 1 - pair : pair);
+        ++round;
+        const int per_tile = p.kv_heads * plan.halves * plan.splits;
+        while (true) {
+            const unsigned hit = __ballot_sync(kFull, base >= 0 && id < upto);
+            if (hit) {
+                const int src = __ffs(hit) - 1;
+                const int t_src = __shfl_sync(kFull, tiles, src);
+                int rest = id - (__shfl_sync(kFull, upto, src) - t_src * per_tile);
+                it.b = base + src;
+                it.n = __shfl_sync(kFull, n, src);
+                it.ctx = __shfl_sync(kFull, ctx, src);
+                const int tile = t_src - 1 - rest / per_tile;   // the longest first
+                rest %= per_tile;
+                it.split = rest % plan.splits;
+                rest /= plan.splits;
+                it.vh = rest % plan.halves;
+                it.c = rest / plan.halves;
+                it.j0 = tile * 2 * plan.tokens;
+                return true;
+            }
+            if (base >= 0) before = __shfl_sync(kFull, upto, 31);
+            base += 32;
+            if (base >= p.batch) return false;
+            tiles = 0;
+            if (base + lane < p.batch) {
+                const Request rq = load_request(p, base + lane);
+                ctx = rq.ctx;
+                n = rq.n;
+                if (request_ok(p, rq)) tiles = (n + 2 * plan.tokens - 1) / (2 * plan.tokens);
+            }
+            upto = tiles * per_tile;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(kFull, upto, o);
+                if (lane >= o) upto += y;
+            }
+            upto += before;
+        }
+    }
+};
+
+// Bounded wait; false on a timeout or when another role of this CTA gave up.  kCluster:
+// what threads of the other CTA wrote before they released the barrier is seen.
+template <bool kCluster>
 __device__ __forceinline__ bool wait_or_abort(uint64_t *bar, uint32_t parity,
                                               volatile int *abort_flag, int *dev_status) {
-    if (tc::mbar_try_wait_cluster(bar, parity)) return true;
+    auto passed = [&]() {
+        return kCluster ? tc::mbar_try_wait_cluster(bar, parity) : tc::mbar_try_wait(bar, parity);
+    };
+    if (passed()) return true;
     const uint64_t t0 = tc::globaltimer_ns();
     for (uint32_t round = 1;; ++round) {
 #pragma unroll 1
         for (int i = 0; i < 32; ++i)
-            if (tc::mbar_try_wait_cluster(bar, parity)) return true;
+            if (passed()) return true;
         if (*abort_flag) return false;
         if (tc::wait_expired(t0, round, 2000000000ull)) {
             *abort_flag = 1;
@@ -161,9 +238,10 @@ __device__ __forceinline__ bool wait_or_abort(uint64_t *bar, uint32_t parity,
 }
 
 // The same for a whole warp, which goes on or stops as one.
+template <bool kCluster = false>
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity,
                                           volatile int *abort_flag, int *dev_status) {
-    return __all_sync(kFull, wait_or_abort(bar, parity, abort_flag, dev_status)) != 0;
+    return __all_sync(kFull, wait_or_abort<kCluster>(bar, parity, abort_flag, dev_status)) != 0;
 }
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
@@ -177,8 +255,18 @@ __device__ __forceinline__ int within(long long x) {
     return (int)(x < -1 ? -1 : x > kKeys ? kKeys : x);
 }
 
-__device__ __forceinline__ void softmax_barrier() {
-    asm volatile("bar.sync 1, 128;" ::: "memory");
+// The two warps that share 32 rows meet; whether one of them has to stop, so that both do.
+__device__ __forceinline__ bool rows_barrier(int quad, bool stop) {
+    uint32_t out;
+    asm volatile(
+        "{\n\t.reg .pred pin, pout;\n\t"
+        "setp.ne.u32 pin, %1, 0;\n\t"
+        "bar.red.or.pred pout, %2, 64, pin;\n\t"
+        "selp.u32 %0, 1, 0, pout;\n\t}"
+        : "=r"(out)
+        : "r"((uint32_t)stop), "r"(1 + quad)
+        : "memory");
+    return out != 0;
 }
 
 template <int D>
@@ -189,74 +277,41 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                        const __grid_constant__ CUtensorMap map_v) {
     using L = Lay<D>;
     constexpr int NS = L::NS, KST = L::KST;
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t *smem = reinterpret_cast<uint8_t *>(
-        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    extern __shared__ __align__(1024) uint8_t smem[];
     auto *sh = reinterpret_cast<Shared<NS> *>(smem + L::kOffMisc);
-    static_assert(sizeof(Shared<NS>) <= 1024, "misc area");
+    static_assert(sizeof(Shared<NS>) <= L::kMisc, "misc area");
     uint8_t *s_q = smem + L::kOffQ;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const int rank = (int)tc::cluster_ctarank();
-
-    wait_for_prior_launch();
-    let_next_launch_start();
-
-    // The item: later row tiles (longer under a causal mask) come first.
-    int idx = blockIdx.x / 2;
-    const int split = idx % plan.splits;
-    idx /= plan.splits;
-    const int vh = idx % plan.halves;
-    idx /= plan.halves;
-    const int c = idx % p.kv_heads;
-    idx /= p.kv_heads;
-    const int b = idx % p.batch;
-    const int tile = plan.tiles - 1 - idx / p.batch;
-    const Request rq = load_request(p, b);
-    const int j0 = tile * 2 * plan.tokens;          // the pair's first token
-    const int mine = j0 + rank * plan.tokens;       // this CTA's
-    if (!request_ok(p, rq)) {
-        if (split == 0) {
-            for (int i = threadIdx.x; i < plan.tokens * p.group * (kDV / 8); i += kThreads) {
-                const int r = i / (kDV / 8), j = mine + r / p.group;
-                if (j < p.k)
-                    *reinterpret_cast<uint4 *>(
-                        p.out + (((size_t)b * p.k + j) * p.q_heads + c * p.group + r % p.group) * D +
-                        vh * kDV + i % (kDV / 8) * 8) =
-                        make_uint4(0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu);
-            }
-            if (threadIdx.x == 0) set_status(p.dev_status, CARAT_DEV_BAD_CONTEXT);
-        }
-        return;
-    }
-    if (j0 >= rq.n) return;
-    const int jend = min(j0 + 2 * plan.tokens, rq.n);
-    const Keys keys(p, rq.ctx + j0, rq.ctx + jend - 1);
-    const int x0 = split_at(keys.count, split, plan.splits);
-    const int n = split_at(keys.count, split + 1, plan.splits) - x0;
-    if (n == 0) return;
+    const int rank = (int)tc::cluster_ctarank(), pair = blockIdx.x / 2;
 
     if (threadIdx.x == 0) {
+        tc::tma_prefetch_map(&map_q);
+        tc::tma_prefetch_map(&map_k);
+        tc::tma_prefetch_map(&map_v);
         for (int i = 0; i < NS; ++i) {
             tc::mbar_init(&sh->full[i], 1);
             tc::mbar_init(&sh->empty[i], 1);
         }
         tc::mbar_init(&sh->q_full, 1);
+        tc::mbar_init(&sh->q_empty, 1);
         for (int i = 0; i < 2; ++i) {
             tc::mbar_init(&sh->s_full[i], 1);
-            tc::mbar_init(&sh->p_full[i], 8);
+            tc::mbar_init(&sh->p_full[i], 16);
         }
+        for (int i = 0; i < 3; ++i) sh->poison[i] = 0;
         tc::mbar_init(&sh->pv_done, 1);
         tc::mbar_init(&sh->v_ready, 1);
         tc::mbar_init(&sh->drain, 1);
         tc::fence_mbar_init();
         sh->abort_flag = 0;
-        sh->poison = 0;
     }
-    if (threadIdx.x < kMasked * 8) (&sh->bad[0][0][0])[threadIdx.x] = 0;
+    if (threadIdx.x < 3 * kMasked * 4) (&sh->bad[0][0][0])[threadIdx.x] = 0;
     if (warp == 1) {
         tc::tmem_alloc_pair(&sh->tmem, 512);
         tc::tmem_relinquish_pair();
     }
+    wait_for_prior_launch();
+    let_next_launch_start();
     tc::tc_fence_before();
     __syncthreads();
     tc::cluster_arrive();
@@ -265,118 +320,153 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     const uint32_t tmem = sh->tmem;
     const uint32_t t_o = tmem, t_s = tmem + kDV;
     volatile int *abort_flag = &sh->abort_flag;
+    auto keys_of = [&](const Item &it) {
+        return Keys(p, it.ctx + it.j0, it.ctx + min(it.j0 + 2 * plan.tokens, it.n) - 1);
+    };
 
     if (warp == 0) {
         // ---------------------------------------------------------------- producer
-        uint32_t cnt = 0;
+        uint32_t cnt = 0, items = 0;
         bool alive = true;
         const uint32_t q_bytes = plan.tokens * p.group * 128;
-        if (lane == 0) {
-            if (rank == 0) tc::mbar_arrive_expect_tx(&sh->q_full, 2 * (D / 64) * q_bytes);
-            const uint32_t bar = tc::map_to_rank(&sh->q_full, 0);
-            for (int i = 0; i < D / 64; ++i)
-                tc::tma_load_4d_pair(s_q + i * L::kSlab, &map_q, i * 64, c * p.group, mine, b, bar);
-        }
-        int row_held = 0;   // lane l: pool row of tile 32 * (x / 32) + l
-        auto row_of = [&](int x) -> int {
-            return __shfl_sync(kFull, row_held, x & 31);
-        };
-        auto fetch = [&](int x) {   // rows of the 32 tiles from x on
-            const int mine_x = x + lane;
-            if (mine_x < n) {
-                const long long t = keys.base(x0 + mine_x);
-                const int page = p.page_table[(size_t)b * p.max_pages + (int)(t / p.page_rows)];
-                if (page < 0 || page >= p.num_pages) {
-                    set_status(p.dev_status, CARAT_DEV_BAD_CACHE_ID);
-                    row_held = -1;
-                } else {
-                    row_held = page * p.page_rows + (int)(t % p.page_rows);
+        Items walk;
+        Item it;
+        while (alive && walk.next(p, plan, lane, pair, it)) {
+            const Keys keys = keys_of(it);
+            const int x0 = split_at(keys.count, it.split, plan.splits);
+            const int n = split_at(keys.count, it.split + 1, plan.splits) - x0;
+            if (n == 0) continue;
+            int row_held = 0;   // lane l: pool row of the item's tile 32 * (x / 32) + l
+            auto fetch = [&](int x) {
+                if (x + lane < n) {
+                    const long long t = keys.base(x0 + x + lane);
+                    const int page = p.page_table[(size_t)it.b * p.max_pages + (int)(t / p.page_rows)];
+                    if (page < 0 || page >= p.num_pages) {
+                        set_status(p.dev_status, CARAT_DEV_BAD_CACHE_ID);
+                        row_held = -1;
+                    } else {
+                        row_held = page * p.page_rows + (int)(t % p.page_rows);
+                    }
                 }
+            };
+            auto load = [&](bool is_v, int row, int part) {
+                const int s = cnt % NS;
+                if (cnt >= NS && alive)
+                    alive = warp_wait(&sh->empty[s], ((cnt / NS) & 1) ^ 1, abort_flag, p.dev_status);
+                if (!alive) return;
+                if (lane == 0) {
+                    if (rank == 0) tc::mbar_arrive_expect_tx(&sh->full[s], 2 * kStage);
+                    const uint32_t bar = tc::map_to_rank(&sh->full[s], 0);
+                    // a page outside the pool: rows behind the tensor's end read as zeros
+                    const int at =
+                        row < 0 ? p.num_pages * p.page_rows : row + (is_v ? 0 : rank * 64);
+                    if (is_v)
+                        tc::tma_load_4d_pair(smem + s * kStage, &map_v, 0, at, it.vh * 4 + rank * 2,
+                                             it.c, bar);
+                    else
+                        tc::tma_load_4d_pair(smem + s * kStage, &map_k, 0, at, part * 4, it.c, bar);
+                }
+                ++cnt;
+            };
+            int prev = 0;
+            for (int x = 0; x <= n && alive; ++x) {
+                int row = 0;
+                if (x < n) {
+                    if ((x & 31) == 0) fetch(x);
+                    row = __shfl_sync(kFull, row_held, x & 31);
+                    for (int k = 0; k < KST; ++k) load(false, row, k);
+                }
+                if (x == 0 && alive) {
+                    // the queries' place is free when the last item's last scores are computed
+                    if (items > 0)
+                        alive = warp_wait(&sh->q_empty, (items - 1) & 1, abort_flag, p.dev_status);
+                    if (alive && lane == 0) {
+                        if (rank == 0) tc::mbar_arrive_expect_tx(&sh->q_full, 2 * (D / 64) * q_bytes);
+                        const uint32_t bar = tc::map_to_rank(&sh->q_full, 0);
+                        for (int i = 0; i < D / 64; ++i)
+                            tc::tma_load_4d_pair(s_q + i * L::kSlab, &map_q, i * 64, it.c * p.group,
+                                                 it.j0 + rank * plan.tokens, it.b, bar);
+                    }
+                    if (alive) ++items;
+                }
+                if (x > 0) load(true, prev, 0);
+                prev = row;
             }
-        };
-        auto load = [&](bool is_v, int row, int part) {
-            const int s = cnt % NS;
-            if (cnt >= NS && alive)
-                alive = warp_wait(&sh->empty[s], ((cnt / NS) & 1) ^ 1, abort_flag, p.dev_status);
-            if (!alive) return;
-            if (lane == 0) {
-                if (rank == 0) tc::mbar_arrive_expect_tx(&sh->full[s], 2 * kStage);
-                const uint32_t bar = tc::map_to_rank(&sh->full[s], 0);
-                // a page outside the pool: rows behind the tensor's end read as zeros
-                const int at = row < 0 ? p.num_pages * p.page_rows : row + (is_v ? 0 : rank * 64);
-                if (is_v)
-                    tc::tma_load_4d_pair(smem + s * kStage, &map_v, 0, at, vh * 4 + rank * 2, c, bar);
-                else
-                    tc::tma_load_4d_pair(smem + s * kStage, &map_k, 0, at, part * 4, c, bar);
-            }
-            ++cnt;
-        };
-        int prev = 0;
-        for (int x = 0; x <= n && alive; ++x) {
-            int row = 0;
-            if (x < n) {
-                if ((x & 31) == 0) fetch(x);
-                row = row_of(x);
-                for (int k = 0; k < KST; ++k) load(false, row, k);
-            }
-            if (x > 0) load(true, prev, 0);
-            prev = row;
         }
         if (!alive && rank == 0) {
             // let what both CTAs' copies still carry land before anyone leaves
+            if (items > 0) tc::mbar_wait(&sh->q_full, (items - 1) & 1);
             for (uint32_t i = cnt > NS ? cnt - NS : 0; i < cnt; ++i)
                 tc::mbar_wait(&sh->full[i % NS], (i / NS) & 1);
         }
     } else if (warp == 1 && rank == 0) {
         // ---------------------------------------------------------------- products
-        const bool negative = p.scale_log2 < 0.f;
         const uint32_t id_qk = tc::idesc_bf16_f32(256, kKeys, false, false) |
-                               (negative ? 1u << 13 : 0u);   // negates A
+                               (p.scale_log2 < 0.f ? 1u << 13 : 0u);   // negates A
         constexpr uint32_t id_pv = tc::idesc_bf16_f32(256, kDV, false, true);
         const uint32_t q_addr = tc::smem_u32(s_q), st_addr = tc::smem_u32(smem);
-        uint32_t cnt = 0;
-        bool alive = warp_wait(&sh->q_full, 0, abort_flag, p.dev_status);
-        for (int x = 0; x <= n && alive; ++x) {
-            if (x < n) {
-                for (int k = 0; k < KST && alive; ++k, ++cnt) {
-                    const int s = cnt % NS;
-                    alive = warp_wait(&sh->full[s], (cnt / NS) & 1, abort_flag, p.dev_status);
-                    if (!alive) break;
-                    tc::tc_fence_after();
+        uint32_t cnt = 0, items = 0, g = 0;   // stages, items, tiles before this item's
+        bool alive = true;
+        Items walk;
+        Item it;
+        while (alive && walk.next(p, plan, lane, pair, it)) {
+            const Keys keys = keys_of(it);
+            const int x0 = split_at(keys.count, it.split, plan.splits);
+            const int n = split_at(keys.count, it.split + 1, plan.splits) - x0;
+            if (n == 0) continue;
+            alive = warp_wait(&sh->q_full, items & 1, abort_flag, p.dev_status);
+            ++items;
+            for (int x = 0; x <= n && alive; ++x) {
+                if (x < n) {
+                    const uint32_t buf = (g + x) & 1;
+                    for (int k = 0; k < KST; ++k, ++cnt) {
+                        const int s = cnt % NS;
+                        alive = warp_wait(&sh->full[s], (cnt / NS) & 1, abort_flag, p.dev_status);
+                        if (!alive) break;
+                        tc::tc_fence_after();
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const uint32_t off = (i & 3) * 32;
-                        tc::mma_bf16_ss_pair(
-                            t_s + (x & 1) * kKeys,
-                            tc::sdesc_sw128(q_addr + (k * 4 + i / 4) * L::kSlab + off, 16, 1024),
-                            tc::sdesc_sw128(st_addr + s * kStage + i / 4 * 8192 + off, 16, 1024),
-                            id_qk, k > 0 || i > 0);
+                        for (int i = 0; i < 16; ++i) {
+                            const uint32_t off = (i & 3) * 32;
+                            tc::mma_bf16_ss_pair(
+                                t_s + buf * kKeys,
+                                tc::sdesc_sw128(q_addr + (k * 4 + i / 4) * L::kSlab + off, 16, 1024),
+                                tc::sdesc_sw128(st_addr + s * kStage + i / 4 * 8192 + off, 16, 1024),
+                                id_qk, k > 0 || i > 0);
+                        }
+                        tc::mma_commit_pair(&sh->empty[s]);
                     }
-                    tc::mma_commit_pair(&sh->empty[s]);
+                    if (!alive) break;
+                    tc::mma_commit_pair(&sh->s_full[buf]);
+                    if (x == n - 1) tc::mma_commit_pair(&sh->q_empty);
+                }
+                if (x == 0) continue;
+                const int y = x - 1, s = cnt % NS;
+                const uint32_t buf = (g + y) & 1;
+                alive = warp_wait(&sh->full[s], (cnt / NS) & 1, abort_flag, p.dev_status);
+                if (!alive) break;
+                const uint32_t phase = ((g + y) >> 1) & 1;
+                if (keys.masked(p, keys.base(x0 + y))) {
+                    if (lane == 0) {
+                        tc::mbar_arrive_cluster(tc::map_to_rank(&sh->v_ready, 0));
+                        tc::mbar_arrive_cluster(tc::map_to_rank(&sh->v_ready, 1));
+                    }
+                    __syncwarp();
+                    alive = warp_wait<true>(&sh->p_full[buf], phase, abort_flag, p.dev_status);
+                } else {
+                    alive = warp_wait(&sh->p_full[buf], phase, abort_flag, p.dev_status);
                 }
                 if (!alive) break;
-                tc::mma_commit_pair(&sh->s_full[x & 1]);
-            }
-            if (x == 0) continue;
-            const int y = x - 1, s = cnt % NS;
-            alive = warp_wait(&sh->full[s], (cnt / NS) & 1, abort_flag, p.dev_status);
-            if (!alive) break;
-            if (keys.masked(p, keys.base(x0 + y)) && lane == 0) {
-                tc::mbar_arrive_cluster(tc::map_to_rank(&sh->v_ready, 0));
-                tc::mbar_arrive_cluster(tc::map_to_rank(&sh->v_ready, 1));
-            }
-            __syncwarp();
-            alive = warp_wait(&sh->p_full[y & 1], (y / 2) & 1, abort_flag, p.dev_status);
-            if (!alive) break;
-            tc::tc_fence_after();
+                tc::tc_fence_after();
 #pragma unroll
-            for (int i = 0; i < kKeys / 16; ++i)
-                tc::mma_bf16_ts_pair(t_o, t_s + (y & 1) * kKeys + i * 8,
-                                     tc::sdesc_sw128(st_addr + s * kStage + i * 2048, 16384, 1024),
-                                     id_pv, y > 0 || i > 0);
-            tc::mma_commit_pair(&sh->empty[s]);
-            tc::mma_commit_pair(&sh->pv_done);
-            ++cnt;
+                for (int i = 0; i < kKeys / 16; ++i)
+                    tc::mma_bf16_ts_pair(t_o, t_s + buf * kKeys + i * 8,
+                                         tc::sdesc_sw128(st_addr + s * kStage + i * 2048, 16384, 1024),
+                                         id_pv, y > 0 || i > 0);
+                tc::mma_commit_pair(&sh->empty[s]);
+                tc::mma_commit_pair(&sh->pv_done);
+                ++cnt;
+            }
+            g += n;
         }
         if (!alive) {
             tc::mma_commit_pair(&sh->drain);
@@ -384,194 +474,225 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         }
     } else if (warp >= 4) {
         // ---------------------------------------------------------------- softmax
-        const int row = threadIdx.x - 128;              // TMEM lane
-        const uint32_t quad = (uint32_t)(warp - 4) << 21;
-        const int j = mine + row / p.group, h = c * p.group + row % p.group;
-        const bool valid = row < plan.tokens * p.group && j < rq.n;
-        const long long pos = rq.ctx + j;
+        const int part = (warp - 4) / 4, quad = warp % 4;   // keys 64 part .. of a tile; lanes
+        const int row = quad * 32 + lane;                   // TMEM lane
+        const uint32_t lanes = (uint32_t)quad << 21;
+        const int token = row / p.group;
         // the sign of the scale is in the product's descriptor; 0 would turn -inf into NaN
         const float scale = fmaxf(fabsf(p.scale_log2), FLT_MIN);
-        float m = -INFINITY, l = 0.f;
-        int masked_tiles = 0;
-        bool alive = true;
-        for (int x = 0; x < n && alive; ++x) {
-            alive = warp_wait(&sh->s_full[x & 1], (x / 2) & 1, abort_flag, p.dev_status);
-            if (!alive) break;
-            tc::tc_fence_after();
-            const uint32_t t_x = t_s + (x & 1) * kKeys + quad;
-            uint32_t s[kKeys];
-#pragma unroll
-            for (int i = 0; i < kKeys; i += 32) tc::tmem_ld32(t_x + i, s + i);
-            tc::tmem_ld_wait();
-            const long long t0 = keys.base(x0 + x);
-            const bool masked = keys.masked(p, t0);
-            if (masked) {
-                const int hi = within(pos - t0);
-                const int lo = p.window > 0 ? within(pos - p.window + 1 - t0) : -1;
-                const int sk = within(p.sinks - t0);
-#pragma unroll
-                for (int i = 0; i < kKeys; ++i)
-                    if (i > hi || (i < lo && i >= sk)) s[i] = 0xff800000u;
-            }
-            float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-            for (int i = 0; i < kKeys; ++i) top[i & 3] = fmaxf(top[i & 3], __uint_as_float(s[i]));
-            const float tm = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * scale;
-            const bool grow = tm > m + kSlack || (m == -INFINITY && tm > m);
-            if (__any_sync(kFull, grow)) {
-                const float m_new = grow ? tm : m;
-                const float f = m == m_new ? 1.f : fast_exp2(m - m_new);
-                m = m_new;
-                l *= f;
-                if (x > 0) {
-                    alive = warp_wait(&sh->pv_done, (x - 1) & 1, abort_flag, p.dev_status);
-                    if (!alive) break;
-                    tc::tc_fence_after();
-#pragma unroll 1
-                    for (int i = 0; i < kDV; i += 32) {
-                        uint32_t o[32];
-                        tc::tmem_ld32(t_o + quad + i, o);
-                        tc::tmem_ld_wait();
-#pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                        tc::tmem_st32(t_o + quad + i, o);
-                    }
-                    tc::tmem_st_wait();
-                }
-            }
-            const float ref = m == -INFINITY ? 0.f : m;
-            float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int i = 0; i < kKeys; i += 2) {
-                const float a = fast_exp2(fmaf(__uint_as_float(s[i]), scale, -ref));
-                const float d = fast_exp2(fmaf(__uint_as_float(s[i + 1]), scale, -ref));
-                const uint32_t w = pack_bf16(a, d);
-                s[i / 2] = w;
-                sum[i / 2 & 3] += bf16lo(w) + bf16hi(w);
-            }
-            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-            tc::tmem_st32(t_x, s);
-            tc::tmem_st32(t_x + 32, s + 32);
-            tc::tmem_st_wait();
-            if (masked) {
-                // V rows that not every row of the pair sees: nothing that is not finite
-                // may meet a weight of 0.  Thread t looks through key t.
-                alive = warp_wait(&sh->v_ready, masked_tiles & 1, abort_flag, p.dev_status);
-                if (!alive) break;
-                // stages in order: K(0), K(1) V(0), K(2) V(1), ..., V(n - 1)
-                const int stage = ((x + 1 < n ? x + 2 : n) * KST + x) % NS;
-                uint8_t *v_row = smem + stage * kStage + row * 128;
-                bool bad = false;
-                const bool stale = t0 + row > keys.hi;
-                if (!stale) {
-                    __nv_bfloat162 acc = __float2bfloat162_rn(0.f);
-                    const __nv_bfloat162 zero = __float2bfloat162_rn(0.f);
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const uint4 v = *reinterpret_cast<const uint4 *>(
-                            v_row + (i >> 3) * 16384 + ((i + row) & 7) * 16);
-                        acc = __hfma2(*reinterpret_cast<const __nv_bfloat162 *>(&v.x), zero, acc);
-                        acc = __hfma2(*reinterpret_cast<const __nv_bfloat162 *>(&v.y), zero, acc);
-                        acc = __hfma2(*reinterpret_cast<const __nv_bfloat162 *>(&v.z), zero, acc);
-                        acc = __hfma2(*reinterpret_cast<const __nv_bfloat162 *>(&v.w), zero, acc);
-                    }
-                    bad = __hisnan(acc.x) || __hisnan(acc.y);
-                }
-                if (bad || stale) {
-#pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        *reinterpret_cast<uint4 *>(v_row + (i >> 3) * 16384 + (i & 7) * 16) =
-                            make_uint4(0, 0, 0, 0);
-                    tc::fence_proxy_async_smem();
-                }
-                const uint32_t mask = __ballot_sync(kFull, bad);
-                if (lane == 0) {
-                    sh->tile_base[masked_tiles] = (int)t0;
-                    if (mask) {
-                        for (int r = 0; r < 2; ++r) {
-                            tc::st_cluster_u32(tc::map_to_rank(&sh->bad[masked_tiles][rank][warp - 4], r),
-                                               mask);
-                            tc::st_cluster_u32(tc::map_to_rank(&sh->poison, r), 1);
-                        }
-                    }
-                }
-                ++masked_tiles;
-            }
-            tc::tc_fence_before();
-            __syncwarp();
-            if (lane == 0) tc::mbar_arrive_cluster(tc::map_to_rank(&sh->p_full[x & 1], 0));
+        // requests rejected on the device
+        for (int b = pair; b < p.batch; b += plan.pairs) {
+            if (request_ok(p, load_request(p, b))) continue;
+            if (threadIdx.x == 128 && rank == 0) set_status(p.dev_status, CARAT_DEV_BAD_CONTEXT);
+            uint4 *o = reinterpret_cast<uint4 *>(p.out + (size_t)b * p.k * p.q_heads * D);
+            const size_t count = (size_t)p.k * p.q_heads * (D / 8);
+            for (size_t i = rank * kSoftmax + threadIdx.x - 128; i < count; i += 2 * kSoftmax)
+                o[i] = make_uint4(0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu);
         }
-        // The last scores say that the product two tiles before is done, no more: a wait for
-        // the last product alone could pass on that one's phase, which has its parity.
-        if (alive && n > 1) alive = warp_wait(&sh->pv_done, n & 1, abort_flag, p.dev_status);
-        if (alive) alive = warp_wait(&sh->pv_done, (n - 1) & 1, abort_flag, p.dev_status);
-        softmax_barrier();
-        if (alive && !*abort_flag) {
-            tc::tc_fence_after();
-            bool poisoned = false;
-            if (*(volatile int *)&sh->poison) {
-                for (int i = 0; i < masked_tiles; ++i)
-                    for (int w = 0; w < 4; ++w)
-                        for (uint32_t bits = sh->bad[i][0][w] | sh->bad[i][1][w]; bits; bits &= bits - 1) {
-                            const long long t = (long long)sh->tile_base[i] + w * 32 + __ffs(bits) - 1;
-                            poisoned |= t <= pos && (p.window == 0 || t > pos - p.window || t < p.sinks);
-                        }
+        uint32_t g = 0, cnt = 0, vcnt = 0;   // tiles, stages, masked tiles before this item's
+        int turn = 0;                        // which third of the poison records
+        bool alive = true;
+        Items walk;
+        Item it;
+        while (alive && walk.next(p, plan, lane, pair, it)) {
+            const Keys keys = keys_of(it);
+            const int x0 = split_at(keys.count, it.split, plan.splits);
+            const int n = split_at(keys.count, it.split + 1, plan.splits) - x0;
+            if (n == 0) continue;
+            const int j = it.j0 + rank * plan.tokens + token;
+            const long long pos = it.ctx + j;
+            float m = -INFINITY, l = 0.f;
+            int masked_tiles = 0;
+            if (warp == 4) {   // the records of the item after this one
+                const int after = turn == 2 ? 0 : turn + 1;
+                (&sh->bad[after][0][0])[lane] = 0;
+                if (lane == 0) sh->poison[after] = 0;
             }
-            // 128 bytes of each of the warp's 32 rows at a time through shared memory (Q's,
-            // which no product reads any more), so that a row leaves as whole lines
-            uint8_t *stage = s_q + (warp - 4) * 4096;
+            for (int x = 0; x < n; ++x) {
+                const uint32_t buf = (g + x) & 1;
+                alive = alive && warp_wait(&sh->s_full[buf], ((g + x) >> 1) & 1, abort_flag,
+                                           p.dev_status);
+                tc::tc_fence_after();
+                const uint32_t t_x = t_s + buf * kKeys + lanes;
+                uint32_t s[64];
+                tc::tmem_ld32(t_x + part * 64, s);
+                tc::tmem_ld32(t_x + part * 64 + 32, s + 32);
+                tc::tmem_ld_wait();
+                const long long t0 = keys.base(x0 + x);
+                const bool masked = keys.masked(p, t0);
+                if (masked) {
+                    const long long first = t0 + part * 64;
+                    const int hi = within(pos - first);
+                    const int lo = p.window > 0 ? within(pos - p.window + 1 - first) : -1;
+                    const int sk = within(p.sinks - first);
+#pragma unroll
+                    for (int i = 0; i < 64; ++i)
+                        if (i > hi || (i < lo && i >= sk)) s[i] = 0xff800000u;
+                }
+                float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                for (int i = 0; i < 64; ++i) top[i & 3] = fmaxf(top[i & 3], __uint_as_float(s[i]));
+                const float own = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+                // After this barrier both threads of a row hold their scores, so the weights
+                // may take their place.
+                sh->row[buf][part][row] = own;
+                if (rows_barrier(quad, !alive)) {
+                    alive = false;
+                    break;
+                }
+                const float tm = fmaxf(own, sh->row[buf][part ^ 1][row]) * scale;
+                const bool grow = tm > m + kSlack;
+                if (__any_sync(kFull, grow)) {
+                    const float m_new = grow ? tm : m;
+                    const float f = m == m_new ? 1.f : fast_exp2(m - m_new);
+                    m = m_new;
+                    l *= f;
+                    if (x > 0) {
+                        // each of the two warps scales half of the columns
+                        alive = warp_wait(&sh->pv_done, (g + x - 1) & 1, abort_flag, p.dev_status);
+                        tc::tc_fence_after();
+#pragma unroll 1
+                        for (int i = part * (kDV / 2); i < (part + 1) * (kDV / 2); i += 32) {
+                            uint32_t o[32];
+                            tc::tmem_ld32(t_o + lanes + i, o);
+                            tc::tmem_ld_wait();
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                            tc::tmem_st32(t_o + lanes + i, o);
+                        }
+                        tc::tmem_st_wait();
+                    }
+                }
+                const float ref = m == -INFINITY ? 0.f : m;
+                float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int i = 0; i < 64; i += 2) {
+                    const float a = fast_exp2(fmaf(__uint_as_float(s[i]), scale, -ref));
+                    const float d = fast_exp2(fmaf(__uint_as_float(s[i + 1]), scale, -ref));
+                    const uint32_t w = pack_bf16(a, d);
+                    s[i / 2] = w;
+                    sum[i / 2 & 3] += bf16lo(w) + bf16hi(w);
+                }
+                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                tc::tmem_st32(t_x + part * 32, s);
+                tc::tmem_st_wait();
+                if (masked) {
+                    // V rows that not every row of the pair sees: nothing that is not finite
+                    // may meet a weight of 0.  Two threads look through a key's row.
+                    alive = alive &&
+                            warp_wait<true>(&sh->v_ready, vcnt & 1, abort_flag, p.dev_status);
+                    // stages in order: K(0), K(1) V(0), K(2) V(1), ..., V(n - 1)
+                    const uint32_t stage = (cnt + (x + 1 < n ? x + 2 : n) * KST + x) % NS;
+                    uint8_t *v_row = smem + stage * kStage + part * 16384 + row * 128;
+                    const bool stale = t0 + row > keys.hi;
+                    bool bad = false;
+                    if (!stale) {
+                        __nv_bfloat162 acc = __float2bfloat162_rn(0.f);
+                        const __nv_bfloat162 zero = __float2bfloat162_rn(0.f);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const uint4 v =
+                                *reinterpret_cast<const uint4 *>(v_row + ((i + row) & 7) * 16);
+                            acc = __hfma2(*reinterpret_cast<const __nv_bfloat162 *>(&v.x), zero, acc);
+                            acc = __hfma2(*reinterpret_cast<const __nv_bfloat162 *>(&v.y), zero, acc);
+                            acc = __hfma2(*reinterpret_cast<const __nv_bfloat162 *>(&v.z), zero, acc);
+                            acc = __hfma2(*reinterpret_cast<const __nv_bfloat162 *>(&v.w), zero, acc);
+                        }
+                        bad = __hisnan(acc.x) || __hisnan(acc.y);
+                    }
+                    if (bad || stale) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            *reinterpret_cast<uint4 *>(v_row + i * 16) = make_uint4(0, 0, 0, 0);
+                        tc::fence_proxy_async_smem();
+                    }
+                    const uint32_t mask = __ballot_sync(kFull, bad);
+                    if (mask && lane == 0) {
+                        for (int r = 0; r < 2; ++r) {
+                            tc::or_cluster_u32(
+                                tc::map_to_rank(&sh->bad[turn][masked_tiles][quad], r), mask);
+                            tc::or_cluster_u32(tc::map_to_rank(&sh->poison[turn], r), 1);
+                        }
+                    }
+                    ++masked_tiles;
+                    ++vcnt;
+                }
+                tc::tc_fence_before();
+                __syncwarp();
+                if (alive && lane == 0) {
+                    const uint32_t bar = tc::map_to_rank(&sh->p_full[buf], 0);
+                    if (masked)
+                        tc::mbar_arrive_cluster(bar);
+                    else
+                        tc::mbar_arrive_remote(bar);
+                }
+            }
+            if (!alive) break;
+            g += n;
+            cnt += n * (KST + 1);
+            // The last scores say that the product two tiles before is done, no more: a wait
+            // for the last product alone could pass on that one's phase, which has its parity.
+            if (g > 1) alive = alive && warp_wait(&sh->pv_done, g & 1, abort_flag, p.dev_status);
+            alive = alive && warp_wait<true>(&sh->pv_done, (g - 1) & 1, abort_flag, p.dev_status);
+            // the last tile's place: the next tile's may be written before the other has read
+            sh->row[(g - 1) & 1][part][row] = l;
+            if (rows_barrier(quad, !alive)) {
+                alive = false;
+                break;
+            }
+            tc::tc_fence_after();
+            l += sh->row[(g - 1) & 1][part ^ 1][row];
+            bool poisoned = false;
+            if (*(volatile uint32_t *)&sh->poison[turn]) {
+                for (int x = 0, i = 0; x < n; ++x) {
+                    const long long t0 = keys.base(x0 + x);
+                    if (!keys.masked(p, t0)) continue;
+                    for (int w = 0; w < 4; ++w)
+                        for (uint32_t bits = sh->bad[turn][i][w]; bits; bits &= bits - 1) {
+                            const long long t = t0 + w * 32 + __ffs(bits) - 1;
+                            poisoned |=
+                                t <= pos && (p.window == 0 || t > pos - p.window || t < p.sinks);
+                        }
+                    ++i;
+                }
+            }
+            turn = turn == 2 ? 0 : turn + 1;
+            const bool valid = token < plan.tokens && j < it.n;
+            const size_t at = ((size_t)it.b * p.k + j) * p.q_heads + it.c * p.group + row % p.group;
             const bool partial = plan.splits > 1;
             const float f = poisoned ? NAN : partial ? 1.f : 1.f / l;
-            const size_t out_row = ((size_t)b * p.k + j) * p.q_heads + h;
-            if (partial && valid && vh == 0)
-                plan.part_ml[out_row * plan.splits + split] = make_float2(m, l);
+            if (partial && valid && it.vh == 0 && part == 0)
+                plan.part_ml[at * plan.splits + it.split] = make_float2(m, l);
+            // a thread writes half of its row
 #pragma unroll 1
-            for (int i = 0; i < kDV; i += 64) {
-                uint32_t o[64];
-                tc::tmem_ld32(t_o + quad + i, o);
-                tc::tmem_ld32(t_o + quad + i + 32, o + 32);
+            for (int i = part * (kDV / 2); i < (part + 1) * (kDV / 2); i += 32) {
+                uint32_t o[32];
+                tc::tmem_ld32(t_o + lanes + i, o);
                 tc::tmem_ld_wait();
 #pragma unroll
-                for (int e = 0; e < 64; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                if (!valid) continue;
+                if (partial) {
+                    uint4 *to = reinterpret_cast<uint4 *>(
+                        plan.part_o + (at * plan.splits + it.split) * D + it.vh * kDV + i);
 #pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    if (!partial && half) break;
-                    __syncwarp();
+                    for (int e = 0; e < 8; ++e)
+                        to[e] = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                } else {
+                    uint4 *to = reinterpret_cast<uint4 *>(p.out + at * D + it.vh * kDV + i);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        uint4 v;
-                        if (partial) {
-                            const uint32_t *from = o + half * 32 + e * 4;
-                            v = make_uint4(from[0], from[1], from[2], from[3]);
-                        } else {
-                            uint32_t w[4];
+                    for (int e = 0; e < 4; ++e) {
+                        uint32_t w[4];
 #pragma unroll
-                            for (int z = 0; z < 4; ++z)
-                                w[z] = pack_bf16(__uint_as_float(o[e * 8 + 2 * z]),
-                                                 __uint_as_float(o[e * 8 + 2 * z + 1]));
-                            v = make_uint4(w[0], w[1], w[2], w[3]);
-                        }
-                        *reinterpret_cast<uint4 *>(stage + lane * 128 + ((e ^ lane) & 7) * 16) = v;
-                    }
-                    __syncwarp();
-                    for (int r8 = 0; r8 < 32; r8 += 4) {
-                        const int r = r8 + lane / 8, e = lane % 8;
-                        const uint4 v = *reinterpret_cast<const uint4 *>(
-                            stage + r * 128 + ((e ^ r) & 7) * 16);
-                        const int rr = (warp - 4) * 32 + r;
-                        const int jj = mine + rr / p.group;
-                        if (rr >= plan.tokens * p.group || jj >= rq.n) continue;
-                        const size_t at =
-                            ((size_t)b * p.k + jj) * p.q_heads + c * p.group + rr % p.group;
-                        if (partial)
-                            *reinterpret_cast<uint4 *>(plan.part_o + (at * plan.splits + split) * D +
-                                                       vh * kDV + i + half * 32 + e * 4) = v;
-                        else
-                            *reinterpret_cast<uint4 *>(p.out + at * D + vh * kDV + i + e * 8) = v;
+                        for (int z = 0; z < 4; ++z)
+                            w[z] = pack_bf16(__uint_as_float(o[e * 8 + 2 * z]),
+                                             __uint_as_float(o[e * 8 + 2 * z + 1]));
+                        to[e] = make_uint4(w[0], w[1], w[2], w[3]);
                     }
                 }
             }
+            tc::tc_fence_before();
         }
     }
     tc::tc_fence_before();
@@ -625,19 +746,18 @@ size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
 struct Sizes {
     Plan plan;
-    long long items;    // CTA pairs
     size_t ml, total;
 };
 
 Sizes sizes_of(int batch, int k, int q_heads, int kv_heads, int head_dim) {
     Sizes z{};
-    const int group = q_heads / kv_heads;
-    z.plan.tokens = kRows / group;
-    z.plan.tiles = (k + 2 * z.plan.tokens - 1) / (2 * z.plan.tokens);
+    z.plan.tokens = kRows / (q_heads / kv_heads);
     z.plan.halves = head_dim / kDV;
-    z.items = (long long)batch * kv_heads * z.plan.tiles * z.plan.halves;
+    const int tiles = (k + 2 * z.plan.tokens - 1) / (2 * z.plan.tokens);
+    const long long items = (long long)batch * kv_heads * tiles * z.plan.halves;
     const int pairs = device_sm_count() / 2;
-    z.plan.splits = z.items > 0 && z.items <= pairs / 2 ? (int)(pairs / z.items) : 1;
+    z.plan.splits = items > 0 && items <= pairs / 2 ? (int)(pairs / items) : 1;
+    z.plan.pairs = (int)std::min<long long>(items * z.plan.splits, pairs);
     if (z.plan.splits > 1) {
         const size_t rows = (size_t)batch * k * q_heads * z.plan.splits;
         z.ml = align256(rows * sizeof(float2));
@@ -675,7 +795,7 @@ cudaError_t launch(const PagedChunkParams &p, Sizes &z, cudaStream_t stream) {
         if (e != cudaSuccess) return e;
         if (dev >= 0 && dev < 64) configured[dev].store(1, std::memory_order_release);
     }
-    e = launch_dependent(kernel, dim3((unsigned)(z.items * z.plan.splits * 2)), dim3(kThreads),
+    e = launch_dependent(kernel, dim3(2 * z.plan.pairs), dim3(kThreads),
                          L::kAlloc, stream, p, z.plan, map_q, map_k, map_v);
     if (e != cudaSuccess || z.plan.splits == 1) return e;
     return launch_dependent(paged_chunk_merge_kernel<D>,
