@@ -89,9 +89,10 @@ struct Shared {
     uint64_t q_full;        // leader
     uint64_t q_empty;       // both: an item's last scores are computed
     uint64_t s_full[2];     // both: a tile's scores are in tensor memory
-    uint64_t p_full[2];     // leader: its weights are, and V is looked through
+    uint64_t p_full[2];     // leader: its weights are
     uint64_t pv_done;       // both: a tile's value product is done
     uint64_t v_ready;       // both: a masked tile's V has landed
+    uint64_t v_clean;       // leader: it is looked through
     uint64_t drain;
     uint32_t tmem;
     int abort_flag;
@@ -125,39 +126,39 @@ struct Plan {
     float *part_o;   // [B k Hq][splits][D]
 };
 
-// Key tiles of the rows at positions [lo, hi]: the sinks', then the window's.
+// Key tiles of the rows at positions [lo, hi]: the sinks', then the window's.  Positions
+// are below 2^31 (a request's capacity).
 struct Keys {
-    long long lo, hi;
-    long long first;
+    int lo, hi;
+    int first;              // the window's first tile
     int sink_tiles, count;
 
-    __device__ __forceinline__ Keys(const PagedChunkParams &p, long long lo_, long long hi_)
+    __device__ __forceinline__ Keys(const PagedChunkParams &p, int lo_, int hi_)
         : lo(lo_), hi(hi_) {
         first = p.window > 0 && lo - p.window + 1 > 0 ? (lo - p.window + 1) / kKeys : 0;
-        const long long s = p.window > 0 ? ((long long)p.sinks + kKeys - 1) / kKeys : 0;
-        sink_tiles = (int)(s < first ? s : first);
-        count = sink_tiles + (int)(hi / kKeys - first) + 1;
+        sink_tiles = p.window > 0 && p.sinks > 0 ? min((p.sinks - 1) / kKeys + 1, first) : 0;
+        count = sink_tiles + hi / kKeys - first + 1;
     }
-    __device__ __forceinline__ long long base(int x) const {
+    __device__ __forceinline__ int base(int x) const {
         return (x < sink_tiles ? x : first + x - sink_tiles) * kKeys;
     }
     // whether some row sees some key of the tile at t0 and not another
-    __device__ __forceinline__ bool masked(const PagedChunkParams &p, long long t0) const {
-        if (t0 + kKeys - 1 > lo) return true;
-        return p.window > 0 && t0 <= hi - p.window && t0 + kKeys > p.sinks;
+    __device__ __forceinline__ bool masked(const PagedChunkParams &p, int t0) const {
+        if (t0 + (kKeys - 1) > lo) return true;
+        return p.window > 0 && t0 <= hi - p.window && t0 + (kKeys - 1) >= p.sinks;
     }
 };
 
 // Pieces of `count` tiles: split s takes [count s / splits, count (s + 1) / splits).
+// (Fewer than 2^24 tiles, fewer splits than SMs: the product fits 32 bits.)
 __device__ __forceinline__ int split_at(int count, int s, int splits) {
-    return (int)((long long)count * s / splits);
+    return splits == 1 ? count * s : (int)((uint32_t)count * (uint32_t)s / (uint32_t)splits);
 }
 
 // One pair's share of a request's chunk for one KV head.
 struct Item {
     int b, c, vh, split;
-    int j0, n;             // the pair's first token; the request's tokens
-    long long ctx;
+    int j0, n, ctx;        // the pair's first token; the request's tokens, and before them
 };
 
 // The items of this pair, in order: the same for every warp that walks them (whole warps).
@@ -166,8 +167,7 @@ struct Items {
     int base = -32;        // first request held
     int upto = 0;          // items of the held requests up to this lane's, and before
     int before = 0;        // items before the held requests
-    int n = 0, tiles = 0;  // this lane's request
-    long long ctx = 0;
+    int n = 0, tiles = 0, ctx = 0;   // this lane's request
     int round = 0;
 
     __device__ __forceinline__ bool next(const PagedChunkParams &p, const Plan &plan, int lane,
@@ -199,7 +199,7 @@ struct Items {
             tiles = 0;
             if (base + lane < p.batch) {
                 const Request rq = load_request(p, base + lane);
-                ctx = rq.ctx;
+                ctx = (int)rq.ctx;
                 n = rq.n;
                 if (request_ok(p, rq)) tiles = (n + 2 * plan.tokens - 1) / (2 * plan.tokens);
             }
@@ -250,9 +250,9 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     return d;
 }
 
-// An offset into a tile, held within [-1, kKeys].
-__device__ __forceinline__ int within(long long x) {
-    return (int)(x < -1 ? -1 : x > kKeys ? kKeys : x);
+// Bits [0, n) of 64, any n.
+__device__ __forceinline__ uint64_t low_bits(int n) {
+    return n >= 64 ? ~0ull : n <= 0 ? 0ull : (1ull << n) - 1ull;
 }
 
 // The two warps that share 32 rows meet; whether one of them has to stop, so that both do.
@@ -301,6 +301,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         for (int i = 0; i < 3; ++i) sh->poison[i] = 0;
         tc::mbar_init(&sh->pv_done, 1);
         tc::mbar_init(&sh->v_ready, 1);
+        tc::mbar_init(&sh->v_clean, 4);
         tc::mbar_init(&sh->drain, 1);
         tc::fence_mbar_init();
         sh->abort_flag = 0;
@@ -330,8 +331,11 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         bool alive = true;
         const uint32_t q_bytes = plan.tokens * p.group * 128;
         Items walk;
-        Item it;
-        while (alive && walk.next(p, plan, lane, pair, it)) {
+        Item ahead;
+        bool more = walk.next(p, plan, lane, pair, ahead);
+        while (alive && more) {
+            const Item it = ahead;
+            more = walk.next(p, plan, lane, pair, ahead);   // known before it is needed
             const Keys keys = keys_of(it);
             const int x0 = split_at(keys.count, it.split, plan.splits);
             const int n = split_at(keys.count, it.split + 1, plan.splits) - x0;
@@ -339,13 +343,13 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
             int row_held = 0;   // lane l: pool row of the item's tile 32 * (x / 32) + l
             auto fetch = [&](int x) {
                 if (x + lane < n) {
-                    const long long t = keys.base(x0 + x + lane);
-                    const int page = p.page_table[(size_t)it.b * p.max_pages + (int)(t / p.page_rows)];
+                    const int t = keys.base(x0 + x + lane), at = t / p.page_rows;
+                    const int page = p.page_table[(size_t)it.b * p.max_pages + at];
                     if (page < 0 || page >= p.num_pages) {
                         set_status(p.dev_status, CARAT_DEV_BAD_CACHE_ID);
                         row_held = -1;
                     } else {
-                        row_held = page * p.page_rows + (int)(t % p.page_rows);
+                        row_held = page * p.page_rows + (t - at * p.page_rows);
                     }
                 }
             };
@@ -405,11 +409,14 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                                (p.scale_log2 < 0.f ? 1u << 13 : 0u);   // negates A
         constexpr uint32_t id_pv = tc::idesc_bf16_f32(256, kDV, false, true);
         const uint32_t q_addr = tc::smem_u32(s_q), st_addr = tc::smem_u32(smem);
-        uint32_t cnt = 0, items = 0, g = 0;   // stages, items, tiles before this item's
+        uint32_t cnt = 0, items = 0, g = 0, vcnt = 0;   // stages, items, tiles, masked tiles
         bool alive = true;
         Items walk;
-        Item it;
-        while (alive && walk.next(p, plan, lane, pair, it)) {
+        Item ahead;
+        bool more = walk.next(p, plan, lane, pair, ahead);
+        while (alive && more) {
+            const Item it = ahead;
+            more = walk.next(p, plan, lane, pair, ahead);   // known before it is needed
             const Keys keys = keys_of(it);
             const int x0 = split_at(keys.count, it.split, plan.splits);
             const int n = split_at(keys.count, it.split + 1, plan.splits) - x0;
@@ -447,14 +454,14 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                 const uint32_t phase = ((g + y) >> 1) & 1;
                 if (keys.masked(p, keys.base(x0 + y))) {
                     if (lane == 0) {
-                        tc::mbar_arrive_cluster(tc::map_to_rank(&sh->v_ready, 0));
-                        tc::mbar_arrive_cluster(tc::map_to_rank(&sh->v_ready, 1));
+                        tc::mbar_arrive_remote(tc::map_to_rank(&sh->v_ready, 0));
+                        tc::mbar_arrive_remote(tc::map_to_rank(&sh->v_ready, 1));
                     }
                     __syncwarp();
-                    alive = warp_wait<true>(&sh->p_full[buf], phase, abort_flag, p.dev_status);
-                } else {
-                    alive = warp_wait(&sh->p_full[buf], phase, abort_flag, p.dev_status);
+                    alive = warp_wait<true>(&sh->v_clean, vcnt & 1, abort_flag, p.dev_status);
+                    ++vcnt;
                 }
+                alive = alive && warp_wait(&sh->p_full[buf], phase, abort_flag, p.dev_status);
                 if (!alive) break;
                 tc::tc_fence_after();
 #pragma unroll
@@ -471,6 +478,84 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         if (!alive) {
             tc::mma_commit_pair(&sh->drain);
             tc::mbar_wait(&sh->drain, 0);
+        }
+    } else if (warp == 2 || warp == 3) {
+        // ---------------------------------------------------------------- V of masked tiles
+        // What not every row of the pair sees must be finite where it meets a weight of 0:
+        // rows of keys that hold something else, and rows behind the last key, are zeroed
+        // while the softmax of the tile runs.
+        uint32_t cnt = 0, vcnt = 0;   // stages, masked tiles before this item's
+        int turn = 0;
+        bool alive = true;
+        Items walk;
+        Item ahead;
+        bool more = walk.next(p, plan, lane, pair, ahead);
+        while (alive && more) {
+            const Item it = ahead;
+            more = walk.next(p, plan, lane, pair, ahead);
+            const Keys keys = keys_of(it);
+            const int x0 = split_at(keys.count, it.split, plan.splits);
+            const int n = split_at(keys.count, it.split + 1, plan.splits) - x0;
+            if (n == 0) continue;
+            if (warp == 2) {   // the records of the item after this one
+                const int after = turn == 2 ? 0 : turn + 1;
+                (&sh->bad[after][0][0])[lane] = 0;
+                if (lane == 0) sh->poison[after] = 0;
+            }
+            for (int x = 0, i = 0; x < n; ++x) {
+                const int t0 = keys.base(x0 + x);
+                if (!keys.masked(p, t0)) continue;
+                alive = warp_wait<true>(&sh->v_ready, vcnt & 1, abort_flag, p.dev_status);
+                if (!alive) break;
+                ++vcnt;
+                // stages in order: K(0), K(1) V(0), K(2) V(1), ..., V(n - 1)
+                const uint32_t stage = (cnt + (x + 1 < n ? x + 2 : n) * KST + x) % NS;
+                bool wrote = false;
+#pragma unroll 1
+                for (int w = warp - 2; w < 4; w += 2) {
+                    const int key = w * 32 + lane;
+                    uint8_t *v_row = smem + stage * kStage + key * 128;
+                    const bool stale = t0 + key > keys.hi;
+                    __nv_bfloat162 acc = __float2bfloat162_rn(0.f);
+                    const __nv_bfloat162 zero = __float2bfloat162_rn(0.f);
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        const uint4 v = *reinterpret_cast<const uint4 *>(
+                            v_row + (e >> 3) * 16384 + ((e + key) & 7) * 16);
+                        acc = __hfma2(*reinterpret_cast<const __nv_bfloat162 *>(&v.x), zero, acc);
+                        acc = __hfma2(*reinterpret_cast<const __nv_bfloat162 *>(&v.y), zero, acc);
+                        acc = __hfma2(*reinterpret_cast<const __nv_bfloat162 *>(&v.z), zero, acc);
+                        acc = __hfma2(*reinterpret_cast<const __nv_bfloat162 *>(&v.w), zero, acc);
+                    }
+                    const bool bad = !stale && (__hisnan(acc.x) || __hisnan(acc.y));
+                    if (bad || stale) {
+#pragma unroll
+                        for (int e = 0; e < 16; ++e)
+                            *reinterpret_cast<uint4 *>(v_row + (e >> 3) * 16384 + (e & 7) * 16) =
+                                make_uint4(0, 0, 0, 0);
+                        tc::fence_proxy_async_smem();
+                    }
+                    const uint32_t mask = __ballot_sync(kFull, bad);
+                    wrote |= __any_sync(kFull, bad || stale) != 0;
+                    if (mask && lane == 0) {
+                        for (int r = 0; r < 2; ++r) {
+                            tc::or_cluster_u32(tc::map_to_rank(&sh->bad[turn][i][w], r), mask);
+                            tc::or_cluster_u32(tc::map_to_rank(&sh->poison[turn], r), 1);
+                        }
+                    }
+                }
+                ++i;
+                __syncwarp();
+                if (lane == 0) {
+                    const uint32_t bar = tc::map_to_rank(&sh->v_clean, 0);
+                    if (wrote)
+                        tc::mbar_arrive_cluster(bar);
+                    else
+                        tc::mbar_arrive_remote(bar);
+                }
+            }
+            cnt += n * (KST + 1);
+            turn = turn == 2 ? 0 : turn + 1;
         }
     } else if (warp >= 4) {
         // ---------------------------------------------------------------- softmax
@@ -489,25 +574,22 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
             for (size_t i = rank * kSoftmax + threadIdx.x - 128; i < count; i += 2 * kSoftmax)
                 o[i] = make_uint4(0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu);
         }
-        uint32_t g = 0, cnt = 0, vcnt = 0;   // tiles, stages, masked tiles before this item's
-        int turn = 0;                        // which third of the poison records
+        uint32_t g = 0;   // tiles before this item's
+        int turn = 0;     // which third of the poison records
         bool alive = true;
         Items walk;
-        Item it;
-        while (alive && walk.next(p, plan, lane, pair, it)) {
+        Item ahead;
+        bool more = walk.next(p, plan, lane, pair, ahead);
+        while (alive && more) {
+            const Item it = ahead;
+            more = walk.next(p, plan, lane, pair, ahead);   // known before it is needed
             const Keys keys = keys_of(it);
             const int x0 = split_at(keys.count, it.split, plan.splits);
             const int n = split_at(keys.count, it.split + 1, plan.splits) - x0;
             if (n == 0) continue;
             const int j = it.j0 + rank * plan.tokens + token;
-            const long long pos = it.ctx + j;
+            const int pos = it.ctx + min(j, it.n - 1);
             float m = -INFINITY, l = 0.f;
-            int masked_tiles = 0;
-            if (warp == 4) {   // the records of the item after this one
-                const int after = turn == 2 ? 0 : turn + 1;
-                (&sh->bad[after][0][0])[lane] = 0;
-                if (lane == 0) sh->poison[after] = 0;
-            }
             for (int x = 0; x < n; ++x) {
                 const uint32_t buf = (g + x) & 1;
                 alive = alive && warp_wait(&sh->s_full[buf], ((g + x) >> 1) & 1, abort_flag,
@@ -518,16 +600,16 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                 tc::tmem_ld32(t_x + part * 64, s);
                 tc::tmem_ld32(t_x + part * 64 + 32, s + 32);
                 tc::tmem_ld_wait();
-                const long long t0 = keys.base(x0 + x);
-                const bool masked = keys.masked(p, t0);
-                if (masked) {
-                    const long long first = t0 + part * 64;
-                    const int hi = within(pos - first);
-                    const int lo = p.window > 0 ? within(pos - p.window + 1 - first) : -1;
-                    const int sk = within(p.sinks - first);
+                const int t0 = keys.base(x0 + x);
+                if (keys.masked(p, t0)) {
+                    const int first = t0 + part * 64;
+                    uint64_t see = low_bits(pos - first + 1);
+                    if (p.window > 0)
+                        see &= ~low_bits(pos - p.window + 1 - first) | low_bits(p.sinks - first);
 #pragma unroll
                     for (int i = 0; i < 64; ++i)
-                        if (i > hi || (i < lo && i >= sk)) s[i] = 0xff800000u;
+                        if (!((i < 32 ? (uint32_t)see >> i : (uint32_t)(see >> 32) >> (i - 32)) & 1u))
+                            s[i] = 0xff800000u;
                 }
                 float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
@@ -577,60 +659,13 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                 l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
                 tc::tmem_st32(t_x + part * 32, s);
                 tc::tmem_st_wait();
-                if (masked) {
-                    // V rows that not every row of the pair sees: nothing that is not finite
-                    // may meet a weight of 0.  Two threads look through a key's row.
-                    alive = alive &&
-                            warp_wait<true>(&sh->v_ready, vcnt & 1, abort_flag, p.dev_status);
-                    // stages in order: K(0), K(1) V(0), K(2) V(1), ..., V(n - 1)
-                    const uint32_t stage = (cnt + (x + 1 < n ? x + 2 : n) * KST + x) % NS;
-                    uint8_t *v_row = smem + stage * kStage + part * 16384 + row * 128;
-                    const bool stale = t0 + row > keys.hi;
-                    bool bad = false;
-                    if (!stale) {
-                        __nv_bfloat162 acc = __float2bfloat162_rn(0.f);
-                        const __nv_bfloat162 zero = __float2bfloat162_rn(0.f);
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const uint4 v =
-                                *reinterpret_cast<const uint4 *>(v_row + ((i + row) & 7) * 16);
-                            acc = __hfma2(*reinterpret_cast<const __nv_bfloat162 *>(&v.x), zero, acc);
-                            acc = __hfma2(*reinterpret_cast<const __nv_bfloat162 *>(&v.y), zero, acc);
-                            acc = __hfma2(*reinterpret_cast<const __nv_bfloat162 *>(&v.z), zero, acc);
-                            acc = __hfma2(*reinterpret_cast<const __nv_bfloat162 *>(&v.w), zero, acc);
-                        }
-                        bad = __hisnan(acc.x) || __hisnan(acc.y);
-                    }
-                    if (bad || stale) {
-#pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            *reinterpret_cast<uint4 *>(v_row + i * 16) = make_uint4(0, 0, 0, 0);
-                        tc::fence_proxy_async_smem();
-                    }
-                    const uint32_t mask = __ballot_sync(kFull, bad);
-                    if (mask && lane == 0) {
-                        for (int r = 0; r < 2; ++r) {
-                            tc::or_cluster_u32(
-                                tc::map_to_rank(&sh->bad[turn][masked_tiles][quad], r), mask);
-                            tc::or_cluster_u32(tc::map_to_rank(&sh->poison[turn], r), 1);
-                        }
-                    }
-                    ++masked_tiles;
-                    ++vcnt;
-                }
                 tc::tc_fence_before();
                 __syncwarp();
-                if (alive && lane == 0) {
-                    const uint32_t bar = tc::map_to_rank(&sh->p_full[buf], 0);
-                    if (masked)
-                        tc::mbar_arrive_cluster(bar);
-                    else
-                        tc::mbar_arrive_remote(bar);
-                }
+                if (alive && lane == 0)
+                    tc::mbar_arrive_remote(tc::map_to_rank(&sh->p_full[buf], 0));
             }
             if (!alive) break;
             g += n;
-            cnt += n * (KST + 1);
             // The last scores say that the product two tiles before is done, no more: a wait
             // for the last product alone could pass on that one's phase, which has its parity.
             if (g > 1) alive = alive && warp_wait(&sh->pv_done, g & 1, abort_flag, p.dev_status);
@@ -646,11 +681,11 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
             bool poisoned = false;
             if (*(volatile uint32_t *)&sh->poison[turn]) {
                 for (int x = 0, i = 0; x < n; ++x) {
-                    const long long t0 = keys.base(x0 + x);
+                    const int t0 = keys.base(x0 + x);
                     if (!keys.masked(p, t0)) continue;
                     for (int w = 0; w < 4; ++w)
                         for (uint32_t bits = sh->bad[turn][i][w]; bits; bits &= bits - 1) {
-                            const long long t = t0 + w * 32 + __ffs(bits) - 1;
+                            const int t = t0 + w * 32 + __ffs(bits) - 1;
                             poisoned |=
                                 t <= pos && (p.window == 0 || t > pos - p.window || t < p.sinks);
                         }
@@ -658,37 +693,71 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                 }
             }
             turn = turn == 2 ? 0 : turn + 1;
-            const bool valid = token < plan.tokens && j < it.n;
-            const size_t at = ((size_t)it.b * p.k + j) * p.q_heads + it.c * p.group + row % p.group;
             const bool partial = plan.splits > 1;
             const float f = poisoned ? NAN : partial ? 1.f : 1.f / l;
-            if (partial && valid && it.vh == 0 && part == 0)
-                plan.part_ml[at * plan.splits + it.split] = make_float2(m, l);
-            // a thread writes half of its row
+            auto row_at = [&](int token_of, int head_of) -> size_t {
+                return ((size_t)it.b * p.k + it.j0 + rank * plan.tokens + token_of) * p.q_heads +
+                       it.c * p.group + head_of;
+            };
+            auto row_valid = [&](int token_of) {
+                return token_of < plan.tokens && it.j0 + rank * plan.tokens + token_of < it.n;
+            };
+            if (partial && row_valid(token) && it.vh == 0 && part == 0)
+                plan.part_ml[row_at(token, row % p.group) * plan.splits + it.split] =
+                    make_float2(m, l);
+            // O leaves by quarters of a warp: lanes 4 i .. 4 i + 3 hold 8 columns of rows i and
+            // i + 8 (and, of a second load, i + 16 and i + 24), two a lane.
 #pragma unroll 1
-            for (int i = part * (kDV / 2); i < (part + 1) * (kDV / 2); i += 32) {
-                uint32_t o[32];
-                tc::tmem_ld32(t_o + lanes + i, o);
-                tc::tmem_ld_wait();
+            for (int r16 = 0; r16 < 32; r16 += 16) {
+                size_t at[2];
+                bool ok[2];
+                float fr[2];
 #pragma unroll
-                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                if (!valid) continue;
-                if (partial) {
-                    uint4 *to = reinterpret_cast<uint4 *>(
-                        plan.part_o + (at * plan.splits + it.split) * D + it.vh * kDV + i);
+                for (int e = 0; e < 2; ++e) {
+                    const int in_warp = r16 + e * 8 + lane / 4;
+                    const int rr = quad * 32 + in_warp, tt = rr / p.group;
+                    ok[e] = row_valid(tt);
+                    at[e] = row_at(tt, rr - tt * p.group);
+                    fr[e] = __shfl_sync(kFull, f, in_warp);
+                }
+#pragma unroll 1
+                for (int i = part * (kDV / 2); i < (part + 1) * (kDV / 2); i += 32) {
+                    uint32_t o[16];
+                    tc::tmem_ld_16x256b_x4(t_o + lanes + ((uint32_t)r16 << 16) + i, o);
+                    tc::tmem_ld_wait();
 #pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        to[e] = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
-                } else {
-                    uint4 *to = reinterpret_cast<uint4 *>(p.out + at * D + it.vh * kDV + i);
+                    for (int e = 0; e < 2; ++e) {
+                        if (partial) {
+                            float *to = plan.part_o + (at[e] * plan.splits + it.split) * D +
+                                        it.vh * kDV + i + (lane & 3) * 2;
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
+                            for (int q = 0; q < 4; ++q)
+                                if (ok[e])
+                                    *reinterpret_cast<float2 *>(to + q * 8) =
+                                        make_float2(__uint_as_float(o[q * 4 + e * 2]) * fr[e],
+                                                    __uint_as_float(o[q * 4 + e * 2 + 1]) * fr[e]);
+                            continue;
+                        }
+                        // w[q]: columns 8 q + 2 (lane & 3) of the row; transposed among the
+                        // four lanes, so that lane q has the eight columns from 8 q on
                         uint32_t w[4];
 #pragma unroll
-                        for (int z = 0; z < 4; ++z)
-                            w[z] = pack_bf16(__uint_as_float(o[e * 8 + 2 * z]),
-                                             __uint_as_float(o[e * 8 + 2 * z + 1]));
-                        to[e] = make_uint4(w[0], w[1], w[2], w[3]);
+                        for (int q = 0; q < 4; ++q)
+                            w[q] = pack_bf16(__uint_as_float(o[q * 4 + e * 2]) * fr[e],
+                                             __uint_as_float(o[q * 4 + e * 2 + 1]) * fr[e]);
+                        const bool odd = lane & 1, high = lane & 2;
+                        uint32_t x0_ = odd ? w[0] : w[1], x1_ = odd ? w[2] : w[3];
+                        x0_ = __shfl_xor_sync(kFull, x0_, 1);
+                        x1_ = __shfl_xor_sync(kFull, x1_, 1);
+                        if (odd) { w[0] = x0_; w[2] = x1_; } else { w[1] = x0_; w[3] = x1_; }
+                        uint32_t y0 = high ? w[0] : w[2], y1 = high ? w[1] : w[3];
+                        y0 = __shfl_xor_sync(kFull, y0, 2);
+                        y1 = __shfl_xor_sync(kFull, y1, 2);
+                        if (high) { w[0] = y0; w[1] = y1; } else { w[2] = y0; w[3] = y1; }
+                        if (ok[e])
+                            *reinterpret_cast<uint4 *>(p.out + at[e] * D + it.vh * kDV + i +
+                                                       (lane & 3) * 8) =
+                                make_uint4(w[0], w[1], w[2], w[3]);
                     }
                 }
             }
@@ -715,7 +784,7 @@ __global__ void __launch_bounds__(D / 4) paged_chunk_merge_kernel(
     const Request rq = load_request(p, b);
     if (!request_ok(p, rq) || j >= rq.n) return;
     const int j0 = j / (2 * plan.tokens) * 2 * plan.tokens;
-    const Keys keys(p, rq.ctx + j0, rq.ctx + min(j0 + 2 * plan.tokens, rq.n) - 1);
+    const Keys keys(p, (int)rq.ctx + j0, (int)rq.ctx + min(j0 + 2 * plan.tokens, rq.n) - 1);
     const size_t at = blockIdx.x;
     float top = -INFINITY;
     for (int s = 0; s < plan.splits; ++s)
