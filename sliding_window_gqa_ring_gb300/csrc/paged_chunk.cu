@@ -90,7 +90,7 @@ struct Shared {
     uint64_t q_empty;       // both: an item's last scores are computed
     uint64_t s_full[2];     // both: a tile's scores are in tensor memory
     uint64_t p_full[2];     // leader: its weights are
-    uint64_t pv_done;       // both: a tile's value product is done
+    uint64_t pv_done[2];    // both: a tile's value product is done (tiles in turn)
     uint64_t v_ready;       // both: a masked tile's V has landed
     uint64_t v_clean;       // leader: it is looked through
     uint64_t drain;
@@ -214,6 +214,27 @@ struct Items {
     }
 };
 
+// The tiles of one item's split, in the order they are taken: from the first that every row
+// sees whole, so that no row's first maximum is that of a few keys (the maxima then rise
+// past the slack tile after tile, 1200 to 1700 cycles each time), round to those before it.
+struct Walk {
+    Keys keys;
+    int x0, n, turn;
+
+    __device__ __forceinline__ Walk(const PagedChunkParams &p, const Plan &plan, const Item &it)
+        : keys(p, it.ctx + it.j0, it.ctx + min(it.j0 + 2 * plan.tokens, it.n) - 1) {
+        x0 = split_at(keys.count, it.split, plan.splits);
+        n = split_at(keys.count, it.split + 1, plan.splits) - x0;
+        turn = 0;
+        while (turn < n && keys.masked(p, keys.base(x0 + turn))) ++turn;
+        if (turn >= n) turn = 0;
+    }
+    __device__ __forceinline__ int base(int x) const {
+        const int y = x + turn;
+        return keys.base(x0 + (y >= n ? y - n : y));
+    }
+};
+
 // Bounded wait; false on a timeout or when another role of this CTA gave up.  kCluster:
 // what threads of the other CTA wrote before they released the barrier is seen.
 template <bool kCluster>
@@ -297,9 +318,9 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         for (int i = 0; i < 2; ++i) {
             tc::mbar_init(&sh->s_full[i], 1);
             tc::mbar_init(&sh->p_full[i], 16);
+            tc::mbar_init(&sh->pv_done[i], 1);
         }
         for (int i = 0; i < 3; ++i) sh->poison[i] = 0;
-        tc::mbar_init(&sh->pv_done, 1);
         tc::mbar_init(&sh->v_ready, 1);
         tc::mbar_init(&sh->v_clean, 4);
         tc::mbar_init(&sh->drain, 1);
@@ -321,29 +342,27 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     const uint32_t tmem = sh->tmem;
     const uint32_t t_o = tmem, t_s = tmem + kDV;
     volatile int *abort_flag = &sh->abort_flag;
-    auto keys_of = [&](const Item &it) {
-        return Keys(p, it.ctx + it.j0, it.ctx + min(it.j0 + 2 * plan.tokens, it.n) - 1);
-    };
 
     if (warp == 0) {
         // ---------------------------------------------------------------- producer
         uint32_t cnt = 0, items = 0;
         bool alive = true;
         const uint32_t q_bytes = plan.tokens * p.group * 128;
-        Items walk;
+        Items list;
         Item ahead;
-        bool more = walk.next(p, plan, lane, pair, ahead);
+        bool more = list.next(p, plan, lane, pair, ahead);
         while (alive && more) {
             const Item it = ahead;
-            more = walk.next(p, plan, lane, pair, ahead);   // known before it is needed
-            const Keys keys = keys_of(it);
-            const int x0 = split_at(keys.count, it.split, plan.splits);
-            const int n = split_at(keys.count, it.split + 1, plan.splits) - x0;
-            if (n == 0) continue;
+            const Walk tiles(p, plan, it);
+            const int n = tiles.n;
+            if (n == 0) {
+                more = list.next(p, plan, lane, pair, ahead);
+                continue;
+            }
             int row_held = 0;   // lane l: pool row of the item's tile 32 * (x / 32) + l
             auto fetch = [&](int x) {
                 if (x + lane < n) {
-                    const int t = keys.base(x0 + x + lane), at = t / p.page_rows;
+                    const int t = tiles.base(x + lane), at = t / p.page_rows;
                     const int page = p.page_table[(size_t)it.b * p.max_pages + at];
                     if (page < 0 || page >= p.num_pages) {
                         set_status(p.dev_status, CARAT_DEV_BAD_CACHE_ID);
@@ -395,6 +414,8 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                 }
                 if (x > 0) load(true, prev, 0);
                 prev = row;
+                // the item after this one, while this one's loads are on their way
+                if (x == 1) more = list.next(p, plan, lane, pair, ahead);
             }
         }
         if (!alive && rank == 0) {
@@ -411,16 +432,17 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         const uint32_t q_addr = tc::smem_u32(s_q), st_addr = tc::smem_u32(smem);
         uint32_t cnt = 0, items = 0, g = 0, vcnt = 0;   // stages, items, tiles, masked tiles
         bool alive = true;
-        Items walk;
+        Items list;
         Item ahead;
-        bool more = walk.next(p, plan, lane, pair, ahead);
+        bool more = list.next(p, plan, lane, pair, ahead);
         while (alive && more) {
             const Item it = ahead;
-            more = walk.next(p, plan, lane, pair, ahead);   // known before it is needed
-            const Keys keys = keys_of(it);
-            const int x0 = split_at(keys.count, it.split, plan.splits);
-            const int n = split_at(keys.count, it.split + 1, plan.splits) - x0;
-            if (n == 0) continue;
+            const Walk tiles(p, plan, it);
+            const int n = tiles.n;
+            if (n == 0) {
+                more = list.next(p, plan, lane, pair, ahead);
+                continue;
+            }
             alive = warp_wait(&sh->q_full, items & 1, abort_flag, p.dev_status);
             ++items;
             for (int x = 0; x <= n && alive; ++x) {
@@ -447,12 +469,14 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                     if (x == n - 1) tc::mma_commit_pair(&sh->q_empty);
                 }
                 if (x == 0) continue;
+                // the item after this one, while the first softmax runs
+                if (x == 1) more = list.next(p, plan, lane, pair, ahead);
                 const int y = x - 1, s = cnt % NS;
                 const uint32_t buf = (g + y) & 1;
                 alive = warp_wait(&sh->full[s], (cnt / NS) & 1, abort_flag, p.dev_status);
                 if (!alive) break;
                 const uint32_t phase = ((g + y) >> 1) & 1;
-                if (keys.masked(p, keys.base(x0 + y))) {
+                if (tiles.keys.masked(p, tiles.base(y))) {
                     if (lane == 0) {
                         tc::mbar_arrive_remote(tc::map_to_rank(&sh->v_ready, 0));
                         tc::mbar_arrive_remote(tc::map_to_rank(&sh->v_ready, 1));
@@ -470,7 +494,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                                          tc::sdesc_sw128(st_addr + s * kStage + i * 2048, 16384, 1024),
                                          id_pv, y > 0 || i > 0);
                 tc::mma_commit_pair(&sh->empty[s]);
-                tc::mma_commit_pair(&sh->pv_done);
+                tc::mma_commit_pair(&sh->pv_done[buf]);
                 ++cnt;
             }
             g += n;
@@ -487,15 +511,14 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         uint32_t cnt = 0, vcnt = 0;   // stages, masked tiles before this item's
         int turn = 0;
         bool alive = true;
-        Items walk;
+        Items list;
         Item ahead;
-        bool more = walk.next(p, plan, lane, pair, ahead);
+        bool more = list.next(p, plan, lane, pair, ahead);
         while (alive && more) {
             const Item it = ahead;
-            more = walk.next(p, plan, lane, pair, ahead);
-            const Keys keys = keys_of(it);
-            const int x0 = split_at(keys.count, it.split, plan.splits);
-            const int n = split_at(keys.count, it.split + 1, plan.splits) - x0;
+            more = list.next(p, plan, lane, pair, ahead);
+            const Walk tiles(p, plan, it);
+            const int n = tiles.n;
             if (n == 0) continue;
             if (warp == 2) {   // the records of the item after this one
                 const int after = turn == 2 ? 0 : turn + 1;
@@ -503,8 +526,8 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                 if (lane == 0) sh->poison[after] = 0;
             }
             for (int x = 0, i = 0; x < n; ++x) {
-                const int t0 = keys.base(x0 + x);
-                if (!keys.masked(p, t0)) continue;
+                const int t0 = tiles.base(x);
+                if (!tiles.keys.masked(p, t0)) continue;
                 alive = warp_wait<true>(&sh->v_ready, vcnt & 1, abort_flag, p.dev_status);
                 if (!alive) break;
                 ++vcnt;
@@ -515,7 +538,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                 for (int w = warp - 2; w < 4; w += 2) {
                     const int key = w * 32 + lane;
                     uint8_t *v_row = smem + stage * kStage + key * 128;
-                    const bool stale = t0 + key > keys.hi;
+                    const bool stale = t0 + key > tiles.keys.hi;
                     __nv_bfloat162 acc = __float2bfloat162_rn(0.f);
                     const __nv_bfloat162 zero = __float2bfloat162_rn(0.f);
 #pragma unroll
@@ -577,16 +600,17 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         uint32_t g = 0;   // tiles before this item's
         int turn = 0;     // which third of the poison records
         bool alive = true;
-        Items walk;
+        Items list;
         Item ahead;
-        bool more = walk.next(p, plan, lane, pair, ahead);
+        bool more = list.next(p, plan, lane, pair, ahead);
         while (alive && more) {
             const Item it = ahead;
-            more = walk.next(p, plan, lane, pair, ahead);   // known before it is needed
-            const Keys keys = keys_of(it);
-            const int x0 = split_at(keys.count, it.split, plan.splits);
-            const int n = split_at(keys.count, it.split + 1, plan.splits) - x0;
-            if (n == 0) continue;
+            const Walk tiles(p, plan, it);
+            const int n = tiles.n;
+            if (n == 0) {
+                more = list.next(p, plan, lane, pair, ahead);
+                continue;
+            }
             const int j = it.j0 + rank * plan.tokens + token;
             const int pos = it.ctx + min(j, it.n - 1);
             float m = -INFINITY, l = 0.f;
@@ -600,8 +624,8 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                 tc::tmem_ld32(t_x + part * 64, s);
                 tc::tmem_ld32(t_x + part * 64 + 32, s + 32);
                 tc::tmem_ld_wait();
-                const int t0 = keys.base(x0 + x);
-                if (keys.masked(p, t0)) {
+                const int t0 = tiles.base(x);
+                if (tiles.keys.masked(p, t0)) {
                     const int first = t0 + part * 64;
                     uint64_t see = low_bits(pos - first + 1);
                     if (p.window > 0)
@@ -631,7 +655,8 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                     l *= f;
                     if (x > 0) {
                         // each of the two warps scales half of the columns
-                        alive = warp_wait(&sh->pv_done, (g + x - 1) & 1, abort_flag, p.dev_status);
+                        alive = warp_wait(&sh->pv_done[buf ^ 1], ((g + x - 1) >> 1) & 1, abort_flag,
+                                          p.dev_status);
                         tc::tc_fence_after();
 #pragma unroll 1
                         for (int i = part * (kDV / 2); i < (part + 1) * (kDV / 2); i += 32) {
@@ -666,10 +691,12 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
             }
             if (!alive) break;
             g += n;
-            // The last scores say that the product two tiles before is done, no more: a wait
-            // for the last product alone could pass on that one's phase, which has its parity.
-            if (g > 1) alive = alive && warp_wait(&sh->pv_done, g & 1, abort_flag, p.dev_status);
-            alive = alive && warp_wait<true>(&sh->pv_done, (g - 1) & 1, abort_flag, p.dev_status);
+            // the item after this one, while the last product runs
+            more = list.next(p, plan, lane, pair, ahead);
+            // The last scores say that the product two tiles before is done, no more: with one
+            // barrier for all products this wait could meet a phase too early or too late.
+            alive = alive && warp_wait<true>(&sh->pv_done[(g - 1) & 1], ((g - 1) >> 1) & 1,
+                                             abort_flag, p.dev_status);
             // the last tile's place: the next tile's may be written before the other has read
             sh->row[(g - 1) & 1][part][row] = l;
             if (rows_barrier(quad, !alive)) {
@@ -681,8 +708,8 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
             bool poisoned = false;
             if (*(volatile uint32_t *)&sh->poison[turn]) {
                 for (int x = 0, i = 0; x < n; ++x) {
-                    const int t0 = keys.base(x0 + x);
-                    if (!keys.masked(p, t0)) continue;
+                    const int t0 = tiles.base(x);
+                    if (!tiles.keys.masked(p, t0)) continue;
                     for (int w = 0; w < 4; ++w)
                         for (uint32_t bits = sh->bad[turn][i][w]; bits; bits &= bits - 1) {
                             const int t = t0 + w * 32 + __ffs(bits) - 1;
@@ -720,11 +747,16 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                     at[e] = row_at(tt, rr - tt * p.group);
                     fr[e] = __shfl_sync(kFull, f, in_warp);
                 }
-#pragma unroll 1
-                for (int i = part * (kDV / 2); i < (part + 1) * (kDV / 2); i += 32) {
-                    uint32_t o[16];
-                    tc::tmem_ld_16x256b_x4(t_o + lanes + ((uint32_t)r16 << 16) + i, o);
-                    tc::tmem_ld_wait();
+                uint32_t all[kDV / 64][16];
+#pragma unroll
+                for (int z = 0; z < kDV / 64; ++z)
+                    tc::tmem_ld_16x256b_x4(
+                        t_o + lanes + ((uint32_t)r16 << 16) + part * (kDV / 2) + z * 32, all[z]);
+                tc::tmem_ld_wait();
+#pragma unroll
+                for (int z = 0; z < kDV / 64; ++z) {
+                    const uint32_t *o = all[z];
+                    const int i = part * (kDV / 2) + z * 32;
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         if (partial) {
