@@ -38,12 +38,15 @@
 //
 // Schedule.  One CTA pair for every two SMs; the items that have rows, request after
 // request, are dealt to them in turn (forth and back, so that the longer ones of a causal
-// mask are shared out), each role walking its pair's items by itself.  The next item's keys
-// and queries are loaded and its first scores computed while the last one's output leaves.
+// mask are shared out); the producer finds them and hands them to the other roles through
+// a ring of four.  The next item's keys and queries are loaded and its first scores computed
+// while the last one's output leaves.  Code that runs once an item is kept short (rolled
+// loops, one copy): it comes from a cold instruction cache, and an unrolled output of the
+// same work took 5000 cycles.
 //
 // Warp roles (384 threads): warp 0 TMA producer (each CTA its own halves, counted on the
-// leader's barriers), warp 1 of the leader issues the products, warps 4-11 softmax, rescale
-// and output: two threads a row, the first 64 keys of a tile and the others (one thread a
+// leader's barriers), warp 1 of the leader issues the products, warps 2-3 look through V,
+// warps 4-11 softmax, rescale and output: two threads a row, the first 64 keys of a tile and the others (one thread a
 // row took 1.9 us a tile at head_dim 256, nearly twice the products' time).  Every wait is
 // bounded: on a timeout CARAT_DEV_TIMEOUT is set and the CTA stops, waits for its own
 // copies and products, and returns.
@@ -66,6 +69,7 @@ constexpr int kRows = 128;              // rows of a CTA
 constexpr int kDV = 256;                // value dimensions of an item
 constexpr int kStage = 32768;           // K: 64 keys x 256 d, or V: 128 keys x 128 d
 constexpr int kThreads = 384, kSoftmax = 256;
+constexpr int kJobs = 4;                // items handed to the other roles
 constexpr int kMasked = 8;              // masked tiles of an item: 3 + 3 + 1 at most
 constexpr uint32_t kFull = 0xffffffffu;
 constexpr float kSlack = 8.0f;          // log2 units
@@ -73,35 +77,17 @@ constexpr float kSlack = 8.0f;          // log2 units
 template <int D>
 struct Lay {
     static constexpr int KST = D / 256;                 // stages of a K tile
-    static constexpr int NS = D == 256 ? 5 : 3;         // stage ring
+    // Stage ring; five stages at head_dim 256 were no faster (323 us against 290, 8191 tokens).
+    static constexpr int NS = D == 256 ? 4 : 3;
     static constexpr int kSlab = kRows * 128;           // 64 d of Q
     static constexpr int kOffQ = NS * kStage;
-    static constexpr int kOffMisc = kOffQ + D / 64 * kSlab;
+    static constexpr int kOffOut = kOffQ + D / 64 * kSlab;
+    // head_dim 256: 32 rows of 128 bytes a softmax warp, on their way out
+    static constexpr int kOut = D == 256 ? 8 * 4096 : 0;
+    static constexpr int kOffMisc = kOffOut + kOut;
     static constexpr int kMisc = 3072;
     static constexpr int kAlloc = kOffMisc + kMisc;
     static_assert(kAlloc <= 232448, "more dynamic shared memory than one CTA may use");
-};
-
-template <int NS>
-struct Shared {
-    uint64_t full[NS];      // leader: a stage's bytes of both CTAs have landed
-    uint64_t empty[NS];     // both: the products that read the stage are done
-    uint64_t q_full;        // leader
-    uint64_t q_empty;       // both: an item's last scores are computed
-    uint64_t s_full[2];     // both: a tile's scores are in tensor memory
-    uint64_t p_full[2];     // leader: its weights are
-    uint64_t pv_done[2];    // both: a tile's value product is done (tiles in turn)
-    uint64_t v_ready;       // both: a masked tile's V has landed
-    uint64_t v_clean;       // leader: it is looked through
-    uint64_t drain;
-    uint32_t tmem;
-    int abort_flag;
-    // Keys of masked tiles with values that are not finite, of three items in turn: the
-    // other CTA may be at the next item's first tile already, and the third is cleared
-    // while nobody can be at its item.
-    uint32_t poison[3];
-    uint32_t bad[3][kMasked][4];
-    float row[2][2][kRows];           // a row's two threads tell each other
 };
 
 struct Request {
@@ -133,6 +119,7 @@ struct Keys {
     int first;              // the window's first tile
     int sink_tiles, count;
 
+    Keys() = default;
     __device__ __forceinline__ Keys(const PagedChunkParams &p, int lo_, int hi_)
         : lo(lo_), hi(hi_) {
         first = p.window > 0 && lo - p.window + 1 > 0 ? (lo - p.window + 1) / kKeys : 0;
@@ -161,8 +148,8 @@ struct Item {
     int j0, n, ctx;        // the pair's first token; the request's tokens, and before them
 };
 
-// The items of this pair, in order: the same for every warp that walks them (whole warps).
-// Requests are looked at 32 at a time, one a lane.
+// The items of this pair, in order, found by a whole warp.  Requests are looked at 32 at a
+// time, one a lane.
 struct Items {
     int base = -32;        // first request held
     int upto = 0;          // items of the held requests up to this lane's, and before
@@ -214,41 +201,72 @@ struct Items {
     }
 };
 
-// The tiles of one item's split, in the order they are taken: from the first that every row
+// One item's split: its tiles in the order they are taken, from the first that every row
 // sees whole, so that no row's first maximum is that of a few keys (the maxima then rise
 // past the slack tile after tile, 1200 to 1700 cycles each time), round to those before it.
-struct Walk {
+// n = 0: no item left.
+struct Job {
+    Item it;
     Keys keys;
     int x0, n, turn;
 
-    __device__ __forceinline__ Walk(const PagedChunkParams &p, const Plan &plan, const Item &it)
-        : keys(p, it.ctx + it.j0, it.ctx + min(it.j0 + 2 * plan.tokens, it.n) - 1) {
-        x0 = split_at(keys.count, it.split, plan.splits);
-        n = split_at(keys.count, it.split + 1, plan.splits) - x0;
-        turn = 0;
-        while (turn < n && keys.masked(p, keys.base(x0 + turn))) ++turn;
-        if (turn >= n) turn = 0;
-    }
     __device__ __forceinline__ int base(int x) const {
         const int y = x + turn;
         return keys.base(x0 + (y >= n ? y - n : y));
     }
 };
 
+__device__ __forceinline__ Job job_of(const PagedChunkParams &p, const Plan &plan, const Item &it) {
+    Job j;
+    j.it = it;
+    j.keys = Keys(p, it.ctx + it.j0, it.ctx + min(it.j0 + 2 * plan.tokens, it.n) - 1);
+    j.x0 = split_at(j.keys.count, it.split, plan.splits);
+    j.n = split_at(j.keys.count, it.split + 1, plan.splits) - j.x0;
+    j.turn = 0;
+    while (j.turn < j.n && j.keys.masked(p, j.keys.base(j.x0 + j.turn))) ++j.turn;
+    if (j.turn >= j.n) j.turn = 0;
+    return j;
+}
+
+template <int NS>
+struct Shared {
+    uint64_t full[NS];      // leader: a stage's bytes of both CTAs have landed
+    uint64_t empty[NS];     // both: the products that read the stage are done
+    uint64_t q_full;        // leader
+    uint64_t q_empty;       // both: an item's last scores are computed
+    uint64_t s_full[2];     // both: a tile's scores are in tensor memory
+    uint64_t p_full[2];     // leader: its weights are
+    uint64_t pv_done[2];    // both: a tile's value product is done (tiles in turn)
+    uint64_t v_ready;       // both: a masked tile's V has landed
+    uint64_t v_clean;       // leader: it is looked through
+    uint64_t drain;
+    uint64_t job_full[kJobs], job_empty[kJobs];   // each CTA's own
+    uint32_t tmem;
+    int abort_flag;
+    Job job[kJobs];
+    // Keys of masked tiles with values that are not finite, of three items in turn: the
+    // other CTA may be at the next item's first tile already, and the third is cleared
+    // while nobody can be at its item.
+    uint32_t poison[3];
+    uint32_t bad[3][kMasked][4];
+    float row[2][2][kRows];           // a row's two threads tell each other
+};
+
 // Bounded wait; false on a timeout or when another role of this CTA gave up.  kCluster:
 // what threads of the other CTA wrote before they released the barrier is seen.
 template <bool kCluster>
-__device__ __forceinline__ bool wait_or_abort(uint64_t *bar, uint32_t parity,
-                                              volatile int *abort_flag, int *dev_status) {
-    auto passed = [&]() {
-        return kCluster ? tc::mbar_try_wait_cluster(bar, parity) : tc::mbar_try_wait(bar, parity);
-    };
-    if (passed()) return true;
+__device__ __forceinline__ bool passed(uint64_t *bar, uint32_t parity) {
+    return kCluster ? tc::mbar_try_wait_cluster(bar, parity) : tc::mbar_try_wait(bar, parity);
+}
+
+template <bool kCluster>
+__device__ __noinline__ bool wait_on(uint64_t *bar, uint32_t parity, volatile int *abort_flag,
+                                     int *dev_status) {
     const uint64_t t0 = tc::globaltimer_ns();
     for (uint32_t round = 1;; ++round) {
 #pragma unroll 1
         for (int i = 0; i < 32; ++i)
-            if (passed()) return true;
+            if (passed<kCluster>(bar, parity)) return true;
         if (*abort_flag) return false;
         if (tc::wait_expired(t0, round, 2000000000ull)) {
             *abort_flag = 1;
@@ -258,11 +276,13 @@ __device__ __forceinline__ bool wait_or_abort(uint64_t *bar, uint32_t parity,
     }
 }
 
-// The same for a whole warp, which goes on or stops as one.
+// A whole warp goes on or stops as one.
 template <bool kCluster = false>
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity,
                                           volatile int *abort_flag, int *dev_status) {
-    return __all_sync(kFull, wait_or_abort<kCluster>(bar, parity, abort_flag, dev_status)) != 0;
+    const bool ok =
+        passed<kCluster>(bar, parity) || wait_on<kCluster>(bar, parity, abort_flag, dev_status);
+    return __all_sync(kFull, ok) != 0;
 }
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
@@ -324,6 +344,10 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         tc::mbar_init(&sh->v_ready, 1);
         tc::mbar_init(&sh->v_clean, 4);
         tc::mbar_init(&sh->drain, 1);
+        for (int i = 0; i < kJobs; ++i) {
+            tc::mbar_init(&sh->job_full[i], 1);
+            tc::mbar_init(&sh->job_empty[i], rank == 0 ? 11 : 10);
+        }
         tc::fence_mbar_init();
         sh->abort_flag = 0;
     }
@@ -342,6 +366,19 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     const uint32_t tmem = sh->tmem;
     const uint32_t t_o = tmem, t_s = tmem + kDV;
     volatile int *abort_flag = &sh->abort_flag;
+    // Every role but the producer: the next item, or false (none left, or a wait ran out).
+    uint32_t taken = 0;
+    auto take = [&](bool &alive) -> const Job * {
+        const int slot = taken % kJobs;
+        alive = alive &&
+                warp_wait(&sh->job_full[slot], (taken / kJobs) & 1, abort_flag, p.dev_status);
+        ++taken;
+        return alive && sh->job[slot].n > 0 ? &sh->job[slot] : nullptr;
+    };
+    auto give_back = [&]() {
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&sh->job_empty[(taken - 1) % kJobs]);
+    };
 
     if (warp == 0) {
         // ---------------------------------------------------------------- producer
@@ -349,16 +386,28 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         bool alive = true;
         const uint32_t q_bytes = plan.tokens * p.group * 128;
         Items list;
-        Item ahead;
-        bool more = list.next(p, plan, lane, pair, ahead);
+        uint32_t published = 0;
+        bool more = true;
         while (alive && more) {
-            const Item it = ahead;
-            const Walk tiles(p, plan, it);
-            const int n = tiles.n;
-            if (n == 0) {
-                more = list.next(p, plan, lane, pair, ahead);
-                continue;
+            Item it;
+            more = list.next(p, plan, lane, pair, it);
+            Job tiles{};
+            if (more) {
+                tiles = job_of(p, plan, it);
+                if (tiles.n == 0) continue;
             }
+            const int slot = published % kJobs;
+            if (published >= kJobs)
+                alive = warp_wait(&sh->job_empty[slot], ((published / kJobs) & 1) ^ 1, abort_flag,
+                                  p.dev_status);
+            if (!alive) break;
+            if (lane == 0) {
+                sh->job[slot] = tiles;
+                tc::mbar_arrive(&sh->job_full[slot]);
+            }
+            ++published;
+            if (!more) break;
+            const int n = tiles.n;
             int row_held = 0;   // lane l: pool row of the item's tile 32 * (x / 32) + l
             auto fetch = [&](int x) {
                 if (x + lane < n) {
@@ -414,8 +463,6 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                 }
                 if (x > 0) load(true, prev, 0);
                 prev = row;
-                // the item after this one, while this one's loads are on their way
-                if (x == 1) more = list.next(p, plan, lane, pair, ahead);
             }
         }
         if (!alive && rank == 0) {
@@ -432,17 +479,13 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         const uint32_t q_addr = tc::smem_u32(s_q), st_addr = tc::smem_u32(smem);
         uint32_t cnt = 0, items = 0, g = 0, vcnt = 0;   // stages, items, tiles, masked tiles
         bool alive = true;
-        Items list;
-        Item ahead;
-        bool more = list.next(p, plan, lane, pair, ahead);
-        while (alive && more) {
-            const Item it = ahead;
-            const Walk tiles(p, plan, it);
+        const uint64_t q_desc = tc::sdesc_sw128(q_addr, 16, 1024);
+        const uint64_t k_desc = tc::sdesc_sw128(st_addr, 16, 1024);
+        const uint64_t v_desc = tc::sdesc_sw128(st_addr, 16384, 1024);
+        while (const Job *job = take(alive)) {
+            const Job tiles = *job;
+            give_back();
             const int n = tiles.n;
-            if (n == 0) {
-                more = list.next(p, plan, lane, pair, ahead);
-                continue;
-            }
             alive = warp_wait(&sh->q_full, items & 1, abort_flag, p.dev_status);
             ++items;
             for (int x = 0; x <= n && alive; ++x) {
@@ -453,15 +496,15 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                         alive = warp_wait(&sh->full[s], (cnt / NS) & 1, abort_flag, p.dev_status);
                         if (!alive) break;
                         tc::tc_fence_after();
+                        // Unrolled: four at a time cost 8% of the whole call.  (Addresses in
+                        // descriptors count 16 bytes.)
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            const uint32_t off = (i & 3) * 32;
+                        for (int i = 0; i < 16; ++i)
                             tc::mma_bf16_ss_pair(
                                 t_s + buf * kKeys,
-                                tc::sdesc_sw128(q_addr + (k * 4 + i / 4) * L::kSlab + off, 16, 1024),
-                                tc::sdesc_sw128(st_addr + s * kStage + i / 4 * 8192 + off, 16, 1024),
-                                id_qk, k > 0 || i > 0);
-                        }
+                                q_desc + ((k * 4 + i / 4) * (L::kSlab / 16) + (i & 3) * 2),
+                                k_desc + (s * (kStage / 16) + i / 4 * 512 + (i & 3) * 2), id_qk,
+                                k > 0 || i > 0);
                         tc::mma_commit_pair(&sh->empty[s]);
                     }
                     if (!alive) break;
@@ -469,8 +512,6 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                     if (x == n - 1) tc::mma_commit_pair(&sh->q_empty);
                 }
                 if (x == 0) continue;
-                // the item after this one, while the first softmax runs
-                if (x == 1) more = list.next(p, plan, lane, pair, ahead);
                 const int y = x - 1, s = cnt % NS;
                 const uint32_t buf = (g + y) & 1;
                 alive = warp_wait(&sh->full[s], (cnt / NS) & 1, abort_flag, p.dev_status);
@@ -491,8 +532,8 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
 #pragma unroll
                 for (int i = 0; i < kKeys / 16; ++i)
                     tc::mma_bf16_ts_pair(t_o, t_s + buf * kKeys + i * 8,
-                                         tc::sdesc_sw128(st_addr + s * kStage + i * 2048, 16384, 1024),
-                                         id_pv, y > 0 || i > 0);
+                                         v_desc + (s * (kStage / 16) + i * 128), id_pv,
+                                         y > 0 || i > 0);
                 tc::mma_commit_pair(&sh->empty[s]);
                 tc::mma_commit_pair(&sh->pv_done[buf]);
                 ++cnt;
@@ -511,15 +552,10 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         uint32_t cnt = 0, vcnt = 0;   // stages, masked tiles before this item's
         int turn = 0;
         bool alive = true;
-        Items list;
-        Item ahead;
-        bool more = list.next(p, plan, lane, pair, ahead);
-        while (alive && more) {
-            const Item it = ahead;
-            more = list.next(p, plan, lane, pair, ahead);
-            const Walk tiles(p, plan, it);
+        while (const Job *job = take(alive)) {
+            const Job tiles = *job;
+            give_back();
             const int n = tiles.n;
-            if (n == 0) continue;
             if (warp == 2) {   // the records of the item after this one
                 const int after = turn == 2 ? 0 : turn + 1;
                 (&sh->bad[after][0][0])[lane] = 0;
@@ -533,36 +569,43 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                 ++vcnt;
                 // stages in order: K(0), K(1) V(0), K(2) V(1), ..., V(n - 1)
                 const uint32_t stage = (cnt + (x + 1 < n ? x + 2 : n) * KST + x) % NS;
-                bool wrote = false;
-#pragma unroll 1
-                for (int w = warp - 2; w < 4; w += 2) {
-                    const int key = w * 32 + lane;
-                    uint8_t *v_row = smem + stage * kStage + key * 128;
-                    const bool stale = t0 + key > tiles.keys.hi;
-                    __nv_bfloat162 acc = __float2bfloat162_rn(0.f);
-                    const __nv_bfloat162 zero = __float2bfloat162_rn(0.f);
+                // this warp's keys 64 (warp - 2) + lane and 32 further on, both at once
+                const int key = (warp - 2) * 64 + lane;
+                uint8_t *v_row = smem + stage * kStage + key * 128;
+                const __nv_bfloat162 zero = __float2bfloat162_rn(0.f);
+                __nv_bfloat162 acc[2][4];
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        const uint4 v = *reinterpret_cast<const uint4 *>(
-                            v_row + (e >> 3) * 16384 + ((e + key) & 7) * 16);
-                        acc = __hfma2(*reinterpret_cast<const __nv_bfloat162 *>(&v.x), zero, acc);
-                        acc = __hfma2(*reinterpret_cast<const __nv_bfloat162 *>(&v.y), zero, acc);
-                        acc = __hfma2(*reinterpret_cast<const __nv_bfloat162 *>(&v.z), zero, acc);
-                        acc = __hfma2(*reinterpret_cast<const __nv_bfloat162 *>(&v.w), zero, acc);
-                    }
-                    const bool bad = !stale && (__hisnan(acc.x) || __hisnan(acc.y));
+                for (int e = 0; e < 8; ++e) acc[e / 4][e % 4] = zero;
+#pragma unroll
+                for (int e = 0; e < 32; ++e) {
+                    const uint4 v = *reinterpret_cast<const uint4 *>(
+                        v_row + (e & 1) * 4096 + (e >> 4) * 16384 + (((e >> 1) + key) & 7) * 16);
+                    const uint32_t word[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        acc[e & 1][q] = __hfma2(*reinterpret_cast<const __nv_bfloat162 *>(&word[q]),
+                                                zero, acc[e & 1][q]);
+                }
+                bool wrote = false;
+#pragma unroll
+                for (int w = 0; w < 2; ++w) {
+                    const bool stale = t0 + key + w * 32 > tiles.keys.hi;
+                    const __nv_bfloat162 all = __hadd2(__hadd2(acc[w][0], acc[w][1]),
+                                                       __hadd2(acc[w][2], acc[w][3]));
+                    const bool bad = !stale && (__hisnan(all.x) || __hisnan(all.y));
                     if (bad || stale) {
 #pragma unroll
                         for (int e = 0; e < 16; ++e)
-                            *reinterpret_cast<uint4 *>(v_row + (e >> 3) * 16384 + (e & 7) * 16) =
-                                make_uint4(0, 0, 0, 0);
+                            *reinterpret_cast<uint4 *>(v_row + w * 4096 + (e >> 3) * 16384 +
+                                                       (e & 7) * 16) = make_uint4(0, 0, 0, 0);
                         tc::fence_proxy_async_smem();
                     }
                     const uint32_t mask = __ballot_sync(kFull, bad);
                     wrote |= __any_sync(kFull, bad || stale) != 0;
                     if (mask && lane == 0) {
                         for (int r = 0; r < 2; ++r) {
-                            tc::or_cluster_u32(tc::map_to_rank(&sh->bad[turn][i][w], r), mask);
+                            tc::or_cluster_u32(
+                                tc::map_to_rank(&sh->bad[turn][i][(warp - 2) * 2 + w], r), mask);
                             tc::or_cluster_u32(tc::map_to_rank(&sh->poison[turn], r), 1);
                         }
                     }
@@ -585,7 +628,8 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         const int part = (warp - 4) / 4, quad = warp % 4;   // keys 64 part .. of a tile; lanes
         const int row = quad * 32 + lane;                   // TMEM lane
         const uint32_t lanes = (uint32_t)quad << 21;
-        const int token = row / p.group;
+        const int token = row / p.group, head = row - token * p.group;
+        const int inv_group = 65536 / p.group + 1;   // r inv_group >> 16 = r / group, r < 128
         // the sign of the scale is in the product's descriptor; 0 would turn -inf into NaN
         const float scale = fmaxf(fabsf(p.scale_log2), FLT_MIN);
         // requests rejected on the device
@@ -600,19 +644,10 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         uint32_t g = 0;   // tiles before this item's
         int turn = 0;     // which third of the poison records
         bool alive = true;
-        Items list;
-        Item ahead;
-        bool more = list.next(p, plan, lane, pair, ahead);
-        while (alive && more) {
-            const Item it = ahead;
-            const Walk tiles(p, plan, it);
-            const int n = tiles.n;
-            if (n == 0) {
-                more = list.next(p, plan, lane, pair, ahead);
-                continue;
-            }
-            const int j = it.j0 + rank * plan.tokens + token;
-            const int pos = it.ctx + min(j, it.n - 1);
+        while (const Job *job = take(alive)) {
+            const Job &tiles = *job;   // given back when the output's places are known
+            const int n = tiles.n, lo_row = tiles.it.j0 + rank * plan.tokens;
+            const int pos = tiles.it.ctx + min(lo_row + token, tiles.it.n - 1);
             float m = -INFINITY, l = 0.f;
             for (int x = 0; x < n; ++x) {
                 const uint32_t buf = (g + x) & 1;
@@ -691,20 +726,29 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
             }
             if (!alive) break;
             g += n;
-            // the item after this one, while the last product runs
-            more = list.next(p, plan, lane, pair, ahead);
-            // The last scores say that the product two tiles before is done, no more: with one
-            // barrier for all products this wait could meet a phase too early or too late.
-            alive = alive && warp_wait<true>(&sh->pv_done[(g - 1) & 1], ((g - 1) >> 1) & 1,
-                                             abort_flag, p.dev_status);
-            // the last tile's place: the next tile's may be written before the other has read
+            // While the last product runs: a row's sum, its place.  (In the last tile's place:
+            // the next tile's may be written before this is read.)
             sh->row[(g - 1) & 1][part][row] = l;
             if (rows_barrier(quad, !alive)) {
                 alive = false;
                 break;
             }
-            tc::tc_fence_after();
             l += sh->row[(g - 1) & 1][part ^ 1][row];
+            const bool partial = plan.splits > 1;
+            const int split = tiles.it.split, d0 = tiles.it.vh * kDV;
+            const int held = min(plan.tokens, tiles.it.n - lo_row);   // tokens that have rows here
+            const size_t at = ((size_t)tiles.it.b * p.k + lo_row) * p.q_heads +
+                              tiles.it.c * p.group;
+            if (partial && token < held && d0 == 0 && part == 0)
+                plan.part_ml[(at + token * p.q_heads + head) * plan.splits + split] =
+                    make_float2(m, l);
+            float f = partial ? 1.f : 1.f / l;
+            // The last scores say that the product two tiles before is done, no more: with one
+            // barrier for all products this wait could meet a phase too early or too late.
+            alive = warp_wait<true>(&sh->pv_done[(g - 1) & 1], ((g - 1) >> 1) & 1, abort_flag,
+                                    p.dev_status);
+            if (!alive) break;
+            tc::tc_fence_after();
             bool poisoned = false;
             if (*(volatile uint32_t *)&sh->poison[turn]) {
                 for (int x = 0, i = 0; x < n; ++x) {
@@ -720,76 +764,111 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                 }
             }
             turn = turn == 2 ? 0 : turn + 1;
-            const bool partial = plan.splits > 1;
-            const float f = poisoned ? NAN : partial ? 1.f : 1.f / l;
-            auto row_at = [&](int token_of, int head_of) -> size_t {
-                return ((size_t)it.b * p.k + it.j0 + rank * plan.tokens + token_of) * p.q_heads +
-                       it.c * p.group + head_of;
+            if (poisoned) f = NAN;
+            give_back();
+            // place behind the CTA's first row of the warp's row r, or -1: no such row
+            auto place = [&](int r) -> int {
+                const int rr = quad * 32 + r, tt = rr * inv_group >> 16;
+                return tt < held ? tt * p.q_heads + rr - tt * p.group : -1;
             };
-            auto row_valid = [&](int token_of) {
-                return token_of < plan.tokens && it.j0 + rank * plan.tokens + token_of < it.n;
-            };
-            if (partial && row_valid(token) && it.vh == 0 && part == 0)
-                plan.part_ml[row_at(token, row % p.group) * plan.splits + it.split] =
-                    make_float2(m, l);
-            // O leaves by quarters of a warp: lanes 4 i .. 4 i + 3 hold 8 columns of rows i and
-            // i + 8 (and, of a second load, i + 16 and i + 24), two a lane.
+            if constexpr (L::kOut > 0) {
+                // O leaves through shared memory, 128 bytes of each of the warp's 32 rows at a
+                // time, so that eight lanes write a whole line.
+                uint8_t *s_out = smem + L::kOffOut + (warp - 4) * 4096;
+                auto leave = [&](uint8_t *base, size_t row_bytes) {
+                    __syncwarp();
+#pragma unroll 4
+                    for (int e = 0; e < 8; ++e) {
+                        const int r = e * 4 + lane / 8, to = place(r);
+                        const uint4 v = *reinterpret_cast<const uint4 *>(
+                            s_out + r * 128 + ((lane ^ r) & 7) * 16);
+                        if (to >= 0)
+                            *reinterpret_cast<uint4 *>(base + (at + to) * row_bytes +
+                                                       (lane & 7) * 16) = v;
+                    }
+                    __syncwarp();
+                };
 #pragma unroll 1
-            for (int r16 = 0; r16 < 32; r16 += 16) {
-                size_t at[2];
-                bool ok[2];
-                float fr[2];
+                for (int i = part * (kDV / 2); i < (part + 1) * (kDV / 2); i += 32) {
+                    uint32_t o[32];
+                    tc::tmem_ld32(t_o + lanes + i, o);
+                    tc::tmem_ld_wait();
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int in_warp = r16 + e * 8 + lane / 4;
-                    const int rr = quad * 32 + in_warp, tt = rr / p.group;
-                    ok[e] = row_valid(tt);
-                    at[e] = row_at(tt, rr - tt * p.group);
-                    fr[e] = __shfl_sync(kFull, f, in_warp);
-                }
-                uint32_t all[kDV / 64][16];
+                    for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                    if (partial) {
 #pragma unroll
-                for (int z = 0; z < kDV / 64; ++z)
-                    tc::tmem_ld_16x256b_x4(
-                        t_o + lanes + ((uint32_t)r16 << 16) + part * (kDV / 2) + z * 32, all[z]);
-                tc::tmem_ld_wait();
+                        for (int e = 0; e < 8; ++e)
+                            *reinterpret_cast<uint4 *>(s_out + lane * 128 + ((e ^ lane) & 7) * 16) =
+                                make_uint4(o[e * 4], o[e * 4 + 1], o[e * 4 + 2], o[e * 4 + 3]);
+                        leave(reinterpret_cast<uint8_t *>(plan.part_o + (size_t)split * D + d0 + i),
+                              (size_t)plan.splits * D * 4);
+                        continue;
+                    }
+                    const int half = (i & 32) / 8;   // of the 128 bytes
 #pragma unroll
-                for (int z = 0; z < kDV / 64; ++z) {
-                    const uint32_t *o = all[z];
-                    const int i = part * (kDV / 2) + z * 32;
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        if (partial) {
-                            float *to = plan.part_o + (at[e] * plan.splits + it.split) * D +
-                                        it.vh * kDV + i + (lane & 3) * 2;
-#pragma unroll
-                            for (int q = 0; q < 4; ++q)
-                                if (ok[e])
-                                    *reinterpret_cast<float2 *>(to + q * 8) =
-                                        make_float2(__uint_as_float(o[q * 4 + e * 2]) * fr[e],
-                                                    __uint_as_float(o[q * 4 + e * 2 + 1]) * fr[e]);
-                            continue;
-                        }
-                        // w[q]: columns 8 q + 2 (lane & 3) of the row; transposed among the
-                        // four lanes, so that lane q has the eight columns from 8 q on
+                    for (int e = 0; e < 4; ++e) {
                         uint32_t w[4];
 #pragma unroll
-                        for (int q = 0; q < 4; ++q)
-                            w[q] = pack_bf16(__uint_as_float(o[q * 4 + e * 2]) * fr[e],
-                                             __uint_as_float(o[q * 4 + e * 2 + 1]) * fr[e]);
-                        const bool odd = lane & 1, high = lane & 2;
-                        uint32_t x0_ = odd ? w[0] : w[1], x1_ = odd ? w[2] : w[3];
-                        x0_ = __shfl_xor_sync(kFull, x0_, 1);
-                        x1_ = __shfl_xor_sync(kFull, x1_, 1);
-                        if (odd) { w[0] = x0_; w[2] = x1_; } else { w[1] = x0_; w[3] = x1_; }
-                        uint32_t y0 = high ? w[0] : w[2], y1 = high ? w[1] : w[3];
-                        y0 = __shfl_xor_sync(kFull, y0, 2);
-                        y1 = __shfl_xor_sync(kFull, y1, 2);
-                        if (high) { w[0] = y0; w[1] = y1; } else { w[2] = y0; w[3] = y1; }
-                        if (ok[e])
-                            *reinterpret_cast<uint4 *>(p.out + at[e] * D + it.vh * kDV + i +
-                                                       (lane & 3) * 8) =
-                                make_uint4(w[0], w[1], w[2], w[3]);
+                        for (int z = 0; z < 4; ++z)
+                            w[z] = pack_bf16(__uint_as_float(o[e * 8 + 2 * z]),
+                                             __uint_as_float(o[e * 8 + 2 * z + 1]));
+                        *reinterpret_cast<uint4 *>(
+                            s_out + lane * 128 + (((e + half) ^ lane) & 7) * 16) =
+                            make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                    if (half)
+                        leave(reinterpret_cast<uint8_t *>(p.out + d0 + i - 32), D * 2);
+                }
+            } else {
+                // The stages and queries leave no shared memory: O leaves by quarters of a warp.
+                // Lanes 4 i .. 4 i + 3 hold 8 columns of rows i and i + 8 (and, of a second load,
+                // i + 16 and i + 24), two a lane.
+                const bool odd = lane & 1, high = lane & 2;
+#pragma unroll 1
+                for (int r16 = 0; r16 < 32; r16 += 16) {
+                    const int r[2] = {r16 + lane / 4, r16 + 8 + lane / 4};
+                    const int to[2] = {place(r[0]), place(r[1])};
+                    const float fr[2] = {__shfl_sync(kFull, f, r[0]), __shfl_sync(kFull, f, r[1])};
+#pragma unroll 1
+                    for (int i = part * (kDV / 2); i < (part + 1) * (kDV / 2); i += 32) {
+                        uint32_t o[16];
+                        tc::tmem_ld_16x256b_x4(t_o + lanes + ((uint32_t)r16 << 16) + i, o);
+                        tc::tmem_ld_wait();
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            if (partial) {
+                                float *dst = plan.part_o +
+                                             ((at + to[e]) * plan.splits + split) * D + d0 + i +
+                                             (lane & 3) * 2;
+#pragma unroll
+                                for (int q = 0; q < 4; ++q)
+                                    if (to[e] >= 0)
+                                        *reinterpret_cast<float2 *>(dst + q * 8) =
+                                            make_float2(__uint_as_float(o[q * 4 + e * 2]) * fr[e],
+                                                        __uint_as_float(o[q * 4 + e * 2 + 1]) * fr[e]);
+                                continue;
+                            }
+                            // w[q]: columns 8 q + 2 (lane & 3) of the row; transposed among the
+                            // four lanes, so that lane q has the eight columns from 8 q on
+                            uint32_t w[4];
+#pragma unroll
+                            for (int q = 0; q < 4; ++q)
+                                w[q] = pack_bf16(__uint_as_float(o[q * 4 + e * 2]) * fr[e],
+                                                 __uint_as_float(o[q * 4 + e * 2 + 1]) * fr[e]);
+                            const uint32_t a0 = __shfl_xor_sync(kFull, odd ? w[0] : w[1], 1);
+                            const uint32_t a1 = __shfl_xor_sync(kFull, odd ? w[2] : w[3], 1);
+                            w[0] = odd ? a0 : w[0];
+                            w[1] = odd ? w[1] : a0;
+                            w[2] = odd ? a1 : w[2];
+                            w[3] = odd ? w[3] : a1;
+                            const uint32_t b0 = __shfl_xor_sync(kFull, high ? w[0] : w[2], 2);
+                            const uint32_t b1 = __shfl_xor_sync(kFull, high ? w[1] : w[3], 2);
+                            if (to[e] >= 0)
+                                *reinterpret_cast<uint4 *>(p.out + (at + to[e]) * D + d0 + i +
+                                                           (lane & 3) * 8) =
+                                    make_uint4(high ? b0 : w[0], high ? b1 : w[1],
+                                               high ? w[2] : b0, high ? w[3] : b1);
+                        }
                     }
                 }
             }
