@@ -36,9 +36,10 @@
 // Few items (fewer than pairs of SMs): the key tiles of an item are split over CTA pairs,
 // each writes (max, sum, unnormalised O), and a second launch merges them.
 //
-// Schedule.  One CTA pair for every two SMs; the items that have rows, request after
-// request, are dealt to them in turn (forth and back, so that the longer ones of a causal
-// mask are shared out); the producer finds them and hands them to the other roles through
+// Schedule.  The grid has a CTA pair for every item, up to a few times the pairs that fit;
+// a pair that has finished takes over the work of one that has not been launched (cluster
+// launch control), so the items, of very different lengths under masks, windows and counts,
+// go to whoever is free.  The producer asks, finds the item and hands it to the other roles through
 // a ring of four.  The next item's keys and queries are loaded and its first scores computed
 // while the last one's output leaves.  Code that runs once an item is kept short (rolled
 // loops, one copy): it comes from a cold instruction cache, and an unrolled output of the
@@ -70,6 +71,7 @@ constexpr int kDV = 256;                // value dimensions of an item
 constexpr int kStage = 32768;           // K: 64 keys x 256 d, or V: 128 keys x 128 d
 constexpr int kThreads = 384, kSoftmax = 256;
 constexpr int kJobs = 4;                // items handed to the other roles
+constexpr int kUnits = 8;               // CTA pairs of the grid, times the pairs that fit
 constexpr int kMasked = 8;              // masked tiles of an item: 3 + 3 + 1 at most
 constexpr uint32_t kFull = 0xffffffffu;
 constexpr float kSlack = 8.0f;          // log2 units
@@ -107,7 +109,7 @@ struct Plan {
     int tokens;      // of a CTA
     int halves;      // value halves
     int splits;
-    int pairs;       // CTA pairs of the grid
+    int units;       // CTA pairs of the grid: pair u has the items u, u + units, ...
     float2 *part_ml; // [B k Hq][splits]
     float *part_o;   // [B k Hq][splits][D]
 };
@@ -148,20 +150,22 @@ struct Item {
     int j0, n, ctx;        // the pair's first token; the request's tokens, and before them
 };
 
-// The items of this pair, in order, found by a whole warp.  Requests are looked at 32 at a
-// time, one a lane.
+// The items in order, request after request, found by a whole warp.  Requests are looked at
+// 32 at a time, one a lane.
 struct Items {
     int base = -32;        // first request held
     int upto = 0;          // items of the held requests up to this lane's, and before
     int before = 0;        // items before the held requests
     int n = 0, tiles = 0, ctx = 0;   // this lane's request
-    int round = 0;
 
-    __device__ __forceinline__ bool next(const PagedChunkParams &p, const Plan &plan, int lane,
-                                         int pair, Item &it) {
-        const int id = round * plan.pairs + ((round & 1) ? plan.pairs - 1 - pair : pair);
-        ++round;
+    // Item number id, or false: there are fewer.
+    __device__ __forceinline__ bool find(const PagedChunkParams &p, const Plan &plan, int lane,
+                                         int id, Item &it) {
         const int per_tile = p.kv_heads * plan.halves * plan.splits;
+        if (id < before) {
+            base = -32;
+            before = 0;
+        }
         while (true) {
             const unsigned hit = __ballot_sync(kFull, base >= 0 && id < upto);
             if (hit) {
@@ -180,9 +184,9 @@ struct Items {
                 it.j0 = tile * 2 * plan.tokens;
                 return true;
             }
+            if (base + 32 >= p.batch) return false;
             if (base >= 0) before = __shfl_sync(kFull, upto, 31);
             base += 32;
-            if (base >= p.batch) return false;
             tiles = 0;
             if (base + lane < p.batch) {
                 const Request rq = load_request(p, base + lane);
@@ -241,6 +245,8 @@ struct Shared {
     uint64_t v_clean;       // leader: it is looked through
     uint64_t drain;
     uint64_t job_full[kJobs], job_empty[kJobs];   // each CTA's own
+    uint64_t answered[kJobs];                     // each CTA's own
+    alignas(16) uint4 answer[kJobs];              // which cluster's work is taken over
     uint32_t tmem;
     int abort_flag;
     Job job[kJobs];
@@ -346,6 +352,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         tc::mbar_init(&sh->drain, 1);
         for (int i = 0; i < kJobs; ++i) {
             tc::mbar_init(&sh->job_full[i], 1);
+            tc::mbar_init(&sh->answered[i], 1);
             tc::mbar_init(&sh->job_empty[i], rank == 0 ? 11 : 10);
         }
         tc::fence_mbar_init();
@@ -386,13 +393,36 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         bool alive = true;
         const uint32_t q_bytes = plan.tokens * p.group * 128;
         Items list;
-        uint32_t published = 0;
-        bool more = true;
-        while (alive && more) {
-            Item it;
-            more = list.next(p, plan, lane, pair, it);
+        uint32_t published = 0, asked = 0;
+        // Both CTAs' producers get the same answers, the leader asks.  An answer's place is
+        // used again after kJobs more: the other CTA is behind by less than the stage ring.
+        int unit = pair, id = pair;
+        auto ask = [&]() {
+            if (lane == 0) {
+                tc::fence_proxy_async_smem();
+                tc::mbar_arrive_expect_tx(&sh->answered[asked % kJobs], 16);
+                if (rank == 0)
+                    tc::ask_for_cluster(&sh->answer[asked % kJobs], &sh->answered[asked % kJobs]);
+            }
+            __syncwarp();
+        };
+        ask();
+        while (alive) {
             Job tiles{};
-            if (more) {
+            Item it;
+            if (unit >= 0) {
+                if (!list.find(p, plan, lane, id, it)) {
+                    // this pair's work is done: the next one's
+                    alive = warp_wait(&sh->answered[asked % kJobs], (asked / kJobs) & 1, abort_flag,
+                                      p.dev_status);
+                    if (!alive) break;
+                    const int first = tc::cluster_taken(&sh->answer[asked % kJobs]);
+                    ++asked;
+                    unit = id = first < 0 ? -1 : first / 2;
+                    if (unit >= 0) ask();
+                    continue;
+                }
+                id += plan.units;
                 tiles = job_of(p, plan, it);
                 if (tiles.n == 0) continue;
             }
@@ -406,7 +436,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                 tc::mbar_arrive(&sh->job_full[slot]);
             }
             ++published;
-            if (!more) break;
+            if (unit < 0) break;
             const int n = tiles.n;
             int row_held = 0;   // lane l: pool row of the item's tile 32 * (x / 32) + l
             auto fetch = [&](int x) {
@@ -465,8 +495,10 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                 prev = row;
             }
         }
+        // An answer that is still on its way lands before anyone leaves, and what both CTAs'
+        // copies still carry.
+        if (!alive && unit >= 0) tc::mbar_wait(&sh->answered[asked % kJobs], (asked / kJobs) & 1);
         if (!alive && rank == 0) {
-            // let what both CTAs' copies still carry land before anyone leaves
             if (items > 0) tc::mbar_wait(&sh->q_full, (items - 1) & 1);
             for (uint32_t i = cnt > NS ? cnt - NS : 0; i < cnt; ++i)
                 tc::mbar_wait(&sh->full[i % NS], (i / NS) & 1);
@@ -632,14 +664,19 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         const int inv_group = 65536 / p.group + 1;   // r inv_group >> 16 = r / group, r < 128
         // the sign of the scale is in the product's descriptor; 0 would turn -inf into NaN
         const float scale = fmaxf(fabsf(p.scale_log2), FLT_MIN);
-        // requests rejected on the device
-        for (int b = pair; b < p.batch; b += plan.pairs) {
-            if (request_ok(p, load_request(p, b))) continue;
-            if (threadIdx.x == 128 && rank == 0) set_status(p.dev_status, CARAT_DEV_BAD_CONTEXT);
-            uint4 *o = reinterpret_cast<uint4 *>(p.out + (size_t)b * p.k * p.q_heads * D);
-            const size_t count = (size_t)p.k * p.q_heads * (D / 8);
-            for (size_t i = rank * kSoftmax + threadIdx.x - 128; i < count; i += 2 * kSoftmax)
-                o[i] = make_uint4(0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu);
+        // Requests rejected on the device, by the pair that is always launched.
+        for (int first = 0; pair == 0 && first < p.batch; first += 32) {
+            const int mine = first + lane;
+            uint32_t bad = __ballot_sync(
+                kFull, mine < p.batch && !request_ok(p, load_request(p, mine)));
+            for (; bad; bad &= bad - 1) {
+                if (threadIdx.x == 128) set_status(p.dev_status, CARAT_DEV_BAD_CONTEXT);
+                const size_t rows = (size_t)p.k * p.q_heads;
+                uint4 *o = reinterpret_cast<uint4 *>(p.out + (first + __ffs(bad) - 1) * rows * D);
+                for (size_t i = rank * kSoftmax + threadIdx.x - 128; i < rows * (D / 8);
+                     i += 2 * kSoftmax)
+                    o[i] = make_uint4(0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu);
+            }
         }
         uint32_t g = 0;   // tiles before this item's
         int turn = 0;     // which third of the poison records
@@ -937,7 +974,9 @@ Sizes sizes_of(int batch, int k, int q_heads, int kv_heads, int head_dim) {
     const long long items = (long long)batch * kv_heads * tiles * z.plan.halves;
     const int pairs = device_sm_count() / 2;
     z.plan.splits = items > 0 && items <= pairs / 2 ? (int)(pairs / items) : 1;
-    z.plan.pairs = (int)std::min<long long>(items * z.plan.splits, pairs);
+    // A pair that finds no item costs about a microsecond (a padded batch has many): the
+    // grid is at most kUnits times the pairs that run at once.
+    z.plan.units = (int)std::min<long long>(items * z.plan.splits, (long long)kUnits * pairs);
     if (z.plan.splits > 1) {
         const size_t rows = (size_t)batch * k * q_heads * z.plan.splits;
         z.ml = align256(rows * sizeof(float2));
@@ -975,7 +1014,7 @@ cudaError_t launch(const PagedChunkParams &p, Sizes &z, cudaStream_t stream) {
         if (e != cudaSuccess) return e;
         if (dev >= 0 && dev < 64) configured[dev].store(1, std::memory_order_release);
     }
-    e = launch_dependent(kernel, dim3(2 * z.plan.pairs), dim3(kThreads),
+    e = launch_dependent(kernel, dim3(2 * z.plan.units), dim3(kThreads),
                          L::kAlloc, stream, p, z.plan, map_q, map_k, map_v);
     if (e != cudaSuccess || z.plan.splits == 1) return e;
     return launch_dependent(paged_chunk_merge_kernel<D>,

@@ -436,6 +436,35 @@ __device__ __forceinline__ void mma_commit_pair(uint64_t *bar) {
 }
 
 // ---------------------------------------------------------------------------
+// Taking over clusters of this grid that have not been launched yet: the answer (16
+// bytes, at the same offset in every CTA of the cluster, counted on the barrier there)
+// names the cluster's first CTA, or says that none is left; then nobody may ask again.
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ void ask_for_cluster(void *answer, uint64_t *bar) {
+    asm volatile(
+        "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes"
+        ".multicast::cluster::all.b128 [%0], [%1];" ::"r"(smem_u32(answer)),
+        "r"(smem_u32(bar))
+        : "memory");
+}
+
+// blockIdx.x of the cluster's first CTA, or -1.
+__device__ __forceinline__ int cluster_taken(const void *answer) {
+    uint32_t ok, x;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b128 a;\n\t"
+        "ld.shared.b128 a, [%2];\n\t"
+        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, a;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t"
+        "mov.u32 %1, 0;\n\t"
+        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, a;\n\t}"
+        : "=r"(ok), "=r"(x)
+        : "r"(smem_u32(answer))
+        : "memory");
+    return ok ? (int)x : -1;
+}
+
+// ---------------------------------------------------------------------------
 // Descriptors
 // ---------------------------------------------------------------------------
 // Shared-memory matrix descriptor for a 128-byte-swizzled operand:

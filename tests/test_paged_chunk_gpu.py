@@ -349,3 +349,12 @@ def test_cold_and_warm_caches_give_the_same_bits(q_heads, kv_heads, head_dim, ct
         c.out.fill_(7.0)
         c.call()
         assert torch.equal(first, c.out), i
+
+
+@pytest.mark.parametrize("counts", [None, [2600, 3, 0, 17]])
+def test_more_items_than_the_grid_has_cta_pairs(counts):
+    """64 heads share a KV head: four tokens an item, 650 of them a request; with counts, most
+    of a padded batch's CTA pairs find nothing to do."""
+    ctx = [100] if counts is None else [100, 0, 7, 500]
+    c = Case(ctx, 2600, 64, 1, 256, counts=counts, window=300, sinks=2, seed=19).device()
+    c.check(c.call(), rows=[0, 1, 2, 3, 4, 16, 1000, 1503, 2431, 2432, 2433, 2598, 2599])
