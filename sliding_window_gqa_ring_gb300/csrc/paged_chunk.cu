@@ -83,10 +83,11 @@ struct Lay {
     static constexpr int NS = D == 256 ? 4 : 3;
     static constexpr int kSlab = kRows * 128;           // 64 d of Q
     static constexpr int kOffQ = NS * kStage;
-    static constexpr int kOffOut = kOffQ + D / 64 * kSlab;
-    // head_dim 256: 32 rows of 128 bytes a softmax warp, on their way out
-    static constexpr int kOut = D == 256 ? 8 * 4096 : 0;
-    static constexpr int kOffMisc = kOffOut + kOut;
+    static constexpr int kOffOut = D == 512 ? kOffQ : kOffQ + D / 64 * kSlab;
+    // The output's way out: 32 rows of 128 bytes a softmax warp.  At head_dim 512 the place
+    // is the queries', and the next item's queries are loaded behind it.
+    static constexpr bool kOutInQ = D == 512;
+    static constexpr int kOffMisc = kOffQ + D / 64 * kSlab + (kOutInQ ? 0 : 8 * 4096);
     static constexpr int kMisc = 3072;
     static constexpr int kAlloc = kOffMisc + kMisc;
     static_assert(kAlloc <= 232448, "more dynamic shared memory than one CTA may use");
@@ -237,7 +238,7 @@ struct Shared {
     uint64_t full[NS];      // leader: a stage's bytes of both CTAs have landed
     uint64_t empty[NS];     // both: the products that read the stage are done
     uint64_t q_full;        // leader
-    uint64_t q_empty;       // both: an item's last scores are computed
+    uint64_t q_empty;       // both: an item's last scores are computed (and its output has left)
     uint64_t s_full[2];     // both: a tile's scores are in tensor memory
     uint64_t p_full[2];     // leader: its weights are
     uint64_t pv_done[2];    // both: a tile's value product is done (tiles in turn)
@@ -331,7 +332,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int rank = (int)tc::cluster_ctarank(), pair = blockIdx.x / 2;
 
-    if (threadIdx.x == 0) {
+    if (threadIdx.x == 96) {
         tc::tma_prefetch_map(&map_q);
         tc::tma_prefetch_map(&map_k);
         tc::tma_prefetch_map(&map_v);
@@ -340,7 +341,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
             tc::mbar_init(&sh->empty[i], 1);
         }
         tc::mbar_init(&sh->q_full, 1);
-        tc::mbar_init(&sh->q_empty, 1);
+        tc::mbar_init(&sh->q_empty, L::kOutInQ ? 9 : 1);
         for (int i = 0; i < 2; ++i) {
             tc::mbar_init(&sh->s_full[i], 1);
             tc::mbar_init(&sh->p_full[i], 16);
@@ -365,6 +366,11 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     }
     wait_for_prior_launch();
     let_next_launch_start();
+    // The first item is looked up while the barriers and tensor memory are made ready.
+    Items list;
+    Item it{};
+    bool found = false;
+    if (warp == 0) found = list.find(p, plan, lane, pair, it);
     tc::tc_fence_before();
     __syncthreads();
     tc::cluster_arrive();
@@ -392,11 +398,11 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         uint32_t cnt = 0, items = 0;
         bool alive = true;
         const uint32_t q_bytes = plan.tokens * p.group * 128;
-        Items list;
         uint32_t published = 0, asked = 0;
         // Both CTAs' producers get the same answers, the leader asks.  An answer's place is
         // used again after kJobs more: the other CTA is behind by less than the stage ring.
         int unit = pair, id = pair;
+        bool pending = false;
         auto ask = [&]() {
             if (lane == 0) {
                 tc::fence_proxy_async_smem();
@@ -405,21 +411,22 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                     tc::ask_for_cluster(&sh->answer[asked % kJobs], &sh->answered[asked % kJobs]);
             }
             __syncwarp();
+            pending = true;
         };
-        ask();
-        while (alive) {
+        for (bool first = true; alive; first = false) {
             Job tiles{};
-            Item it;
             if (unit >= 0) {
-                if (!list.find(p, plan, lane, id, it)) {
-                    // this pair's work is done: the next one's
+                if (!first) found = list.find(p, plan, lane, id, it);
+                if (!found) {
+                    // this pair's work is done: another's
+                    if (!pending) ask();
                     alive = warp_wait(&sh->answered[asked % kJobs], (asked / kJobs) & 1, abort_flag,
                                       p.dev_status);
                     if (!alive) break;
-                    const int first = tc::cluster_taken(&sh->answer[asked % kJobs]);
+                    const int taken_over = tc::cluster_taken(&sh->answer[asked % kJobs]);
                     ++asked;
-                    unit = id = first < 0 ? -1 : first / 2;
-                    if (unit >= 0) ask();
+                    pending = false;
+                    unit = id = taken_over < 0 ? -1 : taken_over / 2;
                     continue;
                 }
                 id += plan.units;
@@ -493,11 +500,12 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                 }
                 if (x > 0) load(true, prev, 0);
                 prev = row;
+                if (x == 0 && !pending && alive) ask();   // for the work after this
             }
         }
         // An answer that is still on its way lands before anyone leaves, and what both CTAs'
         // copies still carry.
-        if (!alive && unit >= 0) tc::mbar_wait(&sh->answered[asked % kJobs], (asked / kJobs) & 1);
+        if (!alive && pending) tc::mbar_wait(&sh->answered[asked % kJobs], (asked / kJobs) & 1);
         if (!alive && rank == 0) {
             if (items > 0) tc::mbar_wait(&sh->q_full, (items - 1) & 1);
             for (uint32_t i = cnt > NS ? cnt - NS : 0; i < cnt; ++i)
@@ -808,106 +816,57 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                 const int rr = quad * 32 + r, tt = rr * inv_group >> 16;
                 return tt < held ? tt * p.q_heads + rr - tt * p.group : -1;
             };
-            if constexpr (L::kOut > 0) {
-                // O leaves through shared memory, 128 bytes of each of the warp's 32 rows at a
-                // time, so that eight lanes write a whole line.
-                uint8_t *s_out = smem + L::kOffOut + (warp - 4) * 4096;
-                auto leave = [&](uint8_t *base, size_t row_bytes) {
-                    __syncwarp();
+            // O leaves through shared memory, 128 bytes of each of the warp's 32 rows at a
+            // time, so that eight lanes write a whole line.
+            uint8_t *s_out = smem + L::kOffOut + (warp - 4) * 4096;
+            auto leave = [&](uint8_t *base, size_t row_bytes) {
+                __syncwarp();
 #pragma unroll 4
-                    for (int e = 0; e < 8; ++e) {
-                        const int r = e * 4 + lane / 8, to = place(r);
-                        const uint4 v = *reinterpret_cast<const uint4 *>(
-                            s_out + r * 128 + ((lane ^ r) & 7) * 16);
-                        if (to >= 0)
-                            *reinterpret_cast<uint4 *>(base + (at + to) * row_bytes +
-                                                       (lane & 7) * 16) = v;
-                    }
-                    __syncwarp();
-                };
-#pragma unroll 1
-                for (int i = part * (kDV / 2); i < (part + 1) * (kDV / 2); i += 32) {
-                    uint32_t o[32];
-                    tc::tmem_ld32(t_o + lanes + i, o);
-                    tc::tmem_ld_wait();
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                    if (partial) {
-#pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            *reinterpret_cast<uint4 *>(s_out + lane * 128 + ((e ^ lane) & 7) * 16) =
-                                make_uint4(o[e * 4], o[e * 4 + 1], o[e * 4 + 2], o[e * 4 + 3]);
-                        leave(reinterpret_cast<uint8_t *>(plan.part_o + (size_t)split * D + d0 + i),
-                              (size_t)plan.splits * D * 4);
-                        continue;
-                    }
-                    const int half = (i & 32) / 8;   // of the 128 bytes
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        uint32_t w[4];
-#pragma unroll
-                        for (int z = 0; z < 4; ++z)
-                            w[z] = pack_bf16(__uint_as_float(o[e * 8 + 2 * z]),
-                                             __uint_as_float(o[e * 8 + 2 * z + 1]));
-                        *reinterpret_cast<uint4 *>(
-                            s_out + lane * 128 + (((e + half) ^ lane) & 7) * 16) =
-                            make_uint4(w[0], w[1], w[2], w[3]);
-                    }
-                    if (half)
-                        leave(reinterpret_cast<uint8_t *>(p.out + d0 + i - 32), D * 2);
+                for (int e = 0; e < 8; ++e) {
+                    const int r = e * 4 + lane / 8, to = place(r);
+                    const uint4 v = *reinterpret_cast<const uint4 *>(
+                        s_out + r * 128 + ((lane ^ r) & 7) * 16);
+                    if (to >= 0)
+                        *reinterpret_cast<uint4 *>(base + (at + to) * row_bytes +
+                                                   (lane & 7) * 16) = v;
                 }
-            } else {
-                // The stages and queries leave no shared memory: O leaves by quarters of a warp.
-                // Lanes 4 i .. 4 i + 3 hold 8 columns of rows i and i + 8 (and, of a second load,
-                // i + 16 and i + 24), two a lane.
-                const bool odd = lane & 1, high = lane & 2;
+                __syncwarp();
+            };
 #pragma unroll 1
-                for (int r16 = 0; r16 < 32; r16 += 16) {
-                    const int r[2] = {r16 + lane / 4, r16 + 8 + lane / 4};
-                    const int to[2] = {place(r[0]), place(r[1])};
-                    const float fr[2] = {__shfl_sync(kFull, f, r[0]), __shfl_sync(kFull, f, r[1])};
-#pragma unroll 1
-                    for (int i = part * (kDV / 2); i < (part + 1) * (kDV / 2); i += 32) {
-                        uint32_t o[16];
-                        tc::tmem_ld_16x256b_x4(t_o + lanes + ((uint32_t)r16 << 16) + i, o);
-                        tc::tmem_ld_wait();
+            for (int i = part * (kDV / 2); i < (part + 1) * (kDV / 2); i += 32) {
+                uint32_t o[32];
+                tc::tmem_ld32(t_o + lanes + i, o);
+                tc::tmem_ld_wait();
 #pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            if (partial) {
-                                float *dst = plan.part_o +
-                                             ((at + to[e]) * plan.splits + split) * D + d0 + i +
-                                             (lane & 3) * 2;
+                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                if (partial) {
 #pragma unroll
-                                for (int q = 0; q < 4; ++q)
-                                    if (to[e] >= 0)
-                                        *reinterpret_cast<float2 *>(dst + q * 8) =
-                                            make_float2(__uint_as_float(o[q * 4 + e * 2]) * fr[e],
-                                                        __uint_as_float(o[q * 4 + e * 2 + 1]) * fr[e]);
-                                continue;
-                            }
-                            // w[q]: columns 8 q + 2 (lane & 3) of the row; transposed among the
-                            // four lanes, so that lane q has the eight columns from 8 q on
-                            uint32_t w[4];
-#pragma unroll
-                            for (int q = 0; q < 4; ++q)
-                                w[q] = pack_bf16(__uint_as_float(o[q * 4 + e * 2]) * fr[e],
-                                                 __uint_as_float(o[q * 4 + e * 2 + 1]) * fr[e]);
-                            const uint32_t a0 = __shfl_xor_sync(kFull, odd ? w[0] : w[1], 1);
-                            const uint32_t a1 = __shfl_xor_sync(kFull, odd ? w[2] : w[3], 1);
-                            w[0] = odd ? a0 : w[0];
-                            w[1] = odd ? w[1] : a0;
-                            w[2] = odd ? a1 : w[2];
-                            w[3] = odd ? w[3] : a1;
-                            const uint32_t b0 = __shfl_xor_sync(kFull, high ? w[0] : w[2], 2);
-                            const uint32_t b1 = __shfl_xor_sync(kFull, high ? w[1] : w[3], 2);
-                            if (to[e] >= 0)
-                                *reinterpret_cast<uint4 *>(p.out + (at + to[e]) * D + d0 + i +
-                                                           (lane & 3) * 8) =
-                                    make_uint4(high ? b0 : w[0], high ? b1 : w[1],
-                                               high ? w[2] : b0, high ? w[3] : b1);
-                        }
-                    }
+                    for (int e = 0; e < 8; ++e)
+                        *reinterpret_cast<uint4 *>(s_out + lane * 128 + ((e ^ lane) & 7) * 16) =
+                            make_uint4(o[e * 4], o[e * 4 + 1], o[e * 4 + 2], o[e * 4 + 3]);
+                    leave(reinterpret_cast<uint8_t *>(plan.part_o + (size_t)split * D + d0 + i),
+                          (size_t)plan.splits * D * 4);
+                    continue;
                 }
+                const int half = (i & 32) / 8;   // of the 128 bytes
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    uint32_t w[4];
+#pragma unroll
+                    for (int z = 0; z < 4; ++z)
+                        w[z] = pack_bf16(__uint_as_float(o[e * 8 + 2 * z]),
+                                         __uint_as_float(o[e * 8 + 2 * z + 1]));
+                    *reinterpret_cast<uint4 *>(
+                        s_out + lane * 128 + (((e + half) ^ lane) & 7) * 16) =
+                        make_uint4(w[0], w[1], w[2], w[3]);
+                }
+                if (half)
+                    leave(reinterpret_cast<uint8_t *>(p.out + d0 + i - 32), D * 2);
+            }
+            if constexpr (L::kOutInQ) {
+                tc::fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(&sh->q_empty);
             }
             tc::tc_fence_before();
         }
@@ -922,41 +881,62 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     }
 }
 
-// Merges the pieces of split items: one CTA a row of the output.
+// Merges the pieces of split items: one CTA a row of the output, 16 bytes of it a thread,
+// kFlight pieces' loads in flight.
 template <int D>
 __global__ void __launch_bounds__(D / 4) paged_chunk_merge_kernel(
     const __grid_constant__ PagedChunkParams p, const Plan plan) {
+    constexpr int kFlight = 8;
     wait_for_prior_launch();
     let_next_launch_start();
-    const int j = blockIdx.x / p.q_heads % p.k, b = blockIdx.x / p.q_heads / p.k;
+    const size_t at = blockIdx.x;
+    const int row = blockIdx.x / p.q_heads;
+    const int b = row / p.k, j = row - b * p.k;
+    const float2 *ml = plan.part_ml + at * plan.splits;
+    const float4 *o = reinterpret_cast<const float4 *>(plan.part_o + at * plan.splits * D) +
+                      threadIdx.x;
     const Request rq = load_request(p, b);
     if (!request_ok(p, rq) || j >= rq.n) return;
     const int j0 = j / (2 * plan.tokens) * 2 * plan.tokens;
     const Keys keys(p, (int)rq.ctx + j0, (int)rq.ctx + min(j0 + 2 * plan.tokens, rq.n) - 1);
-    const size_t at = blockIdx.x;
-    float top = -INFINITY;
-    for (int s = 0; s < plan.splits; ++s)
-        if (split_at(keys.count, s, plan.splits) < split_at(keys.count, s + 1, plan.splits))
-            top = fmaxf(top, plan.part_ml[at * plan.splits + s].x);
-    const float ref = top == -INFINITY ? 0.f : top;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    float sum = 0.f;
-    for (int s = 0; s < plan.splits; ++s) {
-        if (split_at(keys.count, s, plan.splits) == split_at(keys.count, s + 1, plan.splits))
-            continue;
-        const float2 ml = plan.part_ml[at * plan.splits + s];
-        const float w = fast_exp2(ml.x - ref);
-        const float4 v =
-            reinterpret_cast<const float4 *>(plan.part_o + (at * plan.splits + s) * D)[threadIdx.x];
-        sum = fmaf(w, ml.y, sum);
-        o.x = fmaf(w, v.x, o.x);
-        o.y = fmaf(w, v.y, o.y);
-        o.z = fmaf(w, v.z, o.z);
-        o.w = fmaf(w, v.w, o.w);
+    // splits without a tile wrote nothing
+    auto written = [&](int s) {
+        return s < plan.splits &&
+               split_at(keys.count, s, plan.splits) < split_at(keys.count, s + 1, plan.splits);
+    };
+    float top = -INFINITY, sum = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+    for (int s0 = 0; s0 < plan.splits; s0 += kFlight) {
+        float2 l[kFlight];
+        float4 v[kFlight];
+#pragma unroll
+        for (int i = 0; i < kFlight; ++i) {
+            const bool have = written(s0 + i);
+            l[i] = have ? ml[s0 + i] : make_float2(-INFINITY, 0.f);
+            v[i] = have ? o[(size_t)(s0 + i) * (D / 4)] : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+        float most = top;
+#pragma unroll
+        for (int i = 0; i < kFlight; ++i) most = fmaxf(most, l[i].x);
+        const float ref = most == -INFINITY ? 0.f : most;
+        const float keep = fast_exp2(top - ref);
+        top = most;
+        sum *= keep;
+        acc.x *= keep, acc.y *= keep, acc.z *= keep, acc.w *= keep;
+#pragma unroll
+        for (int i = 0; i < kFlight; ++i) {
+            const float w = fast_exp2(l[i].x - ref);
+            sum = fmaf(w, l[i].y, sum);
+            acc.x = fmaf(w, v[i].x, acc.x);
+            acc.y = fmaf(w, v[i].y, acc.y);
+            acc.z = fmaf(w, v[i].z, acc.z);
+            acc.w = fmaf(w, v[i].w, acc.w);
+        }
     }
     const float f = 1.f / sum;
     reinterpret_cast<uint2 *>(p.out + at * D)[threadIdx.x] =
-        make_uint2(pack_bf16(o.x * f, o.y * f), pack_bf16(o.z * f, o.w * f));
+        make_uint2(pack_bf16(acc.x * f, acc.y * f), pack_bf16(acc.z * f, acc.w * f));
 }
 
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
