@@ -201,6 +201,9 @@ struct SkShared {
     long long ucost0;             // cost position of the first segment's unit
     int segc;                     // cost charged per unit, in tiles
     int special_last;             // the units' special tiles come last (see order_tile)
+    // kPagedWindow: rows that see a key with a value that is not finite which other
+    // rows of the tile do not see, of two segments in turn
+    unsigned long long poison[2];
     // FP8 unit mode: the units taken, in order (only FP8 kernels reserve the
     // space: the misc area is 128 bytes with bf16 caches, 256 with FP8)
     UnitDesc uq[kUnitQ];
@@ -213,6 +216,8 @@ __device__ __forceinline__ int request_tiles(const AttnParams &p, int b, int *id
                                              int *special) {
     *special = -1;
     if (!request_ok(p, b, id, ctx)) return 0;
+    if (p.source == KeySource::kPagedWindow)
+        return *id > 0 ? WindowTiles(p, *ctx).count(*ctx + *id) : 0;
     return tc_request_tiles(p.source, p.window, p.k, *ctx + p.k, p.fused != 0, special);
 }
 
@@ -733,10 +738,13 @@ struct KeyInfo {
 
 }  // namespace
 
+// WIN: pages under a window with first tokens that stay visible (kPagedWindow): tiles of
+// two runs, query counts per request, bf16 outputs, and values that are not finite kept
+// from the rows that do not see them.
 // LP: the row sums L^T are kept per lane by the softmax threads (each thread
 // adds its key's P of every row into its own lane, the lanes are added up once
 // per segment) instead of the MMA thread's ONES . P^T product.
-template <int D, int N, int NS, int MINB, int NR = 0, bool LP = false>
+template <int D, int N, int NS, int MINB, int NR = 0, bool LP = false, bool WIN = false>
 __global__ void __launch_bounds__(NR > 0 ? kThreads + kConvThreads : kThreads, MINB)
     attn_tc_kernel(const AttnParams p, const TcPlan plan, const __grid_constant__ TcMaps maps) {
     using L = Layout<D, N, NS, NR>;
@@ -754,7 +762,8 @@ __global__ void __launch_bounds__(NR > 0 ? kThreads + kConvThreads : kThreads, M
     const int upo = paired ? p.kv_heads : upr;      // units per request in the flattened order
     const int my_rg = paired ? (int)(blockIdx.x & 1) : -1;
     const bool ring = p.source == KeySource::kRing;
-    const bool paged = p.source == KeySource::kPaged;
+    const bool paged = p.source == KeySource::kPaged || WIN;
+    static_assert(!WIN || (NR == 0 && !LP), "windows over pages: bf16, stream-K");
 
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>(
@@ -991,7 +1000,8 @@ __global__ void __launch_bounds__(NR > 0 ? kThreads + kConvThreads : kThreads, M
                     // A tile never straddles pages (page_rows is a multiple of
                     // 128).  A page id outside the pool loads the zero fill
                     // past the tensor's end and is reported.
-                    const long long t = (long long)i * kTileKeys;
+                    const long long t = WIN ? WindowTiles(p, ps.ctx).base(i)
+                                            : (long long)i * kTileKeys;
                     const int page = page_of(ps.b, (int)(t / p.page_rows));
                     if (page < 0 || page >= p.num_pages) {
                         set_status(p.dev_status, CARAT_DEV_BAD_CACHE_ID);
@@ -1113,6 +1123,10 @@ __global__ void __launch_bounds__(NR > 0 ? kThreads + kConvThreads : kThreads, M
             if (request_ok(p, b, &id, &ctx)) continue;
             if (t == 0) set_status(p.dev_status, request_error_bits(p, id, ctx));
             const size_t per = (size_t)p.k * p.q_heads * D;
+            if constexpr (WIN) {
+                for (size_t x = t; x < per; x += 128) p.out16[(size_t)b * per + x] = 0x7fff;
+                continue;
+            }
             float *o = p.out + (size_t)b * per;
             for (size_t x = t; x < per; x += 128) o[x] = __int_as_float(0x7fc00000);
         }
@@ -1429,6 +1443,27 @@ __global__ void __launch_bounds__(NR > 0 ? kThreads + kConvThreads : kThreads, M
                                 o[ob * 128] = __uint_as_float(o16[ob][e]) * inv;
                         }
                     }
+                } else if (WIN && pe.whole) {
+                    int jr = (cb * 16) / p.group, hp = (cb * 16) - jr * p.group;
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        const int r = cb * 16 + e;
+                        if (r < pe.rows_here) {
+                            const float inv = ((sk->poison[pe.si & 1] >> r) & 1)
+                                                  ? NAN
+                                                  : 1.f / __uint_as_float(l16[e]);
+                            uint16_t *o = p.out16 + (((size_t)pe.b * p.k + jr) * p.q_heads +
+                                                     (size_t)pe.c * p.group + hp) * D + t;
+#pragma unroll
+                            for (int ob = 0; ob < KS; ++ob)
+                                o[ob * 128] = __bfloat16_as_ushort(
+                                    __float2bfloat16_rn(__uint_as_float(o16[ob][e]) * inv));
+                        }
+                        if (++hp == p.group) {
+                            hp = 0;
+                            ++jr;
+                        }
+                    }
                 } else if (pe.whole) {
                     // The segment saw every key of its rows: normalise and write.
                     // Row r = j * group + h' goes to out[b][j][c * group + h'].
@@ -1460,7 +1495,9 @@ __global__ void __launch_bounds__(NR > 0 ? kThreads + kConvThreads : kThreads, M
 #pragma unroll
                             for (int ob = 0; ob < KS; ++ob)
                                 p.part_o[(base + r) * D + ob * 128 + t] =
-                                    __uint_as_float(o16[ob][e]) * p.out_scale;
+                                    WIN && ((sk->poison[pe.si & 1] >> r) & 1)
+                                        ? NAN
+                                        : __uint_as_float(o16[ob][e]) * p.out_scale;
                         }
                     }
                 }
@@ -1503,9 +1540,12 @@ __global__ void __launch_bounds__(NR > 0 ? kThreads + kConvThreads : kThreads, M
             const int new_tile = p.fused ? sg.special : -1;    // this step's rows (fused append)
             // Tokens the caches hold for this call: all key_count of them, or
             // with a fused append only the context_length older ones.
-            const long long held_tokens = p.fused ? ctx : ctx + p.k;
+            const int queries = WIN ? sg.id : p.k;
+            const long long held_tokens = p.fused ? ctx : ctx + queries;
             const int pos0 = sg.rg * plan.pos_per_group;       // first position of the group
-            const int npos = min(plan.pos_per_group, p.k - pos0);
+            const int npos = min(plan.pos_per_group, queries - pos0);
+            const WindowTiles wt(p, WIN ? ctx : 0);
+            if (WIN && t == 0) sk->poison[si & 1] = 0;   // (a barrier before it is added to)
             const int row0 = pos0 * p.group;                   // first row of the group
             const int rows_here = npos * p.group;
             // Slot that holds the newest token the caches hold (ring source).
@@ -1574,6 +1614,12 @@ __global__ void __launch_bounds__(NR > 0 ? kThreads + kConvThreads : kThreads, M
                     if (delta < 0) delta += p.window;
                     ki.pos = (slot < p.window && newest >= 0) ? newest - delta : -1;
                     ki.data = ki.pos >= 0;
+                } else if constexpr (WIN) {
+                    // data: some query of the group sees the key
+                    const long long u = wt.base(i) + t;
+                    ki.pos = u < held_tokens ? u : -1;
+                    ki.data = ki.pos >= 0 &&
+                              (p.window == 0 || u > ctx - p.window || u < p.sinks);
                 } else {
                     const long long u = (long long)i * kTileKeys + t;
                     ki.pos = u < held_tokens ? u : -1;
@@ -1585,7 +1631,9 @@ __global__ void __launch_bounds__(NR > 0 ? kThreads + kConvThreads : kThreads, M
                 if (ki.data) {
                     const long long d0 = ki.pos - (ctx + pos0);
                     const long long jlo = d0 < 0 ? 0 : d0;
-                    long long jhi = ring ? d0 + p.window : npos;
+                    long long jhi = ring || (WIN && p.window > 0 && ki.pos >= p.sinks)
+                                        ? d0 + p.window
+                                        : npos;
                     if (jhi > npos) jhi = npos;
                     if (jlo < jhi)
                         rowmask = low_bits((int)jhi * p.group) & ~low_bits((int)jlo * p.group);
@@ -1769,7 +1817,11 @@ __global__ void __launch_bounds__(NR > 0 ? kThreads + kConvThreads : kThreads, M
                         i == disp_tile || i == new_tile ||
                         (ring && ((long long)(i + 1) * kTileKeys >
                                   min((long long)p.window, held_tokens))) ||
-                        (!ring && (long long)(i + 1) * kTileKeys > held_tokens);
+                        (!ring && !WIN && (long long)(i + 1) * kTileKeys > held_tokens) ||
+                        // some query does not see some key of the tile
+                        (WIN && (wt.base(i) + kTileKeys - 1 > ctx ||
+                                 (p.window > 0 && wt.base(i) <= ctx + queries - 1 - p.window &&
+                                  wt.base(i) + kTileKeys - 1 >= p.sinks)));
                     // Fused append into a ring: the one CTA that loads tile i
                     // overwrites slots of the tile once its own copies of the
                     // tile have landed.
@@ -1801,6 +1853,48 @@ __global__ void __launch_bounds__(NR > 0 ? kThreads + kConvThreads : kThreads, M
                                 for (int q = 0; q < 8; ++q)
                                     *reinterpret_cast<uint4 *>(vrow + db * kDispBoxBytes +
                                                                q * 16) = make_uint4(0, 0, 0, 0);
+                        }
+                    } else if (WIN && tile_partial) {
+                        // V rows that no query sees are zeroed; one that some see and some
+                        // do not is looked through, and zeroed where it holds a value that
+                        // is not finite: the rows that see it become NaN.
+                        const bool some = ki.data && rowmask != low_bits(rows_here);
+                        bool bad = false;
+                        for (int vs = 0; vs < KS; ++vs) {
+                            const uint32_t x_cnt = cnt_base + stages_before(v_part(idx, n)) + vs;
+                            const int s = x_cnt % NS;
+                            if (!wait_or_abort(&full[s], (x_cnt / NS) & 1, abort_flag,
+                                               p.dev_status)) {
+                                alive = false;
+                                break;
+                            }
+                            if (!some) continue;
+                            const uint8_t *row0p = smem + s * kStageBytes + t * 128;
+                            __nv_bfloat162 acc = __float2bfloat162_rn(0.f);
+#pragma unroll 4
+                            for (int q = 0; q < 16; ++q) {
+                                const uint4 v = *reinterpret_cast<const uint4 *>(
+                                    row0p + (q >> 3) * kBoxBytes + ((q + t) & 7) * 16);
+                                const uint32_t word[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                                for (int w = 0; w < 4; ++w)
+                                    acc = __hfma2(*reinterpret_cast<const __nv_bfloat162 *>(&word[w]),
+                                                  __float2bfloat162_rn(0.f), acc);
+                            }
+                            bad |= __hisnan(acc.x) || __hisnan(acc.y);
+                        }
+                        if (alive && (bad || !ki.data)) {
+                            if (bad) atomicOr(&sk->poison[si & 1], (unsigned long long)rowmask);
+                            for (int vs = 0; vs < KS; ++vs) {
+                                const uint32_t x_cnt =
+                                    cnt_base + stages_before(v_part(idx, n)) + vs;
+                                uint8_t *row0p = smem + (x_cnt % NS) * kStageBytes + t * 128;
+#pragma unroll
+                                for (int q = 0; q < 16; ++q)
+                                    *reinterpret_cast<uint4 *>(row0p + (q >> 3) * kBoxBytes +
+                                                               (q & 7) * 16) =
+                                        make_uint4(0, 0, 0, 0);
+                            }
                         }
                     } else if (tile_partial || tile_writes) {
                         for (int vs = 0; vs < KS; ++vs) {
@@ -2063,7 +2157,7 @@ __global__ void __launch_bounds__(NR > 0 ? kThreads + kConvThreads : kThreads, M
 // first range + q (with the paired schedule, CTA 2g + the unit's row group).  It starts before the attention grid
 // ends (programmatic dependent launch) and waits for it with
 // griddepcontrol.wait, which also makes the grid's writes visible.
-template <int D>
+template <int D, bool WIN = false>
 __global__ void __launch_bounds__(D / 4) attn_fixup_kernel(const AttnParams p, int upr,
                                                             int row_groups, int pos_per_group,
                                                             int slot_rows, int slots, int paired) {
@@ -2074,11 +2168,11 @@ __global__ void __launch_bounds__(D / 4) attn_fixup_kernel(const AttnParams p, i
     if (b >= p.batch) return;
     // the request's validity and the unit's entry, in one round trip
     const long long ctx = p.context_lengths[b];
-    const int id = p.ids ? p.ids[b] : b;
+    const int id = WIN ? (p.new_counts ? p.new_counts[b] : p.k) : p.ids ? p.ids[b] : b;
     const int4 e = p.units[u];
     if (!request_valid(p, id, ctx)) return;     // NaN already written
     const int pos0 = rg * pos_per_group;
-    const int npos = min(pos_per_group, p.k - pos0);
+    const int npos = min(pos_per_group, (WIN ? id : p.k) - pos0);
     if (r >= npos * p.group) return;
     const int np = e.y;
     if (np == 0) return;                          // whole: already written
@@ -2105,11 +2199,13 @@ __global__ void __launch_bounds__(D / 4) attn_fixup_kernel(const AttnParams p, i
         float2 v0 = make_float2(-INFINITY, 0.f), v1 = v0;
         if (lane < np) v0 = p.part_ml[piece_base(lane) + r];
         if (lane + 32 < np) v1 = p.part_ml[piece_base(lane + 32) + r];
-        float M = fmaxf(v0.y > 0.f ? v0.x : -INFINITY, v1.y > 0.f ? v1.x : -INFINITY);
+        // (WIN: a sum that is NaN counts)
+        const bool has0 = WIN ? v0.y != 0.f : v0.y > 0.f, has1 = WIN ? v1.y != 0.f : v1.y > 0.f;
+        float M = fmaxf(has0 ? v0.x : -INFINITY, has1 ? v1.x : -INFINITY);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, o));
-        const float w0 = v0.y > 0.f ? fast_exp2(v0.x - M) : 0.f;
-        const float w1 = v1.y > 0.f ? fast_exp2(v1.x - M) : 0.f;
+        const float w0 = has0 ? fast_exp2(v0.x - M) : 0.f;
+        const float w1 = has1 ? fast_exp2(v1.x - M) : 0.f;
         float lsum = v0.y * w0 + v1.y * w1;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) lsum += __shfl_xor_sync(kFull, lsum, o);
@@ -2141,8 +2237,16 @@ __global__ void __launch_bounds__(D / 4) attn_fixup_kernel(const AttnParams p, i
         }
     }
     const int row = pos0 * p.group + r, j = row / p.group, hp = row - j * p.group;
-    reinterpret_cast<float4 *>(
-        p.out + (((size_t)b * p.k + j) * p.q_heads + (size_t)c * p.group + hp) * D)[d4] = acc;
+    const size_t out_row = ((size_t)b * p.k + j) * p.q_heads + (size_t)c * p.group + hp;
+    if constexpr (WIN) {
+        const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x, acc.y);
+        const __nv_bfloat162 hi = __floats2bfloat162_rn(acc.z, acc.w);
+        reinterpret_cast<uint2 *>(p.out16 + out_row * D)[d4] =
+            make_uint2(*reinterpret_cast<const uint32_t *>(&lo),
+                       *reinterpret_cast<const uint32_t *>(&hi));
+    } else {
+        reinterpret_cast<float4 *>(p.out + out_row * D)[d4] = acc;
+    }
 }
 
 // ---------------------------------------------------------------------------
@@ -2151,12 +2255,12 @@ __global__ void __launch_bounds__(D / 4) attn_fixup_kernel(const AttnParams p, i
 
 namespace {
 
-template <int D, int N, int NS, int MINB, int NR = 0, bool LP = false>
+template <int D, int N, int NS, int MINB, int NR = 0, bool LP = false, bool WIN = false>
 cudaError_t launch_tc(const AttnParams &p, const TcPlan &plan, const TcMaps &maps, int grid,
                       cudaStream_t stream) {
     using L = Layout<D, N, NS, NR>;
     static_assert(MINB == 1 || 2 * (L::kAlloc + 1024) <= 233472, "two CTAs must fit one SM");
-    auto kernel = attn_tc_kernel<D, N, NS, MINB, NR, LP>;
+    auto kernel = attn_tc_kernel<D, N, NS, MINB, NR, LP, WIN>;
     static int configured_devices[64] = {0};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -2184,7 +2288,7 @@ cudaError_t launch_tc(const AttnParams &p, const TcPlan &plan, const TcMaps &map
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     const int upr = p.kv_heads * plan.row_groups;
-    e = cudaLaunchKernelEx(&cfg, attn_fixup_kernel<D>, p, upr, plan.row_groups,
+    e = cudaLaunchKernelEx(&cfg, attn_fixup_kernel<D, WIN>, p, upr, plan.row_groups,
                            plan.pos_per_group, N, plan.paired ? grid / 2 : grid, plan.paired);
     count_launches(1);
     return e;

@@ -20,6 +20,9 @@ enum class KeySource : int {
     kLinear = 1,  // global layer: cache row t holds position t, t < key_count
     kPaged = 2,   // global layer in pages: position t is row t % page_rows of page
                   // page_table[b][t / page_rows]
+    kPagedWindow = 3,  // the same under a window with first tokens that stay visible,
+                       // query counts per request and bf16 outputs; a request's `id`
+                       // is its query count
 };
 
 // Everything an attention launch needs; passed by value as a kernel argument.
@@ -66,6 +69,11 @@ struct AttnParams {
     int max_pages;
     int page_rows;
     int num_pages;
+    // kPagedWindow: the first `sinks` tokens stay visible; queries of each request
+    // (nullptr: k); the output (instead of `out`)
+    int sinks;
+    const int32_t *new_counts;
+    uint16_t *out16;
     float scale_log2;           // softmax scale * log2(e) (FP8: times the K scale)
     float out_scale = 1.f;      // FP8: the V scale, applied to the output
     KeySource source;
@@ -126,6 +134,8 @@ __device__ __forceinline__ void set_status(int *status, int bits) {
 
 // Whether a request's context length and cache/ring id are in range.
 __device__ __forceinline__ bool request_valid(const AttnParams &p, int id, long long ctx) {
+    if (p.source == KeySource::kPagedWindow)
+        return ctx >= 0 && id >= 0 && id <= p.k && ctx + id <= p.capacity;
     if (ctx < 0 || (p.source != KeySource::kRing && ctx + p.k > p.capacity)) return false;
     return id >= 0 && id < p.num_ids;
 }
@@ -135,7 +145,9 @@ __device__ __forceinline__ bool request_valid(const AttnParams &p, int id, long 
 __device__ __forceinline__ bool request_ok(const AttnParams &p, int b, int *id_out,
                                            long long *ctx_out) {
     const long long ctx = p.context_lengths[b];
-    const int id = p.ids ? p.ids[b] : b;
+    const int id = p.source == KeySource::kPagedWindow ? (p.new_counts ? p.new_counts[b] : p.k)
+                   : p.ids                             ? p.ids[b]
+                                                       : b;
     *id_out = id;
     *ctx_out = ctx;
     return request_valid(p, id, ctx);
@@ -143,6 +155,7 @@ __device__ __forceinline__ bool request_ok(const AttnParams &p, int b, int *id_o
 
 // CARAT_DEV_* bits describing why request_ok rejected a request.
 __device__ __forceinline__ int request_error_bits(const AttnParams &p, int id, long long ctx) {
+    if (p.source == KeySource::kPagedWindow) return CARAT_DEV_BAD_CONTEXT;
     int bits = 0;
     if (ctx < 0 || (p.source != KeySource::kRing && ctx + p.k > p.capacity))
         bits |= CARAT_DEV_BAD_CONTEXT;
@@ -180,6 +193,24 @@ __host__ __device__ __forceinline__ int tc_request_tiles(KeySource src, int wind
     *special_tile = -1;
     return (int)((key_count + 127) / 128);
 }
+
+// kPagedWindow: the 128-key tiles that a request's queries see, those of the first tokens,
+// then those from the first query's window on.
+struct WindowTiles {
+    int sinks, first;   // tiles of the first tokens; the window's first tile
+    __device__ __forceinline__ WindowTiles(const AttnParams &p, long long ctx) {
+        const long long lo = p.window > 0 ? ctx - p.window + 1 : 0;
+        first = lo > 0 ? (int)(lo / 128) : 0;
+        sinks = p.sinks > 0 ? min((p.sinks - 1) / 128 + 1, first) : 0;
+    }
+    __device__ __forceinline__ int count(long long keys) const {
+        return sinks + (int)((keys - 1) / 128) - first + 1;
+    }
+    // first position of tile i
+    __device__ __forceinline__ long long base(int i) const {
+        return (long long)(i < sinks ? i : first + i - sinks) * 128;
+    }
+};
 
 // Row of the paged pool that holds position t of request b, or -1 when the
 // page table entry is outside the pool.
@@ -343,6 +374,9 @@ bool tc_fp8_supported(int head_dim, int group, int k);   // FP8 e4m3 rings
 int tc_units_per_request(int group, int k, int kv_heads);
 cudaError_t launch_attention_tc(const AttnParams &p, int grid, bool unit_mode, bool fp8,
                                 cudaStream_t stream, bool deep = false);
+// The same for kPagedWindow (attention_tc_window.cu): at most 64 rows a KV head, stream-K.
+bool tc_window_supported(int head_dim, int group, int k);
+cudaError_t launch_attention_tc_window(const AttnParams &p, int grid, cudaStream_t stream);
 // Whether a one-CTA-per-SM kernel with a deep stage ring exists for this
 // shape (used for calls with at most one tile per SM).
 bool tc_has_deep_variant(int head_dim, int rows_per_tile);

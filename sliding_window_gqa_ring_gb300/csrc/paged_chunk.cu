@@ -33,8 +33,10 @@
 // rows behind the last key, before the product; a row that sees such a key is written as
 // NaN.
 //
-// Few items (fewer than pairs of SMs): the key tiles of an item are split over CTA pairs,
-// each writes (max, sum, unnormalised O), and a second launch merges them.
+// Few items: their key tiles are split over CTA pairs, each piece leaves (max, sum,
+// unnormalised O) and a second launch merges them.  How long a piece is goes by the
+// lengths on the device: the pieces are alike and their number fits the pairs, whether one
+// long request is among short ones or not.
 //
 // Schedule.  The grid has a CTA pair for every item, up to a few times the pairs that fit;
 // a pair that has finished takes over the work of one that has not been launched (cluster
@@ -71,6 +73,7 @@ constexpr int kDV = 256;                // value dimensions of an item
 constexpr int kStage = 32768;           // K: 64 keys x 256 d, or V: 128 keys x 128 d
 constexpr int kThreads = 384, kSoftmax = 256;
 constexpr int kJobs = 4;                // items handed to the other roles
+constexpr int kPieceCost = 3;           // of a piece besides its key tiles, in key tiles
 constexpr int kUnits = 8;               // CTA pairs of the grid, times the pairs that fit
 constexpr int kMasked = 8;              // masked tiles of an item: 3 + 3 + 1 at most
 constexpr uint32_t kFull = 0xffffffffu;
@@ -109,10 +112,12 @@ __device__ __forceinline__ bool request_ok(const PagedChunkParams &p, const Requ
 struct Plan {
     int tokens;      // of a CTA
     int halves;      // value halves
-    int splits;
+    int splits;      // most pieces of an item
+    int by_length;   // how many goes by the requests' lengths (else all have `splits`)
     int units;       // CTA pairs of the grid: pair u has the items u, u + units, ...
     float2 *part_ml; // [B k Hq][splits]
     float *part_o;   // [B k Hq][splits][D]
+    int *pieces;     // [B] pieces of a request's items
 };
 
 // Key tiles of the rows at positions [lo, hi]: the sinks', then the window's.  Positions
@@ -147,22 +152,93 @@ __device__ __forceinline__ int split_at(int count, int s, int splits) {
 
 // One pair's share of a request's chunk for one KV head.
 struct Item {
-    int b, c, vh, split;
+    int b, c, vh, split, splits;
     int j0, n, ctx;        // the pair's first token; the request's tokens, and before them
 };
+
+// Row tiles of a request, and key tiles of the last (the longest).
+struct Load {
+    int rows, keys;
+};
+__device__ __forceinline__ Load load_of(const PagedChunkParams &p, const Plan &plan,
+                                        const Request &rq) {
+    if (!request_ok(p, rq) || rq.n == 0) return {0, 0};
+    const int span = 2 * plan.tokens, rows = (rq.n + span - 1) / span;
+    return {rows, Keys(p, (int)rq.ctx + (rows - 1) * span, (int)rq.ctx + rq.n - 1).count};
+}
+
+// Pieces of an item that has this many key tiles.
+__device__ __forceinline__ int pieces_of(const Plan &plan, int keys, int length) {
+    return min(plan.splits, max(1, (keys + length - 1) / length));
+}
+
+// Key tiles of a piece where requests differ, by a whole warp: of 32 lengths between a
+// quarter of and nearly four times a pair's share of all tiles, the one whose rounds of pieces
+// take the least, a piece costing its tiles and kPieceCost for its start, its output and
+// its share of the merge.
+__device__ __noinline__ int piece_length(const PagedChunkParams &p, const Plan &plan, int lane) {
+    const int per_tile = p.kv_heads * plan.halves;
+    float total = 0.f;
+    Load held{};
+    for (int base = 0; base < p.batch; base += 32) {
+        held = {0, 0};
+        if (base + lane < p.batch) held = load_of(p, plan, load_request(p, base + lane));
+        total += (float)held.rows * held.keys;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(kFull, total, o);
+    const float share = total * per_tile / plan.units;
+    const int length = max(1, (int)(fast_exp2((lane - 16) * 0.125f) * share + 0.5f));
+    int count = 0, longest = 0;
+    for (int base = 0; base < p.batch; base += 32) {
+        if (p.batch > 32) {
+            held = {0, 0};
+            if (base + lane < p.batch) held = load_of(p, plan, load_request(p, base + lane));
+        }
+        for (int i = 0; i < min(32, p.batch - base); ++i) {
+            const int rows = __shfl_sync(kFull, held.rows, i);
+            const int keys = __shfl_sync(kFull, held.keys, i);
+            if (rows == 0) continue;
+            const int n = pieces_of(plan, keys, length);
+            count += rows * n;
+            longest = max(longest, (keys + n - 1) / n);
+        }
+    }
+    const float cost = (float)((count * per_tile + plan.units - 1) / plan.units) *
+                       (longest + kPieceCost);
+    float best = cost;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) best = fminf(best, __shfl_xor_sync(kFull, best, o));
+    return __shfl_sync(kFull, length, __ffs(__ballot_sync(kFull, cost == best)) - 1);
+}
 
 // The items in order, request after request, found by a whole warp.  Requests are looked at
 // 32 at a time, one a lane.
 struct Items {
+    int length = 0;        // key tiles of a piece (items are split)
     int base = -32;        // first request held
     int upto = 0;          // items of the held requests up to this lane's, and before
     int before = 0;        // items before the held requests
-    int n = 0, tiles = 0, ctx = 0;   // this lane's request
+    int n = 0, tiles = 0, ctx = 0, splits = 1;   // this lane's request
 
     // Item number id, or false: there are fewer.
     __device__ __forceinline__ bool find(const PagedChunkParams &p, const Plan &plan, int lane,
                                          int id, Item &it) {
-        const int per_tile = p.kv_heads * plan.halves * plan.splits;
+        const int per_split = p.kv_heads * plan.halves;
+        if (plan.by_length && length == 0) {
+            // Requests alike: as many pieces as pairs, in one round.  (The search takes about
+            // 3 us.)
+            Load held{};
+            if (lane < p.batch) held = load_of(p, plan, load_request(p, lane));
+            const int keys = __reduce_max_sync(kFull, held.keys);
+            const int rows = __reduce_add_sync(kFull, held.rows);
+            if (p.batch <= 32 && __all_sync(kFull, held.rows == 0 || held.keys == keys)) {
+                const int pieces = min(plan.splits, max(1, plan.units / max(1, rows * per_split)));
+                length = max(1, (keys + pieces - 1) / pieces);
+            } else {
+                length = piece_length(p, plan, lane);
+            }
+        }
         if (id < before) {
             base = -32;
             before = 0;
@@ -172,14 +248,16 @@ struct Items {
             if (hit) {
                 const int src = __ffs(hit) - 1;
                 const int t_src = __shfl_sync(kFull, tiles, src);
+                it.splits = __shfl_sync(kFull, splits, src);
+                const int per_tile = per_split * it.splits;
                 int rest = id - (__shfl_sync(kFull, upto, src) - t_src * per_tile);
                 it.b = base + src;
                 it.n = __shfl_sync(kFull, n, src);
                 it.ctx = __shfl_sync(kFull, ctx, src);
                 const int tile = t_src - 1 - rest / per_tile;   // the longest first
                 rest %= per_tile;
-                it.split = rest % plan.splits;
-                rest /= plan.splits;
+                it.split = rest % it.splits;
+                rest /= it.splits;
                 it.vh = rest % plan.halves;
                 it.c = rest / plan.halves;
                 it.j0 = tile * 2 * plan.tokens;
@@ -189,13 +267,16 @@ struct Items {
             if (base >= 0) before = __shfl_sync(kFull, upto, 31);
             base += 32;
             tiles = 0;
+            splits = 1;
             if (base + lane < p.batch) {
                 const Request rq = load_request(p, base + lane);
                 ctx = (int)rq.ctx;
                 n = rq.n;
-                if (request_ok(p, rq)) tiles = (n + 2 * plan.tokens - 1) / (2 * plan.tokens);
+                const Load load = load_of(p, plan, rq);
+                tiles = load.rows;
+                splits = plan.by_length ? pieces_of(plan, load.keys, length) : plan.splits;
             }
-            upto = tiles * per_tile;
+            upto = tiles * per_split * splits;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const int y = __shfl_up_sync(kFull, upto, o);
@@ -225,8 +306,8 @@ __device__ __forceinline__ Job job_of(const PagedChunkParams &p, const Plan &pla
     Job j;
     j.it = it;
     j.keys = Keys(p, it.ctx + it.j0, it.ctx + min(it.j0 + 2 * plan.tokens, it.n) - 1);
-    j.x0 = split_at(j.keys.count, it.split, plan.splits);
-    j.n = split_at(j.keys.count, it.split + 1, plan.splits) - j.x0;
+    j.x0 = split_at(j.keys.count, it.split, it.splits);
+    j.n = split_at(j.keys.count, it.split + 1, it.splits) - j.x0;
     j.turn = 0;
     while (j.turn < j.n && j.keys.masked(p, j.keys.base(j.x0 + j.turn))) ++j.turn;
     if (j.turn >= j.n) j.turn = 0;
@@ -430,6 +511,8 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                     continue;
                 }
                 id += plan.units;
+                // for the merge (a request's last rows have a tile in every piece)
+                if (plan.splits > 1 && it.split == 0 && lane == 0) plan.pieces[it.b] = it.splits;
                 tiles = job_of(p, plan, it);
                 if (tiles.n == 0) continue;
             }
@@ -779,7 +862,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                 break;
             }
             l += sh->row[(g - 1) & 1][part ^ 1][row];
-            const bool partial = plan.splits > 1;
+            const bool partial = tiles.it.splits > 1;
             const int split = tiles.it.split, d0 = tiles.it.vh * kDV;
             const int held = min(plan.tokens, tiles.it.n - lo_row);   // tokens that have rows here
             const size_t at = ((size_t)tiles.it.b * p.k + lo_row) * p.q_heads +
@@ -882,7 +965,8 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
 }
 
 // Merges the pieces of split items: one CTA a row of the output, 16 bytes of it a thread,
-// kFlight pieces' loads in flight.
+// kFlight pieces' loads in flight.  The first of them are on their way before it is known
+// how many pieces there are (one latency, not three after one another).
 template <int D>
 __global__ void __launch_bounds__(D / 4) paged_chunk_merge_kernel(
     const __grid_constant__ PagedChunkParams p, const Plan plan) {
@@ -890,35 +974,42 @@ __global__ void __launch_bounds__(D / 4) paged_chunk_merge_kernel(
     wait_for_prior_launch();
     let_next_launch_start();
     const size_t at = blockIdx.x;
-    const int row = blockIdx.x / p.q_heads;
-    const int b = row / p.k, j = row - b * p.k;
+    const int token = blockIdx.x / p.q_heads;
+    const int b = token / p.k, j = token - b * p.k;
     const float2 *ml = plan.part_ml + at * plan.splits;
     const float4 *o = reinterpret_cast<const float4 *>(plan.part_o + at * plan.splits * D) +
                       threadIdx.x;
+    float2 l[kFlight];
+    float4 v[kFlight];
+    auto load = [&](int s0) {
+#pragma unroll
+        for (int i = 0; i < kFlight; ++i)
+            if (s0 + i < plan.splits) {
+                l[i] = ml[s0 + i];
+                v[i] = o[(size_t)(s0 + i) * (D / 4)];
+            }
+    };
+    load(0);
     const Request rq = load_request(p, b);
-    if (!request_ok(p, rq) || j >= rq.n) return;
+    const int pieces = plan.pieces[b];
+    if (!request_ok(p, rq) || j >= rq.n || pieces == 1) return;   // (one piece: written whole)
     const int j0 = j / (2 * plan.tokens) * 2 * plan.tokens;
     const Keys keys(p, (int)rq.ctx + j0, (int)rq.ctx + min(j0 + 2 * plan.tokens, rq.n) - 1);
-    // splits without a tile wrote nothing
-    auto written = [&](int s) {
-        return s < plan.splits &&
-               split_at(keys.count, s, plan.splits) < split_at(keys.count, s + 1, plan.splits);
-    };
     float top = -INFINITY, sum = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    int from = 0;
 #pragma unroll 1
-    for (int s0 = 0; s0 < plan.splits; s0 += kFlight) {
-        float2 l[kFlight];
-        float4 v[kFlight];
+    for (int s0 = 0; s0 < pieces; s0 += kFlight) {
+        if (s0 > 0) load(s0);
+        float most = top;
+        bool have[kFlight];   // pieces without a tile wrote nothing
 #pragma unroll
         for (int i = 0; i < kFlight; ++i) {
-            const bool have = written(s0 + i);
-            l[i] = have ? ml[s0 + i] : make_float2(-INFINITY, 0.f);
-            v[i] = have ? o[(size_t)(s0 + i) * (D / 4)] : make_float4(0.f, 0.f, 0.f, 0.f);
+            const int to = split_at(keys.count, s0 + i + 1, pieces);
+            have[i] = s0 + i < pieces && to > from;
+            from = to;
+            if (have[i]) most = fmaxf(most, l[i].x);
         }
-        float most = top;
-#pragma unroll
-        for (int i = 0; i < kFlight; ++i) most = fmaxf(most, l[i].x);
         const float ref = most == -INFINITY ? 0.f : most;
         const float keep = fast_exp2(top - ref);
         top = most;
@@ -926,6 +1017,7 @@ __global__ void __launch_bounds__(D / 4) paged_chunk_merge_kernel(
         acc.x *= keep, acc.y *= keep, acc.z *= keep, acc.w *= keep;
 #pragma unroll
         for (int i = 0; i < kFlight; ++i) {
+            if (!have[i]) continue;
             const float w = fast_exp2(l[i].x - ref);
             sum = fmaf(w, l[i].y, sum);
             acc.x = fmaf(w, v[i].x, acc.x);
@@ -941,26 +1033,42 @@ __global__ void __launch_bounds__(D / 4) paged_chunk_merge_kernel(
 
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
+constexpr size_t kPieceBytes = (size_t)32 << 20;
+
 struct Sizes {
     Plan plan;
-    size_t ml, total;
+    size_t ml, o, total;
 };
 
-Sizes sizes_of(int batch, int k, int q_heads, int kv_heads, int head_dim) {
+Sizes sizes_of(int batch, int k, int q_heads, int kv_heads, int head_dim, bool window) {
     Sizes z{};
     z.plan.tokens = kRows / (q_heads / kv_heads);
     z.plan.halves = head_dim / kDV;
     const int tiles = (k + 2 * z.plan.tokens - 1) / (2 * z.plan.tokens);
     const long long items = (long long)batch * kv_heads * tiles * z.plan.halves;
     const int pairs = device_sm_count() / 2;
-    z.plan.splits = items > 0 && items <= pairs / 2 ? (int)(pairs / items) : 1;
-    // A pair that finds no item costs about a microsecond (a padded batch has many): the
-    // grid is at most kUnits times the pairs that run at once.
-    z.plan.units = (int)std::min<long long>(items * z.plan.splits, (long long)kUnits * pairs);
+    const size_t row = (size_t)batch * k * q_heads * head_dim * sizeof(float);
+    // Few items: as many pieces as make one for every pair.  Several requests without a window
+    // may differ much in length: up to kUnits pieces a pair, what they leave kept to
+    // kPieceBytes (planning and an extra launch cost 2 to 3 us, one long request among
+    // short ones up to half of the call).
+    const long long one = items > 0 ? std::max<long long>(1, pairs / items) : 1;
+    z.plan.splits = (int)one;
+    if (items > 0 && items <= (long long)kUnits / 2 * pairs && batch > 1 && !window) {
+        const long long most = std::min<long long>(kUnits * pairs / items, pairs);
+        z.plan.splits = (int)std::max(one, std::min<long long>(most, kPieceBytes / row));
+        z.plan.by_length = z.plan.splits > 1;
+    }
+    // Split items: every pair of the grid runs at once.  Else a pair that finds no item costs
+    // about a microsecond (a padded batch has many): the grid is at most kUnits times the
+    // pairs that run at once.
+    z.plan.units = (int)std::min<long long>(
+        items * z.plan.splits, (z.plan.splits > 1 ? 1LL : (long long)kUnits) * pairs);
     if (z.plan.splits > 1) {
         const size_t rows = (size_t)batch * k * q_heads * z.plan.splits;
         z.ml = align256(rows * sizeof(float2));
-        z.total = z.ml + align256(rows * head_dim * sizeof(float));
+        z.o = align256(rows * head_dim * sizeof(float));
+        z.total = z.ml + z.o + align256((size_t)batch * sizeof(int));
     }
     return z;
 }
@@ -971,6 +1079,7 @@ cudaError_t launch(const PagedChunkParams &p, Sizes &z, cudaStream_t stream) {
     char *w = static_cast<char *>(p.workspace);
     z.plan.part_ml = reinterpret_cast<float2 *>(w);
     z.plan.part_o = reinterpret_cast<float *>(w + z.ml);
+    z.plan.pieces = reinterpret_cast<int *>(w + z.ml + z.o);
     CUtensorMap map_q{}, map_k{}, map_v{};
     const uint64_t row = (uint64_t)p.kv_heads * D * 2;
     const uint64_t dims[4] = {64, (uint64_t)p.num_pages * p.page_rows, D / 64, (uint64_t)p.kv_heads};
@@ -1004,14 +1113,82 @@ cudaError_t launch(const PagedChunkParams &p, Sizes &z, cudaStream_t stream) {
 
 }  // namespace
 
+// Few rows of many requests at head_dim 512: the stream-K kernel with keys as the products'
+// long side (attention_tc.cuh), where a CTA pair would spend 256 rows' products on a
+// request's few, twice over for the scores.  Measured, us, pairs against it: 64 requests of 2
+// KV heads and 4 tokens under a window of 4096 208 and 157, 64 of one token and up to 16000
+// keys 417 and 210, 8 of 4 tokens and up to 32768 keys 100 and 81; but 8 under a window of
+// 1024 20 and 26, and 4 of 6005 keys 37 and 42.
+static bool few_rows(int batch, int k, int q_heads, int kv_heads, int head_dim, bool window) {
+    return batch * (long long)kv_heads >= (window ? 32 : 16) &&
+           tc_window_supported(head_dim, q_heads / kv_heads, k);
+}
+
+struct StepSizes {
+    int grid;
+    size_t ml, o, total;
+};
+
+static StepSizes step_sizes(int batch, int k, int q_heads, int kv_heads, int head_dim) {
+    const int n = tc_rows_per_tile(q_heads / kv_heads, k);
+    StepSizes z{};
+    z.grid = tc_ctas_per_sm(head_dim, n, false) * device_sm_count();
+    const size_t slots = (size_t)z.grid * 2 * n;
+    z.ml = align256(slots * sizeof(float2));
+    z.o = align256(slots * (size_t)head_dim * sizeof(float));
+    z.total = z.ml + z.o + align256((size_t)batch * kv_heads * sizeof(int4));
+    return z;
+}
+
+static cudaError_t launch_step(const PagedChunkParams &p, cudaStream_t stream) {
+    const StepSizes z = step_sizes(p.batch, p.k, p.q_heads, p.kv_heads, p.head_dim);
+    char *w = static_cast<char *>(p.workspace);
+    AttnParams a{};
+    a.q = p.q;
+    a.k_base = p.k_pages;
+    a.v_base = p.v_pages;
+    a.context_lengths = p.context_lengths;
+    a.new_counts = p.new_counts;
+    a.out16 = p.out;
+    a.part_ml = reinterpret_cast<float2 *>(w);
+    a.part_o = reinterpret_cast<float *>(w + z.ml);
+    a.units = reinterpret_cast<int4 *>(w + z.ml + z.o);
+    a.dev_status = p.dev_status;
+    a.batch = p.batch;
+    a.k = p.k;
+    a.q_heads = p.q_heads;
+    a.kv_heads = p.kv_heads;
+    a.head_dim = p.head_dim;
+    a.group = p.group;
+    a.rows = p.group * p.k;
+    a.window = p.window;
+    a.sinks = p.window > 0 ? p.sinks : 0;
+    a.capacity = p.capacity;
+    a.page_table = p.page_table;
+    a.max_pages = p.max_pages;
+    a.page_rows = p.page_rows;
+    a.num_pages = p.num_pages;
+    a.scale_log2 = p.scale_log2;
+    a.source = KeySource::kPagedWindow;
+    return launch_attention_tc_window(a, z.grid, stream);
+}
+
 bool paged_chunk_supported(int head_dim) { return head_dim == 256 || head_dim == 512; }
 
 size_t paged_chunk_workspace(int batch, int k, int q_heads, int kv_heads, int head_dim) {
-    return sizes_of(batch, k, q_heads, kv_heads, head_dim).total;
+    const size_t pairs = few_rows(batch, k, q_heads, kv_heads, head_dim, true)
+                             ? 0
+                             : sizes_of(batch, k, q_heads, kv_heads, head_dim, false).total;
+    const size_t step = few_rows(batch, k, q_heads, kv_heads, head_dim, false)
+                            ? step_sizes(batch, k, q_heads, kv_heads, head_dim).total
+                            : 0;
+    return std::max(pairs, step);
 }
 
 cudaError_t launch_paged_chunk_attention(const PagedChunkParams &p, cudaStream_t stream) {
-    Sizes z = sizes_of(p.batch, p.k, p.q_heads, p.kv_heads, p.head_dim);
+    if (few_rows(p.batch, p.k, p.q_heads, p.kv_heads, p.head_dim, p.window > 0))
+        return launch_step(p, stream);
+    Sizes z = sizes_of(p.batch, p.k, p.q_heads, p.kv_heads, p.head_dim, p.window > 0);
     return p.head_dim == 256 ? launch<256>(p, z, stream) : launch<512>(p, z, stream);
 }
 
