@@ -275,6 +275,7 @@ class PagedGlobalLayer:
             max(carat.global_workspace_bytes(batch, p, q_heads, kv_heads, head_dim, self.capacity)
                 for p in range(1, max_proposals + 1)), self.device)
         most = max(max_proposals, max_chunk)
+        self.max_chunk = most if window or max_chunk else 0
         if cos_sin is not None:
             self.rotated = torch.empty(batch * most * q_heads * head_dim,
                                        dtype=torch.bfloat16, device=self.device)
@@ -308,6 +309,9 @@ class PagedGlobalLayer:
               new_counts=None):
         """Append a chunk's rows (new_counts[b] of request b, or all; counts need a layer
         with a rotary table) and attend to them and to what the pages held: out bf16."""
+        if queries.shape[1] > self.max_chunk:
+            raise ValueError(f"{queries.shape[1]} new tokens: the layer was made for max_chunk "
+                             f"{self.max_chunk}")
         if out is None:
             out = torch.empty(queries.shape, dtype=torch.bfloat16, device=self.device)
         if self.cos_sin is not None:

@@ -358,3 +358,127 @@ def test_more_items_than_the_grid_has_cta_pairs(counts):
     ctx = [100] if counts is None else [100, 0, 7, 500]
     c = Case(ctx, 2600, 64, 1, 256, counts=counts, window=300, sinks=2, seed=19).device()
     c.check(c.call(), rows=[0, 1, 2, 3, 4, 16, 1000, 1503, 2431, 2432, 2433, 2598, 2599])
+
+
+# Many requests of few rows take other ways through the library than one or two: at head_dim
+# 512 the stream-K kernel (32 pairs of request and KV head, 16 without a window), else pieces
+# whose number goes by the requests' lengths.
+MANY = [(16, 2, 512, 17), (3, 1, 512, 33), (64, 4, 512, 9), (16, 8, 256, 5), (4, 1, 256, 40),
+        (2, 1, 256, 2)]
+
+
+def _ragged(n, longest, seed):
+    g = torch.Generator().manual_seed(seed)
+    c = torch.randint(0, 300, (n,), generator=g).tolist()
+    c[0], c[-1] = longest, 0
+    if n > 2:
+        c[1] = 127
+    return c
+
+
+@pytest.mark.parametrize("q_heads,kv_heads,head_dim,batch", MANY)
+@pytest.mark.parametrize("k", [1, 3])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (1, 0), (100, 3), (128, 200), (513, 1 << 30)])
+def test_many_requests(q_heads, kv_heads, head_dim, batch, k, window, sinks):
+    c = Case(_ragged(batch, 2500, k), k, q_heads, kv_heads, head_dim, window=window, sinks=sinks,
+             seed=20, spread=2.0, page_rows=256).device()
+    c.check(c.call())
+
+
+@pytest.mark.parametrize("q_heads,kv_heads,head_dim,batch", MANY)
+@pytest.mark.parametrize("window", [0, 70])
+def test_many_requests_with_counts(q_heads, kv_heads, head_dim, batch, window):
+    counts = [i % 5 for i in range(batch)]
+    c = Case(_ragged(batch, 1000, 3), 4, q_heads, kv_heads, head_dim, counts=counts, window=window,
+             sinks=5, seed=21).device()
+    c.check(c.call())
+    c = Case(_ragged(batch, 1000, 3), 4, q_heads, kv_heads, head_dim, counts=[0] * batch,
+             window=window, seed=21).device()
+    c.check(c.call())
+
+
+@pytest.mark.parametrize("q_heads,kv_heads,head_dim,batch", MANY)
+@pytest.mark.parametrize("window", [0, 40])
+@pytest.mark.parametrize("bad", [float("nan"), float("-inf")])
+def test_non_finite_values_among_many_requests(q_heads, kv_heads, head_dim, batch, window, bad):
+    """In keys that some of a request's queries see: the newest but one, and one that the
+    window leaves between the first query and the last; in the stale rows anyway."""
+    k, ctx = 4, [200 + i for i in range(batch)]
+    clean = Case(ctx, k, q_heads, kv_heads, head_dim, window=window, sinks=2, seed=22)
+    c = Case(ctx, k, q_heads, kv_heads, head_dim, window=window, sinks=2, seed=22)
+    hit = {0: ctx[0] + 2, batch - 1: ctx[-1] + 1 - window if window else ctx[-1] + 1}
+    for b, t in hit.items():
+        c.values[b][t, kv_heads - 1, 11] = bad
+        c.keys[b][ctx[b] + k - 1, 0, 3] = bad
+    c.write()
+    got = c.device().call().cpu()
+    g = q_heads // kv_heads
+    for b in range(batch):
+        want, bound = clean.want(b)
+        for j in range(k):
+            p = ctx[b] + j
+            for h in range(q_heads):
+                n = ctx[b] + k
+                poisoned = b in hit and ((h // g == kv_heads - 1 and bool(
+                    ref.seen(p, n, window, 2)[hit[b]])) or (h // g == 0 and j == k - 1))
+                if not poisoned:
+                    off = (got[b, j, h].double() - want[j, h]).abs()
+                    assert (off <= bound[j, h]).all(), (b, j, h)
+                elif not (h // g == 0 and j == k - 1):
+                    assert not got[b, j, h, 11].isfinite(), (b, j, h)
+
+
+@pytest.mark.parametrize("q_heads,kv_heads,head_dim,batch", MANY)
+def test_many_requests_some_rejected(q_heads, kv_heads, head_dim, batch):
+    ctx = _ragged(batch, 400, 5)
+    counts = [3] * batch
+    c = Case(ctx, 3, q_heads, kv_heads, head_dim, counts=counts, seed=23).device()
+    last = batch - 1
+    c.dc[last] = -5
+    if batch > 2:
+        c.dn[2] = 4
+        c.dc[1] = 1 << 30
+    out = c.call().cpu()
+    assert carat.carat_get_device_status(clear=True) == carat.CARAT_DEV_BAD_CONTEXT
+    rejected = {last, 1, 2} if batch > 2 else {last}
+    for b in range(batch):
+        if b in rejected:
+            assert out[b].isnan().all(), b
+        else:
+            want, bound = c.want(b)
+            assert ((out[b].double() - want).abs() <= bound).all(), b
+
+
+@pytest.mark.parametrize("q_heads,kv_heads,head_dim,batch", MANY)
+def test_many_requests_bad_pages_queries_and_repeats(q_heads, kv_heads, head_dim, batch):
+    c = Case([300] * batch, 2, q_heads, kv_heads, head_dim, seed=24)
+    clean = Case([300] * batch, 2, q_heads, kv_heads, head_dim, seed=24)
+    c.q[0, 1, 0, 5] = float("nan")
+    c.device()
+    c.dt[batch - 1, 1] = -3
+    for x in (clean.keys, clean.values):
+        x[batch - 1][128:256] = 0
+    first = c.call().clone()
+    assert carat.carat_get_device_status(clear=True) == carat.CARAT_DEV_BAD_CACHE_ID
+    assert first[0, 1, 0].isnan().all()
+    for b in range(batch):
+        want, bound = clean.want(b)
+        ok = torch.ones(want.shape[:2], dtype=torch.bool)
+        if b == 0:
+            ok[1, 0] = False
+        assert (((first[b].cpu().double() - want).abs() <= bound)[ok]).all(), b
+    flush = torch.empty(300 << 20, dtype=torch.uint8, device="cuda")
+    for i in range(12):
+        flush.fill_(i)
+        c.out.fill_(7.0)
+        c.call()
+        assert torch.equal(first.view(torch.int16), c.out.view(torch.int16)), i
+    carat.carat_get_device_status(clear=True)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        c.call()
+    c.out.fill_(7.0)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(first.view(torch.int16), c.out.view(torch.int16))
+    carat.carat_get_device_status(clear=True)
