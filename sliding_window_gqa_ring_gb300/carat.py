@@ -1009,6 +1009,7 @@ def _page_args(what, key_pages, value_pages, k_scales, v_scales, lists, tables=N
     for name, t in lists.items():
         if t is not None:
             _expect(t, torch.int32, f"{what}: {name}")
+            _ptr(t)
             if t.dim() != 1 or t.shape != first.shape:
                 raise ValueError(f"{what}: {name} must be one-dimensional, all lists alike")
     _on_device(what, key_pages=key_pages, value_pages=value_pages, k_scales=k_scales,
@@ -1017,16 +1018,62 @@ def _page_args(what, key_pages, value_pages, k_scales, v_scales, lists, tables=N
             page_rows, row_bytes, block_rows, kv_heads), device
 
 
+def _page_head(key_pages, value_pages, k_scales, v_scales):
+    """(device, leading arguments) of the usual call, or None: _page_args says why."""
+    try:
+        pool = key_pages.shape
+        num_pages, page_rows, kv_heads, head_dim = pool
+        dtype, device = key_pages.dtype, key_pages.get_device()
+        if device != _device() or value_pages.shape != pool or \
+                not _plain(device, dtype, key_pages, value_pages):
+            return None
+        row_bytes = kv_heads * head_dim
+        if dtype is _BF16:
+            row_bytes *= 2
+        elif dtype is not _U8:
+            return None
+        if k_scales is None:
+            if v_scales is not None:
+                return None
+            return device, (key_pages.data_ptr(), value_pages.data_ptr(), None, None, num_pages,
+                            page_rows, row_bytes, 0, kv_heads)
+        shape = k_scales.shape
+        pages, blocks, heads = shape
+        if pages != num_pages or heads != kv_heads or blocks < 1 or page_rows % blocks or \
+                v_scales.shape != shape or not _plain(device, _F32, k_scales, v_scales):
+            return None
+        return device, (key_pages.data_ptr(), value_pages.data_ptr(), k_scales.data_ptr(),
+                        v_scales.data_ptr(), num_pages, page_rows, row_bytes, page_rows // blocks,
+                        kv_heads)
+    except (AttributeError, TypeError, ValueError):
+        return None
+
+
+def _lists(device, shape, *lists):
+    """Every list is a contiguous int32 one of this shape on this device."""
+    for t in lists:
+        if not (t.shape == shape and t.dtype is _I32 and t.get_device() == device and
+                t.is_contiguous()):
+            return False
+    return True
+
+
 def carat_pages_copy(key_pages, value_pages, src, dst, *, rows=None, k_scales=None, v_scales=None,
                      stream=None):
     """Copy the first rows[i] rows (default: all) of page src[i] into page dst[i], keys,
     values and (e4m3 pages, uint8) the scales of their blocks.  src, dst, rows: int32
     lists on the device; a source below 0 is skipped."""
     what = "carat_pages_copy"
-    head, device = _page_args(what, key_pages, value_pages, k_scales, v_scales,
-                              {"src": src, "dst": dst, "rows": rows})
+    usual = _page_head(key_pages, value_pages, k_scales, v_scales)
+    if usual is not None and len(src.shape) == 1 and _lists(usual[0], src.shape, src, dst) and \
+            (rows is None or _lists(usual[0], src.shape, rows)):
+        device, head = usual
+    else:
+        head, device = _page_args(what, key_pages, value_pages, k_scales, v_scales,
+                                  {"src": src, "dst": dst, "rows": rows})
     _check((_lib or library()).carat_pages_copy(
-        *head, _ptr(src), _ptr(dst), _ptr(rows), src.shape[0], _stream_of(stream, device)), what)
+        *head, src.data_ptr(), dst.data_ptr(), None if rows is None else rows.data_ptr(),
+        src.shape[0], _stream_of(stream, device)), what)
 
 
 def carat_paged_fork(key_pages, value_pages, page_table, context_lengths, child_table, parents,
@@ -1036,6 +1083,27 @@ def carat_paged_fork(key_pages, value_pages, page_table, context_lengths, child_
     new_pages[i] (below 0: the child takes that page itself).  child_lengths[i] (optional)
     becomes the parent's context length."""
     what = "carat_paged_fork"
+    usual = _page_head(key_pages, value_pages, k_scales, v_scales)
+    lines = page_table.shape
+    if usual is not None and len(lines) == 2 and len(parents.shape) == 1 and \
+            _lists(usual[0], parents.shape, parents, new_pages) and \
+            _lists(usual[0], lines, page_table) and \
+            _lists(usual[0], lines[:1], context_lengths) and \
+            _lists(usual[0], (parents.shape[0], lines[1]), child_table) and \
+            (child_lengths is None or _lists(usual[0], parents.shape, child_lengths)):
+        device, head = usual
+    else:
+        head, device = _fork_args(what, key_pages, value_pages, page_table, context_lengths,
+                                  child_table, parents, new_pages, child_lengths, k_scales, v_scales)
+    _check((_lib or library()).carat_paged_fork(
+        *head, page_table.data_ptr(), lines[0], lines[1], context_lengths.data_ptr(),
+        child_table.data_ptr(), None if child_lengths is None else child_lengths.data_ptr(),
+        parents.data_ptr(), new_pages.data_ptr(), parents.shape[0], _stream_of(stream, device)),
+        what)
+
+
+def _fork_args(what, key_pages, value_pages, page_table, context_lengths, child_table, parents,
+               new_pages, child_lengths, k_scales, v_scales):
     head, device = _page_args(
         what, key_pages, value_pages, k_scales, v_scales,
         {"parents": parents, "new_pages": new_pages, "child_lengths": child_lengths},
@@ -1043,16 +1111,14 @@ def carat_paged_fork(key_pages, value_pages, page_table, context_lengths, child_
     for name, t in (("page_table", page_table), ("context_lengths", context_lengths),
                     ("child_table", child_table)):
         _expect(t, torch.int32, f"{what}: {name}")
+        _ptr(t)
     if page_table.dim() != 2 or child_table.dim() != 2 or \
             child_table.shape[1] != page_table.shape[1] or \
             child_table.shape[0] != parents.shape[0]:
         raise ValueError(f"{what}: child_table must be [children][max_pages]")
     if tuple(context_lengths.shape) != (page_table.shape[0],):
         raise ValueError(f"{what}: context_lengths must be [parents' batch]")
-    _check((_lib or library()).carat_paged_fork(
-        *head, _ptr(page_table), page_table.shape[0], page_table.shape[1], _ptr(context_lengths),
-        _ptr(child_table), _ptr(child_lengths), _ptr(parents), _ptr(new_pages), parents.shape[0],
-        _stream_of(stream, device)), what)
+    return head, device
 
 
 def carat_pages_move(key_pages, value_pages, src, dst, *, page_table=None, k_scales=None,
@@ -1062,10 +1128,18 @@ def carat_pages_move(key_pages, value_pages, src, dst, *, page_table=None, k_sca
     have been moved already, only scales and table follow (num_pages: the pool's, where
     there are no scales to tell)."""
     what = "carat_pages_move"
-    if page_table is not None:
-        _expect(page_table, torch.int32, f"{what}: page_table")
-    head, device = _page_args(what, key_pages, value_pages, k_scales, v_scales,
-                              {"src": src, "dst": dst}, {"page_table": page_table}, num_pages)
+    usual = _page_head(key_pages, value_pages, k_scales, v_scales)
+    if usual is not None and len(src.shape) == 1 and _lists(usual[0], src.shape, src, dst) and \
+            (page_table is None or _lists(usual[0], page_table.shape, page_table)):
+        device, head = usual
+    else:
+        if page_table is not None:
+            _expect(page_table, torch.int32, f"{what}: page_table")
+            _ptr(page_table)
+        head, device = _page_args(what, key_pages, value_pages, k_scales, v_scales,
+                                  {"src": src, "dst": dst}, {"page_table": page_table}, num_pages)
+    table, entries = (None, 0) if page_table is None else (page_table.data_ptr(),
+                                                           page_table.numel())
     _check((_lib or library()).carat_pages_move(
-        *head, _ptr(src), _ptr(dst), src.shape[0], _ptr(page_table),
-        0 if page_table is None else page_table.numel(), _stream_of(stream, device)), what)
+        *head, src.data_ptr(), dst.data_ptr(), src.shape[0], table, entries,
+        _stream_of(stream, device)), what)
