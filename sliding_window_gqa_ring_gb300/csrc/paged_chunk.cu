@@ -871,6 +871,19 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                 plan.part_ml[(at + token * p.q_heads + head) * plan.splits + split] =
                     make_float2(m, l);
             float f = partial ? 1.f : 1.f / l;
+            // where this thread writes of the warp's rows 4 e + lane / 8 (null: no such row)
+            const size_t row_bytes = partial ? (size_t)plan.splits * D * 4 : (size_t)D * 2;
+            uint8_t *const whole = partial ? reinterpret_cast<uint8_t *>(
+                                                 plan.part_o + (size_t)split * D + d0)
+                                           : reinterpret_cast<uint8_t *>(p.out + d0);
+            uint8_t *to[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const int rr = quad * 32 + e * 4 + lane / 8, tt = rr * inv_group >> 16;
+                to[e] = tt < held ? whole + (at + tt * p.q_heads + rr - tt * p.group) * row_bytes +
+                                        (lane & 7) * 16
+                                  : nullptr;
+            }
             // The last scores say that the product two tiles before is done, no more: with one
             // barrier for all products this wait could meet a phase too early or too late.
             alive = warp_wait<true>(&sh->pv_done[(g - 1) & 1], ((g - 1) >> 1) & 1, abort_flag,
@@ -894,24 +907,18 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
             turn = turn == 2 ? 0 : turn + 1;
             if (poisoned) f = NAN;
             give_back();
-            // place behind the CTA's first row of the warp's row r, or -1: no such row
-            auto place = [&](int r) -> int {
-                const int rr = quad * 32 + r, tt = rr * inv_group >> 16;
-                return tt < held ? tt * p.q_heads + rr - tt * p.group : -1;
-            };
             // O leaves through shared memory, 128 bytes of each of the warp's 32 rows at a
             // time, so that eight lanes write a whole line.
             uint8_t *s_out = smem + L::kOffOut + (warp - 4) * 4096;
-            auto leave = [&](uint8_t *base, size_t row_bytes) {
+            const uint8_t *s_from = s_out + lane / 8 * 128;
+            auto leave = [&](int column_bytes) {
                 __syncwarp();
-#pragma unroll 4
+#pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    const int r = e * 4 + lane / 8, to = place(r);
-                    const uint4 v = *reinterpret_cast<const uint4 *>(
-                        s_out + r * 128 + ((lane ^ r) & 7) * 16);
-                    if (to >= 0)
-                        *reinterpret_cast<uint4 *>(base + (at + to) * row_bytes +
-                                                   (lane & 7) * 16) = v;
+                    const int r = e * 4 + lane / 8;
+                    const uint4 v = *reinterpret_cast<const uint4 *>(s_from + e * 512 +
+                                                                     ((lane ^ r) & 7) * 16);
+                    if (to[e]) *reinterpret_cast<uint4 *>(to[e] + column_bytes) = v;
                 }
                 __syncwarp();
             };
@@ -927,8 +934,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                     for (int e = 0; e < 8; ++e)
                         *reinterpret_cast<uint4 *>(s_out + lane * 128 + ((e ^ lane) & 7) * 16) =
                             make_uint4(o[e * 4], o[e * 4 + 1], o[e * 4 + 2], o[e * 4 + 3]);
-                    leave(reinterpret_cast<uint8_t *>(plan.part_o + (size_t)split * D + d0 + i),
-                          (size_t)plan.splits * D * 4);
+                    leave(i * 4);
                     continue;
                 }
                 const int half = (i & 32) / 8;   // of the 128 bytes
@@ -943,8 +949,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                         s_out + lane * 128 + (((e + half) ^ lane) & 7) * 16) =
                         make_uint4(w[0], w[1], w[2], w[3]);
                 }
-                if (half)
-                    leave(reinterpret_cast<uint8_t *>(p.out + d0 + i - 32), D * 2);
+                if (half) leave((i - 32) * 2);
             }
             if constexpr (L::kOutInQ) {
                 tc::fence_proxy_async_smem();
