@@ -332,9 +332,11 @@ struct Shared {
     uint32_t tmem;
     int abort_flag;
     Job job[kJobs];
-    // Keys of masked tiles with values that are not finite, of three items in turn: the
-    // other CTA may be at the next item's first tile already, and the third is cleared
-    // while nobody can be at its item.
+    // Keys of masked tiles with values that are not finite, of three items that have such
+    // tiles in turn.  At a masked tile of one of them every softmax warp is past the one
+    // before the last (the products wait for the weights of all), so its record is cleared
+    // there, for the next: nothing is written to that before this CTA's warps have said
+    // that the tile is looked through.
     uint32_t poison[3];
     uint32_t bad[3][kMasked][4];
     float row[2][2][kRows];           // a row's two threads tell each other
@@ -679,17 +681,18 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
             const Job tiles = *job;
             give_back();
             const int n = tiles.n;
-            if (warp == 2) {   // the records of the item after this one
-                const int after = turn == 2 ? 0 : turn + 1;
-                (&sh->bad[after][0][0])[lane] = 0;
-                if (lane == 0) sh->poison[after] = 0;
-            }
-            for (int x = 0, i = 0; x < n; ++x) {
+            int i = 0;
+            for (int x = 0; x < n; ++x) {
                 const int t0 = tiles.base(x);
                 if (!tiles.keys.masked(p, t0)) continue;
                 alive = warp_wait<true>(&sh->v_ready, vcnt & 1, abort_flag, p.dev_status);
                 if (!alive) break;
                 ++vcnt;
+                if (warp == 2 && i == 0) {   // the record of the next item with masked tiles
+                    const int after = turn == 2 ? 0 : turn + 1;
+                    (&sh->bad[after][0][0])[lane] = 0;
+                    if (lane == 0) sh->poison[after] = 0;
+                }
                 // stages in order: K(0), K(1) V(0), K(2) V(1), ..., V(n - 1)
                 const uint32_t stage = (cnt + (x + 1 < n ? x + 2 : n) * KST + x) % NS;
                 // this warp's keys 64 (warp - 2) + lane and 32 further on, both at once
@@ -744,7 +747,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                 }
             }
             cnt += n * (KST + 1);
-            turn = turn == 2 ? 0 : turn + 1;
+            if (i > 0) turn = turn == 2 ? 0 : turn + 1;
         }
     } else if (warp >= 4) {
         // ---------------------------------------------------------------- softmax
@@ -770,13 +773,14 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
             }
         }
         uint32_t g = 0;   // tiles before this item's
-        int turn = 0;     // which third of the poison records
+        int turn = 0;     // which of the poison records
         bool alive = true;
         while (const Job *job = take(alive)) {
             const Job &tiles = *job;   // given back when the output's places are known
             const int n = tiles.n, lo_row = tiles.it.j0 + rank * plan.tokens;
             const int pos = tiles.it.ctx + min(lo_row + token, tiles.it.n - 1);
             float m = -INFINITY, l = 0.f;
+            bool has_masked = false;
             for (int x = 0; x < n; ++x) {
                 const uint32_t buf = (g + x) & 1;
                 alive = alive && warp_wait(&sh->s_full[buf], ((g + x) >> 1) & 1, abort_flag,
@@ -789,6 +793,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                 tc::tmem_ld_wait();
                 const int t0 = tiles.base(x);
                 if (tiles.keys.masked(p, t0)) {
+                    has_masked = true;
                     const int first = t0 + part * 64;
                     uint64_t see = low_bits(pos - first + 1);
                     if (p.window > 0)
@@ -891,7 +896,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
             if (!alive) break;
             tc::tc_fence_after();
             bool poisoned = false;
-            if (*(volatile uint32_t *)&sh->poison[turn]) {
+            if (has_masked && *(volatile uint32_t *)&sh->poison[turn]) {
                 for (int x = 0, i = 0; x < n; ++x) {
                     const int t0 = tiles.base(x);
                     if (!tiles.keys.masked(p, t0)) continue;
@@ -904,7 +909,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                     ++i;
                 }
             }
-            turn = turn == 2 ? 0 : turn + 1;
+            if (has_masked) turn = turn == 2 ? 0 : turn + 1;
             if (poisoned) f = NAN;
             give_back();
             // O leaves through shared memory, 128 bytes of each of the warp's 32 rows at a
