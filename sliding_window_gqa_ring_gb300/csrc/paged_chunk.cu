@@ -290,7 +290,7 @@ struct Items {
 // One item's split: its tiles in the order they are taken, from the first that every row
 // sees whole, so that no row's first maximum is that of a few keys (the maxima then rise
 // past the slack tile after tile, 1200 to 1700 cycles each time), round to those before it.
-// n = 0: no item left.
+// n = 0: no item left, and it.b says whether this pair writes the rejected requests.
 struct Job {
     Item it;
     Keys keys;
@@ -485,7 +485,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         // Both CTAs' producers get the same answers, the leader asks.  An answer's place is
         // used again after kJobs more: the other CTA is behind by less than the stage ring.
         int unit = pair, id = pair;
-        bool pending = false;
+        bool pending = false, rejects = pair == 0;
         auto ask = [&]() {
             if (lane == 0) {
                 tc::fence_proxy_async_smem();
@@ -510,6 +510,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                     ++asked;
                     pending = false;
                     unit = id = taken_over < 0 ? -1 : taken_over / 2;
+                    rejects |= unit == 0;
                     continue;
                 }
                 id += plan.units;
@@ -523,6 +524,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                 alive = warp_wait(&sh->job_empty[slot], ((published / kJobs) & 1) ^ 1, abort_flag,
                                   p.dev_status);
             if (!alive) break;
+            if (unit < 0) tiles.it.b = rejects;
             if (lane == 0) {
                 sh->job[slot] = tiles;
                 tc::mbar_arrive(&sh->job_full[slot]);
@@ -758,20 +760,6 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         const int inv_group = 65536 / p.group + 1;   // r inv_group >> 16 = r / group, r < 128
         // the sign of the scale is in the product's descriptor; 0 would turn -inf into NaN
         const float scale = fmaxf(fabsf(p.scale_log2), FLT_MIN);
-        // Requests rejected on the device, by the pair that is always launched.
-        for (int first = 0; pair == 0 && first < p.batch; first += 32) {
-            const int mine = first + lane;
-            uint32_t bad = __ballot_sync(
-                kFull, mine < p.batch && !request_ok(p, load_request(p, mine)));
-            for (; bad; bad &= bad - 1) {
-                if (threadIdx.x == 128) set_status(p.dev_status, CARAT_DEV_BAD_CONTEXT);
-                const size_t rows = (size_t)p.k * p.q_heads;
-                uint4 *o = reinterpret_cast<uint4 *>(p.out + (first + __ffs(bad) - 1) * rows * D);
-                for (size_t i = rank * kSoftmax + threadIdx.x - 128; i < rows * (D / 8);
-                     i += 2 * kSoftmax)
-                    o[i] = make_uint4(0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu);
-            }
-        }
         uint32_t g = 0;   // tiles before this item's
         int turn = 0;     // which of the poison records
         bool alive = true;
@@ -962,6 +950,22 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                 if (lane == 0) tc::mbar_arrive(&sh->q_empty);
             }
             tc::tc_fence_before();
+        }
+        // Requests rejected on the device, by the pair that has the first pair's work
+        // (it may have been taken over).
+        const bool rejects = alive && sh->job[(taken - 1) % kJobs].it.b != 0;
+        for (int first = 0; rejects && first < p.batch; first += 32) {
+            const int mine = first + lane;
+            uint32_t bad = __ballot_sync(
+                kFull, mine < p.batch && !request_ok(p, load_request(p, mine)));
+            for (; bad; bad &= bad - 1) {
+                if (threadIdx.x == 128) set_status(p.dev_status, CARAT_DEV_BAD_CONTEXT);
+                const size_t rows = (size_t)p.k * p.q_heads;
+                uint4 *o = reinterpret_cast<uint4 *>(p.out + (first + __ffs(bad) - 1) * rows * D);
+                for (size_t i = rank * kSoftmax + threadIdx.x - 128; i < rows * (D / 8);
+                     i += 2 * kSoftmax)
+                    o[i] = make_uint4(0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu);
+            }
         }
     }
     tc::tc_fence_before();
