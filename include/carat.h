@@ -379,8 +379,9 @@ int carat_pool_stats(carat_pool *pool, int32_t *out4);
 /* Shared pages.  alloc_pages gives a page one owner; carat_pool_share_pages adds
  * one for every time a page is listed (requests that share a beginning, see
  * carat_paged_fork), and carat_pool_free_pages takes one away: the page is free
- * when the last is gone.  Returns 0, or -1 for an id that is not an allocated
- * single page (then nothing changes).
+ * when the last is gone (one call takes one owner of a page: an id listed twice
+ * is refused).  Returns 0, or -1 for an id that is not an allocated single page
+ * (then nothing changes).
  *
  * carat_pool_plan_compaction -- make room for rings: empties blocks that single
  * pages broke up, fewest pages first, into free places past the last block and
@@ -646,7 +647,7 @@ size_t carat_paged_chunk_workspace_bytes(int batch, int proposal_count, int q_he
  * context length outside [0, max_pages * page_rows] skips it and sets
  * CARAT_DEV_BAD_CONTEXT.  A page that one call writes must not be written twice by
  * it nor read by another of its jobs (the contents would be either's).
- * Limits: page_rows * row_bytes <= 2^40.
+ * Limits: page_rows * row_bytes <= 2^40; at most 2^30 jobs, children and parents.
  *
  * carat_pages_copy -- the first rows[i] rows (rows NULL: all) of page src[i] into
  *   page dst[i]; the rows behind them stay as they were.

@@ -276,6 +276,8 @@ carat_status carat_paged_chunk_attention(
     return launch_status(launch_paged_chunk_attention(p, static_cast<cudaStream_t>(stream)));
 }
 
+constexpr int kMostJobs = 1 << 30;   // a CTA's next job still fits an int
+
 // What the operators on pages share: the pool's geometry and arrays.  Without pages (a
 // move whose bytes are moved already) only the scales are looked at.
 static carat_status pages_params(PagesParams *p, bool need_pages, void *key_pages,
@@ -283,7 +285,7 @@ static carat_status pages_params(PagesParams *p, bool need_pages, void *key_page
                                  int num_pages, int page_rows, int64_t row_bytes, int block_rows,
                                  int kv_heads, int count) {
     if (num_pages < 1 || page_rows < 1 || row_bytes < 16 || row_bytes % 16 != 0 || count < 0 ||
-        row_bytes > (1LL << 40) / page_rows)
+        count > kMostJobs || row_bytes > (1LL << 40) / page_rows)
         return CARAT_ERR_INVALID_ARG;
     if ((k_scales == nullptr) != (v_scales == nullptr) ||
         (k_scales && (block_rows < 1 || page_rows % block_rows != 0 || kv_heads < 1 ||
@@ -333,7 +335,7 @@ carat_status carat_paged_fork(void *key_pages, void *value_pages, float *k_scale
                                          num_pages, page_rows, row_bytes, block_rows, kv_heads,
                                          children);
     if (st != CARAT_OK) return st;
-    if (num_parents < 1 || max_pages < 1 || (long long)max_pages * page_rows >= (1LL << 31))
+    if (num_parents < 1 || num_parents > kMostJobs || max_pages < 1 || (long long)max_pages * page_rows >= (1LL << 31))
         return CARAT_ERR_INVALID_ARG;
     if (children == 0) return CARAT_OK;
     if (!page_table || !context_lengths || !child_table || !parents || !new_pages)

@@ -80,7 +80,7 @@ COMMON = [
     (dict(num=0), INVALID), (dict(rows=0), INVALID), (dict(row_bytes=0), INVALID),
     (dict(row_bytes=24), INVALID), (dict(row_bytes=1 << 40), INVALID), (dict(R=0), INVALID),
     (dict(R=48), INVALID), (dict(hkv=0), INVALID), (dict(hkv=1 << 27), INVALID),
-    (dict(count=-1), INVALID), (dict(count=0), OK)]
+    (dict(count=-1), INVALID), (dict(count=0), OK), (dict(count=(1 << 30) + 1), INVALID)]
 
 
 @pytest.mark.parametrize("call", [_copy, _fork, _move])
@@ -101,7 +101,7 @@ def test_page_checks(carat, call, kw, status):
     (_fork, dict(mp=0), INVALID), (_fork, dict(mp=1 << 24), INVALID),
     (_fork, dict(child=FAKE), INVALID), (_fork, dict(child=FAKE + 4 * 32 - 4), INVALID),
     (_fork, dict(child=FAKE - 3 * 32 + 4), INVALID), (_fork, dict(lens=FAKE + 12), INVALID),
-    (_fork, dict(lens=FAKE - 8), INVALID),
+    (_fork, dict(lens=FAKE - 8), INVALID), (_fork, dict(parents_n=(1 << 30) + 1), INVALID),
 ])
 def test_list_and_table_checks(carat, call, kw, status):
     assert call(carat.library(), **kw) == status
