@@ -599,7 +599,8 @@ size_t carat_paged_fp8_workspace_bytes(int batch, int proposal_count, int q_head
  *                    softmax's maximum and sum and the accumulated output are fp32;
  *                    a key's weight is rounded to bf16 for its product with the
  *                    value, and it is the rounded weights that are summed.
- *   queries          bf16, same shape, after the rotation.
+ *   queries          bf16, same shape, after the rotation; neither they nor pages or
+ *                    workspace may overlap out (CARAT_ERR_INVALID_ARG).
  *   proposal_count   new tokens of a request, any number up to the capacity.
  *   new_counts       int32 [batch] or NULL (= proposal_count each): request b has
  *                    queries j < new_counts[b] and no keys behind theirs; the rows

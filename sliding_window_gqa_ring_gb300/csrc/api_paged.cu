@@ -11,6 +11,11 @@ namespace {
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+bool overlap(const void *a, size_t a_bytes, const void *b, size_t b_bytes) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x < y + b_bytes && y < x + a_bytes;
+}
+
 carat_status launch_status(cudaError_t e) { return e == cudaSuccess ? CARAT_OK : CARAT_ERR_CUDA; }
 
 bool page_sizes_ok(int num_pages, int max_pages, int page_rows) {
@@ -250,6 +255,14 @@ carat_status carat_paged_chunk_attention(
     const size_t need = paged_chunk_workspace(batch, proposal_count, q_heads, kv_heads, head_dim);
     if (need > 0 && (!workspace || workspace_bytes < need || !aligned16(workspace)))
         return CARAT_ERR_WORKSPACE;
+    // a pair writes rows while another still reads
+    const size_t out_bytes = (size_t)batch * proposal_count * q_heads * head_dim * 2;
+    const size_t page_bytes = (size_t)num_pages * page_rows * kv_heads * head_dim * 2;
+    if (overlap(out, out_bytes, queries, out_bytes) ||
+        overlap(out, out_bytes, key_pages, page_bytes) ||
+        overlap(out, out_bytes, value_pages, page_bytes) ||
+        (need > 0 && overlap(out, out_bytes, workspace, need)))
+        return CARAT_ERR_INVALID_ARG;
     PagedChunkParams p{};
     p.out = static_cast<uint16_t *>(out);
     p.q = static_cast<const uint16_t *>(queries);
@@ -341,14 +354,10 @@ carat_status carat_paged_fork(void *key_pages, void *value_pages, float *k_scale
     if (!page_table || !context_lengths || !child_table || !parents || !new_pages)
         return CARAT_ERR_INVALID_ARG;
     // a child's line written while another child's parent is read from it
-    const uintptr_t a = reinterpret_cast<uintptr_t>(page_table);
-    const uintptr_t c = reinterpret_cast<uintptr_t>(child_table);
     const size_t line = (size_t)max_pages * sizeof(int32_t);
-    if (a < c + (size_t)children * line && c < a + (size_t)num_parents * line)
-        return CARAT_ERR_INVALID_ARG;
-    const uintptr_t x = reinterpret_cast<uintptr_t>(context_lengths);
-    const uintptr_t y = reinterpret_cast<uintptr_t>(child_lengths);
-    if (child_lengths && x < y + (size_t)children * 4 && y < x + (size_t)num_parents * 4)
+    if (overlap(page_table, num_parents * line, child_table, children * line) ||
+        (child_lengths && overlap(context_lengths, (size_t)num_parents * 4, child_lengths,
+                                  (size_t)children * 4)))
         return CARAT_ERR_INVALID_ARG;
     p.page_table = page_table;
     p.num_parents = num_parents;

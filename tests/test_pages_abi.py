@@ -46,6 +46,21 @@ def test_chunk_checks(carat, kw, status):
     assert _chunk(carat.library(), **kw) == status
 
 
+@pytest.mark.parametrize("name,least,most", [
+    # bytes before and behind `out` (4 x 2 x 16 x 512 bf16 values) that a buffer may begin at
+    ("q", 2 * 4 * 16 * 512 * 2, 2 * 4 * 16 * 512 * 2),
+    ("kp", 8 * 128 * 2 * 512 * 2, 2 * 4 * 16 * 512 * 2),
+    ("vp", 8 * 128 * 2 * 512 * 2, 2 * 4 * 16 * 512 * 2)])
+def test_chunk_output_must_not_overlap(carat, name, least, most):
+    lib = carat.library()
+    at = 1 << 30
+    far = dict(out=at, q=at << 1, kp=at << 2, vp=at << 3, ws=at << 4, wsb=1 << 29)
+    for there in (at, at + most - 16, at - least + 16):
+        assert _chunk(lib, **{**far, name: there}) == INVALID
+    need = lib.carat_paged_chunk_workspace_bytes(2, 4, 16, 2, 512)
+    assert need == 0 or _chunk(lib, **{**far, "ws": at + most - 16}) == INVALID
+
+
 HEAD = ("kp", "vp", "ks", "vs", "num", "rows", "row_bytes", "R", "hkv")
 
 
