@@ -220,6 +220,11 @@ class SharedPool:
         src, dst = self.alloc.plan_compaction(max_moves)
         if src:
             src, dst = _i32(src, self.device), _i32(dst, self.device)
+            if stream is not None:   # not to be given to others before that stream is done
+                if not isinstance(stream, torch.cuda.Stream):
+                    stream = torch.cuda.ExternalStream(int(stream), device=self.device)
+                src.record_stream(stream)
+                dst.record_stream(stream)
             whole = (self.num_pages, 1, 1, self.page_bytes)
             carat.carat_pages_move(self.k.view(torch.uint8).view(whole),
                                    self.v.view(torch.uint8).view(whole), src, dst, stream=stream)

@@ -207,3 +207,33 @@ def test_a_captured_decode_step_over_a_windowed_layer():
     replayed = step.replay()[0].clone()
     assert not torch.equal(replayed, eager)
     assert torch.equal(step.run()[0], replayed)
+
+
+@pytest.mark.parametrize("raw", [False, True])
+def test_a_compaction_on_another_stream_keeps_its_lists(raw):
+    """Lists of the same size are made while the moves still wait on their stream (what they
+    hold, -1, would move nothing)."""
+    pool = engine.SharedPool(num_pages=64, page_bytes=128 * 2 * 256 * 2, pages_per_ring=4, fill=None)
+    pool.k.view(torch.int16).copy_(torch.arange(64, device="cuda").repeat_interleave(
+        pool.page_bytes // 2))
+    pool.v.copy_(pool.k)
+    pages = pool.alloc.alloc_pages(40)
+    assert pool.alloc.free_pages([p for i, p in enumerate(pages) if i % 4 != 1])
+    kept = pages[1::4]
+    layer = engine.PagedGlobalLayer(pool, i32([kept]), q_heads=4, kv_heads=2, head_dim=256,
+                                    max_chunk=4)
+    slow = torch.empty(1 << 30, dtype=torch.uint8, device="cuda")
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for _ in range(100):
+            slow.copy_(slow.flip(0))
+    moved = pool.compact([layer], 100, stream=side.cuda_stream if raw else side)
+    assert moved > 0
+    others = [i32([-1] * moved) for _ in range(64)]
+    torch.cuda.synchronize()
+    assert len(others) == 64
+    table = layer.page_table[0].tolist()
+    assert sum(a != b for a, b in zip(table, kept)) == moved
+    held = pool.k.view(torch.int16).view(64, -1)[:, 0].tolist()
+    assert [held[t] for t in table] == kept
