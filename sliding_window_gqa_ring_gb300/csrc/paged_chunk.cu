@@ -848,13 +848,15 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
             if (!alive) break;
             g += n;
             // While the last product runs: a row's sum, its place.  (In the last tile's place:
-            // the next tile's may be written before this is read.)
-            sh->row[(g - 1) & 1][part][row] = l;
+            // the next tile's may be written before this is read.  Each thread writes over the
+            // other's maximum, which it alone has read, not over its own, which the other may
+            // still read.)
+            sh->row[(g - 1) & 1][part ^ 1][row] = l;
             if (rows_barrier(quad, !alive)) {
                 alive = false;
                 break;
             }
-            l += sh->row[(g - 1) & 1][part ^ 1][row];
+            l += sh->row[(g - 1) & 1][part][row];
             const bool partial = tiles.it.splits > 1;
             const int split = tiles.it.split, d0 = tiles.it.vh * kDV;
             const int held = min(plan.tokens, tiles.it.n - lo_row);   // tokens that have rows here
