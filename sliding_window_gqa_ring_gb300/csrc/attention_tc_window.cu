@@ -1,5 +1,9 @@
 // attention_tc_window.cu -- the stream-K attention over bf16 pages under a window with first
 // tokens that stay visible (kPagedWindow): the few-row form of the attention of a chunk.
+// A request's few rows are the products' short side (16 to 64), its keys the long one: the bound
+// is the keys' and values' bytes.  64 requests of 4 tokens under a window of 4096 with 16 first
+// tokens take 157 us, 67% of the copy rate (104.7 us); where the pairs of paged_chunk.cu take
+// over is at few_rows there.
 // Compiled apart from attention_tc.cu so the builds run side by side.
 #include "attention_tc.cuh"
 

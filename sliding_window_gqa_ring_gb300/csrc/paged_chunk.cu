@@ -16,10 +16,18 @@
 // takes one half of the value dimensions and the scores are computed for each half again
 // (1.5 times the operations).
 //
-// What bounds it: the tensor pipe.  A pair reads K and V tiles at 32 bytes a cycle and SM
-// from L2, against 64 without pairs, which L2 could not give.
+// What bounds it: the tensor pipe, where rows are many.  A pair reads K and V tiles at 32
+// bytes a cycle and SM from L2, against 64 without pairs, which L2 could not give.  Measured:
+// 8191 tokens of 16 heads over 8 of 256, 287 us, 1915 TFLOP/s (the library's product reaches
+// 1917); over 2 of 512, 817 us, 1345 TFLOP/s of what is asked for and 2017 with the scores
+// computed twice.  Under a window an item is short (9 tiles at a window of 1024) and its
+// ends show: 8192 tokens 102 us, 1260 TFLOP/s.  There from the last product of an item to
+// the first of the next 6000 cycles pass: its output 3700 (64 KB a CTA leave at about 32
+// bytes a cycle), then the next scores' way to the softmax, 1500 for their weights.  Storing
+// with the copy engine from shared memory, the output on warps of its own, and finding the
+// next item during the present one gained 2% at most together and cost short calls 5%.
 //
-// Softmax.  One thread a row, 128 keys of a tile in registers.  The running maximum is
+// Softmax.  Two threads a row, 64 keys of a tile each in registers.  The running maximum is
 // replaced only when a tile exceeds it by more than 8 (log2 units), so O is rarely read
 // back and rescaled; P <= 2^8.  P is rounded to bf16 (the tensor core's operand, with V
 // bf16; 2^-8 of each weight) and the rounded weights are summed, so numerator and
@@ -28,8 +36,8 @@
 // Keys.  An item (request, KV head, row tile, value half, split) walks the tiles that hold
 // a key some row of the pair sees: those of the sinks, then from the first row's window to
 // the last row's position.  A tile some row sees only in part is masked by position.  Its
-// V rows could carry what no row may see into O through 0 x infinity: the softmax threads
-// look through such a tile's V for values that are not finite and zero those rows, and
+// V rows could carry what no row may see into O through 0 x infinity: two warps look
+// through such a tile's V for values that are not finite and zero those rows, and
 // rows behind the last key, before the product; a row that sees such a key is written as
 // NaN.
 //
@@ -41,18 +49,18 @@
 // Schedule.  The grid has a CTA pair for every item, up to a few times the pairs that fit;
 // a pair that has finished takes over the work of one that has not been launched (cluster
 // launch control), so the items, of very different lengths under masks, windows and counts,
-// go to whoever is free.  The producer asks, finds the item and hands it to the other roles through
-// a ring of four.  The next item's keys and queries are loaded and its first scores computed
-// while the last one's output leaves.  Code that runs once an item is kept short (rolled
-// loops, one copy): it comes from a cold instruction cache, and an unrolled output of the
-// same work took 5000 cycles.
+// go to whoever is free.  The producer asks, finds the item and hands it to the other roles
+// through a ring of four.  The next item's keys and queries are loaded and its first scores
+// computed while the last one's output leaves.  Code that runs once an item is kept short
+// (rolled loops, one copy): it comes from a cold instruction cache, and an unrolled output
+// of the same work took 5000 cycles.
 //
 // Warp roles (384 threads): warp 0 TMA producer (each CTA its own halves, counted on the
 // leader's barriers), warp 1 of the leader issues the products, warps 2-3 look through V,
-// warps 4-11 softmax, rescale and output: two threads a row, the first 64 keys of a tile and the others (one thread a
-// row took 1.9 us a tile at head_dim 256, nearly twice the products' time).  Every wait is
-// bounded: on a timeout CARAT_DEV_TIMEOUT is set and the CTA stops, waits for its own
-// copies and products, and returns.
+// warps 4-11 softmax, rescale and output (one thread a row took 1.9 us a tile at head_dim
+// 256, nearly twice the products' time).  Every wait is bounded: on a timeout
+// CARAT_DEV_TIMEOUT is set and the CTA stops, waits for its own copies and products, and
+// returns.
 #include <algorithm>
 #include <atomic>
 #include <cfloat>

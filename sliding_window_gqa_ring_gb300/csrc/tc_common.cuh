@@ -308,18 +308,6 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t *r) {
         : "memory");
 }
 
-// 16 TMEM lanes by 32 columns: lane l of the warp reads rows l / 4 (r[4 q], r[4 q + 1]) and
-// l / 4 + 8 (r[4 q + 2], r[4 q + 3]), columns 8 q + 2 (l % 4) and the next, q = 0 .. 3.
-__device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t taddr, uint32_t (&r)[16]) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
-        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
-          "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-        : "r"(taddr));
-}
-
 // ---------------------------------------------------------------------------
 // CTA pairs (cta_group::2 in a cluster of two): one product over both SMs, rows of A
 // and columns of B held half by each CTA at the same shared-memory offsets, D's rows
