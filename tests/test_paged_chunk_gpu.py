@@ -313,6 +313,67 @@ def test_two_calls_at_once_with_workspaces_of_their_own():
         assert torch.equal(a, c.out)
 
 
+@pytest.mark.parametrize("q_heads,kv_heads,head_dim,window,counts", [
+    (16, 8, 256, 700, None), (16, 2, 512, 0, [900, 41])])
+def test_two_long_calls_at_once(q_heads, kv_heads, head_dim, window, counts):
+    """More items than CTA pairs run at once, of two launches: whose work is taken over when
+    depends on the other."""
+    cases = [Case([0, 600], 900, q_heads, kv_heads, head_dim, window=window, sinks=9,
+                  counts=counts, seed=s).device() for s in (21, 22)]
+    alone = [c.call().clone() for c in cases]
+    for c, out in zip(cases, alone):
+        c.check(out, rows=[0, 1, 40, 127, 128, 500, 899])
+    streams = [torch.cuda.Stream() for _ in cases]
+    for _ in range(10):
+        for c in cases:
+            c.out.fill_(7.0)
+        torch.cuda.synchronize()
+        for s, c in zip(streams, cases):
+            with torch.cuda.stream(s):
+                c.call()
+        torch.cuda.synchronize()
+        for a, c in zip(alone, cases):
+            assert torch.equal(a, c.out)
+
+
+@pytest.mark.parametrize("q_heads,kv_heads,head_dim,k", [(16, 8, 256, 130), (16, 2, 512, 130),
+                                                         (16, 2, 512, 3)])
+def test_views_that_begin_on_16_bytes(q_heads, kv_heads, head_dim, k):
+    c = Case([300, 5], k, q_heads, kv_heads, head_dim, window=200, sinks=3, seed=23).device()
+    want = c.call().clone()
+    c.check(want)
+    for name in ("dq", "dk", "dv", "out", "ws"):
+        t = getattr(c, name)
+        if t is None:
+            continue
+        buf = torch.zeros(t.numel() + 16, dtype=t.dtype, device="cuda")
+        at = -buf.data_ptr() % 32 // t.element_size() + 16 // t.element_size()
+        view = buf[at:at + t.numel()].view(t.shape)
+        view.copy_(t)
+        assert view.data_ptr() % 32 == 16
+        setattr(c, name, view)
+    c.out.fill_(7.0)
+    assert torch.equal(c.call(), want)
+
+
+def test_a_call_reads_what_the_one_before_wrote():
+    """Each call's queries are the outputs of the one before, nothing in between waits."""
+    def chain(wait):
+        c = Case([2000, 9], 4, 16, 2, 512, seed=24, spread=20.0).device()
+        outs = []
+        for _ in range(20):
+            c.out = torch.empty_like(c.dq)
+            c.call()
+            if wait:
+                torch.cuda.synchronize()
+            outs.append(c.out)
+            c.dq = c.out
+        torch.cuda.synchronize()
+        return outs
+    for a, b in zip(chain(True), chain(False)):
+        assert torch.equal(a, b)
+
+
 def test_no_requests_and_bad_arguments():
     c = Case([10], 4, 4, 2, 256, seed=17).device()
     carat.carat_paged_chunk_attention(c.out[:0], c.dq[:0], c.dk, c.dv, c.dt[:0], c.dc[:0],
