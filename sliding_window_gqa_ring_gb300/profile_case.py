@@ -8,7 +8,8 @@ repeats ``--calls`` times (with ``--separate``: one carat_ring_append, then the
 attention call alone repeats), so a profiler filtered on the attention kernel
 sees exactly ``--calls`` launches.  The ``paged_*`` cases run the paged operators
 over random contents instead.  Every case but global_mixed keeps a few
-GB or less on the device; every case reads more than the 129 MB L2 per call.
+GB or less on the device; every case but chunk_global, whose keys fit it, reads more
+than the 129 MB L2 per call.
 """
 from __future__ import annotations
 
@@ -43,7 +44,13 @@ PAGED = {
     # rotary appends of eight ragged prompts (the keys are the prompt's)
     "paged_rope": (8, 1024, 16, 8, 256, 0),
     "paged_rope_fp8": (8, 1024, 16, 8, 256, 0),
+    # attention of a chunk: prompts under a window of 1024, one prompt without, and few rows
+    # of many requests under a window of 4096 with 16 first tokens
+    "chunk_window": (8, 2048, 16, 8, 256, 2048),
+    "chunk_global": (1, 8192, 16, 2, 512, 8192),
+    "chunk_few_rows": (64, 4, 16, 2, 512, 4608),
 }
+CHUNK_WINDOWS = {"chunk_window": (1024, 0), "chunk_global": (0, 0), "chunk_few_rows": (4096, 16)}
 
 
 def run_paged(case: str, calls: int):
@@ -65,6 +72,15 @@ def run_paged(case: str, calls: int):
         for _ in range(calls):
             carat.carat_paged_verify_attention_fp8(out, q, kp, vp, scales, scales, table, ctx,
                                                    scale=d ** -0.5, workspace=ws)
+        return
+    if case in CHUNK_WINDOWS:
+        window, sinks = CHUNK_WINDOWS[case]
+        kp, vp = (torch.randn(shape, generator=g, device="cuda").bfloat16() for _ in range(2))
+        ctx = torch.full((batch,), keys - k, dtype=torch.int32, device="cuda")
+        ws = carat.workspace_tensor(carat.paged_chunk_workspace_bytes(batch, k, hq, hkv, d))
+        for _ in range(calls):
+            carat.carat_paged_chunk_attention(out, q, kp, vp, table, ctx, scale=d ** -0.5,
+                                              window=window, sinks=sinks, workspace=ws)
         return
     dtype = torch.uint8 if case.endswith("fp8") else torch.bfloat16
     kp, vp = (torch.zeros(shape, dtype=dtype, device="cuda") for _ in range(2))
