@@ -21,7 +21,7 @@
 // 8191 tokens of 16 heads over 8 of 256, 287 us, 1915 TFLOP/s (the library's product reaches
 // 1917); over 2 of 512, 817 us, 1345 TFLOP/s of what is asked for and 2017 with the scores
 // computed twice.  Under a window an item is short (9 tiles at a window of 1024) and its
-// ends show: 8192 tokens 102 us, 1260 TFLOP/s.  There from the last product of an item to
+// ends show: 8192 tokens 99 us, 1300 TFLOP/s.  There from the last product of an item to
 // the first of the next 6000 cycles pass: its output 3700 (64 KB a CTA leave at about 32
 // bytes a cycle), then the next scores' way to the softmax, 1500 for their weights.  Storing
 // with the copy engine from shared memory, the output on warps of its own, and finding the
@@ -84,6 +84,8 @@ constexpr int kJobs = 4;                // items handed to the other roles
 constexpr int kPieceCost = 3;           // of a piece besides its key tiles, in key tiles
 constexpr int kUnits = 8;               // CTA pairs of the grid, times the pairs that fit
 constexpr int kMasked = 8;              // masked tiles of an item: 3 + 3 + 1 at most
+constexpr int kRecords = 5;             // items whose masked tiles' V is on record
+constexpr uint32_t kInTurn = 3;         // masked tiles whose V is on its way
 constexpr uint32_t kFull = 0xffffffffu;
 constexpr float kSlack = 8.0f;          // log2 units
 
@@ -93,6 +95,7 @@ struct Lay {
     // Stage ring; five stages at head_dim 256 were no faster (323 us against 290, 8191 tokens).
     static constexpr int NS = D == 256 ? 4 : 3;
     static constexpr int kSlab = kRows * 128;           // 64 d of Q
+    static_assert(NS <= 4, "the records of masked tiles and their barriers count on it");
     static constexpr int kOffQ = NS * kStage;
     static constexpr int kOffOut = D == 512 ? kOffQ : kOffQ + D / 64 * kSlab;
     // The output's way out: 32 rows of 128 bytes a softmax warp.  At head_dim 512 the place
@@ -331,8 +334,11 @@ struct Shared {
     uint64_t s_full[2];     // both: a tile's scores are in tensor memory
     uint64_t p_full[2];     // leader: its weights are
     uint64_t pv_done[2];    // both: a tile's value product is done (tiles in turn)
-    uint64_t v_ready;       // both: a masked tile's V has landed
-    uint64_t v_clean;       // leader: it is looked through
+    // Masked tiles in turn.  The third next one's V is loaded four loads later or more, when
+    // this one's product is done; the second next one's can be three later (an item's last
+    // two V's follow one another, an item of one tile has one K before its V).
+    uint64_t v_ready[kInTurn];   // each CTA's own: its half of the tile's V has landed
+    uint64_t v_clean[kInTurn];   // leader: both halves are looked through
     uint64_t drain;
     uint64_t job_full[kJobs], job_empty[kJobs];   // each CTA's own
     uint64_t answered[kJobs];                     // each CTA's own
@@ -340,14 +346,17 @@ struct Shared {
     uint32_t tmem;
     int abort_flag;
     Job job[kJobs];
-    // Keys of masked tiles with values that are not finite, of three items that have such
-    // tiles in turn.  At a masked tile of one of them every softmax warp is past the one
-    // before the last (the products wait for the weights of all), so its record is cleared
-    // there, for the next: nothing is written to that before this CTA's warps have said
-    // that the tile is looked through.
-    uint32_t poison[3];
-    uint32_t bad[3][kMasked][4];
-    float row[2][2][kRows];           // a row's two threads tell each other
+    // Keys of masked tiles with values that are not finite, of kRecords items with such tiles
+    // in turn.  V of a tile lands when the products have used what its stage held, at most
+    // four loads before it, and a tile is two loads or more.  So while a CTA's warps have not
+    // said that the first such tile of item M (of these) is looked through, the other's are
+    // at item M + 1 at most; and the softmax warps are past item M - 3, as the products are
+    // past all of M - 2.  At that tile the record of M + 2, which was that of M - 3, is cleared.
+    uint32_t poison[kRecords];
+    uint32_t bad[kRecords][kMasked][4];
+    // A row's two threads tell each other.  They change places every time: each writes over
+    // what the other told last, which it alone has read.
+    float row[2][kRows];
 };
 
 // Bounded wait; false on a timeout or when another role of this CTA gave up.  kCluster:
@@ -438,9 +447,11 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
             tc::mbar_init(&sh->p_full[i], 16);
             tc::mbar_init(&sh->pv_done[i], 1);
         }
-        for (int i = 0; i < 3; ++i) sh->poison[i] = 0;
-        tc::mbar_init(&sh->v_ready, 1);
-        tc::mbar_init(&sh->v_clean, 4);
+        for (int i = 0; i < kInTurn; ++i) {
+            tc::mbar_init(&sh->v_ready[i], 1);
+            tc::mbar_init(&sh->v_clean[i], 4);
+        }
+        for (int i = 0; i < kRecords; ++i) sh->poison[i] = 0;
         tc::mbar_init(&sh->drain, 1);
         for (int i = 0; i < kJobs; ++i) {
             tc::mbar_init(&sh->job_full[i], 1);
@@ -450,7 +461,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         tc::fence_mbar_init();
         sh->abort_flag = 0;
     }
-    if (threadIdx.x < 3 * kMasked * 4) (&sh->bad[0][0][0])[threadIdx.x] = 0;
+    if (threadIdx.x < kRecords * kMasked * 4) (&sh->bad[0][0][0])[threadIdx.x] = 0;
     if (warp == 1) {
         tc::tmem_alloc_pair(&sh->tmem, 512);
         tc::tmem_relinquish_pair();
@@ -486,7 +497,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
 
     if (warp == 0) {
         // ---------------------------------------------------------------- producer
-        uint32_t cnt = 0, items = 0;
+        uint32_t cnt = 0, items = 0, masked_v = 0;   // stages, items, V of masked tiles
         bool alive = true;
         const uint32_t q_bytes = plan.tokens * p.group * 128;
         uint32_t published = 0, asked = 0;
@@ -553,14 +564,24 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                     }
                 }
             };
-            auto load = [&](bool is_v, int row, int part) {
+            auto load = [&](bool is_v, int row, int part, bool masked) {
                 const int s = cnt % NS;
                 if (cnt >= NS && alive)
                     alive = warp_wait(&sh->empty[s], ((cnt / NS) & 1) ^ 1, abort_flag, p.dev_status);
                 if (!alive) return;
                 if (lane == 0) {
-                    if (rank == 0) tc::mbar_arrive_expect_tx(&sh->full[s], 2 * kStage);
-                    const uint32_t bar = tc::map_to_rank(&sh->full[s], 0);
+                    // V of a masked tile is counted by each CTA for itself, so that it is looked
+                    // through as soon as it is there (the products wait for that, not for the
+                    // bytes): waiting for the products' warp to come to it cost 1700 cycles.
+                    uint64_t *own = &sh->v_ready[masked_v % kInTurn];
+                    if (masked) {
+                        tc::mbar_arrive_expect_tx(own, kStage);
+                        if (rank == 0) tc::mbar_arrive(&sh->full[s]);
+                    } else if (rank == 0) {
+                        tc::mbar_arrive_expect_tx(&sh->full[s], 2 * kStage);
+                    }
+                    const uint32_t bar = masked ? tc::map_to_rank(own, rank)
+                                                : tc::map_to_rank(&sh->full[s], 0);
                     // a page outside the pool: rows behind the tensor's end read as zeros
                     const int at =
                         row < 0 ? p.num_pages * p.page_rows : row + (is_v ? 0 : rank * 64);
@@ -571,6 +592,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                         tc::tma_load_4d_pair(smem + s * kStage, &map_k, 0, at, part * 4, it.c, bar);
                 }
                 ++cnt;
+                masked_v += masked;
             };
             int prev = 0;
             for (int x = 0; x <= n && alive; ++x) {
@@ -578,7 +600,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                 if (x < n) {
                     if ((x & 31) == 0) fetch(x);
                     row = __shfl_sync(kFull, row_held, x & 31);
-                    for (int k = 0; k < KST; ++k) load(false, row, k);
+                    for (int k = 0; k < KST; ++k) load(false, row, k, false);
                 }
                 if (x == 0 && alive) {
                     // the queries' place is free when the last item's last scores are computed
@@ -593,7 +615,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                     }
                     if (alive) ++items;
                 }
-                if (x > 0) load(true, prev, 0);
+                if (x > 0) load(true, prev, 0, tiles.keys.masked(p, tiles.base(x - 1)));
                 prev = row;
                 if (x == 0 && !pending && alive) ask();   // for the work after this
             }
@@ -601,6 +623,8 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         // An answer that is still on its way lands before anyone leaves, and what both CTAs'
         // copies still carry.
         if (!alive && pending) tc::mbar_wait(&sh->answered[asked % kJobs], (asked / kJobs) & 1);
+        for (uint32_t i = masked_v > kInTurn ? masked_v - kInTurn : 0; !alive && i < masked_v; ++i)
+            tc::mbar_wait(&sh->v_ready[i % kInTurn], (i / kInTurn) & 1);
         if (!alive && rank == 0) {
             if (items > 0) tc::mbar_wait(&sh->q_full, (items - 1) & 1);
             for (uint32_t i = cnt > NS ? cnt - NS : 0; i < cnt; ++i)
@@ -653,12 +677,8 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                 if (!alive) break;
                 const uint32_t phase = ((g + y) >> 1) & 1;
                 if (tiles.keys.masked(p, tiles.base(y))) {
-                    if (lane == 0) {
-                        tc::mbar_arrive_remote(tc::map_to_rank(&sh->v_ready, 0));
-                        tc::mbar_arrive_remote(tc::map_to_rank(&sh->v_ready, 1));
-                    }
-                    __syncwarp();
-                    alive = warp_wait<true>(&sh->v_clean, vcnt & 1, abort_flag, p.dev_status);
+                    alive = warp_wait<true>(&sh->v_clean[vcnt % kInTurn], (vcnt / kInTurn) & 1,
+                                            abort_flag, p.dev_status);
                     ++vcnt;
                 }
                 alive = alive && warp_wait(&sh->p_full[buf], phase, abort_flag, p.dev_status);
@@ -695,11 +715,12 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
             for (int x = 0; x < n; ++x) {
                 const int t0 = tiles.base(x);
                 if (!tiles.keys.masked(p, t0)) continue;
-                alive = warp_wait<true>(&sh->v_ready, vcnt & 1, abort_flag, p.dev_status);
+                alive = warp_wait(&sh->v_ready[vcnt % kInTurn], (vcnt / kInTurn) & 1, abort_flag,
+                                  p.dev_status);
                 if (!alive) break;
                 ++vcnt;
-                if (warp == 2 && i == 0) {   // the record of the next item with masked tiles
-                    const int after = turn == 2 ? 0 : turn + 1;
+                if (warp == 2 && i == 0) {   // the record of the item after the next
+                    const int after = turn + 2 < kRecords ? turn + 2 : turn + 2 - kRecords;
                     (&sh->bad[after][0][0])[lane] = 0;
                     if (lane == 0) sh->poison[after] = 0;
                 }
@@ -749,7 +770,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                 ++i;
                 __syncwarp();
                 if (lane == 0) {
-                    const uint32_t bar = tc::map_to_rank(&sh->v_clean, 0);
+                    const uint32_t bar = tc::map_to_rank(&sh->v_clean[(vcnt - 1) % kInTurn], 0);
                     if (wrote)
                         tc::mbar_arrive_cluster(bar);
                     else
@@ -757,7 +778,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                 }
             }
             cnt += n * (KST + 1);
-            if (i > 0) turn = turn == 2 ? 0 : turn + 1;
+            if (i > 0) turn = turn == kRecords - 1 ? 0 : turn + 1;
         }
     } else if (warp >= 4) {
         // ---------------------------------------------------------------- softmax
@@ -770,6 +791,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         const float scale = fmaxf(fabsf(p.scale_log2), FLT_MIN);
         uint32_t g = 0;   // tiles before this item's
         int turn = 0;     // which of the poison records
+        int told = 0;     // whose place is whose
         bool alive = true;
         while (const Job *job = take(alive)) {
             const Job &tiles = *job;   // given back when the output's places are known
@@ -805,12 +827,13 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                 const float own = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
                 // After this barrier both threads of a row hold their scores, so the weights
                 // may take their place.
-                sh->row[buf][part][row] = own;
+                sh->row[part ^ told][row] = own;
                 if (rows_barrier(quad, !alive)) {
                     alive = false;
                     break;
                 }
-                const float tm = fmaxf(own, sh->row[buf][part ^ 1][row]) * scale;
+                told ^= 1;
+                const float tm = fmaxf(own, sh->row[part ^ told][row]) * scale;
                 const bool grow = tm > m + kSlack;
                 if (__any_sync(kFull, grow)) {
                     const float m_new = grow ? tm : m;
@@ -855,16 +878,14 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
             }
             if (!alive) break;
             g += n;
-            // While the last product runs: a row's sum, its place.  (In the last tile's place:
-            // the next tile's may be written before this is read.  Each thread writes over the
-            // other's maximum, which it alone has read, not over its own, which the other may
-            // still read.)
-            sh->row[(g - 1) & 1][part ^ 1][row] = l;
+            // While the last product runs: a row's sum, its place.
+            sh->row[part ^ told][row] = l;
             if (rows_barrier(quad, !alive)) {
                 alive = false;
                 break;
             }
-            l += sh->row[(g - 1) & 1][part][row];
+            told ^= 1;
+            l += sh->row[part ^ told][row];
             const bool partial = tiles.it.splits > 1;
             const int split = tiles.it.split, d0 = tiles.it.vh * kDV;
             const int held = min(plan.tokens, tiles.it.n - lo_row);   // tokens that have rows here
@@ -907,7 +928,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                     ++i;
                 }
             }
-            if (has_masked) turn = turn == 2 ? 0 : turn + 1;
+            if (has_masked) turn = turn == kRecords - 1 ? 0 : turn + 1;
             if (poisoned) f = NAN;
             give_back();
             // O leaves through shared memory, 128 bytes of each of the warp's 32 rows at a
