@@ -1860,9 +1860,9 @@ __global__ void __launch_bounds__(NR > 0 ? kThreads + kConvThreads : kThreads, M
                         // is not finite: the rows that see it become NaN.
                         const bool some = ki.data && rowmask != low_bits(rows_here);
                         bool bad = false;
-                        // The stages of V held the next tile's K before (with four of them), and
-                        // a wait for V could pass by the parity of what was there before that K:
-                        // once the next scores are there, that K has been used.
+                        // A stage of V may have held the next tile's K before (with fewer than two
+                        // tiles of stages), and a wait for V could pass by the parity of what was
+                        // there before that K: once the next scores are there, that K has been used.
                         if (idx + 1 < n &&
                             !wait_or_abort(&s_full[(tile + 1) & 1], ((tile + 1) >> 1) & 1,
                                            abort_flag, p.dev_status))
@@ -1904,7 +1904,12 @@ __global__ void __launch_bounds__(NR > 0 ? kThreads + kConvThreads : kThreads, M
                             }
                         }
                     } else if (tile_partial || tile_writes) {
-                        for (int vs = 0; vs < KS; ++vs) {
+                        // (as above: with fewer than two tiles of stages)
+                        if (NS < 2 * KS && idx + 1 < n &&
+                            !wait_or_abort(&s_full[(tile + 1) & 1], ((tile + 1) >> 1) & 1,
+                                           abort_flag, p.dev_status))
+                            alive = false;
+                        for (int vs = 0; alive && vs < KS; ++vs) {
                             const uint32_t x_cnt = cnt_base + stages_before(v_part(idx, n)) + vs;
                             const int s = x_cnt % NS;
                             if (!wait_or_abort(&full[s], (x_cnt / NS) & 1, abort_flag,

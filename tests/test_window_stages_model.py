@@ -1,7 +1,7 @@
-"""Model of a CTA of the stream-K attention over pages under a window
-(csrc/attention_tc.cuh with kPagedWindow): the softmax looks through the V rows of tiles that
-not every query sees, wherever in a segment such a tile stands, so its waits for V's stages
-must not pass on another load's phase (CPU only)."""
+"""Model of a CTA of the stream-K attention (csrc/attention_tc.cuh): under a window over pages
+its softmax looks through the V rows of tiles that not every query sees, and a fused append
+writes into a ring's tiles once their V has landed, wherever in a segment such a tile stands.
+So its waits for V's stages must not pass on another load's phase (CPU only)."""
 import os
 import random
 import re
@@ -10,12 +10,11 @@ import pytest
 
 from test_paged_chunk_buffers_model import CSRC, Barrier, Wrong
 
-KS = 4              # stages of a K or V tile at head_dim 512
-
 
 class Cta:
-    def __init__(self, segments, rng, stages, next_scores=True):
-        self.segments, self.rng, self.NS, self.next_scores = segments, rng, stages, next_scores
+    def __init__(self, segments, rng, stages, ks, next_scores=True):
+        self.segments, self.rng, self.NS, self.KS = segments, rng, stages, ks
+        self.next_scores = next_scores
         self.full = [Barrier(1) for _ in range(stages)]
         self.empty = [Barrier(1) for _ in range(stages)]
         self.s_full = [Barrier(1) for _ in range(2)]
@@ -37,7 +36,7 @@ class Cta:
         cnt = 0
         for j, masks in enumerate(self.segments):
             for kind, x in self.order(len(masks)):
-                for part in range(KS):
+                for part in range(self.KS):
                     s = cnt % self.NS
                     if cnt >= self.NS:
                         while not self.empty[s].passed(cnt // self.NS - 1):
@@ -63,7 +62,7 @@ class Cta:
                 if kind == "V":
                     while not self.p_full.passed(g + x):
                         yield
-                for part in range(KS):
+                for part in range(self.KS):
                     s = cnt % self.NS
                     while not self.full[s].passed(cnt // self.NS):
                         yield
@@ -94,8 +93,8 @@ class Cta:
                     if self.next_scores and x + 1 < n:
                         while not self.s_full[(tile + 1) & 1].passed((tile + 1) >> 1):
                             yield
-                    at = base + self.order(n).index(("V", x)) * KS
-                    for part in range(KS):
+                    at = base + self.order(n).index(("V", x)) * self.KS
+                    for part in range(self.KS):
                         while not self.full[(at + part) % self.NS].passed((at + part) // self.NS):
                             yield
                         if self.stage[(at + part) % self.NS] != (j, "V", x, part):
@@ -103,7 +102,7 @@ class Cta:
                 yield
                 self.p_full.arrive()
             g += n
-            base += 2 * n * KS
+            base += 2 * n * self.KS
 
     def run(self):
         roles = [self.producer(), self.issuer(), self.softmax()]
@@ -135,22 +134,29 @@ def segments_of(rng):
 
 
 def instantiated():
-    text = open(os.path.join(CSRC, "attention_tc_window.cu")).read()
-    return sorted({int(x) for x in re.findall(r"launch_tc<512, \d+, (\d+), 1, 0, false, true>", text)})
+    """(stages, stages of a tile) of the kernels whose rings are shorter than two tiles."""
+    window = open(os.path.join(CSRC, "attention_tc_window.cu")).read()
+    found = {(int(x), 4) for x in re.findall(r"launch_tc<512, \d+, (\d+), 1, 0, false, true>",
+                                             window)}
+    ring = "".join(open(os.path.join(CSRC, f)).read()
+                   for f in ("attention_tc.cu", "attention_tc_unit.cu"))
+    found |= {(int(x), 2) for x in re.findall(r"launch_tc<256, \d+, (\d+), \d(?:>|, 0, true>)",
+                                              ring) if int(x) < 4}
+    return sorted(found)
 
 
 @pytest.mark.parametrize("seed", range(40))
 def test_the_kernels_rings(seed):
-    assert instantiated() == [4, 5]
-    for stages in instantiated():
-        for i in range(5):
+    assert instantiated() == [(3, 2), (4, 4), (5, 4)]
+    for stages, ks in instantiated():
+        for i in range(4):
             rng = random.Random(1000 * seed + i)
-            Cta(segments_of(rng), rng, stages).run()
+            Cta(segments_of(rng), rng, stages, ks).run()
 
 
-@pytest.mark.parametrize("stages", [4, 5])
-def test_without_the_next_scores_a_wait_passes_too_early(stages):
+@pytest.mark.parametrize("stages,ks", [(3, 2), (4, 4), (5, 4)])
+def test_without_the_next_scores_a_wait_passes_too_early(stages, ks):
     with pytest.raises(Wrong):
         for seed in range(4000):
             rng = random.Random(seed)
-            Cta(segments_of(rng), rng, stages, next_scores=False).run()
+            Cta(segments_of(rng), rng, stages, ks, next_scores=False).run()
