@@ -22,10 +22,11 @@
 // 1917); over 2 of 512, 817 us, 1345 TFLOP/s of what is asked for and 2017 with the scores
 // computed twice.  Under a window an item is short (9 tiles at a window of 1024) and its
 // ends show: 8192 tokens 99 us, 1300 TFLOP/s.  There from the last product of an item to
-// the first of the next 6000 cycles pass: its output 3700 (64 KB a CTA leave at about 32
-// bytes a cycle), then the next scores' way to the softmax, 1500 for their weights.  Storing
-// with the copy engine from shared memory, the output on warps of its own, and finding the
-// next item during the present one gained 2% at most together and cost short calls 5%.
+// the first of the next 6000 to 7000 cycles pass, where a tile takes 2150: its output 2500
+// to 3700 (64 KB a CTA leave at about 32 bytes a cycle), the next scores' way to the
+// softmax, 1500 for their weights.  Storing with the copy engine from shared memory, and
+// finding the next item during the present one, changed that case and the others by 1% and
+// cost short calls up to 7%; the output on warps of its own cost 18%.
 //
 // Softmax.  Two threads a row, 64 keys of a tile each in registers.  The running maximum is
 // replaced only when a tile exceeds it by more than 8 (log2 units), so O is rarely read
