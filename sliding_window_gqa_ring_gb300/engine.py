@@ -217,6 +217,13 @@ class SharedPool:
         max_moves pages move, and the page tables (and block scales) of `layers`, every
         layer with pages in this pool, follow.  Returns the pages moved; their old ids
         are free, so whoever keeps ids on the host reads the tables again."""
+        layers = list(layers)
+        for layer in layers:   # before the allocator counts the moves as done
+            table = layer.page_table
+            if table.dtype != torch.int32 or not table.is_contiguous() or \
+                    table.device != self.k.device:
+                raise ValueError("compact: a layer's page table must be a contiguous int32 "
+                                 "tensor on the pool's device")
         src, dst = self.alloc.plan_compaction(max_moves)
         if src:
             src, dst = _i32(src, self.device), _i32(dst, self.device)

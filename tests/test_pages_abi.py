@@ -237,3 +237,24 @@ def test_random_compactions_keep_every_page(carat, seed):
     for ring in rings:
         assert pool.free_ring(ring)
     assert pool.stats()["free_pages"] == n
+
+
+@pytest.mark.parametrize("table", ["strided", "long", "elsewhere"])
+def test_a_table_that_cannot_follow_is_refused_before_pages_are_counted_as_moved(carat, table):
+    import types
+
+    import torch
+
+    from sliding_window_gqa_ring_gb300 import engine
+    pool = engine.SharedPool(num_pages=8, page_bytes=256, pages_per_ring=4, device="cpu")
+    pages = pool.alloc.alloc_pages(8)
+    assert pool.alloc.free_pages(pages[1:4] + pages[5:])
+    before = pool.alloc.stats()
+    bad = {"strided": torch.zeros((2, 8), dtype=torch.int32)[:, ::2],
+           "long": torch.zeros((2, 4), dtype=torch.int64),
+           "elsewhere": torch.zeros((2, 4), dtype=torch.int32, device="meta")}[table]
+    good = types.SimpleNamespace(page_table=torch.zeros((2, 4), dtype=torch.int32))
+    with pytest.raises(ValueError):
+        pool.compact(iter([good, types.SimpleNamespace(page_table=bad)]), 8)
+    assert pool.alloc.stats() == before
+    assert pool.alloc.plan_compaction(8)[0]
