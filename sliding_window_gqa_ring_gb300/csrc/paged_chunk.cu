@@ -1010,76 +1010,90 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     }
 }
 
-// Merges the pieces of split items: one CTA a row of the output, 16 bytes of it a thread,
-// kFlight pieces' loads in flight.  The first of them are on their way before it is known
-// how many pieces there are (one latency, not three after one another).
-template <int D>
+// Merges the pieces of split items: 16 bytes of a row of the output a thread, kFlight
+// pieces' loads in flight.  With one row a CTA the first of them are on their way before it
+// is known how many pieces there are (one latency, not three after one another).  Rows for
+// more CTAs than run at once (MANY) are shared out, `per` for each, and those of requests in
+// one piece passed over without a load: a CTA for each of 64000 that needed none took 70 us.
+template <int D, bool MANY>
 __global__ void __launch_bounds__(D / 4) paged_chunk_merge_kernel(
-    const __grid_constant__ PagedChunkParams p, const Plan plan) {
+    const __grid_constant__ PagedChunkParams p, const Plan plan, int rows, int per) {
     constexpr int kFlight = 8;
     wait_for_prior_launch();
     let_next_launch_start();
-    const size_t at = blockIdx.x;
-    const int token = blockIdx.x / p.q_heads;
-    const int b = token / p.k, j = token - b * p.k;
-    const float2 *ml = plan.part_ml + at * plan.splits;
-    const float4 *o = reinterpret_cast<const float4 *>(plan.part_o + at * plan.splits * D) +
-                      threadIdx.x;
+    const int last = MANY ? min(rows, (int)(blockIdx.x + 1) * per) : blockIdx.x + 1;
     float2 l[kFlight];
     float4 v[kFlight];
-    auto load = [&](int s0) {
+    for (int at = MANY ? blockIdx.x * per : blockIdx.x; at < last;) {
+        const int token = at / p.q_heads;
+        const int b = token / p.k, j = token - b * p.k;
+        const float2 *ml = plan.part_ml + (size_t)at * plan.splits;
+        const float4 *o = reinterpret_cast<const float4 *>(plan.part_o +
+                                                           (size_t)at * plan.splits * D) +
+                          threadIdx.x;
+        auto load = [&](int s0) {
 #pragma unroll
-        for (int i = 0; i < kFlight; ++i)
-            if (s0 + i < plan.splits) {
-                l[i] = ml[s0 + i];
-                v[i] = o[(size_t)(s0 + i) * (D / 4)];
-            }
-    };
-    load(0);
-    const Request rq = load_request(p, b);
-    const int pieces = plan.pieces[b];
-    if (!request_ok(p, rq) || j >= rq.n || pieces == 1) return;   // (one piece: written whole)
-    const int j0 = j / (2 * plan.tokens) * 2 * plan.tokens;
-    const Keys keys(p, (int)rq.ctx + j0, (int)rq.ctx + min(j0 + 2 * plan.tokens, rq.n) - 1);
-    float top = -INFINITY, sum = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    int from = 0;
+            for (int i = 0; i < kFlight; ++i)
+                if (s0 + i < plan.splits) {
+                    l[i] = ml[s0 + i];
+                    v[i] = o[(size_t)(s0 + i) * (D / 4)];
+                }
+        };
+        if (!MANY) load(0);
+        const Request rq = load_request(p, b);
+        const int pieces = plan.pieces[b];
+        if (!request_ok(p, rq) || j >= rq.n || pieces == 1) {   // (one piece: written whole)
+            if (!MANY) return;
+            at = (b + 1) * p.k * p.q_heads;
+            continue;
+        }
+        if (MANY) load(0);
+        const int j0 = j / (2 * plan.tokens) * 2 * plan.tokens;
+        const Keys keys(p, (int)rq.ctx + j0, (int)rq.ctx + min(j0 + 2 * plan.tokens, rq.n) - 1);
+        float top = -INFINITY, sum = 0.f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        int from = 0;
 #pragma unroll 1
-    for (int s0 = 0; s0 < pieces; s0 += kFlight) {
-        if (s0 > 0) load(s0);
-        float most = top;
-        bool have[kFlight];   // pieces without a tile wrote nothing
+        for (int s0 = 0; s0 < pieces; s0 += kFlight) {
+            if (s0 > 0) load(s0);
+            float most = top;
+            bool have[kFlight];   // pieces without a tile wrote nothing
 #pragma unroll
-        for (int i = 0; i < kFlight; ++i) {
-            const int to = split_at(keys.count, s0 + i + 1, pieces);
-            have[i] = s0 + i < pieces && to > from;
-            from = to;
-            if (have[i]) most = fmaxf(most, l[i].x);
-        }
-        const float ref = most == -INFINITY ? 0.f : most;
-        const float keep = fast_exp2(top - ref);
-        top = most;
-        sum *= keep;
-        acc.x *= keep, acc.y *= keep, acc.z *= keep, acc.w *= keep;
+            for (int i = 0; i < kFlight; ++i) {
+                const int to = split_at(keys.count, s0 + i + 1, pieces);
+                have[i] = s0 + i < pieces && to > from;
+                from = to;
+                if (have[i]) most = fmaxf(most, l[i].x);
+            }
+            const float ref = most == -INFINITY ? 0.f : most;
+            const float keep = fast_exp2(top - ref);
+            top = most;
+            sum *= keep;
+            acc.x *= keep, acc.y *= keep, acc.z *= keep, acc.w *= keep;
 #pragma unroll
-        for (int i = 0; i < kFlight; ++i) {
-            if (!have[i]) continue;
-            const float w = fast_exp2(l[i].x - ref);
-            sum = fmaf(w, l[i].y, sum);
-            acc.x = fmaf(w, v[i].x, acc.x);
-            acc.y = fmaf(w, v[i].y, acc.y);
-            acc.z = fmaf(w, v[i].z, acc.z);
-            acc.w = fmaf(w, v[i].w, acc.w);
+            for (int i = 0; i < kFlight; ++i) {
+                if (!have[i]) continue;
+                const float w = fast_exp2(l[i].x - ref);
+                sum = fmaf(w, l[i].y, sum);
+                acc.x = fmaf(w, v[i].x, acc.x);
+                acc.y = fmaf(w, v[i].y, acc.y);
+                acc.z = fmaf(w, v[i].z, acc.z);
+                acc.w = fmaf(w, v[i].w, acc.w);
+            }
         }
+        const float f = 1.f / sum;
+        reinterpret_cast<uint2 *>(p.out + (size_t)at * D)[threadIdx.x] =
+            make_uint2(pack_bf16(acc.x * f, acc.y * f), pack_bf16(acc.z * f, acc.w * f));
+        if (!MANY) return;
+        ++at;
     }
-    const float f = 1.f / sum;
-    reinterpret_cast<uint2 *>(p.out + at * D)[threadIdx.x] =
-        make_uint2(pack_bf16(acc.x * f, acc.y * f), pack_bf16(acc.z * f, acc.w * f));
 }
 
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
-constexpr size_t kPieceBytes = (size_t)32 << 20;
+// What pieces may leave, where the items are few (kFewItems for each pair) and where not.
+constexpr size_t kPieceBytes = (size_t)128 << 20, kPieceBytesMany = (size_t)32 << 20;
+constexpr int kFewItems = 3;
 
 struct Sizes {
     Plan plan;
@@ -1095,14 +1109,18 @@ Sizes sizes_of(int batch, int k, int q_heads, int kv_heads, int head_dim, bool w
     const int pairs = device_sm_count() / 2;
     const size_t row = (size_t)batch * k * q_heads * head_dim * sizeof(float);
     // Few items: as many pieces as make one for every pair.  Several requests without a window
-    // may differ much in length: up to kUnits pieces a pair, what they leave kept to
-    // kPieceBytes (planning and an extra launch cost 2 to 3 us, one long request among
-    // short ones up to half of the call).
+    // may differ much in length: up to kUnits pieces a pair, within what may be left.  Planning
+    // and an extra launch cost 3 us and more, and pieces are not taken over; one long request
+    // among short ones costs up to half of the call.  us, without and with pieces, requests of
+    // 64 tokens behind 500 to 30000 (16/2 heads of 512, 128 items) 575 and 321, 3 of 512 behind
+    // 500 to 12000 (192 items) 366 and 265, 5 of 842 behind up to 11349 (70 items) 113 and 71;
+    // but 8 of up to 512 behind up to 8000 (16/8 of 256, 256 items, 64 MB) 45 and 67.
     const long long one = items > 0 ? std::max<long long>(1, pairs / items) : 1;
     z.plan.splits = (int)one;
     if (items > 0 && items <= (long long)kUnits / 2 * pairs && batch > 1 && !window) {
         const long long most = std::min<long long>(kUnits * pairs / items, pairs);
-        z.plan.splits = (int)std::max(one, std::min<long long>(most, kPieceBytes / row));
+        const size_t room = items <= kFewItems * (long long)pairs ? kPieceBytes : kPieceBytesMany;
+        z.plan.splits = (int)std::max(one, std::min<long long>(most, room / row));
         z.plan.by_length = z.plan.splits > 1;
     }
     // Split items: every pair of the grid runs at once.  Else a pair that finds no item costs
@@ -1152,9 +1170,12 @@ cudaError_t launch(const PagedChunkParams &p, Sizes &z, cudaStream_t stream) {
     e = launch_dependent(kernel, dim3(2 * z.plan.units), dim3(kThreads),
                          L::kAlloc, stream, p, z.plan, map_q, map_k, map_v);
     if (e != cudaSuccess || z.plan.splits == 1) return e;
-    return launch_dependent(paged_chunk_merge_kernel<D>,
-                            dim3((unsigned)(p.batch * p.k * p.q_heads)), dim3(D / 4), 0, stream, p,
-                            z.plan);
+    const int rows = p.batch * p.k * p.q_heads;
+    const int at_once = device_sm_count() * (2048 / (D / 4)), per = (rows - 1) / at_once + 1;
+    return launch_dependent(per > 1 ? paged_chunk_merge_kernel<D, true>
+                                    : paged_chunk_merge_kernel<D, false>,
+                            dim3((rows - 1) / per + 1), dim3(D / 4), 0, stream, p, z.plan, rows,
+                            per);
 }
 
 }  // namespace

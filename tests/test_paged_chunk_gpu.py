@@ -336,6 +336,35 @@ def test_two_long_calls_at_once(q_heads, kv_heads, head_dim, window, counts):
             assert torch.equal(a, c.out)
 
 
+@pytest.mark.parametrize("q_heads,kv_heads,head_dim,ctx,k,counts", [
+    (16, 2, 512, [3000, 10, 500], 200, None),             # more rows than CTAs merge at once
+    (16, 2, 512, [3000, 10, 0, 700], 170, [170, 33, 0, 1]),
+    (16, 8, 256, [5000, 0, 130, 2900], 150, [3, 150, 0, 149]),
+    (8, 2, 256, [9, 7000, 64, 80, 300], 250, [250, 250, 1, 0, 129]),
+    (16, 8, 256, [0, 1], 400, None)])                      # no request needs a second piece
+def test_many_rows_in_pieces(q_heads, kv_heads, head_dim, ctx, k, counts):
+    c = Case(ctx, k, q_heads, kv_heads, head_dim, counts=counts, seed=25, spread=2.0).device()
+    assert c.ws is not None
+    out = c.call()
+    c.check(out, rows=[0, 1, 2, 15, 16, 31, 32, 63, 64, 127, 128, 148, 149, 169, 199, 249, 399])
+    again = out.clone()
+    c.out.fill_(7.0)
+    assert torch.equal(c.call(), again)
+
+
+def test_many_rows_in_pieces_with_a_rejected_request():
+    c = Case([3000, 40, 200], 200, 16, 2, 512, seed=26)
+    c.device()
+    c.dc[1] = c.kp.shape[1] * c.table.shape[1]     # its new tokens do not fit
+    out = c.call()
+    assert out[1].isnan().all()
+    assert carat.carat_get_device_status(clear=True) == carat.CARAT_DEV_BAD_CONTEXT
+    for b in (0, 2):
+        for j in (0, 63, 64, 199):
+            want, bound = c.want(b, [j])
+            assert ((out[b, j].cpu().double() - want[0]).abs() <= bound[0]).all()
+
+
 @pytest.mark.parametrize("q_heads,kv_heads,head_dim,k", [(16, 8, 256, 130), (16, 2, 512, 130),
                                                          (16, 2, 512, 3)])
 def test_views_that_begin_on_16_bytes(q_heads, kv_heads, head_dim, k):
