@@ -83,6 +83,7 @@ constexpr int kStage = 32768;           // K: 64 keys x 256 d, or V: 128 keys x 
 constexpr int kThreads = 384, kSoftmax = 256;
 constexpr int kJobs = 4;                // items handed to the other roles
 constexpr int kPieceCost = 3;           // of a piece besides its key tiles, in key tiles
+constexpr int kMergeCost = 4;           // of the merge of what was split, in key tiles
 constexpr int kUnits = 8;               // CTA pairs of the grid, times the pairs that fit
 constexpr int kMasked = 8;              // masked tiles of an item: 3 + 3 + 1 at most
 constexpr int kRecords = 5;             // items whose masked tiles' V is on record
@@ -186,22 +187,27 @@ __device__ __forceinline__ int pieces_of(const Plan &plan, int keys, int length)
 
 // Key tiles of a piece where requests differ, by a whole warp: of 32 lengths between a
 // quarter of and nearly four times a pair's share of all tiles, the one whose rounds of pieces
-// take the least, a piece costing its tiles and kPieceCost for its start, its output and
-// its share of the merge.
+// take the least, a piece costing its tiles and kPieceCost for its start and its output, and
+// the merge kMergeCost.  Requests of which none is longer than a pair's share by more than
+// those costs are left whole without a search.
 __device__ __noinline__ int piece_length(const PagedChunkParams &p, const Plan &plan, int lane) {
     const int per_tile = p.kv_heads * plan.halves;
     float total = 0.f;
+    int most = 0;
     Load held{};
     for (int base = 0; base < p.batch; base += 32) {
         held = {0, 0};
         if (base + lane < p.batch) held = load_of(p, plan, load_request(p, base + lane));
         total += (float)held.rows * held.keys;
+        most = max(most, held.keys);
     }
+    most = __reduce_max_sync(kFull, most);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(kFull, total, o);
     const float share = total * per_tile / plan.units;
+    if (most <= share + (kPieceCost + kMergeCost)) return max(most, 1);
     const int length = max(1, (int)(fast_exp2((lane - 16) * 0.125f) * share + 0.5f));
-    int count = 0, longest = 0;
+    int count = 0, whole = 0, longest = 0;
     for (int base = 0; base < p.batch; base += 32) {
         if (p.batch > 32) {
             held = {0, 0};
@@ -213,11 +219,13 @@ __device__ __noinline__ int piece_length(const PagedChunkParams &p, const Plan &
             if (rows == 0) continue;
             const int n = pieces_of(plan, keys, length);
             count += rows * n;
+            whole += rows;
             longest = max(longest, (keys + n - 1) / n);
         }
     }
     const float cost = (float)((count * per_tile + plan.units - 1) / plan.units) *
-                       (longest + kPieceCost);
+                           (longest + kPieceCost) +
+                       (count > whole ? kMergeCost : 0);
     float best = cost;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) best = fminf(best, __shfl_xor_sync(kFull, best, o));
@@ -1112,8 +1120,8 @@ Sizes sizes_of(int batch, int k, int q_heads, int kv_heads, int head_dim, bool w
     // may differ much in length: up to kUnits pieces a pair, within what may be left.  Planning
     // and an extra launch cost 3 us and more, and pieces are not taken over; one long request
     // among short ones costs up to half of the call.  us, without and with pieces, requests of
-    // 64 tokens behind 500 to 30000 (16/2 heads of 512, 128 items) 575 and 321, 3 of 512 behind
-    // 500 to 12000 (192 items) 366 and 265, 5 of 842 behind up to 11349 (70 items) 113 and 71;
+    // 64 tokens behind 500 to 30000 (16/2 heads of 512, 128 items) 575 and 315, 3 of 512 behind
+    // 500 to 12000 (192 items) 366 and 241, 5 of 842 behind up to 11349 (70 items) 113 and 71;
     // but 8 of up to 512 behind up to 8000 (16/8 of 256, 256 items, 64 MB) 45 and 67.
     const long long one = items > 0 ? std::max<long long>(1, pairs / items) : 1;
     z.plan.splits = (int)one;
