@@ -65,6 +65,7 @@
 #include <algorithm>
 #include <atomic>
 #include <cfloat>
+#include <climits>
 #include <cmath>
 
 #include <cuda_bf16.h>
@@ -1108,7 +1109,9 @@ struct Sizes {
     size_t ml, o, total;
 };
 
-Sizes sizes_of(int batch, int k, int q_heads, int kv_heads, int head_dim, bool window) {
+// For a page table of `capacity` keys; the workspace is that of any (INT_MAX), without a window.
+Sizes sizes_of(int batch, int k, int q_heads, int kv_heads, int head_dim, int window, int sinks,
+               int capacity) {
     Sizes z{};
     z.plan.tokens = kRows / (q_heads / kv_heads);
     z.plan.halves = head_dim / kDV;
@@ -1123,10 +1126,21 @@ Sizes sizes_of(int batch, int k, int q_heads, int kv_heads, int head_dim, bool w
     // 64 tokens behind 500 to 30000 (16/2 heads of 512, 128 items) 575 and 315, 3 of 512 behind
     // 500 to 12000 (192 items) 366 and 241, 5 of 842 behind up to 11349 (70 items) 113 and 71;
     // but 8 of up to 512 behind up to 8000 (16/8 of 256, 256 items, 64 MB) 45 and 67.
-    const long long one = items > 0 ? std::max<long long>(1, pairs / items) : 1;
+    // An item has no more pieces than its window and the page table can have key tiles, and
+    // few tiles are not split at all, as a merge costs kMergeCost of them.  us, before and
+    // with that: 5 tokens in a table of 384 keys (5/1 heads of 256) 21 and 11, 21 tokens under
+    // a window of 1024 (10/2) 18.7 and 14.2, 31 prompts of up to 283 (4/2) 27.5 and 21.7.
+    long long tiles_most = capacity / kKeys;
+    if (window > 0)
+        tiles_most = std::min(tiles_most, ((long long)window + 2 * z.plan.tokens) / kKeys + 2 +
+                                              ((long long)sinks + kKeys - 1) / kKeys);
+    const long long one = items > 0 && tiles_most > kMergeCost
+                              ? std::max<long long>(1, std::min(pairs / items, tiles_most))
+                              : 1;
     z.plan.splits = (int)one;
-    if (items > 0 && items <= (long long)kUnits / 2 * pairs && batch > 1 && !window) {
-        const long long most = std::min<long long>(kUnits * pairs / items, pairs);
+    if (items > 0 && items <= (long long)kUnits / 2 * pairs && batch > 1 && window == 0 &&
+        tiles_most > kPieceCost + kMergeCost) {
+        const long long most = std::min({kUnits * pairs / items, (long long)pairs, tiles_most});
         const size_t room = items <= kFewItems * (long long)pairs ? kPieceBytes : kPieceBytesMany;
         z.plan.splits = (int)std::max(one, std::min<long long>(most, room / row));
         z.plan.by_length = z.plan.splits > 1;
@@ -1253,7 +1267,7 @@ bool paged_chunk_supported(int head_dim) { return head_dim == 256 || head_dim ==
 size_t paged_chunk_workspace(int batch, int k, int q_heads, int kv_heads, int head_dim) {
     const size_t pairs = few_rows(batch, k, q_heads, kv_heads, head_dim, true)
                              ? 0
-                             : sizes_of(batch, k, q_heads, kv_heads, head_dim, false).total;
+                             : sizes_of(batch, k, q_heads, kv_heads, head_dim, 0, 0, INT_MAX).total;
     const size_t step = few_rows(batch, k, q_heads, kv_heads, head_dim, false)
                             ? step_sizes(batch, k, q_heads, kv_heads, head_dim).total
                             : 0;
@@ -1263,7 +1277,8 @@ size_t paged_chunk_workspace(int batch, int k, int q_heads, int kv_heads, int he
 cudaError_t launch_paged_chunk_attention(const PagedChunkParams &p, cudaStream_t stream) {
     if (few_rows(p.batch, p.k, p.q_heads, p.kv_heads, p.head_dim, p.window > 0))
         return launch_step(p, stream);
-    Sizes z = sizes_of(p.batch, p.k, p.q_heads, p.kv_heads, p.head_dim, p.window > 0);
+    Sizes z = sizes_of(p.batch, p.k, p.q_heads, p.kv_heads, p.head_dim, p.window, p.sinks,
+                       p.capacity);
     return p.head_dim == 256 ? launch<256>(p, z, stream) : launch<512>(p, z, stream);
 }
 

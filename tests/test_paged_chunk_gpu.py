@@ -352,6 +352,18 @@ def test_many_rows_in_pieces(q_heads, kv_heads, head_dim, ctx, k, counts):
     assert torch.equal(c.call(), again)
 
 
+@pytest.mark.parametrize("q_heads,kv_heads,head_dim", [(5, 1, 256), (16, 2, 512), (8, 1, 512)])
+@pytest.mark.parametrize("per", [1, 2, 4, 5, 7, 8, 9, 40])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (1, 0), (130, 5), (600, 700)])
+def test_as_many_pieces_as_tiles(q_heads, kv_heads, head_dim, per, window, sinks):
+    """Tables of `per` pages of 128 keys, requests that fill them and others that do not."""
+    for ctx in ([128 * per - 3], [128 * per - 3, 20, 0]):
+        c = Case(ctx, 3, q_heads, kv_heads, head_dim, window=window, sinks=sinks, seed=per,
+                 spread=2.0).device()
+        assert c.table.shape[1] == per
+        c.check(c.call())
+
+
 def test_many_rows_in_pieces_with_a_rejected_request():
     c = Case([3000, 40, 200], 200, 16, 2, 512, seed=26)
     c.device()
