@@ -1109,6 +1109,14 @@ struct Sizes {
     size_t ml, o, total;
 };
 
+// The most key tiles that `tokens` tokens one after another can see.
+long long tiles_most(int tokens, int window, int sinks, int capacity) {
+    const long long all = capacity / kKeys;
+    if (window == 0) return all;
+    return std::min(all, ((long long)window + tokens) / kKeys + 2 +
+                             ((long long)sinks + kKeys - 1) / kKeys);
+}
+
 // For a page table of `capacity` keys; the workspace is that of any (INT_MAX), without a window.
 Sizes sizes_of(int batch, int k, int q_heads, int kv_heads, int head_dim, int window, int sinks,
                int capacity) {
@@ -1130,17 +1138,14 @@ Sizes sizes_of(int batch, int k, int q_heads, int kv_heads, int head_dim, int wi
     // few tiles are not split at all, as a merge costs kMergeCost of them.  us, before and
     // with that: 5 tokens in a table of 384 keys (5/1 heads of 256) 21 and 11, 21 tokens under
     // a window of 1024 (10/2) 18.7 and 14.2, 31 prompts of up to 283 (4/2) 27.5 and 21.7.
-    long long tiles_most = capacity / kKeys;
-    if (window > 0)
-        tiles_most = std::min(tiles_most, ((long long)window + 2 * z.plan.tokens) / kKeys + 2 +
-                                              ((long long)sinks + kKeys - 1) / kKeys);
-    const long long one = items > 0 && tiles_most > kMergeCost
-                              ? std::max<long long>(1, std::min(pairs / items, tiles_most))
+    const long long most_tiles = tiles_most(2 * z.plan.tokens, window, sinks, capacity);
+    const long long one = items > 0 && most_tiles > kMergeCost
+                              ? std::max<long long>(1, std::min(pairs / items, most_tiles))
                               : 1;
     z.plan.splits = (int)one;
     if (items > 0 && items <= (long long)kUnits / 2 * pairs && batch > 1 && window == 0 &&
-        tiles_most > kPieceCost + kMergeCost) {
-        const long long most = std::min({kUnits * pairs / items, (long long)pairs, tiles_most});
+        most_tiles > kPieceCost + kMergeCost) {
+        const long long most = std::min({kUnits * pairs / items, (long long)pairs, most_tiles});
         const size_t room = items <= kFewItems * (long long)pairs ? kPieceBytes : kPieceBytesMany;
         z.plan.splits = (int)std::max(one, std::min<long long>(most, room / row));
         z.plan.by_length = z.plan.splits > 1;
@@ -1204,13 +1209,20 @@ cudaError_t launch(const PagedChunkParams &p, Sizes &z, cudaStream_t stream) {
 
 // Few rows of many requests at head_dim 512: the stream-K kernel with keys as the products'
 // long side (attention_tc.cuh), where a CTA pair would spend 256 rows' products on a
-// request's few, twice over for the scores.  Measured, us, pairs against it: 64 requests of 2
-// KV heads and 4 tokens under a window of 4096 208 and 157, 64 of one token and up to 16000
-// keys 417 and 210, 8 of 4 tokens and up to 32768 keys 100 and 81; but 8 under a window of
-// 1024 20 and 26, and 4 of 6005 keys 37 and 42.
-static bool few_rows(int batch, int k, int q_heads, int kv_heads, int head_dim, bool window) {
-    return batch * (long long)kv_heads >= (window ? 32 : 16) &&
-           tc_window_supported(head_dim, q_heads / kv_heads, k);
+// request's few, twice over for the scores.  It takes 25 us for little or no work, so the
+// requests have to be able to fill kStepTiles key tiles of KV heads.  Measured, us, pairs
+// against it: 64 requests of 2 KV heads and 4 tokens under a window of 4096 (4480 tiles) 208
+// and 157, of 1024 (1280) 94 and 90, of up to 1000 keys (1024) 73 and 63, 64 of one token and
+// up to 16000 keys 417 and 210, 8 of 4 tokens and up to 32768 keys (4096) 100 and 81; but 32
+// under a window of 1024 (640) 52 and 58, 16 under it (288) 28 and 39, 16 of up to 1000 keys
+// (256) 29 and 37, and 4 of 6005 keys 37 and 42.
+constexpr int kStepUnits = 16, kStepTiles = 640;
+
+static bool few_rows(int batch, int k, int q_heads, int kv_heads, int head_dim, int window,
+                     int sinks, int capacity) {
+    const long long units = batch * (long long)kv_heads;
+    return units >= kStepUnits && tc_window_supported(head_dim, q_heads / kv_heads, k) &&
+           units * tiles_most(k, window, sinks, capacity) > kStepTiles;
 }
 
 struct StepSizes {
@@ -1265,17 +1277,15 @@ static cudaError_t launch_step(const PagedChunkParams &p, cudaStream_t stream) {
 bool paged_chunk_supported(int head_dim) { return head_dim == 256 || head_dim == 512; }
 
 size_t paged_chunk_workspace(int batch, int k, int q_heads, int kv_heads, int head_dim) {
-    const size_t pairs = few_rows(batch, k, q_heads, kv_heads, head_dim, true)
-                             ? 0
-                             : sizes_of(batch, k, q_heads, kv_heads, head_dim, 0, 0, INT_MAX).total;
-    const size_t step = few_rows(batch, k, q_heads, kv_heads, head_dim, false)
+    const size_t pairs = sizes_of(batch, k, q_heads, kv_heads, head_dim, 0, 0, INT_MAX).total;
+    const size_t step = few_rows(batch, k, q_heads, kv_heads, head_dim, 0, 0, INT_MAX)
                             ? step_sizes(batch, k, q_heads, kv_heads, head_dim).total
                             : 0;
     return std::max(pairs, step);
 }
 
 cudaError_t launch_paged_chunk_attention(const PagedChunkParams &p, cudaStream_t stream) {
-    if (few_rows(p.batch, p.k, p.q_heads, p.kv_heads, p.head_dim, p.window > 0))
+    if (few_rows(p.batch, p.k, p.q_heads, p.kv_heads, p.head_dim, p.window, p.sinks, p.capacity))
         return launch_step(p, stream);
     Sizes z = sizes_of(p.batch, p.k, p.q_heads, p.kv_heads, p.head_dim, p.window, p.sinks,
                        p.capacity);
