@@ -615,9 +615,9 @@ size_t carat_paged_fp8_workspace_bytes(int batch, int proposal_count, int q_head
  *   see it, NaN and infinities included.  A NaN or infinity among the values of a key
  *   makes the elements it belongs to non-finite for every query that sees it, or
  *   the whole rows NaN where other queries of the request do not see it.
- *   workspace        >= carat_paged_chunk_workspace_bytes(...) bytes; NULL when that
- *                    is 0.  Needs no initialisation; calls that may overlap on the
- *                    GPU need separate workspaces.
+ *   workspace        >= carat_paged_chunk_workspace_bytes(...) bytes (136 MB at most);
+ *                    NULL when that is 0.  Needs no initialisation; calls that may
+ *                    overlap on the GPU need separate workspaces.
  *
  * Supported: head_dim 256 or 512; q_heads/kv_heads <= 64; batch * proposal_count *
  * q_heads <= 2^28; kv_heads * head_dim <= 2^24 (others: CARAT_ERR_UNSUPPORTED).
