@@ -352,6 +352,7 @@ struct Shared {
     uint64_t drain;
     uint64_t job_full[kJobs], job_empty[kJobs];   // each CTA's own
     uint64_t answered[kJobs];                     // each CTA's own
+    uint64_t answer_read[kJobs];                  // leader: the other CTA has read its answer
     alignas(16) uint4 answer[kJobs];              // which cluster's work is taken over
     uint32_t tmem;
     int abort_flag;
@@ -466,6 +467,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         for (int i = 0; i < kJobs; ++i) {
             tc::mbar_init(&sh->job_full[i], 1);
             tc::mbar_init(&sh->answered[i], 1);
+            tc::mbar_init(&sh->answer_read[i], 1);
             tc::mbar_init(&sh->job_empty[i], rank == 0 ? 11 : 10);
         }
         tc::fence_mbar_init();
@@ -512,15 +514,21 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         const uint32_t q_bytes = plan.tokens * p.group * 128;
         uint32_t published = 0, asked = 0;
         // Both CTAs' producers get the same answers, the leader asks.  An answer's place is
-        // used again after kJobs more: the other CTA is behind by less than the stage ring.
+        // used again after kJobs more, once the other CTA has read it there: work taken over
+        // that turns out to be none (a padded batch) goes through no other ring, and the
+        // other CTA may still wait for its queries' place.
         int unit = pair, id = pair;
         bool pending = false, rejects = pair == 0;
         auto ask = [&]() {
+            const int slot = asked % kJobs;
+            if (rank == 0 && asked >= kJobs)
+                alive = warp_wait<true>(&sh->answer_read[slot], ((asked / kJobs) & 1) ^ 1,
+                                        abort_flag, p.dev_status);
+            if (!alive) return;
             if (lane == 0) {
                 tc::fence_proxy_async_smem();
-                tc::mbar_arrive_expect_tx(&sh->answered[asked % kJobs], 16);
-                if (rank == 0)
-                    tc::ask_for_cluster(&sh->answer[asked % kJobs], &sh->answered[asked % kJobs]);
+                tc::mbar_arrive_expect_tx(&sh->answered[slot], 16);
+                if (rank == 0) tc::ask_for_cluster(&sh->answer[slot], &sh->answered[slot]);
             }
             __syncwarp();
             pending = true;
@@ -531,11 +539,17 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                 if (!first) found = list.find(p, plan, lane, id, it);
                 if (!found) {
                     // this pair's work is done: another's
+                    const int slot = asked % kJobs;
                     if (!pending) ask();
-                    alive = warp_wait(&sh->answered[asked % kJobs], (asked / kJobs) & 1, abort_flag,
-                                      p.dev_status);
+                    alive = alive && warp_wait(&sh->answered[slot], (asked / kJobs) & 1, abort_flag,
+                                               p.dev_status);
                     if (!alive) break;
-                    const int taken_over = tc::cluster_taken(&sh->answer[asked % kJobs]);
+                    const int taken_over = tc::cluster_taken(&sh->answer[slot]);
+                    __syncwarp();
+                    if (rank == 1 && lane == 0) {
+                        tc::fence_proxy_async_smem();
+                        tc::mbar_arrive_cluster(tc::map_to_rank(&sh->answer_read[slot], 0));
+                    }
                     ++asked;
                     pending = false;
                     unit = id = taken_over < 0 ? -1 : taken_over / 2;
