@@ -1065,7 +1065,14 @@ __global__ void __launch_bounds__(D / 4) paged_chunk_merge_kernel(
         if (!MANY) load(0);
         const Request rq = load_request(p, b);
         const int pieces = plan.pieces[b];
-        if (!request_ok(p, rq) || j >= rq.n || pieces == 1) {   // (one piece: written whole)
+        bool skip = !request_ok(p, rq) || j >= rq.n;
+        // A number that the attention did not write this time (it stopped on a timeout before
+        // the request) is not used: it may stand for more pieces than there are places.
+        if (!skip && (pieces < 1 || pieces > plan.splits)) {
+            if (threadIdx.x == 0) set_status(p.dev_status, CARAT_DEV_TIMEOUT);
+            skip = true;
+        }
+        if (skip || pieces == 1) {   // (one piece: written whole)
             if (!MANY) return;
             at = (b + 1) * p.k * p.q_heads;
             continue;
