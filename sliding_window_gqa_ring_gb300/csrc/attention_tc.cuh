@@ -2238,8 +2238,10 @@ __global__ void __launch_bounds__(D / 4) attn_fixup_kernel(const AttnParams p, i
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             if (q0 + i < np) {
+                // (WIN: a value that is not finite counts where its piece weighs nothing, as in
+                // a unit that is not split; a piece that saw no key left zeros)
                 const float w = s_w[q0 + i];
-                if (w != 0.f) {
+                if (WIN || w != 0.f) {
                     acc.x += v[i].x * w;
                     acc.y += v[i].y * w;
                     acc.z += v[i].z * w;
