@@ -91,6 +91,11 @@ constexpr int kRecords = 5;             // items whose masked tiles' V is on rec
 constexpr uint32_t kInTurn = 3;         // masked tiles whose V is on its way
 constexpr uint32_t kFull = 0xffffffffu;
 constexpr float kSlack = 8.0f;          // log2 units
+// Maxima from which on a score is rounded before the maximum is taken from it.  Below, the
+// two are one fused operation whose exact product differs from the rounded maximum by half a
+// unit of its last place, the same for the whole row: a factor of 2^(1/2) at most, which numerator
+// and denominator share.  From 2^31 on it would leave the range of a float.
+constexpr float kRounded = 16777216.f;  // 2^24
 
 template <int D>
 struct Lay {
@@ -822,7 +827,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
             const int n = tiles.n, lo_row = tiles.it.j0 + rank * plan.tokens;
             const int pos = tiles.it.ctx + min(lo_row + token, tiles.it.n - 1);
             float m = -INFINITY, l = 0.f;
-            bool has_masked = false;
+            bool has_masked = false, rounded = false;
             for (int x = 0; x < n; ++x) {
                 const uint32_t buf = (g + x) & 1;
                 alive = alive && warp_wait(&sh->s_full[buf], ((g + x) >> 1) & 1, abort_flag,
@@ -864,6 +869,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                     const float f = m == m_new ? 1.f : fast_exp2(m - m_new);
                     m = m_new;
                     l *= f;
+                    rounded = __any_sync(kFull, fabsf(m) >= kRounded && fabsf(m) < INFINITY);
                     if (x > 0) {
                         // each of the two warps scales half of the columns
                         alive = warp_wait(&sh->pv_done[buf ^ 1], ((g + x - 1) >> 1) & 1, abort_flag,
@@ -884,13 +890,21 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                 }
                 const float ref = m == -INFINITY ? 0.f : m;
                 float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int i = 0; i < 64; i += 2) {
-                    const float a = fast_exp2(fmaf(__uint_as_float(s[i]), scale, -ref));
-                    const float d = fast_exp2(fmaf(__uint_as_float(s[i + 1]), scale, -ref));
-                    const uint32_t w = pack_bf16(a, d);
+                auto weigh = [&](int i, float a, float d) {
+                    const uint32_t w = pack_bf16(fast_exp2(a), fast_exp2(d));
                     s[i / 2] = w;
                     sum[i / 2 & 3] += bf16lo(w) + bf16hi(w);
+                };
+                if (rounded) {
+#pragma unroll
+                    for (int i = 0; i < 64; i += 2)
+                        weigh(i, __fsub_rn(__fmul_rn(__uint_as_float(s[i]), scale), ref),
+                              __fsub_rn(__fmul_rn(__uint_as_float(s[i + 1]), scale), ref));
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 64; i += 2)
+                        weigh(i, fmaf(__uint_as_float(s[i]), scale, -ref),
+                              fmaf(__uint_as_float(s[i + 1]), scale, -ref));
                 }
                 l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
                 tc::tmem_st32(t_x + part * 32, s);

@@ -47,3 +47,35 @@ def test_a_value_that_is_not_finite_counts_where_its_key_weighs_nothing(
             else:
                 assert got[b, j].isfinite().all(), (b, j)
     assert rows
+
+
+@pytest.mark.parametrize("form,q_heads,kv_heads,head_dim,ctx,k", FORMS)
+@pytest.mark.parametrize("power", [9, 16, 24, 40, 56])
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+def test_large_scores(form, q_heads, kv_heads, head_dim, ctx, k, power, sign):
+    """Queries and keys of 2^power: scores of about 2^(2 power + 5), of which the products'
+    fp32 sums hold some 24 bits.  Where the largest lies further above the others than that
+    rounding, (D + 64) 2^-24 of scale sum |q k|, the softmax is one-hot and the output its
+    value, rounded twice to bf16 with its weight; no row may be anything but a number."""
+    c = form(ctx, k, q_heads, kv_heads, head_dim, scale=sign, seed=41)
+    c.q = (c.q.float() * 2.0 ** power).bfloat16()
+    for x in c.keys:
+        x[:] = (x.float() * 2.0 ** power).bfloat16()
+    c.write()
+    got = c.device().call().cpu()
+    assert got.isfinite().all()
+    g, compared = q_heads // kv_heads, 0
+    for b, n in enumerate(ctx):
+        for j in range(k):
+            for h in range(q_heads):
+                q = c.q[b, j, h].double()
+                keys = c.keys[b][:n + j + 1, h // g].double()
+                s = sign * (keys @ q)
+                off = float((keys.abs() @ q.abs()).max()) * (head_dim + 64) * 2.0 ** -24
+                top = s.topk(min(2, len(s))).values
+                if len(s) == 1 or top[0] - top[1] > 2 * off + 40:
+                    want = c.values[b][int(s.argmax()), h // g].double()
+                    size = 2.0 ** -7 * want.abs() + 2.0 ** -30
+                    assert ((got[b, j, h].double() - want).abs() <= size).all(), (b, j, h)
+                    compared += 1
+    assert compared > sum(1 for _ in ctx) * k
