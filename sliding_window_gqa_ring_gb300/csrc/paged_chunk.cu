@@ -816,8 +816,9 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         const uint32_t lanes = (uint32_t)quad << 21;
         const int token = row / p.group, head = row - token * p.group;
         const int inv_group = 65536 / p.group + 1;   // r inv_group >> 16 = r / group, r < 128
-        // the sign of the scale is in the product's descriptor; 0 would turn -inf into NaN
-        const float scale = fmaxf(fabsf(p.scale_log2), FLT_MIN);
+        // The sign of the scale is in the product's descriptor.  0 would turn the -inf of a masked
+        // score into NaN: the least number above it takes every finite score below 2^-20.
+        const float scale = fmaxf(fabsf(p.scale_log2), FLT_TRUE_MIN);
         uint32_t g = 0;   // tiles before this item's
         int turn = 0;     // which of the poison records
         int told = 0;     // whose place is whose

@@ -79,3 +79,18 @@ def test_large_scores(form, q_heads, kv_heads, head_dim, ctx, k, power, sign):
                     assert ((got[b, j, h].double() - want).abs() <= size).all(), (b, j, h)
                     compared += 1
     assert compared > sum(1 for _ in ctx) * k
+
+
+@pytest.mark.parametrize("form,q_heads,kv_heads,head_dim,ctx,k", FORMS)
+@pytest.mark.parametrize("scale", [0.0, 1e-40, -1e-40])
+def test_scales_of_next_to_nothing_over_large_scores(form, q_heads, kv_heads, head_dim, ctx, k,
+                                                     scale):
+    """Scores of about 2^123 times 1e-40 are below 2^-7, times 0 they are 0."""
+    scale = float(torch.tensor(scale, dtype=torch.float32))
+    c = form(ctx, k, q_heads, kv_heads, head_dim, scale=scale, seed=42)
+    c.q = (c.q.float() * 2.0 ** 59).bfloat16()
+    for x in c.keys:
+        x[:] = (x.float() * 2.0 ** 59).bfloat16()
+    c.write()
+    c.device()
+    c.check(c.call(), rows=[0, 1, 2, 3, 29, 100, 139])
