@@ -216,20 +216,37 @@ class SharedPool:
         """Empty blocks that single pages broke up, so that rings find room: at most
         max_moves pages move, and the page tables (and block scales) of `layers`, every
         layer with pages in this pool, follow.  Returns the pages moved; their old ids
-        are free, so whoever keeps ids on the host reads the tables again."""
+        are free, so whoever keeps ids on the host reads the tables again.  The pool is on
+        the current device, and no graph is being captured."""
         layers = list(layers)
-        for layer in layers:   # before the allocator counts the moves as done
+        for layer in layers:   # all that may be refused, before the moves count as done
             table = layer.page_table
             if table.dtype != torch.int32 or not table.is_contiguous() or \
                     table.device != self.k.device:
                 raise ValueError("compact: a layer's page table must be a contiguous int32 "
                                  "tensor on the pool's device")
+            scales = [getattr(layer, x, None) for x in ("k_scales", "v_scales")]
+            if any(t is not None for t in scales) and not all(
+                    t is not None and t.dtype == torch.float32 and t.is_contiguous() and
+                    t.device == self.k.device and t.dim() == 3 and t.shape[0] == self.num_pages and
+                    t.shape == scales[0].shape for t in scales):
+                raise ValueError("compact: a layer's block scales must be two contiguous fp32 "
+                                 "tensors [num_pages][blocks][kv_heads] on the pool's device")
+        if self.page_bytes % 16:
+            raise ValueError("compact: pages of a multiple of 16 bytes")
+        if not self.k.is_cuda or self.k.get_device() != torch.cuda.current_device():
+            raise ValueError("compact: the pool must be on the current CUDA device")
+        if stream is not None and not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(int(stream), device=self.device)
+        capturing = torch.cuda.is_current_stream_capturing()   # lists are made on that one
+        with torch.cuda.stream(stream):
+            capturing |= torch.cuda.is_current_stream_capturing()
+        if capturing:   # the allocator counts the moves once, not at every replay
+            raise ValueError("compact: not while a stream is captured")
         src, dst = self.alloc.plan_compaction(max_moves)
         if src:
             src, dst = _i32(src, self.device), _i32(dst, self.device)
             if stream is not None:   # not to be given to others before that stream is done
-                if not isinstance(stream, torch.cuda.Stream):
-                    stream = torch.cuda.ExternalStream(int(stream), device=self.device)
                 src.record_stream(stream)
                 dst.record_stream(stream)
             whole = (self.num_pages, 1, 1, self.page_bytes)
