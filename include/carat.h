@@ -615,7 +615,8 @@ size_t carat_paged_fp8_workspace_bytes(int batch, int proposal_count, int q_head
  *   see it, NaN and infinities included.  A NaN or infinity among the values of a key
  *   makes the elements it belongs to non-finite for every query that sees it, or
  *   the whole rows NaN where other queries of the request do not see it.
- *   workspace        >= carat_paged_chunk_workspace_bytes(...) bytes (136 MB at most);
+ *   workspace        >= carat_paged_chunk_workspace_bytes(...) bytes (at most 136 MB, or
+ *                    41 MB and 16 bytes for each request and KV head where that is more);
  *                    NULL when that is 0.  Needs no initialisation; calls that may
  *                    overlap on the GPU need separate workspaces.
  *
