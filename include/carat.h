@@ -613,8 +613,9 @@ size_t carat_paged_fp8_workspace_bytes(int batch, int proposal_count, int q_head
  *   in rows at or past a request's key count (context_length + new_counts[b]) never
  *   reaches the result, nor does what lies in a key the rows of a query that does not
  *   see it, NaN and infinities included.  A NaN or infinity among the values of a key
- *   makes the elements it belongs to non-finite for every query that sees it, or
- *   the whole rows NaN where other queries of the request do not see it.
+ *   makes the elements it belongs to non-finite for every query that sees it, whatever
+ *   the key's weight; where other queries of the request do not see that key or one within
+ *   128 positions of it, other elements of those rows, up to all of them, may be NaN too.
  *   workspace        >= carat_paged_chunk_workspace_bytes(...) bytes (at most 136 MB, or
  *                    41 MB and 16 bytes for each request and KV head where that is more);
  *                    NULL when that is 0.  Needs no initialisation; calls that may

@@ -94,3 +94,27 @@ def test_scales_of_next_to_nothing_over_large_scores(form, q_heads, kv_heads, he
     c.write()
     c.device()
     c.check(c.call(), rows=[0, 1, 2, 3, 29, 100, 139])
+
+
+@pytest.mark.parametrize("form,q_heads,kv_heads,head_dim,ctx,k", FORMS)
+@pytest.mark.parametrize("at", [3, 300, 500])
+def test_a_value_that_is_not_finite_near_the_newest_keys(form, q_heads, kv_heads, head_dim, ctx, k,
+                                                         at):
+    """In the newest key but one, which the queries before the last but one do not see: the
+    element itself is not finite for those that see it, others of their rows may be; no
+    other row, and no other head's, changes."""
+    at %= head_dim
+    clean = form(ctx, k, q_heads, kv_heads, head_dim, seed=43)
+    c = form(ctx, k, q_heads, kv_heads, head_dim, seed=43)
+    for b, n in enumerate(ctx):
+        c.values[b][n + k - 2, 0, at] = float("inf")
+    c.write()
+    got = c.device().call().cpu()
+    g = q_heads // kv_heads
+    for b in {0, len(ctx) - 1}:
+        for j in {0, k - 3, k - 2, k - 1} - {-1}:
+            want, bound = (x[0] for x in clean.want(b, [j]))
+            hit = torch.zeros(q_heads, dtype=torch.bool)
+            hit[:g] = j >= k - 2
+            assert not got[b, j, hit][:, at].isfinite().any(), (b, j)
+            assert ((got[b, j].double() - want).abs() <= bound)[~hit].all(), (b, j)
