@@ -394,14 +394,18 @@ class Fp8PagedLayer:
     Queries and new keys arrive unrotated; step() is the rotary append
     (quantising on the way) and the attention over the pages.  Outputs are
     bf16.  The pages come from a SharedPool (a page of the pool holds twice the
-    rows it holds in bf16)."""
+    rows it holds in bf16).
+
+    k_scales, v_scales: another layer's, where the two share pages (children of
+    its requests, see fork()); block_rows is then that layer's."""
 
     out_dtype = torch.bfloat16
 
     def __init__(self, pool: SharedPool, page_table: torch.Tensor, cos_sin: torch.Tensor, *,
                  q_heads: int = 16, kv_heads: int = 2, head_dim: int = 512,
                  max_proposals: int = 4, block_rows: int = 32, window: int = 0,
-                 scale: float | None = None, interleaved: bool = False):
+                 scale: float | None = None, interleaved: bool = False,
+                 k_scales: torch.Tensor | None = None, v_scales: torch.Tensor | None = None):
         self.key_pages, self.value_pages = pool.pages_fp8(kv_heads, head_dim)
         num_pages, self.page_rows = self.key_pages.shape[:2]
         if block_rows not in (16, 32, 64, 128):
@@ -412,8 +416,17 @@ class Fp8PagedLayer:
         self.scale = (1.0 / math.sqrt(head_dim)) if scale is None else scale
         self.device = pool.device
         shape = (num_pages, self.page_rows // block_rows, kv_heads)
-        self.k_scales = torch.ones(shape, dtype=torch.float32, device=self.device)
-        self.v_scales = torch.ones(shape, dtype=torch.float32, device=self.device)
+        if (k_scales is None) != (v_scales is None):
+            raise ValueError("k_scales and v_scales go together")
+        for t in (k_scales, v_scales):
+            if t is not None and (tuple(t.shape) != shape or t.dtype != torch.float32 or
+                                  not t.is_contiguous() or t.device != self.key_pages.device):
+                raise ValueError(f"scales of these pages are contiguous fp32 {list(shape)} on the "
+                                 "pool's device")
+        if k_scales is None:
+            k_scales, v_scales = (torch.ones(shape, dtype=torch.float32, device=self.device)
+                                  for _ in range(2))
+        self.k_scales, self.v_scales = k_scales, v_scales
         batch = page_table.shape[0]
         self.rotated = torch.empty(batch * max_proposals * q_heads * head_dim,
                                    dtype=torch.bfloat16, device=self.device)
@@ -444,7 +457,8 @@ class Fp8PagedLayer:
 
     def fork(self, context_lengths, child_table, parents, new_pages, child_lengths=None,
              stream=None):
-        """Children of this table's requests (carat_paged_fork), block scales too."""
+        """Children of this table's requests (carat_paged_fork), block scales too: a layer
+        over child_table takes this one's k_scales and v_scales."""
         carat.carat_paged_fork(self.key_pages, self.value_pages, self.page_table, context_lengths,
                                child_table, parents, new_pages, child_lengths=child_lengths,
                                k_scales=self.k_scales, v_scales=self.v_scales, stream=stream)
