@@ -362,7 +362,8 @@ carat_status carat_paged_append(void *key_pages, void *value_pages, int num_page
  * entry points take in ring_ids when k_ring / v_ring point at the pool.  A
  * global-layer page is any single page.  Single pages come first from blocks
  * that single pages already use, so whole blocks stay free for rings.
- * Thread-safe.  Returns: alloc_ring -> ring id or -1 (no whole free block);
+ * Thread-safe.  Returns: create -> NULL for a size below 1 or without memory;
+ * alloc_ring -> ring id or -1 (no whole free block);
  * alloc_pages -> n, writing n page ids to out_pages, or -1 (fewer than n free:
  * nothing allocated); free_* -> 0, or -1 for an id that is not allocated (then
  * nothing is freed); stats -> out4 = {free pages, whole free blocks, rings in

@@ -54,10 +54,15 @@ carat_pool *carat_pool_create(int num_pages, int pages_per_ring) {
     p->num_pages = num_pages;
     p->pages_per_ring = pages_per_ring;
     p->num_blocks = num_pages / pages_per_ring;
-    p->page_state.assign((size_t)num_pages, 0);
-    p->page_owners.assign((size_t)num_pages, 0);
-    p->block_free.assign((size_t)p->num_blocks, pages_per_ring);
-    p->block_ring.assign((size_t)p->num_blocks, 0);
+    try {
+        p->page_state.assign((size_t)num_pages, 0);
+        p->page_owners.assign((size_t)num_pages, 0);
+        p->block_free.assign((size_t)p->num_blocks, pages_per_ring);
+        p->block_ring.assign((size_t)p->num_blocks, 0);
+    } catch (...) {   // out of memory
+        delete p;
+        return nullptr;
+    }
     return p;
 }
 
