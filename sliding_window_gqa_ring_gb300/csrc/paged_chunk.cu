@@ -110,7 +110,7 @@ struct Lay {
     // is the queries', and the next item's queries are loaded behind it.
     static constexpr bool kOutInQ = D == 512;
     static constexpr int kOffMisc = kOffQ + D / 64 * kSlab + (kOutInQ ? 0 : 8 * 4096);
-    static constexpr int kMisc = 3072;
+    static constexpr int kMisc = 2560;
     static constexpr int kAlloc = kOffMisc + kMisc;
     static_assert(kAlloc <= 232448, "more dynamic shared memory than one CTA may use");
 };
