@@ -828,7 +828,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
             const int n = tiles.n, lo_row = tiles.it.j0 + rank * plan.tokens;
             const int pos = tiles.it.ctx + min(lo_row + token, tiles.it.n - 1);
             float m = -INFINITY, l = 0.f;
-            bool has_masked = false, rounded = false;
+            bool has_masked = false, large = false, rounded = false;
             for (int x = 0; x < n; ++x) {
                 const uint32_t buf = (g + x) & 1;
                 alive = alive && warp_wait(&sh->s_full[buf], ((g + x) >> 1) & 1, abort_flag,
@@ -870,7 +870,10 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                     const float f = m == m_new ? 1.f : fast_exp2(m - m_new);
                     m = m_new;
                     l *= f;
-                    rounded = __any_sync(kFull, fabsf(m) >= kRounded && fabsf(m) < INFINITY);
+                    // (rows of no query hold anything, and no row changes another's bits)
+                    large = fabsf(m) >= kRounded && fabsf(m) < INFINITY &&
+                            token < min(plan.tokens, tiles.it.n - lo_row);
+                    rounded = __any_sync(kFull, large);
                     if (x > 0) {
                         // each of the two warps scales half of the columns
                         alive = warp_wait(&sh->pv_done[buf ^ 1], ((g + x - 1) >> 1) & 1, abort_flag,
@@ -897,10 +900,12 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                     sum[i / 2 & 3] += bf16lo(w) + bf16hi(w);
                 };
                 if (rounded) {
+                    auto less = [&](uint32_t score) {
+                        const float x = __uint_as_float(score);
+                        return large ? __fsub_rn(__fmul_rn(x, scale), ref) : fmaf(x, scale, -ref);
+                    };
 #pragma unroll
-                    for (int i = 0; i < 64; i += 2)
-                        weigh(i, __fsub_rn(__fmul_rn(__uint_as_float(s[i]), scale), ref),
-                              __fsub_rn(__fmul_rn(__uint_as_float(s[i + 1]), scale), ref));
+                    for (int i = 0; i < 64; i += 2) weigh(i, less(s[i]), less(s[i + 1]));
                 } else {
 #pragma unroll
                     for (int i = 0; i < 64; i += 2)

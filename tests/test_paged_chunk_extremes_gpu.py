@@ -118,3 +118,24 @@ def test_a_value_that_is_not_finite_near_the_newest_keys(form, q_heads, kv_heads
             hit[:g] = j >= k - 2
             assert not got[b, j, hit][:, at].isfinite().any(), (b, j)
             assert ((got[b, j].double() - want).abs() <= bound)[~hit].all(), (b, j)
+
+
+@pytest.mark.parametrize("form,q_heads,kv_heads,head_dim,ctx,k", FORMS + [
+    (base.Case, 10, 2, 512, [200, 900], 40), (base.Case, 5, 1, 256, [30], 60)])
+@pytest.mark.parametrize("power", [20, 50, 200])
+def test_no_query_changes_anothers_bits(form, q_heads, kv_heads, head_dim, ctx, k, power):
+    """Every third query is zero, or of 2^power (200: infinite), or not there (behind its
+    request's count): the others' outputs are the same bits."""
+    counts = [max(1, k - 1 - b % 3) for b in range(len(ctx))]
+    outs = []
+    for size in (0.0, 1.0, 2.0 ** power):
+        c = form(ctx, k, q_heads, kv_heads, head_dim, counts=counts, seed=44)
+        c.q[:, ::3] = (c.q[:, ::3].float() * size).bfloat16()
+        for b, n in enumerate(counts):
+            c.q[b, n:] = (c.q[b, n:].float() * size).bfloat16()
+        outs.append(c.device().call().cpu().view(torch.int16))
+    for b, n in enumerate(counts):
+        rows = [j for j in range(n) if j % 3]
+        for out in outs[1:]:
+            assert torch.equal(out[b, rows], outs[0][b, rows]), b
+            assert torch.equal(out[b, n:], outs[0][b, n:]), b
