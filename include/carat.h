@@ -622,6 +622,9 @@ size_t carat_paged_fp8_workspace_bytes(int batch, int proposal_count, int q_head
  *                    NULL when that is 0.  Needs no initialisation; calls that may
  *                    overlap on the GPU need separate workspaces.
  *
+ * How a call is cut up goes by what the host knows: where few rows meet short contexts, a
+ * page table much wider than they need (max_pages) takes up to twice as long.
+ *
  * Supported: head_dim 256 or 512; q_heads/kv_heads <= 64; batch * proposal_count *
  * q_heads <= 2^28; kv_heads * head_dim <= 2^24 (others: CARAT_ERR_UNSUPPORTED).
  */
