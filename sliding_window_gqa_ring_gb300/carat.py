@@ -410,11 +410,28 @@ def carat_global_append_verify_attention_paged(out, queries, key_pages, value_pa
 
 def carat_paged_append(key_pages, value_pages, page_table, k_new, v_new, context_lengths, *,
                        stream=None):
-    """Write rows for positions context_lengths[b] + j through the page table."""
-    _expect(key_pages, torch.bfloat16, "key_pages")
-    _expect(k_new, torch.bfloat16, "k_new")
+    """Write rows for positions context_lengths[b] + j through the page table: k_new and
+    v_new bf16 [B][k][Hkv][D], a table line and a length for each request (or more)."""
+    what = "carat_paged_append"
+    for name, t in (("key_pages", key_pages), ("value_pages", value_pages), ("k_new", k_new),
+                    ("v_new", v_new)):
+        _expect(t, torch.bfloat16, f"{what}: {name}")
+        if t.dim() != 4:
+            raise ValueError(f"{what}: {name} must be 4-D")
+    _expect(page_table, torch.int32, f"{what}: page_table")
+    _expect(context_lengths, torch.int32, f"{what}: context_lengths")
     num_pages, page_rows, kv_heads, head_dim = key_pages.shape
     batch, k = k_new.shape[0], k_new.shape[1]
+    if value_pages.shape != key_pages.shape:
+        raise ValueError(f"{what}: key and value pages differ in shape")
+    if tuple(k_new.shape) != (batch, k, kv_heads, head_dim) or v_new.shape != k_new.shape:
+        raise ValueError(f"{what}: k_new and v_new must be [batch][k][{kv_heads}][{head_dim}]")
+    if page_table.dim() != 2 or page_table.shape[0] < batch or context_lengths.dim() != 1 or \
+            context_lengths.shape[0] < batch:
+        raise ValueError(f"{what}: page_table and context_lengths must have a line for each of "
+                         f"{batch} requests")
+    _on_device(what, key_pages=key_pages, value_pages=value_pages, page_table=page_table,
+               k_new=k_new, v_new=v_new, context_lengths=context_lengths)
     _check(library().carat_paged_append(
         _ptr(key_pages), _ptr(value_pages), num_pages, _ptr(page_table), page_table.shape[1],
         page_rows, _ptr(k_new), _ptr(v_new), _ptr(context_lengths), k, batch, kv_heads,

@@ -341,6 +341,9 @@ class PagedGlobalLayer:
         if queries.shape[1] > self.max_chunk:
             raise ValueError(f"{queries.shape[1]} new tokens: the layer was made for max_chunk "
                              f"{self.max_chunk}")
+        if k_new.shape[:2] != queries.shape[:2]:
+            raise ValueError(f"k_new of {tuple(k_new.shape[:2])} [batch][k] for queries of "
+                             f"{tuple(queries.shape[:2])}")
         if out is None:
             out = torch.empty(queries.shape, dtype=torch.bfloat16, device=self.device)
         if self.cos_sin is not None:
