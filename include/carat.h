@@ -625,8 +625,9 @@ size_t carat_paged_fp8_workspace_bytes(int batch, int proposal_count, int q_head
  * How a call is cut up goes by what the host knows: where few rows meet short contexts, a
  * page table much wider than they need (max_pages) takes up to twice as long.
  *
- * Supported: head_dim 256 or 512; q_heads/kv_heads <= 64; batch * proposal_count *
- * q_heads <= 2^28; kv_heads * head_dim <= 2^24 (others: CARAT_ERR_UNSUPPORTED).
+ * Supported: head_dim 256 or 512; q_heads/kv_heads <= 64; batch <= 2^22; batch *
+ * proposal_count * q_heads <= 2^28; kv_heads * head_dim <= 2^24 (others:
+ * CARAT_ERR_UNSUPPORTED).
  */
 carat_status carat_paged_chunk_attention(
     void *out, const void *queries, const void *key_pages, const void *value_pages, int num_pages,
