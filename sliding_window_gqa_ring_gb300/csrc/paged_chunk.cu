@@ -21,7 +21,7 @@
 // 8191 tokens of 16 heads over 8 of 256, 288 us, 1910 TFLOP/s (the library's product reaches
 // 1917); over 2 of 512, 817 us, 1345 TFLOP/s of what is asked for and 2017 with the scores
 // computed twice.  (A few replays; in a long stream of calls the power limit makes the latter
-// 920 to 930, as the library's product falls to 1703.)  Under a window an item is short (9 tiles
+// 915 to 932, as the library's product falls to 1703.)  Under a window an item is short (9 tiles
 // at a window of 1024) and its ends show: 8192 tokens 101 us, 1270 TFLOP/s.  There from the last
 // product of an item to the first of the next 6000 to 7000 cycles pass, where a tile takes 2150:
 // its output 2500 to 3700 (64 KB a CTA leave at about 32 bytes a cycle), the next scores' way to
